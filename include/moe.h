@@ -363,6 +363,140 @@ moe_status moe_route_noalloc(const moe_config *cfg, const float *router_w, const
                              const float *x, int32_t T, int32_t *topk_idx, float *topk_w,
                              void *stream);
 
+/*
+ * Operators around the router and its experts: for training a layer and for
+ * serving experts whose weights stay in 8-bit floating point (e4m3) with one
+ * scale per block of 128.  (The pages state the block format as the input of
+ * their int4 conversion, reader.mx section 06; the balance loss and the
+ * gradients have no counterpart there.)
+ *
+ * Common to all of them.  No handle: every buffer is the caller's, on the
+ * current CUDA device, and nothing is allocated.  A call launches on `stream`
+ * and returns without waiting; it may be captured in a CUDA graph.  Calls may
+ * overlap as long as they do not share an output or a workspace.  Results are
+ * bit-identical from run to run.  Outputs must not overlap inputs.  A size of
+ * zero tokens or rows is valid.  Errors: MOE_ERR_INVALID for NULL or
+ * misaligned pointers, bad enumerators and sizes that contradict each other;
+ * MOE_ERR_UNSUPPORTED for sizes outside the stated limits; MOE_ERR_CUDA when a
+ * launch fails; moe_last_error has the message.  Values read on the device
+ * (indices, offsets) are range-checked there and never used as addresses
+ * unchecked.
+ */
+
+/* Element types of the floating tensors below. */
+#define MOE_DTYPE_F32 0
+#define MOE_DTYPE_F16 1
+#define MOE_DTYPE_BF16 2
+
+/* Token lists of a router's choice topk_idx[T, K] (int32; a value outside
+ * [0, E), e.g. -1, is a pair that was dropped).  Pairs p = t * K + k are
+ * grouped by expert, stable in p, each expert's segment starting at a multiple
+ * of `align`:
+ *   counts[E]       pairs of every expert
+ *   offsets[E + 1]  first row of every segment; offsets[e + 1] - offsets[e] is
+ *                   counts[e] rounded up to a multiple of align
+ *   rows[room]      the token t of every row, -1 in rows without one (behind a
+ *                   segment's pairs and behind the last segment)
+ *   pos[T, K]       the row of every pair, -1 for dropped ones
+ * room = moe_expert_lists_rows(...), the most rows any choice of that size
+ * needs, a multiple of align.  align = 1 packs the rows; 128 makes the
+ * segments whole blocks, as moe_fp8_wgrad needs.  workspace:
+ * moe_expert_lists_workspace(...) bytes (16-byte aligned; may be NULL if 0).
+ * Limits: E in 1..1024, K in 1..1024, align in 1..4096, room below 2^31. */
+int64_t moe_expert_lists_rows(int32_t T, int32_t top_k, int32_t n_experts, int32_t align);
+size_t moe_expert_lists_workspace(int32_t T, int32_t top_k, int32_t n_experts);
+moe_status moe_expert_lists(const int32_t *topk_idx, int32_t T, int32_t top_k, int32_t n_experts, int32_t align,
+                            int32_t *counts, int32_t *offsets, int32_t *rows, int32_t *pos, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
+/* Balance loss of a router.  logits[T, E] (dtype; rows ld elements apart),
+ * topk_idx[T, K] the choice (values outside [0, E) are not counted).  The
+ * tokens form n_seq segments, segment s = [seq_offsets[s], seq_offsets[s + 1])
+ * (device int32, ascending; NULL with n_seq = 1: all T tokens); mask[T]
+ * (device, one byte per token; NULL: none) takes tokens with 0 out, whatever
+ * their logits hold.  With
+ * p = softmax(logits) or sigmoid(l) / (sum_e sigmoid(l) + 1e-20) (score_func),
+ * n_s the segment's unmasked tokens and c_se its choices of expert e,
+ *   loss = coef / n_seq  sum_s  E / (K n_s^2)  sum_e c_se sum_{t in s} p_te
+ * (an empty segment adds nothing; a perfectly even one adds coef / n_seq).
+ * Writes loss[1], counts[n_seq, E] (c), prob_sums[n_seq, E] (sum_t p) and
+ * tokens[n_seq] (n), all float32 / int32.  A softmax row of -infinity alone
+ * has p = 0.  workspace: moe_balance_workspace(...) bytes, 16-byte aligned.
+ * Limits: E in 1..1024, n_seq in 1..65535. */
+size_t moe_balance_workspace(int32_t T, int32_t n_experts, int32_t n_seq);
+moe_status moe_balance_forward(const void *logits, int32_t dtype, int64_t ld, int32_t T, int32_t n_experts,
+                               const int32_t *topk_idx, int32_t top_k, int32_t score_func, float coef,
+                               const int32_t *seq_offsets, int32_t n_seq, const uint8_t *mask, float *loss,
+                               int32_t *counts, float *prob_sums, int32_t *tokens, void *workspace,
+                               size_t workspace_bytes, void *stream);
+
+/* Its gradient (the counts are constants): dlogits[T, E] (dtype of logits, rows
+ * ldd elements apart) = grad_loss * d loss / d logits, with counts and tokens
+ * as moe_balance_forward wrote them and grad_loss a device float32 (NULL: 1).
+ * Masked tokens get zeros; rows of tokens outside every segment stay as they
+ * are. */
+moe_status moe_balance_backward(const void *logits, int32_t dtype, int64_t ld, int32_t T, int32_t n_experts,
+                                int32_t top_k, int32_t score_func, float coef, const int32_t *counts,
+                                const int32_t *tokens, const int32_t *seq_offsets, int32_t n_seq,
+                                const uint8_t *mask, const float *grad_loss, void *dlogits, int64_t ldd,
+                                void *stream);
+
+/* e4m3 codes with one scale per 1 x 128 block along each row: for row r of the
+ * output, x row `rows[r]` (device int32; negative or >= n_tokens: a row of
+ * zeros; rows NULL: row r itself, R = n_tokens), x[n_tokens, width] in dtype,
+ * rows ld elements apart;
+ *   s = the least power of two >= 2^-126 with max |x| / s <= 448 over the block
+ *       (1 for a block of zeros)
+ *   codes = x / s rounded to the nearest e4m3 value, ties to even
+ * codes[R, width], scales[ceil(width / 128), R] (block-major).  A block with a
+ * NaN or an infinity gets the scale NaN.  With codes_t (not NULL) also the
+ * codes along the columns, blocks of 128 consecutive output rows, zeros behind
+ * row R: codes_t[width, Rp], scales_t[Rp / 128, width], Rp = R rounded up to a
+ * multiple of 128.  width: a multiple of 16 in 16..131072; R up to 8388480; x
+ * and ld such that every row starts on a 16-byte boundary; code buffers
+ * 16-byte aligned. */
+moe_status moe_fp8_quantize(const void *x, int32_t dtype, int64_t ld, int32_t n_tokens, int32_t width,
+                            const int32_t *rows, int32_t R, uint8_t *codes, float *scales, uint8_t *codes_t,
+                            float *scales_t, void *stream);
+
+/* The same with one scale per 128 x 128 block, for weights w[E, N, K] (dtype,
+ * contiguous): codes[E, N, K], scales[E, ceil(N / 128), ceil(K / 128)], and when
+ * codes_t is not NULL the transposed matrices codes_t[E, K, N] with
+ * scales_t[E, ceil(K / 128), ceil(N / 128)] (the same values; what the gradient
+ * of the activations multiplies by).  K: a multiple of 16 in 16..131072; E up
+ * to 65535, N up to 131072. */
+moe_status moe_fp8_quantize_weights(const void *w, int32_t dtype, int32_t E, int32_t N, int32_t K, uint8_t *codes,
+                                    float *scales, uint8_t *codes_t, float *scales_t, void *stream);
+
+/* y[r, n] = sum_b x_scale[b, r] w_scale[e, n / 128, b] sum_{k in block b} x[r, k] w[e, n, k]
+ * over the 128-blocks b of the inner axis, in float32, rounded once to y's
+ * dtype: x[R, K] and w[E, N, K] e4m3 codes, x_scale[ceil(K / 128), R] and
+ * w_scale[E, ceil(N / 128), ceil(K / 128)] any float32 values.  With offsets
+ * (device int32 [E + 1], ascending) row r belongs to the expert e with
+ * offsets[e] <= r < offsets[e + 1]; rows outside every segment are left as they
+ * are in y.  offsets NULL: E = 1, every row.  y[R, N], rows ldy elements apart.
+ * K: a multiple of 16 in 16..131072; N in 1..131072; E in 1..1024; x and w
+ * 16-byte aligned. */
+moe_status moe_fp8_matmul(const uint8_t *x, const float *x_scale, int32_t R, const uint8_t *w, const float *w_scale,
+                          int32_t E, int32_t N, int32_t K, const int32_t *offsets, void *y, int32_t y_dtype,
+                          int64_t ldy, void *stream);
+
+/* Weight gradients dw[e, n, k] = sum over the rows r of expert e of dy[r, n] x[r, k],
+ * from column-quantised dy and x (moe_fp8_quantize's codes_t and scales_t):
+ * xt[K, R], dyt[N, R] codes, xt_scale[R / 128, K], dyt_scale[R / 128, N]; R a
+ * multiple of 128.  offsets as above, every entry a multiple of 128 (others are
+ * rounded down); NULL: E = 1, all rows.  Float32 sums; dw[E, N, K] in dw_dtype,
+ * zeros for an expert without rows.  N, K in 1..131072; E in 1..1024; xt and
+ * dyt 16-byte aligned. */
+moe_status moe_fp8_wgrad(const uint8_t *xt, const float *xt_scale, const uint8_t *dyt, const float *dyt_scale,
+                         int32_t R, int32_t N, int32_t K, int32_t E, const int32_t *offsets, void *dw,
+                         int32_t dw_dtype, void *stream);
+
+/* Waits for the device, then reads and clears the error word of the two
+ * products on it: MOE_DEVICE_ERR_TC if a pipeline wait of a kernel ran out (its
+ * output is invalid); returns MOE_ERR_CUDA when it was set. */
+moe_status moe_fp8_device_error(uint32_t *flags);
+
 #ifdef __cplusplus
 }
 #endif

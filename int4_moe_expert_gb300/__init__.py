@@ -27,6 +27,9 @@ __all__ = [
     "MOE_DEVICE_ERR_CHECK",
     "MOE_DEVICE_ERR_TC",
     "moe_uses_streaming_decode", "moe_streaming_decode_max_tokens", "moe_uses_tensor_cores",
+    "MOE_DTYPE_F32", "MOE_DTYPE_F16", "MOE_DTYPE_BF16",
+    "moe_expert_lists", "moe_balance_forward", "moe_balance_backward", "moe_fp8_quantize",
+    "moe_fp8_quantize_weights", "moe_fp8_matmul", "moe_fp8_wgrad", "moe_fp8_device_error",
 ]
 
 MOE_OK, MOE_ERR_INVALID, MOE_ERR_CUDA, MOE_ERR_NOMEM, MOE_ERR_UNSUPPORTED = 0, 1, 2, 3, 4
@@ -38,6 +41,7 @@ MOE_DEVICE_ERR_GRID, MOE_DEVICE_ERR_CHECK, MOE_DEVICE_ERR_TC = 8, 16, 32
 MOE_TRACE_SLOTS = 64
 MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX = 0, 1
 MOE_FORMAT_INT4, MOE_FORMAT_INT8, MOE_FORMAT_G64 = 0, 1, 2
+MOE_DTYPE_F32, MOE_DTYPE_F16, MOE_DTYPE_BF16 = 0, 1, 2
 _STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID", 2: "MOE_ERR_CUDA", 3: "MOE_ERR_NOMEM",
            4: "MOE_ERR_UNSUPPORTED"}
 
@@ -118,6 +122,25 @@ def lib():
         L.moe_route_noalloc.restype = C.c_int
         L.moe_trace_read.argtypes = [vp, vp, i32, C.POINTER(i32)]
         L.moe_trace_read.restype = C.c_int
+        i64, sz, f32 = C.c_int64, C.c_size_t, C.c_float
+        L.moe_expert_lists_rows.argtypes = [i32, i32, i32, i32]
+        L.moe_expert_lists_rows.restype = i64
+        L.moe_expert_lists_workspace.argtypes = [i32, i32, i32]
+        L.moe_expert_lists_workspace.restype = sz
+        L.moe_expert_lists.argtypes = [vp, i32, i32, i32, i32, vp, vp, vp, vp, vp, sz, vp]
+        L.moe_balance_workspace.argtypes = [i32, i32, i32]
+        L.moe_balance_workspace.restype = sz
+        L.moe_balance_forward.argtypes = [vp, i32, i64, i32, i32, vp, i32, i32, f32, vp, i32, vp, vp, vp, vp, vp,
+                                          vp, sz, vp]
+        L.moe_balance_backward.argtypes = [vp, i32, i64, i32, i32, i32, i32, f32, vp, vp, vp, i32, vp, vp, vp, i64, vp]
+        L.moe_fp8_quantize.argtypes = [vp, i32, i64, i32, i32, vp, i32, vp, vp, vp, vp, vp]
+        L.moe_fp8_quantize_weights.argtypes = [vp, i32, i32, i32, i32, vp, vp, vp, vp, vp]
+        L.moe_fp8_matmul.argtypes = [vp, vp, i32, vp, vp, i32, i32, i32, vp, vp, i32, i64, vp]
+        L.moe_fp8_wgrad.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, i32, vp]
+        L.moe_fp8_device_error.argtypes = [C.POINTER(C.c_uint32)]
+        for name in ("moe_expert_lists", "moe_balance_forward", "moe_balance_backward", "moe_fp8_quantize",
+                     "moe_fp8_quantize_weights", "moe_fp8_matmul", "moe_fp8_wgrad", "moe_fp8_device_error"):
+            getattr(L, name).restype = C.c_int
         _lib = L
     return _lib
 
@@ -359,3 +382,247 @@ class MoeLayer:
             self.close()
         except Exception:
             pass
+
+
+# --- operators around the router and its experts ----------------------------------------------
+#
+# Thin calls of the handle-less C entry points (include/moe.h has each one's formula, limits and
+# layouts).  Tensors are checked for type, shape, layout and device here, since the C side sees
+# pointers only; what is not given as an argument is allocated by PyTorch on the call's stream.
+
+def _dtype_code(t, where, name):
+    import torch
+    code = {torch.float32: MOE_DTYPE_F32, torch.float16: MOE_DTYPE_F16, torch.bfloat16: MOE_DTYPE_BF16}.get(t.dtype)
+    if code is None:
+        raise MoeError(MOE_ERR_INVALID, where, f"{name}: need float32, float16 or bfloat16, got {t.dtype}")
+    return code
+
+
+class _Args:
+    """Checks of one call's tensors, and the stream that its allocations belong to."""
+
+    def __init__(self, where, first, stream):
+        import torch
+        self.where, self.torch, self.stream = where, torch, stream
+        if not isinstance(first, torch.Tensor) or not first.is_cuda:
+            self.fail("the tensors must be on a CUDA device")
+        self.device = first.device
+        if self.device.index != torch.cuda.current_device():
+            self.fail(f"the tensors are on {self.device}, the current device is cuda:{torch.cuda.current_device()}")
+        self.handle = _stream_handle(stream)
+
+    def fail(self, msg):
+        raise MoeError(MOE_ERR_INVALID, self.where, msg)
+
+    def tensor(self, t, name, dtypes, shape, rows=False):
+        """t of one of dtypes and of `shape` (None: any extent); contiguous, or (rows) each row so."""
+        if not isinstance(t, self.torch.Tensor) or t.device != self.device:
+            self.fail(f"{name}: need a tensor on {self.device}")
+        if dtypes is not None and t.dtype not in dtypes:
+            self.fail(f"{name}: need {' or '.join(map(str, dtypes))}, got {t.dtype}")
+        if t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape)):
+            self.fail(f"{name}: need shape {tuple('any' if w is None else w for w in shape)}, got {tuple(t.shape)}")
+        if not t.is_contiguous() and not (rows and t.stride(-1) == 1 and t.stride(0) >= t.shape[-1]):
+            self.fail(f"{name}: need {'contiguous rows' if rows else 'a contiguous tensor'}, got strides {t.stride()}")
+        return t
+
+    def row_stride(self, t):
+        return max(t.stride(0), t.shape[1]) if t.shape[0] > 1 else t.shape[1]
+
+    def empty(self, *specs):
+        """Tensors for (shape, dtype) each, allocated for the call's stream."""
+        torch = self.torch
+        if self.stream is None or self.handle == torch.cuda.current_stream(self.device).cuda_stream:
+            return [torch.empty(s, dtype=d, device=self.device) for s, d in specs]
+        on = torch.cuda.ExternalStream(self.handle, device=self.device) if self.handle else torch.cuda.default_stream(self.device)
+        with torch.cuda.stream(on):
+            return [torch.empty(s, dtype=d, device=self.device) for s, d in specs]
+
+
+def _int(a, v, name, lo=0):
+    if not isinstance(v, (int, np.integer)) or isinstance(v, bool) or not lo <= v < 1 << 31:
+        a.fail(f"{name}={v!r}: need an integer from {lo}")
+    return int(v)
+
+
+def moe_expert_lists(topk_idx, n_experts: int, align: int = 1, stream=None):
+    """Token lists of topk_idx [T, K] int32 (values outside [0, n_experts): dropped pairs).
+    -> counts [E], offsets [E + 1], rows [room] (token of each row, -1 in padding), pos [T, K]
+    (row of each pair, -1 for dropped ones), all int32."""
+    import torch
+    a = _Args("moe_expert_lists", topk_idx, stream)
+    T, K = a.tensor(topk_idx, "topk_idx", (torch.int32,), (None, None)).shape
+    E, align = _int(a, n_experts, "n_experts", 1), _int(a, align, "align", 1)
+    L = lib()
+    room = L.moe_expert_lists_rows(T, K, E, align)
+    if not 0 <= room < 1 << 31:
+        raise MoeError(MOE_ERR_UNSUPPORTED, a.where, f"{room} rows: need fewer than 2^31, and at least one choice a token")
+    need = L.moe_expert_lists_workspace(T, K, E)
+    i32 = torch.int32
+    counts, offsets, rows, pos, ws = a.empty(((E,), i32), ((E + 1,), i32), ((room,), i32), ((T, K), i32), ((need,), torch.uint8))
+    _check(L.moe_expert_lists(_ptr(topk_idx), T, K, E, align, _ptr(counts), _ptr(offsets), _ptr(rows), _ptr(pos), _ptr(ws), need,
+                              a.handle), a.where)
+    return counts, offsets, rows, pos
+
+
+def _balance_args(a, logits, seq_offsets, mask):
+    import torch
+    dt = _dtype_code(logits, a.where, "logits")
+    T, E = a.tensor(logits, "logits", None, (None, None), rows=True).shape
+    S = 1
+    if seq_offsets is not None:
+        S = a.tensor(seq_offsets, "seq_offsets", (torch.int32,), (None,)).shape[0] - 1
+    if mask is not None:
+        a.tensor(mask, "mask", (torch.bool, torch.uint8), (T,))
+    return dt, T, E, S
+
+
+def moe_balance_forward(logits, topk_idx, coef: float, score_func: int = MOE_SCORE_SIGMOID, seq_offsets=None, mask=None, stream=None):
+    """Balance loss of a router: logits [T, E] float32 / float16 / bfloat16 (rows may be strided),
+    topk_idx [T, K] int32, seq_offsets [S + 1] int32 (None: one sequence), mask [T] bool (False:
+    left out).  -> loss [1], counts [S, E] int32, prob_sums [S, E], tokens [S] int32."""
+    import torch
+    a = _Args("moe_balance_forward", logits, stream)
+    dt, T, E, S = _balance_args(a, logits, seq_offsets, mask)
+    K = a.tensor(topk_idx, "topk_idx", (torch.int32,), (T, None)).shape[1]
+    L = lib()
+    need = L.moe_balance_workspace(T, E, S)
+    i32, f32 = torch.int32, torch.float32
+    n = max(S, 0)
+    loss, counts, sums, tokens, ws = a.empty(((1,), f32), ((n, E), i32), ((n, E), f32), ((n,), i32), ((need,), torch.uint8))
+    _check(L.moe_balance_forward(_ptr(logits), dt, a.row_stride(logits), T, E, _ptr(topk_idx), K, score_func, coef, _ptr(seq_offsets), S,
+                                 _ptr(mask), _ptr(loss), _ptr(counts), _ptr(sums), _ptr(tokens), _ptr(ws), need, a.handle), a.where)
+    return loss, counts, sums, tokens
+
+
+def moe_balance_backward(logits, top_k: int, counts, tokens, coef: float, score_func: int = MOE_SCORE_SIGMOID, seq_offsets=None,
+                         mask=None, grad_loss=None, out=None, stream=None):
+    """Gradient of moe_balance_forward's loss with respect to logits, with its counts and tokens;
+    grad_loss [1] float32 (None: 1).  Rows outside every sequence of `out` (None: a new tensor)
+    stay as they are.  -> dlogits [T, E] in logits' dtype."""
+    import torch
+    a = _Args("moe_balance_backward", logits, stream)
+    dt, T, E, S = _balance_args(a, logits, seq_offsets, mask)
+    a.tensor(counts, "counts", (torch.int32,), (S, E))
+    a.tensor(tokens, "tokens", (torch.int32,), (S,))
+    if grad_loss is not None and a.tensor(grad_loss.reshape(-1), "grad_loss", (torch.float32,), (1,)) is None:
+        return None
+    if out is None:
+        out, = a.empty(((T, E), logits.dtype))
+    a.tensor(out, "out", (logits.dtype,), (T, E), rows=True)
+    _check(lib().moe_balance_backward(_ptr(logits), dt, a.row_stride(logits), T, E, _int(a, top_k, "top_k", 1), score_func, coef,
+                                      _ptr(counts), _ptr(tokens), _ptr(seq_offsets), S, _ptr(mask), _ptr(grad_loss), _ptr(out),
+                                      a.row_stride(out), a.handle), a.where)
+    return out
+
+
+def _f8(torch):
+    return (torch.float8_e4m3fn, torch.uint8)
+
+
+def _blocks(n: int) -> int:
+    return -(-n // 128)
+
+
+def moe_fp8_quantize(x, rows=None, transposed: bool = False, stream=None):
+    """e4m3 codes of x [T, width] (float32 / float16 / bfloat16; rows may be strided), or of its rows
+    rows [R] int32 (negative: zeros), with a power-of-two scale per 1 x 128 block.
+    -> codes [R, width] float8_e4m3fn, scales [ceil(width / 128), R]; with transposed also
+    codes_t [width, Rp], scales_t [Rp / 128, width], Rp = R rounded up to a multiple of 128."""
+    import torch
+    a = _Args("moe_fp8_quantize", x, stream)
+    dt = _dtype_code(x, a.where, "x")
+    T, n = a.tensor(x, "x", None, (None, None), rows=True).shape
+    R = T if rows is None else a.tensor(rows, "rows", (torch.int32,), (None,)).shape[0]
+    f8, f32, rb = torch.float8_e4m3fn, torch.float32, _blocks(R)
+    specs = [((R, n), f8), ((_blocks(n), R), f32)] + ([((n, rb * 128), f8), ((rb, n), f32)] if transposed else [])
+    out = a.empty(*specs)
+    ct, st = (out[2], out[3]) if transposed and R else (None, None)
+    _check(lib().moe_fp8_quantize(_ptr(x), dt, a.row_stride(x), T, n, _ptr(rows), R, _ptr(out[0]), _ptr(out[1]), _ptr(ct), _ptr(st),
+                                  a.handle), a.where)
+    return tuple(out)
+
+
+def moe_fp8_quantize_weights(w, transposed: bool = False, stream=None):
+    """e4m3 codes of weights w [E, N, K] or [N, K], one scale per 128 x 128 block.
+    -> codes, scales [(E,) ceil(N / 128), ceil(K / 128)]; with transposed also the transposed
+    matrices' codes and scales."""
+    import torch
+    a = _Args("moe_fp8_quantize_weights", w, stream)
+    dt = _dtype_code(w, a.where, "w")
+    a.tensor(w, "w", None, (None,) * (2 if w.dim() == 2 else 3))
+    lead, (N, K) = tuple(w.shape[:-2]), w.shape[-2:]
+    f8, f32 = torch.float8_e4m3fn, torch.float32
+    specs = [(lead + (N, K), f8), (lead + (_blocks(N), _blocks(K)), f32)]
+    if transposed:
+        specs += [(lead + (K, N), f8), (lead + (_blocks(K), _blocks(N)), f32)]
+    out = a.empty(*specs)
+    ct, st = out[2:] if transposed else (None, None)
+    _check(lib().moe_fp8_quantize_weights(_ptr(w), dt, lead[0] if lead else 1, N, K, _ptr(out[0]), _ptr(out[1]), _ptr(ct), _ptr(st),
+                                          a.handle), a.where)
+    return tuple(out)
+
+
+def moe_fp8_matmul(x, x_scale, w, w_scale, offsets=None, out=None, out_dtype=None, stream=None):
+    """y [R, N] = x w^T of e4m3 codes x [R, K], w [E, N, K] or [N, K] with their block scales
+    x_scale [ceil(K / 128), R], w_scale [(E,) ceil(N / 128), ceil(K / 128)]; offsets [E + 1] int32:
+    row r is multiplied with the expert whose segment holds it, other rows of `out` stay as they
+    are (None: one weight matrix).  out_dtype (bfloat16 by default) or out's type."""
+    import torch
+    a = _Args("moe_fp8_matmul", x, stream)
+    R, K = a.tensor(x, "x", _f8(torch), (None, None)).shape
+    E = 1
+    if w.dim() == 2 or offsets is None:
+        if w.dim() == 3 and w.shape[0] != 1 or offsets is not None:
+            a.fail("w [E, N, K] and offsets belong together")
+        w, w_scale = w.view(w.shape[-2:]), w_scale.view(w_scale.shape[-2:])
+        N = a.tensor(w, "w", _f8(torch), (None, K)).shape[0]
+        a.tensor(w_scale, "w_scale", (torch.float32,), (_blocks(N), _blocks(K)))
+    else:
+        E, N = a.tensor(w, "w", _f8(torch), (None, None, K)).shape[:2]
+        a.tensor(w_scale, "w_scale", (torch.float32,), (E, _blocks(N), _blocks(K)))
+        a.tensor(offsets, "offsets", (torch.int32,), (E + 1,))
+    a.tensor(x_scale, "x_scale", (torch.float32,), (_blocks(K), R))
+    if out is None:
+        out, = a.empty(((R, N), out_dtype or torch.bfloat16))
+    elif out_dtype is not None and out.dtype != out_dtype:
+        a.fail(f"out is {out.dtype}, out_dtype {out_dtype}")
+    a.tensor(out, "out", None, (R, N), rows=True)
+    _check(lib().moe_fp8_matmul(_ptr(x), _ptr(x_scale), R, _ptr(w), _ptr(w_scale), E, N, K, _ptr(offsets), _ptr(out),
+                                _dtype_code(out, a.where, "out"), a.row_stride(out), a.handle), a.where)
+    return out
+
+
+def moe_fp8_wgrad(xt, xt_scale, dyt, dyt_scale, offsets=None, out=None, out_dtype=None, stream=None):
+    """Weight gradients from column-quantised x and dy (moe_fp8_quantize(..., transposed=True)):
+    xt [K, R], dyt [N, R] codes, R a multiple of 128, xt_scale [R / 128, K], dyt_scale [R / 128, N];
+    offsets [E + 1] int32, multiples of 128 (None: one matrix).
+    -> dw [E, N, K] ([N, K] without offsets), float32 by default."""
+    import torch
+    a = _Args("moe_fp8_wgrad", xt, stream)
+    K, R = a.tensor(xt, "xt", _f8(torch), (None, None)).shape
+    N = a.tensor(dyt, "dyt", _f8(torch), (None, R)).shape[0]
+    a.tensor(xt_scale, "xt_scale", (torch.float32,), (R // 128, K))
+    a.tensor(dyt_scale, "dyt_scale", (torch.float32,), (R // 128, N))
+    E = 1 if offsets is None else a.tensor(offsets, "offsets", (torch.int32,), (None,)).shape[0] - 1
+    shape = (N, K) if offsets is None else (E, N, K)
+    if out is None:
+        if E < 1:
+            a.fail("offsets: need at least two entries")
+        out, = a.empty((shape, out_dtype or torch.float32))
+    elif out_dtype is not None and out.dtype != out_dtype:
+        a.fail(f"out is {out.dtype}, out_dtype {out_dtype}")
+    a.tensor(out, "out", None, shape)
+    _check(lib().moe_fp8_wgrad(_ptr(xt), _ptr(xt_scale), _ptr(dyt), _ptr(dyt_scale), R, N, K, E, _ptr(offsets), _ptr(out),
+                               _dtype_code(out, a.where, "out"), a.handle), a.where)
+    return out
+
+
+def moe_fp8_device_error(check: bool = True) -> int:
+    """Error flags of the block-scaled products on the current device since the last check (0: none);
+    raises if any, unless check is False.  Waits for the device."""
+    f = C.c_uint32()
+    st = lib().moe_fp8_device_error(C.byref(f))
+    if check or st != MOE_ERR_CUDA or f.value == 0:
+        _check(st, "moe_fp8_device_error")
+    return f.value

@@ -472,4 +472,191 @@ moe_status moe_destroy(moe_handle *h) {
     return MOE_OK;
 }
 
+
+// --- operators around the router and its experts (no handle) ---------------
+
+#define MOE_NEED(cond, status, ...) \
+    do { if (!(cond)) return fail(status, __VA_ARGS__); } while (0)
+
+static bool dtype_ok(int32_t d) { return d == MOE_DTYPE_F32 || d == MOE_DTYPE_F16 || d == MOE_DTYPE_BF16; }
+static bool aligned4(const void *ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 3u) == 0; }
+static bool aligned_el(const void *ptr, int32_t dtype) {
+    return (reinterpret_cast<uintptr_t>(ptr) & (dtype == MOE_DTYPE_F32 ? 3u : 1u)) == 0;
+}
+static moe_status launched(cudaError_t e, const char *what) { return e == cudaSuccess ? MOE_OK : cuda_fail(e, what); }
+
+int64_t moe_expert_lists_rows(int32_t T, int32_t top_k, int32_t n_experts, int32_t align) {
+    if (T < 0 || top_k < 1 || n_experts < 1 || align < 1) return -1;
+    const int64_t pairs = (int64_t)T * top_k, most = pairs < n_experts ? pairs : n_experts;
+    return (pairs + most * (align - 1) + align - 1) / align * align;
+}
+
+size_t moe_expert_lists_workspace(int32_t T, int32_t top_k, int32_t n_experts) {
+    if (T < 0 || top_k < 1 || n_experts < 1) return 0;
+    return moe::lists_workspace((long long)T * top_k, n_experts);
+}
+
+moe_status moe_expert_lists(const int32_t *topk_idx, int32_t T, int32_t top_k, int32_t n_experts, int32_t align,
+                            int32_t *counts, int32_t *offsets, int32_t *rows, int32_t *pos, void *workspace,
+                            size_t workspace_bytes, void *stream) {
+    MOE_NEED(T >= 0, MOE_ERR_INVALID, "T=%d is negative", T);
+    MOE_NEED(n_experts >= 1 && n_experts <= 1024, MOE_ERR_UNSUPPORTED, "n_experts=%d: need 1..1024", n_experts);
+    MOE_NEED(top_k >= 1 && top_k <= 1024, MOE_ERR_UNSUPPORTED, "top_k=%d: need 1..1024", top_k);
+    MOE_NEED(align >= 1 && align <= 4096, MOE_ERR_UNSUPPORTED, "align=%d: need 1..4096", align);
+    const int64_t room = moe_expert_lists_rows(T, top_k, n_experts, align);
+    MOE_NEED(room < (1ll << 31), MOE_ERR_UNSUPPORTED, "%lld rows: need fewer than 2^31", (long long)room);
+    MOE_NEED(counts && offsets, MOE_ERR_INVALID, "counts / offsets is NULL");
+    MOE_NEED(T == 0 || (topk_idx && rows && pos), MOE_ERR_INVALID, "topk_idx / rows / pos is NULL");
+    MOE_NEED(aligned4(topk_idx) && aligned4(counts) && aligned4(offsets) && aligned4(rows) && aligned4(pos),
+             MOE_ERR_INVALID, "int32 buffers must be 4-byte aligned");
+    const size_t need = moe_expert_lists_workspace(T, top_k, n_experts);
+    MOE_NEED(need == 0 || (workspace && aligned16(workspace) && workspace_bytes >= need), MOE_ERR_INVALID,
+             "workspace: need %zu bytes, 16-byte aligned", need);
+    return launched(moe::launch_lists(topk_idx, T, top_k, n_experts, align, room, counts, offsets, rows, pos, workspace,
+                                      static_cast<cudaStream_t>(stream)), "moe_expert_lists");
+}
+
+static moe_status check_balance(const void *logits, int32_t dtype, int64_t ld, int32_t T, int32_t E, int32_t top_k,
+                                int32_t score_func, float coef, const int32_t *seq, int32_t n_seq) {
+    MOE_NEED(dtype_ok(dtype), MOE_ERR_INVALID, "dtype=%d: need a MOE_DTYPE_* value", dtype);
+    MOE_NEED(T >= 0, MOE_ERR_INVALID, "T=%d is negative", T);
+    MOE_NEED(E >= 1 && E <= 1024, MOE_ERR_UNSUPPORTED, "n_experts=%d: need 1..1024", E);
+    MOE_NEED(top_k >= 1 && top_k <= E, MOE_ERR_INVALID, "top_k=%d: need 1..n_experts", top_k);
+    MOE_NEED(ld >= E, MOE_ERR_INVALID, "ld=%lld: need n_experts or more", (long long)ld);
+    MOE_NEED(score_func == MOE_SCORE_SIGMOID || score_func == MOE_SCORE_SOFTMAX, MOE_ERR_INVALID,
+             "score_func=%d: need MOE_SCORE_SIGMOID or MOE_SCORE_SOFTMAX", score_func);
+    MOE_NEED(isfinite(coef), MOE_ERR_INVALID, "coef is not finite");
+    MOE_NEED(n_seq >= 1 && n_seq <= 65535, MOE_ERR_UNSUPPORTED, "n_seq=%d: need 1..65535", n_seq);
+    MOE_NEED(seq || n_seq == 1, MOE_ERR_INVALID, "n_seq=%d without seq_offsets", n_seq);
+    MOE_NEED(T == 0 || logits, MOE_ERR_INVALID, "logits is NULL");
+    MOE_NEED(aligned_el(logits, dtype) && aligned4(seq), MOE_ERR_INVALID, "logits / seq_offsets are not aligned to their elements");
+    return MOE_OK;
+}
+
+size_t moe_balance_workspace(int32_t T, int32_t n_experts, int32_t n_seq) {
+    if (T < 0 || n_experts < 1 || n_seq < 1) return 0;
+    return moe::balance_workspace(T, n_experts, n_seq);
+}
+
+moe_status moe_balance_forward(const void *logits, int32_t dtype, int64_t ld, int32_t T, int32_t n_experts,
+                               const int32_t *topk_idx, int32_t top_k, int32_t score_func, float coef,
+                               const int32_t *seq_offsets, int32_t n_seq, const uint8_t *mask, float *loss,
+                               int32_t *counts, float *prob_sums, int32_t *tokens, void *workspace,
+                               size_t workspace_bytes, void *stream) {
+    const moe_status s = check_balance(logits, dtype, ld, T, n_experts, top_k, score_func, coef, seq_offsets, n_seq);
+    if (s != MOE_OK) return s;
+    MOE_NEED(T == 0 || topk_idx, MOE_ERR_INVALID, "topk_idx is NULL");
+    MOE_NEED(loss && counts && prob_sums && tokens, MOE_ERR_INVALID, "an output is NULL");
+    MOE_NEED(aligned4(topk_idx) && aligned4(loss) && aligned4(counts) && aligned4(prob_sums) && aligned4(tokens),
+             MOE_ERR_INVALID, "int32 / float32 buffers must be 4-byte aligned");
+    const size_t need = moe_balance_workspace(T, n_experts, n_seq);
+    MOE_NEED(workspace && aligned16(workspace) && workspace_bytes >= need, MOE_ERR_INVALID,
+             "workspace: need %zu bytes, 16-byte aligned", need);
+    return launched(moe::launch_balance_forward(logits, dtype, ld, T, n_experts, topk_idx, top_k, score_func == MOE_SCORE_SOFTMAX,
+                                                coef, seq_offsets, n_seq, mask, loss, counts, prob_sums, tokens, workspace,
+                                                static_cast<cudaStream_t>(stream)), "moe_balance_forward");
+}
+
+moe_status moe_balance_backward(const void *logits, int32_t dtype, int64_t ld, int32_t T, int32_t n_experts, int32_t top_k,
+                                int32_t score_func, float coef, const int32_t *counts, const int32_t *tokens,
+                                const int32_t *seq_offsets, int32_t n_seq, const uint8_t *mask, const float *grad_loss,
+                                void *dlogits, int64_t ldd, void *stream) {
+    const moe_status s = check_balance(logits, dtype, ld, T, n_experts, top_k, score_func, coef, seq_offsets, n_seq);
+    if (s != MOE_OK) return s;
+    MOE_NEED(counts && tokens, MOE_ERR_INVALID, "counts / tokens is NULL");
+    MOE_NEED(ldd >= n_experts, MOE_ERR_INVALID, "ldd=%lld: need n_experts or more", (long long)ldd);
+    MOE_NEED(aligned4(counts) && aligned4(tokens) && aligned4(grad_loss) && aligned_el(dlogits, dtype), MOE_ERR_INVALID,
+             "a buffer is not aligned to its elements");
+    if (T == 0) return MOE_OK;
+    MOE_NEED(dlogits, MOE_ERR_INVALID, "dlogits is NULL");
+    return launched(moe::launch_balance_backward(logits, dtype, ld, T, n_experts, top_k, score_func == MOE_SCORE_SOFTMAX, coef,
+                                                 counts, tokens, seq_offsets, n_seq, mask, grad_loss, dlogits, ldd,
+                                                 static_cast<cudaStream_t>(stream)), "moe_balance_backward");
+}
+
+static const int32_t kMaxWidth = 131072, kMaxRows = 65535 * 128;
+
+moe_status moe_fp8_quantize(const void *x, int32_t dtype, int64_t ld, int32_t n_tokens, int32_t width, const int32_t *rows,
+                            int32_t R, uint8_t *codes, float *scales, uint8_t *codes_t, float *scales_t, void *stream) {
+    MOE_NEED(dtype_ok(dtype), MOE_ERR_INVALID, "dtype=%d: need a MOE_DTYPE_* value", dtype);
+    MOE_NEED(n_tokens >= 0 && R >= 0, MOE_ERR_INVALID, "n_tokens=%d, R=%d: negative", n_tokens, R);
+    MOE_NEED(rows || R == n_tokens, MOE_ERR_INVALID, "R=%d without rows: need n_tokens=%d", R, n_tokens);
+    MOE_NEED(width >= 16 && width <= kMaxWidth && width % 16 == 0, MOE_ERR_UNSUPPORTED,
+             "width=%d: need a multiple of 16 in 16..%d", width, kMaxWidth);
+    MOE_NEED(R <= kMaxRows, MOE_ERR_UNSUPPORTED, "R=%d: need %d or fewer", R, kMaxRows);
+    MOE_NEED(ld >= width, MOE_ERR_INVALID, "ld=%lld: need width or more", (long long)ld);
+    MOE_NEED((codes_t == nullptr) == (scales_t == nullptr), MOE_ERR_INVALID, "codes_t and scales_t: give both or neither");
+    if (R == 0) return MOE_OK;
+    MOE_NEED((x || n_tokens == 0) && codes && scales, MOE_ERR_INVALID, "x / codes / scales is NULL");
+    MOE_NEED(aligned16(x) && ld * (dtype == MOE_DTYPE_F32 ? 4 : 2) % 16 == 0, MOE_ERR_INVALID,
+             "every row of x must start on a 16-byte boundary");
+    MOE_NEED(aligned16(codes) && aligned16(codes_t) && aligned4(scales) && aligned4(scales_t) && aligned4(rows), MOE_ERR_INVALID,
+             "code buffers must be 16-byte aligned, scales and rows 4-byte aligned");
+    return launched(moe::launch_quantize(x, dtype, ld, n_tokens, width, rows, R, codes, scales, codes_t, scales_t,
+                                         static_cast<cudaStream_t>(stream)), "moe_fp8_quantize");
+}
+
+moe_status moe_fp8_quantize_weights(const void *w, int32_t dtype, int32_t E, int32_t N, int32_t K, uint8_t *codes, float *scales,
+                                    uint8_t *codes_t, float *scales_t, void *stream) {
+    MOE_NEED(dtype_ok(dtype), MOE_ERR_INVALID, "dtype=%d: need a MOE_DTYPE_* value", dtype);
+    MOE_NEED(E >= 1 && E <= 65535, MOE_ERR_UNSUPPORTED, "E=%d: need 1..65535", E);
+    MOE_NEED(N >= 1 && N <= kMaxWidth, MOE_ERR_UNSUPPORTED, "N=%d: need 1..%d", N, kMaxWidth);
+    MOE_NEED(K >= 16 && K <= kMaxWidth && K % 16 == 0, MOE_ERR_UNSUPPORTED, "K=%d: need a multiple of 16 in 16..%d", K, kMaxWidth);
+    MOE_NEED((codes_t == nullptr) == (scales_t == nullptr), MOE_ERR_INVALID, "codes_t and scales_t: give both or neither");
+    MOE_NEED(w && codes && scales, MOE_ERR_INVALID, "w / codes / scales is NULL");
+    MOE_NEED(aligned16(w) && aligned16(codes) && aligned16(codes_t) && aligned4(scales) && aligned4(scales_t), MOE_ERR_INVALID,
+             "w and the code buffers must be 16-byte aligned, scales 4-byte aligned");
+    return launched(moe::launch_quantize_weights(w, dtype, E, N, K, codes, scales, codes_t, scales_t,
+                                                 static_cast<cudaStream_t>(stream)), "moe_fp8_quantize_weights");
+}
+
+moe_status moe_fp8_matmul(const uint8_t *x, const float *x_scale, int32_t R, const uint8_t *w, const float *w_scale, int32_t E,
+                          int32_t N, int32_t K, const int32_t *offsets, void *y, int32_t y_dtype, int64_t ldy, void *stream) {
+    MOE_NEED(dtype_ok(y_dtype), MOE_ERR_INVALID, "y_dtype=%d: need a MOE_DTYPE_* value", y_dtype);
+    MOE_NEED(R >= 0, MOE_ERR_INVALID, "R=%d is negative", R);
+    MOE_NEED(R <= kMaxRows, MOE_ERR_UNSUPPORTED, "R=%d: need %d or fewer", R, kMaxRows);
+    MOE_NEED(E >= 1 && E <= 1024, MOE_ERR_UNSUPPORTED, "E=%d: need 1..1024", E);
+    MOE_NEED(offsets || E == 1, MOE_ERR_INVALID, "E=%d without offsets", E);
+    MOE_NEED(N >= 1 && N <= kMaxWidth, MOE_ERR_UNSUPPORTED, "N=%d: need 1..%d", N, kMaxWidth);
+    MOE_NEED(K >= 16 && K <= kMaxWidth && K % 16 == 0, MOE_ERR_UNSUPPORTED, "K=%d: need a multiple of 16 in 16..%d", K, kMaxWidth);
+    MOE_NEED(ldy >= N, MOE_ERR_INVALID, "ldy=%lld: need N or more", (long long)ldy);
+    if (R == 0) return MOE_OK;
+    MOE_NEED(x && x_scale && w && w_scale && y, MOE_ERR_INVALID, "a pointer is NULL");
+    MOE_NEED(aligned16(x) && aligned16(w) && aligned4(x_scale) && aligned4(w_scale) && aligned4(offsets) && aligned_el(y, y_dtype),
+             MOE_ERR_INVALID, "codes must be 16-byte aligned, the other buffers to their elements");
+    return launched(moe::launch_fp8_matmul(x, x_scale, R, w, w_scale, E, N, K, offsets, y, y_dtype, ldy,
+                                           static_cast<cudaStream_t>(stream)), "moe_fp8_matmul");
+}
+
+moe_status moe_fp8_wgrad(const uint8_t *xt, const float *xt_scale, const uint8_t *dyt, const float *dyt_scale, int32_t R,
+                         int32_t N, int32_t K, int32_t E, const int32_t *offsets, void *dw, int32_t dw_dtype, void *stream) {
+    MOE_NEED(dtype_ok(dw_dtype), MOE_ERR_INVALID, "dw_dtype=%d: need a MOE_DTYPE_* value", dw_dtype);
+    MOE_NEED(R >= 0 && R % 128 == 0, MOE_ERR_INVALID, "R=%d: need a multiple of 128", R);
+    MOE_NEED(R <= kMaxRows, MOE_ERR_UNSUPPORTED, "R=%d: need %d or fewer", R, kMaxRows);
+    MOE_NEED(E >= 1 && E <= 1024, MOE_ERR_UNSUPPORTED, "E=%d: need 1..1024", E);
+    MOE_NEED(offsets || E == 1, MOE_ERR_INVALID, "E=%d without offsets", E);
+    MOE_NEED(N >= 1 && N <= kMaxWidth && K >= 1 && K <= kMaxWidth, MOE_ERR_UNSUPPORTED, "N=%d, K=%d: need 1..%d", N, K, kMaxWidth);
+    MOE_NEED(dw && aligned_el(dw, dw_dtype), MOE_ERR_INVALID, "dw is NULL or not aligned to its elements");
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (R == 0)
+        return launched(cudaMemsetAsync(dw, 0, (size_t)E * N * K * (dw_dtype == MOE_DTYPE_F32 ? 4 : 2), st), "moe_fp8_wgrad");
+    MOE_NEED(xt && xt_scale && dyt && dyt_scale, MOE_ERR_INVALID, "a pointer is NULL");
+    MOE_NEED(aligned16(xt) && aligned16(dyt) && aligned4(xt_scale) && aligned4(dyt_scale) && aligned4(offsets), MOE_ERR_INVALID,
+             "codes must be 16-byte aligned, scales and offsets 4-byte aligned");
+    return launched(moe::launch_fp8_wgrad(xt, xt_scale, dyt, dyt_scale, R, N, K, E, offsets, dw, dw_dtype, st), "moe_fp8_wgrad");
+}
+
+moe_status moe_fp8_device_error(uint32_t *flags) {
+    MOE_NEED(flags, MOE_ERR_INVALID, "flags is NULL");
+    *flags = 0;
+    unsigned f = 0;
+    const cudaError_t e = moe::fp8_error_read(&f);
+    if (e != cudaSuccess) return cuda_fail(e, "reading the device error word");
+    *flags = f;
+    MOE_NEED(f == 0, MOE_ERR_CUDA, "device error word 0x%x: a pipeline wait of a block-scaled product ran out", f);
+    return MOE_OK;
+}
+
+#undef MOE_NEED
+
 }  // extern "C"

@@ -133,4 +133,27 @@ cudaError_t launch_decode_fast(const Params &p, const float *x, float *y, cudaSt
 cudaError_t launch_forward(const Params &p, const float *x, int T, float *y, cudaStream_t stream,
                            bool want_buckets, cudaEvent_t *ev);
 
+// Token lists and the balance loss (moe_route_ops.cu).
+size_t lists_workspace(long long pairs, int E);
+cudaError_t launch_lists(const int *idx, int T, int K, int E, int align, long long room, int *counts, int *offsets,
+                         int *rows, int *pos, void *ws, cudaStream_t st);
+size_t balance_workspace(int T, int E, int S);
+cudaError_t launch_balance_forward(const void *logits, int dtype, long long ld, int T, int E, const int *idx, int K,
+                                   int softmax, float coef, const int *seq, int S, const uint8_t *mask, float *loss,
+                                   int *counts, float *sums, int *tokens, void *ws, cudaStream_t st);
+cudaError_t launch_balance_backward(const void *logits, int dtype, long long ld, int T, int E, int K, int softmax,
+                                    float coef, const int *counts, const int *tokens, const int *seq, int S,
+                                    const uint8_t *mask, const float *grad, void *dlogits, long long ldd, cudaStream_t st);
+
+// Block-scaled e4m3 quantisers and products (moe_fp8.cu).
+cudaError_t launch_quantize(const void *x, int dtype, long long ld, int n_src, int width, const int *rows, int R,
+                            uint8_t *codes, float *scales, uint8_t *codes_t, float *scales_t, cudaStream_t st);
+cudaError_t launch_quantize_weights(const void *w, int dtype, int E, int N, int K, uint8_t *codes, float *scales,
+                                    uint8_t *codes_t, float *scales_t, cudaStream_t st);
+cudaError_t launch_fp8_matmul(const uint8_t *x, const float *xs, int R, const uint8_t *w, const float *ws, int E, int N, int K,
+                              const int *offsets, void *y, int y_dtype, long long ldy, cudaStream_t st);
+cudaError_t launch_fp8_wgrad(const uint8_t *xt, const float *xs, const uint8_t *dyt, const float *dys, int R, int N, int K, int E,
+                             const int *offsets, void *dw, int dw_dtype, cudaStream_t st);
+cudaError_t fp8_error_read(unsigned *flags);
+
 }  // namespace moe

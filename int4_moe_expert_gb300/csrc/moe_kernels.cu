@@ -23,6 +23,7 @@
 #include <vector>
 
 #include "moe_internal.h"
+#include "moe_ptx.h"
 
 namespace moe {
 
@@ -1036,9 +1037,6 @@ constexpr int kMmaBBytes = kMmaItemMax * kMmaBLd * 2;
 constexpr int kMmaStageBytes = kMmaABytes + kMmaBBytes;
 constexpr size_t kMmaSmem = (size_t)kMmaStages * kMmaStageBytes;
 
-__device__ __forceinline__ uint32_t smem_u32(const void *ptr) {
-    return static_cast<uint32_t>(__cvta_generic_to_shared(ptr));
-}
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -1398,7 +1396,6 @@ constexpr size_t kTcSmem = (size_t)kTcS * kTcBTile + (size_t)kTcR * kTcRawSlot +
 constexpr unsigned kErrTc = MOE_DEVICE_ERR_TC;
 // kind::f16: D f32 (bits 4-5 = 1), A and B f16 (0), both K-major (0), N >> 3 at bit 17, M >> 4 at bit 24
 constexpr uint32_t kTcIdesc = (1u << 4) | ((uint32_t)(kTcTok >> 3) << 17) | ((128u >> 4) << 24);
-constexpr unsigned long long kTcWaitNs = 500ull * 1000 * 1000;
 static_assert(kTcSmem + 1024 <= 227 * 1024, "both rings and the static arrays fit one block's shared memory");
 static_assert(kTcTiles == 2, "one MMA-issuing warp per tile: warps 0 and 1");
 static_assert(kTcTiles * kTcTok + kTcS * kTcACols <= kTcCols, "accumulators and the A ring fit the allocation");
@@ -1410,46 +1407,6 @@ static_assert(kTcRows / 32 == 8 && kTcDq0 % 4 == 0, "eight dequantising warps co
 __device__ __forceinline__ uint64_t tc_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
     return (uint64_t)((saddr >> 4) & 0x3FFF) | ((uint64_t)(lbo >> 4) << 16) |
            ((uint64_t)(sbo >> 4) << 32) | (1ull << 46);
-}
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-    return ok != 0;
-}
-__device__ __forceinline__ unsigned long long tc_now() {
-    unsigned long long t;
-    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-    return t;
-}
-// wait (bounded) for phase `parity` of an mbarrier; false when the wait ran out
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
-    if (mbar_try(bar, parity)) return true;
-    const unsigned long long t0 = tc_now();
-    for (;;) {
-        for (int i = 0; i < 64; i++)
-            if (mbar_try(bar, parity)) return true;
-        if (tc_now() - t0 > kTcWaitNs) return false;
-    }
-}
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-// this thread's arrival, announcing `bytes` of tensor copies that complete the phase
-__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-// 2-D tensor copy global -> shared (box of the tensor map at element x, row y; rows outside the
-// tensor read as zeros), counted on the mbarrier
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const void *map, int x, int y, uint32_t bar) {
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-                 ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
 }
 __device__ __forceinline__ void tc_ld16(uint32_t taddr, float (&v)[16]) {
     uint32_t r[16];

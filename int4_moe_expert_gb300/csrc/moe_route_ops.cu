@@ -1,0 +1,584 @@
+// Router operators around a choice of experts: token lists per expert, and the balance loss with
+// its gradient.  No per-call state outside the caller's buffers, no atomics on floats: results are
+// the same bits every run.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "moe_internal.h"
+
+namespace moe {
+namespace {
+
+// ---------------------------------------------------------------------------
+// Token lists.  A stable counting sort of the pairs (t, k) by expert: every block owns a contiguous
+// range of pairs, every warp of a block a contiguous part of it, so that a pair's place is its
+// expert's offset + the expert's pairs in earlier blocks + in earlier warps + earlier in the warp.
+// Bound by latency (one launch for up to kListsOne pairs, else two: every block adds up the other
+// blocks' counts from L2 itself, which costs less than a third launch).
+// ---------------------------------------------------------------------------
+
+constexpr int kListThreads = 1024;
+constexpr int kListWarps = kListThreads / 32;
+constexpr int kListsOne = 8192;         // pairs that one block sorts alone
+constexpr int kListsMin = 2048;         // pairs per block otherwise, at least
+constexpr int kListsBlocks = 148;       // blocks, at most
+
+struct ListArgs {
+    const int *idx;
+    int *counts, *offsets, *rows, *pos;
+    int *hist;          // [blocks][E] (more than one block)
+    long long pairs, room;
+    int K, E, align, chunk, blocks;
+};
+
+__device__ __forceinline__ int pair_expert(const ListArgs &p, long long i, long long end) {
+    const int e = i < end ? __ldg(p.idx + i) : -1;
+    return (unsigned)e < (unsigned)p.E ? e : -1;
+}
+
+__global__ void __launch_bounds__(kListThreads) lists_count_kernel(const ListArgs p) {
+    extern __shared__ int h[];
+    for (int e = threadIdx.x; e < p.E; e += kListThreads) h[e] = 0;
+    __syncthreads();
+    const long long lo = (long long)blockIdx.x * p.chunk, hi = min(lo + p.chunk, p.pairs);
+    for (long long i = lo + threadIdx.x; i < hi; i += kListThreads) {
+        const int e = pair_expert(p, i, hi);
+        if (e >= 0) atomicAdd(&h[e], 1);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < p.E; e += kListThreads) p.hist[(size_t)blockIdx.x * p.E + e] = h[e];
+}
+
+__global__ void __launch_bounds__(kListThreads) lists_kernel(const ListArgs p) {
+    extern __shared__ int sm[];
+    int *h = sm;                              // [warps][E] pairs of each warp, then each warp's next place
+    int *off = sm + kListWarps * p.E;         // [E + 1]
+    int *before = off + p.E + 1;              // [E] this expert's pairs in earlier blocks
+    int *total = before + p.E;                // [E]
+    __shared__ int s_run;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const bool one = p.blocks == 1;
+    for (int i = tid; i < kListWarps * p.E; i += kListThreads) h[i] = 0;
+    for (int e = tid; e < p.E; e += kListThreads) before[e] = total[e] = 0;
+    __syncthreads();
+    const long long lo = (long long)blockIdx.x * p.chunk, hi = min(lo + p.chunk, p.pairs);
+    const int part = ((p.chunk + kListWarps - 1) / kListWarps + 31) & ~31;   // pairs of a warp
+    const long long wlo = lo + (long long)warp * part, whi = min(wlo + part, hi);
+    int *hw = h + warp * p.E;
+    for (long long i = wlo; i < whi; i += 32) {
+        const int e = pair_expert(p, i + lane, whi);
+        const unsigned same = __match_any_sync(0xffffffffu, e);
+        if (e >= 0 && lane == __ffs(same) - 1) hw[e] += __popc(same);
+        __syncwarp();
+    }
+    if (!one) {
+        // counts of the other blocks: thread = (expert, part of the blocks)
+        const int groups = p.E >= kListThreads ? 1 : kListThreads / p.E;
+        for (int i = tid; i < groups * p.E; i += kListThreads) {
+            const int e = i % p.E, g = i / p.E;
+            int b4 = 0, all = 0;
+#pragma unroll 4
+            for (int b = g; b < p.blocks; b += groups) {
+                const int v = p.hist[(size_t)b * p.E + e];
+                all += v;
+                if (b < (int)blockIdx.x) b4 += v;
+            }
+            if (b4) atomicAdd(&before[e], b4);
+            if (all) atomicAdd(&total[e], all);
+        }
+    }
+    __syncthreads();
+    if (one) {
+        for (int e = tid; e < p.E; e += kListThreads) {
+            int n = 0;
+            for (int w = 0; w < kListWarps; w++) n += h[w * p.E + e];
+            total[e] = n;
+        }
+        __syncthreads();
+    }
+    // offsets: running sum of the padded counts, 32 experts at a time
+    if (warp == 0) {
+        int run = 0;
+        for (int e0 = 0; e0 < p.E; e0 += 32) {
+            const int n = e0 + lane < p.E ? total[e0 + lane] : 0;
+            int v = (n + p.align - 1) / p.align * p.align;
+            const int own = v;
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const int u = __shfl_up_sync(0xffffffffu, v, d);
+                if (lane >= d) v += u;
+            }
+            if (e0 + lane < p.E) off[e0 + lane] = run + v - own;
+            run += __shfl_sync(0xffffffffu, v, 31);
+        }
+        if (lane == 0) {
+            off[p.E] = run;
+            s_run = run;
+        }
+    }
+    __syncthreads();
+    for (int e = tid; e < p.E; e += kListThreads) {
+        int at = off[e] + before[e];
+        for (int w = 0; w < kListWarps; w++) {
+            const int n = h[w * p.E + e];
+            h[w * p.E + e] = at;
+            at += n;
+        }
+        if (blockIdx.x == 0) {
+            p.counts[e] = total[e];
+            p.offsets[e] = off[e];
+        }
+    }
+    if (blockIdx.x == 0 && tid == 0) p.offsets[p.E] = s_run;
+    __syncthreads();
+    for (long long i = wlo; i < whi; i += 32) {
+        const int e = pair_expert(p, i + lane, whi);
+        const unsigned same = __match_any_sync(0xffffffffu, e);
+        const int leader = __ffs(same) - 1;
+        int at = 0;
+        if (e >= 0 && lane == leader) {
+            at = hw[e];
+            hw[e] = at + __popc(same);
+        }
+        at = __shfl_sync(0xffffffffu, at, leader) + __popc(same & ((1u << lane) - 1u));
+        if (i + lane < whi) {
+            p.pos[i + lane] = e >= 0 ? at : -1;
+            if (e >= 0) p.rows[at] = (int)((i + lane) / p.K);
+        }
+        __syncwarp();
+    }
+    // rows without a token: behind each expert's pairs (its block's warps) and behind the last segment
+    for (int e = (int)blockIdx.x * kListWarps + warp; e < p.E; e += p.blocks * kListWarps)
+        for (int r = off[e] + total[e] + lane; r < off[e + 1]; r += 32) p.rows[r] = -1;
+    for (long long r = off[p.E] + (long long)blockIdx.x * kListThreads + tid; r < p.room; r += (long long)p.blocks * kListThreads)
+        p.rows[r] = -1;
+}
+
+// ---------------------------------------------------------------------------
+// Balance loss.  For the segment (sequence) s of n_s unmasked tokens, with p_te the router's
+// normalised score (softmax(l), or sigma(l) / (sum_e sigma(l) + 1e-20)) and c_se the number of the
+// segment's choices that fell on expert e:
+//     L = coef / S  sum_s  E / (K n_s^2)  sum_e c_se sum_t p_te
+//     dL / dl_te = coef E / (S K n_s^2) p_te (c_se - sum_j p_tj c_sj)  [x (1 - sigma_te), sigmoid]
+// (the counts are constants).  Memory-bound: the forward reads the logits once, keeps each block's
+// sums per expert in registers and adds the blocks' sums in block order; the gradient needs every
+// count first, so it reads the logits again and writes.  A block of tokens b that meets segment s
+// leaves its sums in slot b + s: both only grow along the tokens, so slots never meet.
+// ---------------------------------------------------------------------------
+
+constexpr int kBalThreads = 256;
+constexpr int kBalWarps = kBalThreads / 32;
+constexpr int kSumThreads = 1024;
+
+struct BalArgs {
+    const void *logits;
+    long long ld, ldd;
+    const int *idx;
+    const int *seq;            // [S + 1] or NULL: one segment of all tokens
+    const uint8_t *mask;       // [T] or NULL
+    const float *grad;         // upstream gradient, or NULL: 1
+    float *loss;
+    int *counts, *tokens;      // [S, E], [S]
+    float *sums;               // [S, E]
+    void *dlogits;
+    float *part_sums;          // [slots][E]
+    int *part_counts;          // [slots][E]
+    int *part_tokens;          // [slots]
+    double *part_loss;         // [S][groups of 32 experts]
+    unsigned *ticket;
+    float coef;
+    int T, E, K, S, per_block, softmax;
+};
+
+template <typename T>
+__device__ __forceinline__ float ld1(const T *p);
+template <>
+__device__ __forceinline__ float ld1<float>(const float *p) { return __ldg(p); }
+template <>
+__device__ __forceinline__ float ld1<__nv_bfloat16>(const __nv_bfloat16 *p) {
+    return __uint_as_float((uint32_t)__ldg(reinterpret_cast<const unsigned short *>(p)) << 16);
+}
+template <>
+__device__ __forceinline__ float ld1<__half>(const __half *p) { return __half2float(__ldg(p)); }
+template <typename T>
+__device__ __forceinline__ T cast1(float v);
+template <>
+__device__ __forceinline__ float cast1<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 cast1<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half cast1<__half>(float v) { return __float2half_rn(v); }
+
+__device__ __forceinline__ float warp_add(float v) {
+#pragma unroll
+    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    return v;
+}
+__device__ __forceinline__ float warp_max(float v) {   // a NaN anywhere may be passed over: the sum carries it
+#pragma unroll
+    for (int d = 16; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+    return v;
+}
+__device__ __forceinline__ int seq_at(const BalArgs &p, int s) {
+    return p.seq ? min(max(__ldg(p.seq + s), 0), p.T) : (s ? p.T : 0);
+}
+// first segment that ends after token t (S when none does)
+__device__ __forceinline__ int seq_of(const BalArgs &p, int t) {
+    int lo = 0, hi = p.S;
+    while (lo < hi) {
+        const int m = (lo + hi) >> 1;
+        if (seq_at(p, m + 1) > t) hi = m;
+        else lo = m + 1;
+    }
+    return lo;
+}
+// a token's normalised scores, lane's experts lane + 32 j (0 outside); c1: 1 - sigma (sigmoid only)
+template <int J>
+__device__ __forceinline__ void scores(const float (&x)[J], int E, int lane, int softmax, float (&pr)[J], float (&c1)[J]) {
+    float z = 0.0f;
+    if (softmax) {
+        float m = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < J; j++)
+            if (lane + 32 * j < E) m = fmaxf(m, x[j]);
+        m = warp_max(m);
+        if (m == -INFINITY) m = 0.0f;      // no expert left: every probability 0 (below)
+#pragma unroll
+        for (int j = 0; j < J; j++) {
+            pr[j] = lane + 32 * j < E ? expf(x[j] - m) : 0.0f;
+            z += pr[j];
+        }
+        z = warp_add(z);
+        z = z == 0.0f ? 1.0f : z;
+    } else {
+#pragma unroll
+        for (int j = 0; j < J; j++) {
+            const float t = expf(-fabsf(x[j])), r = 1.0f / (1.0f + t);
+            pr[j] = lane + 32 * j < E ? (x[j] >= 0.0f ? r : t * r) : 0.0f;
+            if (x[j] != x[j] && lane + 32 * j < E) pr[j] = x[j];
+            c1[j] = x[j] >= 0.0f ? t * r : r;
+            z += pr[j];
+        }
+        z = warp_add(z) + 1e-20f;
+    }
+    const float inv = 1.0f / z;
+#pragma unroll
+    for (int j = 0; j < J; j++) pr[j] *= inv;
+}
+
+template <typename T, int J>
+__global__ void __launch_bounds__(kBalThreads) balance_part_kernel(const BalArgs p) {
+    extern __shared__ float bsm[];
+    float *ws = bsm;                                          // [warps][E]
+    int *cnt = reinterpret_cast<int *>(bsm + kBalWarps * p.E);   // [E]
+    __shared__ int s_n;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (blockIdx.x == 0 && tid == 0) *p.ticket = 0;
+    const int t0 = (int)blockIdx.x * p.per_block, t1 = min(t0 + p.per_block, p.T);
+    const T *logits = static_cast<const T *>(p.logits);
+    for (int s = seq_of(p, t0); s < p.S && seq_at(p, s) < t1; s++) {
+        const int a = max(seq_at(p, s), t0), b = min(seq_at(p, s + 1), t1);
+        if (a >= b) continue;
+        for (int e = tid; e < p.E; e += kBalThreads) cnt[e] = 0;
+        if (tid == 0) s_n = 0;
+        __syncthreads();
+        float sum[J];
+#pragma unroll
+        for (int j = 0; j < J; j++) sum[j] = 0.0f;
+        int n = 0;
+        constexpr int U = J <= 8 ? 2 : 1;                     // tokens in flight
+        for (int t = a + warp; t < b; t += U * kBalWarps) {
+            float x[U][J];
+            bool on[U];
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                const int tt = t + u * kBalWarps;
+                on[u] = tt < b && (!p.mask || p.mask[tt]);
+#pragma unroll
+                for (int j = 0; j < J; j++) x[u][j] = on[u] && lane + 32 * j < p.E ? ld1(logits + tt * p.ld + lane + 32 * j) : 0.0f;
+            }
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                if (!on[u]) continue;
+                float pr[J], c1[J];
+                scores<J>(x[u], p.E, lane, p.softmax, pr, c1);
+#pragma unroll
+                for (int j = 0; j < J; j++) sum[j] += pr[j];
+                n++;
+            }
+        }
+        const long long i0 = (long long)a * p.K, i1 = (long long)b * p.K;
+        for (long long i = i0 + tid; i < i1; i += kBalThreads) {
+            const int e = __ldg(p.idx + i);
+            if ((unsigned)e < (unsigned)p.E && (!p.mask || p.mask[i / p.K])) atomicAdd(&cnt[e], 1);
+        }
+#pragma unroll
+        for (int j = 0; j < J; j++)
+            if (lane + 32 * j < p.E) ws[warp * p.E + lane + 32 * j] = sum[j];
+        if (lane == 0) atomicAdd(&s_n, n);
+        __syncthreads();
+        const size_t slot = (size_t)blockIdx.x + s;
+        for (int e = tid; e < p.E; e += kBalThreads) {
+            float v = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kBalWarps; w++) v += ws[w * p.E + e];
+            p.part_sums[slot * p.E + e] = v;
+            p.part_counts[slot * p.E + e] = cnt[e];
+        }
+        if (tid == 0) p.part_tokens[slot] = s_n;
+        __syncthreads();
+    }
+}
+
+// One block per (32 experts, segment): the slots' sums in a fixed order (32 strands, then the strands),
+// then the block's part of the loss; the last block to finish adds the parts in order.
+__global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(const BalArgs p) {
+    __shared__ float s_sum[32][33];
+    __shared__ int s_cnt[32][33], s_tok[32];
+    __shared__ bool s_last;
+    const int lane = threadIdx.x & 31, strand = threadIdx.x >> 5;
+    const int s = (int)blockIdx.y, g = (int)blockIdx.x, G = (int)gridDim.x, e = 32 * g + lane;
+    const int a = seq_at(p, s), b = seq_at(p, s + 1);
+    float sum = 0.0f;
+    int cnt = 0, tok = 0;
+    if (b > a) {
+        const int b0 = a / p.per_block, b1 = (b - 1) / p.per_block;
+#pragma unroll 4
+        for (int k = b0 + strand; k <= b1; k += 32) {
+            const size_t slot = (size_t)k + s;
+            if (e < p.E) {
+                sum += p.part_sums[slot * p.E + e];
+                cnt += p.part_counts[slot * p.E + e];
+            }
+            tok += p.part_tokens[slot];
+        }
+    }
+    s_sum[strand][lane] = sum;
+    s_cnt[strand][lane] = cnt;
+    if (lane == 0) s_tok[strand] = tok;
+    __syncthreads();
+    if (strand == 0) {
+        sum = 0.0f;
+        cnt = tok = 0;
+        for (int i = 0; i < 32; i++) {
+            sum += s_sum[i][lane];
+            cnt += s_cnt[i][lane];
+            tok += s_tok[i];
+        }
+        if (e < p.E) {
+            p.sums[(size_t)s * p.E + e] = sum;
+            p.counts[(size_t)s * p.E + e] = cnt;
+        }
+        if (g == 0 && lane == 0) p.tokens[s] = tok;
+        double l = e < p.E ? (double)sum * (double)cnt : 0.0;
+#pragma unroll
+        for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+        if (lane == 0) {
+            const double n = tok > 0 ? tok : 1;
+            p.part_loss[(size_t)s * G + g] = (double)p.coef * p.E / ((double)p.K * p.S * n * n) * l;
+            __threadfence();
+            s_last = atomicAdd(p.ticket, 1u) == (unsigned)G * p.S - 1u;
+        }
+    }
+    __syncthreads();
+    if (s_last && strand == 0) {
+        __threadfence();
+        double l = 0.0;
+        const int parts = G * p.S;
+        for (int i = lane; i < parts; i += 32) l += __ldcg(p.part_loss + i);
+#pragma unroll
+        for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+        if (lane == 0) *p.loss = (float)l;
+    }
+}
+
+// A warp per token, per_block / warps of them in a row; a segment's counts stay in registers.
+template <typename T, int J>
+__global__ void __launch_bounds__(kBalThreads) balance_grad_kernel(const BalArgs p) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int each = p.per_block / kBalWarps;
+    const int ta = ((int)blockIdx.x * kBalWarps + warp) * each, tb = min(ta + each, p.T);
+    const T *logits = static_cast<const T *>(p.logits);
+    T *out = static_cast<T *>(p.dlogits);
+    const double g = (p.grad ? (double)__ldg(p.grad) : 1.0) * p.coef * p.E / ((double)p.K * p.S);
+    for (int s = ta < tb ? seq_of(p, ta) : p.S; s < p.S && seq_at(p, s) < tb; s++) {
+        const int a = max(seq_at(p, s), ta), b = min(seq_at(p, s + 1), tb);
+        if (a >= b) continue;
+        const int n = max(__ldg(p.tokens + s), 1);
+        const float up = (float)(g / ((double)n * n));
+        float c[J];
+#pragma unroll
+        for (int j = 0; j < J; j++) c[j] = lane + 32 * j < p.E ? (float)__ldg(p.counts + (size_t)s * p.E + lane + 32 * j) : 0.0f;
+        constexpr int U = J <= 8 ? 2 : 1;
+        for (int t = a; t < b; t += U) {
+            float x[U][J];
+            bool on[U];
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                on[u] = t + u < b && (!p.mask || p.mask[t + u]);
+#pragma unroll
+                for (int j = 0; j < J; j++)
+                    x[u][j] = on[u] && lane + 32 * j < p.E ? ld1(logits + (t + u) * p.ld + lane + 32 * j) : 0.0f;
+            }
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                if (t + u >= b) continue;
+                float d[J];
+                if (on[u]) {
+                    float pr[J], c1[J], dot = 0.0f;
+                    scores<J>(x[u], p.E, lane, p.softmax, pr, c1);
+#pragma unroll
+                    for (int j = 0; j < J; j++) dot = fmaf(pr[j], c[j], dot);
+                    dot = warp_add(dot);
+#pragma unroll
+                    for (int j = 0; j < J; j++) {
+                        d[j] = up * pr[j] * (c[j] - dot);
+                        if (!p.softmax) d[j] *= c1[j];
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < J; j++) d[j] = 0.0f;
+                }
+#pragma unroll
+                for (int j = 0; j < J; j++)
+                    if (lane + 32 * j < p.E) out[(t + u) * p.ldd + lane + 32 * j] = cast1<T>(d[j]);
+            }
+        }
+    }
+}
+
+template <typename F>
+cudaError_t by_type(int dtype, int E, F &&f) {
+#define MOE_BAL_J(T)                                                                      \
+    do {                                                                                  \
+        if (E <= 64) return f(T{}, std::integral_constant<int, 2>{});                     \
+        if (E <= 128) return f(T{}, std::integral_constant<int, 4>{});                    \
+        if (E <= 256) return f(T{}, std::integral_constant<int, 8>{});                    \
+        if (E <= 512) return f(T{}, std::integral_constant<int, 16>{});                   \
+        return f(T{}, std::integral_constant<int, 32>{});                                 \
+    } while (0)
+    if (dtype == MOE_DTYPE_F32) MOE_BAL_J(float);
+    if (dtype == MOE_DTYPE_BF16) MOE_BAL_J(__nv_bfloat16);
+    MOE_BAL_J(__half);
+#undef MOE_BAL_J
+}
+
+// tokens of a forward block: enough blocks to cover the card, at most 64 tokens each
+int tokens_per_block(int T) {
+    int n = 64;
+    while (n > kBalWarps && (T + n - 1) / n < 4 * 152) n /= 2;
+    return n;
+}
+size_t balance_slots(int T, int S) {
+    const int per = tokens_per_block(T);
+    return (size_t)((T + per - 1) / per) + (size_t)S;
+}
+size_t up16(size_t n) { return (n + 15) & ~(size_t)15; }
+
+}  // namespace
+
+int lists_blocks(long long pairs) {
+    if (pairs <= kListsOne) return 1;
+    const long long b = (pairs + kListsMin - 1) / kListsMin;
+    return (int)(b < kListsBlocks ? b : kListsBlocks);
+}
+
+size_t lists_workspace(long long pairs, int E) {
+    const int b = lists_blocks(pairs);
+    return b == 1 ? 0 : (size_t)b * E * sizeof(int);
+}
+
+cudaError_t launch_lists(const int *idx, int T, int K, int E, int align, long long room, int *counts, int *offsets, int *rows,
+                         int *pos, void *ws, cudaStream_t st) {
+    ListArgs p = {idx, counts, offsets, rows, pos, static_cast<int *>(ws), (long long)T * K, room, K, E, align, 0, 1};
+    p.blocks = lists_blocks(p.pairs);
+    p.chunk = (int)((p.pairs + p.blocks - 1) / p.blocks);
+    if (p.blocks > 1) {
+        lists_count_kernel<<<p.blocks, kListThreads, E * sizeof(int), st>>>(p);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    const size_t smem = ((size_t)kListWarps * E + 3 * (size_t)E + 1) * sizeof(int);
+    const cudaError_t e = cudaFuncSetAttribute(lists_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    lists_kernel<<<p.blocks, kListThreads, smem, st>>>(p);
+    return cudaGetLastError();
+}
+
+size_t balance_workspace(int T, int E, int S) {
+    const size_t slots = balance_slots(T, S);
+    return up16(slots * E * 4) + up16(slots * E * 4) + up16(slots * 4) + up16((size_t)S * ((E + 31) / 32) * 8) + 16;
+}
+
+cudaError_t launch_balance_forward(const void *logits, int dtype, long long ld, int T, int E, const int *idx, int K, int softmax,
+                                   float coef, const int *seq, int S, const uint8_t *mask, float *loss, int *counts, float *sums,
+                                   int *tokens, void *ws, cudaStream_t st) {
+    BalArgs p = {};
+    p.logits = logits;
+    p.ld = ld;
+    p.idx = idx;
+    p.seq = seq;
+    p.mask = mask;
+    p.loss = loss;
+    p.counts = counts;
+    p.tokens = tokens;
+    p.sums = sums;
+    p.coef = coef;
+    p.T = T;
+    p.E = E;
+    p.K = K;
+    p.S = S;
+    p.softmax = softmax;
+    p.per_block = tokens_per_block(T);
+    const size_t slots = balance_slots(T, S);
+    char *w = static_cast<char *>(ws);
+    p.part_sums = reinterpret_cast<float *>(w);
+    w += up16(slots * E * 4);
+    p.part_counts = reinterpret_cast<int *>(w);
+    w += up16(slots * E * 4);
+    p.part_tokens = reinterpret_cast<int *>(w);
+    w += up16(slots * 4);
+    p.part_loss = reinterpret_cast<double *>(w);
+    w += up16((size_t)S * ((E + 31) / 32) * 8);
+    p.ticket = reinterpret_cast<unsigned *>(w);
+    const cudaError_t e = by_type(dtype, E, [&](auto t, auto j) {
+        const int blocks = T > 0 ? (T + p.per_block - 1) / p.per_block : 1;
+        balance_part_kernel<decltype(t), decltype(j)::value>
+            <<<blocks, kBalThreads, ((size_t)kBalWarps + 1) * E * sizeof(float), st>>>(p);
+        return cudaGetLastError();
+    });
+    if (e != cudaSuccess) return e;
+    balance_sum_kernel<<<dim3((E + 31) / 32, S), kSumThreads, 0, st>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_balance_backward(const void *logits, int dtype, long long ld, int T, int E, int K, int softmax, float coef,
+                                    const int *counts, const int *tokens, const int *seq, int S, const uint8_t *mask,
+                                    const float *grad, void *dlogits, long long ldd, cudaStream_t st) {
+    BalArgs p = {};
+    p.logits = logits;
+    p.ld = ld;
+    p.ldd = ldd;
+    p.seq = seq;
+    p.mask = mask;
+    p.grad = grad;
+    p.counts = const_cast<int *>(counts);
+    p.tokens = const_cast<int *>(tokens);
+    p.dlogits = dlogits;
+    p.coef = coef;
+    p.T = T;
+    p.E = E;
+    p.K = K;
+    p.S = S;
+    p.softmax = softmax;
+    p.per_block = tokens_per_block(T);
+    return by_type(dtype, E, [&](auto t, auto j) {
+        balance_grad_kernel<decltype(t), decltype(j)::value><<<(T + p.per_block - 1) / p.per_block, kBalThreads, 0, st>>>(p);
+        return cudaGetLastError();
+    });
+}
+
+}  // namespace moe
