@@ -390,138 +390,176 @@ class MoeLayer:
 # layouts).  Tensors are checked for type, shape, layout and device here, since the C side sees
 # pointers only; what is not given as an argument is allocated by PyTorch on the call's stream.
 
-def _dtype_code(t, where, name):
-    import torch
-    code = {torch.float32: MOE_DTYPE_F32, torch.float16: MOE_DTYPE_F16, torch.bfloat16: MOE_DTYPE_BF16}.get(t.dtype)
-    if code is None:
-        raise MoeError(MOE_ERR_INVALID, where, f"{name}: need float32, float16 or bfloat16, got {t.dtype}")
-    return code
+class _Call:
+    """One call's checks: the device and stream of its first tensor, and what each tensor must be.
 
-
-class _Args:
-    """Checks of one call's tensors, and the stream that its allocations belong to."""
+    The checks run on every call, so they are one chain of cheap comparisons (bad()) and the
+    message is made only after one failed (refuse())."""
+    __slots__ = ("where", "torch", "device", "stream", "own_stream")
 
     def __init__(self, where, first, stream):
-        import torch
-        self.where, self.torch, self.stream = where, torch, stream
+        torch = _torch()
+        self.where, self.torch = where, torch
         if not isinstance(first, torch.Tensor) or not first.is_cuda:
             self.fail("the tensors must be on a CUDA device")
-        self.device = first.device
-        if self.device.index != torch.cuda.current_device():
-            self.fail(f"the tensors are on {self.device}, the current device is cuda:{torch.cuda.current_device()}")
-        self.handle = _stream_handle(stream)
+        self.device = dev = first.get_device()
+        if dev != torch.cuda.current_device():
+            self.fail(f"the tensors are on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+        self.stream = now = _raw_stream(dev)
+        self.own_stream = True                      # the stream that PyTorch allocates on
+        if stream is not None:
+            self.stream = _stream_handle(stream) or 0
+            self.own_stream = self.stream == now
 
     def fail(self, msg):
         raise MoeError(MOE_ERR_INVALID, self.where, msg)
 
-    def tensor(self, t, name, dtypes, shape, rows=False):
-        """t of one of dtypes and of `shape` (None: any extent); contiguous, or (rows) each row so."""
-        if not isinstance(t, self.torch.Tensor) or t.device != self.device:
-            self.fail(f"{name}: need a tensor on {self.device}")
-        if dtypes is not None and t.dtype not in dtypes:
+    def need(self, t, name, dtypes, shape, rows=False):
+        """t is on the device, of one of dtypes and of `shape`, contiguous or (rows) each row so."""
+        try:
+            if t.dtype in dtypes and t.shape == shape and t.get_device() == self.device and (
+                    t.is_contiguous() or (rows and t.stride(-1) == 1 and t.stride(0) >= shape[-1])):
+                return t.data_ptr()
+        except AttributeError:
+            pass
+        if not isinstance(t, self.torch.Tensor):
+            self.fail(f"{name}: need a tensor")
+        if t.get_device() != self.device:
+            self.fail(f"{name}: is on {t.device}, the call on cuda:{self.device}")
+        if t.dtype not in dtypes:
             self.fail(f"{name}: need {' or '.join(map(str, dtypes))}, got {t.dtype}")
-        if t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape)):
-            self.fail(f"{name}: need shape {tuple('any' if w is None else w for w in shape)}, got {tuple(t.shape)}")
-        if not t.is_contiguous() and not (rows and t.stride(-1) == 1 and t.stride(0) >= t.shape[-1]):
-            self.fail(f"{name}: need {'contiguous rows' if rows else 'a contiguous tensor'}, got strides {t.stride()}")
-        return t
+        if t.shape != shape:
+            self.fail(f"{name}: need shape {tuple(shape)}, got {tuple(t.shape)}")
+        self.fail(f"{name}: need {'contiguous rows' if rows else 'a contiguous tensor'}, got strides {t.stride()}")
 
-    def row_stride(self, t):
-        return max(t.stride(0), t.shape[1]) if t.shape[0] > 1 else t.shape[1]
+    def dims(self, t, name, n):
+        if not isinstance(t, self.torch.Tensor) or t.dim() != n:
+            self.fail(f"{name}: need a tensor of {n} dimensions")
+        return t.shape
 
-    def empty(self, *specs):
-        """Tensors for (shape, dtype) each, allocated for the call's stream."""
+    def code(self, t, name):
+        c = _dtypes().get(t.dtype)
+        if c is None:
+            self.fail(f"{name}: need float32, float16 or bfloat16, got {t.dtype}")
+        return c
+
+    def integer(self, v, name, lo=0):
+        if not isinstance(v, (int, np.integer)) or isinstance(v, bool) or not lo <= v < 1 << 31:
+            self.fail(f"{name}={v!r}: need an integer from {lo}")
+        return int(v)
+
+    def empty(self, *shapes):
+        """One new tensor for each (shape, dtype), allocated for the call's stream."""
         torch = self.torch
-        if self.stream is None or self.handle == torch.cuda.current_stream(self.device).cuda_stream:
-            return [torch.empty(s, dtype=d, device=self.device) for s, d in specs]
-        on = torch.cuda.ExternalStream(self.handle, device=self.device) if self.handle else torch.cuda.default_stream(self.device)
+        if self.own_stream:
+            return [torch.empty(s, dtype=d, device="cuda") for s, d in shapes]
+        dev = torch.device("cuda", self.device)
+        on = torch.cuda.ExternalStream(self.stream, device=dev) if self.stream else torch.cuda.default_stream(dev)
         with torch.cuda.stream(on):
-            return [torch.empty(s, dtype=d, device=self.device) for s, d in specs]
+            return [torch.empty(s, dtype=d, device=dev) for s, d in shapes]
 
 
-def _int(a, v, name, lo=0):
-    if not isinstance(v, (int, np.integer)) or isinstance(v, bool) or not lo <= v < 1 << 31:
-        a.fail(f"{name}={v!r}: need an integer from {lo}")
-    return int(v)
+_cache = {}
+
+
+def _torch():
+    t = _cache.get("torch")
+    if t is None:
+        import torch
+        f8 = torch.float8_e4m3fn
+        _cache.update(torch=torch, dtypes={torch.float32: MOE_DTYPE_F32, torch.float16: MOE_DTYPE_F16, torch.bfloat16: MOE_DTYPE_BF16},
+                      f8=(f8, torch.uint8), i32=(torch.int32,), f32=(torch.float32,), mask=(torch.bool, torch.uint8))
+        t = torch
+    return t
+
+
+def _dtypes():
+    return _cache["dtypes"]
+
+
+def _raw_stream(dev: int) -> int:
+    torch = _cache["torch"]
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)     # what current_stream() wraps
+    return raw(dev) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
+
+
+def _row_stride(t) -> int:
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _blocks(n: int) -> int:
+    return -(-n // 128)
 
 
 def moe_expert_lists(topk_idx, n_experts: int, align: int = 1, stream=None):
     """Token lists of topk_idx [T, K] int32 (values outside [0, n_experts): dropped pairs).
     -> counts [E], offsets [E + 1], rows [room] (token of each row, -1 in padding), pos [T, K]
     (row of each pair, -1 for dropped ones), all int32."""
-    import torch
-    a = _Args("moe_expert_lists", topk_idx, stream)
-    T, K = a.tensor(topk_idx, "topk_idx", (torch.int32,), (None, None)).shape
-    E, align = _int(a, n_experts, "n_experts", 1), _int(a, align, "align", 1)
+    c = _Call("moe_expert_lists", topk_idx, stream)
+    i32 = _cache["i32"][0]
+    T, K = shape = c.dims(topk_idx, "topk_idx", 2)
+    idx = c.need(topk_idx, "topk_idx", _cache["i32"], shape)
+    E, align = c.integer(n_experts, "n_experts", 1), c.integer(align, "align", 1)
     L = lib()
     room = L.moe_expert_lists_rows(T, K, E, align)
     if not 0 <= room < 1 << 31:
-        raise MoeError(MOE_ERR_UNSUPPORTED, a.where, f"{room} rows: need fewer than 2^31, and at least one choice a token")
+        raise MoeError(MOE_ERR_UNSUPPORTED, c.where, f"{room} rows: need fewer than 2^31, and at least one choice a token")
+    counts, offsets, rows, pos = c.empty(((E,), i32), ((E + 1,), i32), ((room,), i32), (shape, i32))
     need = L.moe_expert_lists_workspace(T, K, E)
-    i32 = torch.int32
-    counts, offsets, rows, pos, ws = a.empty(((E,), i32), ((E + 1,), i32), ((room,), i32), ((T, K), i32), ((need,), torch.uint8))
-    _check(L.moe_expert_lists(_ptr(topk_idx), T, K, E, align, _ptr(counts), _ptr(offsets), _ptr(rows), _ptr(pos), _ptr(ws), need,
-                              a.handle), a.where)
+    ws = c.empty(((need,), c.torch.uint8))[0] if need else None
+    _check(L.moe_expert_lists(idx, T, K, E, align, counts.data_ptr(), offsets.data_ptr(), rows.data_ptr(), pos.data_ptr(),
+                              ws.data_ptr() if need else None, need, c.stream), c.where)
     return counts, offsets, rows, pos
 
 
-def _balance_args(a, logits, seq_offsets, mask):
-    import torch
-    dt = _dtype_code(logits, a.where, "logits")
-    T, E = a.tensor(logits, "logits", None, (None, None), rows=True).shape
-    S = 1
+def _balance_args(c, logits, seq_offsets, mask):
+    T, E = shape = c.dims(logits, "logits", 2)
+    dt = c.code(logits, "logits")
+    x = c.need(logits, "logits", _cache["dtypes"], shape, rows=True)
+    S, seq = 1, None
     if seq_offsets is not None:
-        S = a.tensor(seq_offsets, "seq_offsets", (torch.int32,), (None,)).shape[0] - 1
-    if mask is not None:
-        a.tensor(mask, "mask", (torch.bool, torch.uint8), (T,))
-    return dt, T, E, S
+        n = c.dims(seq_offsets, "seq_offsets", 1)
+        seq, S = c.need(seq_offsets, "seq_offsets", _cache["i32"], n), n[0] - 1
+        if S < 1:
+            c.fail("seq_offsets: need at least two entries")
+    return x, dt, T, E, seq, S, None if mask is None else c.need(mask, "mask", _cache["mask"], (T,))
 
 
 def moe_balance_forward(logits, topk_idx, coef: float, score_func: int = MOE_SCORE_SIGMOID, seq_offsets=None, mask=None, stream=None):
     """Balance loss of a router: logits [T, E] float32 / float16 / bfloat16 (rows may be strided),
     topk_idx [T, K] int32, seq_offsets [S + 1] int32 (None: one sequence), mask [T] bool (False:
     left out).  -> loss [1], counts [S, E] int32, prob_sums [S, E], tokens [S] int32."""
-    import torch
-    a = _Args("moe_balance_forward", logits, stream)
-    dt, T, E, S = _balance_args(a, logits, seq_offsets, mask)
-    K = a.tensor(topk_idx, "topk_idx", (torch.int32,), (T, None)).shape[1]
+    c = _Call("moe_balance_forward", logits, stream)
+    x, dt, T, E, seq, S, m = _balance_args(c, logits, seq_offsets, mask)
+    K = c.dims(topk_idx, "topk_idx", 2)[1]
+    idx = c.need(topk_idx, "topk_idx", _cache["i32"], (T, K))
     L = lib()
     need = L.moe_balance_workspace(T, E, S)
-    i32, f32 = torch.int32, torch.float32
-    n = max(S, 0)
-    loss, counts, sums, tokens, ws = a.empty(((1,), f32), ((n, E), i32), ((n, E), f32), ((n,), i32), ((need,), torch.uint8))
-    _check(L.moe_balance_forward(_ptr(logits), dt, a.row_stride(logits), T, E, _ptr(topk_idx), K, score_func, coef, _ptr(seq_offsets), S,
-                                 _ptr(mask), _ptr(loss), _ptr(counts), _ptr(sums), _ptr(tokens), _ptr(ws), need, a.handle), a.where)
+    i32, f32 = _cache["i32"][0], _cache["f32"][0]
+    loss, counts, sums, tokens, ws = c.empty(((1,), f32), ((S, E), i32), ((S, E), f32), ((S,), i32), ((need,), c.torch.uint8))
+    _check(L.moe_balance_forward(x, dt, _row_stride(logits), T, E, idx, K, score_func, coef, seq, S, m, loss.data_ptr(),
+                                 counts.data_ptr(), sums.data_ptr(), tokens.data_ptr(), ws.data_ptr(), need, c.stream), c.where)
     return loss, counts, sums, tokens
 
 
 def moe_balance_backward(logits, top_k: int, counts, tokens, coef: float, score_func: int = MOE_SCORE_SIGMOID, seq_offsets=None,
                          mask=None, grad_loss=None, out=None, stream=None):
     """Gradient of moe_balance_forward's loss with respect to logits, with its counts and tokens;
-    grad_loss [1] float32 (None: 1).  Rows outside every sequence of `out` (None: a new tensor)
-    stay as they are.  -> dlogits [T, E] in logits' dtype."""
-    import torch
-    a = _Args("moe_balance_backward", logits, stream)
-    dt, T, E, S = _balance_args(a, logits, seq_offsets, mask)
-    a.tensor(counts, "counts", (torch.int32,), (S, E))
-    a.tensor(tokens, "tokens", (torch.int32,), (S,))
-    if grad_loss is not None and a.tensor(grad_loss.reshape(-1), "grad_loss", (torch.float32,), (1,)) is None:
-        return None
+    grad_loss float32, one value (None: 1).  Rows outside every sequence of `out` (None: a new
+    tensor) stay as they are.  -> dlogits [T, E] in logits' dtype."""
+    c = _Call("moe_balance_backward", logits, stream)
+    x, dt, T, E, seq, S, m = _balance_args(c, logits, seq_offsets, mask)
+    n = c.need(counts, "counts", _cache["i32"], (S, E))
+    tok = c.need(tokens, "tokens", _cache["i32"], (S,))
+    g = None
+    if grad_loss is not None:
+        g = c.need(grad_loss, "grad_loss", _cache["f32"], () if isinstance(grad_loss, c.torch.Tensor) and grad_loss.dim() == 0 else (1,))
     if out is None:
-        out, = a.empty(((T, E), logits.dtype))
-    a.tensor(out, "out", (logits.dtype,), (T, E), rows=True)
-    _check(lib().moe_balance_backward(_ptr(logits), dt, a.row_stride(logits), T, E, _int(a, top_k, "top_k", 1), score_func, coef,
-                                      _ptr(counts), _ptr(tokens), _ptr(seq_offsets), S, _ptr(mask), _ptr(grad_loss), _ptr(out),
-                                      a.row_stride(out), a.handle), a.where)
+        out, = c.empty(((T, E), logits.dtype))
+    d = c.need(out, "out", (logits.dtype,), (T, E), rows=True)
+    _check(lib().moe_balance_backward(x, dt, _row_stride(logits), T, E, c.integer(top_k, "top_k", 1), score_func, coef, n, tok, seq,
+                                      S, m, g, d, _row_stride(out), c.stream), c.where)
     return out
-
-
-def _f8(torch):
-    return (torch.float8_e4m3fn, torch.uint8)
-
-
-def _blocks(n: int) -> int:
-    return -(-n // 128)
 
 
 def moe_fp8_quantize(x, rows=None, transposed: bool = False, stream=None):
@@ -529,17 +567,23 @@ def moe_fp8_quantize(x, rows=None, transposed: bool = False, stream=None):
     rows [R] int32 (negative: zeros), with a power-of-two scale per 1 x 128 block.
     -> codes [R, width] float8_e4m3fn, scales [ceil(width / 128), R]; with transposed also
     codes_t [width, Rp], scales_t [Rp / 128, width], Rp = R rounded up to a multiple of 128."""
-    import torch
-    a = _Args("moe_fp8_quantize", x, stream)
-    dt = _dtype_code(x, a.where, "x")
-    T, n = a.tensor(x, "x", None, (None, None), rows=True).shape
-    R = T if rows is None else a.tensor(rows, "rows", (torch.int32,), (None,)).shape[0]
-    f8, f32, rb = torch.float8_e4m3fn, torch.float32, _blocks(R)
-    specs = [((R, n), f8), ((_blocks(n), R), f32)] + ([((n, rb * 128), f8), ((rb, n), f32)] if transposed else [])
-    out = a.empty(*specs)
-    ct, st = (out[2], out[3]) if transposed and R else (None, None)
-    _check(lib().moe_fp8_quantize(_ptr(x), dt, a.row_stride(x), T, n, _ptr(rows), R, _ptr(out[0]), _ptr(out[1]), _ptr(ct), _ptr(st),
-                                  a.handle), a.where)
+    c = _Call("moe_fp8_quantize", x, stream)
+    T, n = shape = c.dims(x, "x", 2)
+    dt = c.code(x, "x")
+    px, R, pr = c.need(x, "x", _cache["dtypes"], shape, rows=True), T, None
+    if rows is not None:
+        R = c.dims(rows, "rows", 1)[0]
+        pr = c.need(rows, "rows", _cache["i32"], (R,))
+    f8, f32 = _cache["f8"][0], _cache["f32"][0]
+    pt = ps = None
+    if transposed:
+        rb = _blocks(R)
+        out = c.empty(((R, n), f8), ((_blocks(n), R), f32), ((n, rb * 128), f8), ((rb, n), f32))
+        if R:
+            pt, ps = out[2].data_ptr(), out[3].data_ptr()
+    else:
+        out = c.empty(((R, n), f8), ((_blocks(n), R), f32))
+    _check(lib().moe_fp8_quantize(px, dt, _row_stride(x), T, n, pr, R, out[0].data_ptr(), out[1].data_ptr(), pt, ps, c.stream), c.where)
     return tuple(out)
 
 
@@ -547,49 +591,48 @@ def moe_fp8_quantize_weights(w, transposed: bool = False, stream=None):
     """e4m3 codes of weights w [E, N, K] or [N, K], one scale per 128 x 128 block.
     -> codes, scales [(E,) ceil(N / 128), ceil(K / 128)]; with transposed also the transposed
     matrices' codes and scales."""
-    import torch
-    a = _Args("moe_fp8_quantize_weights", w, stream)
-    dt = _dtype_code(w, a.where, "w")
-    a.tensor(w, "w", None, (None,) * (2 if w.dim() == 2 else 3))
-    lead, (N, K) = tuple(w.shape[:-2]), w.shape[-2:]
-    f8, f32 = torch.float8_e4m3fn, torch.float32
+    c = _Call("moe_fp8_quantize_weights", w, stream)
+    shape = c.dims(w, "w", 2 if w.dim() == 2 else 3)
+    dt = c.code(w, "w")
+    pw = c.need(w, "w", _cache["dtypes"], shape)
+    lead, (N, K) = tuple(shape[:-2]), shape[-2:]
+    f8, f32 = _cache["f8"][0], _cache["f32"][0]
     specs = [(lead + (N, K), f8), (lead + (_blocks(N), _blocks(K)), f32)]
     if transposed:
         specs += [(lead + (K, N), f8), (lead + (_blocks(K), _blocks(N)), f32)]
-    out = a.empty(*specs)
-    ct, st = out[2:] if transposed else (None, None)
-    _check(lib().moe_fp8_quantize_weights(_ptr(w), dt, lead[0] if lead else 1, N, K, _ptr(out[0]), _ptr(out[1]), _ptr(ct), _ptr(st),
-                                          a.handle), a.where)
+    out = c.empty(*specs)
+    p = [t.data_ptr() for t in out] + [None, None]
+    _check(lib().moe_fp8_quantize_weights(pw, dt, lead[0] if lead else 1, N, K, p[0], p[1], p[2], p[3], c.stream), c.where)
     return tuple(out)
 
 
 def moe_fp8_matmul(x, x_scale, w, w_scale, offsets=None, out=None, out_dtype=None, stream=None):
-    """y [R, N] = x w^T of e4m3 codes x [R, K], w [E, N, K] or [N, K] with their block scales
-    x_scale [ceil(K / 128), R], w_scale [(E,) ceil(N / 128), ceil(K / 128)]; offsets [E + 1] int32:
-    row r is multiplied with the expert whose segment holds it, other rows of `out` stay as they
-    are (None: one weight matrix).  out_dtype (bfloat16 by default) or out's type."""
-    import torch
-    a = _Args("moe_fp8_matmul", x, stream)
-    R, K = a.tensor(x, "x", _f8(torch), (None, None)).shape
-    E = 1
-    if w.dim() == 2 or offsets is None:
-        if w.dim() == 3 and w.shape[0] != 1 or offsets is not None:
-            a.fail("w [E, N, K] and offsets belong together")
-        w, w_scale = w.view(w.shape[-2:]), w_scale.view(w_scale.shape[-2:])
-        N = a.tensor(w, "w", _f8(torch), (None, K)).shape[0]
-        a.tensor(w_scale, "w_scale", (torch.float32,), (_blocks(N), _blocks(K)))
+    """y [R, N] = x w^T of e4m3 codes x [R, K], w [N, K] with their block scales
+    x_scale [ceil(K / 128), R], w_scale [ceil(N / 128), ceil(K / 128)].  With offsets [E + 1] int32,
+    w [E, N, K] and w_scale [E, ...]: row r is multiplied with the expert whose segment holds it;
+    rows outside every segment of `out` stay as they are.  out_dtype: bfloat16 by default."""
+    c = _Call("moe_fp8_matmul", x, stream)
+    f8, f32 = _cache["f8"], _cache["f32"]
+    R, K = c.dims(x, "x", 2)
+    kb, off = _blocks(K), None
+    if offsets is None:
+        E, N = 1, c.dims(w, "w", 2)[0]
+        pw = c.need(w, "w", f8, (N, K))
+        ps = c.need(w_scale, "w_scale", f32, (_blocks(N), kb))
     else:
-        E, N = a.tensor(w, "w", _f8(torch), (None, None, K)).shape[:2]
-        a.tensor(w_scale, "w_scale", (torch.float32,), (E, _blocks(N), _blocks(K)))
-        a.tensor(offsets, "offsets", (torch.int32,), (E + 1,))
-    a.tensor(x_scale, "x_scale", (torch.float32,), (_blocks(K), R))
+        E, N, _ = c.dims(w, "w", 3)
+        pw = c.need(w, "w", f8, (E, N, K))
+        ps = c.need(w_scale, "w_scale", f32, (E, _blocks(N), kb))
+        off = c.need(offsets, "offsets", _cache["i32"], (E + 1,))
+    px = c.need(x, "x", f8, (R, K))
+    pxs = c.need(x_scale, "x_scale", f32, (kb, R))
     if out is None:
-        out, = a.empty(((R, N), out_dtype or torch.bfloat16))
+        out, = c.empty(((R, N), out_dtype or c.torch.bfloat16))
     elif out_dtype is not None and out.dtype != out_dtype:
-        a.fail(f"out is {out.dtype}, out_dtype {out_dtype}")
-    a.tensor(out, "out", None, (R, N), rows=True)
-    _check(lib().moe_fp8_matmul(_ptr(x), _ptr(x_scale), R, _ptr(w), _ptr(w_scale), E, N, K, _ptr(offsets), _ptr(out),
-                                _dtype_code(out, a.where, "out"), a.row_stride(out), a.handle), a.where)
+        c.fail(f"out is {out.dtype}, out_dtype {out_dtype}")
+    dt = c.code(out, "out")
+    py = c.need(out, "out", _cache["dtypes"], (R, N), rows=True)
+    _check(lib().moe_fp8_matmul(px, pxs, R, pw, ps, E, N, K, off, py, dt, _row_stride(out), c.stream), c.where)
     return out
 
 
@@ -598,23 +641,25 @@ def moe_fp8_wgrad(xt, xt_scale, dyt, dyt_scale, offsets=None, out=None, out_dtyp
     xt [K, R], dyt [N, R] codes, R a multiple of 128, xt_scale [R / 128, K], dyt_scale [R / 128, N];
     offsets [E + 1] int32, multiples of 128 (None: one matrix).
     -> dw [E, N, K] ([N, K] without offsets), float32 by default."""
-    import torch
-    a = _Args("moe_fp8_wgrad", xt, stream)
-    K, R = a.tensor(xt, "xt", _f8(torch), (None, None)).shape
-    N = a.tensor(dyt, "dyt", _f8(torch), (None, R)).shape[0]
-    a.tensor(xt_scale, "xt_scale", (torch.float32,), (R // 128, K))
-    a.tensor(dyt_scale, "dyt_scale", (torch.float32,), (R // 128, N))
-    E = 1 if offsets is None else a.tensor(offsets, "offsets", (torch.int32,), (None,)).shape[0] - 1
-    shape = (N, K) if offsets is None else (E, N, K)
-    if out is None:
+    c = _Call("moe_fp8_wgrad", xt, stream)
+    f8, f32 = _cache["f8"], _cache["f32"]
+    K, R = c.dims(xt, "xt", 2)
+    N = c.dims(dyt, "dyt", 2)[0]
+    px, pd = c.need(xt, "xt", f8, (K, R)), c.need(dyt, "dyt", f8, (N, R))
+    pxs, pds = c.need(xt_scale, "xt_scale", f32, (R // 128, K)), c.need(dyt_scale, "dyt_scale", f32, (R // 128, N))
+    E, shape, off = 1, (N, K), None
+    if offsets is not None:
+        E = c.dims(offsets, "offsets", 1)[0] - 1
         if E < 1:
-            a.fail("offsets: need at least two entries")
-        out, = a.empty((shape, out_dtype or torch.float32))
+            c.fail("offsets: need at least two entries")
+        off, shape = c.need(offsets, "offsets", _cache["i32"], (E + 1,)), (E, N, K)
+    if out is None:
+        out, = c.empty((shape, out_dtype or c.torch.float32))
     elif out_dtype is not None and out.dtype != out_dtype:
-        a.fail(f"out is {out.dtype}, out_dtype {out_dtype}")
-    a.tensor(out, "out", None, shape)
-    _check(lib().moe_fp8_wgrad(_ptr(xt), _ptr(xt_scale), _ptr(dyt), _ptr(dyt_scale), R, N, K, E, _ptr(offsets), _ptr(out),
-                               _dtype_code(out, a.where, "out"), a.handle), a.where)
+        c.fail(f"out is {out.dtype}, out_dtype {out_dtype}")
+    dt = c.code(out, "out")
+    po = c.need(out, "out", _cache["dtypes"], shape)
+    _check(lib().moe_fp8_wgrad(px, pxs, pd, pds, R, N, K, E, off, po, dt, c.stream), c.where)
     return out
 
 

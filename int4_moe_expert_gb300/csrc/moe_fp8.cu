@@ -43,39 +43,33 @@ constexpr int kARows = 128;              // lanes of a tile
 constexpr int kABytes = kARows * kKB;    // A bytes of a stage
 
 struct GemmArgs {
-    const float *sa;        // block scales [E][ceil(na / 128)][nkb], or (wgrad) row scales [nkb][na]
+    const float *sa;        // block scales [E][ceil(na / 128)][nkb]
     const float *sb;        // column scales [nkb][nb]
     const int *offsets;     // [E + 1] or NULL
     void *out;
     long long ldo;          // elements between columns of out
-    long long out_stride;   // elements between experts of out (wgrad)
     int na, nb;             // rows of A (of one expert), rows of B
-    int nkb;                // 128-blocks of the inner axis (wgrad: of all experts' rows)
+    int nkb;                // 128-blocks of the inner axis
     int E;
     int out_dtype;
     unsigned *err;
 };
 
-template <int BT_, int CH_, bool WG_, bool SPLIT_, int STAGES_>
+template <int BT_, bool SPLIT_, int STAGES_>
 struct Cfg {
     static constexpr int BT = BT_;           // columns of a tile
-    static constexpr int CH = CH_;           // column parts, four epilogue warps each
-    static constexpr bool WG = WG_;          // wgrad: per-lane A scales, inner range per expert
     static constexpr bool SPLIT = SPLIT_;    // a cluster shares one tile, each block part of the inner axis
     static constexpr int S = STAGES_;
-    static constexpr int EW = 4 * CH;        // epilogue warps
+    static constexpr int EW = 4;             // epilogue warps
     static constexpr int THREADS = 32 * (EW + 4);
     static constexpr int NT = (512 / BT < 4) ? 512 / BT : 4;   // accumulator ring
     static constexpr int TCOLS = NT * BT < 32 ? 32 : NT * BT;
     static constexpr int BBYTES = BT * kKB;
     static constexpr int STAGE = kABytes + BBYTES;
-    static constexpr int SS = 4;             // scale ring
-    static constexpr int SF = BT + (WG ? kARows : 0);   // floats of a scale slot
-    static constexpr int CW = BT / CH;       // columns of an epilogue thread
-    static constexpr int LD = CW < 32 || CW > 32 ? 16 : 32;   // columns of one tcgen05.ld
-    static constexpr int PER_SM = CH == 1 ? 2 : 1;   // blocks an SM holds
+    static constexpr int SS = 8;             // scale ring
+    static constexpr int LD = BT < 32 ? 16 : 32;        // columns of one tcgen05.ld
+    static constexpr int PER_SM = 2;         // blocks an SM holds
     static constexpr size_t SMEM = (size_t)S * STAGE + 1024;
-    static constexpr bool BIGREG = CW > 64;
     static constexpr uint32_t IDESC = (1u << 4) | ((uint32_t)(BT >> 3) << 17) | ((128u >> 4) << 24);
     static_assert(!SPLIT || (size_t)kARows * BT * 4 <= (size_t)S * STAGE, "partial sums reuse the stage ring");
 };
@@ -128,6 +122,14 @@ __device__ __forceinline__ void tc_wait_ld(uint32_t (&r)[N]) {
                               "+r"(r[i + 6]), "+r"(r[i + 7]), "+r"(r[i + 8]), "+r"(r[i + 9]), "+r"(r[i + 10]), "+r"(r[i + 11]),
                               "+r"(r[i + 12]), "+r"(r[i + 13]), "+r"(r[i + 14]), "+r"(r[i + 15]) :: "memory");
     }
+}
+// 4-byte asynchronous copy global -> shared; !in: zeros
+__device__ __forceinline__ void cp_async4(uint32_t dst, const float *src, bool in) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
+}
+// this thread's arrival, once its asynchronous copies so far have landed
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ uint64_t pack2(uint32_t a, uint32_t b) {
     uint64_t r;
@@ -215,44 +217,43 @@ struct Walk {
     const int *first;   // shared memory, [E + 1]: column tiles before each expert (matmul with offsets)
     int nat, e;
     __device__ Walk(const GemmArgs &p_, const int *first_) : p(p_), first(first_), nat((p_.na + kARows - 1) / kARows), e(0) {}
-    __device__ __forceinline__ int total() const {
-        if (C::WG) return p.E * nat * ((p.nb + C::BT - 1) / C::BT);
-        return nat * (p.offsets ? first[p.E] : (p.nb + C::BT - 1) / C::BT);
-    }
+    __device__ __forceinline__ int total() const { return nat * (p.offsets ? first[p.E] : (p.nb + C::BT - 1) / C::BT); }
     __device__ __forceinline__ Tile at(int t) {
         Tile r;
         const int j = t / nat;
         r.a0 = (t - j * nat) * kARows;
-        if (C::WG) {
-            const int nbt = (p.nb + C::BT - 1) / C::BT;
-            r.e = j / nbt;
-            r.b0 = (j - r.e * nbt) * C::BT;
-            r.bend = p.nb;
-            if (p.offsets) {
-                r.k0 = min(max(p.offsets[r.e], 0) / kKB, p.nkb);
-                r.k1 = min(max(p.offsets[r.e + 1] / kKB, r.k0), p.nkb);
-            } else {
-                r.k0 = 0;
-                r.k1 = p.nkb;
-            }
+        r.k0 = 0;
+        r.k1 = p.nkb;
+        if (p.offsets) {
+            while (first[e + 1] <= j) e++;
+            const int a = min(max(p.offsets[e], 0), p.nb);
+            r.e = e;
+            r.b0 = a + (j - first[e]) * C::BT;
+            r.bend = min(max(p.offsets[e + 1], a), p.nb);
         } else {
-            r.k0 = 0;
-            r.k1 = p.nkb;
-            if (p.offsets) {
-                while (first[e + 1] <= j) e++;
-                const int a = min(max(p.offsets[e], 0), p.nb);
-                r.e = e;
-                r.b0 = a + (j - first[e]) * C::BT;
-                r.bend = min(max(p.offsets[e + 1], a), p.nb);
-            } else {
-                r.e = 0;
-                r.b0 = j * C::BT;
-                r.bend = p.nb;
-            }
+            r.e = 0;
+            r.b0 = j * C::BT;
+            r.bend = p.nb;
         }
         return r;
     }
 };
+
+// first[e + 1] holds expert e's tiles: makes it the tiles of experts 0..e (one warp)
+__device__ __forceinline__ void prefix_tiles(int *first, int E, int lane) {
+    int run = 0;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+        int v = e0 + lane < E ? first[e0 + lane + 1] : 0;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int u = __shfl_up_sync(0xffffffffu, v, d);
+            if (lane >= d) v += u;
+        }
+        if (e0 + lane < E) first[e0 + lane + 1] = run + v;
+        run += __shfl_sync(0xffffffffu, v, 31);
+    }
+    if (lane == 0) first[0] = 0;
+}
 
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, C::PER_SM) fp8_gemm_kernel(const __grid_constant__ CUtensorMap amap,
@@ -263,8 +264,9 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) fp8_gemm_kernel(const _
     __shared__ __align__(8) unsigned long long s_tfull[C::NT], s_tempty[C::NT];
     __shared__ __align__(8) unsigned long long s_sfull[C::SS], s_sempty[C::SS];
     __shared__ __align__(8) unsigned long long s_drain;
-    __shared__ __align__(16) float s_scale[C::SS][C::SF];
-    __shared__ int s_first[C::WG ? 1 : kMaxExperts + 1];
+    __shared__ __align__(16) float s_scale[C::SS][C::BT];
+    __shared__ float s_wscale[C::SS];
+    __shared__ int s_first[kMaxExperts + 1];
     __shared__ uint32_t s_taddr;
     __shared__ int s_fail, s_issued;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -293,27 +295,14 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) fp8_gemm_kernel(const _
                      ::"r"(smem_u32(&s_taddr)), "n"(C::TCOLS) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    if (!C::WG && p.offsets) {
+    if (p.offsets) {
         // column tiles of every expert; the running sum by one warp
         for (int e = tid; e < p.E; e += C::THREADS) {
             const int a = min(max(p.offsets[e], 0), p.nb), b = min(max(p.offsets[e + 1], a), p.nb);
             s_first[e + 1] = (b - a + C::BT - 1) / C::BT;
         }
         __syncthreads();
-        if (warp == 0) {
-            int run = 0;
-            for (int e0 = 0; e0 < p.E; e0 += 32) {
-                int v = e0 + lane < p.E ? s_first[e0 + lane + 1] : 0;
-#pragma unroll
-                for (int d = 1; d < 32; d *= 2) {
-                    const int u = __shfl_up_sync(0xffffffffu, v, d);
-                    if (lane >= d) v += u;
-                }
-                if (e0 + lane < p.E) s_first[e0 + lane + 1] = run + v;
-                run += __shfl_sync(0xffffffffu, v, 31);
-            }
-            if (lane == 0) s_first[0] = 0;
-        }
+        if (warp == 0) prefix_tiles(s_first, p.E, lane);
     }
     __syncthreads();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -336,19 +325,17 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) fp8_gemm_kernel(const _
     };
 
     if (warp < C::EW) {
-        // 384 threads x 168 registers at launch = 256 x 216 + 128 x 72
-        if constexpr (C::BIGREG) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-        // epilogue: lane quarter warp % 4, columns of part warp / 4
-        const int q4 = warp & 3, part_c = (warp >> 2) * C::CW;
-        const uint32_t trow = taddr + ((uint32_t)(32 * q4) << 16) + (uint32_t)part_c;
+        // epilogue: lane quarter warp % 4
+        const int q4 = warp & 3;
+        const uint32_t trow = taddr + ((uint32_t)(32 * q4) << 16);
         int it = 0;
         bool ok = true;
         for (int t = t0; t < total && ok; t += tstep) {
             Tile ti = walk.at(t);
             part(ti);
-            uint64_t acc[C::CW / 2];
+            uint64_t acc[C::BT / 2];
 #pragma unroll
-            for (int i = 0; i < C::CW / 2; i++) acc[i] = 0ull;
+            for (int i = 0; i < C::BT / 2; i++) acc[i] = 0ull;
             for (int kb = ti.k0; kb < ti.k1; kb++, it++) {
                 const int q = it % C::NT, s = it % C::SS;
                 const bool w = !*fail && mbar_wait(smem_u32(&s_sfull[s]), (uint32_t)(it / C::SS) & 1u) &&
@@ -359,19 +346,14 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) fp8_gemm_kernel(const _
                     break;
                 }
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                const uint32_t sc = smem_u32(&s_scale[s][part_c]);
-                uint64_t la = 0;
-                if (C::WG) {
-                    const uint32_t f = __float_as_uint(s_scale[s][C::BT + 32 * q4 + lane]);
-                    la = pack2(f, f);
-                }
-                constexpr int NL = C::CW / C::LD;
-                uint32_t r[2][C::LD];
-                tc_ld<C::LD>(trow + (uint32_t)(q * C::BT), r[0]);
+                const uint32_t sc = smem_u32(&s_scale[s][0]), f = __float_as_uint(s_wscale[s]);
+                const uint64_t ws = pack2(f, f);
+                constexpr int NL = C::BT / C::LD;
 #pragma unroll
                 for (int l = 0; l < NL; l++) {
-                    tc_wait_ld(r[l & 1]);
-                    if (l + 1 < NL) tc_ld<C::LD>(trow + (uint32_t)(q * C::BT + (l + 1) * C::LD), r[(l + 1) & 1]);
+                    uint32_t r[C::LD];
+                    tc_ld<C::LD>(trow + (uint32_t)(q * C::BT + l * C::LD), r);
+                    tc_wait_ld(r);
                     if (l + 1 == NL) {
                         // the accumulator is in registers: the slot may be written again
                         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -381,13 +363,9 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) fp8_gemm_kernel(const _
                     for (int i = 0; i < C::LD; i += 4) {
                         uint64_t s0, s1;
                         lds_2x64(sc + (uint32_t)(l * C::LD + i) * 4u, s0, s1);
-                        if (C::WG) {
-                            s0 = mul2(s0, la);
-                            s1 = mul2(s1, la);
-                        }
                         const int o = (l * C::LD + i) / 2;
-                        acc[o] = fma2(pack2(r[l & 1][i], r[l & 1][i + 1]), s0, acc[o]);
-                        acc[o + 1] = fma2(pack2(r[l & 1][i + 2], r[l & 1][i + 3]), s1, acc[o + 1]);
+                        acc[o] = fma2(pack2(r[i], r[i + 1]), mul2(s0, ws), acc[o]);
+                        acc[o + 1] = fma2(pack2(r[i + 2], r[i + 3]), mul2(s1, ws), acc[o + 1]);
                     }
                 }
                 __syncwarp();
@@ -399,22 +377,21 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) fp8_gemm_kernel(const _
                 // partial sums [column][lane] over the stage ring: every copy into it was consumed
                 float *ps = reinterpret_cast<float *>(smem_raw + (ring - smem_u32(smem_raw)));
 #pragma unroll
-                for (int i = 0; i < C::CW / 2; i++) {
+                for (int i = 0; i < C::BT / 2; i++) {
                     float x, y;
                     unpack2(acc[i], x, y);
-                    ps[(part_c + 2 * i) * kARows + 32 * q4 + lane] = x;
-                    ps[(part_c + 2 * i + 1) * kARows + 32 * q4 + lane] = y;
+                    ps[2 * i * kARows + 32 * q4 + lane] = x;
+                    ps[(2 * i + 1) * kARows + 32 * q4 + lane] = y;
                 }
             } else if (n < p.na) {
-                const int c = ti.b0 + part_c, cols = ti.bend - c;
-                const long long at = (C::WG ? (long long)ti.e * p.out_stride : 0ll) + (long long)c * p.ldo + n;
+                const int cols = ti.bend - ti.b0;
+                const long long at = (long long)ti.b0 * p.ldo + n;
                 if (p.out_dtype == MOE_DTYPE_F32) store_columns<float>(p.out, at, p.ldo, acc, cols);
                 else if (p.out_dtype == MOE_DTYPE_BF16) store_columns<__nv_bfloat16>(p.out, at, p.ldo, acc, cols);
                 else store_columns<__half>(p.out, at, p.ldo, acc, cols);
             }
         }
     } else {
-        if constexpr (C::BIGREG) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == C::EW) {
             // tensor copies
             if (lane == 0) {
@@ -432,7 +409,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) fp8_gemm_kernel(const _
                         }
                         const uint32_t bar = smem_u32(&s_full[j]), dst = ring + (uint32_t)(j * C::STAGE);
                         mbar_expect_tx(bar, C::STAGE);
-                        tma_load_3d(dst, &amap, kb * kKB, ti.a0, C::WG ? 0 : ti.e, bar);
+                        tma_load_3d(dst, &amap, kb * kKB, ti.a0, ti.e, bar);
                         tma_load_2d(dst + kABytes, &bmap, kb * kKB, ti.b0, bar);
                         s_issued = it + 1;
                     }
@@ -472,57 +449,33 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) fp8_gemm_kernel(const _
                 }
             }
         } else if (warp == C::EW + 2) {
-            // scales: column scales (times the weight block's scale) of every stage, four stages' loads at once
+            // scales: the columns' and the weight block's, copied asynchronously up to SS stages ahead
             int it = 0;
             bool ok = true;
-            constexpr int PB = (C::BT + 31) / 32, U = PB > 4 ? 2 : 4;
             for (int t = t0; t < total && ok; t += tstep) {
                 Tile ti = walk.at(t);
                 part(ti);
-                const float *sa = C::WG ? p.sa : p.sa + ((size_t)ti.e * ((p.na + kARows - 1) / kARows) + ti.a0 / kARows) * p.nkb;
-                for (int kb0 = ti.k0; kb0 < ti.k1 && ok; kb0 += U) {
-                    float v[U][PB], a[U][C::WG ? 4 : 1];
-    #pragma unroll
-                    for (int u = 0; u < U; u++) {
-                        const bool in = kb0 + u < ti.k1;
-                        const float *sb = p.sb + (size_t)(kb0 + u) * p.nb;
-    #pragma unroll
-                        for (int i = 0; i < PB; i++) {
-                            const int c = 32 * i + lane;
-                            v[u][i] = in && (C::BT >= 32 || c < C::BT) && ti.b0 + c < ti.bend ? __ldg(sb + ti.b0 + c) : 0.0f;
-                        }
-                        if (C::WG) {
-    #pragma unroll
-                            for (int i = 0; i < 4; i++) {
-                                const int c = ti.a0 + 32 * i + lane;
-                                a[u][i] = in && c < p.na ? __ldg(p.sa + (size_t)(kb0 + u) * p.na + c) : 0.0f;
-                            }
-                        } else {
-                            a[u][0] = in ? __ldg(sa + kb0 + u) : 0.0f;
-                        }
+                const float *sa = p.sa + ((size_t)ti.e * walk.nat + ti.a0 / kARows) * p.nkb;
+                for (int kb = ti.k0; kb < ti.k1; kb++, it++) {
+                    const int q = it % C::SS;
+                    const bool w = it < C::SS || mbar_wait(smem_u32(&s_sempty[q]), (uint32_t)(it / C::SS + 1) & 1u);
+                    if (!__all_sync(0xffffffffu, w && !*fail)) {
+                        *fail = 1;
+                        ok = false;
+                        break;
                     }
-    #pragma unroll
-                    for (int u = 0; u < U; u++) {
-                        if (kb0 + u >= ti.k1) break;
-                        const int q = it % C::SS;
-                        const bool w = it < C::SS || mbar_wait(smem_u32(&s_sempty[q]), (uint32_t)(it / C::SS + 1) & 1u);
-                        if (!__all_sync(0xffffffffu, w && !*fail)) {
-                            *fail = 1;
-                            ok = false;
-                            break;
-                        }
-    #pragma unroll
-                        for (int i = 0; i < PB; i++)
-                            if (C::BT >= 32 || lane < C::BT) s_scale[q][32 * i + lane] = C::WG ? v[u][i] : v[u][i] * a[u][0];
-                        if (C::WG) {
-    #pragma unroll
-                            for (int i = 0; i < 4; i++) s_scale[q][C::BT + 32 * i + lane] = a[u][i];
-                        }
-                        mbar_arrive(smem_u32(&s_sfull[q]));
-                        it++;
+                    const float *sb = p.sb + (size_t)kb * p.nb;
+#pragma unroll
+                    for (int i = 0; i < (C::BT + 31) / 32; i++) {
+                        const int c = 32 * i + lane;
+                        const bool in = ti.b0 + c < ti.bend;
+                        if (C::BT >= 32 || c < C::BT) cp_async4(smem_u32(&s_scale[q][c]), in ? sb + ti.b0 + c : p.sb, in);
                     }
+                    if (lane == 0) cp_async4(smem_u32(&s_wscale[q]), sa + kb, true);
+                    cp_async_arrive(smem_u32(&s_sfull[q]));
                 }
             }
+            asm volatile("cp.async.wait_all;" ::: "memory");
         }
     }
     __syncthreads();
@@ -552,6 +505,598 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) fp8_gemm_kernel(const _
     if (warp == C::EW + 3) {
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "n"(C::TCOLS) : "memory");
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Wide tiles: lanes are the rows of the output, columns its contiguous elements, 128 (PAIR: 256)
+// x 256.  PAIR: a cluster of two blocks shares a tile (cta_group::2: one MMA of M 256 over both
+// SMs' tensor cores), each block copying its own 128 rows of A and half of B: 32 KB for
+// 128 x 256 x 128 products instead of 48 KB, which is what an SM's path from L2 can carry at the
+// tensor cores' e4m3 rate (512 cycles a stage x 64 bytes).
+//   matmul  A = x (lanes: rows r), B = w (columns n): a lane's scale is one number per block and
+//           128 columns, so adding a block's product costs one two-wide fma per two elements.
+//   wgrad   (MX) A = dy, B = x, both column-quantised.  Their scales are powers of two, so the
+//           tensor core applies them itself (kind::mxf8f6f4, the float32's exponent byte is the
+//           ue8m0 scale) and the sums stay in tensor memory over the whole inner range: the
+//           registers see each output once.
+// ---------------------------------------------------------------------------
+
+template <bool PAIR_, bool MX_>
+struct WideCfg {
+    static constexpr bool PAIR = PAIR_, MX = MX_;
+    static constexpr int BN = 256;
+    static constexpr int ROWS = PAIR ? 256 : 128;             // rows of a tile
+    static constexpr int BROWS = PAIR ? 128 : 256;            // rows of B that one block copies
+    static constexpr int STAGE = kABytes + BROWS * kKB;
+    static constexpr int S = PAIR ? 5 : 3;
+    static constexpr int EW = 8;
+    static constexpr int THREADS = 32 * (EW + 4);
+    static constexpr int SS = 8;                              // scale ring (matmul)
+    static constexpr int SFBYTES = 512 + 1024;                // staged scales of a stage (MX): 128 + 256 words
+    static constexpr int SFCOLS = 12;                         // their tensor-memory columns: 4 + 8
+    static constexpr int OUTB = 4096;                         // staging of an epilogue warp: 32 rows x 128 bytes
+    static constexpr int ACC1 = MX ? 512 - SFCOLS * S - BN : BN;   // second accumulator (MX: overlaps the first)
+    static constexpr size_t SMEM = 1024 + (size_t)S * STAGE + EW * OUTB + (MX ? S * SFBYTES : 0);
+    // f8f6f4: D f32 at bit 4; mxf8f6f4: ue8m0 scales at bit 23
+    static constexpr uint32_t IDESC = (MX ? 1u << 23 : 1u << 4) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(ROWS >> 4) << 24);
+};
+
+// address of this shared variable in the cluster's first block
+__device__ __forceinline__ uint32_t in_leader(uint32_t saddr) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(saddr));
+    return a;
+}
+// arrival on a barrier of the other block.  No ordinary memory passes between the blocks (tensor
+// memory is ordered by tcgen05.fence, the scales by a proxy fence in their own block), so no
+// cluster-wide release: it costs a memory barrier of a microsecond (measured: 447 -> see below)
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t caddr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(caddr) : "memory");
+}
+template <bool PAIR>
+__device__ __forceinline__ void wide_load(uint32_t dst, const void *map, int x, int y, int z, uint32_t bar) {
+    if constexpr (PAIR)
+        asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+                     ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
+    else
+        tma_load_3d(dst, map, x, y, z, bar);
+}
+template <bool PAIR>
+__device__ __forceinline__ void wide_commit(uint32_t bar) {
+    if constexpr (PAIR)
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                     ::"r"(bar), "h"((uint16_t)3) : "memory");
+    else
+        tc_commit(bar);
+}
+template <bool PAIR>
+__device__ __forceinline__ void wide_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    if constexpr (PAIR)
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+                     ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+    else
+        mma_f8(d, a, b, idesc, acc);
+}
+template <bool PAIR>
+__device__ __forceinline__ void wide_mma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb, uint32_t acc) {
+    if constexpr (PAIR)
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+                     "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+                     ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc) : "memory");
+    else
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+                     "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+                     ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc) : "memory");
+}
+// 32 rows x 16 bytes of shared memory -> 4 columns of tensor memory, in all four lane quarters
+template <bool PAIR>
+__device__ __forceinline__ void wide_cp_scales(uint32_t taddr, uint64_t desc) {
+    if constexpr (PAIR)
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+struct WideArgs {
+    const float *sa;        // row scales of A [nkb][na] (wgrad: power of two)
+    const float *sb;        // matmul: block scales of B [E][ceil(nb / 128)][nkb]; wgrad: row scales [nkb][nb]
+    const int *offsets;     // [E + 1] or NULL
+    void *out;
+    long long ldo, out_stride;
+    int na, nb, nkb, E, out_dtype, vec;   // vec: every output row starts on a 16-byte boundary
+    unsigned *err;
+};
+
+// rows [r0, rend) (this block's 128), columns c0.., inner blocks [k0, k1) of expert e
+struct WideTile {
+    int e, r0, rend, c0, k0, k1;
+};
+
+template <class C>
+struct WideWalk {
+    const WideArgs &p;
+    const int *first;    // matmul with offsets: row tiles before each expert
+    int nct, nrt, e, rank;
+    __device__ WideWalk(const WideArgs &p_, const int *first_, int rank_)
+        : p(p_), first(first_), nct((p_.nb + C::BN - 1) / C::BN), nrt((p_.na + C::ROWS - 1) / C::ROWS), e(0), rank(rank_) {}
+    __device__ __forceinline__ int total() const { return nct * (C::MX ? p.E * nrt : (p.offsets ? first[p.E] : nrt)); }
+    __device__ __forceinline__ WideTile at(int t) {
+        WideTile r;
+        const int j = t / nct;
+        r.c0 = (t - j * nct) * C::BN;
+        r.k0 = 0;
+        r.k1 = p.nkb;
+        r.e = 0;
+        r.rend = p.na;
+        if (C::MX) {
+            r.e = j / nrt;
+            r.r0 = (j - r.e * nrt) * C::ROWS;
+            if (p.offsets) {
+                r.k0 = min(max(p.offsets[r.e], 0) / kKB, p.nkb);
+                r.k1 = min(max(p.offsets[r.e + 1] / kKB, r.k0), p.nkb);
+            }
+        } else if (p.offsets) {
+            while (first[e + 1] <= j) e++;
+            const int a = min(max(p.offsets[e], 0), p.na);
+            r.e = e;
+            r.r0 = a + (j - first[e]) * C::ROWS;
+            r.rend = min(max(p.offsets[e + 1], a), p.na);
+        } else {
+            r.r0 = j * C::ROWS;
+        }
+        r.r0 += 128 * rank;
+        return r;
+    }
+};
+
+// A warp's 32 rows x 32 float32 (64 16-bit) columns: packed values through shared memory (16-byte
+// chunks permuted by the row against bank conflicts) to full 128-byte stores; rows from `rows` on
+// and columns from `cols` on are not written.
+template <typename T>
+__device__ __forceinline__ void store_chunk(const uint4 (&v)[8], uint32_t stage, T *out, long long ldo, int rows, int cols, bool vec, int lane) {
+    constexpr int PER = 16 / (int)sizeof(T);       // elements of 16 bytes
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stage + (uint32_t)(lane * 128 + ((i ^ (lane & 7)) << 4))), "r"(v[i].x),
+                     "r"(v[i].y), "r"(v[i].z), "r"(v[i].w) : "memory");
+    __syncwarp();
+    if (vec && cols >= 8 * PER) {
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const int r = 4 * i + (lane >> 3), k = lane & 7;
+            uint4 u;
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                         : "r"(stage + (uint32_t)(r * 128 + ((k ^ (r & 7)) << 4))) : "memory");
+            if (r < rows) *reinterpret_cast<uint4 *>(out + (long long)r * ldo + k * PER) = u;
+        }
+    } else {
+        for (int r = 0; r < min(rows, 32); r++)
+            for (int c = lane; c < min(cols, 8 * PER); c += 32) {
+                const uint32_t a = stage + (uint32_t)(r * 128 + (((c / PER) ^ (r & 7)) << 4) + (c % PER) * (int)sizeof(T));
+                if constexpr (sizeof(T) == 4) {
+                    uint32_t u;
+                    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(u) : "r"(a) : "memory");
+                    reinterpret_cast<uint32_t *>(out)[(long long)r * ldo + c] = u;
+                } else {
+                    uint16_t u;
+                    asm volatile("ld.shared.b16 %0, [%1];" : "=h"(u) : "r"(a) : "memory");
+                    reinterpret_cast<uint16_t *>(out)[(long long)r * ldo + c] = u;
+                }
+            }
+    }
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack16(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pack16<__nv_bfloat16>(float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+template <>
+__device__ __forceinline__ uint32_t pack16<__half>(float a, float b) {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+// 64 columns' sums of a lane's row (two neighbours in each element of v)
+template <typename T>
+__device__ __forceinline__ void store_64(const uint64_t *v, uint32_t stage, void *out, long long at, long long ldo, int rows, int cols, bool vec, int lane) {
+    T *o = static_cast<T *>(out) + at;
+    uint4 q[8];
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                float a, b, c, d;
+                unpack2(v[16 * h + 2 * i], a, b);
+                unpack2(v[16 * h + 2 * i + 1], c, d);
+                q[i] = make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d));
+            }
+            if (cols > 32 * h) store_chunk<T>(q, stage, o + 32 * h, ldo, rows, cols - 32 * h, vec, lane);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                float a, b;
+                unpack2(v[4 * i + k], a, b);
+                w[k] = pack16<T>(a, b);
+            }
+            q[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        if (cols > 0) store_chunk<T>(q, stage, o, ldo, rows, cols, vec, lane);
+    }
+}
+__device__ __forceinline__ void store_cols(const uint64_t *v, uint32_t stage, const WideArgs &p, long long at, int rows, int cols, int lane) {
+    if (p.out_dtype == MOE_DTYPE_F32) store_64<float>(v, stage, p.out, at, p.ldo, rows, cols, p.vec, lane);
+    else if (p.out_dtype == MOE_DTYPE_BF16) store_64<__nv_bfloat16>(v, stage, p.out, at, p.ldo, rows, cols, p.vec, lane);
+    else store_64<__half>(v, stage, p.out, at, p.ldo, rows, cols, p.vec, lane);
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_constant__ CUtensorMap amap,
+                                                                 const __grid_constant__ CUtensorMap bmap,
+                                                                 const WideArgs p) {
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ __align__(8) unsigned long long s_full[C::S], s_empty[C::S];
+    __shared__ __align__(8) unsigned long long s_tfull[2], s_tempty[2];
+    __shared__ __align__(8) unsigned long long s_sfull[C::SS], s_sempty[C::SS];   // MX: s_sfull by stage
+    __shared__ __align__(8) unsigned long long s_drain;
+    __shared__ float s_scale[C::MX ? 1 : C::SS][128], s_wscale[C::MX ? 1 : C::SS][2];   // matmul: rows', weight blocks'
+    __shared__ int s_first[C::MX ? 1 : kMaxExperts + 1];
+    __shared__ uint32_t s_taddr;
+    __shared__ int s_fail, s_issued;
+    static_assert(C::S <= C::SS, "a scale barrier for every stage");
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t staging = ring + (uint32_t)(C::S * C::STAGE), sfring = staging + (uint32_t)(C::EW * C::OUTB);
+    const int rank = C::PAIR ? (int)cluster_rank() : 0;
+    constexpr int NB = C::PAIR ? 2 : 1;      // blocks of a tile
+
+    if (tid == 0) {
+        s_fail = 0;
+        s_issued = 0;
+        for (int i = 0; i < C::S; i++) {
+            mbar_init(smem_u32(&s_full[i]), 1);
+            mbar_init(smem_u32(&s_empty[i]), 1);
+        }
+        for (int i = 0; i < 2; i++) {
+            mbar_init(smem_u32(&s_tfull[i]), 1);
+            mbar_init(smem_u32(&s_tempty[i]), NB * C::EW);
+        }
+        for (int i = 0; i < C::SS; i++) {
+            mbar_init(smem_u32(&s_sfull[i]), C::MX ? NB * 32 : 32);
+            mbar_init(smem_u32(&s_sempty[i]), C::EW);
+        }
+        mbar_init(smem_u32(&s_drain), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == C::EW + 3) {
+        if constexpr (C::PAIR) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_taddr)) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_taddr)) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        }
+    }
+    if (!C::MX && p.offsets) {
+        for (int e = tid; e < p.E; e += C::THREADS) {
+            const int a = min(max(p.offsets[e], 0), p.na), b = min(max(p.offsets[e + 1], a), p.na);
+            s_first[e + 1] = (b - a + C::ROWS - 1) / C::ROWS;
+        }
+        __syncthreads();
+        if (warp == 0) prefix_tiles(s_first, p.E, lane);
+    }
+    __syncthreads();
+    if (C::PAIR) cluster_sync_all();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    const uint32_t taddr = s_taddr;
+    volatile int *fail = &s_fail;
+    WideWalk<C> walk(p, s_first, rank);
+    const int total = walk.total(), t0 = (int)blockIdx.x / NB, tstep = (int)gridDim.x / NB;
+
+    if (warp < C::EW) {
+        // 384 threads x 168 registers at launch = 256 x 216 + 128 x 72
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        const int q4 = warp & 3, half = warp >> 2;          // lane quarter, 128-column half
+        const uint32_t trow = taddr + ((uint32_t)(32 * q4) << 16);
+        const uint32_t stage = staging + (uint32_t)(warp * C::OUTB);
+        const uint32_t te0 = C::PAIR ? in_leader(smem_u32(&s_tempty[0])) : smem_u32(&s_tempty[0]);
+        auto release = [&](int q) {      // tensor-memory part q of this tile is in registers
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            if (lane == 0) {
+                if (C::PAIR) mbar_arrive_cluster(te0 + 8u * q);
+                else mbar_arrive(te0 + 8u * q);
+            }
+        };
+        int it = 0, done = 0;
+        bool ok = true;
+        for (int t = t0; t < total && ok; t += tstep) {
+            const WideTile ti = walk.at(t);
+            const int row = ti.r0 + 32 * q4, rows = ti.rend - row, c0 = ti.c0 + 128 * half, cols = p.nb - c0;
+            const long long at = (C::MX ? (long long)ti.e * p.out_stride : 0ll) + (long long)row * p.ldo + c0;
+            if constexpr (C::MX) {
+                const int q = done & 1;
+                if (ti.k0 == ti.k1) {      // an expert without rows
+                    uint64_t z[32];
+#pragma unroll
+                    for (int i = 0; i < 32; i++) z[i] = 0ull;
+                    for (int c = 0; c < 128; c += 64)
+                        if (rows > 0) store_cols(z, stage, p, at + c, rows, cols - c, lane);
+                    continue;
+                }
+                const bool w = !*fail && mbar_wait(smem_u32(&s_tfull[q]), (uint32_t)(done >> 1) & 1u);
+                if (!__all_sync(0xffffffffu, w)) {
+                    *fail = 1;
+                    ok = false;
+                    break;
+                }
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                // the accumulators overlap: the first one's last columns are the second one's first,
+                // so those 64 columns leave first and the next tile may start
+                const int first = q ? 0 : 64;
+                const uint32_t base = trow + (uint32_t)((q ? C::ACC1 : 0) + 128 * half);
+#pragma unroll 1
+                for (int h = 0; h < 2; h++) {
+                    const int c = h ? 64 - first : first;
+                    uint32_t r0[32], r1[32];
+                    tc_ld<32>(base + (uint32_t)c, r0);
+                    tc_ld<32>(base + (uint32_t)c + 32, r1);
+                    tc_wait_ld(r0);
+                    tc_wait_ld(r1);
+                    if (h == 0) release(0);
+                    uint64_t v[32];
+#pragma unroll
+                    for (int i = 0; i < 16; i++) {
+                        v[i] = pack2(r0[2 * i], r0[2 * i + 1]);
+                        v[16 + i] = pack2(r1[2 * i], r1[2 * i + 1]);
+                    }
+                    if (rows > 0) store_cols(v, stage, p, at + c, rows, cols - c, lane);
+                }
+                done++;
+            } else {
+                uint64_t acc[64];
+#pragma unroll
+                for (int i = 0; i < 64; i++) acc[i] = 0ull;
+                for (int kb = ti.k0; kb < ti.k1; kb++, it++) {
+                    const int q = it & 1, s = it % C::SS;
+                    const bool w = !*fail && mbar_wait(smem_u32(&s_sfull[s]), (uint32_t)(it / C::SS) & 1u) &&
+                                   mbar_wait(smem_u32(&s_tfull[q]), (uint32_t)(it >> 1) & 1u);
+                    if (!__all_sync(0xffffffffu, w)) {
+                        *fail = 1;
+                        ok = false;
+                        break;
+                    }
+                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    const uint32_t f = __float_as_uint(s_scale[s][32 * q4 + lane] * s_wscale[s][half]);
+                    const uint64_t sc = pack2(f, f);
+                    const uint32_t base = trow + (uint32_t)(256 * q + 128 * half);
+                    uint32_t r[2][32];
+                    tc_ld<32>(base, r[0]);
+#pragma unroll
+                    for (int l = 0; l < 4; l++) {
+                        tc_wait_ld(r[l & 1]);
+                        if (l < 3) tc_ld<32>(base + (uint32_t)(32 * (l + 1)), r[(l + 1) & 1]);
+                        else release(q);
+#pragma unroll
+                        for (int i = 0; i < 16; i++) acc[16 * l + i] = fma2(pack2(r[l & 1][2 * i], r[l & 1][2 * i + 1]), sc, acc[16 * l + i]);
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&s_sempty[s]));
+                }
+                if (!ok) break;
+                if (rows > 0) {
+                    store_cols(acc, stage, p, at, rows, cols, lane);
+                    store_cols(acc + 32, stage, p, at + 64, rows, cols - 64, lane);
+                }
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp == C::EW) {
+            // tensor copies: this block's rows of A and its part of B
+            if (lane == 0) {
+                int it = 0;
+                bool ok = true;
+                for (int t = t0; t < total && ok; t += tstep) {
+                    const WideTile ti = walk.at(t);
+                    for (int kb = ti.k0; kb < ti.k1; kb++, it++) {
+                        const int j = it % C::S;
+                        if (*fail || (it >= C::S && !mbar_wait(smem_u32(&s_empty[j]), (uint32_t)(it / C::S + 1) & 1u))) {
+                            *fail = 1;
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t bar = smem_u32(&s_full[j]), dst = ring + (uint32_t)(j * C::STAGE);
+                        if (rank == 0) mbar_expect_tx(bar, NB * C::STAGE);
+                        const uint32_t lbar = C::PAIR ? in_leader(bar) : bar;
+                        wide_load<C::PAIR>(dst, &amap, kb * kKB, ti.r0, 0, lbar);
+                        wide_load<C::PAIR>(dst + kABytes, &bmap, kb * kKB, ti.c0 + rank * C::BROWS, C::MX ? 0 : ti.e, lbar);
+                        s_issued = it + 1;
+                    }
+                }
+            }
+        } else if (warp == C::EW + 1) {
+            // MMA issue (by the tile's first block)
+            if (lane == 0 && rank == 0) {
+                int it = 0, tile = 0;
+                bool ok = true;
+                const uint64_t ad0 = sw128_desc(ring), bd0 = sw128_desc(ring + kABytes);
+                for (int t = t0; t < total && ok; t += tstep) {
+                    const WideTile ti = walk.at(t);
+                    const int k1 = ti.k1;
+                    // MX: the previous tile's overlapping columns are in registers (its epilogue follows
+                    // that of the tile before it, which used this accumulator)
+                    if (C::MX && ti.k0 < k1 && tile > 0 && !mbar_wait(smem_u32(&s_tempty[0]), (uint32_t)(tile - 1) & 1u)) {
+                        *fail = 1;
+                        ok = false;
+                        break;
+                    }
+                    for (int kb = ti.k0; kb < k1; kb++, it++) {
+                        const int j = it % C::S, q = it & 1;
+                        bool w = !*fail;
+                        if (!C::MX && w && it >= 2) w = mbar_wait(smem_u32(&s_tempty[q]), (uint32_t)((it >> 1) + 1) & 1u);
+                        if (C::MX && w) w = mbar_wait(smem_u32(&s_sfull[j]), (uint32_t)(it / C::S) & 1u);
+                        if (!w || !mbar_wait(smem_u32(&s_full[j]), (uint32_t)(it / C::S) & 1u)) {
+                            *fail = 1;
+                            ok = false;
+                            break;
+                        }
+                        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                        const uint64_t off = (uint64_t)((j * C::STAGE) >> 4);
+                        if constexpr (C::MX) {
+                            // shared-memory operand of the scale copies: 8-row groups of 16 bytes 128 bytes apart, no swizzle
+                            const uint32_t sf = sfring + (uint32_t)(j * C::SFBYTES), tsf = taddr + (uint32_t)(512 - C::SFCOLS * (C::S - j));
+                            const uint64_t sd = (uint64_t)((sf >> 4) & 0x3FFF) | (1ull << 16) | ((uint64_t)(128 >> 4) << 32) | (1ull << 46);
+#pragma unroll
+                            for (int i = 0; i < 3; i++) wide_cp_scales<C::PAIR>(tsf + 4 * i, sd + (uint64_t)(i * (512 >> 4)));
+                            const uint32_t d = taddr + (uint32_t)((tile & 1) ? C::ACC1 : 0);
+#pragma unroll
+                            for (int ks = 0; ks < 4; ks++)
+                                wide_mma_mx<C::PAIR>(d, ad0 + off + 2 * ks, bd0 + off + 2 * ks, C::IDESC, tsf, tsf + 4, kb > ti.k0 || ks > 0);
+                        } else {
+                            const uint32_t d = taddr + (uint32_t)(256 * q);
+#pragma unroll
+                            for (int ks = 0; ks < 4; ks++) wide_mma<C::PAIR>(d, ad0 + off + 2 * ks, bd0 + off + 2 * ks, C::IDESC, ks > 0);
+                        }
+                        wide_commit<C::PAIR>(smem_u32(&s_empty[j]));
+                        if (!C::MX) wide_commit<C::PAIR>(smem_u32(&s_tfull[q]));
+                        else if (kb + 1 == k1) wide_commit<C::PAIR>(smem_u32(&s_tfull[tile & 1]));
+                    }
+                    if (ti.k0 < k1) tile++;
+                }
+                if (it > 0) {
+                    // every MMA is done before the shared memory and the tensor memory go (bounded)
+                    if constexpr (C::PAIR)
+                        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(&s_drain)) : "memory");
+                    else
+                        tc_commit(smem_u32(&s_drain));
+                    if (!mbar_wait(smem_u32(&s_drain), 0u)) *fail = 1;
+                }
+            }
+        } else if constexpr (!C::MX) {
+            if (warp == C::EW + 2) {
+                // scales: the rows' and the two weight blocks', copied asynchronously up to SS stages ahead
+                int it = 0;
+                bool ok = true;
+                const int nbb = (p.nb + kKB - 1) / kKB;
+                for (int t = t0; t < total && ok; t += tstep) {
+                    const WideTile ti = walk.at(t);
+                    const float *sw = p.sb + ((size_t)ti.e * nbb + ti.c0 / kKB + (lane & 1)) * p.nkb;
+                    const bool in_w = ti.c0 + kKB * (lane & 1) < p.nb;
+                    for (int kb = ti.k0; kb < ti.k1; kb++, it++) {
+                        const int s = it % C::SS;
+                        const bool w = it < C::SS || mbar_wait(smem_u32(&s_sempty[s]), (uint32_t)(it / C::SS + 1) & 1u);
+                        if (!__all_sync(0xffffffffu, w && !*fail)) {
+                            *fail = 1;
+                            ok = false;
+                            break;
+                        }
+                        const float *sr = p.sa + (size_t)kb * p.na;
+#pragma unroll
+                        for (int i = 0; i < 4; i++) {
+                            const int r = ti.r0 + 32 * i + lane;
+                            cp_async4(smem_u32(&s_scale[s][32 * i + lane]), r < p.na ? sr + r : p.sa, r < p.na);
+                        }
+                        if (lane < 2) cp_async4(smem_u32(&s_wscale[s][lane]), in_w ? sw + kb : p.sb, in_w);
+                        cp_async_arrive(smem_u32(&s_sfull[s]));
+                    }
+                }
+                asm volatile("cp.async.wait_all;" ::: "memory");
+            }
+        } else {
+            // scales: the exponent bytes of this block's 128 rows of A and all 256 of B, by two warps in
+            // turn, each D of its stages ahead in registers
+            constexpr int D = 3;
+            int t = t0, kb = 0, n = 0, mine = warp - (C::EW + 2);    // next stage to load: its tile, block and number
+            WideTile ti = {};
+            bool live = t < total;
+            if (live) {
+                ti = walk.at(t);
+                kb = ti.k0;
+            }
+            float v[D][12];
+            int num[D];
+            auto load = [&](float (&d)[12]) {
+                // this warp's next stage into d; its number, -1 behind the last
+                for (;;) {
+                    while (live && kb >= ti.k1) {
+                        t += tstep;
+                        live = t < total;
+                        if (live) {
+                            ti = walk.at(t);
+                            kb = ti.k0;
+                        }
+                    }
+                    if (!live) return -1;
+                    if (n == mine) break;
+                    const int skip = min(mine - n, ti.k1 - kb);
+                    n += skip;
+                    kb += skip;
+                }
+#pragma unroll
+                for (int i = 0; i < 12; i++) {
+                    const int r = (i < 4 ? ti.r0 : ti.c0 - 128) + 32 * i + lane;
+                    d[i] = r < (i < 4 ? p.na : p.nb) ? __ldg(i < 4 ? p.sa + (size_t)kb * p.na + r : p.sb + (size_t)kb * p.nb + r) : 0.0f;
+                }
+                mine += 2;
+                n++;
+                kb++;
+                return n - 1;
+            };
+#pragma unroll
+            for (int d = 0; d < D; d++) num[d] = load(v[d]);
+            bool ok = true;
+            while (ok) {
+#pragma unroll
+                for (int d = 0; d < D; d++) {
+                    const int it = num[d];
+                    if (it < 0) ok = false;
+                    if (!ok) break;
+                    const int s = it % C::S;
+                    const bool w = it < C::S || mbar_wait(smem_u32(&s_empty[s]), (uint32_t)(it / C::S + 1) & 1u);
+                    if (!__all_sync(0xffffffffu, w && !*fail)) {
+                        *fail = 1;
+                        ok = false;
+                        break;
+                    }
+                    // word of row r: 16-byte line r % 32, its (r / 32) % 4-th word, 512 bytes per 128 rows
+                    const uint32_t sf = sfring + (uint32_t)(s * C::SFBYTES + lane * 16);
+#pragma unroll
+                    for (int i = 0; i < 3; i++) {
+                        uint32_t b[4];
+#pragma unroll
+                        for (int k = 0; k < 4; k++) b[k] = ((__float_as_uint(v[d][4 * i + k]) >> 23) & 0xFFu) * 0x01010101u;
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sf + (uint32_t)(i * 512)), "r"(b[0]), "r"(b[1]), "r"(b[2]), "r"(b[3]) : "memory");
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    if (C::PAIR) mbar_arrive_cluster(in_leader(smem_u32(&s_sfull[s])));
+                    else mbar_arrive(smem_u32(&s_sfull[s]));
+                    num[d] = load(v[d]);
+                }
+            }
+        }
+    }
+    __syncthreads();
+    if (s_fail && tid == 0) {
+        // after a wait that ran out: copies still in flight land before the shared memory goes (bounded)
+        if (rank == 0)
+            for (int i = max(0, s_issued - C::S); i < s_issued; i++) mbar_wait(smem_u32(&s_full[i % C::S]), (uint32_t)(i / C::S) & 1u);
+        atomicOr(p.err, MOE_DEVICE_ERR_TC);
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    if (C::PAIR) cluster_sync_all();     // the other block's MMAs, copies and arrivals reach into this one's memory
+    if (warp == C::EW + 3) {
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        if constexpr (C::PAIR) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(taddr) : "memory");
+        else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(taddr) : "memory");
     }
 }
 
@@ -887,6 +1432,34 @@ cudaError_t launch_gemm(const GemmArgs &p, const CUtensorMap &am, const uint8_t 
     return cudaLaunchKernelEx(&cfg, fp8_gemm_kernel<C>, am, bm, p);
 }
 
+template <class C>
+cudaError_t launch_wide(const WideArgs &p, const uint8_t *a, uint64_t a_cols, const uint8_t *b, uint64_t b_cols, uint64_t b_mats,
+                        long long tiles, cudaStream_t st) {
+    CUtensorMap am, bm;
+    if (!tmap(&am, 3, a, a_cols, p.na, 1, 128) || !tmap(&bm, 3, b, b_cols, p.nb, b_mats, C::BROWS)) return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(fp8_wide_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    const long long nb = C::PAIR ? 2 : 1, most = sm_count() / nb;
+    cfg.gridDim = dim3((unsigned)(nb * (tiles < most ? tiles : most)));
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)nb;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = C::PAIR ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, fp8_wide_kernel<C>, am, bm, p);
+}
+
+bool rows_aligned(const void *out, long long ldo, int dtype) {
+    const int el = dtype == MOE_DTYPE_F32 ? 4 : 2;
+    return (reinterpret_cast<uintptr_t>(out) & 15u) == 0 && ldo * el % 16 == 0;
+}
+
 }  // namespace
 
 cudaError_t launch_fp8_matmul(const uint8_t *x, const float *xs, int R, const uint8_t *w, const float *ws, int E, int N, int K,
@@ -922,39 +1495,56 @@ cudaError_t launch_fp8_matmul(const uint8_t *x, const float *xs, int R, const ui
         return launch_gemm<C>(p, am, x, K, R, tiles(C::BT), 2, cs, st);
     };
     if (each <= 16) {
-        if (tiles(16) <= 2 * sm_count()) return go_split(Cfg<16, 1, false, true, 5>{});
-        return go(Cfg<16, 1, false, false, 5>{}, 2);
+        if (tiles(16) <= 2 * sm_count()) return go_split(Cfg<16, true, 5>{});
+        return go(Cfg<16, false, 5>{}, 2);
     }
     if (each <= 64) {
-        if (tiles(64) <= 2 * sm_count()) return go_split(Cfg<64, 1, false, true, 4>{});
-        return go(Cfg<64, 1, false, false, 4>{}, 2);
+        if (tiles(64) <= 2 * sm_count()) return go_split(Cfg<64, true, 4>{});
+        return go(Cfg<64, false, 4>{}, 2);
     }
-    if (each <= 256) return go(Cfg<128, 2, false, false, 6>{}, 1);
-    return go(Cfg<256, 2, false, false, 4>{}, 1);
+    WideArgs q = {};
+    q.sa = xs;
+    q.sb = ws;
+    q.offsets = offsets;
+    q.out = y;
+    q.ldo = ldy;
+    q.na = R;
+    q.nb = N;
+    q.nkb = p.nkb;
+    q.E = E;
+    q.out_dtype = y_dtype;
+    q.vec = rows_aligned(y, ldy, y_dtype);
+    q.err = p.err;
+    const long long nct = (N + 255) / 256;
+    auto wide = [&](auto c) {
+        using C = decltype(c);
+        return launch_wide<C>(q, x, K, w, K, E, nct * (offsets ? (long long)R / C::ROWS + used : ((long long)R + C::ROWS - 1) / C::ROWS), st);
+    };
+    if (each <= 256) return wide(WideCfg<false, false>{});
+    return wide(WideCfg<true, false>{});
 }
 
 cudaError_t launch_fp8_wgrad(const uint8_t *xt, const float *xs, const uint8_t *dyt, const float *dys, int R, int N, int K, int E,
                              const int *offsets, void *dw, int dw_dtype, cudaStream_t st) {
     if (!tmap_encoder()) return cudaErrorNotSupported;
-    GemmArgs p = {};
-    p.sa = xs;
-    p.sb = dys;
+    WideArgs p = {};
+    p.sa = dys;
+    p.sb = xs;
     p.offsets = offsets;
     p.out = dw;
     p.ldo = K;
     p.out_stride = (long long)N * K;
-    p.na = K;
-    p.nb = N;
+    p.na = N;
+    p.nb = K;
     p.nkb = R / kKB;
     p.E = E;
     p.out_dtype = dw_dtype;
-    cudaError_t e = error_word(&p.err);
+    p.vec = rows_aligned(dw, K, dw_dtype);
+    const cudaError_t e = error_word(&p.err);
     if (e != cudaSuccess) return e;
-    CUtensorMap am;
-    if (!tmap(&am, 3, xt, R, K, 1, kARows)) return cudaErrorInvalidValue;
-    using C = Cfg<128, 2, true, false, 6>;
-    const long long tiles = (long long)E * ((K + kARows - 1) / kARows) * ((N + C::BT - 1) / C::BT);
-    return launch_gemm<C>(p, am, dyt, R, N, tiles, 1, 1, st);
+    using C = WideCfg<true, true>;
+    const long long tiles = (long long)E * ((N + C::ROWS - 1) / C::ROWS) * ((K + C::BN - 1) / C::BN);
+    return launch_wide<C>(p, dyt, R, xt, R, 1, tiles, st);
 }
 
 cudaError_t fp8_error_read(unsigned *flags) {
