@@ -89,40 +89,77 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint3
                  "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
                  ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
 }
+// N columns of this lane from tensor memory, and the wait for them: one block of code, so that the
+// registers are not named before they are filled (a separate wait that names them costs a move each)
 template <int N>
 __device__ __forceinline__ void tc_ld(uint32_t taddr, uint32_t (&r)[N]) {
-    static_assert(N == 16 || N == 32, "columns of a load");
-    if constexpr (N == 32) {
-        asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-                     "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+    static_assert(N == 16 || N == 32 || N == 64, "columns of a load");
+    if constexpr (N == 64) {
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+                     "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                     "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+                     "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+                     "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
+                     "tcgen05.wait::ld.sync.aligned;"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                       "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+                       "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+                       "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+                       "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+                       "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+                       "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+                       "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+                     : "r"(taddr) : "memory");
+    } else if constexpr (N == 32) {
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+                     "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                     "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+                     "tcgen05.wait::ld.sync.aligned;"
                      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
                        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
                        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
                        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-                     : "r"(taddr));
+                     : "r"(taddr) : "memory");
     } else {
-        asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+                     "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+                     "tcgen05.wait::ld.sync.aligned;"
                      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
                        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-                     : "r"(taddr));
+                     : "r"(taddr) : "memory");
     }
 }
-// waits for this warp's tensor-memory loads; names the registers so that no use of them moves above it
+// one lane of a converged warp, chosen so that the compiler keeps the warp's values in uniform
+// registers: the tensor copies and MMAs take their operands there, and a branch on the lane number
+// costs ~100 cycles for each of them (measured: 980 cycles a stage in the issuing thread, 512 of
+// tensor work)
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+// mbar_wait that also gives up once another role of the block has
+__device__ __forceinline__ bool ring_wait(uint32_t bar, uint32_t parity, const volatile int *fail) {
+    if (mbar_try(bar, parity)) return true;
+    const unsigned long long t0 = tc_now();
+    for (;;) {
+        for (int i = 0; i < 64; i++)
+            if (mbar_try(bar, parity)) return true;
+        if (*fail || tc_now() - t0 > kTcWaitNs) return false;
+    }
+}
+// slot and phase of a ring of N, counted without divisions
 template <int N>
-__device__ __forceinline__ void tc_wait_ld(uint32_t (&r)[N]) {
-#pragma unroll
-    for (int i = 0; i < N; i += 16) {
-        if (i == 0)
-            asm volatile("tcgen05.wait::ld.sync.aligned;"
-                         : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                           "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-                         :: "memory");
-        else
-            asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
-                              "+r"(r[i + 6]), "+r"(r[i + 7]), "+r"(r[i + 8]), "+r"(r[i + 9]), "+r"(r[i + 10]), "+r"(r[i + 11]),
-                              "+r"(r[i + 12]), "+r"(r[i + 13]), "+r"(r[i + 14]), "+r"(r[i + 15]) :: "memory");
+struct Ring {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++slot == N) {
+            slot = 0;
+            phase ^= 1u;
+        }
     }
-}
+};
 // 4-byte asynchronous copy global -> shared; !in: zeros
 __device__ __forceinline__ void cp_async4(uint32_t dst, const float *src, bool in) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
@@ -269,7 +306,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) fp8_gemm_kernel(const _
     __shared__ int s_first[kMaxExperts + 1];
     __shared__ uint32_t s_taddr;
     __shared__ int s_fail, s_issued;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
 
     if (tid == 0) {
@@ -328,7 +365,8 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) fp8_gemm_kernel(const _
         // epilogue: lane quarter warp % 4
         const int q4 = warp & 3;
         const uint32_t trow = taddr + ((uint32_t)(32 * q4) << 16);
-        int it = 0;
+        Ring<C::NT> tq;
+        Ring<C::SS> ts;
         bool ok = true;
         for (int t = t0; t < total && ok; t += tstep) {
             Tile ti = walk.at(t);
@@ -336,15 +374,16 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) fp8_gemm_kernel(const _
             uint64_t acc[C::BT / 2];
 #pragma unroll
             for (int i = 0; i < C::BT / 2; i++) acc[i] = 0ull;
-            for (int kb = ti.k0; kb < ti.k1; kb++, it++) {
-                const int q = it % C::NT, s = it % C::SS;
-                const bool w = !*fail && mbar_wait(smem_u32(&s_sfull[s]), (uint32_t)(it / C::SS) & 1u) &&
-                               mbar_wait(smem_u32(&s_tfull[q]), (uint32_t)(it / C::NT) & 1u);
-                if (!__all_sync(0xffffffffu, w)) {
+            for (int kb = ti.k0; kb < ti.k1; kb++) {
+                const int q = tq.slot, s = ts.slot;
+                if (!__all_sync(0xffffffffu, ring_wait(smem_u32(&s_sfull[s]), ts.phase, fail) &&
+                                                 ring_wait(smem_u32(&s_tfull[q]), tq.phase, fail))) {
                     *fail = 1;
                     ok = false;
                     break;
                 }
+                tq.next();
+                ts.next();
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 const uint32_t sc = smem_u32(&s_scale[s][0]), f = __float_as_uint(s_wscale[s]);
                 const uint64_t ws = pack2(f, f);
@@ -353,7 +392,6 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) fp8_gemm_kernel(const _
                 for (int l = 0; l < NL; l++) {
                     uint32_t r[C::LD];
                     tc_ld<C::LD>(trow + (uint32_t)(q * C::BT + l * C::LD), r);
-                    tc_wait_ld(r);
                     if (l + 1 == NL) {
                         // the accumulator is in registers: the slot may be written again
                         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -394,76 +432,83 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) fp8_gemm_kernel(const _
     } else {
         if (warp == C::EW) {
             // tensor copies
-            if (lane == 0) {
-                int it = 0;
-                for (int t = t0; t < total; t += tstep) {
-                    Tile ti = walk.at(t);
-                    part(ti);
-                    bool ok = true;
-                    for (int kb = ti.k0; kb < ti.k1; kb++, it++) {
-                        const int j = it % C::S;
-                        if (*fail || (it >= C::S && !mbar_wait(smem_u32(&s_empty[j]), (uint32_t)(it / C::S + 1) & 1u))) {
-                            *fail = 1;
-                            ok = false;
-                            break;
-                        }
-                        const uint32_t bar = smem_u32(&s_full[j]), dst = ring + (uint32_t)(j * C::STAGE);
+            Ring<C::S> r;
+            bool ok = true;
+            int n = 0;
+            for (int t = t0; t < total && ok; t += tstep) {
+                Tile ti = walk.at(t);
+                part(ti);
+                for (int kb = ti.k0; kb < ti.k1; kb++) {
+                    // a fresh ring's slots pass: the phase before the first is over
+                    if (!__all_sync(0xffffffffu, ring_wait(smem_u32(&s_empty[r.slot]), r.phase ^ 1u, fail))) {
+                        ok = false;
+                        break;
+                    }
+                    if (elect_one()) {
+                        const uint32_t bar = smem_u32(&s_full[r.slot]), dst = ring + (uint32_t)(r.slot * C::STAGE);
                         mbar_expect_tx(bar, C::STAGE);
                         tma_load_3d(dst, &amap, kb * kKB, ti.a0, ti.e, bar);
                         tma_load_2d(dst + kABytes, &bmap, kb * kKB, ti.b0, bar);
-                        s_issued = it + 1;
                     }
-                    if (!ok) break;
+                    r.next();
+                    n++;
                 }
             }
+            if (lane == 0) s_issued = n;
+            if (!ok) *fail = 1;
         } else if (warp == C::EW + 1) {
             // MMA issue: one fresh accumulator of the ring per stage
-            if (lane == 0) {
-                int it = 0;
-                bool ok = true;
-                const uint64_t ad0 = sw128_desc(ring), bd0 = sw128_desc(ring + kABytes);
-                for (int t = t0; t < total && ok; t += tstep) {
-                    Tile ti = walk.at(t);
-                    part(ti);
-                    for (int kb = ti.k0; kb < ti.k1; kb++, it++) {
-                        const int j = it % C::S, q = it % C::NT;
-                        if (*fail || (it >= C::NT && !mbar_wait(smem_u32(&s_tempty[q]), (uint32_t)(it / C::NT + 1) & 1u)) ||
-                            !mbar_wait(smem_u32(&s_full[j]), (uint32_t)(it / C::S) & 1u)) {
-                            *fail = 1;
-                            ok = false;
-                            break;
-                        }
-                        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                        const uint64_t off = (uint64_t)((j * C::STAGE) >> 4);
-                        const uint32_t d = taddr + (uint32_t)(q * C::BT);
-    #pragma unroll
+            Ring<C::S> r;
+            Ring<C::NT> q;
+            bool ok = true, any = false;
+            const uint64_t ad0 = sw128_desc(ring), bd0 = sw128_desc(ring + kABytes);
+            for (int t = t0; t < total && ok; t += tstep) {
+                Tile ti = walk.at(t);
+                part(ti);
+                for (int kb = ti.k0; kb < ti.k1; kb++) {
+                    if (!__all_sync(0xffffffffu, ring_wait(smem_u32(&s_tempty[q.slot]), q.phase ^ 1u, fail) &&
+                                                     ring_wait(smem_u32(&s_full[r.slot]), r.phase, fail))) {
+                        ok = false;
+                        break;
+                    }
+                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    if (elect_one()) {
+                        const uint64_t off = (uint64_t)((r.slot * C::STAGE) >> 4);
+                        const uint32_t d = taddr + (uint32_t)(q.slot * C::BT);
+#pragma unroll
                         for (int ks = 0; ks < 4; ks++)
                             mma_f8(d, ad0 + off + 2 * ks, bd0 + off + 2 * ks, C::IDESC, ks > 0);
-                        tc_commit(smem_u32(&s_empty[j]));
-                        tc_commit(smem_u32(&s_tfull[q]));
+                        tc_commit(smem_u32(&s_empty[r.slot]));
+                        tc_commit(smem_u32(&s_tfull[q.slot]));
                     }
+                    r.next();
+                    q.next();
+                    any = true;
                 }
-                if (it > 0 || !ok) {
-                    tc_commit(smem_u32(&s_drain));
-                    if (!mbar_wait(smem_u32(&s_drain), 0u)) *fail = 1;
-                }
+            }
+            if (!ok) *fail = 1;
+            if (any) {
+                // every MMA is done before the shared memory and the tensor memory go (bounded)
+                __syncwarp();
+                if (elect_one()) tc_commit(smem_u32(&s_drain));
+                if (!mbar_wait(smem_u32(&s_drain), 0u)) *fail = 1;
             }
         } else if (warp == C::EW + 2) {
             // scales: the columns' and the weight block's, copied asynchronously up to SS stages ahead
-            int it = 0;
+            Ring<C::SS> s;
             bool ok = true;
             for (int t = t0; t < total && ok; t += tstep) {
                 Tile ti = walk.at(t);
                 part(ti);
                 const float *sa = p.sa + ((size_t)ti.e * walk.nat + ti.a0 / kARows) * p.nkb;
-                for (int kb = ti.k0; kb < ti.k1; kb++, it++) {
-                    const int q = it % C::SS;
-                    const bool w = it < C::SS || mbar_wait(smem_u32(&s_sempty[q]), (uint32_t)(it / C::SS + 1) & 1u);
-                    if (!__all_sync(0xffffffffu, w && !*fail)) {
+                for (int kb = ti.k0; kb < ti.k1; kb++) {
+                    const int q = s.slot;
+                    if (!__all_sync(0xffffffffu, ring_wait(smem_u32(&s_sempty[q]), s.phase ^ 1u, fail))) {
                         *fail = 1;
                         ok = false;
                         break;
                     }
+                    s.next();
                     const float *sb = p.sb + (size_t)kb * p.nb;
 #pragma unroll
                     for (int i = 0; i < (C::BT + 31) / 32; i++) {
@@ -752,7 +797,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
     __shared__ uint32_t s_taddr;
     __shared__ int s_fail, s_issued;
     static_assert(C::S <= C::SS, "a scale barrier for every stage");
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t staging = ring + (uint32_t)(C::S * C::STAGE), sfring = staging + (uint32_t)(C::EW * C::OUTB);
     const int rank = C::PAIR ? (int)cluster_rank() : 0;
@@ -815,7 +860,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
                 else mbar_arrive(te0 + 8u * q);
             }
         };
-        int it = 0, done = 0;
+        Ring<2> tq;
+        Ring<C::SS> ts;
+        int done = 0;
         bool ok = true;
         for (int t = t0; t < total && ok; t += tstep) {
             const WideTile ti = walk.at(t);
@@ -831,8 +878,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
                         if (rows > 0) store_cols(z, stage, p, at + c, rows, cols - c, lane);
                     continue;
                 }
-                const bool w = !*fail && mbar_wait(smem_u32(&s_tfull[q]), (uint32_t)(done >> 1) & 1u);
-                if (!__all_sync(0xffffffffu, w)) {
+                if (!__all_sync(0xffffffffu, ring_wait(smem_u32(&s_tfull[q]), (uint32_t)(done >> 1) & 1u, fail))) {
                     *fail = 1;
                     ok = false;
                     break;
@@ -845,18 +891,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
 #pragma unroll 1
                 for (int h = 0; h < 2; h++) {
                     const int c = h ? 64 - first : first;
-                    uint32_t r0[32], r1[32];
-                    tc_ld<32>(base + (uint32_t)c, r0);
-                    tc_ld<32>(base + (uint32_t)c + 32, r1);
-                    tc_wait_ld(r0);
-                    tc_wait_ld(r1);
+                    uint32_t r[64];
+                    tc_ld<64>(base + (uint32_t)c, r);
                     if (h == 0) release(0);
                     uint64_t v[32];
 #pragma unroll
-                    for (int i = 0; i < 16; i++) {
-                        v[i] = pack2(r0[2 * i], r0[2 * i + 1]);
-                        v[16 + i] = pack2(r1[2 * i], r1[2 * i + 1]);
-                    }
+                    for (int i = 0; i < 32; i++) v[i] = pack2(r[2 * i], r[2 * i + 1]);
                     if (rows > 0) store_cols(v, stage, p, at + c, rows, cols - c, lane);
                 }
                 done++;
@@ -864,28 +904,27 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
                 uint64_t acc[64];
 #pragma unroll
                 for (int i = 0; i < 64; i++) acc[i] = 0ull;
-                for (int kb = ti.k0; kb < ti.k1; kb++, it++) {
-                    const int q = it & 1, s = it % C::SS;
-                    const bool w = !*fail && mbar_wait(smem_u32(&s_sfull[s]), (uint32_t)(it / C::SS) & 1u) &&
-                                   mbar_wait(smem_u32(&s_tfull[q]), (uint32_t)(it >> 1) & 1u);
-                    if (!__all_sync(0xffffffffu, w)) {
+                for (int kb = ti.k0; kb < ti.k1; kb++) {
+                    const int q = tq.slot, s = ts.slot;
+                    if (!__all_sync(0xffffffffu, ring_wait(smem_u32(&s_sfull[s]), ts.phase, fail) &&
+                                                     ring_wait(smem_u32(&s_tfull[q]), tq.phase, fail))) {
                         *fail = 1;
                         ok = false;
                         break;
                     }
+                    tq.next();
+                    ts.next();
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                     const uint32_t f = __float_as_uint(s_scale[s][32 * q4 + lane] * s_wscale[s][half]);
                     const uint64_t sc = pack2(f, f);
                     const uint32_t base = trow + (uint32_t)(256 * q + 128 * half);
-                    uint32_t r[2][32];
-                    tc_ld<32>(base, r[0]);
 #pragma unroll
-                    for (int l = 0; l < 4; l++) {
-                        tc_wait_ld(r[l & 1]);
-                        if (l < 3) tc_ld<32>(base + (uint32_t)(32 * (l + 1)), r[(l + 1) & 1]);
-                        else release(q);
+                    for (int l = 0; l < 2; l++) {
+                        uint32_t r[64];
+                        tc_ld<64>(base + (uint32_t)(64 * l), r);
+                        if (l == 1) release(q);
 #pragma unroll
-                        for (int i = 0; i < 16; i++) acc[16 * l + i] = fma2(pack2(r[l & 1][2 * i], r[l & 1][2 * i + 1]), sc, acc[16 * l + i]);
+                        for (int i = 0; i < 32; i++) acc[32 * l + i] = fma2(pack2(r[2 * i], r[2 * i + 1]), sc, acc[32 * l + i]);
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&s_sempty[s]));
@@ -901,103 +940,117 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == C::EW) {
             // tensor copies: this block's rows of A and its part of B
-            if (lane == 0) {
-                int it = 0;
-                bool ok = true;
-                for (int t = t0; t < total && ok; t += tstep) {
-                    const WideTile ti = walk.at(t);
-                    for (int kb = ti.k0; kb < ti.k1; kb++, it++) {
-                        const int j = it % C::S;
-                        if (*fail || (it >= C::S && !mbar_wait(smem_u32(&s_empty[j]), (uint32_t)(it / C::S + 1) & 1u))) {
-                            *fail = 1;
-                            ok = false;
-                            break;
-                        }
-                        const uint32_t bar = smem_u32(&s_full[j]), dst = ring + (uint32_t)(j * C::STAGE);
-                        if (rank == 0) mbar_expect_tx(bar, NB * C::STAGE);
-                        const uint32_t lbar = C::PAIR ? in_leader(bar) : bar;
-                        wide_load<C::PAIR>(dst, &amap, kb * kKB, ti.r0, 0, lbar);
-                        wide_load<C::PAIR>(dst + kABytes, &bmap, kb * kKB, ti.c0 + rank * C::BROWS, C::MX ? 0 : ti.e, lbar);
-                        s_issued = it + 1;
+            Ring<C::S> r;
+            bool ok = true;
+            int n = 0;
+            const uint32_t full0 = C::PAIR ? in_leader(smem_u32(&s_full[0])) : smem_u32(&s_full[0]);
+            for (int t = t0; t < total && ok; t += tstep) {
+                const WideTile ti = walk.at(t);
+                for (int kb = ti.k0; kb < ti.k1; kb++) {
+                    // a fresh ring's slots pass: the phase before the first is over
+                    if (!__all_sync(0xffffffffu, ring_wait(smem_u32(&s_empty[r.slot]), r.phase ^ 1u, fail))) {
+                        ok = false;
+                        break;
                     }
+                    if (elect_one()) {
+                        const uint32_t bar = full0 + 8u * (uint32_t)r.slot, dst = ring + (uint32_t)(r.slot * C::STAGE);
+                        if (rank == 0) mbar_expect_tx(smem_u32(&s_full[r.slot]), NB * C::STAGE);
+                        wide_load<C::PAIR>(dst, &amap, kb * kKB, ti.r0, 0, bar);
+                        wide_load<C::PAIR>(dst + kABytes, &bmap, kb * kKB, ti.c0 + rank * C::BROWS, C::MX ? 0 : ti.e, bar);
+                    }
+                    r.next();
+                    n++;
                 }
             }
+            if (lane == 0) s_issued = n;
+            if (!ok) *fail = 1;
         } else if (warp == C::EW + 1) {
             // MMA issue (by the tile's first block)
-            if (lane == 0 && rank == 0) {
-                int it = 0, tile = 0;
-                bool ok = true;
+            if (rank == 0) {
+                Ring<C::S> r;
+                Ring<2> q;      // matmul: accumulator of the stage; MX: of the tile
+                int tile = 0;
+                bool ok = true, any = false;
                 const uint64_t ad0 = sw128_desc(ring), bd0 = sw128_desc(ring + kABytes);
+                // shared-memory operand of the scale copies: 8-row groups of 16 bytes 128 bytes apart, no swizzle
+                const uint64_t sd0 = (uint64_t)((sfring >> 4) & 0x3FFF) | (1ull << 16) | ((uint64_t)(128 >> 4) << 32) | (1ull << 46);
                 for (int t = t0; t < total && ok; t += tstep) {
                     const WideTile ti = walk.at(t);
                     const int k1 = ti.k1;
                     // MX: the previous tile's overlapping columns are in registers (its epilogue follows
                     // that of the tile before it, which used this accumulator)
-                    if (C::MX && ti.k0 < k1 && tile > 0 && !mbar_wait(smem_u32(&s_tempty[0]), (uint32_t)(tile - 1) & 1u)) {
-                        *fail = 1;
+                    if (C::MX && ti.k0 < k1 && tile > 0 &&
+                        !__all_sync(0xffffffffu, ring_wait(smem_u32(&s_tempty[0]), (uint32_t)(tile - 1) & 1u, fail))) {
                         ok = false;
                         break;
                     }
-                    for (int kb = ti.k0; kb < k1; kb++, it++) {
-                        const int j = it % C::S, q = it & 1;
-                        bool w = !*fail;
-                        if (!C::MX && w && it >= 2) w = mbar_wait(smem_u32(&s_tempty[q]), (uint32_t)((it >> 1) + 1) & 1u);
-                        if (C::MX && w) w = mbar_wait(smem_u32(&s_sfull[j]), (uint32_t)(it / C::S) & 1u);
-                        if (!w || !mbar_wait(smem_u32(&s_full[j]), (uint32_t)(it / C::S) & 1u)) {
-                            *fail = 1;
+                    for (int kb = ti.k0; kb < k1; kb++) {
+                        const bool w = C::MX ? ring_wait(smem_u32(&s_sfull[r.slot]), r.phase, fail)
+                                             : ring_wait(smem_u32(&s_tempty[q.slot]), q.phase ^ 1u, fail);
+                        if (!__all_sync(0xffffffffu, w && ring_wait(smem_u32(&s_full[r.slot]), r.phase, fail))) {
                             ok = false;
                             break;
                         }
                         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                        const uint64_t off = (uint64_t)((j * C::STAGE) >> 4);
-                        if constexpr (C::MX) {
-                            // shared-memory operand of the scale copies: 8-row groups of 16 bytes 128 bytes apart, no swizzle
-                            const uint32_t sf = sfring + (uint32_t)(j * C::SFBYTES), tsf = taddr + (uint32_t)(512 - C::SFCOLS * (C::S - j));
-                            const uint64_t sd = (uint64_t)((sf >> 4) & 0x3FFF) | (1ull << 16) | ((uint64_t)(128 >> 4) << 32) | (1ull << 46);
+                        if (elect_one()) {
+                            const uint64_t off = (uint64_t)((r.slot * C::STAGE) >> 4);
+                            if constexpr (C::MX) {
+                                const uint32_t tsf = taddr + (uint32_t)(512 - C::SFCOLS * (C::S - r.slot));
+                                const uint64_t sd = sd0 + (uint64_t)((r.slot * C::SFBYTES) >> 4);
 #pragma unroll
-                            for (int i = 0; i < 3; i++) wide_cp_scales<C::PAIR>(tsf + 4 * i, sd + (uint64_t)(i * (512 >> 4)));
-                            const uint32_t d = taddr + (uint32_t)((tile & 1) ? C::ACC1 : 0);
+                                for (int i = 0; i < 3; i++) wide_cp_scales<C::PAIR>(tsf + 4 * i, sd + (uint64_t)(i * (512 >> 4)));
+                                const uint32_t d = taddr + (uint32_t)(q.slot ? C::ACC1 : 0);
 #pragma unroll
-                            for (int ks = 0; ks < 4; ks++)
-                                wide_mma_mx<C::PAIR>(d, ad0 + off + 2 * ks, bd0 + off + 2 * ks, C::IDESC, tsf, tsf + 4, kb > ti.k0 || ks > 0);
-                        } else {
-                            const uint32_t d = taddr + (uint32_t)(256 * q);
+                                for (int ks = 0; ks < 4; ks++)
+                                    wide_mma_mx<C::PAIR>(d, ad0 + off + 2 * ks, bd0 + off + 2 * ks, C::IDESC, tsf, tsf + 4, kb > ti.k0 || ks > 0);
+                            } else {
+                                const uint32_t d = taddr + (uint32_t)(256 * q.slot);
 #pragma unroll
-                            for (int ks = 0; ks < 4; ks++) wide_mma<C::PAIR>(d, ad0 + off + 2 * ks, bd0 + off + 2 * ks, C::IDESC, ks > 0);
+                                for (int ks = 0; ks < 4; ks++) wide_mma<C::PAIR>(d, ad0 + off + 2 * ks, bd0 + off + 2 * ks, C::IDESC, ks > 0);
+                            }
+                            wide_commit<C::PAIR>(smem_u32(&s_empty[r.slot]));
+                            if (!C::MX || kb + 1 == k1) wide_commit<C::PAIR>(smem_u32(&s_tfull[q.slot]));
                         }
-                        wide_commit<C::PAIR>(smem_u32(&s_empty[j]));
-                        if (!C::MX) wide_commit<C::PAIR>(smem_u32(&s_tfull[q]));
-                        else if (kb + 1 == k1) wide_commit<C::PAIR>(smem_u32(&s_tfull[tile & 1]));
+                        r.next();
+                        if (!C::MX) q.next();
+                        any = true;
                     }
-                    if (ti.k0 < k1) tile++;
+                    if (ti.k0 < k1) {
+                        tile++;
+                        if (C::MX) q.next();
+                    }
                 }
-                if (it > 0) {
+                if (!ok) *fail = 1;
+                if (any) {
                     // every MMA is done before the shared memory and the tensor memory go (bounded)
-                    if constexpr (C::PAIR)
-                        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(&s_drain)) : "memory");
-                    else
-                        tc_commit(smem_u32(&s_drain));
+                    __syncwarp();
+                    if (elect_one()) {
+                        if constexpr (C::PAIR)
+                            asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(&s_drain)) : "memory");
+                        else
+                            tc_commit(smem_u32(&s_drain));
+                    }
                     if (!mbar_wait(smem_u32(&s_drain), 0u)) *fail = 1;
                 }
             }
         } else if constexpr (!C::MX) {
             if (warp == C::EW + 2) {
                 // scales: the rows' and the two weight blocks', copied asynchronously up to SS stages ahead
-                int it = 0;
+                Ring<C::SS> r;
                 bool ok = true;
                 const int nbb = (p.nb + kKB - 1) / kKB;
                 for (int t = t0; t < total && ok; t += tstep) {
                     const WideTile ti = walk.at(t);
                     const float *sw = p.sb + ((size_t)ti.e * nbb + ti.c0 / kKB + (lane & 1)) * p.nkb;
                     const bool in_w = ti.c0 + kKB * (lane & 1) < p.nb;
-                    for (int kb = ti.k0; kb < ti.k1; kb++, it++) {
-                        const int s = it % C::SS;
-                        const bool w = it < C::SS || mbar_wait(smem_u32(&s_sempty[s]), (uint32_t)(it / C::SS + 1) & 1u);
-                        if (!__all_sync(0xffffffffu, w && !*fail)) {
+                    for (int kb = ti.k0; kb < ti.k1; kb++) {
+                        const int s = r.slot;
+                        if (!__all_sync(0xffffffffu, ring_wait(smem_u32(&s_sempty[s]), r.phase ^ 1u, fail))) {
                             *fail = 1;
                             ok = false;
                             break;
                         }
+                        r.next();
                         const float *sr = p.sa + (size_t)kb * p.na;
 #pragma unroll
                         for (int i = 0; i < 4; i++) {
@@ -1060,8 +1113,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
                     if (it < 0) ok = false;
                     if (!ok) break;
                     const int s = it % C::S;
-                    const bool w = it < C::S || mbar_wait(smem_u32(&s_empty[s]), (uint32_t)(it / C::S + 1) & 1u);
-                    if (!__all_sync(0xffffffffu, w && !*fail)) {
+                    if (!__all_sync(0xffffffffu, ring_wait(smem_u32(&s_empty[s]), (uint32_t)(it / C::S + 1) & 1u, fail))) {
                         *fail = 1;
                         ok = false;
                         break;
