@@ -1253,97 +1253,168 @@ __global__ void __launch_bounds__(kQThreads) quantize_rows_kernel(const QuantArg
     }
 }
 
-// element (r, c) of a 128 x 128 tile in shared memory: 16-byte chunks of a row permuted by the
-// row's group of 16, so that rows are written and columns read without bank conflicts
-__device__ __forceinline__ int tile_at(int r, int c) { return r * kKB + (c ^ ((r >> 4) << 2)); }
+// A lane's four neighbouring elements of a row, as loaded: float4, or two packed 16-bit pairs.
+// Magnitudes are compared as unsigned integers (so that a NaN is the largest).
+template <typename T>
+struct Quad;
+template <>
+struct Quad<float> {
+    float4 v;
+    __device__ __forceinline__ void load(const float *p) { v = __ldg(reinterpret_cast<const float4 *>(p)); }
+    __device__ __forceinline__ void zero() { v = make_float4(0, 0, 0, 0); }
+    __device__ __forceinline__ float4 get() const { return v; }
+    __device__ __forceinline__ unsigned most() const { return max_bits(v); }
+};
+struct Pairs {
+    uint2 v;
+    __device__ __forceinline__ void zero() { v = make_uint2(0, 0); }
+    __device__ __forceinline__ unsigned most16() const {
+        const unsigned m = __vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu);
+        return max(m >> 16, m & 0xFFFFu);
+    }
+};
+template <>
+struct Quad<__nv_bfloat16> : Pairs {
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { v = __ldg(reinterpret_cast<const uint2 *>(p)); }
+    __device__ __forceinline__ float4 get() const {
+        return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
+                           __uint_as_float(v.y & 0xFFFF0000u));
+    }
+    __device__ __forceinline__ unsigned most() const { return most16() << 16; }
+    static __device__ __forceinline__ unsigned bits(unsigned h) { return h << 16; }      // float32 bits of a magnitude
+};
+template <>
+struct Quad<__half> : Pairs {
+    __device__ __forceinline__ void load(const __half *p) { v = __ldg(reinterpret_cast<const uint2 *>(p)); }
+    __device__ __forceinline__ float4 get() const {
+        const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&v.x)), b = __half22float2(*reinterpret_cast<const __half2 *>(&v.y));
+        return make_float4(a.x, a.y, b.x, b.y);
+    }
+    static __device__ __forceinline__ unsigned bits(unsigned h) { return __float_as_uint(__half2float(__ushort_as_half((unsigned short)h))); }
+    __device__ __forceinline__ unsigned most() const { return bits(most16()); }
+};
+// largest magnitudes of the four columns so far
+template <typename T>
+struct ColMax {
+    uint2 m;
+    __device__ __forceinline__ void zero() { m = make_uint2(0, 0); }
+    __device__ __forceinline__ void add(const Quad<T> &q) {
+        m.x = __vmaxu2(m.x, q.v.x & 0x7FFF7FFFu);
+        m.y = __vmaxu2(m.y, q.v.y & 0x7FFF7FFFu);
+    }
+    __device__ __forceinline__ uint4 get() const {
+        return make_uint4(Quad<T>::bits(m.x & 0xFFFFu), Quad<T>::bits(m.x >> 16), Quad<T>::bits(m.y & 0xFFFFu), Quad<T>::bits(m.y >> 16));
+    }
+};
+template <>
+struct ColMax<float> {
+    uint4 m;
+    __device__ __forceinline__ void zero() { m = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void add(const Quad<float> &q) {
+        m.x = max(m.x, abs_bits(q.v.x));
+        m.y = max(m.y, abs_bits(q.v.y));
+        m.z = max(m.z, abs_bits(q.v.z));
+        m.w = max(m.w, abs_bits(q.v.w));
+    }
+    __device__ __forceinline__ uint4 get() const { return m; }
+};
 
-// Rows and columns of a 128 x 128 tile, or (WT) one scale for the whole tile of a weight matrix:
-// x is read once, the transposed codes leave shared memory 16 rows a lane.
+// Rows and columns of a 128 x 128 tile, or (WT) one scale for the whole tile of a weight matrix.
+// x is read once and stays in registers, 16 rows a warp and four columns a lane: a lane's 16 codes of
+// a column are 16 neighbouring bytes of the transposed output, and only codes pass through shared
+// memory (16-byte chunks permuted by the column) to leave as whole 128-byte rows.  Memory-bound.
 template <typename T, bool WT>
-__global__ void __launch_bounds__(kQThreads) quantize_tile_kernel(const QuantArgs p) {
-    extern __shared__ __align__(16) float tile[];
+__global__ void __launch_bounds__(kQThreads, sizeof(T) == 4 ? 2 : 3) quantize_tile_kernel(const QuantArgs p) {
+    __shared__ __align__(16) uint8_t s_codes[kKB * kKB];
+    __shared__ __align__(16) uint4 s_col[kQThreads / 32][32];    // column maxima of every warp's rows
     __shared__ unsigned s_max[kQThreads / 32];
+    constexpr int NR = kKB / (kQThreads / 32);                   // rows of a warp
+    static_assert(NR == 16, "a lane's codes of a column are one 16-byte chunk");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r0 = (int)blockIdx.y * kKB, kb = (int)blockIdx.x, e = (int)blockIdx.z;
-    const int c = kb * kKB + 4 * lane;
+    const int c = kb * kKB + 4 * lane, rw = r0 + NR * warp;
     const T *x = static_cast<const T *>(p.x) + (WT ? (size_t)e * p.R * p.ld : 0);
     uint8_t *codes = p.codes + (WT ? (size_t)e * p.R * p.width : 0);
-    const int ldt = WT ? p.R : ((p.R + kKB - 1) / kKB) * kKB;   // bytes between rows of codes_t
+    const int ldt = WT ? p.R : ((p.R + kKB - 1) / kKB) * kKB;    // bytes between rows of codes_t
     uint8_t *codes_t = p.codes_t + (WT ? (size_t)e * p.R * p.width : 0);
     const int nrb = (p.R + kKB - 1) / kKB, nkb = (p.width + kKB - 1) / kKB;
-    float wscale = 0.0f, winv = 0.0f;
-    constexpr int U = 8;
-    unsigned most = 0;
-    for (int i0 = warp; i0 < kKB; i0 += U * (kQThreads / 32)) {
-        float4 v[U];
+
+    const int src = lane < NR ? src_row(p.rows, rw + lane, p.R, p.n_src) : -1;
+    Quad<T> v[NR];
 #pragma unroll
-        for (int u = 0; u < U; u++) {
-            const int i = i0 + u * (kQThreads / 32), s = src_row(p.rows, r0 + i, p.R, p.n_src);
-            v[u] = s >= 0 && c < p.width ? load4(x + (long long)s * p.ld + c) : make_float4(0, 0, 0, 0);
-        }
-#pragma unroll
-        for (int u = 0; u < U; u++) {
-            const int i = i0 + u * (kQThreads / 32), r = r0 + i;
-            *reinterpret_cast<float4 *>(&tile[tile_at(i, 4 * lane)]) = v[u];
-            const unsigned m = max_bits(v[u]);
-            if (WT) {
-                most = max(most, m);
-            } else {
-                float inv;
-                const float s = block_scale(__reduce_max_sync(0xffffffffu, m), inv);
-                if (r < p.R && c < p.width) {
-                    *reinterpret_cast<uint32_t *>(codes + (size_t)r * p.width + c) = codes4(v[u], inv);
-                    if (lane == 0) p.scales[(size_t)kb * p.R + r] = s;
-                }
-            }
-        }
+    for (int i = 0; i < NR; i++) {
+        const int s = __shfl_sync(0xffffffffu, src, i);
+        if (s >= 0 && c < p.width) v[i].load(x + (long long)s * p.ld + c);
+        else v[i].zero();
     }
+    ColMax<T> cm;
+    cm.zero();
+    float wscale = 0.0f, winv = 0.0f;
     if (WT) {
+        unsigned most = 0;
+#pragma unroll
+        for (int i = 0; i < NR; i++) most = max(most, v[i].most());
         most = __reduce_max_sync(0xffffffffu, most);
         if (lane == 0) s_max[warp] = most;
-    }
-    __syncthreads();
-    if (WT) {
+        __syncthreads();
         for (int i = 0; i < kQThreads / 32; i++) most = max(most, s_max[i]);
         wscale = block_scale(most, winv);
         if (threadIdx.x == 0) {
             p.scales[((size_t)e * nrb + blockIdx.y) * nkb + kb] = wscale;
             if (p.codes_t) p.scales_t[((size_t)e * nkb + kb) * nrb + blockIdx.y] = wscale;
         }
-        for (int i = warp; i < kKB; i += kQThreads / 32)
-            if (r0 + i < p.R && c < p.width)
-                *reinterpret_cast<uint32_t *>(codes + (size_t)(r0 + i) * p.width + c) =
-                    codes4(*reinterpret_cast<const float4 *>(&tile[tile_at(i, 4 * lane)]), winv);
-        if (!p.codes_t) return;
     }
-    // columns: lane = 16-row chunk (lane & 7) of column 4 j + (lane >> 3)
-    const int ch = lane & 7;
-    for (int j = warp; j < kKB / 4; j += kQThreads / 32) {
-        const int cc = 4 * j + (lane >> 3), col = kb * kKB + cc;
-        float v[16];
-        unsigned m = 0;
+    float mine = 0.0f;                                           // the scale of row `lane`
 #pragma unroll
-        for (int i = 0; i < 16; i++) {
-            v[i] = tile[tile_at(16 * ch + i, cc)];
-            m = max(m, abs_bits(v[i]));
-        }
+    for (int i = 0; i < NR; i++) {
         float s = wscale, inv = winv;
         if (!WT) {
-#pragma unroll
-            for (int d = 1; d < 8; d *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-            s = block_scale(m, inv);
+            cm.add(v[i]);
+            s = block_scale(__reduce_max_sync(0xffffffffu, v[i].most()), inv);
+            if (lane == i) mine = s;
         }
-        if (col >= p.width) continue;
-        if (!WT && ch == 0) p.scales_t[(size_t)blockIdx.y * p.width + col] = s;
-        uint32_t q[4];
+        if (rw + i < p.R && c < p.width) *reinterpret_cast<uint32_t *>(codes + (size_t)(rw + i) * p.width + c) = codes4(v[i].get(), inv);
+    }
+    if (!WT && lane < NR && rw + lane < p.R) p.scales[(size_t)kb * p.R + rw + lane] = mine;
+    if (WT && !p.codes_t) return;
+    float inv[4] = {winv, winv, winv, winv};
+    if (!WT) {
+        s_col[warp][lane] = cm.get();
+        __syncthreads();
+        uint4 m = s_col[0][lane];
 #pragma unroll
-        for (int i = 0; i < 4; i++) q[i] = codes4(make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]), inv);
-        uint8_t *o = codes_t + (size_t)col * ldt + r0 + 16 * ch;
-        if (!WT || (p.R % 16 == 0 && r0 + 16 * ch < p.R)) {
-            *reinterpret_cast<uint4 *>(o) = make_uint4(q[0], q[1], q[2], q[3]);
+        for (int w = 1; w < kQThreads / 32; w++) {
+            const uint4 o = s_col[w][lane];
+            m = make_uint4(max(m.x, o.x), max(m.y, o.y), max(m.z, o.z), max(m.w, o.w));
+        }
+        const float4 s = make_float4(block_scale(m.x, inv[0]), block_scale(m.y, inv[1]), block_scale(m.z, inv[2]), block_scale(m.w, inv[3]));
+        if (warp == 0 && c < p.width) *reinterpret_cast<float4 *>(p.scales_t + (size_t)blockIdx.y * p.width + c) = s;
+    }
+    // chunk `warp` of column 4 lane + k, at chunk position warp ^ (lane & 7) of that column's 128 bytes
+    uint32_t q[4][4];
+#pragma unroll
+    for (int i = 0; i < NR; i += 4) {
+        const float4 a = v[i].get(), b = v[i + 1].get(), d = v[i + 2].get(), f = v[i + 3].get();
+        q[0][i / 4] = codes4(make_float4(a.x, b.x, d.x, f.x), inv[0]);
+        q[1][i / 4] = codes4(make_float4(a.y, b.y, d.y, f.y), inv[1]);
+        q[2][i / 4] = codes4(make_float4(a.z, b.z, d.z, f.z), inv[2]);
+        q[3][i / 4] = codes4(make_float4(a.w, b.w, d.w, f.w), inv[3]);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; k++)
+        *reinterpret_cast<uint4 *>(&s_codes[(4 * lane + k) * kKB + 16 * (warp ^ (lane & 7))]) = make_uint4(q[k][0], q[k][1], q[k][2], q[k][3]);
+    __syncthreads();
+    for (int i = threadIdx.x; i < kKB * 8; i += kQThreads) {
+        const int cc = i >> 3, ch = i & 7, col = kb * kKB + cc, r = r0 + 16 * ch;
+        if (col >= p.width) continue;
+        const uint4 u = *reinterpret_cast<const uint4 *>(&s_codes[cc * kKB + 16 * (ch ^ ((cc >> 2) & 7))]);
+        uint8_t *o = codes_t + (size_t)col * ldt + r;
+        if (!WT || (p.R % 16 == 0 && r < p.R)) {
+            *reinterpret_cast<uint4 *>(o) = u;
         } else if constexpr (WT) {
-            for (int i = 0; i < 16; i++)
-                if (r0 + 16 * ch + i < p.R) o[i] = (uint8_t)(q[i >> 2] >> (8 * (i & 3)));
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+            for (int k = 0; k < 16; k++)
+                if (r + k < p.R) o[k] = (uint8_t)(w[k >> 2] >> (8 * (k & 3)));
         }
     }
 }
@@ -1364,18 +1435,10 @@ cudaError_t launch_quantize(const void *x, int dtype, long long ld, int n_src, i
     const int nkb = (width + kKB - 1) / kKB;
     if (codes_t) {
         const dim3 grid(nkb, (R + kKB - 1) / kKB);
-        constexpr int smem = kKB * kKB * 4;
-        auto go = [&](auto kernel) {
-            cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-            if (e == cudaSuccess) {
-                kernel<<<grid, kQThreads, smem, st>>>(p);
-                e = cudaGetLastError();
-            }
-            return e;
-        };
-        if (dtype == MOE_DTYPE_F32) return go(quantize_tile_kernel<float, false>);
-        if (dtype == MOE_DTYPE_BF16) return go(quantize_tile_kernel<__nv_bfloat16, false>);
-        return go(quantize_tile_kernel<__half, false>);
+        if (dtype == MOE_DTYPE_F32) quantize_tile_kernel<float, false><<<grid, kQThreads, 0, st>>>(p);
+        else if (dtype == MOE_DTYPE_BF16) quantize_tile_kernel<__nv_bfloat16, false><<<grid, kQThreads, 0, st>>>(p);
+        else quantize_tile_kernel<__half, false><<<grid, kQThreads, 0, st>>>(p);
+        return cudaGetLastError();
     }
     // few rows: one block a warp, so that the blocks cover the card; many: four rows of four blocks
     const bool few = (long long)R * nkb < 16ll * 8 * 4 * sm_count();
@@ -1398,18 +1461,10 @@ cudaError_t launch_quantize_weights(const void *w, int dtype, int E, int N, int 
                                     uint8_t *codes_t, float *scales_t, cudaStream_t st) {
     const QuantArgs p = {w, K, nullptr, codes, scales, codes_t, scales_t, N, N, K};
     const dim3 grid((K + kKB - 1) / kKB, (N + kKB - 1) / kKB, E);
-    constexpr int smem = kKB * kKB * 4;
-    auto go = [&](auto kernel) {
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e == cudaSuccess) {
-            kernel<<<grid, kQThreads, smem, st>>>(p);
-            e = cudaGetLastError();
-        }
-        return e;
-    };
-    if (dtype == MOE_DTYPE_F32) return go(quantize_tile_kernel<float, true>);
-    if (dtype == MOE_DTYPE_BF16) return go(quantize_tile_kernel<__nv_bfloat16, true>);
-    return go(quantize_tile_kernel<__half, true>);
+    if (dtype == MOE_DTYPE_F32) quantize_tile_kernel<float, true><<<grid, kQThreads, 0, st>>>(p);
+    else if (dtype == MOE_DTYPE_BF16) quantize_tile_kernel<__nv_bfloat16, true><<<grid, kQThreads, 0, st>>>(p);
+    else quantize_tile_kernel<__half, true><<<grid, kQThreads, 0, st>>>(p);
+    return cudaGetLastError();
 }
 
 // ---------------------------------------------------------------------------
