@@ -1263,61 +1263,83 @@ struct Quad<float> {
     __device__ __forceinline__ void load(const float *p) { v = __ldg(reinterpret_cast<const float4 *>(p)); }
     __device__ __forceinline__ void zero() { v = make_float4(0, 0, 0, 0); }
     __device__ __forceinline__ float4 get() const { return v; }
-    __device__ __forceinline__ unsigned most() const { return max_bits(v); }
 };
-struct Pairs {
-    uint2 v;
-    __device__ __forceinline__ void zero() { v = make_uint2(0, 0); }
-    __device__ __forceinline__ unsigned most16() const {
-        const unsigned m = __vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu);
-        return max(m >> 16, m & 0xFFFFu);
-    }
-};
+// the larger magnitudes of two packed pairs (a NaN is the largest)
+template <typename T>
+__device__ __forceinline__ uint32_t pair_max(uint32_t a, uint32_t b);
 template <>
-struct Quad<__nv_bfloat16> : Pairs {
+__device__ __forceinline__ uint32_t pair_max<__nv_bfloat16>(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+template <>
+__device__ __forceinline__ uint32_t pair_max<__half>(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+template <>
+struct Quad<__nv_bfloat16> {
+    uint2 v;
     __device__ __forceinline__ void load(const __nv_bfloat16 *p) { v = __ldg(reinterpret_cast<const uint2 *>(p)); }
+    __device__ __forceinline__ void zero() { v = make_uint2(0, 0); }
     __device__ __forceinline__ float4 get() const {
         return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
                            __uint_as_float(v.y & 0xFFFF0000u));
     }
-    __device__ __forceinline__ unsigned most() const { return most16() << 16; }
     static __device__ __forceinline__ unsigned bits(unsigned h) { return h << 16; }      // float32 bits of a magnitude
 };
 template <>
-struct Quad<__half> : Pairs {
+struct Quad<__half> {
+    uint2 v;
     __device__ __forceinline__ void load(const __half *p) { v = __ldg(reinterpret_cast<const uint2 *>(p)); }
+    __device__ __forceinline__ void zero() { v = make_uint2(0, 0); }
     __device__ __forceinline__ float4 get() const {
         const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&v.x)), b = __half22float2(*reinterpret_cast<const __half2 *>(&v.y));
         return make_float4(a.x, a.y, b.x, b.y);
     }
     static __device__ __forceinline__ unsigned bits(unsigned h) { return __float_as_uint(__half2float(__ushort_as_half((unsigned short)h))); }
-    __device__ __forceinline__ unsigned most() const { return bits(most16()); }
 };
-// largest magnitudes of the four columns so far
+// largest magnitudes of the four columns so far; add() gives back the row's own largest, in a form
+// that compares as an unsigned integer and that bits() makes a float32's bits
 template <typename T>
 struct ColMax {
     uint2 m;
     __device__ __forceinline__ void zero() { m = make_uint2(0, 0); }
-    __device__ __forceinline__ void add(const Quad<T> &q) {
-        m.x = __vmaxu2(m.x, q.v.x & 0x7FFF7FFFu);
-        m.y = __vmaxu2(m.y, q.v.y & 0x7FFF7FFFu);
+    __device__ __forceinline__ unsigned add(const Quad<T> &q) {
+        const uint32_t a = q.v.x & 0x7FFF7FFFu, b = q.v.y & 0x7FFF7FFFu, r = pair_max<T>(a, b);
+        m.x = pair_max<T>(m.x, a);
+        m.y = pair_max<T>(m.y, b);
+        return max(r >> 16, r & 0xFFFFu);
     }
+    static __device__ __forceinline__ unsigned bits(unsigned r) { return Quad<T>::bits(r); }
     __device__ __forceinline__ uint4 get() const {
-        return make_uint4(Quad<T>::bits(m.x & 0xFFFFu), Quad<T>::bits(m.x >> 16), Quad<T>::bits(m.y & 0xFFFFu), Quad<T>::bits(m.y >> 16));
+        return make_uint4(bits(m.x & 0xFFFFu), bits(m.x >> 16), bits(m.y & 0xFFFFu), bits(m.y >> 16));
     }
 };
 template <>
 struct ColMax<float> {
     uint4 m;
     __device__ __forceinline__ void zero() { m = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void add(const Quad<float> &q) {
-        m.x = max(m.x, abs_bits(q.v.x));
-        m.y = max(m.y, abs_bits(q.v.y));
-        m.z = max(m.z, abs_bits(q.v.z));
-        m.w = max(m.w, abs_bits(q.v.w));
+    __device__ __forceinline__ unsigned add(const Quad<float> &q) {
+        const uint4 a = make_uint4(abs_bits(q.v.x), abs_bits(q.v.y), abs_bits(q.v.z), abs_bits(q.v.w));
+        m = make_uint4(max(m.x, a.x), max(m.y, a.y), max(m.z, a.z), max(m.w, a.w));
+        return max(max(a.x, a.y), max(a.z, a.w));
     }
+    static __device__ __forceinline__ unsigned bits(unsigned r) { return r; }
     __device__ __forceinline__ uint4 get() const { return m; }
 };
+__device__ __forceinline__ float4 scaled(float4 v, uint64_t s01, uint64_t s23) {
+    float4 r;
+    unpack2(mul2(pack2(__float_as_uint(v.x), __float_as_uint(v.y)), s01), r.x, r.y);
+    unpack2(mul2(pack2(__float_as_uint(v.z), __float_as_uint(v.w)), s23), r.z, r.w);
+    return r;
+}
+__device__ __forceinline__ uint64_t pair_of(float a, float b) { return pack2(__float_as_uint(a), __float_as_uint(b)); }
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+    return __byte_perm(codes2(a, b), codes2(c, d), 0x5410);
+}
 
 // Rows and columns of a 128 x 128 tile, or (WT) one scale for the whole tile of a weight matrix.
 // x is read once and stays in registers, 16 rows a warp and four columns a lane: a lane's 16 codes of
@@ -1347,38 +1369,31 @@ __global__ void __launch_bounds__(kQThreads, sizeof(T) == 4 ? 2 : 3) quantize_ti
         if (s >= 0 && c < p.width) v[i].load(x + (long long)s * p.ld + c);
         else v[i].zero();
     }
+    // maxima: of the columns in packed form, of row i in lane i
     ColMax<T> cm;
     cm.zero();
-    float wscale = 0.0f, winv = 0.0f;
-    if (WT) {
-        unsigned most = 0;
-#pragma unroll
-        for (int i = 0; i < NR; i++) most = max(most, v[i].most());
-        most = __reduce_max_sync(0xffffffffu, most);
-        if (lane == 0) s_max[warp] = most;
-        __syncthreads();
-        for (int i = 0; i < kQThreads / 32; i++) most = max(most, s_max[i]);
-        wscale = block_scale(most, winv);
-        if (threadIdx.x == 0) {
-            p.scales[((size_t)e * nrb + blockIdx.y) * nkb + kb] = wscale;
-            if (p.codes_t) p.scales_t[((size_t)e * nkb + kb) * nrb + blockIdx.y] = wscale;
-        }
-    }
-    float mine = 0.0f;                                           // the scale of row `lane`
+    unsigned mine = 0;
 #pragma unroll
     for (int i = 0; i < NR; i++) {
-        float s = wscale, inv = winv;
-        if (!WT) {
-            cm.add(v[i]);
-            s = block_scale(__reduce_max_sync(0xffffffffu, v[i].most()), inv);
-            if (lane == i) mine = s;
-        }
-        if (rw + i < p.R && c < p.width) *reinterpret_cast<uint32_t *>(codes + (size_t)(rw + i) * p.width + c) = codes4(v[i].get(), inv);
+        const unsigned m = __reduce_max_sync(0xffffffffu, cm.add(v[i]));
+        if (lane == i) mine = m;
     }
-    if (!WT && lane < NR && rw + lane < p.R) p.scales[(size_t)kb * p.R + rw + lane] = mine;
-    if (WT && !p.codes_t) return;
-    float inv[4] = {winv, winv, winv, winv};
-    if (!WT) {
+    float rinv, cinv[4];
+    if (WT) {
+        const unsigned m = __reduce_max_sync(0xffffffffu, mine);
+        if (lane == 0) s_max[warp] = m;
+        __syncthreads();
+        unsigned most = 0;
+        for (int i = 0; i < kQThreads / 32; i++) most = max(most, s_max[i]);
+        const float s = block_scale(ColMax<T>::bits(most), rinv);
+        cinv[0] = cinv[1] = cinv[2] = cinv[3] = rinv;
+        if (threadIdx.x == 0) {
+            p.scales[((size_t)e * nrb + blockIdx.y) * nkb + kb] = s;
+            if (p.codes_t) p.scales_t[((size_t)e * nkb + kb) * nrb + blockIdx.y] = s;
+        }
+    } else {
+        const float s = block_scale(ColMax<T>::bits(mine), rinv);
+        if (lane < NR && rw + lane < p.R) p.scales[(size_t)kb * p.R + rw + lane] = s;
         s_col[warp][lane] = cm.get();
         __syncthreads();
         uint4 m = s_col[0][lane];
@@ -1387,19 +1402,35 @@ __global__ void __launch_bounds__(kQThreads, sizeof(T) == 4 ? 2 : 3) quantize_ti
             const uint4 o = s_col[w][lane];
             m = make_uint4(max(m.x, o.x), max(m.y, o.y), max(m.z, o.z), max(m.w, o.w));
         }
-        const float4 s = make_float4(block_scale(m.x, inv[0]), block_scale(m.y, inv[1]), block_scale(m.z, inv[2]), block_scale(m.w, inv[3]));
-        if (warp == 0 && c < p.width) *reinterpret_cast<float4 *>(p.scales_t + (size_t)blockIdx.y * p.width + c) = s;
+        const float4 t = make_float4(block_scale(m.x, cinv[0]), block_scale(m.y, cinv[1]), block_scale(m.z, cinv[2]), block_scale(m.w, cinv[3]));
+        if (warp == 0 && c < p.width) *reinterpret_cast<float4 *>(p.scales_t + (size_t)blockIdx.y * p.width + c) = t;
     }
-    // chunk `warp` of column 4 lane + k, at chunk position warp ^ (lane & 7) of that column's 128 bytes
+    // codes of four rows at a time, both orientations from the same float32 values; q: this lane's
+    // chunk `warp` of its four columns
+    const uint64_t c01 = pair_of(cinv[0], cinv[1]), c23 = pair_of(cinv[2], cinv[3]);
+    const bool in = c < p.width;
+    uint8_t *o = codes + (size_t)rw * p.width + c;
     uint32_t q[4][4];
 #pragma unroll
     for (int i = 0; i < NR; i += 4) {
-        const float4 a = v[i].get(), b = v[i + 1].get(), d = v[i + 2].get(), f = v[i + 3].get();
-        q[0][i / 4] = codes4(make_float4(a.x, b.x, d.x, f.x), inv[0]);
-        q[1][i / 4] = codes4(make_float4(a.y, b.y, d.y, f.y), inv[1]);
-        q[2][i / 4] = codes4(make_float4(a.z, b.z, d.z, f.z), inv[2]);
-        q[3][i / 4] = codes4(make_float4(a.w, b.w, d.w, f.w), inv[3]);
+        float4 f[4];
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            const float4 u = v[i + k].get();
+            const float r = WT ? rinv : __shfl_sync(0xffffffffu, rinv, i + k);
+            const uint64_t rr = pair_of(r, r);
+            const float4 a = scaled(u, rr, rr);
+            f[k] = WT ? a : scaled(u, c01, c23);
+            if (in && rw + i + k < p.R) *reinterpret_cast<uint32_t *>(o) = codes4(a.x, a.y, a.z, a.w);
+            o += p.width;
+        }
+        q[0][i / 4] = codes4(f[0].x, f[1].x, f[2].x, f[3].x);
+        q[1][i / 4] = codes4(f[0].y, f[1].y, f[2].y, f[3].y);
+        q[2][i / 4] = codes4(f[0].z, f[1].z, f[2].z, f[3].z);
+        q[3][i / 4] = codes4(f[0].w, f[1].w, f[2].w, f[3].w);
     }
+    if (WT && !p.codes_t) return;
+    // chunk `warp` of column 4 lane + k, at chunk position warp ^ (lane & 7) of that column's 128 bytes
 #pragma unroll
     for (int k = 0; k < 4; k++)
         *reinterpret_cast<uint4 *>(&s_codes[(4 * lane + k) * kKB + 16 * (warp ^ (lane & 7))]) = make_uint4(q[k][0], q[k][1], q[k][2], q[k][3]);
@@ -1408,13 +1439,13 @@ __global__ void __launch_bounds__(kQThreads, sizeof(T) == 4 ? 2 : 3) quantize_ti
         const int cc = i >> 3, ch = i & 7, col = kb * kKB + cc, r = r0 + 16 * ch;
         if (col >= p.width) continue;
         const uint4 u = *reinterpret_cast<const uint4 *>(&s_codes[cc * kKB + 16 * (ch ^ ((cc >> 2) & 7))]);
-        uint8_t *o = codes_t + (size_t)col * ldt + r;
+        uint8_t *t = codes_t + (size_t)col * ldt + r;
         if (!WT || (p.R % 16 == 0 && r < p.R)) {
-            *reinterpret_cast<uint4 *>(o) = u;
+            *reinterpret_cast<uint4 *>(t) = u;
         } else if constexpr (WT) {
             const uint32_t w[4] = {u.x, u.y, u.z, u.w};
             for (int k = 0; k < 16; k++)
-                if (r + k < p.R) o[k] = (uint8_t)(w[k >> 2] >> (8 * (k & 3)));
+                if (r + k < p.R) t[k] = (uint8_t)(w[k >> 2] >> (8 * (k & 3)));
         }
     }
 }
