@@ -28,6 +28,7 @@
 #include <stdint.h>
 
 #include <cstring>
+#include <type_traits>
 
 #include "moe_internal.h"
 #include "moe_ptx.h"
@@ -1253,192 +1254,218 @@ __global__ void __launch_bounds__(kQThreads) quantize_rows_kernel(const QuantArg
     }
 }
 
-// A lane's four neighbouring elements of a row, as loaded: float4, or two packed 16-bit pairs.
-// Magnitudes are compared as unsigned integers (so that a NaN is the largest).
-template <typename T>
-struct Quad;
-template <>
-struct Quad<float> {
-    float4 v;
-    __device__ __forceinline__ void load(const float *p) { v = __ldg(reinterpret_cast<const float4 *>(p)); }
-    __device__ __forceinline__ void zero() { v = make_float4(0, 0, 0, 0); }
-    __device__ __forceinline__ float4 get() const { return v; }
-};
 // the larger magnitudes of two packed pairs (a NaN is the largest)
 template <typename T>
-__device__ __forceinline__ uint32_t pair_max(uint32_t a, uint32_t b);
+__device__ __forceinline__ uint32_t word_max(uint32_t a, uint32_t b);
 template <>
-__device__ __forceinline__ uint32_t pair_max<__nv_bfloat16>(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t word_max<__nv_bfloat16>(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 template <>
-__device__ __forceinline__ uint32_t pair_max<__half>(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t word_max<__half>(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 template <>
-struct Quad<__nv_bfloat16> {
-    uint2 v;
-    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { v = __ldg(reinterpret_cast<const uint2 *>(p)); }
-    __device__ __forceinline__ void zero() { v = make_uint2(0, 0); }
-    __device__ __forceinline__ float4 get() const {
-        return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
-                           __uint_as_float(v.y & 0xFFFF0000u));
-    }
-    static __device__ __forceinline__ unsigned bits(unsigned h) { return h << 16; }      // float32 bits of a magnitude
-};
-template <>
-struct Quad<__half> {
-    uint2 v;
-    __device__ __forceinline__ void load(const __half *p) { v = __ldg(reinterpret_cast<const uint2 *>(p)); }
-    __device__ __forceinline__ void zero() { v = make_uint2(0, 0); }
-    __device__ __forceinline__ float4 get() const {
-        const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&v.x)), b = __half22float2(*reinterpret_cast<const __half2 *>(&v.y));
-        return make_float4(a.x, a.y, b.x, b.y);
-    }
-    static __device__ __forceinline__ unsigned bits(unsigned h) { return __float_as_uint(__half2float(__ushort_as_half((unsigned short)h))); }
-};
-// largest magnitudes of the four columns so far; add() gives back the row's own largest, in a form
-// that compares as an unsigned integer and that bits() makes a float32's bits
+__device__ __forceinline__ uint32_t word_max<float>(uint32_t a, uint32_t b) { return max(a, b); }   // bits of magnitudes
+
+// A lane's eight neighbouring elements of a row, as loaded (32-bit words of one or two elements).
+// Maxima are kept in the same form: words of magnitudes, one 16-bit magnitude m(k) per column.
 template <typename T>
-struct ColMax {
-    uint2 m;
-    __device__ __forceinline__ void zero() { m = make_uint2(0, 0); }
-    __device__ __forceinline__ unsigned add(const Quad<T> &q) {
-        const uint32_t a = q.v.x & 0x7FFF7FFFu, b = q.v.y & 0x7FFF7FFFu, r = pair_max<T>(a, b);
-        m.x = pair_max<T>(m.x, a);
-        m.y = pair_max<T>(m.y, b);
-        return max(r >> 16, r & 0xFFFFu);
+struct Oct {
+    static constexpr int W = 8 * (int)sizeof(T) / 4;
+    static constexpr uint32_t ABS = sizeof(T) == 4 ? 0x7FFFFFFFu : 0x7FFF7FFFu;
+    uint32_t w[W];
+    __device__ __forceinline__ void load(const T *p) {
+#pragma unroll
+        for (int i = 0; i < W; i += 4) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p) + i / 4);
+            w[i] = v.x;
+            w[i + 1] = v.y;
+            w[i + 2] = v.z;
+            w[i + 3] = v.w;
+        }
     }
-    static __device__ __forceinline__ unsigned bits(unsigned r) { return Quad<T>::bits(r); }
-    __device__ __forceinline__ uint4 get() const {
-        return make_uint4(bits(m.x & 0xFFFFu), bits(m.x >> 16), bits(m.y & 0xFFFFu), bits(m.y >> 16));
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < W; i++) w[i] = 0;
+    }
+    // elements 2 k and 2 k + 1
+    __device__ __forceinline__ uint64_t pair(int k) const {
+        if constexpr (sizeof(T) == 4) return pack2(w[2 * k], w[2 * k + 1]);
+        else if constexpr (std::is_same<T, __nv_bfloat16>::value) return pack2(w[k] << 16, w[k] & 0xFFFF0000u);
+        else {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[k]));
+            return pack2(__float_as_uint(f.x), __float_as_uint(f.y));
+        }
+    }
+    // float32 bits of the larger magnitude in a word of maxima
+    static __device__ __forceinline__ unsigned bits(uint32_t m) {
+        if constexpr (sizeof(T) == 4) return m;
+        const unsigned h = max(m >> 16, m & 0xFFFFu);
+        return std::is_same<T, __nv_bfloat16>::value ? h << 16 : __float_as_uint(__half2float(__ushort_as_half((unsigned short)h)));
     }
 };
-template <>
-struct ColMax<float> {
-    uint4 m;
-    __device__ __forceinline__ void zero() { m = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ unsigned add(const Quad<float> &q) {
-        const uint4 a = make_uint4(abs_bits(q.v.x), abs_bits(q.v.y), abs_bits(q.v.z), abs_bits(q.v.w));
-        m = make_uint4(max(m.x, a.x), max(m.y, a.y), max(m.z, a.z), max(m.w, a.w));
-        return max(max(a.x, a.y), max(a.z, a.w));
-    }
-    static __device__ __forceinline__ unsigned bits(unsigned r) { return r; }
-    __device__ __forceinline__ uint4 get() const { return m; }
-};
-__device__ __forceinline__ float4 scaled(float4 v, uint64_t s01, uint64_t s23) {
-    float4 r;
-    unpack2(mul2(pack2(__float_as_uint(v.x), __float_as_uint(v.y)), s01), r.x, r.y);
-    unpack2(mul2(pack2(__float_as_uint(v.z), __float_as_uint(v.w)), s23), r.z, r.w);
-    return r;
-}
-__device__ __forceinline__ uint64_t pair_of(float a, float b) { return pack2(__float_as_uint(a), __float_as_uint(b)); }
-__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+__device__ __forceinline__ uint32_t codes4(uint64_t ab, uint64_t cd) {
+    float a, b, c, d;
+    unpack2(ab, a, b);
+    unpack2(cd, c, d);
     return __byte_perm(codes2(a, b), codes2(c, d), 0x5410);
 }
 
 // Rows and columns of a 128 x 128 tile, or (WT) one scale for the whole tile of a weight matrix.
-// x is read once and stays in registers, 16 rows a warp and four columns a lane: a lane's 16 codes of
-// a column are 16 neighbouring bytes of the transposed output, and only codes pass through shared
-// memory (16-byte chunks permuted by the column) to leave as whole 128-byte rows.  Memory-bound.
+// x is read once and stays in registers: a warp holds 16 rows, a half-warp one row at a time, a lane
+// eight neighbouring columns of eight neighbouring rows, so that a lane's codes of a column are eight
+// neighbouring bytes of the transposed output; only codes and the columns' maxima pass through shared
+// memory.  Bound by instruction issue, then by memory: the row maxima meet in one transposing
+// butterfly (a lane ends with one row), a row's scale is computed once.
 template <typename T, bool WT>
 __global__ void __launch_bounds__(kQThreads, sizeof(T) == 4 ? 2 : 3) quantize_tile_kernel(const QuantArgs p) {
+    constexpr int NW = kQThreads / 32, W = Oct<T>::W;
     __shared__ __align__(16) uint8_t s_codes[kKB * kKB];
-    __shared__ __align__(16) uint4 s_col[kQThreads / 32][32];    // column maxima of every warp's rows
-    __shared__ unsigned s_max[kQThreads / 32];
-    constexpr int NR = kKB / (kQThreads / 32);                   // rows of a warp
-    static_assert(NR == 16, "a lane's codes of a column are one 16-byte chunk");
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __shared__ __align__(16) uint32_t s_col[NW][16 * W];         // column maxima of every warp's rows
+    __shared__ __align__(16) float s_inv[kKB];                   // 1 / scale of every column
+    __shared__ unsigned s_max[NW];
+    static_assert(NW == 8, "16 rows a warp");
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, half = lane >> 4, l16 = lane & 15;
     const int r0 = (int)blockIdx.y * kKB, kb = (int)blockIdx.x, e = (int)blockIdx.z;
-    const int c = kb * kKB + 4 * lane, rw = r0 + NR * warp;
+    const int c = kb * kKB + 8 * l16, rw = r0 + 16 * warp;
     const T *x = static_cast<const T *>(p.x) + (WT ? (size_t)e * p.R * p.ld : 0);
     uint8_t *codes = p.codes + (WT ? (size_t)e * p.R * p.width : 0);
     const int ldt = WT ? p.R : ((p.R + kKB - 1) / kKB) * kKB;    // bytes between rows of codes_t
     uint8_t *codes_t = p.codes_t + (WT ? (size_t)e * p.R * p.width : 0);
     const int nrb = (p.R + kKB - 1) / kKB, nkb = (p.width + kKB - 1) / kKB;
+    const bool in = c < p.width;
 
-    const int src = lane < NR ? src_row(p.rows, rw + lane, p.R, p.n_src) : -1;
-    Quad<T> v[NR];
+    const int src = src_row(p.rows, rw + l16, p.R, p.n_src);
+    Oct<T> v[8];
+    if (__all_sync(0xffffffffu, src >= 0 && in)) {
 #pragma unroll
-    for (int i = 0; i < NR; i++) {
-        const int s = __shfl_sync(0xffffffffu, src, i);
-        if (s >= 0 && c < p.width) v[i].load(x + (long long)s * p.ld + c);
-        else v[i].zero();
-    }
-    // maxima: of the columns in packed form, of row i in lane i
-    ColMax<T> cm;
-    cm.zero();
-    unsigned mine = 0;
+        for (int i = 0; i < 8; i++) v[i].load(x + (long long)__shfl_sync(0xffffffffu, src, 8 * half + i) * p.ld + c);
+    } else {
 #pragma unroll
-    for (int i = 0; i < NR; i++) {
-        const unsigned m = __reduce_max_sync(0xffffffffu, cm.add(v[i]));
-        if (lane == i) mine = m;
+        for (int i = 0; i < 8; i++) {
+            const int s = __shfl_sync(0xffffffffu, src, 8 * half + i);
+            if (s >= 0 && in) v[i].load(x + (long long)s * p.ld + c);
+            else v[i].zero();
+        }
     }
-    float rinv, cinv[4];
+    uint32_t cm[W], rm[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+#pragma unroll
+        for (int k = 0; k < W; k++) {
+            const uint32_t a = v[i].w[k] & Oct<T>::ABS;
+            cm[k] = i ? word_max<T>(cm[k], a) : a;
+            rm[i] = k ? word_max<T>(rm[i], a) : a;
+        }
+    }
+    // lane ends with the maximum of row 8 half + (l16 >> 1)
+#pragma unroll
+    for (int d = 8; d > 1; d >>= 1) {
+#pragma unroll
+        for (int i = 0; i < d / 2; i++) {
+            const uint32_t give = (lane & d) ? rm[i] : rm[i + d / 2], keep = (lane & d) ? rm[i + d / 2] : rm[i];
+            rm[i] = word_max<T>(keep, __shfl_xor_sync(0xffffffffu, give, d));
+        }
+    }
+    const unsigned mine = Oct<T>::bits(word_max<T>(rm[0], __shfl_xor_sync(0xffffffffu, rm[0], 1)));
+    float rinv;
     if (WT) {
         const unsigned m = __reduce_max_sync(0xffffffffu, mine);
         if (lane == 0) s_max[warp] = m;
         __syncthreads();
         unsigned most = 0;
-        for (int i = 0; i < kQThreads / 32; i++) most = max(most, s_max[i]);
-        const float s = block_scale(ColMax<T>::bits(most), rinv);
-        cinv[0] = cinv[1] = cinv[2] = cinv[3] = rinv;
-        if (threadIdx.x == 0) {
+#pragma unroll
+        for (int i = 0; i < NW; i++) most = max(most, s_max[i]);
+        const float s = block_scale(most, rinv);
+        if (tid == 0) {
             p.scales[((size_t)e * nrb + blockIdx.y) * nkb + kb] = s;
             if (p.codes_t) p.scales_t[((size_t)e * nkb + kb) * nrb + blockIdx.y] = s;
         }
     } else {
-        const float s = block_scale(ColMax<T>::bits(mine), rinv);
-        if (lane < NR && rw + lane < p.R) p.scales[(size_t)kb * p.R + rw + lane] = s;
-        s_col[warp][lane] = cm.get();
-        __syncthreads();
-        uint4 m = s_col[0][lane];
+        const float s = block_scale(mine, rinv);
+        const int r = rw + (lane >> 1);
+        if (!(lane & 1) && r < p.R) p.scales[(size_t)kb * p.R + r] = s;
 #pragma unroll
-        for (int w = 1; w < kQThreads / 32; w++) {
-            const uint4 o = s_col[w][lane];
-            m = make_uint4(max(m.x, o.x), max(m.y, o.y), max(m.z, o.z), max(m.w, o.w));
+        for (int k = 0; k < W; k++) cm[k] = word_max<T>(cm[k], __shfl_xor_sync(0xffffffffu, cm[k], 16));
+        if (half == 0) {
+#pragma unroll
+            for (int k = 0; k < W; k += 4) *reinterpret_cast<uint4 *>(&s_col[warp][l16 * W + k]) = make_uint4(cm[k], cm[k + 1], cm[k + 2], cm[k + 3]);
         }
-        const float4 t = make_float4(block_scale(m.x, cinv[0]), block_scale(m.y, cinv[1]), block_scale(m.z, cinv[2]), block_scale(m.w, cinv[3]));
-        if (warp == 0 && c < p.width) *reinterpret_cast<float4 *>(p.scales_t + (size_t)blockIdx.y * p.width + c) = t;
-    }
-    // codes of four rows at a time, both orientations from the same float32 values; q: this lane's
-    // chunk `warp` of its four columns
-    const uint64_t c01 = pair_of(cinv[0], cinv[1]), c23 = pair_of(cinv[2], cinv[3]);
-    const bool in = c < p.width;
-    uint8_t *o = codes + (size_t)rw * p.width + c;
-    uint32_t q[4][4];
+        __syncthreads();
+        if (tid < kKB) {
+            // column tid: its 16-bit half of the word that two columns share, or its own word
+            constexpr bool wide = sizeof(T) == 4;
+            uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < NR; i += 4) {
-        float4 f[4];
+            for (int w = 0; w < NW; w++) m = word_max<T>(m, s_col[w][wide ? tid : tid >> 1]);
+            float ci;
+            const float t = block_scale(Oct<T>::bits(wide ? m : (tid & 1) ? m & 0xFFFF0000u : m & 0xFFFFu), ci);
+            s_inv[tid] = ci;
+            if (kb * kKB + tid < p.width) p.scales_t[(size_t)blockIdx.y * p.width + kb * kKB + tid] = t;
+        }
+        __syncthreads();
+    }
+    uint64_t cs[4];
+    if (!WT) {
+#pragma unroll
+        for (int k = 0; k < 4; k += 2) {
+            const float4 f = *reinterpret_cast<const float4 *>(&s_inv[8 * l16 + 2 * k]);
+            cs[k] = pack2(__float_as_uint(f.x), __float_as_uint(f.y));
+            cs[k + 1] = pack2(__float_as_uint(f.z), __float_as_uint(f.w));
+        }
+    }
+    // codes of two rows at a time, both orientations from the same float32 values; q: this lane's
+    // eight bytes of each of its columns
+    const int ra = rw + 8 * half;
+    uint8_t *o = codes + (size_t)ra * p.width + c;
+    uint32_t q[8][2];
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        uint64_t f[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            const uint32_t r = __float_as_uint(WT ? rinv : __shfl_sync(0xffffffffu, rinv, 16 * half + 2 * (i + h)));
+            const uint64_t rr = pack2(r, r);
+            uint64_t a[4];
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                const uint64_t u = v[i + h].pair(k);
+                a[k] = mul2(u, rr);
+                f[h][k] = WT ? a[k] : mul2(u, cs[k]);
+            }
+            if (in && ra + i + h < p.R)
+                *reinterpret_cast<uint2 *>(o + (size_t)((i + h) * p.width)) = make_uint2(codes4(a[0], a[1]), codes4(a[2], a[3]));
+        }
 #pragma unroll
         for (int k = 0; k < 4; k++) {
-            const float4 u = v[i + k].get();
-            const float r = WT ? rinv : __shfl_sync(0xffffffffu, rinv, i + k);
-            const uint64_t rr = pair_of(r, r);
-            const float4 a = scaled(u, rr, rr);
-            f[k] = WT ? a : scaled(u, c01, c23);
-            if (in && rw + i + k < p.R) *reinterpret_cast<uint32_t *>(o) = codes4(a.x, a.y, a.z, a.w);
-            o += p.width;
+            float a0, a1, b0, b1;
+            unpack2(f[0][k], a0, b0);
+            unpack2(f[1][k], a1, b1);
+            const uint32_t x0 = codes2(a0, a1), x1 = codes2(b0, b1);
+            if (i % 4 == 0) {
+                q[2 * k][i / 4] = x0;
+                q[2 * k + 1][i / 4] = x1;
+            } else {
+                q[2 * k][i / 4] = __byte_perm(q[2 * k][i / 4], x0, 0x5410);
+                q[2 * k + 1][i / 4] = __byte_perm(q[2 * k + 1][i / 4], x1, 0x5410);
+            }
         }
-        q[0][i / 4] = codes4(f[0].x, f[1].x, f[2].x, f[3].x);
-        q[1][i / 4] = codes4(f[0].y, f[1].y, f[2].y, f[3].y);
-        q[2][i / 4] = codes4(f[0].z, f[1].z, f[2].z, f[3].z);
-        q[3][i / 4] = codes4(f[0].w, f[1].w, f[2].w, f[3].w);
     }
     if (WT && !p.codes_t) return;
-    // chunk `warp` of column 4 lane + k, at chunk position warp ^ (lane & 7) of that column's 128 bytes
+    // 16-byte chunk `warp` of column 8 l16 + k, at chunk position warp ^ (l16 & 7) of that column's 128 bytes
 #pragma unroll
-    for (int k = 0; k < 4; k++)
-        *reinterpret_cast<uint4 *>(&s_codes[(4 * lane + k) * kKB + 16 * (warp ^ (lane & 7))]) = make_uint4(q[k][0], q[k][1], q[k][2], q[k][3]);
+    for (int k = 0; k < 8; k++)
+        *reinterpret_cast<uint2 *>(&s_codes[(8 * l16 + k) * kKB + 16 * (warp ^ (l16 & 7)) + 8 * half]) = make_uint2(q[k][0], q[k][1]);
     __syncthreads();
-    for (int i = threadIdx.x; i < kKB * 8; i += kQThreads) {
+    for (int i = tid; i < kKB * 8; i += kQThreads) {
         const int cc = i >> 3, ch = i & 7, col = kb * kKB + cc, r = r0 + 16 * ch;
         if (col >= p.width) continue;
-        const uint4 u = *reinterpret_cast<const uint4 *>(&s_codes[cc * kKB + 16 * (ch ^ ((cc >> 2) & 7))]);
+        const uint4 u = *reinterpret_cast<const uint4 *>(&s_codes[cc * kKB + 16 * (ch ^ ((cc >> 3) & 7))]);
         uint8_t *t = codes_t + (size_t)col * ldt + r;
         if (!WT || (p.R % 16 == 0 && r < p.R)) {
             *reinterpret_cast<uint4 *>(t) = u;

@@ -184,8 +184,7 @@ struct BalArgs {
     int *counts, *tokens;      // [S, E], [S]
     float *sums;               // [S, E]
     void *dlogits;
-    float *part_sums;          // [slots][E]
-    int *part_counts;          // [slots][E]
+    int2 *part;                // [slots][E]: sum (float32 bits) and count of a block's tokens of one segment
     int *part_tokens;          // [slots]
     double *part_loss;         // [S][groups of 32 experts]
     unsigned *ticket;
@@ -211,17 +210,79 @@ template <>
 __device__ __forceinline__ __nv_bfloat16 cast1<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 template <>
 __device__ __forceinline__ __half cast1<__half>(float v) { return __float2half_rn(v); }
+// four neighbours
+__device__ __forceinline__ void ld4(const float *p, float *v) {
+    const float4 f = __ldg(reinterpret_cast<const float4 *>(p));
+    v[0] = f.x;
+    v[1] = f.y;
+    v[2] = f.z;
+    v[3] = f.w;
+}
+__device__ __forceinline__ void ld4(const __nv_bfloat16 *p, float *v) {
+    const uint2 f = __ldg(reinterpret_cast<const uint2 *>(p));
+    v[0] = __uint_as_float(f.x << 16);
+    v[1] = __uint_as_float(f.x & 0xFFFF0000u);
+    v[2] = __uint_as_float(f.y << 16);
+    v[3] = __uint_as_float(f.y & 0xFFFF0000u);
+}
+__device__ __forceinline__ void ld4(const __half *p, float *v) {
+    const uint2 f = __ldg(reinterpret_cast<const uint2 *>(p));
+    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&f.x)), b = __half22float2(*reinterpret_cast<const __half2 *>(&f.y));
+    v[0] = a.x;
+    v[1] = a.y;
+    v[2] = b.x;
+    v[3] = b.y;
+}
+__device__ __forceinline__ void st4(float *p, const float *v) { *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]); }
+template <typename T>
+__device__ __forceinline__ void st4(T *p, const float *v) {
+    const T t[4] = {cast1<T>(v[0]), cast1<T>(v[1]), cast1<T>(v[2]), cast1<T>(v[3])};
+    *reinterpret_cast<uint2 *>(p) = *reinterpret_cast<const uint2 *>(t);
+}
 
-__device__ __forceinline__ float warp_add(float v) {
+// How a warp holds tokens: LPT lanes a token (32 / LPT tokens at once), J experts a lane; with VEC
+// (E a multiple of 4, rows aligned) quads of neighbouring experts, else every LPT-th expert.
+template <typename T_, int J_, int LPT_, bool VEC_>
+struct Lay {
+    using T = T_;
+    static constexpr int J = J_, LPT = LPT_, G = 32 / LPT;
+    static constexpr bool VEC = VEC_;
+    static constexpr int U = J <= 8 ? 2 : 1;      // tokens in flight for every group of lanes
+    __device__ __forceinline__ static int expert(int l, int j) { return VEC ? 4 * (l + LPT * (j / 4)) + j % 4 : l + LPT * j; }
+    __device__ __forceinline__ static void load(const T *row, int E, int l, bool on, float (&x)[J]) {
+        if constexpr (VEC) {
 #pragma unroll
-    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-    return v;
-}
-__device__ __forceinline__ float warp_max(float v) {   // a NaN anywhere may be passed over: the sum carries it
+            for (int j = 0; j < J; j += 4) {
+                if (on && expert(l, j) < E) ld4(row + expert(l, j), &x[j]);
+                else x[j] = x[j + 1] = x[j + 2] = x[j + 3] = 0.0f;
+            }
+        } else {
 #pragma unroll
-    for (int d = 16; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
-    return v;
-}
+            for (int j = 0; j < J; j++) x[j] = on && expert(l, j) < E ? ld1(row + expert(l, j)) : 0.0f;
+        }
+    }
+    __device__ __forceinline__ static void store(T *row, int E, int l, const float (&x)[J]) {
+        if constexpr (VEC) {
+#pragma unroll
+            for (int j = 0; j < J; j += 4)
+                if (expert(l, j) < E) st4(row + expert(l, j), &x[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < J; j++)
+                if (expert(l, j) < E) row[expert(l, j)] = cast1<T>(x[j]);
+        }
+    }
+    __device__ __forceinline__ static float add(float v) {
+#pragma unroll
+        for (int d = LPT / 2; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+        return v;
+    }
+    __device__ __forceinline__ static float most(float v) {   // a NaN may be passed over: the sum carries it
+#pragma unroll
+        for (int d = LPT / 2; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+        return v;
+    }
+};
 __device__ __forceinline__ int seq_at(const BalArgs &p, int s) {
     return p.seq ? min(max(__ldg(p.seq + s), 0), p.T) : (s ? p.T : 0);
 }
@@ -235,50 +296,51 @@ __device__ __forceinline__ int seq_of(const BalArgs &p, int t) {
     }
     return lo;
 }
-// a token's normalised scores, lane's experts lane + 32 j (0 outside); c1: 1 - sigma (sigmoid only)
-template <int J>
-__device__ __forceinline__ void scores(const float (&x)[J], int E, int lane, int softmax, float (&pr)[J], float (&c1)[J]) {
+// a token's normalised scores (0 outside E); c1: 1 - sigma (sigmoid only)
+template <class L>
+__device__ __forceinline__ void scores(const float (&x)[L::J], int E, int l, int softmax, float (&pr)[L::J], float (&c1)[L::J]) {
+    constexpr int J = L::J;
     float z = 0.0f;
     if (softmax) {
         float m = -INFINITY;
 #pragma unroll
         for (int j = 0; j < J; j++)
-            if (lane + 32 * j < E) m = fmaxf(m, x[j]);
-        m = warp_max(m);
+            if (L::expert(l, j) < E) m = fmaxf(m, x[j]);
+        m = L::most(m);
         if (m == -INFINITY) m = 0.0f;      // no expert left: every probability 0 (below)
 #pragma unroll
         for (int j = 0; j < J; j++) {
-            pr[j] = lane + 32 * j < E ? expf(x[j] - m) : 0.0f;
+            pr[j] = L::expert(l, j) < E ? expf(x[j] - m) : 0.0f;
             z += pr[j];
         }
-        z = warp_add(z);
+        z = L::add(z);
         z = z == 0.0f ? 1.0f : z;
     } else {
 #pragma unroll
         for (int j = 0; j < J; j++) {
-            const float t = expf(-fabsf(x[j])), r = 1.0f / (1.0f + t);
-            pr[j] = lane + 32 * j < E ? (x[j] >= 0.0f ? r : t * r) : 0.0f;
-            if (x[j] != x[j] && lane + 32 * j < E) pr[j] = x[j];
+            const float t = expf(-fabsf(x[j])), r = __fdividef(1.0f, 1.0f + t);
+            pr[j] = L::expert(l, j) < E ? (x[j] >= 0.0f ? r : t * r) : 0.0f;   // a NaN stays one
             c1[j] = x[j] >= 0.0f ? t * r : r;
             z += pr[j];
         }
-        z = warp_add(z) + 1e-20f;
+        z = L::add(z) + 1e-20f;
     }
     const float inv = 1.0f / z;
 #pragma unroll
     for (int j = 0; j < J; j++) pr[j] *= inv;
 }
 
-template <typename T, int J>
+template <class L>
 __global__ void __launch_bounds__(kBalThreads) balance_part_kernel(const BalArgs p) {
+    constexpr int J = L::J, U = L::U, G = L::G;
     extern __shared__ float bsm[];
-    float *ws = bsm;                                          // [warps][E]
-    int *cnt = reinterpret_cast<int *>(bsm + kBalWarps * p.E);   // [E]
+    float *ws = bsm;                                                 // [warps * G][E]
+    int *cnt = reinterpret_cast<int *>(bsm + kBalWarps * G * p.E);   // [E]
     __shared__ int s_n;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, l = lane % L::LPT, g = lane / L::LPT;
     if (blockIdx.x == 0 && tid == 0) *p.ticket = 0;
     const int t0 = (int)blockIdx.x * p.per_block, t1 = min(t0 + p.per_block, p.T);
-    const T *logits = static_cast<const T *>(p.logits);
+    const typename L::T *logits = static_cast<const typename L::T *>(p.logits);
     for (int s = seq_of(p, t0); s < p.S && seq_at(p, s) < t1; s++) {
         const int a = max(seq_at(p, s), t0), b = min(seq_at(p, s + 1), t1);
         if (a >= b) continue;
@@ -289,25 +351,22 @@ __global__ void __launch_bounds__(kBalThreads) balance_part_kernel(const BalArgs
 #pragma unroll
         for (int j = 0; j < J; j++) sum[j] = 0.0f;
         int n = 0;
-        constexpr int U = J <= 8 ? 2 : 1;                     // tokens in flight
-        for (int t = a + warp; t < b; t += U * kBalWarps) {
+        for (int t = a + warp * G; t < b; t += U * kBalWarps * G) {      // the warp's lanes together
             float x[U][J];
             bool on[U];
 #pragma unroll
             for (int u = 0; u < U; u++) {
-                const int tt = t + u * kBalWarps;
+                const int tt = t + u * kBalWarps * G + g;
                 on[u] = tt < b && (!p.mask || p.mask[tt]);
-#pragma unroll
-                for (int j = 0; j < J; j++) x[u][j] = on[u] && lane + 32 * j < p.E ? ld1(logits + tt * p.ld + lane + 32 * j) : 0.0f;
+                L::load(logits + (long long)tt * p.ld, p.E, l, on[u], x[u]);
             }
 #pragma unroll
             for (int u = 0; u < U; u++) {
-                if (!on[u]) continue;
                 float pr[J], c1[J];
-                scores<J>(x[u], p.E, lane, p.softmax, pr, c1);
+                scores<L>(x[u], p.E, l, p.softmax, pr, c1);
 #pragma unroll
-                for (int j = 0; j < J; j++) sum[j] += pr[j];
-                n++;
+                for (int j = 0; j < J; j++) sum[j] += on[u] ? pr[j] : 0.0f;
+                n += on[u] ? 1 : 0;
             }
         }
         const long long i0 = (long long)a * p.K, i1 = (long long)b * p.K;
@@ -317,16 +376,15 @@ __global__ void __launch_bounds__(kBalThreads) balance_part_kernel(const BalArgs
         }
 #pragma unroll
         for (int j = 0; j < J; j++)
-            if (lane + 32 * j < p.E) ws[warp * p.E + lane + 32 * j] = sum[j];
-        if (lane == 0) atomicAdd(&s_n, n);
+            if (L::expert(l, j) < p.E) ws[(warp * G + g) * p.E + L::expert(l, j)] = sum[j];
+        if (l == 0) atomicAdd(&s_n, n);
         __syncthreads();
         const size_t slot = (size_t)blockIdx.x + s;
         for (int e = tid; e < p.E; e += kBalThreads) {
             float v = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kBalWarps; w++) v += ws[w * p.E + e];
-            p.part_sums[slot * p.E + e] = v;
-            p.part_counts[slot * p.E + e] = cnt[e];
+            for (int w = 0; w < kBalWarps * G; w++) v += ws[w * p.E + e];
+            p.part[slot * p.E + e] = make_int2(__float_as_int(v), cnt[e]);
         }
         if (tid == 0) p.part_tokens[slot] = s_n;
         __syncthreads();
@@ -346,15 +404,16 @@ __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(const BalArgs 
     int cnt = 0, tok = 0;
     if (b > a) {
         const int b0 = a / p.per_block, b1 = (b - 1) / p.per_block;
-#pragma unroll 4
-        for (int k = b0 + strand; k <= b1; k += 32) {
-            const size_t slot = (size_t)k + s;
-            if (e < p.E) {
-                sum += p.part_sums[slot * p.E + e];
-                cnt += p.part_counts[slot * p.E + e];
+        if (e < p.E) {
+#pragma unroll 8
+            for (int k = b0 + strand; k <= b1; k += 32) {
+                const int2 v = __ldg(p.part + ((size_t)k + s) * p.E + e);
+                sum += __int_as_float(v.x);
+                cnt += v.y;
             }
-            tok += p.part_tokens[slot];
         }
+        for (int k = b0 + (int)threadIdx.x; k <= b1; k += kSumThreads) tok += p.part_tokens[(size_t)k + s];
+        tok = __reduce_add_sync(0xffffffffu, tok);
     }
     s_sum[strand][lane] = sum;
     s_cnt[strand][lane] = cnt;
@@ -395,14 +454,15 @@ __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(const BalArgs 
     }
 }
 
-// A warp per token, per_block / warps of them in a row; a segment's counts stay in registers.
-template <typename T, int J>
+// Every warp a run of tokens; a segment's counts stay in registers.
+template <class L>
 __global__ void __launch_bounds__(kBalThreads) balance_grad_kernel(const BalArgs p) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int J = L::J, U = L::U, G = L::G;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % L::LPT, k = lane / L::LPT;
     const int each = p.per_block / kBalWarps;
     const int ta = ((int)blockIdx.x * kBalWarps + warp) * each, tb = min(ta + each, p.T);
-    const T *logits = static_cast<const T *>(p.logits);
-    T *out = static_cast<T *>(p.dlogits);
+    const typename L::T *logits = static_cast<const typename L::T *>(p.logits);
+    typename L::T *out = static_cast<typename L::T *>(p.dlogits);
     const double g = (p.grad ? (double)__ldg(p.grad) : 1.0) * p.coef * p.E / ((double)p.K * p.S);
     for (int s = ta < tb ? seq_of(p, ta) : p.S; s < p.S && seq_at(p, s) < tb; s++) {
         const int a = max(seq_at(p, s), ta), b = min(seq_at(p, s + 1), tb);
@@ -411,64 +471,62 @@ __global__ void __launch_bounds__(kBalThreads) balance_grad_kernel(const BalArgs
         const float up = (float)(g / ((double)n * n));
         float c[J];
 #pragma unroll
-        for (int j = 0; j < J; j++) c[j] = lane + 32 * j < p.E ? (float)__ldg(p.counts + (size_t)s * p.E + lane + 32 * j) : 0.0f;
-        constexpr int U = J <= 8 ? 2 : 1;
-        for (int t = a; t < b; t += U) {
+        for (int j = 0; j < J; j++) c[j] = L::expert(l, j) < p.E ? (float)__ldg(p.counts + (size_t)s * p.E + L::expert(l, j)) : 0.0f;
+        for (int t = a; t < b; t += U * G) {
             float x[U][J];
             bool on[U];
 #pragma unroll
             for (int u = 0; u < U; u++) {
-                on[u] = t + u < b && (!p.mask || p.mask[t + u]);
-#pragma unroll
-                for (int j = 0; j < J; j++)
-                    x[u][j] = on[u] && lane + 32 * j < p.E ? ld1(logits + (t + u) * p.ld + lane + 32 * j) : 0.0f;
+                const int tt = t + u * G + k;
+                on[u] = tt < b && (!p.mask || p.mask[tt]);
+                L::load(logits + (long long)tt * p.ld, p.E, l, on[u], x[u]);
             }
 #pragma unroll
             for (int u = 0; u < U; u++) {
-                if (t + u >= b) continue;
-                float d[J];
-                if (on[u]) {
-                    float pr[J], c1[J], dot = 0.0f;
-                    scores<J>(x[u], p.E, lane, p.softmax, pr, c1);
+                const int tt = t + u * G + k;
+                float pr[J], c1[J], dot = 0.0f;
+                scores<L>(x[u], p.E, l, p.softmax, pr, c1);
 #pragma unroll
-                    for (int j = 0; j < J; j++) dot = fmaf(pr[j], c[j], dot);
-                    dot = warp_add(dot);
+                for (int j = 0; j < J; j++) dot = fmaf(pr[j], c[j], dot);
+                dot = L::add(dot);
 #pragma unroll
-                    for (int j = 0; j < J; j++) {
-                        d[j] = up * pr[j] * (c[j] - dot);
-                        if (!p.softmax) d[j] *= c1[j];
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < J; j++) d[j] = 0.0f;
+                for (int j = 0; j < J; j++) {
+                    float d = up * pr[j] * (c[j] - dot);
+                    if (!p.softmax) d *= c1[j];
+                    x[u][j] = on[u] ? d : 0.0f;
                 }
-#pragma unroll
-                for (int j = 0; j < J; j++)
-                    if (lane + 32 * j < p.E) out[(t + u) * p.ldd + lane + 32 * j] = cast1<T>(d[j]);
+                if (tt < b) L::store(out + (long long)tt * p.ldd, p.E, l, x[u]);
             }
         }
     }
 }
 
-template <typename F>
-cudaError_t by_type(int dtype, int E, F &&f) {
-#define MOE_BAL_J(T)                                                                      \
-    do {                                                                                  \
-        if (E <= 64) return f(T{}, std::integral_constant<int, 2>{});                     \
-        if (E <= 128) return f(T{}, std::integral_constant<int, 4>{});                    \
-        if (E <= 256) return f(T{}, std::integral_constant<int, 8>{});                    \
-        if (E <= 512) return f(T{}, std::integral_constant<int, 16>{});                   \
-        return f(T{}, std::integral_constant<int, 32>{});                                 \
+template <bool VEC, typename F>
+cudaError_t by_layout(int dtype, int E, F &&f) {
+#define MOE_BAL_E(T)                                         \
+    do {                                                     \
+        if (E <= 32) return f(Lay<T, 4, 8, VEC>{});          \
+        if (E <= 64) return f(Lay<T, 8, 8, VEC>{});          \
+        if (E <= 128) return f(Lay<T, 8, 16, VEC>{});        \
+        if (E <= 256) return f(Lay<T, 8, 32, VEC>{});        \
+        if (E <= 512) return f(Lay<T, 16, 32, VEC>{});       \
+        return f(Lay<T, 32, 32, VEC>{});                     \
     } while (0)
-    if (dtype == MOE_DTYPE_F32) MOE_BAL_J(float);
-    if (dtype == MOE_DTYPE_BF16) MOE_BAL_J(__nv_bfloat16);
-    MOE_BAL_J(__half);
-#undef MOE_BAL_J
+    if (dtype == MOE_DTYPE_F32) MOE_BAL_E(float);
+    if (dtype == MOE_DTYPE_BF16) MOE_BAL_E(__nv_bfloat16);
+    MOE_BAL_E(__half);
+#undef MOE_BAL_E
+}
+// quads: E and the rows' strides multiples of four, the rows on four elements' boundary
+bool quads(const void *x, long long ld, int dtype, int E) {
+    const int el = dtype == MOE_DTYPE_F32 ? 4 : 2;
+    return E % 4 == 0 && ld % 4 == 0 && (reinterpret_cast<uintptr_t>(x) & (uintptr_t)(4 * el - 1)) == 0;
 }
 
-// tokens of a forward block: enough blocks to cover the card, at most 64 tokens each
+// tokens of a block: enough blocks to cover the card four times, at most 128 tokens each (fewer slots
+// for the sums to read)
 int tokens_per_block(int T) {
-    int n = 64;
+    int n = 128;
     while (n > kBalWarps && (T + n - 1) / n < 4 * 152) n /= 2;
     return n;
 }
@@ -510,7 +568,7 @@ cudaError_t launch_lists(const int *idx, int T, int K, int E, int align, long lo
 
 size_t balance_workspace(int T, int E, int S) {
     const size_t slots = balance_slots(T, S);
-    return up16(slots * E * 4) + up16(slots * E * 4) + up16(slots * 4) + up16((size_t)S * ((E + 31) / 32) * 8) + 16;
+    return up16(slots * E * 8) + up16(slots * 4) + up16((size_t)S * ((E + 31) / 32) * 8) + 16;
 }
 
 cudaError_t launch_balance_forward(const void *logits, int dtype, long long ld, int T, int E, const int *idx, int K, int softmax,
@@ -535,21 +593,20 @@ cudaError_t launch_balance_forward(const void *logits, int dtype, long long ld, 
     p.per_block = tokens_per_block(T);
     const size_t slots = balance_slots(T, S);
     char *w = static_cast<char *>(ws);
-    p.part_sums = reinterpret_cast<float *>(w);
-    w += up16(slots * E * 4);
-    p.part_counts = reinterpret_cast<int *>(w);
-    w += up16(slots * E * 4);
+    p.part = reinterpret_cast<int2 *>(w);
+    w += up16(slots * E * 8);
     p.part_tokens = reinterpret_cast<int *>(w);
     w += up16(slots * 4);
     p.part_loss = reinterpret_cast<double *>(w);
     w += up16((size_t)S * ((E + 31) / 32) * 8);
     p.ticket = reinterpret_cast<unsigned *>(w);
-    const cudaError_t e = by_type(dtype, E, [&](auto t, auto j) {
+    auto go = [&](auto lay) {
+        using L = decltype(lay);
         const int blocks = T > 0 ? (T + p.per_block - 1) / p.per_block : 1;
-        balance_part_kernel<decltype(t), decltype(j)::value>
-            <<<blocks, kBalThreads, ((size_t)kBalWarps + 1) * E * sizeof(float), st>>>(p);
+        balance_part_kernel<L><<<blocks, kBalThreads, ((size_t)kBalWarps * L::G + 1) * E * sizeof(float), st>>>(p);
         return cudaGetLastError();
-    });
+    };
+    const cudaError_t e = quads(logits, ld, dtype, E) ? by_layout<true>(dtype, E, go) : by_layout<false>(dtype, E, go);
     if (e != cudaSuccess) return e;
     balance_sum_kernel<<<dim3((E + 31) / 32, S), kSumThreads, 0, st>>>(p);
     return cudaGetLastError();
@@ -575,10 +632,11 @@ cudaError_t launch_balance_backward(const void *logits, int dtype, long long ld,
     p.S = S;
     p.softmax = softmax;
     p.per_block = tokens_per_block(T);
-    return by_type(dtype, E, [&](auto t, auto j) {
-        balance_grad_kernel<decltype(t), decltype(j)::value><<<(T + p.per_block - 1) / p.per_block, kBalThreads, 0, st>>>(p);
+    auto go = [&](auto lay) {
+        balance_grad_kernel<decltype(lay)><<<(T + p.per_block - 1) / p.per_block, kBalThreads, 0, st>>>(p);
         return cudaGetLastError();
-    });
+    };
+    return quads(logits, ld, dtype, E) && quads(dlogits, ldd, dtype, E) ? by_layout<true>(dtype, E, go) : by_layout<false>(dtype, E, go);
 }
 
 }  // namespace moe
