@@ -467,8 +467,8 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) fp8_gemm_kernel(const _
                 Tile ti = walk.at(t);
                 part(ti);
                 for (int kb = ti.k0; kb < ti.k1; kb++) {
-                    if (!__all_sync(0xffffffffu, ring_wait(smem_u32(&s_tempty[q.slot]), q.phase ^ 1u, fail) &&
-                                                     ring_wait(smem_u32(&s_full[r.slot]), r.phase, fail))) {
+                    if (!__all_sync(0xffffffffu, ring_wait(smem_u32(&s_full[r.slot]), r.phase, fail) &&
+                                                     ring_wait(smem_u32(&s_tempty[q.slot]), q.phase ^ 1u, fail))) {
                         ok = false;
                         break;
                     }
@@ -986,9 +986,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
                         break;
                     }
                     for (int kb = ti.k0; kb < k1; kb++) {
-                        const bool w = C::MX ? ring_wait(smem_u32(&s_sfull[r.slot]), r.phase, fail)
-                                             : ring_wait(smem_u32(&s_tempty[q.slot]), q.phase ^ 1u, fail);
-                        if (!__all_sync(0xffffffffu, w && ring_wait(smem_u32(&s_full[r.slot]), r.phase, fail))) {
+                        // the operands first: they are there early, the accumulator comes back last
+                        const bool w = ring_wait(smem_u32(&s_full[r.slot]), r.phase, fail) &&
+                                       (C::MX ? ring_wait(smem_u32(&s_sfull[r.slot]), r.phase, fail)
+                                              : ring_wait(smem_u32(&s_tempty[q.slot]), q.phase ^ 1u, fail));
+                        if (!__all_sync(0xffffffffu, w)) {
                             ok = false;
                             break;
                         }
@@ -1323,7 +1325,7 @@ __device__ __forceinline__ uint32_t codes4(uint64_t ab, uint64_t cd) {
 // memory.  Bound by instruction issue, then by memory: the row maxima meet in one transposing
 // butterfly (a lane ends with one row), a row's scale is computed once.
 template <typename T, bool WT>
-__global__ void __launch_bounds__(kQThreads, sizeof(T) == 4 ? 2 : 3) quantize_tile_kernel(const QuantArgs p) {
+__global__ void __launch_bounds__(kQThreads, sizeof(T) == 4 ? 2 : 4) quantize_tile_kernel(const QuantArgs p) {
     constexpr int NW = kQThreads / 32, W = Oct<T>::W;
     __shared__ __align__(16) uint8_t s_codes[kKB * kKB];
     __shared__ __align__(16) uint32_t s_col[NW][16 * W];         // column maxima of every warp's rows

@@ -186,9 +186,9 @@ struct BalArgs {
     void *dlogits;
     int2 *part;                // [slots][E]: sum (float32 bits) and count of a block's tokens of one segment
     int *part_tokens;          // [slots]
-    double *part_loss;         // [S][groups of 32 experts]
+    float *part_loss;          // [S][groups of kSumE experts]
     unsigned *ticket;
-    float coef;
+    float scale;               // coef E / (K S)
     int T, E, K, S, per_block, softmax;
 };
 
@@ -283,19 +283,30 @@ struct Lay {
         return v;
     }
 };
-__device__ __forceinline__ int seq_at(const BalArgs &p, int s) {
-    return p.seq ? min(max(__ldg(p.seq + s), 0), p.T) : (s ? p.T : 0);
-}
-// first segment that ends after token t (S when none does)
-__device__ __forceinline__ int seq_of(const BalArgs &p, int t) {
-    int lo = 0, hi = p.S;
-    while (lo < hi) {
-        const int m = (lo + hi) >> 1;
-        if (seq_at(p, m + 1) > t) hi = m;
-        else lo = m + 1;
+// The segments' offsets, in shared memory where they fit: a chain of dependent loads costs a
+// microsecond a step.  Clamped to [0, T].
+constexpr int kSegs = 512;
+struct Segs {
+    const int *g, *sm;
+    int T, S;
+    // all threads of the block; ends with a barrier
+    __device__ __forceinline__ Segs(const BalArgs &p, int *buf) : g(p.seq), sm(p.seq && p.S < kSegs ? buf : nullptr), T(p.T), S(p.S) {
+        if (sm)
+            for (int i = threadIdx.x; i <= S; i += blockDim.x) buf[i] = min(max(__ldg(g + i), 0), T);
+        __syncthreads();
     }
-    return lo;
-}
+    __device__ __forceinline__ int at(int s) const { return sm ? sm[s] : g ? min(max(__ldg(g + s), 0), T) : (s ? T : 0); }
+    // first segment that ends after token t (S when none does)
+    __device__ __forceinline__ int of(int t) const {
+        int lo = 0, hi = S;
+        while (lo < hi) {
+            const int m = (lo + hi) >> 1;
+            if (at(m + 1) > t) hi = m;
+            else lo = m + 1;
+        }
+        return lo;
+    }
+};
 // a token's normalised scores (0 outside E); c1: 1 - sigma (sigmoid only)
 template <class L>
 __device__ __forceinline__ void scores(const float (&x)[L::J], int E, int l, int softmax, float (&pr)[L::J], float (&c1)[L::J]) {
@@ -336,13 +347,14 @@ __global__ void __launch_bounds__(kBalThreads) balance_part_kernel(const BalArgs
     extern __shared__ float bsm[];
     float *ws = bsm;                                                 // [warps * G][E]
     int *cnt = reinterpret_cast<int *>(bsm + kBalWarps * G * p.E);   // [E]
-    __shared__ int s_n;
+    __shared__ int s_n, s_seg[kSegs];
+    const Segs seg(p, s_seg);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, l = lane % L::LPT, g = lane / L::LPT;
     if (blockIdx.x == 0 && tid == 0) *p.ticket = 0;
     const int t0 = (int)blockIdx.x * p.per_block, t1 = min(t0 + p.per_block, p.T);
     const typename L::T *logits = static_cast<const typename L::T *>(p.logits);
-    for (int s = seq_of(p, t0); s < p.S && seq_at(p, s) < t1; s++) {
-        const int a = max(seq_at(p, s), t0), b = min(seq_at(p, s + 1), t1);
+    for (int s = seg.of(t0); s < p.S && seg.at(s) < t1; s++) {
+        const int a = max(seg.at(s), t0), b = min(seg.at(s + 1), t1);
         if (a >= b) continue;
         for (int e = tid; e < p.E; e += kBalThreads) cnt[e] = 0;
         if (tid == 0) s_n = 0;
@@ -391,66 +403,83 @@ __global__ void __launch_bounds__(kBalThreads) balance_part_kernel(const BalArgs
     }
 }
 
-// One block per (32 experts, segment): the slots' sums in a fixed order (32 strands, then the strands),
-// then the block's part of the loss; the last block to finish adds the parts in order.
+// One block per (kSumE experts, segment): the slots' sums in a fixed order (128 strands of slots, then
+// the strands in pairs), then the block's part of the loss; the last block to finish adds the parts in
+// order.  Bound by latency: few loads a thread, all in flight.
+constexpr int kSumE = 8;
 __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(const BalArgs p) {
-    __shared__ float s_sum[32][33];
-    __shared__ int s_cnt[32][33], s_tok[32];
+    constexpr int STRANDS = kSumThreads / kSumE;
+    __shared__ float s_sum[32][kSumE];
+    __shared__ int s_cnt[32][kSumE], s_tok[32];
     __shared__ bool s_last;
-    const int lane = threadIdx.x & 31, strand = threadIdx.x >> 5;
-    const int s = (int)blockIdx.y, g = (int)blockIdx.x, G = (int)gridDim.x, e = 32 * g + lane;
-    const int a = seq_at(p, s), b = seq_at(p, s + 1);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int s = (int)blockIdx.y, g = (int)blockIdx.x, G = (int)gridDim.x, e = kSumE * g + tid % kSumE;
+    const int a = p.seq ? min(max(__ldg(p.seq + s), 0), p.T) : 0, b = p.seq ? min(max(__ldg(p.seq + s + 1), 0), p.T) : p.T;
     float sum = 0.0f;
     int cnt = 0, tok = 0;
     if (b > a) {
         const int b0 = a / p.per_block, b1 = (b - 1) / p.per_block;
         if (e < p.E) {
 #pragma unroll 8
-            for (int k = b0 + strand; k <= b1; k += 32) {
+            for (int k = b0 + tid / kSumE; k <= b1; k += STRANDS) {
                 const int2 v = __ldg(p.part + ((size_t)k + s) * p.E + e);
                 sum += __int_as_float(v.x);
                 cnt += v.y;
             }
         }
-        for (int k = b0 + (int)threadIdx.x; k <= b1; k += kSumThreads) tok += p.part_tokens[(size_t)k + s];
-        tok = __reduce_add_sync(0xffffffffu, tok);
+        for (int k = b0 + tid; k <= b1; k += kSumThreads) tok += p.part_tokens[(size_t)k + s];
     }
-    s_sum[strand][lane] = sum;
-    s_cnt[strand][lane] = cnt;
-    if (lane == 0) s_tok[strand] = tok;
+#pragma unroll
+    for (int d = kSumE; d < 32; d *= 2) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        cnt += __shfl_xor_sync(0xffffffffu, cnt, d);
+    }
+    tok = __reduce_add_sync(0xffffffffu, tok);
+    if (lane < kSumE) {
+        s_sum[warp][lane] = sum;
+        s_cnt[warp][lane] = cnt;
+    }
+    if (lane == 0) s_tok[warp] = tok;
     __syncthreads();
-    if (strand == 0) {
+    if (warp == 0) {
+        // lane: expert lane % kSumE of every (32 / kSumE)-th warp's sums
         sum = 0.0f;
-        cnt = tok = 0;
-        for (int i = 0; i < 32; i++) {
-            sum += s_sum[i][lane];
-            cnt += s_cnt[i][lane];
-            tok += s_tok[i];
+        cnt = 0;
+#pragma unroll
+        for (int i = 0; i < kSumE; i++) {
+            sum += s_sum[lane / kSumE + i * (32 / kSumE)][lane % kSumE];
+            cnt += s_cnt[lane / kSumE + i * (32 / kSumE)][lane % kSumE];
         }
-        if (e < p.E) {
+#pragma unroll
+        for (int d = kSumE; d < 32; d *= 2) {
+            sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            cnt += __shfl_xor_sync(0xffffffffu, cnt, d);
+        }
+        tok = __reduce_add_sync(0xffffffffu, s_tok[lane]);
+        if (lane < kSumE && e < p.E) {
             p.sums[(size_t)s * p.E + e] = sum;
             p.counts[(size_t)s * p.E + e] = cnt;
         }
         if (g == 0 && lane == 0) p.tokens[s] = tok;
-        double l = e < p.E ? (double)sum * (double)cnt : 0.0;
+        float l = e < p.E ? sum * (float)cnt : 0.0f;
 #pragma unroll
-        for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+        for (int d = kSumE / 2; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
         if (lane == 0) {
-            const double n = tok > 0 ? tok : 1;
-            p.part_loss[(size_t)s * G + g] = (double)p.coef * p.E / ((double)p.K * p.S * n * n) * l;
+            const float n = (float)max(tok, 1);
+            p.part_loss[(size_t)s * G + g] = p.scale / n * (l / n);
             __threadfence();
             s_last = atomicAdd(p.ticket, 1u) == (unsigned)G * p.S - 1u;
         }
     }
     __syncthreads();
-    if (s_last && strand == 0) {
+    if (s_last && warp == 0) {
         __threadfence();
-        double l = 0.0;
+        float l = 0.0f;
         const int parts = G * p.S;
         for (int i = lane; i < parts; i += 32) l += __ldcg(p.part_loss + i);
 #pragma unroll
         for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-        if (lane == 0) *p.loss = (float)l;
+        if (lane == 0) *p.loss = l;
     }
 }
 
@@ -458,17 +487,18 @@ __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(const BalArgs 
 template <class L>
 __global__ void __launch_bounds__(kBalThreads) balance_grad_kernel(const BalArgs p) {
     constexpr int J = L::J, U = L::U, G = L::G;
+    __shared__ int s_seg[kSegs];
+    const Segs seg(p, s_seg);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % L::LPT, k = lane / L::LPT;
     const int each = p.per_block / kBalWarps;
     const int ta = ((int)blockIdx.x * kBalWarps + warp) * each, tb = min(ta + each, p.T);
     const typename L::T *logits = static_cast<const typename L::T *>(p.logits);
     typename L::T *out = static_cast<typename L::T *>(p.dlogits);
-    const double g = (p.grad ? (double)__ldg(p.grad) : 1.0) * p.coef * p.E / ((double)p.K * p.S);
-    for (int s = ta < tb ? seq_of(p, ta) : p.S; s < p.S && seq_at(p, s) < tb; s++) {
-        const int a = max(seq_at(p, s), ta), b = min(seq_at(p, s + 1), tb);
+    const float g = (p.grad ? __ldg(p.grad) : 1.0f) * p.scale;
+    for (int s = ta < tb ? seg.of(ta) : p.S; s < p.S && seg.at(s) < tb; s++) {
+        const int a = max(seg.at(s), ta), b = min(seg.at(s + 1), tb);
         if (a >= b) continue;
-        const int n = max(__ldg(p.tokens + s), 1);
-        const float up = (float)(g / ((double)n * n));
+        const float n = (float)max(__ldg(p.tokens + s), 1), up = g / n / n;
         float c[J];
 #pragma unroll
         for (int j = 0; j < J; j++) c[j] = L::expert(l, j) < p.E ? (float)__ldg(p.counts + (size_t)s * p.E + L::expert(l, j)) : 0.0f;
@@ -568,7 +598,7 @@ cudaError_t launch_lists(const int *idx, int T, int K, int E, int align, long lo
 
 size_t balance_workspace(int T, int E, int S) {
     const size_t slots = balance_slots(T, S);
-    return up16(slots * E * 8) + up16(slots * 4) + up16((size_t)S * ((E + 31) / 32) * 8) + 16;
+    return up16(slots * E * 8) + up16(slots * 4) + up16((size_t)S * ((E + kSumE - 1) / kSumE) * 4) + 16;
 }
 
 cudaError_t launch_balance_forward(const void *logits, int dtype, long long ld, int T, int E, const int *idx, int K, int softmax,
@@ -584,7 +614,7 @@ cudaError_t launch_balance_forward(const void *logits, int dtype, long long ld, 
     p.counts = counts;
     p.tokens = tokens;
     p.sums = sums;
-    p.coef = coef;
+    p.scale = (float)((double)coef * E / ((double)K * S));
     p.T = T;
     p.E = E;
     p.K = K;
@@ -597,8 +627,8 @@ cudaError_t launch_balance_forward(const void *logits, int dtype, long long ld, 
     w += up16(slots * E * 8);
     p.part_tokens = reinterpret_cast<int *>(w);
     w += up16(slots * 4);
-    p.part_loss = reinterpret_cast<double *>(w);
-    w += up16((size_t)S * ((E + 31) / 32) * 8);
+    p.part_loss = reinterpret_cast<float *>(w);
+    w += up16((size_t)S * ((E + kSumE - 1) / kSumE) * 4);
     p.ticket = reinterpret_cast<unsigned *>(w);
     auto go = [&](auto lay) {
         using L = decltype(lay);
@@ -608,7 +638,7 @@ cudaError_t launch_balance_forward(const void *logits, int dtype, long long ld, 
     };
     const cudaError_t e = quads(logits, ld, dtype, E) ? by_layout<true>(dtype, E, go) : by_layout<false>(dtype, E, go);
     if (e != cudaSuccess) return e;
-    balance_sum_kernel<<<dim3((E + 31) / 32, S), kSumThreads, 0, st>>>(p);
+    balance_sum_kernel<<<dim3((E + kSumE - 1) / kSumE, S), kSumThreads, 0, st>>>(p);
     return cudaGetLastError();
 }
 
@@ -625,7 +655,7 @@ cudaError_t launch_balance_backward(const void *logits, int dtype, long long ld,
     p.counts = const_cast<int *>(counts);
     p.tokens = const_cast<int *>(tokens);
     p.dlogits = dlogits;
-    p.coef = coef;
+    p.scale = (float)((double)coef * E / ((double)K * S));
     p.T = T;
     p.E = E;
     p.K = K;
