@@ -386,160 +386,47 @@ class MoeLayer:
 
 # --- operators around the router and its experts ----------------------------------------------
 #
-# Thin calls of the handle-less C entry points (include/moe.h has each one's formula, limits and
-# layouts).  Tensors are checked for type, shape, layout and device here, since the C side sees
-# pointers only; what is not given as an argument is allocated by PyTorch on the call's stream.
+# Calls of the handle-less C entry points (include/moe.h has each one's formula, limits and layouts)
+# through the compiled binding _moe_torch.so: it checks the tensors' types, shapes, layouts and
+# devices (MoeError with MOE_ERR_INVALID), and allocates what is not given as an argument on the
+# call's stream.  The tensors must be on the current device.
 
-class _Call:
-    """One call's checks: the device and stream of its first tensor, and what each tensor must be.
-
-    The checks run on every call, so they are one chain of cheap comparisons (bad()) and the
-    message is made only after one failed (refuse())."""
-    __slots__ = ("where", "torch", "device", "stream", "own_stream")
-
-    def __init__(self, where, first, stream):
-        torch = _torch()
-        self.where, self.torch = where, torch
-        if not isinstance(first, torch.Tensor) or not first.is_cuda:
-            self.fail("the tensors must be on a CUDA device")
-        self.device = dev = first.get_device()
-        if dev != torch.cuda.current_device():
-            self.fail(f"the tensors are on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
-        self.stream = now = _raw_stream(dev)
-        self.own_stream = True                      # the stream that PyTorch allocates on
-        if stream is not None:
-            self.stream = _stream_handle(stream) or 0
-            self.own_stream = self.stream == now
-
-    def fail(self, msg):
-        raise MoeError(MOE_ERR_INVALID, self.where, msg)
-
-    def need(self, t, name, dtypes, shape, rows=False):
-        """t is on the device, of one of dtypes and of `shape`, contiguous or (rows) each row so."""
-        try:
-            if t.dtype in dtypes and t.shape == shape and t.get_device() == self.device and (
-                    t.is_contiguous() or (rows and t.stride(-1) == 1 and t.stride(0) >= shape[-1])):
-                return t.data_ptr()
-        except AttributeError:
-            pass
-        if not isinstance(t, self.torch.Tensor):
-            self.fail(f"{name}: need a tensor")
-        if t.get_device() != self.device:
-            self.fail(f"{name}: is on {t.device}, the call on cuda:{self.device}")
-        if t.dtype not in dtypes:
-            self.fail(f"{name}: need {' or '.join(map(str, dtypes))}, got {t.dtype}")
-        if t.shape != shape:
-            self.fail(f"{name}: need shape {tuple(shape)}, got {tuple(t.shape)}")
-        self.fail(f"{name}: need {'contiguous rows' if rows else 'a contiguous tensor'}, got strides {t.stride()}")
-
-    def dims(self, t, name, n):
-        if not isinstance(t, self.torch.Tensor) or t.dim() != n:
-            self.fail(f"{name}: need a tensor of {n} dimensions")
-        return t.shape
-
-    def code(self, t, name):
-        c = _dtypes().get(t.dtype)
-        if c is None:
-            self.fail(f"{name}: need float32, float16 or bfloat16, got {t.dtype}")
-        return c
-
-    def integer(self, v, name, lo=0):
-        if not isinstance(v, (int, np.integer)) or isinstance(v, bool) or not lo <= v < 1 << 31:
-            self.fail(f"{name}={v!r}: need an integer from {lo}")
-        return int(v)
-
-    def empty(self, *shapes):
-        """One new tensor for each (shape, dtype), allocated for the call's stream."""
-        torch = self.torch
-        if self.own_stream:
-            return [torch.empty(s, dtype=d, device="cuda") for s, d in shapes]
-        dev = torch.device("cuda", self.device)
-        on = torch.cuda.ExternalStream(self.stream, device=dev) if self.stream else torch.cuda.default_stream(dev)
-        with torch.cuda.stream(on):
-            return [torch.empty(s, dtype=d, device=dev) for s, d in shapes]
+_native_mod = None
 
 
-_cache = {}
+def _native():
+    global _native_mod
+    if _native_mod is None:
+        path = _PKG / "_moe_torch.so"
+        if not path.exists():
+            raise RuntimeError(f"{path} is missing: build it with `python -c 'import __graft_entry__ as g; g.build()'`")
+        import importlib.machinery
+        import importlib.util
+        import torch  # noqa: F401  (its libraries come first)
+        spec = importlib.util.spec_from_file_location("_moe_torch", path, loader=importlib.machinery.ExtensionFileLoader("_moe_torch", str(path)))
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        m.set_error(MoeError)
+        _native_mod = m
+    return _native_mod
 
 
-def _torch():
-    t = _cache.get("torch")
-    if t is None:
-        import torch
-        f8 = torch.float8_e4m3fn
-        _cache.update(torch=torch, dtypes={torch.float32: MOE_DTYPE_F32, torch.float16: MOE_DTYPE_F16, torch.bfloat16: MOE_DTYPE_BF16},
-                      f8=(f8, torch.uint8), i32=(torch.int32,), f32=(torch.float32,), mask=(torch.bool, torch.uint8))
-        t = torch
-    return t
-
-
-def _dtypes():
-    return _cache["dtypes"]
-
-
-def _raw_stream(dev: int) -> int:
-    torch = _cache["torch"]
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)     # what current_stream() wraps
-    return raw(dev) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
-
-
-def _row_stride(t) -> int:
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
-
-
-def _blocks(n: int) -> int:
-    return -(-n // 128)
+def _handle(stream):
+    return None if stream is None else _stream_handle(stream) or 0
 
 
 def moe_expert_lists(topk_idx, n_experts: int, align: int = 1, stream=None):
     """Token lists of topk_idx [T, K] int32 (values outside [0, n_experts): dropped pairs).
     -> counts [E], offsets [E + 1], rows [room] (token of each row, -1 in padding), pos [T, K]
     (row of each pair, -1 for dropped ones), all int32."""
-    c = _Call("moe_expert_lists", topk_idx, stream)
-    i32 = _cache["i32"][0]
-    T, K = shape = c.dims(topk_idx, "topk_idx", 2)
-    idx = c.need(topk_idx, "topk_idx", _cache["i32"], shape)
-    E, align = c.integer(n_experts, "n_experts", 1), c.integer(align, "align", 1)
-    L = lib()
-    room = L.moe_expert_lists_rows(T, K, E, align)
-    if not 0 <= room < 1 << 31:
-        raise MoeError(MOE_ERR_UNSUPPORTED, c.where, f"{room} rows: need fewer than 2^31, and at least one choice a token")
-    counts, offsets, rows, pos = c.empty(((E,), i32), ((E + 1,), i32), ((room,), i32), (shape, i32))
-    need = L.moe_expert_lists_workspace(T, K, E)
-    ws = c.empty(((need,), c.torch.uint8))[0] if need else None
-    _check(L.moe_expert_lists(idx, T, K, E, align, counts.data_ptr(), offsets.data_ptr(), rows.data_ptr(), pos.data_ptr(),
-                              ws.data_ptr() if need else None, need, c.stream), c.where)
-    return counts, offsets, rows, pos
-
-
-def _balance_args(c, logits, seq_offsets, mask):
-    T, E = shape = c.dims(logits, "logits", 2)
-    dt = c.code(logits, "logits")
-    x = c.need(logits, "logits", _cache["dtypes"], shape, rows=True)
-    S, seq = 1, None
-    if seq_offsets is not None:
-        n = c.dims(seq_offsets, "seq_offsets", 1)
-        seq, S = c.need(seq_offsets, "seq_offsets", _cache["i32"], n), n[0] - 1
-        if S < 1:
-            c.fail("seq_offsets: need at least two entries")
-    return x, dt, T, E, seq, S, None if mask is None else c.need(mask, "mask", _cache["mask"], (T,))
+    return _native().expert_lists(topk_idx, n_experts, align, _handle(stream))
 
 
 def moe_balance_forward(logits, topk_idx, coef: float, score_func: int = MOE_SCORE_SIGMOID, seq_offsets=None, mask=None, stream=None):
     """Balance loss of a router: logits [T, E] float32 / float16 / bfloat16 (rows may be strided),
     topk_idx [T, K] int32, seq_offsets [S + 1] int32 (None: one sequence), mask [T] bool (False:
     left out).  -> loss [1], counts [S, E] int32, prob_sums [S, E], tokens [S] int32."""
-    c = _Call("moe_balance_forward", logits, stream)
-    x, dt, T, E, seq, S, m = _balance_args(c, logits, seq_offsets, mask)
-    K = c.dims(topk_idx, "topk_idx", 2)[1]
-    idx = c.need(topk_idx, "topk_idx", _cache["i32"], (T, K))
-    L = lib()
-    need = L.moe_balance_workspace(T, E, S)
-    i32, f32 = _cache["i32"][0], _cache["f32"][0]
-    loss, counts, sums, tokens, ws = c.empty(((1,), f32), ((S, E), i32), ((S, E), f32), ((S,), i32), ((need,), c.torch.uint8))
-    _check(L.moe_balance_forward(x, dt, _row_stride(logits), T, E, idx, K, score_func, coef, seq, S, m, loss.data_ptr(),
-                                 counts.data_ptr(), sums.data_ptr(), tokens.data_ptr(), ws.data_ptr(), need, c.stream), c.where)
-    return loss, counts, sums, tokens
+    return _native().balance_forward(logits, topk_idx, coef, score_func, seq_offsets, mask, _handle(stream))
 
 
 def moe_balance_backward(logits, top_k: int, counts, tokens, coef: float, score_func: int = MOE_SCORE_SIGMOID, seq_offsets=None,
@@ -547,19 +434,8 @@ def moe_balance_backward(logits, top_k: int, counts, tokens, coef: float, score_
     """Gradient of moe_balance_forward's loss with respect to logits, with its counts and tokens;
     grad_loss float32, one value (None: 1).  Rows outside every sequence of `out` (None: a new
     tensor) stay as they are.  -> dlogits [T, E] in logits' dtype."""
-    c = _Call("moe_balance_backward", logits, stream)
-    x, dt, T, E, seq, S, m = _balance_args(c, logits, seq_offsets, mask)
-    n = c.need(counts, "counts", _cache["i32"], (S, E))
-    tok = c.need(tokens, "tokens", _cache["i32"], (S,))
-    g = None
-    if grad_loss is not None:
-        g = c.need(grad_loss, "grad_loss", _cache["f32"], () if isinstance(grad_loss, c.torch.Tensor) and grad_loss.dim() == 0 else (1,))
-    if out is None:
-        out, = c.empty(((T, E), logits.dtype))
-    d = c.need(out, "out", (logits.dtype,), (T, E), rows=True)
-    _check(lib().moe_balance_backward(x, dt, _row_stride(logits), T, E, c.integer(top_k, "top_k", 1), score_func, coef, n, tok, seq,
-                                      S, m, g, d, _row_stride(out), c.stream), c.where)
-    return out
+    return _native().balance_backward(logits, top_k, counts, tokens, coef, score_func, seq_offsets, mask, grad_loss, out,
+                                      _handle(stream))
 
 
 def moe_fp8_quantize(x, rows=None, transposed: bool = False, stream=None):
@@ -567,43 +443,14 @@ def moe_fp8_quantize(x, rows=None, transposed: bool = False, stream=None):
     rows [R] int32 (negative: zeros), with a power-of-two scale per 1 x 128 block.
     -> codes [R, width] float8_e4m3fn, scales [ceil(width / 128), R]; with transposed also
     codes_t [width, Rp], scales_t [Rp / 128, width], Rp = R rounded up to a multiple of 128."""
-    c = _Call("moe_fp8_quantize", x, stream)
-    T, n = shape = c.dims(x, "x", 2)
-    dt = c.code(x, "x")
-    px, R, pr = c.need(x, "x", _cache["dtypes"], shape, rows=True), T, None
-    if rows is not None:
-        R = c.dims(rows, "rows", 1)[0]
-        pr = c.need(rows, "rows", _cache["i32"], (R,))
-    f8, f32 = _cache["f8"][0], _cache["f32"][0]
-    pt = ps = None
-    if transposed:
-        rb = _blocks(R)
-        out = c.empty(((R, n), f8), ((_blocks(n), R), f32), ((n, rb * 128), f8), ((rb, n), f32))
-        if R:
-            pt, ps = out[2].data_ptr(), out[3].data_ptr()
-    else:
-        out = c.empty(((R, n), f8), ((_blocks(n), R), f32))
-    _check(lib().moe_fp8_quantize(px, dt, _row_stride(x), T, n, pr, R, out[0].data_ptr(), out[1].data_ptr(), pt, ps, c.stream), c.where)
-    return tuple(out)
+    return _native().fp8_quantize(x, rows, transposed, _handle(stream))
 
 
 def moe_fp8_quantize_weights(w, transposed: bool = False, stream=None):
     """e4m3 codes of weights w [E, N, K] or [N, K], one scale per 128 x 128 block.
     -> codes, scales [(E,) ceil(N / 128), ceil(K / 128)]; with transposed also the transposed
     matrices' codes and scales."""
-    c = _Call("moe_fp8_quantize_weights", w, stream)
-    shape = c.dims(w, "w", 2 if w.dim() == 2 else 3)
-    dt = c.code(w, "w")
-    pw = c.need(w, "w", _cache["dtypes"], shape)
-    lead, (N, K) = tuple(shape[:-2]), shape[-2:]
-    f8, f32 = _cache["f8"][0], _cache["f32"][0]
-    specs = [(lead + (N, K), f8), (lead + (_blocks(N), _blocks(K)), f32)]
-    if transposed:
-        specs += [(lead + (K, N), f8), (lead + (_blocks(K), _blocks(N)), f32)]
-    out = c.empty(*specs)
-    p = [t.data_ptr() for t in out] + [None, None]
-    _check(lib().moe_fp8_quantize_weights(pw, dt, lead[0] if lead else 1, N, K, p[0], p[1], p[2], p[3], c.stream), c.where)
-    return tuple(out)
+    return _native().fp8_quantize_weights(w, transposed, _handle(stream))
 
 
 def moe_fp8_matmul(x, x_scale, w, w_scale, offsets=None, out=None, out_dtype=None, stream=None):
@@ -611,29 +458,7 @@ def moe_fp8_matmul(x, x_scale, w, w_scale, offsets=None, out=None, out_dtype=Non
     x_scale [ceil(K / 128), R], w_scale [ceil(N / 128), ceil(K / 128)].  With offsets [E + 1] int32,
     w [E, N, K] and w_scale [E, ...]: row r is multiplied with the expert whose segment holds it;
     rows outside every segment of `out` stay as they are.  out_dtype: bfloat16 by default."""
-    c = _Call("moe_fp8_matmul", x, stream)
-    f8, f32 = _cache["f8"], _cache["f32"]
-    R, K = c.dims(x, "x", 2)
-    kb, off = _blocks(K), None
-    if offsets is None:
-        E, N = 1, c.dims(w, "w", 2)[0]
-        pw = c.need(w, "w", f8, (N, K))
-        ps = c.need(w_scale, "w_scale", f32, (_blocks(N), kb))
-    else:
-        E, N, _ = c.dims(w, "w", 3)
-        pw = c.need(w, "w", f8, (E, N, K))
-        ps = c.need(w_scale, "w_scale", f32, (E, _blocks(N), kb))
-        off = c.need(offsets, "offsets", _cache["i32"], (E + 1,))
-    px = c.need(x, "x", f8, (R, K))
-    pxs = c.need(x_scale, "x_scale", f32, (kb, R))
-    if out is None:
-        out, = c.empty(((R, N), out_dtype or c.torch.bfloat16))
-    elif out_dtype is not None and out.dtype != out_dtype:
-        c.fail(f"out is {out.dtype}, out_dtype {out_dtype}")
-    dt = c.code(out, "out")
-    py = c.need(out, "out", _cache["dtypes"], (R, N), rows=True)
-    _check(lib().moe_fp8_matmul(px, pxs, R, pw, ps, E, N, K, off, py, dt, _row_stride(out), c.stream), c.where)
-    return out
+    return _native().fp8_matmul(x, x_scale, w, w_scale, offsets, out, out_dtype, _handle(stream))
 
 
 def moe_fp8_wgrad(xt, xt_scale, dyt, dyt_scale, offsets=None, out=None, out_dtype=None, stream=None):
@@ -641,26 +466,7 @@ def moe_fp8_wgrad(xt, xt_scale, dyt, dyt_scale, offsets=None, out=None, out_dtyp
     xt [K, R], dyt [N, R] codes, R a multiple of 128, xt_scale [R / 128, K], dyt_scale [R / 128, N];
     offsets [E + 1] int32, multiples of 128 (None: one matrix).
     -> dw [E, N, K] ([N, K] without offsets), float32 by default."""
-    c = _Call("moe_fp8_wgrad", xt, stream)
-    f8, f32 = _cache["f8"], _cache["f32"]
-    K, R = c.dims(xt, "xt", 2)
-    N = c.dims(dyt, "dyt", 2)[0]
-    px, pd = c.need(xt, "xt", f8, (K, R)), c.need(dyt, "dyt", f8, (N, R))
-    pxs, pds = c.need(xt_scale, "xt_scale", f32, (R // 128, K)), c.need(dyt_scale, "dyt_scale", f32, (R // 128, N))
-    E, shape, off = 1, (N, K), None
-    if offsets is not None:
-        E = c.dims(offsets, "offsets", 1)[0] - 1
-        if E < 1:
-            c.fail("offsets: need at least two entries")
-        off, shape = c.need(offsets, "offsets", _cache["i32"], (E + 1,)), (E, N, K)
-    if out is None:
-        out, = c.empty((shape, out_dtype or c.torch.float32))
-    elif out_dtype is not None and out.dtype != out_dtype:
-        c.fail(f"out is {out.dtype}, out_dtype {out_dtype}")
-    dt = c.code(out, "out")
-    po = c.need(out, "out", _cache["dtypes"], shape)
-    _check(lib().moe_fp8_wgrad(px, pxs, pd, pds, R, N, K, E, off, po, dt, c.stream), c.where)
-    return out
+    return _native().fp8_wgrad(xt, xt_scale, dyt, dyt_scale, offsets, out, out_dtype, _handle(stream))
 
 
 def moe_fp8_device_error(check: bool = True) -> int:

@@ -1,5 +1,6 @@
 """Builds libmoe_gb300.so in-tree with nvcc for sm_103a (no torch extension
-machinery: the library is plain C ABI + CUDA)."""
+machinery: the library is plain C ABI + CUDA), and beside it _moe_torch.so, the
+compiled PyTorch binding of the handle-less operators (host code only)."""
 from __future__ import annotations
 
 import os
@@ -12,6 +13,7 @@ ROOT = PKG.parent
 CSRC = PKG / "csrc"
 BUILD = PKG / "_build"
 LIB = PKG / "libmoe_gb300.so"
+BINDING = PKG / "_moe_torch.so"
 SOURCES = ["moe_kernels.cu", "moe_decode.cu", "moe_fp8.cu", "moe_route_ops.cu", "moe_abi.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -30,6 +32,26 @@ def _stale(target: Path, deps) -> bool:
     return any(Path(d).stat().st_mtime > t for d in deps)
 
 
+def _binding_command(obj: Path) -> list[str]:
+    """Compiles the binding's object: g++ on PyTorch's and Python's headers."""
+    import sysconfig
+    import torch
+    inc = Path(torch.__file__).resolve().parent / "include"
+    cuda = Path(nvcc()).resolve().parent.parent / "include"
+    dirs = [ROOT / "include", sysconfig.get_paths()["include"], inc, inc / "torch/csrc/api/include", cuda]
+    return ["g++", "-std=c++17", "-O2", "-fPIC", "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *[a for d in dirs for a in ("-isystem", str(d))], "-c", str(CSRC / "moe_torch.cpp"), "-o", str(obj)]
+
+
+def _link_binding(obj: Path) -> None:
+    import torch
+    libs = Path(torch.__file__).resolve().parent / "lib"
+    tmp = BINDING.with_suffix(".so.tmp%d" % os.getpid())
+    subprocess.run(["g++", "-shared", "-o", str(tmp), str(obj), f"-L{libs}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+                    f"-L{PKG}", f"-l:{LIB.name}", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{libs}"], check=True)
+    os.replace(tmp, BINDING)
+
+
 def build_library(force: bool = False, verbose: bool = False) -> Path:
     headers = list(CSRC.glob("*.h")) + list((ROOT / "include").glob("*.h"))
     BUILD.mkdir(exist_ok=True)
@@ -46,6 +68,10 @@ def build_library(force: bool = False, verbose: bool = False) -> Path:
             procs.append((subprocess.Popen([nvcc(), *flags, "-c", str(CSRC / src), "-o", str(tmp)],
                                            stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True),
                           tmp, obj))
+    binding = BUILD / "moe_torch.o"
+    if force or _stale(binding, [CSRC / "moe_torch.cpp", ROOT / "include" / "moe.h"]):
+        tmp = binding.with_suffix(".o.tmp%d" % os.getpid())
+        procs.append((subprocess.Popen(_binding_command(tmp), stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True), tmp, binding))
     errors = []
     for proc, tmp, obj in procs:
         out, _ = proc.communicate()
@@ -56,11 +82,13 @@ def build_library(force: bool = False, verbose: bool = False) -> Path:
             if verbose and out:
                 print(out)
     if errors:
-        raise RuntimeError("nvcc failed:\n" + "\n".join(errors))
+        raise RuntimeError("compilation failed:\n" + "\n".join(errors))
     if force or _stale(LIB, objs):
         tmp = LIB.with_suffix(".so.tmp%d" % os.getpid())
         subprocess.run([nvcc(), *ARCH, "-shared", "-o", str(tmp), *map(str, objs)], check=True)
         os.replace(tmp, LIB)
+    if force or _stale(BINDING, [binding, LIB]):
+        _link_binding(binding)
     return LIB
 
 

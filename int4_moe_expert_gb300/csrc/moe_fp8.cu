@@ -1579,7 +1579,7 @@ cudaError_t launch_gemm(const GemmArgs &p, const CUtensorMap &am, const uint8_t 
                         long long tiles, int per_sm, int cluster, cudaStream_t st) {
     CUtensorMap bm;
     if (!tmap(&bm, 2, b, b_cols, b_rows, 1, C::BT)) return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(fp8_gemm_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+    const cudaError_t e = allow_smem<fp8_gemm_kernel<C>>(C::SMEM);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     const long long most = (long long)sm_count() * per_sm;
@@ -1604,7 +1604,7 @@ cudaError_t launch_wide(const WideArgs &p, const uint8_t *a, uint64_t a_cols, co
                         long long tiles, cudaStream_t st) {
     CUtensorMap am, bm;
     if (!tmap(&am, 3, a, a_cols, p.na, 1, 128) || !tmap(&bm, 3, b, b_cols, p.nb, b_mats, C::BROWS)) return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(fp8_wide_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+    const cudaError_t e = allow_smem<fp8_wide_kernel<C>>(C::SMEM);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     const long long nb = C::PAIR ? 2 : 1, most = sm_count() / nb;

@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "moe.h"
 
 namespace moe {
@@ -132,6 +134,20 @@ cudaError_t launch_decode_fast(const Params &p, const float *x, float *y, cudaSt
 // Returns the first launch error (cudaSuccess when all launches were issued).
 cudaError_t launch_forward(const Params &p, const float *x, int T, float *y, cudaStream_t stream,
                            bool want_buckets, cudaEvent_t *ev);
+
+// Raises a kernel's dynamic shared-memory limit once per device (the calls that need it are short).
+template <auto Kernel>
+cudaError_t allow_smem(size_t bytes) {
+    static std::atomic<bool> done[64] = {};
+    int dev = -1;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) done[dev].store(true, std::memory_order_release);
+    return e;
+}
 
 // Token lists and the balance loss (moe_route_ops.cu).
 size_t lists_workspace(long long pairs, int E);

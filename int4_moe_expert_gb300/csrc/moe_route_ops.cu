@@ -589,10 +589,10 @@ cudaError_t launch_lists(const int *idx, int T, int K, int E, int align, long lo
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    const size_t smem = ((size_t)kListWarps * E + 3 * (size_t)E + 1) * sizeof(int);
-    const cudaError_t e = cudaFuncSetAttribute(lists_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    auto smem = [](size_t e) { return (kListWarps * e + 3 * e + 1) * sizeof(int); };
+    const cudaError_t e = allow_smem<lists_kernel>(smem(1024));
     if (e != cudaSuccess) return e;
-    lists_kernel<<<p.blocks, kListThreads, smem, st>>>(p);
+    lists_kernel<<<p.blocks, kListThreads, smem((size_t)E), st>>>(p);
     return cudaGetLastError();
 }
 
