@@ -81,6 +81,7 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *map, int x
     asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
                  ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
 }
+__device__ __forceinline__ void prefetch_map(const void *map) { asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory"); }
 // K-major operand with the 128-byte swizzle: groups of 8 rows 1024 bytes apart
 __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
     return (uint64_t)((saddr >> 4) & 0x3FFF) | (1ull << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
@@ -311,6 +312,8 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) fp8_gemm_kernel(const _
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
 
     if (tid == 0) {
+        prefetch_map(&amap);
+        prefetch_map(&bmap);
         s_fail = 0;
         s_issued = 0;
         for (int i = 0; i < C::S; i++) {
@@ -333,6 +336,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) fp8_gemm_kernel(const _
                      ::"r"(smem_u32(&s_taddr)), "n"(C::TCOLS) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    wait_for_stream();
     if (p.offsets) {
         // column tiles of every expert; the running sum by one warp
         for (int e = tid; e < p.E; e += C::THREADS) {
@@ -805,6 +809,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
     constexpr int NB = C::PAIR ? 2 : 1;      // blocks of a tile
 
     if (tid == 0) {
+        prefetch_map(&amap);
+        prefetch_map(&bmap);
         s_fail = 0;
         s_issued = 0;
         for (int i = 0; i < C::S; i++) {
@@ -831,6 +837,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
             asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
         }
     }
+    wait_for_stream();
     if (!C::MX && p.offsets) {
         for (int e = tid; e < p.E; e += C::THREADS) {
             const int a = min(max(p.offsets[e], 0), p.na), b = min(max(p.offsets[e + 1], a), p.na);
@@ -1229,6 +1236,7 @@ template <typename T, int RW, int KG>
 __global__ void __launch_bounds__(kQThreads) quantize_rows_kernel(const QuantArgs p) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r0 = (int)blockIdx.x * (kQThreads / 32 * RW) + warp, kb0 = (int)blockIdx.y * KG;
+    wait_for_stream();
     const T *x = static_cast<const T *>(p.x);
     float4 v[RW][KG];
 #pragma unroll
@@ -1342,6 +1350,7 @@ __global__ void __launch_bounds__(kQThreads, sizeof(T) == 4 ? 2 : 4) quantize_ti
     const int nrb = (p.R + kKB - 1) / kKB, nkb = (p.width + kKB - 1) / kKB;
     const bool in = c < p.width;
 
+    wait_for_stream();
     const int src = src_row(p.rows, rw + l16, p.R, p.n_src);
     Oct<T> v[8];
     if (__all_sync(0xffffffffu, src >= 0 && in)) {
@@ -1495,36 +1504,31 @@ cudaError_t launch_quantize(const void *x, int dtype, long long ld, int n_src, i
     const int nkb = (width + kKB - 1) / kKB;
     if (codes_t) {
         const dim3 grid(nkb, (R + kKB - 1) / kKB);
-        if (dtype == MOE_DTYPE_F32) quantize_tile_kernel<float, false><<<grid, kQThreads, 0, st>>>(p);
-        else if (dtype == MOE_DTYPE_BF16) quantize_tile_kernel<__nv_bfloat16, false><<<grid, kQThreads, 0, st>>>(p);
-        else quantize_tile_kernel<__half, false><<<grid, kQThreads, 0, st>>>(p);
-        return cudaGetLastError();
+        if (dtype == MOE_DTYPE_F32) return launch_early(quantize_tile_kernel<float, false>, grid, kQThreads, 0, st, 1, p);
+        if (dtype == MOE_DTYPE_BF16) return launch_early(quantize_tile_kernel<__nv_bfloat16, false>, grid, kQThreads, 0, st, 1, p);
+        return launch_early(quantize_tile_kernel<__half, false>, grid, kQThreads, 0, st, 1, p);
     }
     // few rows: one block a warp, so that the blocks cover the card; many: four rows of four blocks
     const bool few = (long long)R * nkb < 16ll * 8 * 4 * sm_count();
     const int rw = few ? 1 : 4, kg = few ? 1 : 4;
     const dim3 grid((R + 8 * rw - 1) / (8 * rw), (nkb + kg - 1) / kg);
-    if (dtype == MOE_DTYPE_F32) {
-        if (few) quantize_rows_kernel<float, 1, 1><<<grid, kQThreads, 0, st>>>(p);
-        else quantize_rows_kernel<float, 4, 4><<<grid, kQThreads, 0, st>>>(p);
-    } else if (dtype == MOE_DTYPE_BF16) {
-        if (few) quantize_rows_kernel<__nv_bfloat16, 1, 1><<<grid, kQThreads, 0, st>>>(p);
-        else quantize_rows_kernel<__nv_bfloat16, 4, 4><<<grid, kQThreads, 0, st>>>(p);
-    } else {
-        if (few) quantize_rows_kernel<__half, 1, 1><<<grid, kQThreads, 0, st>>>(p);
-        else quantize_rows_kernel<__half, 4, 4><<<grid, kQThreads, 0, st>>>(p);
-    }
-    return cudaGetLastError();
+    auto go = [&](auto t) {
+        using T = decltype(t);
+        if (few) return launch_early(quantize_rows_kernel<T, 1, 1>, grid, kQThreads, 0, st, 1, p);
+        return launch_early(quantize_rows_kernel<T, 4, 4>, grid, kQThreads, 0, st, 1, p);
+    };
+    if (dtype == MOE_DTYPE_F32) return go(float{});
+    if (dtype == MOE_DTYPE_BF16) return go(__nv_bfloat16{});
+    return go(__half{});
 }
 
 cudaError_t launch_quantize_weights(const void *w, int dtype, int E, int N, int K, uint8_t *codes, float *scales,
                                     uint8_t *codes_t, float *scales_t, cudaStream_t st) {
     const QuantArgs p = {w, K, nullptr, codes, scales, codes_t, scales_t, N, N, K};
     const dim3 grid((K + kKB - 1) / kKB, (N + kKB - 1) / kKB, E);
-    if (dtype == MOE_DTYPE_F32) quantize_tile_kernel<float, true><<<grid, kQThreads, 0, st>>>(p);
-    else if (dtype == MOE_DTYPE_BF16) quantize_tile_kernel<__nv_bfloat16, true><<<grid, kQThreads, 0, st>>>(p);
-    else quantize_tile_kernel<__half, true><<<grid, kQThreads, 0, st>>>(p);
-    return cudaGetLastError();
+    if (dtype == MOE_DTYPE_F32) return launch_early(quantize_tile_kernel<float, true>, grid, kQThreads, 0, st, 1, p);
+    if (dtype == MOE_DTYPE_BF16) return launch_early(quantize_tile_kernel<__nv_bfloat16, true>, grid, kQThreads, 0, st, 1, p);
+    return launch_early(quantize_tile_kernel<__half, true>, grid, kQThreads, 0, st, 1, p);
 }
 
 // ---------------------------------------------------------------------------
@@ -1581,22 +1585,9 @@ cudaError_t launch_gemm(const GemmArgs &p, const CUtensorMap &am, const uint8_t 
     if (!tmap(&bm, 2, b, b_cols, b_rows, 1, C::BT)) return cudaErrorInvalidValue;
     const cudaError_t e = allow_smem<fp8_gemm_kernel<C>>(C::SMEM);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
     const long long most = (long long)sm_count() * per_sm;
-    cfg.gridDim = dim3((unsigned)(C::SPLIT ? tiles * cluster : (tiles < most ? tiles : most)));
-    cfg.blockDim = dim3(C::THREADS);
-    cfg.dynamicSmemBytes = C::SMEM;
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    if (C::SPLIT) {
-        at[0].id = cudaLaunchAttributeClusterDimension;
-        at[0].val.clusterDim.x = (unsigned)cluster;
-        at[0].val.clusterDim.y = 1;
-        at[0].val.clusterDim.z = 1;
-        cfg.attrs = at;
-        cfg.numAttrs = 1;
-    }
-    return cudaLaunchKernelEx(&cfg, fp8_gemm_kernel<C>, am, bm, p);
+    const dim3 grid((unsigned)(C::SPLIT ? tiles * cluster : (tiles < most ? tiles : most)));
+    return launch_early(fp8_gemm_kernel<C>, grid, C::THREADS, C::SMEM, st, C::SPLIT ? (unsigned)cluster : 1u, am, bm, p);
 }
 
 template <class C>
@@ -1606,20 +1597,8 @@ cudaError_t launch_wide(const WideArgs &p, const uint8_t *a, uint64_t a_cols, co
     if (!tmap(&am, 3, a, a_cols, p.na, 1, 128) || !tmap(&bm, 3, b, b_cols, p.nb, b_mats, C::BROWS)) return cudaErrorInvalidValue;
     const cudaError_t e = allow_smem<fp8_wide_kernel<C>>(C::SMEM);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
     const long long nb = C::PAIR ? 2 : 1, most = sm_count() / nb;
-    cfg.gridDim = dim3((unsigned)(nb * (tiles < most ? tiles : most)));
-    cfg.blockDim = dim3(C::THREADS);
-    cfg.dynamicSmemBytes = C::SMEM;
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)nb;
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = C::PAIR ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, fp8_wide_kernel<C>, am, bm, p);
+    return launch_early(fp8_wide_kernel<C>, dim3((unsigned)(nb * (tiles < most ? tiles : most))), C::THREADS, C::SMEM, st, (unsigned)nb, am, bm, p);
 }
 
 bool rows_aligned(const void *out, long long ldo, int dtype) {

@@ -149,6 +149,31 @@ cudaError_t allow_smem(size_t bytes) {
     return e;
 }
 
+// Launch that may begin while the kernel before it on the stream ends (programmatic dependent
+// launch): the kernel's first step is wait_for_stream() below, before it touches memory, so only its
+// launch and its set-up overlap.
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st, unsigned cluster, A &&...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = cluster;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+#ifdef __CUDACC__
+__device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+#endif
+
 // Token lists and the balance loss (moe_route_ops.cu).
 size_t lists_workspace(long long pairs, int E);
 cudaError_t launch_lists(const int *idx, int T, int K, int E, int align, long long room, int *counts, int *offsets,

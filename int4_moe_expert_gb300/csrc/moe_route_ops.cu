@@ -25,13 +25,14 @@ constexpr int kListWarps = kListThreads / 32;
 constexpr int kListsOne = 8192;         // pairs that one block sorts alone
 constexpr int kListsMin = 2048;         // pairs per block otherwise, at least
 constexpr int kListsBlocks = 148;       // blocks, at most
+constexpr int kAhead = 4;               // 32-pair loads of a warp in flight
 
 struct ListArgs {
     const int *idx;
     int *counts, *offsets, *rows, *pos;
     int *hist;          // [blocks][E] (more than one block)
     long long pairs, room;
-    int K, E, align, chunk, blocks;
+    int K, E, align, chunk, blocks, small;   // small: pair numbers fit 32 bits
 };
 
 __device__ __forceinline__ int pair_expert(const ListArgs &p, long long i, long long end) {
@@ -43,7 +44,9 @@ __global__ void __launch_bounds__(kListThreads) lists_count_kernel(const ListArg
     extern __shared__ int h[];
     for (int e = threadIdx.x; e < p.E; e += kListThreads) h[e] = 0;
     __syncthreads();
+    wait_for_stream();
     const long long lo = (long long)blockIdx.x * p.chunk, hi = min(lo + p.chunk, p.pairs);
+#pragma unroll 4
     for (long long i = lo + threadIdx.x; i < hi; i += kListThreads) {
         const int e = pair_expert(p, i, hi);
         if (e >= 0) atomicAdd(&h[e], 1);
@@ -52,103 +55,145 @@ __global__ void __launch_bounds__(kListThreads) lists_count_kernel(const ListArg
     for (int e = threadIdx.x; e < p.E; e += kListThreads) p.hist[(size_t)blockIdx.x * p.E + e] = h[e];
 }
 
-__global__ void __launch_bounds__(kListThreads) lists_kernel(const ListArgs p) {
+__global__ void __launch_bounds__(kListThreads, 1) lists_kernel(const ListArgs p) {
     extern __shared__ int sm[];
     int *h = sm;                              // [warps][E] pairs of each warp, then each warp's next place
     int *off = sm + kListWarps * p.E;         // [E + 1]
     int *before = off + p.E + 1;              // [E] this expert's pairs in earlier blocks
     int *total = before + p.E;                // [E]
-    __shared__ int s_run;
+    __shared__ int s_warp[kListWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const bool one = p.blocks == 1;
-    for (int i = tid; i < kListWarps * p.E; i += kListThreads) h[i] = 0;
+    const int part = max(((p.chunk + kListWarps - 1) / kListWarps + 31) & ~31, 32);   // pairs of a warp
+    const int nw = min((p.chunk + part - 1) / part, kListWarps);                      // warps with pairs
+    for (int i = tid; i < nw * p.E; i += kListThreads) h[i] = 0;
     for (int e = tid; e < p.E; e += kListThreads) before[e] = total[e] = 0;
     __syncthreads();
+    wait_for_stream();
     const long long lo = (long long)blockIdx.x * p.chunk, hi = min(lo + p.chunk, p.pairs);
-    const int part = ((p.chunk + kListWarps - 1) / kListWarps + 31) & ~31;   // pairs of a warp
     const long long wlo = lo + (long long)warp * part, whi = min(wlo + part, hi);
     int *hw = h + warp * p.E;
-    for (long long i = wlo; i < whi; i += 32) {
-        const int e = pair_expert(p, i + lane, whi);
-        const unsigned same = __match_any_sync(0xffffffffu, e);
-        if (e >= 0 && lane == __ffs(same) - 1) hw[e] += __popc(same);
-        __syncwarp();
+    // kAhead x 32 pairs' experts at once: the loads are what the warp waits for
+    int ex[kAhead];
+    auto load = [&](long long i) {
+#pragma unroll
+        for (int k = 0; k < kAhead; k++) ex[k] = pair_expert(p, i + 32 * k + lane, whi);
+    };
+    for (long long i = wlo; i < whi; i += 32 * kAhead) {
+        load(i);
+#pragma unroll
+        for (int k = 0; k < kAhead; k++) {
+            const int e = ex[k];
+            const unsigned same = __match_any_sync(0xffffffffu, e);
+            if (e >= 0 && lane == __ffs(same) - 1) hw[e] += __popc(same);
+            __syncwarp();
+        }
     }
-    if (!one) {
-        // counts of the other blocks: thread = (expert, part of the blocks)
+    if (!one && p.E % 4 == 0) {
+        // counts of the other blocks: thread = (four experts, part of the blocks)
+        const int quads = p.E / 4, groups = kListThreads / quads;
+        const int q = tid % quads, g = tid / quads;
+        if (g < groups) {
+            int4 b4 = make_int4(0, 0, 0, 0), all = b4;
+#pragma unroll 8
+            for (int b = g; b < p.blocks; b += groups) {
+                const int4 v = __ldg(reinterpret_cast<const int4 *>(p.hist + (size_t)b * p.E) + q);
+                all = make_int4(all.x + v.x, all.y + v.y, all.z + v.z, all.w + v.w);
+                if (b < (int)blockIdx.x) b4 = make_int4(b4.x + v.x, b4.y + v.y, b4.z + v.z, b4.w + v.w);
+            }
+            const int bv[4] = {b4.x, b4.y, b4.z, b4.w}, av[4] = {all.x, all.y, all.z, all.w};
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                if (bv[k]) atomicAdd(&before[4 * q + k], bv[k]);
+                if (av[k]) atomicAdd(&total[4 * q + k], av[k]);
+            }
+        }
+    } else if (!one) {
         const int groups = p.E >= kListThreads ? 1 : kListThreads / p.E;
         for (int i = tid; i < groups * p.E; i += kListThreads) {
             const int e = i % p.E, g = i / p.E;
             int b4 = 0, all = 0;
-#pragma unroll 4
+#pragma unroll 16
             for (int b = g; b < p.blocks; b += groups) {
-                const int v = p.hist[(size_t)b * p.E + e];
+                const int v = __ldg(p.hist + (size_t)b * p.E + e);
                 all += v;
-                if (b < (int)blockIdx.x) b4 += v;
+                b4 += b < (int)blockIdx.x ? v : 0;
             }
             if (b4) atomicAdd(&before[e], b4);
             if (all) atomicAdd(&total[e], all);
         }
     }
     __syncthreads();
-    if (one) {
-        for (int e = tid; e < p.E; e += kListThreads) {
-            int n = 0;
-            for (int w = 0; w < kListWarps; w++) n += h[w * p.E + e];
-            total[e] = n;
-        }
-        __syncthreads();
-    }
-    // offsets: running sum of the padded counts, 32 experts at a time
-    if (warp == 0) {
-        int run = 0;
-        for (int e0 = 0; e0 < p.E; e0 += 32) {
-            const int n = e0 + lane < p.E ? total[e0 + lane] : 0;
-            int v = (n + p.align - 1) / p.align * p.align;
-            const int own = v;
+    // thread = expert (E <= threads): the warps' counts become each warp's first place within this
+    // block's pairs of the expert; then the running sum of the padded counts over the experts
+    int mine = 0, place = 0, n = 0, padded = 0;
+    if (tid < p.E) {
+        int at = before[tid];
+        for (int w0 = 0; w0 < nw; w0 += 8) {
+            int c[8];
 #pragma unroll
-            for (int d = 1; d < 32; d *= 2) {
-                const int u = __shfl_up_sync(0xffffffffu, v, d);
-                if (lane >= d) v += u;
+            for (int w = 0; w < 8; w++) c[w] = w0 + w < nw ? h[(w0 + w) * p.E + tid] : 0;
+#pragma unroll
+            for (int w = 0; w < 8; w++) {
+                if (w0 + w < nw) h[(w0 + w) * p.E + tid] = at;
+                at += c[w];
             }
-            if (e0 + lane < p.E) off[e0 + lane] = run + v - own;
-            run += __shfl_sync(0xffffffffu, v, 31);
         }
-        if (lane == 0) {
-            off[p.E] = run;
-            s_run = run;
+        n = one ? at : total[tid];
+        if (one) total[tid] = n;
+        padded = (n + p.align - 1) / p.align * p.align;
+        mine = padded;
+    }
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const int u = __shfl_up_sync(0xffffffffu, mine, d);
+        if (lane >= d) mine += u;
+    }
+    if (lane == 31) s_warp[warp] = mine;
+    __syncthreads();
+    if (warp == 0) {
+        int v = s_warp[lane];
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int u = __shfl_up_sync(0xffffffffu, v, d);
+            if (lane >= d) v += u;
         }
+        s_warp[lane] = v;
     }
     __syncthreads();
-    for (int e = tid; e < p.E; e += kListThreads) {
-        int at = off[e] + before[e];
-        for (int w = 0; w < kListWarps; w++) {
-            const int n = h[w * p.E + e];
-            h[w * p.E + e] = at;
-            at += n;
-        }
+    place = mine - padded + (warp ? s_warp[warp - 1] : 0);
+    if (tid < p.E) {
+        off[tid] = place;
+        if (tid == p.E - 1) off[p.E] = place + padded;
         if (blockIdx.x == 0) {
-            p.counts[e] = total[e];
-            p.offsets[e] = off[e];
+            p.counts[tid] = n;
+            p.offsets[tid] = place;
+            if (tid == p.E - 1) p.offsets[p.E] = place + padded;
         }
     }
-    if (blockIdx.x == 0 && tid == 0) p.offsets[p.E] = s_run;
     __syncthreads();
-    for (long long i = wlo; i < whi; i += 32) {
-        const int e = pair_expert(p, i + lane, whi);
-        const unsigned same = __match_any_sync(0xffffffffu, e);
-        const int leader = __ffs(same) - 1;
-        int at = 0;
-        if (e >= 0 && lane == leader) {
-            at = hw[e];
-            hw[e] = at + __popc(same);
+    const bool kept = whi - wlo <= 32 * kAhead;      // the experts are still in registers
+    for (long long i = wlo; i < whi; i += 32 * kAhead) {
+        if (!kept) load(i);
+#pragma unroll
+        for (int k = 0; k < kAhead; k++) {
+            const int e = ex[k];
+            const long long j = i + 32 * k + lane;
+            const unsigned same = __match_any_sync(0xffffffffu, e);
+            const int leader = __ffs(same) - 1;
+            int at = 0;
+            if (e >= 0 && lane == leader) {
+                at = hw[e];
+                hw[e] = at + __popc(same);
+            }
+            at = __shfl_sync(0xffffffffu, at, leader) + __popc(same & ((1u << lane) - 1u));
+            if (j < whi) {
+                if (e >= 0) at += off[e];
+                p.pos[j] = e >= 0 ? at : -1;
+                if (e >= 0) p.rows[at] = p.small ? (int)((unsigned)j / (unsigned)p.K) : (int)(j / p.K);
+            }
+            __syncwarp();
         }
-        at = __shfl_sync(0xffffffffu, at, leader) + __popc(same & ((1u << lane) - 1u));
-        if (i + lane < whi) {
-            p.pos[i + lane] = e >= 0 ? at : -1;
-            if (e >= 0) p.rows[at] = (int)((i + lane) / p.K);
-        }
-        __syncwarp();
     }
     // rows without a token: behind each expert's pairs (its block's warps) and behind the last segment
     for (int e = (int)blockIdx.x * kListWarps + warp; e < p.E; e += p.blocks * kListWarps)
@@ -249,16 +294,17 @@ struct Lay {
     static constexpr bool VEC = VEC_;
     static constexpr int U = J <= 8 ? 2 : 1;      // tokens in flight for every group of lanes
     __device__ __forceinline__ static int expert(int l, int j) { return VEC ? 4 * (l + LPT * (j / 4)) + j % 4 : l + LPT * j; }
+    // a token's logits; -infinity (a score of 0) outside E and, without `on`, everywhere
     __device__ __forceinline__ static void load(const T *row, int E, int l, bool on, float (&x)[J]) {
         if constexpr (VEC) {
 #pragma unroll
             for (int j = 0; j < J; j += 4) {
                 if (on && expert(l, j) < E) ld4(row + expert(l, j), &x[j]);
-                else x[j] = x[j + 1] = x[j + 2] = x[j + 3] = 0.0f;
+                else x[j] = x[j + 1] = x[j + 2] = x[j + 3] = -INFINITY;
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < J; j++) x[j] = on && expert(l, j) < E ? ld1(row + expert(l, j)) : 0.0f;
+            for (int j = 0; j < J; j++) x[j] = on && expert(l, j) < E ? ld1(row + expert(l, j)) : -INFINITY;
         }
     }
     __device__ __forceinline__ static void store(T *row, int E, int l, const float (&x)[J]) {
@@ -307,21 +353,20 @@ struct Segs {
         return lo;
     }
 };
-// a token's normalised scores (0 outside E); c1: 1 - sigma (sigmoid only)
+// a token's normalised scores (0 where the logit is -infinity); c1: 1 - sigma (sigmoid only)
 template <class L>
-__device__ __forceinline__ void scores(const float (&x)[L::J], int E, int l, int softmax, float (&pr)[L::J], float (&c1)[L::J]) {
+__device__ __forceinline__ void scores(const float (&x)[L::J], int softmax, float (&pr)[L::J], float (&c1)[L::J]) {
     constexpr int J = L::J;
     float z = 0.0f;
     if (softmax) {
         float m = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < J; j++)
-            if (L::expert(l, j) < E) m = fmaxf(m, x[j]);
+        for (int j = 0; j < J; j++) m = fmaxf(m, x[j]);
         m = L::most(m);
         if (m == -INFINITY) m = 0.0f;      // no expert left: every probability 0 (below)
 #pragma unroll
         for (int j = 0; j < J; j++) {
-            pr[j] = L::expert(l, j) < E ? expf(x[j] - m) : 0.0f;
+            pr[j] = expf(x[j] - m);
             z += pr[j];
         }
         z = L::add(z);
@@ -330,7 +375,7 @@ __device__ __forceinline__ void scores(const float (&x)[L::J], int E, int l, int
 #pragma unroll
         for (int j = 0; j < J; j++) {
             const float t = expf(-fabsf(x[j])), r = __fdividef(1.0f, 1.0f + t);
-            pr[j] = L::expert(l, j) < E ? (x[j] >= 0.0f ? r : t * r) : 0.0f;   // a NaN stays one
+            pr[j] = x[j] >= 0.0f ? r : t * r;      // a NaN stays one
             c1[j] = x[j] >= 0.0f ? t * r : r;
             z += pr[j];
         }
@@ -348,6 +393,7 @@ __global__ void __launch_bounds__(kBalThreads) balance_part_kernel(const BalArgs
     float *ws = bsm;                                                 // [warps * G][E]
     int *cnt = reinterpret_cast<int *>(bsm + kBalWarps * G * p.E);   // [E]
     __shared__ int s_n, s_seg[kSegs];
+    wait_for_stream();
     const Segs seg(p, s_seg);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, l = lane % L::LPT, g = lane / L::LPT;
     if (blockIdx.x == 0 && tid == 0) *p.ticket = 0;
@@ -375,9 +421,9 @@ __global__ void __launch_bounds__(kBalThreads) balance_part_kernel(const BalArgs
 #pragma unroll
             for (int u = 0; u < U; u++) {
                 float pr[J], c1[J];
-                scores<L>(x[u], p.E, l, p.softmax, pr, c1);
+                scores<L>(x[u], p.softmax, pr, c1);
 #pragma unroll
-                for (int j = 0; j < J; j++) sum[j] += on[u] ? pr[j] : 0.0f;
+                for (int j = 0; j < J; j++) sum[j] += pr[j];
                 n += on[u] ? 1 : 0;
             }
         }
@@ -412,6 +458,7 @@ __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(const BalArgs 
     __shared__ float s_sum[32][kSumE];
     __shared__ int s_cnt[32][kSumE], s_tok[32];
     __shared__ bool s_last;
+    wait_for_stream();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int s = (int)blockIdx.y, g = (int)blockIdx.x, G = (int)gridDim.x, e = kSumE * g + tid % kSumE;
     const int a = p.seq ? min(max(__ldg(p.seq + s), 0), p.T) : 0, b = p.seq ? min(max(__ldg(p.seq + s + 1), 0), p.T) : p.T;
@@ -488,6 +535,7 @@ template <class L>
 __global__ void __launch_bounds__(kBalThreads) balance_grad_kernel(const BalArgs p) {
     constexpr int J = L::J, U = L::U, G = L::G;
     __shared__ int s_seg[kSegs];
+    wait_for_stream();
     const Segs seg(p, s_seg);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % L::LPT, k = lane / L::LPT;
     const int each = p.per_block / kBalWarps;
@@ -515,7 +563,7 @@ __global__ void __launch_bounds__(kBalThreads) balance_grad_kernel(const BalArgs
             for (int u = 0; u < U; u++) {
                 const int tt = t + u * G + k;
                 float pr[J], c1[J], dot = 0.0f;
-                scores<L>(x[u], p.E, l, p.softmax, pr, c1);
+                scores<L>(x[u], p.softmax, pr, c1);
 #pragma unroll
                 for (int j = 0; j < J; j++) dot = fmaf(pr[j], c[j], dot);
                 dot = L::add(dot);
@@ -523,7 +571,7 @@ __global__ void __launch_bounds__(kBalThreads) balance_grad_kernel(const BalArgs
                 for (int j = 0; j < J; j++) {
                     float d = up * pr[j] * (c[j] - dot);
                     if (!p.softmax) d *= c1[j];
-                    x[u][j] = on[u] ? d : 0.0f;
+                    x[u][j] = d;
                 }
                 if (tt < b) L::store(out + (long long)tt * p.ldd, p.E, l, x[u]);
             }
@@ -581,19 +629,17 @@ size_t lists_workspace(long long pairs, int E) {
 
 cudaError_t launch_lists(const int *idx, int T, int K, int E, int align, long long room, int *counts, int *offsets, int *rows,
                          int *pos, void *ws, cudaStream_t st) {
-    ListArgs p = {idx, counts, offsets, rows, pos, static_cast<int *>(ws), (long long)T * K, room, K, E, align, 0, 1};
+    ListArgs p = {idx, counts, offsets, rows, pos, static_cast<int *>(ws), (long long)T * K, room, K, E, align, 0, 1, (long long)T * K < (1ll << 31)};
     p.blocks = lists_blocks(p.pairs);
     p.chunk = (int)((p.pairs + p.blocks - 1) / p.blocks);
     if (p.blocks > 1) {
-        lists_count_kernel<<<p.blocks, kListThreads, E * sizeof(int), st>>>(p);
-        const cudaError_t e = cudaGetLastError();
+        const cudaError_t e = launch_early(lists_count_kernel, p.blocks, kListThreads, E * sizeof(int), st, 1, p);
         if (e != cudaSuccess) return e;
     }
     auto smem = [](size_t e) { return (kListWarps * e + 3 * e + 1) * sizeof(int); };
     const cudaError_t e = allow_smem<lists_kernel>(smem(1024));
     if (e != cudaSuccess) return e;
-    lists_kernel<<<p.blocks, kListThreads, smem((size_t)E), st>>>(p);
-    return cudaGetLastError();
+    return launch_early(lists_kernel, p.blocks, kListThreads, smem((size_t)E), st, 1, p);
 }
 
 size_t balance_workspace(int T, int E, int S) {
@@ -633,13 +679,11 @@ cudaError_t launch_balance_forward(const void *logits, int dtype, long long ld, 
     auto go = [&](auto lay) {
         using L = decltype(lay);
         const int blocks = T > 0 ? (T + p.per_block - 1) / p.per_block : 1;
-        balance_part_kernel<L><<<blocks, kBalThreads, ((size_t)kBalWarps * L::G + 1) * E * sizeof(float), st>>>(p);
-        return cudaGetLastError();
+        return launch_early(balance_part_kernel<L>, blocks, kBalThreads, ((size_t)kBalWarps * L::G + 1) * E * sizeof(float), st, 1, p);
     };
     const cudaError_t e = quads(logits, ld, dtype, E) ? by_layout<true>(dtype, E, go) : by_layout<false>(dtype, E, go);
     if (e != cudaSuccess) return e;
-    balance_sum_kernel<<<dim3((E + kSumE - 1) / kSumE, S), kSumThreads, 0, st>>>(p);
-    return cudaGetLastError();
+    return launch_early(balance_sum_kernel, dim3((E + kSumE - 1) / kSumE, S), kSumThreads, 0, st, 1, p);
 }
 
 cudaError_t launch_balance_backward(const void *logits, int dtype, long long ld, int T, int E, int K, int softmax, float coef,
@@ -663,8 +707,7 @@ cudaError_t launch_balance_backward(const void *logits, int dtype, long long ld,
     p.softmax = softmax;
     p.per_block = tokens_per_block(T);
     auto go = [&](auto lay) {
-        balance_grad_kernel<decltype(lay)><<<(T + p.per_block - 1) / p.per_block, kBalThreads, 0, st>>>(p);
-        return cudaGetLastError();
+        return launch_early(balance_grad_kernel<decltype(lay)>, (T + p.per_block - 1) / p.per_block, kBalThreads, 0, st, 1, p);
     };
     return quads(logits, ld, dtype, E) && quads(dlogits, ldd, dtype, E) ? by_layout<true>(dtype, E, go) : by_layout<false>(dtype, E, go);
 }
