@@ -1231,36 +1231,20 @@ struct QuantArgs {
     int n_src, R, width;
 };
 
-// Rows only: a warp per 1 x 128 block (four elements a lane), KG blocks of RW rows each.
-template <typename T, int RW, int KG>
+// Few rows: a warp per 1 x 128 block (four elements a lane), so that the blocks cover the card.
+// Bound by latency.
+template <typename T>
 __global__ void __launch_bounds__(kQThreads) quantize_rows_kernel(const QuantArgs p) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int r0 = (int)blockIdx.x * (kQThreads / 32 * RW) + warp, kb0 = (int)blockIdx.y * KG;
+    const int r = (int)blockIdx.x * (kQThreads / 32) + warp, kb = (int)blockIdx.y, c = kb * kKB + 4 * lane;
     wait_for_stream();
-    const T *x = static_cast<const T *>(p.x);
-    float4 v[RW][KG];
-#pragma unroll
-    for (int i = 0; i < RW; i++) {
-        const int r = r0 + i * (kQThreads / 32), s = src_row(p.rows, r, p.R, p.n_src);
-#pragma unroll
-        for (int g = 0; g < KG; g++) {
-            const int c = (kb0 + g) * kKB + 4 * lane;
-            v[i][g] = s >= 0 && c < p.width ? load4(x + (long long)s * p.ld + c) : make_float4(0, 0, 0, 0);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < RW; i++) {
-        const int r = r0 + i * (kQThreads / 32);
-#pragma unroll
-        for (int g = 0; g < KG; g++) {
-            const int kb = kb0 + g, c = kb * kKB + 4 * lane;
-            float inv;
-            const float s = block_scale(__reduce_max_sync(0xffffffffu, max_bits(v[i][g])), inv);
-            if (r < p.R && c < p.width) {
-                *reinterpret_cast<uint32_t *>(p.codes + (size_t)r * p.width + c) = codes4(v[i][g], inv);
-                if (lane == 0) p.scales[(size_t)kb * p.R + r] = s;
-            }
-        }
+    const int s = src_row(p.rows, r, p.R, p.n_src);
+    const float4 v = s >= 0 && c < p.width ? load4(static_cast<const T *>(p.x) + (long long)s * p.ld + c) : make_float4(0, 0, 0, 0);
+    float inv;
+    const float scale = block_scale(__reduce_max_sync(0xffffffffu, max_bits(v)), inv);
+    if (r < p.R && c < p.width) {
+        *reinterpret_cast<uint32_t *>(p.codes + (size_t)r * p.width + c) = codes4(v, inv);
+        if (lane == 0) p.scales[(size_t)kb * p.R + r] = scale;
     }
 }
 
@@ -1326,17 +1310,20 @@ __device__ __forceinline__ uint32_t codes4(uint64_t ab, uint64_t cd) {
     return __byte_perm(codes2(a, b), codes2(c, d), 0x5410);
 }
 
-// Rows and columns of a 128 x 128 tile, or (WT) one scale for the whole tile of a weight matrix.
+// The 1 x 128 blocks of a 128 x 128 tile, along the rows (kRows) or both ways (kBoth), or one scale for
+// the whole tile of a weight matrix (kWeights).
 // x is read once and stays in registers: a warp holds 16 rows, a half-warp one row at a time, a lane
 // eight neighbouring columns of eight neighbouring rows, so that a lane's codes of a column are eight
 // neighbouring bytes of the transposed output; only codes and the columns' maxima pass through shared
 // memory.  Bound by instruction issue, then by memory: the row maxima meet in one transposing
 // butterfly (a lane ends with one row), a row's scale is computed once.
-template <typename T, bool WT>
+enum QuantMode { kRows, kBoth, kWeights };
+template <typename T, QuantMode MODE>
 __global__ void __launch_bounds__(kQThreads, sizeof(T) == 4 ? 2 : 4) quantize_tile_kernel(const QuantArgs p) {
+    constexpr bool WT = MODE == kWeights, COLS = MODE != kRows;
     constexpr int NW = kQThreads / 32, W = Oct<T>::W;
-    __shared__ __align__(16) uint8_t s_codes[kKB * kKB];
-    __shared__ __align__(16) uint32_t s_col[NW][16 * W];         // column maxima of every warp's rows
+    __shared__ __align__(16) uint8_t s_codes[COLS ? kKB * kKB : 16];
+    __shared__ __align__(16) uint32_t s_col[COLS ? NW : 1][16 * W];         // column maxima of every warp's rows
     __shared__ __align__(16) float s_inv[kKB];                   // 1 / scale of every column
     __shared__ unsigned s_max[NW];
     static_assert(NW == 8, "16 rows a warp");
@@ -1401,28 +1388,30 @@ __global__ void __launch_bounds__(kQThreads, sizeof(T) == 4 ? 2 : 4) quantize_ti
         const float s = block_scale(mine, rinv);
         const int r = rw + (lane >> 1);
         if (!(lane & 1) && r < p.R) p.scales[(size_t)kb * p.R + r] = s;
+        if constexpr (COLS) {
 #pragma unroll
-        for (int k = 0; k < W; k++) cm[k] = word_max<T>(cm[k], __shfl_xor_sync(0xffffffffu, cm[k], 16));
-        if (half == 0) {
+            for (int k = 0; k < W; k++) cm[k] = word_max<T>(cm[k], __shfl_xor_sync(0xffffffffu, cm[k], 16));
+            if (half == 0) {
 #pragma unroll
-            for (int k = 0; k < W; k += 4) *reinterpret_cast<uint4 *>(&s_col[warp][l16 * W + k]) = make_uint4(cm[k], cm[k + 1], cm[k + 2], cm[k + 3]);
+                for (int k = 0; k < W; k += 4) *reinterpret_cast<uint4 *>(&s_col[warp][l16 * W + k]) = make_uint4(cm[k], cm[k + 1], cm[k + 2], cm[k + 3]);
+            }
+            __syncthreads();
+            if (tid < kKB) {
+                // column tid: its 16-bit half of the word that two columns share, or its own word
+                constexpr bool wide = sizeof(T) == 4;
+                uint32_t m = 0;
+#pragma unroll
+                for (int w = 0; w < NW; w++) m = word_max<T>(m, s_col[w][wide ? tid : tid >> 1]);
+                float ci;
+                const float t = block_scale(Oct<T>::bits(wide ? m : (tid & 1) ? m & 0xFFFF0000u : m & 0xFFFFu), ci);
+                s_inv[tid] = ci;
+                if (kb * kKB + tid < p.width) p.scales_t[(size_t)blockIdx.y * p.width + kb * kKB + tid] = t;
+            }
+            __syncthreads();
         }
-        __syncthreads();
-        if (tid < kKB) {
-            // column tid: its 16-bit half of the word that two columns share, or its own word
-            constexpr bool wide = sizeof(T) == 4;
-            uint32_t m = 0;
-#pragma unroll
-            for (int w = 0; w < NW; w++) m = word_max<T>(m, s_col[w][wide ? tid : tid >> 1]);
-            float ci;
-            const float t = block_scale(Oct<T>::bits(wide ? m : (tid & 1) ? m & 0xFFFF0000u : m & 0xFFFFu), ci);
-            s_inv[tid] = ci;
-            if (kb * kKB + tid < p.width) p.scales_t[(size_t)blockIdx.y * p.width + kb * kKB + tid] = t;
-        }
-        __syncthreads();
     }
-    uint64_t cs[4];
-    if (!WT) {
+    uint64_t cs[4] = {};
+    if (MODE == kBoth) {
 #pragma unroll
         for (int k = 0; k < 4; k += 2) {
             const float4 f = *reinterpret_cast<const float4 *>(&s_inv[8 * l16 + 2 * k]);
@@ -1447,26 +1436,29 @@ __global__ void __launch_bounds__(kQThreads, sizeof(T) == 4 ? 2 : 4) quantize_ti
             for (int k = 0; k < 4; k++) {
                 const uint64_t u = v[i + h].pair(k);
                 a[k] = mul2(u, rr);
-                f[h][k] = WT ? a[k] : mul2(u, cs[k]);
+                f[h][k] = MODE == kBoth ? mul2(u, cs[k]) : a[k];
             }
             if (in && ra + i + h < p.R)
                 *reinterpret_cast<uint2 *>(o + (size_t)((i + h) * p.width)) = make_uint2(codes4(a[0], a[1]), codes4(a[2], a[3]));
         }
+        if constexpr (COLS) {
 #pragma unroll
-        for (int k = 0; k < 4; k++) {
-            float a0, a1, b0, b1;
-            unpack2(f[0][k], a0, b0);
-            unpack2(f[1][k], a1, b1);
-            const uint32_t x0 = codes2(a0, a1), x1 = codes2(b0, b1);
-            if (i % 4 == 0) {
-                q[2 * k][i / 4] = x0;
-                q[2 * k + 1][i / 4] = x1;
-            } else {
-                q[2 * k][i / 4] = __byte_perm(q[2 * k][i / 4], x0, 0x5410);
-                q[2 * k + 1][i / 4] = __byte_perm(q[2 * k + 1][i / 4], x1, 0x5410);
+            for (int k = 0; k < 4; k++) {
+                float a0, a1, b0, b1;
+                unpack2(f[0][k], a0, b0);
+                unpack2(f[1][k], a1, b1);
+                const uint32_t x0 = codes2(a0, a1), x1 = codes2(b0, b1);
+                if (i % 4 == 0) {
+                    q[2 * k][i / 4] = x0;
+                    q[2 * k + 1][i / 4] = x1;
+                } else {
+                    q[2 * k][i / 4] = __byte_perm(q[2 * k][i / 4], x0, 0x5410);
+                    q[2 * k + 1][i / 4] = __byte_perm(q[2 * k + 1][i / 4], x1, 0x5410);
+                }
             }
         }
     }
+    if constexpr (!COLS) return;
     if (WT && !p.codes_t) return;
     // 16-byte chunk `warp` of column 8 l16 + k, at chunk position warp ^ (l16 & 7) of that column's 128 bytes
 #pragma unroll
@@ -1504,18 +1496,18 @@ cudaError_t launch_quantize(const void *x, int dtype, long long ld, int n_src, i
     const int nkb = (width + kKB - 1) / kKB;
     if (codes_t) {
         const dim3 grid(nkb, (R + kKB - 1) / kKB);
-        if (dtype == MOE_DTYPE_F32) return launch_early(quantize_tile_kernel<float, false>, grid, kQThreads, 0, st, 1, p);
-        if (dtype == MOE_DTYPE_BF16) return launch_early(quantize_tile_kernel<__nv_bfloat16, false>, grid, kQThreads, 0, st, 1, p);
-        return launch_early(quantize_tile_kernel<__half, false>, grid, kQThreads, 0, st, 1, p);
+        if (dtype == MOE_DTYPE_F32) return launch_early(quantize_tile_kernel<float, kBoth>, grid, kQThreads, 0, st, 1, p);
+        if (dtype == MOE_DTYPE_BF16) return launch_early(quantize_tile_kernel<__nv_bfloat16, kBoth>, grid, kQThreads, 0, st, 1, p);
+        return launch_early(quantize_tile_kernel<__half, kBoth>, grid, kQThreads, 0, st, 1, p);
     }
-    // few rows: one block a warp, so that the blocks cover the card; many: four rows of four blocks
-    const bool few = (long long)R * nkb < 16ll * 8 * 4 * sm_count();
-    const int rw = few ? 1 : 4, kg = few ? 1 : 4;
-    const dim3 grid((R + 8 * rw - 1) / (8 * rw), (nkb + kg - 1) / kg);
+    // tiles where they cover two thirds of the card, else a block a warp (bf16, width 2048: 1024 rows 2.7 us
+    // in tiles, 3.2 us by warps; 512 rows 2.7 and 2.5 us; 65536 rows 59 us, 0.99 of the copy rate, and 122 us)
+    const dim3 tiles(nkb, (R + kKB - 1) / kKB), grid((R + 7) / 8, nkb);
+    const bool few = (long long)tiles.x * tiles.y * 3 < 2 * sm_count();
     auto go = [&](auto t) {
         using T = decltype(t);
-        if (few) return launch_early(quantize_rows_kernel<T, 1, 1>, grid, kQThreads, 0, st, 1, p);
-        return launch_early(quantize_rows_kernel<T, 4, 4>, grid, kQThreads, 0, st, 1, p);
+        if (few) return launch_early(quantize_rows_kernel<T>, grid, kQThreads, 0, st, 1, p);
+        return launch_early(quantize_tile_kernel<T, kRows>, tiles, kQThreads, 0, st, 1, p);
     };
     if (dtype == MOE_DTYPE_F32) return go(float{});
     if (dtype == MOE_DTYPE_BF16) return go(__nv_bfloat16{});
@@ -1526,9 +1518,9 @@ cudaError_t launch_quantize_weights(const void *w, int dtype, int E, int N, int 
                                     uint8_t *codes_t, float *scales_t, cudaStream_t st) {
     const QuantArgs p = {w, K, nullptr, codes, scales, codes_t, scales_t, N, N, K};
     const dim3 grid((K + kKB - 1) / kKB, (N + kKB - 1) / kKB, E);
-    if (dtype == MOE_DTYPE_F32) return launch_early(quantize_tile_kernel<float, true>, grid, kQThreads, 0, st, 1, p);
-    if (dtype == MOE_DTYPE_BF16) return launch_early(quantize_tile_kernel<__nv_bfloat16, true>, grid, kQThreads, 0, st, 1, p);
-    return launch_early(quantize_tile_kernel<__half, true>, grid, kQThreads, 0, st, 1, p);
+    if (dtype == MOE_DTYPE_F32) return launch_early(quantize_tile_kernel<float, kWeights>, grid, kQThreads, 0, st, 1, p);
+    if (dtype == MOE_DTYPE_BF16) return launch_early(quantize_tile_kernel<__nv_bfloat16, kWeights>, grid, kQThreads, 0, st, 1, p);
+    return launch_early(quantize_tile_kernel<__half, kWeights>, grid, kQThreads, 0, st, 1, p);
 }
 
 // ---------------------------------------------------------------------------

@@ -145,7 +145,7 @@ def test_quantize(gpu, T, width, dtype):
 
 @pytest.mark.gpu
 def test_quantize_many_rows(gpu):
-    """The variant for many rows (four rows of four blocks a warp) gives the same codes as the tile's."""
+    """The variant for many rows gives the same codes as the one for few and the one for both ways."""
     for width, dtype in ((528, torch.bfloat16), (640, torch.float32), (400, torch.float16)):
         x = hard_values(20011, width, 1, dtype).cuda()
         codes, scales = gpu.moe_fp8_quantize(x)
