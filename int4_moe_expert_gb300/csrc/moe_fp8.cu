@@ -76,6 +76,7 @@ struct Cfg {
 };
 
 constexpr int kMaxExperts = 1024;
+constexpr uint32_t kMaxSplit = 8;        // blocks of a cluster that share a tile
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *map, int x, int y, int z, uint32_t bar) {
     asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
@@ -235,11 +236,20 @@ __device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.release;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
-__device__ __forceinline__ float ld_peer(uint32_t saddr, uint32_t rank) {
+__device__ __forceinline__ uint32_t peer_addr(uint32_t saddr, uint32_t rank) {
     uint32_t a;
-    float v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return a;
+}
+__device__ __forceinline__ float ld_peer(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float4 ld_peer4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
     return v;
 }
 
@@ -537,15 +547,23 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) fp8_gemm_kernel(const _
         atomicOr(p.err, MOE_DEVICE_ERR_TC);
     }
     if (C::SPLIT) {
-        // sums of all blocks of the cluster, in block order: block r adds columns r, r + csize, ...
+        // sums of all blocks of the cluster, in block order: block r adds columns r, r + csize, ...;
+        // every block's value of a column in flight at once (one after the other, eight blocks' partial
+        // sums of 64 columns took 3 us)
         cluster_sync_all();
         if (t0 < total) {
             const Tile ti = walk.at(t0);
+            uint32_t peer[kMaxSplit];
+#pragma unroll
+            for (uint32_t r = 0; r < kMaxSplit; r++) peer[r] = peer_addr(ring, r < csize ? r : 0u);
+            const int l = tid & 127, n = ti.a0 + l;
             for (int c = (int)crank + (int)csize * (tid >> 7); c < C::BT; c += (int)csize * (C::THREADS >> 7)) {
-                const int l = tid & 127, n = ti.a0 + l;
-                float v = 0.0f;
-                for (uint32_t r = 0; r < csize; r++) v += ld_peer(ring + (uint32_t)(c * kARows + l) * 4u, r);
-                if (n < p.na && ti.b0 + c < ti.bend) store_out(p.out, (long long)(ti.b0 + c) * p.ldo + n, v, p.out_dtype);
+                float v[kMaxSplit], sum = 0.0f;
+#pragma unroll
+                for (uint32_t r = 0; r < kMaxSplit; r++) v[r] = r < csize ? ld_peer(peer[r] + (uint32_t)(c * kARows + l) * 4u) : 0.0f;
+#pragma unroll
+                for (uint32_t r = 0; r < kMaxSplit; r++) sum += v[r];
+                if (n < p.na && ti.b0 + c < ti.bend) store_out(p.out, (long long)(ti.b0 + c) * p.ldo + n, sum, p.out_dtype);
             }
         }
         cluster_sync_all();
@@ -572,24 +590,32 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) fp8_gemm_kernel(const _
 //           registers see each output once.
 // ---------------------------------------------------------------------------
 
-template <bool PAIR_, bool MX_>
+template <bool PAIR_, bool MX_, int BN_ = 256, bool SPLIT_ = false>
 struct WideCfg {
     static constexpr bool PAIR = PAIR_, MX = MX_;
-    static constexpr int BN = 256;
+    static constexpr bool SPLIT = SPLIT_;                     // a cluster shares a tile, each block part of the inner axis
+    static constexpr int BN = BN_;                            // columns of a tile
     static constexpr int ROWS = PAIR ? 256 : 128;             // rows of a tile
-    static constexpr int BROWS = PAIR ? 128 : 256;            // rows of B that one block copies
+    static constexpr int BROWS = PAIR ? BN / 2 : BN;          // rows of B that one block copies
     static constexpr int STAGE = kABytes + BROWS * kKB;
-    static constexpr int S = PAIR ? 5 : 3;
-    static constexpr int EW = 8;
+    static constexpr int S = STAGE > 32768 ? 3 : 5;
+    static constexpr int EW = 8;                              // epilogue warps: a lane quarter, half of the columns each
+    static constexpr int WC = BN / 2;
     static constexpr int THREADS = 32 * (EW + 4);
+    static constexpr bool BIGREG = WC > 64;
     static constexpr int SS = 8;                              // scale ring (matmul)
     static constexpr int SFBYTES = 512 + 1024;                // staged scales of a stage (MX): 128 + 256 words
     static constexpr int SFCOLS = 12;                         // their tensor-memory columns: 4 + 8
     static constexpr int OUTB = 4096;                         // staging of an epilogue warp: 32 rows x 128 bytes
-    static constexpr int ACC1 = MX ? 512 - SFCOLS * S - BN : BN;   // second accumulator (MX: overlaps the first)
+    static constexpr int NT = MX ? 2 : 512 / BN;              // accumulators: of tiles (MX), of stages
+    static constexpr int ACC1 = MX ? 512 - SFCOLS * S - BN : BN;   // from one to the next (MX: the second overlaps the first)
+    static constexpr int PLD = BN + 4;                        // floats of a row of partial sums (SPLIT)
     static constexpr size_t SMEM = 1024 + (size_t)S * STAGE + EW * OUTB + (MX ? S * SFBYTES : 0);
     // f8f6f4: D f32 at bit 4; mxf8f6f4: ue8m0 scales at bit 23
     static constexpr uint32_t IDESC = (MX ? 1u << 23 : 1u << 4) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(ROWS >> 4) << 24);
+    static_assert(!MX || BN == 256, "the scales' layout is written for 256 columns");
+    static_assert(!SPLIT || (!PAIR && !MX && 128 * PLD * 4 <= S * STAGE), "partial sums reuse the stage ring");
+    static_assert(SMEM + 16 * 1024 <= 227 * 1024, "the rings and the static arrays fit one block's shared memory");
 };
 
 // address of this shared variable in the cluster's first block
@@ -794,7 +820,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
                                                                  const WideArgs p) {
     extern __shared__ unsigned char smem_raw[];
     __shared__ __align__(8) unsigned long long s_full[C::S], s_empty[C::S];
-    __shared__ __align__(8) unsigned long long s_tfull[2], s_tempty[2];
+    __shared__ __align__(8) unsigned long long s_tfull[C::NT], s_tempty[C::NT];
     __shared__ __align__(8) unsigned long long s_sfull[C::SS], s_sempty[C::SS];   // MX: s_sfull by stage
     __shared__ __align__(8) unsigned long long s_drain;
     __shared__ float s_scale[C::MX ? 1 : C::SS][128], s_wscale[C::MX ? 1 : C::SS][2];   // matmul: rows', weight blocks'
@@ -817,7 +843,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
             mbar_init(smem_u32(&s_full[i]), 1);
             mbar_init(smem_u32(&s_empty[i]), 1);
         }
-        for (int i = 0; i < 2; i++) {
+        for (int i = 0; i < C::NT; i++) {
             mbar_init(smem_u32(&s_tfull[i]), 1);
             mbar_init(smem_u32(&s_tempty[i]), NB * C::EW);
         }
@@ -852,12 +878,22 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
     const uint32_t taddr = s_taddr;
     volatile int *fail = &s_fail;
     WideWalk<C> walk(p, s_first, rank);
-    const int total = walk.total(), t0 = (int)blockIdx.x / NB, tstep = (int)gridDim.x / NB;
+    const int crank = C::SPLIT ? (int)cluster_rank() : 0, csize = C::SPLIT ? (int)cluster_size() : 1;
+    const int total = walk.total(), t0 = (int)blockIdx.x / (C::SPLIT ? csize : NB), tstep = C::SPLIT ? 1 << 30 : (int)gridDim.x / NB;
+    auto tile_at = [&](int t) {
+        WideTile r = walk.at(t);
+        if (C::SPLIT) {      // this block's part of the inner axis
+            const int n = r.k1 - r.k0, lo = r.k0 + (int)((long long)n * crank / csize);
+            r.k1 = r.k0 + (int)((long long)n * (crank + 1) / csize);
+            r.k0 = lo;
+        }
+        return r;
+    };
 
     if (warp < C::EW) {
         // 384 threads x 168 registers at launch = 256 x 216 + 128 x 72
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-        const int q4 = warp & 3, half = warp >> 2;          // lane quarter, 128-column half
+        if constexpr (C::BIGREG) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        const int q4 = warp & 3, half = warp >> 2;          // lane quarter, half of the columns
         const uint32_t trow = taddr + ((uint32_t)(32 * q4) << 16);
         const uint32_t stage = staging + (uint32_t)(warp * C::OUTB);
         const uint32_t te0 = C::PAIR ? in_leader(smem_u32(&s_tempty[0])) : smem_u32(&s_tempty[0]);
@@ -868,13 +904,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
                 else mbar_arrive(te0 + 8u * q);
             }
         };
-        Ring<2> tq;
+        Ring<C::NT> tq;
         Ring<C::SS> ts;
         int done = 0;
         bool ok = true;
         for (int t = t0; t < total && ok; t += tstep) {
-            const WideTile ti = walk.at(t);
-            const int row = ti.r0 + 32 * q4, rows = ti.rend - row, c0 = ti.c0 + 128 * half, cols = p.nb - c0;
+            const WideTile ti = tile_at(t);
+            const int row = ti.r0 + 32 * q4, rows = ti.rend - row, c0 = ti.c0 + C::WC * half, cols = p.nb - c0;
             const long long at = (C::MX ? (long long)ti.e * p.out_stride : 0ll) + (long long)row * p.ldo + c0;
             if constexpr (C::MX) {
                 const int q = done & 1;
@@ -909,9 +945,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
                 }
                 done++;
             } else {
-                uint64_t acc[64];
+                uint64_t acc[C::WC / 2];
 #pragma unroll
-                for (int i = 0; i < 64; i++) acc[i] = 0ull;
+                for (int i = 0; i < C::WC / 2; i++) acc[i] = 0ull;
                 for (int kb = ti.k0; kb < ti.k1; kb++) {
                     const int q = tq.slot, s = ts.slot;
                     if (!__all_sync(0xffffffffu, ring_wait(smem_u32(&s_sfull[s]), ts.phase, fail) &&
@@ -923,14 +959,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
                     tq.next();
                     ts.next();
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                    const uint32_t f = __float_as_uint(s_scale[s][32 * q4 + lane] * s_wscale[s][half]);
+                    const uint32_t f = __float_as_uint(s_scale[s][32 * q4 + lane] * s_wscale[s][C::WC * half / kKB]);
                     const uint64_t sc = pack2(f, f);
-                    const uint32_t base = trow + (uint32_t)(256 * q + 128 * half);
+                    const uint32_t base = trow + (uint32_t)(C::BN * q + C::WC * half);
 #pragma unroll
-                    for (int l = 0; l < 2; l++) {
+                    for (int l = 0; l < C::WC / 64; l++) {
                         uint32_t r[64];
                         tc_ld<64>(base + (uint32_t)(64 * l), r);
-                        if (l == 1) release(q);
+                        if (l + 1 == C::WC / 64) release(q);
 #pragma unroll
                         for (int i = 0; i < 32; i++) acc[32 * l + i] = fma2(pack2(r[2 * i], r[2 * i + 1]), sc, acc[32 * l + i]);
                     }
@@ -938,14 +974,20 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
                     if (lane == 0) mbar_arrive(smem_u32(&s_sempty[s]));
                 }
                 if (!ok) break;
-                if (rows > 0) {
-                    store_cols(acc, stage, p, at, rows, cols, lane);
-                    store_cols(acc + 32, stage, p, at + 64, rows, cols - 64, lane);
+                if constexpr (C::SPLIT) {
+                    // partial sums [row][column] over the stage ring: every copy into it was consumed
+                    const uint32_t ps = ring + (uint32_t)((32 * q4 + lane) * C::PLD + C::WC * half) * 4u;
+#pragma unroll
+                    for (int i = 0; i < C::WC / 2; i += 2)
+                        asm volatile("st.shared.v2.b64 [%0], {%1, %2};" ::"r"(ps + 8u * i), "l"(acc[i]), "l"(acc[i + 1]) : "memory");
+                } else if (rows > 0) {
+#pragma unroll
+                    for (int l = 0; l < C::WC / 64; l++) store_cols(acc + 32 * l, stage, p, at + 64 * l, rows, cols - 64 * l, lane);
                 }
             }
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if constexpr (C::BIGREG) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == C::EW) {
             // tensor copies: this block's rows of A and its part of B
             Ring<C::S> r;
@@ -953,7 +995,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
             int n = 0;
             const uint32_t full0 = C::PAIR ? in_leader(smem_u32(&s_full[0])) : smem_u32(&s_full[0]);
             for (int t = t0; t < total && ok; t += tstep) {
-                const WideTile ti = walk.at(t);
+                const WideTile ti = tile_at(t);
                 for (int kb = ti.k0; kb < ti.k1; kb++) {
                     // a fresh ring's slots pass: the phase before the first is over
                     if (!__all_sync(0xffffffffu, ring_wait(smem_u32(&s_empty[r.slot]), r.phase ^ 1u, fail))) {
@@ -976,14 +1018,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
             // MMA issue (by the tile's first block)
             if (rank == 0) {
                 Ring<C::S> r;
-                Ring<2> q;      // matmul: accumulator of the stage; MX: of the tile
+                Ring<C::NT> q;  // matmul: accumulator of the stage; MX: of the tile
                 int tile = 0;
                 bool ok = true, any = false;
                 const uint64_t ad0 = sw128_desc(ring), bd0 = sw128_desc(ring + kABytes);
                 // shared-memory operand of the scale copies: 8-row groups of 16 bytes 128 bytes apart, no swizzle
                 const uint64_t sd0 = (uint64_t)((sfring >> 4) & 0x3FFF) | (1ull << 16) | ((uint64_t)(128 >> 4) << 32) | (1ull << 46);
                 for (int t = t0; t < total && ok; t += tstep) {
-                    const WideTile ti = walk.at(t);
+                    const WideTile ti = tile_at(t);
                     const int k1 = ti.k1;
                     // MX: the previous tile's overlapping columns are in registers (its epilogue follows
                     // that of the tile before it, which used this accumulator)
@@ -1014,7 +1056,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
                                 for (int ks = 0; ks < 4; ks++)
                                     wide_mma_mx<C::PAIR>(d, ad0 + off + 2 * ks, bd0 + off + 2 * ks, C::IDESC, tsf, tsf + 4, kb > ti.k0 || ks > 0);
                             } else {
-                                const uint32_t d = taddr + (uint32_t)(256 * q.slot);
+                                const uint32_t d = taddr + (uint32_t)(C::BN * q.slot);
 #pragma unroll
                                 for (int ks = 0; ks < 4; ks++) wide_mma<C::PAIR>(d, ad0 + off + 2 * ks, bd0 + off + 2 * ks, C::IDESC, ks > 0);
                             }
@@ -1050,9 +1092,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
                 bool ok = true;
                 const int nbb = (p.nb + kKB - 1) / kKB;
                 for (int t = t0; t < total && ok; t += tstep) {
-                    const WideTile ti = walk.at(t);
+                    const WideTile ti = tile_at(t);
                     const float *sw = p.sb + ((size_t)ti.e * nbb + ti.c0 / kKB + (lane & 1)) * p.nkb;
-                    const bool in_w = ti.c0 + kKB * (lane & 1) < p.nb;
+                    const bool in_w = ti.c0 + kKB * (lane & 1) < p.nb && kKB * (lane & 1) < C::BN;
                     for (int kb = ti.k0; kb < ti.k1; kb++) {
                         const int s = r.slot;
                         if (!__all_sync(0xffffffffu, ring_wait(smem_u32(&s_sempty[s]), r.phase ^ 1u, fail))) {
@@ -1081,7 +1123,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
             WideTile ti = {};
             bool live = t < total;
             if (live) {
-                ti = walk.at(t);
+                ti = tile_at(t);
                 kb = ti.k0;
             }
             float v[D][12];
@@ -1093,7 +1135,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
                         t += tstep;
                         live = t < total;
                         if (live) {
-                            ti = walk.at(t);
+                            ti = tile_at(t);
                             kb = ti.k0;
                         }
                     }
@@ -1151,6 +1193,42 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
         if (rank == 0)
             for (int i = max(0, s_issued - C::S); i < s_issued; i++) mbar_wait(smem_u32(&s_full[i % C::S]), (uint32_t)(i / C::S) & 1u);
         atomicOr(p.err, MOE_DEVICE_ERR_TC);
+    }
+    if constexpr (C::SPLIT) {
+        // sums of all blocks of the cluster, in block order: block r adds rows r, r + csize, ..., a warp a
+        // row, every block's value in flight at once
+        cluster_sync_all();
+        if (t0 < total) {
+            const WideTile ti = walk.at(t0);
+            uint32_t peer[kMaxSplit];
+#pragma unroll
+            for (uint32_t r = 0; r < kMaxSplit; r++) peer[r] = peer_addr(ring, (int)r < csize ? r : 0u);
+            for (int row = crank + csize * warp; row < 128; row += csize * (C::THREADS / 32)) {
+                if (ti.r0 + row >= ti.rend) break;
+                float4 v[kMaxSplit], sum = make_float4(0, 0, 0, 0);
+                const uint32_t off = (uint32_t)(row * C::PLD + 4 * lane) * 4u;
+#pragma unroll
+                for (int r = 0; r < (int)kMaxSplit; r++) v[r] = r < csize ? ld_peer4(peer[r] + off) : make_float4(0, 0, 0, 0);
+#pragma unroll
+                for (int r = 0; r < (int)kMaxSplit; r++) sum = make_float4(sum.x + v[r].x, sum.y + v[r].y, sum.z + v[r].z, sum.w + v[r].w);
+                const int c = ti.c0 + 4 * lane;
+                const long long at = (long long)(ti.r0 + row) * p.ldo + c;
+                if (p.vec && c + 4 <= p.nb) {
+                    if (p.out_dtype == MOE_DTYPE_F32)
+                        *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) = sum;
+                    else if (p.out_dtype == MOE_DTYPE_BF16)
+                        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + at) = make_uint2(pack16<__nv_bfloat16>(sum.x, sum.y), pack16<__nv_bfloat16>(sum.z, sum.w));
+                    else
+                        *reinterpret_cast<uint2 *>(static_cast<__half *>(p.out) + at) = make_uint2(pack16<__half>(sum.x, sum.y), pack16<__half>(sum.z, sum.w));
+                } else {
+                    const float f[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+                    for (int k = 0; k < 4; k++)
+                        if (c + k < p.nb) store_out(p.out, at + k, f[k], p.out_dtype);
+                }
+            }
+        }
+        cluster_sync_all();
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
@@ -1584,13 +1662,14 @@ cudaError_t launch_gemm(const GemmArgs &p, const CUtensorMap &am, const uint8_t 
 
 template <class C>
 cudaError_t launch_wide(const WideArgs &p, const uint8_t *a, uint64_t a_cols, const uint8_t *b, uint64_t b_cols, uint64_t b_mats,
-                        long long tiles, cudaStream_t st) {
+                        long long tiles, int cluster, cudaStream_t st) {
     CUtensorMap am, bm;
     if (!tmap(&am, 3, a, a_cols, p.na, 1, 128) || !tmap(&bm, 3, b, b_cols, p.nb, b_mats, C::BROWS)) return cudaErrorInvalidValue;
     const cudaError_t e = allow_smem<fp8_wide_kernel<C>>(C::SMEM);
     if (e != cudaSuccess) return e;
     const long long nb = C::PAIR ? 2 : 1, most = sm_count() / nb;
-    return launch_early(fp8_wide_kernel<C>, dim3((unsigned)(nb * (tiles < most ? tiles : most))), C::THREADS, C::SMEM, st, (unsigned)nb, am, bm, p);
+    const long long blocks = C::SPLIT ? tiles * cluster : nb * (tiles < most ? tiles : most);
+    return launch_early(fp8_wide_kernel<C>, dim3((unsigned)blocks), C::THREADS, C::SMEM, st, (unsigned)(C::SPLIT ? cluster : nb), am, bm, p);
 }
 
 bool rows_aligned(const void *out, long long ldo, int dtype) {
@@ -1621,24 +1700,14 @@ cudaError_t launch_fp8_matmul(const uint8_t *x, const float *xs, int R, const ui
     const long long nat = (N + kARows - 1) / kARows;
     const int used = offsets ? (E < R ? E : R) : 1;      // weight matrices that rows can belong to
     const int each = (R + used - 1) / used;
-    auto tiles = [&](int bt) { return nat * (offsets ? (long long)R / bt + used : ((long long)R + bt - 1) / bt); };
-    auto go = [&](auto c, int per_sm) {
-        using C = decltype(c);
-        return launch_gemm<C>(p, am, x, K, R, tiles(C::BT), per_sm, 1, st);
-    };
-    auto go_split = [&](auto c) {
-        using C = decltype(c);
-        int cs = 8;
-        while (cs > 1 && (cs > p.nkb || tiles(C::BT) * cs > 4ll * sm_count())) cs /= 2;
-        return launch_gemm<C>(p, am, x, K, R, tiles(C::BT), 2, cs, st);
-    };
     if (each <= 16) {
-        if (tiles(16) <= 2 * sm_count()) return go_split(Cfg<16, true, 5>{});
-        return go(Cfg<16, false, 5>{}, 2);
-    }
-    if (each <= 64) {
-        if (tiles(64) <= 2 * sm_count()) return go_split(Cfg<64, true, 4>{});
-        return go(Cfg<64, false, 4>{}, 2);
+        // few rows of every weight matrix: weights as lanes, 16 rows as columns, two blocks an SM; bound by
+        // the weights' bytes.  Up to eight blocks share a tile's inner axis while all fit at once.
+        const long long most = nat * (offsets ? (long long)R / 16 + used : ((long long)R + 15) / 16);
+        int cs = (int)kMaxSplit;
+        while (cs > 1 && (cs > p.nkb || most * cs > 2ll * sm_count())) cs /= 2;
+        if (cs > 1) return launch_gemm<Cfg<16, true, 5>>(p, am, x, K, R, most, 2, cs, st);
+        return launch_gemm<Cfg<16, false, 5>>(p, am, x, K, R, most, 2, 1, st);
     }
     WideArgs q = {};
     q.sa = xs;
@@ -1653,13 +1722,29 @@ cudaError_t launch_fp8_matmul(const uint8_t *x, const float *xs, int R, const ui
     q.out_dtype = y_dtype;
     q.vec = rows_aligned(y, ldy, y_dtype);
     q.err = p.err;
-    const long long nct = (N + 255) / 256;
-    auto wide = [&](auto c) {
-        using C = decltype(c);
-        return launch_wide<C>(q, x, K, w, K, E, nct * (offsets ? (long long)R / C::ROWS + used : ((long long)R + C::ROWS - 1) / C::ROWS), st);
+    auto wide_tiles = [&](int rows, int bn, int per_expert) {      // at most (2) or expected (1: half a tile more an expert)
+        return (long long)((N + bn - 1) / bn) * (offsets ? (long long)R / rows + (used * per_expert + 1) / 2 : ((long long)R + rows - 1) / rows);
     };
-    if (each <= 256) return wide(WideCfg<false, false>{});
-    return wide(WideCfg<true, false>{});
+    auto wide = [&](auto c, int cluster) {
+        using C = decltype(c);
+        return launch_wide<C>(q, x, K, w, K, E, wide_tiles(C::ROWS, C::BN, 2), cluster, st);
+    };
+    // The tile with the least estimated time: rounds over the card's SMs x (inner blocks x the time of
+    // one + the time to store a tile), in us.  Measured a block (a stage) and a tile: 128 x 128 0.30 and
+    // 0.5, 128 x 256 0.43 and 0.8, a pair's 256 x 256 0.385 and 1.4; sharing a tile's inner axis costs
+    // 2.2.  (N 4096, K 6144: 512 rows 20.2 / 24.7 / 24.2 us, 16381 rows 410 / 299 / 277 us; 128 rows
+    // 19.1 us alone, 11.7 us with four blocks a tile.  64 experts, N = K = 2048, 8192 rows: 66 / 62 / 71 us.)
+    const long long sms = sm_count();
+    auto rounds = [&](int rows, int bn, long long at_once) { return (double)((wide_tiles(rows, bn, 1) + at_once - 1) / at_once); };
+    const double mid = rounds(128, 128, sms) * (0.30 * p.nkb + 0.5), one = rounds(128, 256, sms) * (0.43 * p.nkb + 0.8),
+                 pair = rounds(256, 256, sms / 2) * (0.385 * p.nkb + 1.4);
+    int split = 1;
+    for (int cs = 2; cs <= 4; cs *= 2)      // clusters that all fit at once: a second round would start from nothing
+        if (wide_tiles(128, 128, 2) * cs <= sms - 4 && p.nkb >= 2 * cs) split = cs;
+    if (split > 1 && 2.2 + 0.30 * p.nkb / split < (mid < one ? mid : one)) return wide(WideCfg<false, false, 128, true>{}, split);
+    if (mid <= one && mid <= pair) return wide(WideCfg<false, false, 128>{}, 1);
+    if (one <= pair) return wide(WideCfg<false, false>{}, 1);
+    return wide(WideCfg<true, false>{}, 1);
 }
 
 cudaError_t launch_fp8_wgrad(const uint8_t *xt, const float *xs, const uint8_t *dyt, const float *dys, int R, int N, int K, int E,
@@ -1682,7 +1767,7 @@ cudaError_t launch_fp8_wgrad(const uint8_t *xt, const float *xs, const uint8_t *
     if (e != cudaSuccess) return e;
     using C = WideCfg<true, true>;
     const long long tiles = (long long)E * ((N + C::ROWS - 1) / C::ROWS) * ((K + C::BN - 1) / C::BN);
-    return launch_wide<C>(p, dyt, R, xt, R, 1, tiles, st);
+    return launch_wide<C>(p, dyt, R, xt, R, 1, tiles, 1, st);
 }
 
 cudaError_t fp8_error_read(unsigned *flags) {
