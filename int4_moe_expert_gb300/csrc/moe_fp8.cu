@@ -604,17 +604,17 @@ struct WideCfg {
     static constexpr int THREADS = 32 * (EW + 4);
     static constexpr bool BIGREG = WC > 64;
     static constexpr int SS = 8;                              // scale ring (matmul)
-    static constexpr int SFBYTES = 512 + 1024;                // staged scales of a stage (MX): 128 + 256 words
-    static constexpr int SFCOLS = 12;                         // their tensor-memory columns: 4 + 8
+    static constexpr int SFBYTES = 512 + 4 * BN;              // staged scales of a stage (MX): 128 + BN words
+    static constexpr int SFCOLS = 4 + BN / 32;                // their tensor-memory columns
     static constexpr int OUTB = 4096;                         // staging of an epilogue warp: 32 rows x 128 bytes
     static constexpr int NT = MX ? 2 : 512 / BN;              // accumulators: of tiles (MX), of stages
-    static constexpr int ACC1 = MX ? 512 - SFCOLS * S - BN : BN;   // from one to the next (MX: the second overlaps the first)
+    static constexpr int ACC1 = MX && 2 * BN + SFCOLS * S > 512 ? 512 - SFCOLS * S - BN : BN;   // from one to the next (MX: may overlap)
     static constexpr int PLD = BN + 4;                        // floats of a row of partial sums (SPLIT)
     static constexpr size_t SMEM = 1024 + (size_t)S * STAGE + EW * OUTB + (MX ? S * SFBYTES : 0);
     // f8f6f4: D f32 at bit 4; mxf8f6f4: ue8m0 scales at bit 23
     static constexpr uint32_t IDESC = (MX ? 1u << 23 : 1u << 4) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(ROWS >> 4) << 24);
-    static_assert(!MX || BN == 256, "the scales' layout is written for 256 columns");
-    static_assert(!SPLIT || (!PAIR && !MX && 128 * PLD * 4 <= S * STAGE), "partial sums reuse the stage ring");
+    static_assert(ACC1 >= BN - 64, "the columns that two accumulators share leave first");
+    static_assert(!SPLIT || (!PAIR && 128 * PLD * 4 <= S * STAGE), "partial sums reuse the stage ring");
     static_assert(SMEM + 16 * 1024 <= 227 * 1024, "the rings and the static arrays fit one block's shared memory");
 };
 
@@ -814,6 +814,12 @@ __device__ __forceinline__ void store_cols(const uint64_t *v, uint32_t stage, co
     else store_64<__half>(v, stage, p.out, at, p.ldo, rows, cols, p.vec, lane);
 }
 
+// 64 columns' partial sums of a row to shared memory
+__device__ __forceinline__ void partial_64(const uint64_t *v, uint32_t at) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) asm volatile("st.shared.v2.b64 [%0], {%1, %2};" ::"r"(at + 8u * i), "l"(v[i]), "l"(v[i + 1]) : "memory");
+}
+
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_constant__ CUtensorMap amap,
                                                                  const __grid_constant__ CUtensorMap bmap,
@@ -914,12 +920,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
             const long long at = (C::MX ? (long long)ti.e * p.out_stride : 0ll) + (long long)row * p.ldo + c0;
             if constexpr (C::MX) {
                 const int q = done & 1;
-                if (ti.k0 == ti.k1) {      // an expert without rows
+                if (ti.k0 == ti.k1) {      // an expert without rows, or no block of the inner axis left
                     uint64_t z[32];
 #pragma unroll
                     for (int i = 0; i < 32; i++) z[i] = 0ull;
-                    for (int c = 0; c < 128; c += 64)
-                        if (rows > 0) store_cols(z, stage, p, at + c, rows, cols - c, lane);
+                    if constexpr (C::SPLIT) {
+                        partial_64(z, ring + (uint32_t)((32 * q4 + lane) * C::PLD + C::WC * half) * 4u);
+                    } else {
+                        for (int c = 0; c < C::WC; c += 64)
+                            if (rows > 0) store_cols(z, stage, p, at + c, rows, cols - c, lane);
+                    }
                     continue;
                 }
                 if (!__all_sync(0xffffffffu, ring_wait(smem_u32(&s_tfull[q]), (uint32_t)(done >> 1) & 1u, fail))) {
@@ -930,10 +940,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 // the accumulators overlap: the first one's last columns are the second one's first,
                 // so those 64 columns leave first and the next tile may start
-                const int first = q ? 0 : 64;
-                const uint32_t base = trow + (uint32_t)((q ? C::ACC1 : 0) + 128 * half);
+                const int first = q || C::WC == 64 ? 0 : 64;
+                const uint32_t base = trow + (uint32_t)((q ? C::ACC1 : 0) + C::WC * half);
 #pragma unroll 1
-                for (int h = 0; h < 2; h++) {
+                for (int h = 0; h < C::WC / 64; h++) {
                     const int c = h ? 64 - first : first;
                     uint32_t r[64];
                     tc_ld<64>(base + (uint32_t)c, r);
@@ -941,7 +951,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
                     uint64_t v[32];
 #pragma unroll
                     for (int i = 0; i < 32; i++) v[i] = pack2(r[2 * i], r[2 * i + 1]);
-                    if (rows > 0) store_cols(v, stage, p, at + c, rows, cols - c, lane);
+                    if constexpr (C::SPLIT) partial_64(v, ring + (uint32_t)((32 * q4 + lane) * C::PLD + C::WC * half) * 4u);
+                    else if (rows > 0) store_cols(v, stage, p, at + c, rows, cols - c, lane);
                 }
                 done++;
             } else {
@@ -976,10 +987,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
                 if (!ok) break;
                 if constexpr (C::SPLIT) {
                     // partial sums [row][column] over the stage ring: every copy into it was consumed
-                    const uint32_t ps = ring + (uint32_t)((32 * q4 + lane) * C::PLD + C::WC * half) * 4u;
-#pragma unroll
-                    for (int i = 0; i < C::WC / 2; i += 2)
-                        asm volatile("st.shared.v2.b64 [%0], {%1, %2};" ::"r"(ps + 8u * i), "l"(acc[i]), "l"(acc[i + 1]) : "memory");
+                    partial_64(acc, ring + (uint32_t)((32 * q4 + lane) * C::PLD + C::WC * half) * 4u);
                 } else if (rows > 0) {
 #pragma unroll
                     for (int l = 0; l < C::WC / 64; l++) store_cols(acc + 32 * l, stage, p, at + 64 * l, rows, cols - 64 * l, lane);
@@ -1050,7 +1058,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
                                 const uint32_t tsf = taddr + (uint32_t)(512 - C::SFCOLS * (C::S - r.slot));
                                 const uint64_t sd = sd0 + (uint64_t)((r.slot * C::SFBYTES) >> 4);
 #pragma unroll
-                                for (int i = 0; i < 3; i++) wide_cp_scales<C::PAIR>(tsf + 4 * i, sd + (uint64_t)(i * (512 >> 4)));
+                                for (int i = 0; i < 1 + C::BN / 128; i++) wide_cp_scales<C::PAIR>(tsf + 4 * i, sd + (uint64_t)(i * (512 >> 4)));
                                 const uint32_t d = taddr + (uint32_t)(q.slot ? C::ACC1 : 0);
 #pragma unroll
                                 for (int ks = 0; ks < 4; ks++)
@@ -1116,7 +1124,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
                 asm volatile("cp.async.wait_all;" ::: "memory");
             }
         } else {
-            // scales: the exponent bytes of this block's 128 rows of A and all 256 of B, by two warps in
+            // scales: the exponent bytes of this block's 128 rows of A and all columns' of B, by two warps in
             // turn, each D of its stages ahead in registers
             constexpr int D = 3;
             int t = t0, kb = 0, n = 0, mine = warp - (C::EW + 2);    // next stage to load: its tile, block and number
@@ -1126,9 +1134,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
                 ti = tile_at(t);
                 kb = ti.k0;
             }
-            float v[D][12];
+            constexpr int NV = 4 + C::BN / 32;      // values a lane: 128 rows of A, the tile's of B
+            float v[D][NV];
             int num[D];
-            auto load = [&](float (&d)[12]) {
+            auto load = [&](float (&d)[NV]) {
                 // this warp's next stage into d; its number, -1 behind the last
                 for (;;) {
                     while (live && kb >= ti.k1) {
@@ -1146,7 +1155,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
                     kb += skip;
                 }
 #pragma unroll
-                for (int i = 0; i < 12; i++) {
+                for (int i = 0; i < NV; i++) {
                     const int r = (i < 4 ? ti.r0 : ti.c0 - 128) + 32 * i + lane;
                     d[i] = r < (i < 4 ? p.na : p.nb) ? __ldg(i < 4 ? p.sa + (size_t)kb * p.na + r : p.sb + (size_t)kb * p.nb + r) : 0.0f;
                 }
@@ -1173,7 +1182,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
                     // word of row r: 16-byte line r % 32, its (r / 32) % 4-th word, 512 bytes per 128 rows
                     const uint32_t sf = sfring + (uint32_t)(s * C::SFBYTES + lane * 16);
 #pragma unroll
-                    for (int i = 0; i < 3; i++) {
+                    for (int i = 0; i < NV / 4; i++) {
                         uint32_t b[4];
 #pragma unroll
                         for (int k = 0; k < 4; k++) b[k] = ((__float_as_uint(v[d][4 * i + k]) >> 23) & 0xFFu) * 0x01010101u;
@@ -1212,7 +1221,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
 #pragma unroll
                 for (int r = 0; r < (int)kMaxSplit; r++) sum = make_float4(sum.x + v[r].x, sum.y + v[r].y, sum.z + v[r].z, sum.w + v[r].w);
                 const int c = ti.c0 + 4 * lane;
-                const long long at = (long long)(ti.r0 + row) * p.ldo + c;
+                const long long at = (C::MX ? (long long)ti.e * p.out_stride : 0ll) + (long long)(ti.r0 + row) * p.ldo + c;
                 if (p.vec && c + 4 <= p.nb) {
                     if (p.out_dtype == MOE_DTYPE_F32)
                         *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) = sum;
@@ -1765,9 +1774,23 @@ cudaError_t launch_fp8_wgrad(const uint8_t *xt, const float *xs, const uint8_t *
     p.vec = rows_aligned(dw, K, dw_dtype);
     const cudaError_t e = error_word(&p.err);
     if (e != cudaSuccess) return e;
-    using C = WideCfg<true, true>;
-    const long long tiles = (long long)E * ((N + C::ROWS - 1) / C::ROWS) * ((K + C::BN - 1) / C::BN);
-    return launch_wide<C>(p, dyt, R, xt, R, 1, tiles, 1, st);
+    auto tiles = [&](int rows, int bn) { return (long long)E * ((N + rows - 1) / rows) * ((K + bn - 1) / bn); };
+    // Few outputs from many rows: 128 x 128 tiles, whose inner range a cluster shares, all at once (clusters
+    // of eight fit about 14 times); else a pair's 256 x 256 tiles.  Estimated in us from measurements: a
+    // pair's block 0.273 and tile 1.2, a cluster's block 0.31 and its exchange 2.5 more (512 x 512 from
+    // 32768 rows: 76 us by pairs, 28 us by four blocks a tile; from 256 rows 8.3 and 8.4 us).
+    const long long sms = sm_count();
+    const double per = (double)p.nkb / E;
+    const double pair = (double)((tiles(256, 256) + sms / 2 - 1) / (sms / 2)) * (0.273 * per + 1.2);
+    int split = 1;
+    for (int cs = 2; cs <= (int)kMaxSplit; cs *= 2)
+        if (tiles(128, 128) * cs <= sms - (cs > 4 ? 40 : 4) && per >= 2 * cs) split = cs;
+    auto go = [&](auto c, int cluster) {
+        using C = decltype(c);
+        return launch_wide<C>(p, dyt, R, xt, R, 1, tiles(C::ROWS, C::BN), cluster, st);
+    };
+    if (split > 1 && 0.31 * per / split + 2.5 < pair) return go(WideCfg<false, true, 128, true>{}, split);
+    return go(WideCfg<true, true>{}, 1);
 }
 
 cudaError_t fp8_error_read(unsigned *flags) {

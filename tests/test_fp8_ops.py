@@ -399,6 +399,14 @@ def test_wgrad_many_tiles_with_and_without_rows(gpu):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("N,K,off", [(256, 256, None), (130, 300, None), (200, 136, [0, 2048, 2048, 4096]), (512, 500, [0, 128, 4096])])
+def test_wgrad_few_outputs_from_many_rows(gpu, N, K, off):
+    """Blocks that share a tile's rows, experts with fewer row blocks than sharers and with none."""
+    check_wgrad(gpu, 4096, N, K, off)
+    check_wgrad(gpu, 4096, N, K, off, torch.bfloat16)
+
+
+@pytest.mark.gpu
 def test_wgrad_no_rows_and_nan(gpu):
     z = lambda *s: torch.zeros(*s, device="cuda")    # noqa: E731
     dw = gpu.moe_fp8_wgrad(z(16, 0).to(F8), z(0, 16), z(24, 0).to(F8), z(0, 24), offsets=torch.zeros(4, dtype=torch.int32, device="cuda"))
