@@ -187,6 +187,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
     return d;
 }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     uint64_t d;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -623,7 +628,6 @@ struct WideCfg {
     static constexpr size_t SMEM = 1024 + (size_t)S * STAGE + EW * OUTB + (MX ? S * SFBYTES : 0);
     // f8f6f4: D f32 at bit 4; mxf8f6f4: ue8m0 scales at bit 23
     static constexpr uint32_t IDESC = (MX ? 1u << 23 : 1u << 4) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(ROWS >> 4) << 24);
-    static_assert(ACC1 >= BN - 64, "the columns that two accumulators share leave first");
     static_assert(!SPLIT || (!PAIR && 128 * PLD * 4 <= S * STAGE), "partial sums reuse the stage ring");
     static_assert(SMEM + 16 * 1024 <= 227 * 1024, "the rings and the static arrays fit one block's shared memory");
 };
@@ -684,6 +688,11 @@ __device__ __forceinline__ void wide_cp_scales(uint32_t taddr, uint64_t desc) {
     else
         asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
+
+// MX: blocks of the inner axis that the tensor core adds up before the registers take the sum over.  Its
+// additions truncate, so an error grows with the length (2-norm against 64 bits, float32 outputs from
+// 32768 rows: 6.5e-6 in one go).
+constexpr int kFlush = 16;
 
 struct WideArgs {
     const float *sa;        // row scales of A [nkb][na] (wgrad: power of two)
@@ -929,42 +938,37 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
             const int row = ti.r0 + 32 * q4, rows = ti.rend - row, c0 = ti.c0 + C::WC * half, cols = p.nb - c0;
             const long long at = (C::MX ? (long long)ti.e * p.out_stride : 0ll) + (long long)row * p.ldo + c0;
             if constexpr (C::MX) {
-                const int q = done & 1;
-                if (ti.k0 == ti.k1) {      // an expert without rows, or no block of the inner axis left
-                    uint64_t z[32];
+                // every kFlush blocks the registers take the sums over from tensor memory (none: zeros)
+                uint64_t acc[C::WC / 64][32];
 #pragma unroll
-                    for (int i = 0; i < 32; i++) z[i] = 0ull;
-                    if constexpr (C::SPLIT) {
-                        partial_64(z, ring + (uint32_t)((32 * q4 + lane) * C::PLD + C::WC * half) * 4u);
-                    } else {
-                        for (int c = 0; c < C::WC; c += 64)
-                            if (rows > 0) store_cols(z, stage, p, at + c, rows, cols - c, lane);
+                for (int l = 0; l < C::WC / 64; l++)
+#pragma unroll
+                    for (int i = 0; i < 32; i++) acc[l][i] = 0ull;
+                for (int kc = ti.k0; kc < ti.k1; kc += kFlush) {
+                    const int q = done & 1;
+                    if (!__all_sync(0xffffffffu, ring_wait(smem_u32(&s_tfull[q]), (uint32_t)(done >> 1) & 1u, fail))) {
+                        *fail = 1;
+                        ok = false;
+                        break;
                     }
-                    continue;
-                }
-                if (!__all_sync(0xffffffffu, ring_wait(smem_u32(&s_tfull[q]), (uint32_t)(done >> 1) & 1u, fail))) {
-                    *fail = 1;
-                    ok = false;
-                    break;
-                }
-                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                // the accumulators overlap: the first one's last columns are the second one's first,
-                // so those 64 columns leave first and the next tile may start
-                const int first = q || C::WC == 64 ? 0 : 64;
-                const uint32_t base = trow + (uint32_t)((q ? C::ACC1 : 0) + C::WC * half);
-#pragma unroll 1
-                for (int h = 0; h < C::WC / 64; h++) {
-                    const int c = h ? 64 - first : first;
-                    uint32_t r[64];
-                    tc_ld<64>(base + (uint32_t)c, r);
-                    if (h == 0) release(0);
-                    uint64_t v[32];
+                    done++;
+                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    const uint32_t base = trow + (uint32_t)((q ? C::ACC1 : 0) + C::WC * half);
 #pragma unroll
-                    for (int i = 0; i < 32; i++) v[i] = pack2(r[2 * i], r[2 * i + 1]);
-                    if constexpr (C::SPLIT) partial_64(v, ring + (uint32_t)((32 * q4 + lane) * C::PLD + C::WC * half) * 4u);
-                    else if (rows > 0) store_cols(v, stage, p, at + c, rows, cols - c, lane);
+                    for (int l = 0; l < C::WC / 64; l++) {
+                        uint32_t r[64];
+                        tc_ld<64>(base + 64u * l, r);
+                        if (l + 1 == C::WC / 64) release(0);      // the next sums may start (the accumulators overlap)
+#pragma unroll
+                        for (int i = 0; i < 32; i++) acc[l][i] = add2(acc[l][i], pack2(r[2 * i], r[2 * i + 1]));
+                    }
                 }
-                done++;
+                if (!ok) break;
+#pragma unroll
+                for (int l = 0; l < C::WC / 64; l++) {
+                    if constexpr (C::SPLIT) partial_64(acc[l], ring + (uint32_t)((32 * q4 + lane) * C::PLD + C::WC * half) * 4u);
+                    else if (rows > 0) store_cols(acc[l], stage, p, at + 64 * l, rows, cols - 64 * l, lane);
+                }
             } else {
                 uint64_t acc[C::WC / 2];
 #pragma unroll
@@ -1037,7 +1041,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
             if (rank == 0) {
                 Ring<C::S> r;
                 Ring<C::NT> q;  // matmul: accumulator of the stage; MX: of the tile
-                int tile = 0;
+                int sums = 0;   // MX: accumulators begun
                 bool ok = true, any = false;
                 const uint64_t ad0 = sw128_desc(ring), bd0 = sw128_desc(ring + kABytes);
                 // shared-memory operand of the scale copies: 8-row groups of 16 bytes 128 bytes apart, no swizzle
@@ -1045,14 +1049,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
                 for (int t = t0; t < total && ok; t += tstep) {
                     const WideTile ti = tile_at(t);
                     const int k1 = ti.k1;
-                    // MX: the previous tile's overlapping columns are in registers (its epilogue follows
-                    // that of the tile before it, which used this accumulator)
-                    if (C::MX && ti.k0 < k1 && tile > 0 &&
-                        !__all_sync(0xffffffffu, ring_wait(smem_u32(&s_tempty[0]), (uint32_t)(tile - 1) & 1u, fail))) {
-                        ok = false;
-                        break;
-                    }
                     for (int kb = ti.k0; kb < k1; kb++) {
+                        const bool fresh = C::MX && (kb - ti.k0) % kFlush == 0;
+                        // MX: the previous sums, whose columns overlap these, are in registers (and so those
+                        // before them, which used this accumulator)
+                        if (fresh && sums > 0 && !__all_sync(0xffffffffu, ring_wait(smem_u32(&s_tempty[0]), (uint32_t)(sums - 1) & 1u, fail))) {
+                            ok = false;
+                            break;
+                        }
+                        const bool last = C::MX && (kb + 1 == k1 || (kb + 1 - ti.k0) % kFlush == 0);
                         // the operands first: they are there early, the accumulator comes back last
                         const bool w = ring_wait(smem_u32(&s_full[r.slot]), r.phase, fail) &&
                                        (C::MX ? ring_wait(smem_u32(&s_sfull[r.slot]), r.phase, fail)
@@ -1072,22 +1077,19 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
                                 const uint32_t d = taddr + (uint32_t)(q.slot ? C::ACC1 : 0);
 #pragma unroll
                                 for (int ks = 0; ks < 4; ks++)
-                                    wide_mma_mx<C::PAIR>(d, ad0 + off + 2 * ks, bd0 + off + 2 * ks, C::IDESC, tsf, tsf + 4, kb > ti.k0 || ks > 0);
+                                    wide_mma_mx<C::PAIR>(d, ad0 + off + 2 * ks, bd0 + off + 2 * ks, C::IDESC, tsf, tsf + 4, !fresh || ks > 0);
                             } else {
                                 const uint32_t d = taddr + (uint32_t)(C::BN * q.slot);
 #pragma unroll
                                 for (int ks = 0; ks < 4; ks++) wide_mma<C::PAIR>(d, ad0 + off + 2 * ks, bd0 + off + 2 * ks, C::IDESC, ks > 0);
                             }
                             wide_commit<C::PAIR>(smem_u32(&s_empty[r.slot]));
-                            if (!C::MX || kb + 1 == k1) wide_commit<C::PAIR>(smem_u32(&s_tfull[q.slot]));
+                            if (!C::MX || last) wide_commit<C::PAIR>(smem_u32(&s_tfull[q.slot]));
                         }
                         r.next();
-                        if (!C::MX) q.next();
+                        if (!C::MX || last) q.next();
+                        if (last) sums++;
                         any = true;
-                    }
-                    if (ti.k0 < k1) {
-                        tile++;
-                        if (C::MX) q.next();
                     }
                 }
                 if (!ok) *fail = 1;

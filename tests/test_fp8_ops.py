@@ -407,6 +407,22 @@ def test_wgrad_few_outputs_from_many_rows(gpu, N, K, off):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("N,K", [(256, 256), (2000, 2560)])
+def test_wgrad_long_sums_keep_float32(gpu, N, K):
+    """32768 rows: the 2-norm of the error against 64 bits stays within a few float32 roundings a level,
+    16 x 2^-24 (sums of 2048 rows by the tensor core, which truncates, then float32 additions); sums in
+    one go would be off by 6e-6."""
+    R = 32768
+    xt, xs, dyt, ds = (t.cuda() for t in wgrad_case(R, N, K, 7))
+    xs.fill_(1.0), ds.fill_(1.0)
+    dw = gpu.moe_fp8_wgrad(xt, xs, dyt, ds)
+    ref = torch.zeros(N, K, dtype=torch.float64, device="cuda")
+    for r in range(0, R, 4096):
+        ref += dyt[:, r:r + 4096].double() @ xt[:, r:r + 4096].double().t()
+    assert float((dw.double() - ref).norm() / ref.norm()) <= 16 * 2.0 ** -24
+
+
+@pytest.mark.gpu
 def test_wgrad_no_rows_and_nan(gpu):
     z = lambda *s: torch.zeros(*s, device="cuda")    # noqa: E731
     dw = gpu.moe_fp8_wgrad(z(16, 0).to(F8), z(0, 16), z(24, 0).to(F8), z(0, 24), offsets=torch.zeros(4, dtype=torch.int32, device="cuda"))
