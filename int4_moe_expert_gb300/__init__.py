@@ -463,8 +463,9 @@ def moe_fp8_matmul(x, x_scale, w, w_scale, offsets=None, out=None, out_dtype=Non
 
 def moe_fp8_wgrad(xt, xt_scale, dyt, dyt_scale, offsets=None, out=None, out_dtype=None, stream=None):
     """Weight gradients from column-quantised x and dy (moe_fp8_quantize(..., transposed=True)):
-    xt [K, R], dyt [N, R] codes, R a multiple of 128, xt_scale [R / 128, K], dyt_scale [R / 128, N];
-    offsets [E + 1] int32, multiples of 128 (None: one matrix).
+    xt [K, R], dyt [N, R] codes, R a multiple of 128, xt_scale [R / 128, K], dyt_scale [R / 128, N]
+    powers of two (only their exponents are used); offsets [E + 1] int32, multiples of 128 (None:
+    one matrix).
     -> dw [E, N, K] ([N, K] without offsets), float32 by default."""
     return _native().fp8_wgrad(xt, xt_scale, dyt, dyt_scale, offsets, out, out_dtype, _handle(stream))
 

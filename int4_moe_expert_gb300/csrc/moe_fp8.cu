@@ -1,25 +1,25 @@
-// Block-scaled e4m3 products on the 5th-generation tensor cores.
+// Block-scaled e4m3 quantisers and products on the 5th-generation tensor cores.
 //
-// One kernel serves three products (a "column" is a row of the B operand, a "lane" a row of A):
 //   matmul  y[r, n]     = sum_kb xs[kb, r] ws[e, n / 128, kb] sum_{k in kb} x[r, k] w[e][n, k]
-//           A = the weights (lanes n), B = the activations (columns r), e = the expert whose
-//           offsets hold r; without offsets one weight matrix
-//   dgrad   the same call with the transposed weights
+//           (e: the expert whose offsets hold r; without offsets one weight matrix).  The gradient
+//           of x is the same product with the transposed weights.
 //   wgrad   dw[e][n, k] = sum_kb dys[kb, n] xs[kb, k] sum_{r in kb} dy[n, r] x[k, r]
-//           A = the column-quantised x (lanes k), B = the column-quantised dy (columns n),
-//           kb over the 128-row blocks of expert e
-// always out[column][lane], so a warp stores 32 neighbouring values of one output row.
+//           over the 128-row blocks kb of expert e
 //
-// The scales are general float32, so a block's product cannot stay in the tensor core's
-// accumulator: each 128-element block of the inner axis is one stage (128 bytes a row, exactly
-// one 128-byte swizzle atom), its four MMAs (K 32) write a fresh accumulator of a small ring in
-// tensor memory, and eight (four for narrow tiles) warps add it, times its scales, to the float32
-// sums in their registers.  All sums over blocks are float32 in block order.
+// Every 128-element block of the inner axis is one stage of a shared-memory ring: 128 bytes a row,
+// exactly one 128-byte swizzle atom, four MMAs of K 32.  The matmul's scales are general float32, so
+// a block's product cannot stay in the tensor core's accumulator: its MMAs write a fresh one, and
+// the epilogue warps add that, times its scales, to float32 sums in their registers, in block order.
+// The wgrad's scales are powers of two and the tensor core applies them.
+//
+// Two kernels.  fp8_narrow_kernel: 16 rows or fewer of a weight matrix, weights as lanes (M 128),
+// rows as columns (N 16), bound by the weights' bytes.  fp8_wide_kernel: rows as lanes, contiguous
+// outputs as columns, tiles of 128 x 128, 128 x 256, or 256 x 256 by a pair of blocks.
 //
 // Warp roles: epilogue warps (tcgen05.ld, two-wide fused multiply-adds, the stores), one warp of
-// tensor copies, one MMA-issuing warp, one warp that multiplies and stages the scales.  mbarrier
-// rings connect them; every wait is bounded, and a block that gives up sets the error word, waits
-// (bounded) for its copies and MMAs and frees its tensor memory.
+// tensor copies, one MMA-issuing warp, one or two warps of scales.  mbarrier rings connect them;
+// every wait is bounded, and a block that gives up sets the error word, waits (bounded) for its
+// copies and MMAs and frees its tensor memory.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -43,36 +43,36 @@ constexpr int kKB = 128;                 // inner elements per stage and per sca
 constexpr int kARows = 128;              // lanes of a tile
 constexpr int kABytes = kARows * kKB;    // A bytes of a stage
 
-struct GemmArgs {
-    const float *sa;        // block scales [E][ceil(na / 128)][nkb]
-    const float *sb;        // column scales [nkb][nb]
+struct NarrowArgs {
+    const float *sa;        // weights' block scales [E][ceil(na / 128)][nkb]
+    const float *sb;        // rows' scales [nkb][nb]
     const int *offsets;     // [E + 1] or NULL
     void *out;
-    long long ldo;          // elements between columns of out
-    int na, nb;             // rows of A (of one expert), rows of B
+    long long ldo;          // elements between rows of out
+    int na, nb;             // weight rows (of one expert), rows of x
     int nkb;                // 128-blocks of the inner axis
     int E;
     int out_dtype;
     unsigned *err;
 };
 
-template <int BT_, bool SPLIT_, int STAGES_>
-struct Cfg {
-    static constexpr int BT = BT_;           // columns of a tile
+template <bool SPLIT_>
+struct NarrowCfg {
+    static constexpr int BT = 16;            // rows of x of a tile, the MMA's columns
     static constexpr bool SPLIT = SPLIT_;    // a cluster shares one tile, each block part of the inner axis
-    static constexpr int S = STAGES_;
+    static constexpr int S = 5;              // stages: two blocks an SM keep 180 KB of weights in flight
     static constexpr int EW = 4;             // epilogue warps
     static constexpr int THREADS = 32 * (EW + 4);
-    static constexpr int NT = (512 / BT < 4) ? 512 / BT : 4;   // accumulator ring
-    static constexpr int TCOLS = NT * BT < 32 ? 32 : NT * BT;
-    static constexpr int BBYTES = BT * kKB;
-    static constexpr int STAGE = kABytes + BBYTES;
+    static constexpr int NT = 4;             // accumulator ring
+    static constexpr int TCOLS = NT * BT;
+    static constexpr int STAGE = kABytes + BT * kKB;
     static constexpr int SS = 8;             // scale ring
-    static constexpr int LD = BT < 32 ? 16 : 32;        // columns of one tcgen05.ld
     static constexpr int PER_SM = 2;         // blocks an SM holds
     static constexpr size_t SMEM = (size_t)S * STAGE + 1024;
+    // f8f6f4: D f32 at bit 4, A and B e4m3 (0), N / 8 at bit 17, M / 16 at bit 24
     static constexpr uint32_t IDESC = (1u << 4) | ((uint32_t)(BT >> 3) << 17) | ((128u >> 4) << 24);
     static_assert(!SPLIT || (size_t)kARows * BT * 4 <= (size_t)S * STAGE, "partial sums reuse the stage ring");
+    static_assert(PER_SM * (SMEM + 6 * 1024) <= 227 * 1024, "two blocks fit an SM");
 };
 
 constexpr int kMaxExperts = 1024;
@@ -96,7 +96,7 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint3
 // registers are not named before they are filled (a separate wait that names them costs a move each)
 template <int N>
 __device__ __forceinline__ void tc_ld(uint32_t taddr, uint32_t (&r)[N]) {
-    static_assert(N == 16 || N == 32 || N == 64, "columns of a load");
+    static_assert(N == 16 || N == 64, "columns of a load");
     if constexpr (N == 64) {
         asm volatile("tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
                      "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
@@ -112,16 +112,6 @@ __device__ __forceinline__ void tc_ld(uint32_t taddr, uint32_t (&r)[N]) {
                        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
                        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
                        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
-                     : "r"(taddr) : "memory");
-    } else if constexpr (N == 32) {
-        asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
-                     "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-                     "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
-                     "tcgen05.wait::ld.sync.aligned;"
-                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-                       "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-                       "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-                       "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
                      : "r"(taddr) : "memory");
     } else {
         asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
@@ -274,10 +264,10 @@ struct Tile {
 // the blocks that run together share their columns, and the weights stay in L2).
 template <class C>
 struct Walk {
-    const GemmArgs &p;
+    const NarrowArgs &p;
     const int *first;   // shared memory, [E + 1]: column tiles before each expert (matmul with offsets)
     int nat, e;
-    __device__ Walk(const GemmArgs &p_, const int *first_) : p(p_), first(first_), nat((p_.na + kARows - 1) / kARows), e(0) {}
+    __device__ Walk(const NarrowArgs &p_, const int *first_) : p(p_), first(first_), nat((p_.na + kARows - 1) / kARows), e(0) {}
     __device__ __forceinline__ int total() const { return nat * (p.offsets ? first[p.E] : (p.nb + C::BT - 1) / C::BT); }
     __device__ __forceinline__ Tile at(int t) {
         Tile r;
@@ -317,9 +307,9 @@ __device__ __forceinline__ void prefix_tiles(int *first, int E, int lane) {
 }
 
 template <class C>
-__global__ void __launch_bounds__(C::THREADS, C::PER_SM) fp8_gemm_kernel(const __grid_constant__ CUtensorMap amap,
-                                                                 const __grid_constant__ CUtensorMap bmap,
-                                                                 const GemmArgs p) {
+__global__ void __launch_bounds__(C::THREADS, C::PER_SM) fp8_narrow_kernel(const __grid_constant__ CUtensorMap amap,
+                                                                           const __grid_constant__ CUtensorMap bmap,
+                                                                           const NarrowArgs p) {
     extern __shared__ unsigned char smem_raw[];
     __shared__ __align__(8) unsigned long long s_full[C::S], s_empty[C::S];
     __shared__ __align__(8) unsigned long long s_tfull[C::NT], s_tempty[C::NT];
@@ -414,24 +404,17 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) fp8_gemm_kernel(const _
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 const uint32_t sc = smem_u32(&s_scale[s][0]), f = __float_as_uint(s_wscale[s]);
                 const uint64_t ws = pack2(f, f);
-                constexpr int NL = C::BT / C::LD;
+                uint32_t r[C::BT];
+                tc_ld<C::BT>(trow + (uint32_t)(q * C::BT), r);
+                // the accumulator is in registers: the slot may be written again
+                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                if (lane == 0) mbar_arrive(smem_u32(&s_tempty[q]));
 #pragma unroll
-                for (int l = 0; l < NL; l++) {
-                    uint32_t r[C::LD];
-                    tc_ld<C::LD>(trow + (uint32_t)(q * C::BT + l * C::LD), r);
-                    if (l + 1 == NL) {
-                        // the accumulator is in registers: the slot may be written again
-                        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-                        if (lane == 0) mbar_arrive(smem_u32(&s_tempty[q]));
-                    }
-#pragma unroll
-                    for (int i = 0; i < C::LD; i += 4) {
-                        uint64_t s0, s1;
-                        lds_2x64(sc + (uint32_t)(l * C::LD + i) * 4u, s0, s1);
-                        const int o = (l * C::LD + i) / 2;
-                        acc[o] = fma2(pack2(r[i], r[i + 1]), mul2(s0, ws), acc[o]);
-                        acc[o + 1] = fma2(pack2(r[i + 2], r[i + 3]), mul2(s1, ws), acc[o + 1]);
-                    }
+                for (int i = 0; i < C::BT; i += 4) {
+                    uint64_t s0, s1;
+                    lds_2x64(sc + 4u * i, s0, s1);
+                    acc[i / 2] = fma2(pack2(r[i], r[i + 1]), mul2(s0, ws), acc[i / 2]);
+                    acc[i / 2 + 1] = fma2(pack2(r[i + 2], r[i + 3]), mul2(s1, ws), acc[i / 2 + 1]);
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&s_sempty[s]));
@@ -537,12 +520,8 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) fp8_gemm_kernel(const _
                     }
                     s.next();
                     const float *sb = p.sb + (size_t)kb * p.nb;
-#pragma unroll
-                    for (int i = 0; i < (C::BT + 31) / 32; i++) {
-                        const int c = 32 * i + lane;
-                        const bool in = ti.b0 + c < ti.bend;
-                        if (C::BT >= 32 || c < C::BT) cp_async4(smem_u32(&s_scale[q][c]), in ? sb + ti.b0 + c : p.sb, in);
-                    }
+                    const bool in = ti.b0 + lane < ti.bend;
+                    if (lane < C::BT) cp_async4(smem_u32(&s_scale[q][lane]), in ? sb + ti.b0 + lane : p.sb, in);
                     if (lane == 0) cp_async4(smem_u32(&s_wscale[q]), sa + kb, true);
                     cp_async_arrive(smem_u32(&s_sfull[q]));
                 }
@@ -560,8 +539,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) fp8_gemm_kernel(const _
     }
     if (C::SPLIT) {
         // sums of all blocks of the cluster, in block order: block r adds columns r, r + csize, ...;
-        // every block's value of a column in flight at once (one after the other, eight blocks' partial
-        // sums of 64 columns took 3 us)
+        // every block's value of a column in flight at once
         cluster_sync_all();
         uint32_t zero = 0;
         if (t0 < total) {
@@ -592,17 +570,26 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) fp8_gemm_kernel(const _
 }
 
 // ---------------------------------------------------------------------------
-// Wide tiles: lanes are the rows of the output, columns its contiguous elements, 128 (PAIR: 256)
-// x 256.  PAIR: a cluster of two blocks shares a tile (cta_group::2: one MMA of M 256 over both
-// SMs' tensor cores), each block copying its own 128 rows of A and half of B: 32 KB for
-// 128 x 256 x 128 products instead of 48 KB, which is what an SM's path from L2 can carry at the
-// tensor cores' e4m3 rate (512 cycles a stage x 64 bytes).
-//   matmul  A = x (lanes: rows r), B = w (columns n): a lane's scale is one number per block and
-//           128 columns, so adding a block's product costs one two-wide fma per two elements.
-//   wgrad   (MX) A = dy, B = x, both column-quantised.  Their scales are powers of two, so the
-//           tensor core applies them itself (kind::mxf8f6f4, the float32's exponent byte is the
-//           ue8m0 scale) and the sums stay in tensor memory over the whole inner range: the
-//           registers see each output once.
+// Wide tiles: lanes are the rows of the output, columns its contiguous elements.  PAIR: a cluster of
+// two blocks shares a tile of 256 x 256 (cta_group::2: one MMA of M 256 over both SMs' tensor cores),
+// each block copying its own 128 rows of A and half of B: 32 KB for 128 x 256 x 128 products instead
+// of 48 KB, which is what an SM's path from L2 carries at the tensor cores' e4m3 rate (512 cycles a
+// stage x 64 bytes).
+//   matmul  A = x (lanes: rows r), B = w (columns n): a lane's scale is one number per block and 128
+//           columns, so adding a block's product costs one two-wide fma per two elements.  Bound by
+//           that: MMAs into one of two accumulators (512 cycles), the commit's way to the epilogue
+//           warps (~280), their 2 x 64 columns out of tensor memory and into the sums (~380), the
+//           release's way back (~400; from the other block through its shared memory) make ~840 cycles
+//           a stage where the tensor cores need 512: 16381 x 4096 x 6144 278 us, 2.97 PFLOP/s.
+//           Measured and not kept: accumulators of 128 columns (298-359 us: twice the waits), 32-column
+//           loads, pipelined or not (420-444 us: each costs its latency), 16 warps (no registers).
+//   wgrad   (MX) A = dy, B = x, both column-quantised.  Their scales are powers of two, so the tensor
+//           core applies them itself (kind::mxf8f6f4; the float32's exponent byte is the ue8m0 scale)
+//           and sums stay in tensor memory for kFlush blocks: 273 ns a stage, the tensor cores' rate
+//           (3.4 PFLOP/s on 2048 x 2048 from 65536 rows).  64 experts' 2048 x 2048 float32 outputs:
+//           273 us, bound by memory traffic (1.07 GB of stores alone take 188 us in this pattern, a
+//           fill 143 us); prefetching operands, mixing experts' tiles, streaming stores, 4 or 6 stages:
+//           no gain or slower.
 // ---------------------------------------------------------------------------
 
 template <bool PAIR_, bool MX_, int BN_ = 256, bool SPLIT_ = false>
@@ -619,12 +606,12 @@ struct WideCfg {
     static constexpr int THREADS = 32 * (EW + 4);
     static constexpr bool BIGREG = WC > 64;
     static constexpr int SS = 8;                              // scale ring (matmul)
-    static constexpr int SFBYTES = 512 + 4 * BN;              // staged scales of a stage (MX): 128 + BN words
-    static constexpr int SFCOLS = 4 + BN / 32;                // their tensor-memory columns
+    [[maybe_unused]] static constexpr int SFBYTES = 512 + 4 * BN;              // staged scales of a stage (MX): 128 + BN words
+    [[maybe_unused]] static constexpr int SFCOLS = 4 + BN / 32;                // their tensor-memory columns
     static constexpr int OUTB = 4096;                         // staging of an epilogue warp: 32 rows x 128 bytes
     static constexpr int NT = MX ? 2 : 512 / BN;              // accumulators: of tiles (MX), of stages
-    static constexpr int ACC1 = MX && 2 * BN + SFCOLS * S > 512 ? 512 - SFCOLS * S - BN : BN;   // from one to the next (MX: may overlap)
-    static constexpr int PLD = BN + 4;                        // floats of a row of partial sums (SPLIT)
+    [[maybe_unused]] static constexpr int ACC1 = MX && 2 * BN + SFCOLS * S > 512 ? 512 - SFCOLS * S - BN : BN;   // from one to the next (MX: may overlap)
+    [[maybe_unused]] static constexpr int PLD = BN + 4;                        // floats of a row of partial sums (SPLIT)
     static constexpr size_t SMEM = 1024 + (size_t)S * STAGE + EW * OUTB + (MX ? S * SFBYTES : 0);
     // f8f6f4: D f32 at bit 4; mxf8f6f4: ue8m0 scales at bit 23
     static constexpr uint32_t IDESC = (MX ? 1u << 23 : 1u << 4) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(ROWS >> 4) << 24);
@@ -1673,15 +1660,15 @@ cudaError_t error_word(unsigned **err) {
 
 // grid: blocks (of clusters of `cluster`); the B map's box is the tile's columns
 template <class C>
-cudaError_t launch_gemm(const GemmArgs &p, const CUtensorMap &am, const uint8_t *b, uint64_t b_cols, uint64_t b_rows,
+cudaError_t launch_narrow(const NarrowArgs &p, const CUtensorMap &am, const uint8_t *b, uint64_t b_cols, uint64_t b_rows,
                         long long tiles, int per_sm, int cluster, cudaStream_t st) {
     CUtensorMap bm;
     if (!tmap(&bm, 2, b, b_cols, b_rows, 1, C::BT)) return cudaErrorInvalidValue;
-    const cudaError_t e = allow_smem<fp8_gemm_kernel<C>>(C::SMEM);
+    const cudaError_t e = allow_smem<fp8_narrow_kernel<C>>(C::SMEM);
     if (e != cudaSuccess) return e;
     const long long most = (long long)sm_count() * per_sm;
     const dim3 grid((unsigned)(C::SPLIT ? tiles * cluster : (tiles < most ? tiles : most)));
-    return launch_early(fp8_gemm_kernel<C>, grid, C::THREADS, C::SMEM, st, C::SPLIT ? (unsigned)cluster : 1u, am, bm, p);
+    return launch_early(fp8_narrow_kernel<C>, grid, C::THREADS, C::SMEM, st, C::SPLIT ? (unsigned)cluster : 1u, am, bm, p);
 }
 
 template <class C>
@@ -1706,7 +1693,7 @@ bool rows_aligned(const void *out, long long ldo, int dtype) {
 cudaError_t launch_fp8_matmul(const uint8_t *x, const float *xs, int R, const uint8_t *w, const float *ws, int E, int N, int K,
                               const int *offsets, void *y, int y_dtype, long long ldy, cudaStream_t st) {
     if (!tmap_encoder()) return cudaErrorNotSupported;
-    GemmArgs p = {};
+    NarrowArgs p = {};
     p.sa = ws;
     p.sb = xs;
     p.offsets = offsets;
@@ -1730,8 +1717,8 @@ cudaError_t launch_fp8_matmul(const uint8_t *x, const float *xs, int R, const ui
         const long long most = nat * (offsets ? (long long)R / 16 + used : ((long long)R + 15) / 16);
         int cs = (int)kMaxSplit;
         while (cs > 1 && (cs > p.nkb || most * cs > 2ll * sm_count())) cs /= 2;
-        if (cs > 1) return launch_gemm<Cfg<16, true, 5>>(p, am, x, K, R, most, 2, cs, st);
-        return launch_gemm<Cfg<16, false, 5>>(p, am, x, K, R, most, 2, 1, st);
+        if (cs > 1) return launch_narrow<NarrowCfg<true>>(p, am, x, K, R, most, 2, cs, st);
+        return launch_narrow<NarrowCfg<false>>(p, am, x, K, R, most, 2, 1, st);
     }
     WideArgs q = {};
     q.sa = xs;

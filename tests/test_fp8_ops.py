@@ -582,3 +582,36 @@ def test_explicit_stream_argument(gpu):
         y = gpu.moe_fp8_matmul(x, xs, w[0], ws[0], stream=h)
         torch.cuda.synchronize()
         assert torch.equal(y, want)
+
+
+@pytest.mark.gpu
+def test_first_calls_of_a_process_may_be_captured(gpu):
+    """Nothing that a first call sets up (kernels' shared memory, the error word, the encoder of tensor
+    maps) breaks a capture: a fresh process whose first calls are captured gets the same results."""
+    import subprocess
+    import sys
+    from pathlib import Path
+    code = """
+import torch, int4_moe_expert_gb300 as moe
+torch.manual_seed(0)
+x = torch.randn(300, 256, device="cuda"); w = torch.randn(3, 264, 256, device="cuda")
+idx = torch.randint(0, 3, (300, 2), dtype=torch.int32, device="cuda"); logits = torch.randn(300, 3, device="cuda")
+torch.cuda.synchronize()
+def step():
+    c, off, rows, pos = moe.moe_expert_lists(idx, 3, 128)
+    loss, n, s, t = moe.moe_balance_forward(logits, idx, 1.0)
+    q, qs, qt, qts = moe.moe_fp8_quantize(x, rows=rows, transposed=True)
+    few = moe.moe_fp8_quantize(x[:4])
+    wq, ws, wt, wts = moe.moe_fp8_quantize_weights(w, transposed=True)
+    y = moe.moe_fp8_matmul(q, qs, wq, ws, offsets=off, out=torch.zeros(rows.numel(), 264, device="cuda"))
+    z = moe.moe_fp8_matmul(few[0], few[1], wq[0], ws[0])
+    return [c, off, rows, pos, loss, moe.moe_balance_backward(logits, 2, n, t, 1.0), y, z, moe.moe_fp8_wgrad(qt, qts, qt, qts, offsets=off)]
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = step()
+g.replay(); torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, step()))
+print("captured")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=Path(__file__).resolve().parents[1], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
