@@ -374,7 +374,8 @@ moe_status moe_route_noalloc(const moe_config *cfg, const float *router_w, const
  * current CUDA device, and nothing is allocated.  A call launches on `stream`
  * and returns without waiting; it may be captured in a CUDA graph.  Calls may
  * overlap as long as they do not share an output or a workspace.  Results are
- * bit-identical from run to run.  Outputs must not overlap inputs.  A size of
+ * bit-identical from run to run (a product's row may differ in its last float32
+ * bits with the number of rows in the call: the order of the sums goes by it).  Outputs must not overlap inputs.  A size of
  * zero tokens or rows is valid.  Errors: MOE_ERR_INVALID for NULL or
  * misaligned pointers, bad enumerators and sizes that contradict each other;
  * MOE_ERR_UNSUPPORTED for sizes outside the stated limits; MOE_ERR_CUDA when a

@@ -405,6 +405,11 @@ __global__ void __launch_bounds__(kBalThreads) balance_part_kernel(const BalArgs
         for (int e = tid; e < p.E; e += kBalThreads) cnt[e] = 0;
         if (tid == 0) s_n = 0;
         __syncthreads();
+        const long long i0 = (long long)a * p.K, i1 = (long long)b * p.K;
+        for (long long i = i0 + tid; i < i1; i += kBalThreads) {
+            const int e = __ldg(p.idx + i);
+            if ((unsigned)e < (unsigned)p.E && (!p.mask || p.mask[i / p.K])) atomicAdd(&cnt[e], 1);
+        }
         float sum[J];
 #pragma unroll
         for (int j = 0; j < J; j++) sum[j] = 0.0f;
@@ -426,11 +431,6 @@ __global__ void __launch_bounds__(kBalThreads) balance_part_kernel(const BalArgs
                 for (int j = 0; j < J; j++) sum[j] += pr[j];
                 n += on[u] ? 1 : 0;
             }
-        }
-        const long long i0 = (long long)a * p.K, i1 = (long long)b * p.K;
-        for (long long i = i0 + tid; i < i1; i += kBalThreads) {
-            const int e = __ldg(p.idx + i);
-            if ((unsigned)e < (unsigned)p.E && (!p.mask || p.mask[i / p.K])) atomicAdd(&cnt[e], 1);
         }
 #pragma unroll
         for (int j = 0; j < J; j++)

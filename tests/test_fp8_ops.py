@@ -585,6 +585,32 @@ def test_explicit_stream_argument(gpu):
 
 
 @pytest.mark.gpu
+def test_more_than_two_to_the_31_elements(gpu):
+    """Rows whose elements lie beyond 2^31 of x, of the codes, of the transposed codes and of y: the last
+    rows of a long call are those of a short one."""
+    R, width, N = 1_100_032, 2048, 2048
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.empty(R, width, dtype=torch.bfloat16, device="cuda")
+    x[:-512] = 1.0
+    x[-512:] = torch.randn(512, width, generator=g, device="cuda").bfloat16()
+    w = gpu.moe_fp8_quantize_weights(0.02 * torch.randn(N, width, generator=g, device="cuda"))
+    c, s, ct, st = gpu.moe_fp8_quantize(x, transposed=True)
+    c1, s1 = gpu.moe_fp8_quantize(x)
+    c2, s2, ct2, st2 = gpu.moe_fp8_quantize(x[-512:].contiguous(), transposed=True)
+    for a, b in ((c[-512:], c2), (c1[-512:], c2), (ct[:, -512:], ct2)):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    assert torch.equal(s[:, -512:], s2) and torch.equal(s1[:, -512:], s2) and torch.equal(st[-4:], st2)
+    del x, c1, ct
+    y = gpu.moe_fp8_matmul(c, s, *w)
+    # against 64 bits (a short call may add the blocks up in another order)
+    ref, size = matmul_ref(c2.cpu(), s2.cpu(), w[0].cpu()[None], w[1].cpu()[None], [0, 512])
+    close(y[-512:], ref, size, width, torch.bfloat16)
+    assert bool((y[1000] == y[R - 600]).all())
+
+
+@pytest.mark.gpu
 def test_first_calls_of_a_process_may_be_captured(gpu):
     """Nothing that a first call sets up (kernels' shared memory, the error word, the encoder of tensor
     maps) breaks a capture: a fresh process whose first calls are captured gets the same results."""

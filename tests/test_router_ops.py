@@ -324,6 +324,27 @@ def test_balance_no_tokens(gpu):
 
 
 @pytest.mark.gpu
+def test_balance_more_than_two_to_the_31_elements(gpu):
+    """The last sequence of a call whose logits pass 2^31 elements: as in a call of its own."""
+    T, E, last = 2_200_000, 1024, 300
+    if torch.cuda.mem_get_info()[0] < 30 << 30:
+        pytest.skip("needs 30 GB")
+    x = torch.zeros(T, E, dtype=torch.bfloat16, device="cuda")
+    tail, idx = router(last, E, 2, 13, torch.bfloat16)
+    x[-last:] = tail.cuda()
+    full = torch.zeros(T, 2, dtype=torch.int32, device="cuda")
+    full[-last:] = idx.cuda()
+    seq = torch.tensor([0, T - last, T], dtype=torch.int32, device="cuda")
+    _, counts, sums, tokens = gpu.moe_balance_forward(x, full, 2.0, seq_offsets=seq)
+    _, c1, s1, t1 = gpu.moe_balance_forward(tail.cuda(), idx.cuda(), 1.0)
+    assert torch.equal(counts[1], c1[0]) and tokens.tolist() == [T - last, last] and counts[0, 0] == 2 * (T - last)
+    assert bool(((sums[1] - s1[0]).abs() <= 2.0 ** -18 * s1[0]).all())
+    d = gpu.moe_balance_backward(x, 2, counts, tokens, 2.0, seq_offsets=seq)
+    want = gpu.moe_balance_backward(tail.cuda(), 2, c1, t1, 1.0)
+    assert torch.equal(d[-last:], want)
+
+
+@pytest.mark.gpu
 def test_balance_refuses_in_the_binding(gpu):
     x, idx = torch.zeros(4, 8, device="cuda"), torch.zeros(4, 2, dtype=torch.int32, device="cuda")
     seq = torch.tensor([0, 4], dtype=torch.int32, device="cuda")
