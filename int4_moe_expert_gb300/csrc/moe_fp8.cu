@@ -1156,7 +1156,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
 #pragma unroll
                 for (int i = 0; i < NV; i++) {
                     const int r = (i < 4 ? ti.r0 : ti.c0 - 128) + 32 * i + lane;
-                    d[i] = r < (i < 4 ? p.na : p.nb) ? __ldg(i < 4 ? p.sa + (size_t)kb * p.na + r : p.sb + (size_t)kb * p.nb + r) : 0.0f;
+                    d[i] = r < (i < 4 ? p.na : p.nb) ? load_in(i < 4 ? p.sa + (size_t)kb * p.na + r : p.sb + (size_t)kb * p.nb + r) : 0.0f;
                 }
                 mine += 2;
                 n++;
@@ -1262,16 +1262,16 @@ constexpr int kQThreads = 256;
 template <typename T>
 __device__ __forceinline__ float4 load4(const T *p);
 template <>
-__device__ __forceinline__ float4 load4<float>(const float *p) { return __ldg(reinterpret_cast<const float4 *>(p)); }
+__device__ __forceinline__ float4 load4<float>(const float *p) { return load_in(reinterpret_cast<const float4 *>(p)); }
 template <>
 __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16 *p) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
+    const uint2 v = load_in(reinterpret_cast<const uint2 *>(p));
     return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
                        __uint_as_float(v.y & 0xFFFF0000u));
 }
 template <>
 __device__ __forceinline__ float4 load4<__half>(const __half *p) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
+    const uint2 v = load_in(reinterpret_cast<const uint2 *>(p));
     const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&v.x)), b = __half22float2(*reinterpret_cast<const __half2 *>(&v.y));
     return make_float4(a.x, a.y, b.x, b.y);
 }
@@ -1305,7 +1305,7 @@ __device__ __forceinline__ uint32_t codes4(float4 v, float inv) {
 __device__ __forceinline__ int src_row(const int *rows, int r, int R, int n_src) {
     if (r >= R) return -1;
     if (!rows) return r;
-    const int s = __ldg(rows + r);
+    const int s = load_in(rows + r);
     return (s >= 0 && s < n_src) ? s : -1;
 }
 
@@ -1365,7 +1365,7 @@ struct Oct {
     __device__ __forceinline__ void load(const T *p) {
 #pragma unroll
         for (int i = 0; i < W; i += 4) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p) + i / 4);
+            const uint4 v = load_in(reinterpret_cast<const uint4 *>(p) + i / 4);
             w[i] = v.x;
             w[i + 1] = v.y;
             w[i + 2] = v.z;

@@ -172,6 +172,10 @@ cudaError_t launch_early(void (*kernel)(P...), dim3 grid, unsigned threads, size
 }
 #ifdef __CUDACC__
 __device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// A load of what the kernel before may have written: not __ldg, whose read-only path promises that
+// nobody writes while this kernel runs, and an early one runs while its inputs are still being made.
+template <typename T>
+__device__ __forceinline__ T load_in(const T *p) { return *p; }
 #endif
 
 // Token lists and the balance loss (moe_route_ops.cu).

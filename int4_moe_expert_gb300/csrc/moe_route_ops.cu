@@ -36,7 +36,7 @@ struct ListArgs {
 };
 
 __device__ __forceinline__ int pair_expert(const ListArgs &p, long long i, long long end) {
-    const int e = i < end ? __ldg(p.idx + i) : -1;
+    const int e = i < end ? load_in(p.idx + i) : -1;
     return (unsigned)e < (unsigned)p.E ? e : -1;
 }
 
@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kListThreads, 1) lists_kernel(const ListArgs p
             int4 b4 = make_int4(0, 0, 0, 0), all = b4;
 #pragma unroll 8
             for (int b = g; b < p.blocks; b += groups) {
-                const int4 v = __ldg(reinterpret_cast<const int4 *>(p.hist + (size_t)b * p.E) + q);
+                const int4 v = load_in(reinterpret_cast<const int4 *>(p.hist + (size_t)b * p.E) + q);
                 all = make_int4(all.x + v.x, all.y + v.y, all.z + v.z, all.w + v.w);
                 if (b < (int)blockIdx.x) b4 = make_int4(b4.x + v.x, b4.y + v.y, b4.z + v.z, b4.w + v.w);
             }
@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kListThreads, 1) lists_kernel(const ListArgs p
             int b4 = 0, all = 0;
 #pragma unroll 16
             for (int b = g; b < p.blocks; b += groups) {
-                const int v = __ldg(p.hist + (size_t)b * p.E + e);
+                const int v = load_in(p.hist + (size_t)b * p.E + e);
                 all += v;
                 b4 += b < (int)blockIdx.x ? v : 0;
             }
@@ -240,13 +240,13 @@ struct BalArgs {
 template <typename T>
 __device__ __forceinline__ float ld1(const T *p);
 template <>
-__device__ __forceinline__ float ld1<float>(const float *p) { return __ldg(p); }
+__device__ __forceinline__ float ld1<float>(const float *p) { return load_in(p); }
 template <>
 __device__ __forceinline__ float ld1<__nv_bfloat16>(const __nv_bfloat16 *p) {
-    return __uint_as_float((uint32_t)__ldg(reinterpret_cast<const unsigned short *>(p)) << 16);
+    return __uint_as_float((uint32_t)load_in(reinterpret_cast<const unsigned short *>(p)) << 16);
 }
 template <>
-__device__ __forceinline__ float ld1<__half>(const __half *p) { return __half2float(__ldg(p)); }
+__device__ __forceinline__ float ld1<__half>(const __half *p) { return __half2float(load_in(p)); }
 template <typename T>
 __device__ __forceinline__ T cast1(float v);
 template <>
@@ -257,21 +257,21 @@ template <>
 __device__ __forceinline__ __half cast1<__half>(float v) { return __float2half_rn(v); }
 // four neighbours
 __device__ __forceinline__ void ld4(const float *p, float *v) {
-    const float4 f = __ldg(reinterpret_cast<const float4 *>(p));
+    const float4 f = load_in(reinterpret_cast<const float4 *>(p));
     v[0] = f.x;
     v[1] = f.y;
     v[2] = f.z;
     v[3] = f.w;
 }
 __device__ __forceinline__ void ld4(const __nv_bfloat16 *p, float *v) {
-    const uint2 f = __ldg(reinterpret_cast<const uint2 *>(p));
+    const uint2 f = load_in(reinterpret_cast<const uint2 *>(p));
     v[0] = __uint_as_float(f.x << 16);
     v[1] = __uint_as_float(f.x & 0xFFFF0000u);
     v[2] = __uint_as_float(f.y << 16);
     v[3] = __uint_as_float(f.y & 0xFFFF0000u);
 }
 __device__ __forceinline__ void ld4(const __half *p, float *v) {
-    const uint2 f = __ldg(reinterpret_cast<const uint2 *>(p));
+    const uint2 f = load_in(reinterpret_cast<const uint2 *>(p));
     const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&f.x)), b = __half22float2(*reinterpret_cast<const __half2 *>(&f.y));
     v[0] = a.x;
     v[1] = a.y;
@@ -338,10 +338,10 @@ struct Segs {
     // all threads of the block; ends with a barrier
     __device__ __forceinline__ Segs(const BalArgs &p, int *buf) : g(p.seq), sm(p.seq && p.S < kSegs ? buf : nullptr), T(p.T), S(p.S) {
         if (sm)
-            for (int i = threadIdx.x; i <= S; i += blockDim.x) buf[i] = min(max(__ldg(g + i), 0), T);
+            for (int i = threadIdx.x; i <= S; i += blockDim.x) buf[i] = min(max(load_in(g + i), 0), T);
         __syncthreads();
     }
-    __device__ __forceinline__ int at(int s) const { return sm ? sm[s] : g ? min(max(__ldg(g + s), 0), T) : (s ? T : 0); }
+    __device__ __forceinline__ int at(int s) const { return sm ? sm[s] : g ? min(max(load_in(g + s), 0), T) : (s ? T : 0); }
     // first segment that ends after token t (S when none does)
     __device__ __forceinline__ int of(int t) const {
         int lo = 0, hi = S;
@@ -405,10 +405,19 @@ __global__ void __launch_bounds__(kBalThreads) balance_part_kernel(const BalArgs
         for (int e = tid; e < p.E; e += kBalThreads) cnt[e] = 0;
         if (tid == 0) s_n = 0;
         __syncthreads();
-        const long long i0 = (long long)a * p.K, i1 = (long long)b * p.K;
-        for (long long i = i0 + tid; i < i1; i += kBalThreads) {
-            const int e = __ldg(p.idx + i);
-            if ((unsigned)e < (unsigned)p.E && (!p.mask || p.mask[i / p.K])) atomicAdd(&cnt[e], 1);
+        const int *idx = p.idx + (long long)a * p.K;
+        const int n_idx = (b - a) * p.K;                         // at most 128 tokens' choices
+        constexpr int UI = 4;                                    // choices in flight
+        for (int i = tid; i < n_idx; i += UI * kBalThreads) {
+            int e[UI];
+#pragma unroll
+            for (int u = 0; u < UI; u++) {
+                const int k = i + u * kBalThreads;
+                e[u] = k < n_idx && (!p.mask || load_in(p.mask + a + k / p.K)) ? load_in(idx + k) : -1;
+            }
+#pragma unroll
+            for (int u = 0; u < UI; u++)
+                if ((unsigned)e[u] < (unsigned)p.E) atomicAdd(&cnt[e[u]], 1);
         }
         float sum[J];
 #pragma unroll
@@ -461,7 +470,7 @@ __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(const BalArgs 
     wait_for_stream();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int s = (int)blockIdx.y, g = (int)blockIdx.x, G = (int)gridDim.x, e = kSumE * g + tid % kSumE;
-    const int a = p.seq ? min(max(__ldg(p.seq + s), 0), p.T) : 0, b = p.seq ? min(max(__ldg(p.seq + s + 1), 0), p.T) : p.T;
+    const int a = p.seq ? min(max(load_in(p.seq + s), 0), p.T) : 0, b = p.seq ? min(max(load_in(p.seq + s + 1), 0), p.T) : p.T;
     float sum = 0.0f;
     int cnt = 0, tok = 0;
     if (b > a) {
@@ -469,7 +478,7 @@ __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(const BalArgs 
         if (e < p.E) {
 #pragma unroll 8
             for (int k = b0 + tid / kSumE; k <= b1; k += STRANDS) {
-                const int2 v = __ldg(p.part + ((size_t)k + s) * p.E + e);
+                const int2 v = load_in(p.part + ((size_t)k + s) * p.E + e);
                 sum += __int_as_float(v.x);
                 cnt += v.y;
             }
@@ -542,14 +551,14 @@ __global__ void __launch_bounds__(kBalThreads) balance_grad_kernel(const BalArgs
     const int ta = ((int)blockIdx.x * kBalWarps + warp) * each, tb = min(ta + each, p.T);
     const typename L::T *logits = static_cast<const typename L::T *>(p.logits);
     typename L::T *out = static_cast<typename L::T *>(p.dlogits);
-    const float g = (p.grad ? __ldg(p.grad) : 1.0f) * p.scale;
+    const float g = (p.grad ? load_in(p.grad) : 1.0f) * p.scale;
     for (int s = ta < tb ? seg.of(ta) : p.S; s < p.S && seg.at(s) < tb; s++) {
         const int a = max(seg.at(s), ta), b = min(seg.at(s + 1), tb);
         if (a >= b) continue;
-        const float n = (float)max(__ldg(p.tokens + s), 1), up = g / n / n;
+        const float n = (float)max(load_in(p.tokens + s), 1), up = g / n / n;
         float c[J];
 #pragma unroll
-        for (int j = 0; j < J; j++) c[j] = L::expert(l, j) < p.E ? (float)__ldg(p.counts + (size_t)s * p.E + L::expert(l, j)) : 0.0f;
+        for (int j = 0; j < J; j++) c[j] = L::expert(l, j) < p.E ? (float)load_in(p.counts + (size_t)s * p.E + L::expert(l, j)) : 0.0f;
         for (int t = a; t < b; t += U * G) {
             float x[U][J];
             bool on[U];
