@@ -580,7 +580,10 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) fp8_narrow_kernel(const
 //           that: MMAs into one of two accumulators (512 cycles), the commit's way to the epilogue
 //           warps (~280), their 2 x 64 columns out of tensor memory and into the sums (~380), the
 //           release's way back (~400; from the other block through its shared memory) make ~840 cycles
-//           a stage where the tensor cores need 512: 16381 x 4096 x 6144 278 us, 2.97 PFLOP/s.
+//           a stage where the tensor cores need 512: 16381 x 4096 x 6144 273-276 us, 3.0 PFLOP/s.
+//           A pair's full warps store by tensor copies, so that the next tile's sums do not wait for
+//           the stores (with two more staging buffers and a stage less, against the others' path: 275
+//           and 278 us; 65536 x 2048 x 2048 200 and 213 us; 64 experts of it 250 and 250 us).
 //           Measured and not kept: accumulators of 128 columns (298-359 us: twice the waits), 32-column
 //           loads, pipelined or not (420-444 us: each costs its latency), 16 warps (no registers).
 //   wgrad   (MX) A = dy, B = x, both column-quantised.  Their scales are powers of two, so the tensor
@@ -600,7 +603,8 @@ struct WideCfg {
     static constexpr int ROWS = PAIR ? 256 : 128;             // rows of a tile
     static constexpr int BROWS = PAIR ? BN / 2 : BN;          // rows of B that one block copies
     static constexpr int STAGE = kABytes + BROWS * kKB;
-    static constexpr int S = STAGE > 32768 ? 3 : 5;
+    static constexpr int S = STAGE > 32768 ? 3 : (PAIR && !MX) ? 4 : 5;
+    static constexpr bool TST = PAIR && !MX;                  // full warps store by tensor copies
     static constexpr int EW = 8;                              // epilogue warps: a lane quarter, half of the columns each
     static constexpr int WC = BN / 2;
     static constexpr int THREADS = 32 * (EW + 4);
@@ -608,7 +612,7 @@ struct WideCfg {
     static constexpr int SS = 8;                              // scale ring (matmul)
     [[maybe_unused]] static constexpr int SFBYTES = 512 + 4 * BN;              // staged scales of a stage (MX): 128 + BN words
     [[maybe_unused]] static constexpr int SFCOLS = 4 + BN / 32;                // their tensor-memory columns
-    static constexpr int OUTB = 4096;                         // staging of an epilogue warp: 32 rows x 128 bytes
+    static constexpr int OUTB = TST ? 8192 : 4096;            // staging of an epilogue warp: (two times) 32 rows x 128 bytes
     static constexpr int NT = MX ? 2 : 512 / BN;              // accumulators: of tiles (MX), of stages
     [[maybe_unused]] static constexpr int ACC1 = MX && 2 * BN + SFCOLS * S > 512 ? 512 - SFCOLS * S - BN : BN;   // from one to the next (MX: may overlap)
     [[maybe_unused]] static constexpr int PLD = BN + 4;                        // floats of a row of partial sums (SPLIT)
@@ -687,7 +691,8 @@ struct WideArgs {
     const int *offsets;     // [E + 1] or NULL
     void *out;
     long long ldo, out_stride;
-    int na, nb, nkb, E, out_dtype, vec;   // vec: every output row starts on a 16-byte boundary
+    int na, nb, nkb, E, out_dtype;
+    int vec;                              // every output row starts on a 16-byte boundary (2: and the tensor copies can take it)
     unsigned *err;
 };
 
@@ -826,10 +831,52 @@ __device__ __forceinline__ void partial_64(const uint64_t *v, uint32_t at) {
     for (int i = 0; i < 32; i += 2) asm volatile("st.shared.v2.b64 [%0], {%1, %2};" ::"r"(at + 8u * i), "l"(v[i]), "l"(v[i + 1]) : "memory");
 }
 
+// A warp's full 32 rows x 128 columns from row `row`, column c0 on, by tensor copies from two staged
+// chunks of 32 x 128 bytes (the copy's swizzle is store_chunk's permutation).  All of them inside the
+// matrix: at its edge a copy writes whole 16-byte pieces, past a width that does not end with one.
+// The registers are free once the chunks are staged.
+template <typename T>
+__device__ __forceinline__ void store_async(const uint64_t (&v)[64], uint32_t stage, const void *map, int row, int c0, int lane) {
+    constexpr int PER = 128 / (int)sizeof(T), NCH = 128 / PER;      // columns of a chunk, chunks
+#pragma unroll
+    for (int c = 0; c < NCH; c++) {
+        if (c % 2 == 0) {      // both buffers have been read
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            __syncwarp();
+        }
+        const uint32_t buf = stage + (uint32_t)((c & 1) * 4096);
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            uint32_t w[4];
+            if constexpr (sizeof(T) == 4) {
+                float f[4];
+                unpack2(v[c * 16 + 2 * i], f[0], f[1]);
+                unpack2(v[c * 16 + 2 * i + 1], f[2], f[3]);
+#pragma unroll
+                for (int k = 0; k < 4; k++) w[k] = __float_as_uint(f[k]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; k++) {
+                    float a, b;
+                    unpack2(v[c * 32 + 4 * i + k], a, b);
+                    w[k] = pack16<T>(a, b);
+                }
+            }
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + (uint32_t)(lane * 128 + ((i ^ (lane & 7)) << 4))), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+            asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(c0 + c * PER), "r"(row), "r"(buf) : "memory");
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+    }
+}
+
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_constant__ CUtensorMap amap,
                                                                  const __grid_constant__ CUtensorMap bmap,
-                                                                 const WideArgs p) {
+                                                                 const __grid_constant__ CUtensorMap omap, const WideArgs p) {
     extern __shared__ unsigned char smem_raw[];
     __shared__ __align__(8) unsigned long long s_full[C::S], s_empty[C::S];
     __shared__ __align__(8) unsigned long long s_tfull[C::NT], s_tempty[C::NT];
@@ -989,12 +1036,23 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
                 if constexpr (C::SPLIT) {
                     // partial sums [row][column] over the stage ring: every copy into it was consumed
                     partial_64(acc, ring + (uint32_t)((32 * q4 + lane) * C::PLD + C::WC * half) * 4u);
+                } else if (C::TST && p.vec == 2 && rows >= 32 && cols >= 128) {
+                    if constexpr (C::TST) {
+                        if (p.out_dtype == MOE_DTYPE_F32) store_async<float>(acc, stage, &omap, row, c0, lane);
+                        else if (p.out_dtype == MOE_DTYPE_BF16) store_async<__nv_bfloat16>(acc, stage, &omap, row, c0, lane);
+                        else store_async<__half>(acc, stage, &omap, row, c0, lane);
+                    }
                 } else if (rows > 0) {
+                    if constexpr (C::TST) {      // an earlier tile's copies may still read the staging
+                        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                        __syncwarp();
+                    }
 #pragma unroll
                     for (int l = 0; l < C::WC / 64; l++) store_cols(acc + 32 * l, stage, p, at + 64 * l, rows, cols - 64 * l, lane);
                 }
             }
         }
+        if (C::TST && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     } else {
         if constexpr (C::BIGREG) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == C::EW) {
@@ -1671,8 +1729,21 @@ cudaError_t launch_narrow(const NarrowArgs &p, const CUtensorMap &am, const uint
     return launch_early(fp8_narrow_kernel<C>, grid, C::THREADS, C::SMEM, st, C::SPLIT ? (unsigned)cluster : 1u, am, bm, p);
 }
 
+// y [nb columns, na rows] as boxes of 128 bytes x 32 rows for the stores; rows on 16-byte boundaries
+// (no: a stride that the tensor copies cannot take)
+bool out_tmap(CUtensorMap *m, const WideArgs &p) {
+    const int el = p.out_dtype == MOE_DTYPE_F32 ? 4 : 2;
+    const cuuint64_t dims[2] = {(cuuint64_t)p.nb, (cuuint64_t)p.na}, strides[1] = {(cuuint64_t)p.ldo * el};
+    const cuuint32_t box[2] = {(cuuint32_t)(128 / el), 32}, es[2] = {1, 1};
+    const CUtensorMapDataType type = p.out_dtype == MOE_DTYPE_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                     : p.out_dtype == MOE_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    std::memset(m, 0, sizeof(*m));
+    return tmap_encoder()(m, type, 2, p.out, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <class C>
-cudaError_t launch_wide(const WideArgs &p, const uint8_t *a, uint64_t a_cols, const uint8_t *b, uint64_t b_cols, uint64_t b_mats,
+cudaError_t launch_wide(WideArgs p, const uint8_t *a, uint64_t a_cols, const uint8_t *b, uint64_t b_cols, uint64_t b_mats,
                         long long tiles, int cluster, cudaStream_t st) {
     CUtensorMap am, bm;
     if (!tmap(&am, 3, a, a_cols, p.na, 1, 128) || !tmap(&bm, 3, b, b_cols, p.nb, b_mats, C::BROWS)) return cudaErrorInvalidValue;
@@ -1680,7 +1751,9 @@ cudaError_t launch_wide(const WideArgs &p, const uint8_t *a, uint64_t a_cols, co
     if (e != cudaSuccess) return e;
     const long long nb = C::PAIR ? 2 : 1, most = sm_count() / nb;
     const long long blocks = C::SPLIT ? tiles * cluster : nb * (tiles < most ? tiles : most);
-    return launch_early(fp8_wide_kernel<C>, dim3((unsigned)blocks), C::THREADS, C::SMEM, st, (unsigned)(C::SPLIT ? cluster : nb), am, bm, p);
+    CUtensorMap om = {};
+    if (C::TST && p.vec && out_tmap(&om, p)) p.vec = 2;
+    return launch_early(fp8_wide_kernel<C>, dim3((unsigned)blocks), C::THREADS, C::SMEM, st, (unsigned)(C::SPLIT ? cluster : nb), am, bm, om, p);
 }
 
 bool rows_aligned(const void *out, long long ldo, int dtype) {

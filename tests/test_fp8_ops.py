@@ -311,6 +311,16 @@ def test_matmul_into_strided_rows(gpu, R, dtype, pad, shift):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,N,pad,shift", [(torch.bfloat16, 2000, 0, 0), (torch.float32, 1924, 4, 0), (torch.float16, 2047, 1, 0),
+                                               (torch.float16, 1928, 16, 8), (torch.float32, 2000, 1, 0)])
+@pytest.mark.parametrize("off", [None, [0, 1303, 3990], [5, 2100, 3900]])
+def test_matmul_large_tiles(gpu, dtype, N, pad, shift, off):
+    """Sizes whose tiles two blocks share: full and ragged tiles, rows on 16-byte boundaries or not, columns
+    beside the output and rows outside every segment left as they were."""
+    check_matmul(gpu, 3990, N, 2560, E=len(off) - 1 if off else 1, dtype=dtype, off=off, pad=pad, shift=shift)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("R", [4, 60, 200, 600])
 def test_matmul_keeps_rows_apart(gpu, R):
     """A NaN in one row's codes or scale, or in a row that no expert has, stays in that row."""
