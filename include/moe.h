@@ -434,13 +434,13 @@ moe_status moe_balance_forward(const void *logits, int32_t dtype, int64_t ld, in
 /* Its gradient (the counts are constants): dlogits[T, E] (dtype of logits, rows
  * ldd elements apart) = grad_loss * d loss / d logits, with counts and tokens
  * as moe_balance_forward wrote them and grad_loss a device float32 (NULL: 1).
- * Masked tokens get zeros; rows of tokens outside every segment stay as they
- * are. */
+ * Masked tokens get zeros; rows of tokens outside every segment get zeros too if
+ * zero_rest is not 0 and stay as they are if it is. */
 moe_status moe_balance_backward(const void *logits, int32_t dtype, int64_t ld, int32_t T, int32_t n_experts,
                                 int32_t top_k, int32_t score_func, float coef, const int32_t *counts,
                                 const int32_t *tokens, const int32_t *seq_offsets, int32_t n_seq,
                                 const uint8_t *mask, const float *grad_loss, void *dlogits, int64_t ldd,
-                                void *stream);
+                                int32_t zero_rest, void *stream);
 
 /* e4m3 codes with one scale per 1 x 128 block along each row: for row r of the
  * output, x row `rows[r]` (device int32; negative or >= n_tokens: a row of

@@ -132,7 +132,7 @@ def lib():
         L.moe_balance_workspace.restype = sz
         L.moe_balance_forward.argtypes = [vp, i32, i64, i32, i32, vp, i32, i32, f32, vp, i32, vp, vp, vp, vp, vp,
                                           vp, sz, vp]
-        L.moe_balance_backward.argtypes = [vp, i32, i64, i32, i32, i32, i32, f32, vp, vp, vp, i32, vp, vp, vp, i64, vp]
+        L.moe_balance_backward.argtypes = [vp, i32, i64, i32, i32, i32, i32, f32, vp, vp, vp, i32, vp, vp, vp, i64, i32, vp]
         L.moe_fp8_quantize.argtypes = [vp, i32, i64, i32, i32, vp, i32, vp, vp, vp, vp, vp]
         L.moe_fp8_quantize_weights.argtypes = [vp, i32, i32, i32, i32, vp, vp, vp, vp, vp]
         L.moe_fp8_matmul.argtypes = [vp, vp, i32, vp, vp, i32, i32, i32, vp, vp, i32, i64, vp]
@@ -432,8 +432,8 @@ def moe_balance_forward(logits, topk_idx, coef: float, score_func: int = MOE_SCO
 def moe_balance_backward(logits, top_k: int, counts, tokens, coef: float, score_func: int = MOE_SCORE_SIGMOID, seq_offsets=None,
                          mask=None, grad_loss=None, out=None, stream=None):
     """Gradient of moe_balance_forward's loss with respect to logits, with its counts and tokens;
-    grad_loss float32, one value (None: 1).  Rows outside every sequence of `out` (None: a new
-    tensor) stay as they are.  -> dlogits [T, E] in logits' dtype."""
+    grad_loss float32, one value (None: 1).  Rows outside every sequence stay as they are in `out`;
+    without it (None) they are zeros of a new tensor.  -> dlogits [T, E] in logits' dtype."""
     return _native().balance_backward(logits, top_k, counts, tokens, coef, score_func, seq_offsets, mask, grad_loss, out,
                                       _handle(stream))
 
@@ -457,7 +457,8 @@ def moe_fp8_matmul(x, x_scale, w, w_scale, offsets=None, out=None, out_dtype=Non
     """y [R, N] = x w^T of e4m3 codes x [R, K], w [N, K] with their block scales
     x_scale [ceil(K / 128), R], w_scale [ceil(N / 128), ceil(K / 128)].  With offsets [E + 1] int32,
     w [E, N, K] and w_scale [E, ...]: row r is multiplied with the expert whose segment holds it;
-    rows outside every segment of `out` stay as they are.  out_dtype: bfloat16 by default."""
+    rows outside every segment of `out` stay as they are (None: a new tensor, whose such rows are not
+    written).  out_dtype: bfloat16 by default."""
     return _native().fp8_matmul(x, x_scale, w, w_scale, offsets, out, out_dtype, _handle(stream))
 
 

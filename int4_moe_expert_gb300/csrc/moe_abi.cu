@@ -560,7 +560,7 @@ moe_status moe_balance_forward(const void *logits, int32_t dtype, int64_t ld, in
 moe_status moe_balance_backward(const void *logits, int32_t dtype, int64_t ld, int32_t T, int32_t n_experts, int32_t top_k,
                                 int32_t score_func, float coef, const int32_t *counts, const int32_t *tokens,
                                 const int32_t *seq_offsets, int32_t n_seq, const uint8_t *mask, const float *grad_loss,
-                                void *dlogits, int64_t ldd, void *stream) {
+                                void *dlogits, int64_t ldd, int32_t zero_rest, void *stream) {
     const moe_status s = check_balance(logits, dtype, ld, T, n_experts, top_k, score_func, coef, seq_offsets, n_seq);
     if (s != MOE_OK) return s;
     MOE_NEED(counts && tokens, MOE_ERR_INVALID, "counts / tokens is NULL");
@@ -570,7 +570,7 @@ moe_status moe_balance_backward(const void *logits, int32_t dtype, int64_t ld, i
     if (T == 0) return MOE_OK;
     MOE_NEED(dlogits, MOE_ERR_INVALID, "dlogits is NULL");
     return launched(moe::launch_balance_backward(logits, dtype, ld, T, n_experts, top_k, score_func == MOE_SCORE_SOFTMAX, coef,
-                                                 counts, tokens, seq_offsets, n_seq, mask, grad_loss, dlogits, ldd,
+                                                 counts, tokens, seq_offsets, n_seq, mask, grad_loss, dlogits, ldd, zero_rest != 0,
                                                  static_cast<cudaStream_t>(stream)), "moe_balance_backward");
 }
 

@@ -591,7 +591,8 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) fp8_narrow_kernel(const
 //           and sums stay in tensor memory for kFlush blocks: 273 ns a stage, the tensor cores' rate
 //           (3.4 PFLOP/s on 2048 x 2048 from 65536 rows).  64 experts' 2048 x 2048 float32 outputs:
 //           273 us, bound by memory traffic (1.07 GB of stores alone take 188 us in this pattern, a
-//           fill 143 us); prefetching operands, mixing experts' tiles, streaming stores, 4 or 6 stages:
+//           fill 143 us); stores by tensor copies, whose staging takes a stage: 292 us, one long sum 193
+//           for 171 us; prefetching operands, mixing experts' tiles, streaming stores, 6 stages:
 //           no gain or slower.
 // ---------------------------------------------------------------------------
 
@@ -1628,11 +1629,12 @@ __global__ void __launch_bounds__(kQThreads, sizeof(T) == 4 ? 2 : 4) quantize_ti
 }
 
 int sm_count() {
-    static int n[64] = {};
+    static std::atomic<int> n[64] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 152;
-    if (!n[dev]) cudaDeviceGetAttribute(&n[dev], cudaDevAttrMultiProcessorCount, dev);
-    return n[dev] > 0 ? n[dev] : 152;
+    int v = n[dev].load(std::memory_order_relaxed);
+    if (!v && cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess) n[dev].store(v, std::memory_order_relaxed);
+    return v > 0 ? v : 152;
 }
 
 }  // namespace
@@ -1701,18 +1703,18 @@ bool tmap(CUtensorMap *m, int rank, const void *base, uint64_t cols, uint64_t ro
 }
 
 cudaError_t error_word(unsigned **err) {
-    static unsigned *word[64] = {};
+    static std::atomic<unsigned *> word[64] = {};
     int dev = -1;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!word[dev]) {
-        void *ptr = nullptr;
-        e = cudaGetSymbolAddress(&ptr, g_fp8_err);
-        if (e != cudaSuccess) return e;
-        word[dev] = static_cast<unsigned *>(ptr);
-    }
-    *err = word[dev];
+    *err = word[dev].load(std::memory_order_relaxed);
+    if (*err) return cudaSuccess;
+    void *ptr = nullptr;
+    e = cudaGetSymbolAddress(&ptr, g_fp8_err);
+    if (e != cudaSuccess) return e;
+    *err = static_cast<unsigned *>(ptr);
+    word[dev].store(*err, std::memory_order_relaxed);
     return cudaSuccess;
 }
 

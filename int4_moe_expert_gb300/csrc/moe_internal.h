@@ -188,7 +188,8 @@ cudaError_t launch_balance_forward(const void *logits, int dtype, long long ld, 
                                    int *counts, float *sums, int *tokens, void *ws, cudaStream_t st);
 cudaError_t launch_balance_backward(const void *logits, int dtype, long long ld, int T, int E, int K, int softmax,
                                     float coef, const int *counts, const int *tokens, const int *seq, int S,
-                                    const uint8_t *mask, const float *grad, void *dlogits, long long ldd, cudaStream_t st);
+                                    const uint8_t *mask, const float *grad, void *dlogits, long long ldd, bool zero_rest,
+                                    cudaStream_t st);
 
 // Block-scaled e4m3 quantisers and products (moe_fp8.cu).
 cudaError_t launch_quantize(const void *x, int dtype, long long ld, int n_src, int width, const int *rows, int R,

@@ -234,7 +234,7 @@ struct BalArgs {
     float *part_loss;          // [S][groups of kSumE experts]
     unsigned *ticket;
     float scale;               // coef E / (K S)
-    int T, E, K, S, per_block, softmax;
+    int T, E, K, S, per_block, softmax, zero_rest;
 };
 
 template <typename T>
@@ -552,9 +552,16 @@ __global__ void __launch_bounds__(kBalThreads) balance_grad_kernel(const BalArgs
     const typename L::T *logits = static_cast<const typename L::T *>(p.logits);
     typename L::T *out = static_cast<typename L::T *>(p.dlogits);
     const float g = (p.grad ? load_in(p.grad) : 1.0f) * p.scale;
+    int done = ta;      // the run's tokens before it are written, or outside every segment and to be kept
+    auto zeros = [&](int end) {
+        const float z[J] = {};
+        for (int t = done + k; p.zero_rest && t < end; t += G) L::store(out + (long long)t * p.ldd, p.E, l, z);
+    };
     for (int s = ta < tb ? seg.of(ta) : p.S; s < p.S && seg.at(s) < tb; s++) {
         const int a = max(seg.at(s), ta), b = min(seg.at(s + 1), tb);
         if (a >= b) continue;
+        zeros(a);
+        done = b;
         const float n = (float)max(load_in(p.tokens + s), 1), up = g / n / n;
         float c[J];
 #pragma unroll
@@ -586,6 +593,7 @@ __global__ void __launch_bounds__(kBalThreads) balance_grad_kernel(const BalArgs
             }
         }
     }
+    zeros(tb);
 }
 
 template <bool VEC, typename F>
@@ -697,7 +705,7 @@ cudaError_t launch_balance_forward(const void *logits, int dtype, long long ld, 
 
 cudaError_t launch_balance_backward(const void *logits, int dtype, long long ld, int T, int E, int K, int softmax, float coef,
                                     const int *counts, const int *tokens, const int *seq, int S, const uint8_t *mask,
-                                    const float *grad, void *dlogits, long long ldd, cudaStream_t st) {
+                                    const float *grad, void *dlogits, long long ldd, bool zero_rest, cudaStream_t st) {
     BalArgs p = {};
     p.logits = logits;
     p.ld = ld;
@@ -714,6 +722,7 @@ cudaError_t launch_balance_backward(const void *logits, int dtype, long long ld,
     p.K = K;
     p.S = S;
     p.softmax = softmax;
+    p.zero_rest = zero_rest && seq;
     p.per_block = tokens_per_block(T);
     auto go = [&](auto lay) {
         return launch_early(balance_grad_kernel<decltype(lay)>, (T + p.per_block - 1) / p.per_block, kBalThreads, 0, st, 1, p);

@@ -180,7 +180,7 @@ PyObject *expert_lists(PyObject *const *a, Py_ssize_t n) {
     const int32_t E = c.integer(a[1], "n_experts"), align = c.integer(a[2], "align");
     // sizes that the call refuses allocate nothing first
     const int64_t room = moe_expert_lists_rows(T, K, E, align);
-    const bool ok = room >= 0 && room < (1ll << 31) && E <= 1024;
+    const bool ok = room >= 0 && room < (1ll << 31) && E <= 1024 && K <= 1024 && align <= 4096;
     at::Tensor counts = c.empty({ok ? E : 0}, at::kInt), off = c.empty({ok ? E + 1 : 0}, at::kInt), rows = c.empty({ok ? room : 0}, at::kInt),
                pos = c.empty(idx.sizes(), at::kInt), ws;
     const size_t need = ok ? moe_expert_lists_workspace(T, K, E) : 0;
@@ -219,9 +219,11 @@ PyObject *balance_forward(PyObject *const *a, Py_ssize_t n) {
     const Balance b(c, a[0], a[4], a[5]);
     const at::Tensor &idx = c.dims(a[1], "topk_idx", 2);
     const void *p = c.need(idx, "topk_idx", kI32, {b.T, idx.size(1)});
-    at::Tensor loss = c.empty({1}, at::kFloat), counts = c.empty({b.S, b.E}, at::kInt), sums = c.empty({b.S, b.E}, at::kFloat),
-               tokens = c.empty({b.S}, at::kInt);
-    const size_t need = moe_balance_workspace(b.T, b.E, b.S);
+    // sizes that the call refuses allocate nothing first
+    const int32_t S = b.S <= 65535 && b.E <= 1024 ? b.S : 0;
+    at::Tensor loss = c.empty({1}, at::kFloat), counts = c.empty({S, b.E}, at::kInt), sums = c.empty({S, b.E}, at::kFloat),
+               tokens = c.empty({S}, at::kInt);
+    const size_t need = S ? moe_balance_workspace(b.T, b.E, S) : 0;
     at::Tensor ws = c.empty({(int64_t)need}, at::kByte);
     c.check(moe_balance_forward(b.x, b.dtype, b.ld, b.T, b.E, static_cast<const int32_t *>(p), c.size(idx.size(1), "top_k"),
                                 c.integer(a[3], "score_func"), c.real(a[2], "coef"), b.seq, b.S, b.mask, loss.data_ptr<float>(),
@@ -245,7 +247,7 @@ PyObject *balance_backward(PyObject *const *a, Py_ssize_t n) {
     if (out.scalar_type() != type) c.fail("out: its type is %s, that of logits %s", at::toString(out.scalar_type()), at::toString(type));
     c.check(moe_balance_backward(b.x, b.dtype, b.ld, b.T, b.E, c.integer(a[1], "top_k"), c.integer(a[5], "score_func"), c.real(a[4], "coef"),
                                  static_cast<const int32_t *>(counts), static_cast<const int32_t *>(tokens), b.seq, b.S, b.mask,
-                                 static_cast<const float *>(g), out.data_ptr(), Call::row_stride(out), c.stream()));
+                                 static_cast<const float *>(g), out.data_ptr(), Call::row_stride(out), a[9] == Py_None, c.stream()));
     return THPVariable_Wrap(out);
 }
 

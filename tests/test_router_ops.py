@@ -73,7 +73,7 @@ def test_balance_refusals(moe):
     def bwd(d=P, ldd=8, g=None, **kw):
         a = {**base, **kw}
         return L.moe_balance_backward(a["x"], a["dt"], a["ld"], a["T"], a["E"], a["K"], a["score"], a["coef"], a["cnt"], a["tok"], a["seq"],
-                                      a["S"], a["mask"], g, d, ldd, None)
+                                      a["S"], a["mask"], g, d, ldd, 0, None)
     for call in (fwd, bwd):
         for kw in (dict(x=None), dict(dt=3), dict(dt=-1), dict(ld=7), dict(T=-1), dict(K=0), dict(K=9), dict(score=2), dict(S=2),
                    dict(coef=float("nan")), dict(x=P + 1), dict(cnt=None), dict(tok=None), dict(seq=P + 1, S=2)):
@@ -221,6 +221,10 @@ def check_balance(moe, logits, idx, coef, score, seq=None, mask=None, g=None):
     least = fin.smallest_normal * fin.eps           # half a step of subnormal results, rounded up
     assert bool((err <= 2.0 ** -18 * scale * ref[5][lo:hi] + fin.eps / 2 * (scale * ref[4][lo:hi]).abs() + least).all())
     assert bool((d[:lo] == 7.0).all()) and bool((d[hi:] == 7.0).all())        # rows outside every segment
+    fill = torch.full_like(out, 7.0)                # a new tensor, likely in this one's memory
+    del fill
+    n = moe.moe_balance_backward(x, idx.shape[1], counts, tokens, coef, score, seq_offsets=sq, mask=mk, grad_loss=up).cpu().double()
+    assert torch.equal(n[lo:hi], d[lo:hi]) and bool((n[:lo] == 0).all()) and bool((n[hi:] == 0).all())
     return loss, counts, sums, tokens
 
 
