@@ -216,7 +216,6 @@ __global__ void __launch_bounds__(kListThreads, 1) lists_kernel(const ListArgs p
 
 constexpr int kBalThreads = 256;
 constexpr int kBalWarps = kBalThreads / 32;
-constexpr int kSumThreads = 1024;
 
 struct BalArgs {
     const void *logits;
@@ -231,8 +230,7 @@ struct BalArgs {
     void *dlogits;
     int2 *part;                // [slots][E]: sum (float32 bits) and count of a block's tokens of one segment
     int *part_tokens;          // [slots]
-    float *part_loss;          // [S][groups of kSumE experts]
-    unsigned *ticket;
+    float *part_loss;          // [S][groups of EB experts]
     float scale;               // coef E / (K S)
     int T, E, K, S, per_block, softmax, zero_rest;
 };
@@ -396,7 +394,6 @@ __global__ void __launch_bounds__(kBalThreads) balance_part_kernel(const BalArgs
     wait_for_stream();
     const Segs seg(p, s_seg);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, l = lane % L::LPT, g = lane / L::LPT;
-    if (blockIdx.x == 0 && tid == 0) *p.ticket = 0;
     const int t0 = (int)blockIdx.x * p.per_block, t1 = min(t0 + p.per_block, p.T);
     const typename L::T *logits = static_cast<const typename L::T *>(p.logits);
     for (int s = seg.of(t0); s < p.S && seg.at(s) < t1; s++) {
@@ -458,18 +455,19 @@ __global__ void __launch_bounds__(kBalThreads) balance_part_kernel(const BalArgs
     }
 }
 
-// One block per (kSumE experts, segment): the slots' sums in a fixed order (128 strands of slots, then
-// the strands in pairs), then the block's part of the loss; the last block to finish adds the parts in
-// order.  Bound by latency: few loads a thread, all in flight.
-constexpr int kSumE = 8;
-__global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(const BalArgs p) {
-    constexpr int STRANDS = kSumThreads / kSumE;
-    __shared__ float s_sum[32][kSumE];
-    __shared__ int s_cnt[32][kSumE], s_tok[32];
-    __shared__ bool s_last;
+// One block per (segment, EB experts): the slots' sums in a fixed order (strands of slots, then the
+// strands), then the block's part of the loss.  Bound by latency: few loads a thread, all in flight.
+constexpr int kSumE = 8;           // the least EB: the most parts of the loss
+constexpr int kLossThreads = 1024;
+template <int EB, int THREADS>
+__global__ void __launch_bounds__(THREADS, 2048 / THREADS) balance_sum_kernel(const BalArgs p) {
+    constexpr int STRANDS = THREADS / EB, WARPS = THREADS / 32, LE = EB < 32 ? EB : 32, ROWS = STRANDS * LE / 32;
+    static_assert(WARPS <= 32 && (EB < 32 ? ROWS == WARPS && ROWS % (32 / EB) == 0 : EB % 32 == 0), "");
+    __shared__ float s_sum[ROWS][EB], s_part[(EB + 31) / 32];
+    __shared__ int s_cnt[ROWS][EB], s_tok[WARPS];
     wait_for_stream();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int s = (int)blockIdx.y, g = (int)blockIdx.x, G = (int)gridDim.x, e = kSumE * g + tid % kSumE;
+    const int s = (int)blockIdx.x, g = (int)blockIdx.y, G = (int)gridDim.y, e = EB * g + tid % EB;
     const int a = p.seq ? min(max(load_in(p.seq + s), 0), p.T) : 0, b = p.seq ? min(max(load_in(p.seq + s + 1), 0), p.T) : p.T;
     float sum = 0.0f;
     int cnt = 0, tok = 0;
@@ -477,65 +475,86 @@ __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(const BalArgs 
         const int b0 = a / p.per_block, b1 = (b - 1) / p.per_block;
         if (e < p.E) {
 #pragma unroll 8
-            for (int k = b0 + tid / kSumE; k <= b1; k += STRANDS) {
+            for (int k = b0 + tid / EB; k <= b1; k += STRANDS) {
                 const int2 v = load_in(p.part + ((size_t)k + s) * p.E + e);
                 sum += __int_as_float(v.x);
                 cnt += v.y;
             }
         }
-        for (int k = b0 + tid; k <= b1; k += kSumThreads) tok += p.part_tokens[(size_t)k + s];
+        for (int k = b0 + tid; k <= b1; k += THREADS) tok += p.part_tokens[(size_t)k + s];
     }
 #pragma unroll
-    for (int d = kSumE; d < 32; d *= 2) {
+    for (int d = LE; d < 32; d *= 2) {
         sum += __shfl_xor_sync(0xffffffffu, sum, d);
         cnt += __shfl_xor_sync(0xffffffffu, cnt, d);
     }
     tok = __reduce_add_sync(0xffffffffu, tok);
-    if (lane < kSumE) {
-        s_sum[warp][lane] = sum;
-        s_cnt[warp][lane] = cnt;
+    if (lane < LE) {
+        s_sum[EB < 32 ? warp : tid / EB][tid % EB] = sum;
+        s_cnt[EB < 32 ? warp : tid / EB][tid % EB] = cnt;
     }
     if (lane == 0) s_tok[warp] = tok;
     __syncthreads();
-    if (warp == 0) {
-        // lane: expert lane % kSumE of every (32 / kSumE)-th warp's sums
+    // the first warps: a lane an expert (EB < 32: of every (32 / EB)-th row, then the lanes' sums)
+    constexpr int STEP = 32 / LE;
+    if (warp < (EB + 31) / 32) {
         sum = 0.0f;
         cnt = 0;
 #pragma unroll
-        for (int i = 0; i < kSumE; i++) {
-            sum += s_sum[lane / kSumE + i * (32 / kSumE)][lane % kSumE];
-            cnt += s_cnt[lane / kSumE + i * (32 / kSumE)][lane % kSumE];
+        for (int i = 0; i < ROWS / STEP; i++) {
+            sum += s_sum[lane / LE + i * STEP][tid % EB];
+            cnt += s_cnt[lane / LE + i * STEP][tid % EB];
         }
 #pragma unroll
-        for (int d = kSumE; d < 32; d *= 2) {
+        for (int d = LE; d < 32; d *= 2) {
             sum += __shfl_xor_sync(0xffffffffu, sum, d);
             cnt += __shfl_xor_sync(0xffffffffu, cnt, d);
         }
-        tok = __reduce_add_sync(0xffffffffu, s_tok[lane]);
-        if (lane < kSumE && e < p.E) {
+        if (lane < LE && e < p.E) {
             p.sums[(size_t)s * p.E + e] = sum;
             p.counts[(size_t)s * p.E + e] = cnt;
         }
-        if (g == 0 && lane == 0) p.tokens[s] = tok;
         float l = e < p.E ? sum * (float)cnt : 0.0f;
 #pragma unroll
-        for (int d = kSumE / 2; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+        for (int d = LE / 2; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+        if (EB > 32 && lane == 0) s_part[warp] = l;
+        sum = l;
+    }
+    if (EB > 32) __syncthreads();
+    if (warp == 0) {
+        if (EB > 32) {
+            sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < EB / 32; i++) sum += s_part[i];
+        }
+        tok = __reduce_add_sync(0xffffffffu, lane < WARPS ? s_tok[lane] : 0);
         if (lane == 0) {
+            if (g == 0) p.tokens[s] = tok;
             const float n = (float)max(tok, 1);
-            p.part_loss[(size_t)s * G + g] = p.scale / n * (l / n);
-            __threadfence();
-            s_last = atomicAdd(p.ticket, 1u) == (unsigned)G * p.S - 1u;
+            p.part_loss[(size_t)s * G + g] = p.scale / n * (sum / n);
         }
     }
+}
+
+// The parts of the loss, in a fixed order.  A launch of its own costs less than a count of the blocks
+// that are done, for the last of them to add up (9 sequences of 4099 tokens, 256 experts: 11.1 and
+// 11.7 us of the forward; 128 sequences of 32768: 48 and 56 us, every block's count at one address).
+__global__ void __launch_bounds__(kLossThreads) balance_loss_kernel(const float *part, int n, float *loss) {
+    __shared__ float s_part[32];
+    wait_for_stream();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    float l = 0.0f;
+#pragma unroll 8
+    for (int i = tid; i < n; i += kLossThreads) l += load_in(part + i);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+    if (lane == 0) s_part[warp] = l;
     __syncthreads();
-    if (s_last && warp == 0) {
-        __threadfence();
-        float l = 0.0f;
-        const int parts = G * p.S;
-        for (int i = lane; i < parts; i += 32) l += __ldcg(p.part_loss + i);
+    if (warp == 0) {
+        l = s_part[lane];
 #pragma unroll
         for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-        if (lane == 0) *p.loss = l;
+        if (lane == 0) *loss = l;
     }
 }
 
@@ -661,7 +680,7 @@ cudaError_t launch_lists(const int *idx, int T, int K, int E, int align, long lo
 
 size_t balance_workspace(int T, int E, int S) {
     const size_t slots = balance_slots(T, S);
-    return up16(slots * E * 8) + up16(slots * 4) + up16((size_t)S * ((E + kSumE - 1) / kSumE) * 4) + 16;
+    return up16(slots * E * 8) + up16(slots * 4) + up16((size_t)S * ((E + kSumE - 1) / kSumE) * 4);
 }
 
 cudaError_t launch_balance_forward(const void *logits, int dtype, long long ld, int T, int E, const int *idx, int K, int softmax,
@@ -691,8 +710,6 @@ cudaError_t launch_balance_forward(const void *logits, int dtype, long long ld, 
     p.part_tokens = reinterpret_cast<int *>(w);
     w += up16(slots * 4);
     p.part_loss = reinterpret_cast<float *>(w);
-    w += up16((size_t)S * ((E + kSumE - 1) / kSumE) * 4);
-    p.ticket = reinterpret_cast<unsigned *>(w);
     auto go = [&](auto lay) {
         using L = decltype(lay);
         const int blocks = T > 0 ? (T + p.per_block - 1) / p.per_block : 1;
@@ -700,7 +717,19 @@ cudaError_t launch_balance_forward(const void *logits, int dtype, long long ld, 
     };
     const cudaError_t e = quads(logits, ld, dtype, E) ? by_layout<true>(dtype, E, go) : by_layout<false>(dtype, E, go);
     if (e != cudaSuccess) return e;
-    return launch_early(balance_sum_kernel, dim3((E + kSumE - 1) / kSumE, S), kSumThreads, 0, st, 1, p);
+    auto add_up = [&](auto kernel, int eb, int threads) {
+        const int groups = (E + eb - 1) / eb;
+        const cudaError_t er = launch_early(kernel, dim3(S, groups), threads, 0, st, 1, p);
+        if (er != cudaSuccess) return er;
+        return launch_early(balance_loss_kernel, 1, kLossThreads, 0, st, 1, p.part_loss, S * groups, loss);
+    };
+    // By the slots of a sequence: many strands for many of them, else few blocks.  The forward of 32768
+    // x 256 scores, 1024 slots, by 8 experts x 128 strands / 32 x 8 / 256 x 1: 1 sequence 17 / 28 / 91 us,
+    // 9 18 / 22 / 43, 32 24 / 19 / 28, 128 48 / 21 / 23, 500 133 / 29 / 24, 4000 901 / 87 / 49.
+    const size_t each = slots / S;
+    if (each >= 48) return add_up(balance_sum_kernel<8, 1024>, 8, 1024);
+    if (each >= 5) return add_up(balance_sum_kernel<32, 256>, 32, 256);
+    return add_up(balance_sum_kernel<256, 256>, 256, 256);
 }
 
 cudaError_t launch_balance_backward(const void *logits, int dtype, long long ld, int T, int E, int K, int softmax, float coef,

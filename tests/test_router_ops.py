@@ -261,6 +261,16 @@ def test_balance_segments_and_masks(gpu, score, seq):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("E", [1, 8, 40, 300, 1024])
+@pytest.mark.parametrize("S", [1, 5, 30, 130, 600])
+def test_balance_numbers_of_segments(gpu, S, E):
+    x, idx = router(2500, E, min(E, 3), S + E)
+    cut = sorted(torch.randint(0, 2501, (S - 1,), generator=torch.Generator().manual_seed(S)).tolist())
+    mask = torch.rand(2500, generator=torch.Generator().manual_seed(E)) < 0.9
+    check_balance(gpu, x, idx, 1.0, 1, [0] + cut + [2500], mask)
+
+
+@pytest.mark.gpu
 def test_balance_many_segments_and_long_ones(gpu):
     x, idx = router(3000, 16, 2, 7)
     check_balance(gpu, x, idx, 1.0, 0, sorted([0, 3000] + torch.randint(0, 3001, (700,), generator=torch.Generator().manual_seed(8)).tolist()))
