@@ -351,15 +351,16 @@ struct Segs {
         return lo;
     }
 };
-// a token's normalised scores (0 where the logit is -infinity); c1: 1 - sigma (sigmoid only)
+// a token's scores (0 where the logit is -infinity) and one over their sum, which normalises them;
+// c1: 1 - sigma (sigmoid only)
 template <class L>
-__device__ __forceinline__ void scores(const float (&x)[L::J], int softmax, float (&pr)[L::J], float (&c1)[L::J]) {
+__device__ __forceinline__ float scores(const float (&x)[L::J], int softmax, float (&pr)[L::J], float (&c1)[L::J]) {
     constexpr int J = L::J;
     float z = 0.0f;
     if (softmax) {
-        float m = -INFINITY;
+        float m = x[0];
 #pragma unroll
-        for (int j = 0; j < J; j++) m = fmaxf(m, x[j]);
+        for (int j = 1; j < J; j++) m = fmaxf(m, x[j]);
         m = L::most(m);
         if (m == -INFINITY) m = 0.0f;      // no expert left: every probability 0 (below)
 #pragma unroll
@@ -379,9 +380,7 @@ __device__ __forceinline__ void scores(const float (&x)[L::J], int softmax, floa
         }
         z = L::add(z) + 1e-20f;
     }
-    const float inv = 1.0f / z;
-#pragma unroll
-    for (int j = 0; j < J; j++) pr[j] *= inv;
+    return 1.0f / z;
 }
 
 template <class L>
@@ -432,9 +431,9 @@ __global__ void __launch_bounds__(kBalThreads) balance_part_kernel(const BalArgs
 #pragma unroll
             for (int u = 0; u < U; u++) {
                 float pr[J], c1[J];
-                scores<L>(x[u], p.softmax, pr, c1);
+                const float inv = scores<L>(x[u], p.softmax, pr, c1);
 #pragma unroll
-                for (int j = 0; j < J; j++) sum[j] += pr[j];
+                for (int j = 0; j < J; j++) sum[j] = fmaf(pr[j], inv, sum[j]);
                 n += on[u] ? 1 : 0;
             }
         }
@@ -584,7 +583,7 @@ __global__ void __launch_bounds__(kBalThreads) balance_grad_kernel(const BalArgs
         const float n = (float)max(load_in(p.tokens + s), 1), up = g / n / n;
         float c[J];
 #pragma unroll
-        for (int j = 0; j < J; j++) c[j] = L::expert(l, j) < p.E ? (float)load_in(p.counts + (size_t)s * p.E + L::expert(l, j)) : 0.0f;
+        for (int j = 0; j < J; j++) c[j] = L::expert(l, j) < p.E ? (float)load_in(p.counts + (size_t)s * p.E + L::expert(l, j)) * up : 0.0f;
         for (int t = a; t < b; t += U * G) {
             float x[U][J];
             bool on[U];
@@ -598,15 +597,16 @@ __global__ void __launch_bounds__(kBalThreads) balance_grad_kernel(const BalArgs
             for (int u = 0; u < U; u++) {
                 const int tt = t + u * G + k;
                 float pr[J], c1[J], dot = 0.0f;
-                scores<L>(x[u], p.softmax, pr, c1);
+                const float inv = scores<L>(x[u], p.softmax, pr, c1);
 #pragma unroll
                 for (int j = 0; j < J; j++) dot = fmaf(pr[j], c[j], dot);
-                dot = L::add(dot);
+                dot = L::add(dot) * inv;
+                if (p.softmax) {
 #pragma unroll
-                for (int j = 0; j < J; j++) {
-                    float d = up * pr[j] * (c[j] - dot);
-                    if (!p.softmax) d *= c1[j];
-                    x[u][j] = d;
+                    for (int j = 0; j < J; j++) x[u][j] = pr[j] * inv * (c[j] - dot);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < J; j++) x[u][j] = pr[j] * inv * (c[j] - dot) * c1[j];
                 }
                 if (tt < b) L::store(out + (long long)tt * p.ldd, p.E, l, x[u]);
             }
