@@ -598,15 +598,20 @@ __global__ void __launch_bounds__(kBalThreads) balance_grad_kernel(const BalArgs
                 const int tt = t + u * G + k;
                 float pr[J], c1[J], dot = 0.0f;
                 const float inv = scores<L>(x[u], p.softmax, pr, c1);
+                if (!p.softmax) {      // normalised first: sigmoids can all be so small that their sum with c underflows
+#pragma unroll
+                    for (int j = 0; j < J; j++) pr[j] *= inv;
+                }
 #pragma unroll
                 for (int j = 0; j < J; j++) dot = fmaf(pr[j], c[j], dot);
-                dot = L::add(dot) * inv;
+                dot = L::add(dot);
                 if (p.softmax) {
+                    dot *= inv;
 #pragma unroll
                     for (int j = 0; j < J; j++) x[u][j] = pr[j] * inv * (c[j] - dot);
                 } else {
 #pragma unroll
-                    for (int j = 0; j < J; j++) x[u][j] = pr[j] * inv * (c[j] - dot) * c1[j];
+                    for (int j = 0; j < J; j++) x[u][j] = pr[j] * (c[j] - dot) * c1[j];
                 }
                 if (tt < b) L::store(out + (long long)tt * p.ldd, p.E, l, x[u]);
             }

@@ -261,6 +261,16 @@ def test_balance_segments_and_masks(gpu, score, seq):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("score", [0, 1])
+def test_balance_small_scores_and_gradients(gpu, score):
+    """Logits whose sigmoids are near the smallest numbers, and an upstream gradient that makes the scaled
+    counts small too: no product of the two may underflow where the result does not."""
+    x, idx = router(300, 64, 4, 11)
+    for low in (-42.0, -60.0, -85.0):
+        check_balance(gpu, x + low, idx, 1.0, score, g=1e-22)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("E", [1, 8, 40, 300, 1024])
 @pytest.mark.parametrize("S", [1, 5, 30, 130, 600])
 def test_balance_numbers_of_segments(gpu, S, E):
