@@ -585,7 +585,8 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) fp8_narrow_kernel(const
 //           the stores (with two more staging buffers and a stage less, against the others' path: 275
 //           and 278 us; 65536 x 2048 x 2048 200 and 213 us; 64 experts of it 250 and 250 us).
 //           Measured and not kept: accumulators of 128 columns (298-359 us: twice the waits), 32-column
-//           loads, pipelined or not (420-444 us: each costs its latency), 16 warps (no registers).
+//           loads, pipelined or not (420-444 us: each costs its latency), 16 warps (no registers), an MMA
+//           a block with B copied to both (no way between the blocks, but 48 KB into each SM: 295 us).
 //   wgrad   (MX) A = dy, B = x, both column-quantised.  Their scales are powers of two, so the tensor
 //           core applies them itself (kind::mxf8f6f4; the float32's exponent byte is the ue8m0 scale)
 //           and sums stay in tensor memory for kFlush blocks: 273 ns a stage, the tensor cores' rate
