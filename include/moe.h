@@ -422,8 +422,12 @@ moe_status moe_expert_lists(const int32_t *topk_idx, int32_t T, int32_t top_k, i
  * (an empty segment adds nothing; a perfectly even one adds coef / n_seq).
  * Writes loss[1], counts[n_seq, E] (c), prob_sums[n_seq, E] (sum_t p) and
  * tokens[n_seq] (n), all float32 / int32.  A softmax row of -infinity alone
- * has p = 0.  workspace: moe_balance_workspace(...) bytes, 16-byte aligned.
- * Limits: E in 1..1024, n_seq in 1..65535. */
+ * has p = 0.  workspace: moe_balance_workspace(...) bytes, 16-byte aligned (0
+ * for a T beyond the limit).
+ * Limits: E in 1..1024, n_seq in 1..65535, T up to MOE_BALANCE_MAX_TOKENS (token
+ * numbers, one block of tokens further included, are 32-bit); one expert's
+ * choices in a segment below 2^31. */
+#define MOE_BALANCE_MAX_TOKENS 2147483520 /* 2^31 - 128 */
 size_t moe_balance_workspace(int32_t T, int32_t n_experts, int32_t n_seq);
 moe_status moe_balance_forward(const void *logits, int32_t dtype, int64_t ld, int32_t T, int32_t n_experts,
                                const int32_t *topk_idx, int32_t top_k, int32_t score_func, float coef,

@@ -520,6 +520,7 @@ static moe_status check_balance(const void *logits, int32_t dtype, int64_t ld, i
                                 int32_t score_func, float coef, const int32_t *seq, int32_t n_seq) {
     MOE_NEED(dtype_ok(dtype), MOE_ERR_INVALID, "dtype=%d: need a MOE_DTYPE_* value", dtype);
     MOE_NEED(T >= 0, MOE_ERR_INVALID, "T=%d is negative", T);
+    MOE_NEED(T <= MOE_BALANCE_MAX_TOKENS, MOE_ERR_UNSUPPORTED, "T=%d: need %d or fewer", T, MOE_BALANCE_MAX_TOKENS);
     MOE_NEED(E >= 1 && E <= 1024, MOE_ERR_UNSUPPORTED, "n_experts=%d: need 1..1024", E);
     MOE_NEED(top_k >= 1 && top_k <= E, MOE_ERR_INVALID, "top_k=%d: need 1..n_experts", top_k);
     MOE_NEED(ld >= E, MOE_ERR_INVALID, "ld=%lld: need n_experts or more", (long long)ld);
@@ -534,7 +535,7 @@ static moe_status check_balance(const void *logits, int32_t dtype, int64_t ld, i
 }
 
 size_t moe_balance_workspace(int32_t T, int32_t n_experts, int32_t n_seq) {
-    if (T < 0 || n_experts < 1 || n_seq < 1) return 0;
+    if (T < 0 || T > MOE_BALANCE_MAX_TOKENS || n_experts < 1 || n_seq < 1) return 0;
     return moe::balance_workspace(T, n_experts, n_seq);
 }
 

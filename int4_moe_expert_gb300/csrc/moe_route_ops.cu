@@ -647,7 +647,7 @@ bool quads(const void *x, long long ld, int dtype, int E) {
 }
 
 // tokens of a block: enough blocks to cover the card four times, at most 128 tokens each (fewer slots
-// for the sums to read)
+// for the sums to read; the kernels step up to a block past T in 32 bits: MOE_BALANCE_MAX_TOKENS)
 int tokens_per_block(int T) {
     int n = 128;
     while (n > kBalWarps && (T + n - 1) / n < 4 * 152) n /= 2;

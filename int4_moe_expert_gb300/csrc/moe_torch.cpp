@@ -80,6 +80,8 @@ public:
     }
     template <typename... A>
     [[noreturn]] void fail(const char *fmt, A... a) const { refuse(where_, MOE_ERR_INVALID, fmt, a...); }
+    template <typename... A>
+    [[noreturn]] void unsupported(const char *fmt, A... a) const { refuse(where_, MOE_ERR_UNSUPPORTED, fmt, a...); }
 
     const at::Tensor &tensor(PyObject *o, const char *name) const {
         if (!THPVariable_Check(o)) fail("%s: need a tensor", name);
@@ -202,6 +204,7 @@ struct Balance {
         dtype = dtype_code(t.scalar_type());
         ld = Call::row_stride(t);
         T = c.size(t.size(0), "tokens");
+        if (T > MOE_BALANCE_MAX_TOKENS) c.unsupported("logits: %d tokens, need %d or fewer", T, MOE_BALANCE_MAX_TOKENS);
         E = c.size(t.size(1), "experts");
         if (seq_o != Py_None) {
             const at::Tensor &s = c.dims(seq_o, "seq_offsets", 1);

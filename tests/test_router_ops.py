@@ -87,6 +87,21 @@ def test_balance_refusals(moe):
     assert bwd(T=0) == moe.MOE_OK
 
 
+def test_balance_refuses_token_numbers_beyond_32_bits(moe):
+    """The kernels step up to a block of 128 tokens past T in 32-bit token numbers, so the last 127
+    values of T are refused."""
+    L = moe.lib()
+    most = 2**31 - 128
+    fwd = lambda T, K=1: L.moe_balance_forward(P, 2, 4, T, 4, P, K, 0, 0.1, None, 1, None, P, P, P, P, P, 1 << 40, None)   # noqa: E731
+    bwd = lambda T, K=1: L.moe_balance_backward(P, 2, 4, T, 4, K, 0, 0.1, P, P, None, 1, None, None, P, 4, 0, None)        # noqa: E731
+    for T in (2**31 - 1, 2**31 - 8, 2**31 - 63, most + 1):
+        for call in (fwd, bwd):
+            assert call(T) == moe.MOE_ERR_UNSUPPORTED and f"T={T}" in moe.moe_last_error()
+        assert L.moe_balance_workspace(T, 4, 1) == 0
+    assert fwd(most, 0) == bwd(most, 0) == moe.MOE_ERR_INVALID           # refused for top_k, not for T
+    assert L.moe_balance_workspace(most, 4, 1) >= most // 128 * 4 * 8
+
+
 def test_binding_refuses_what_is_not_on_the_device(moe):
     with pytest.raises(moe.MoeError):
         moe.moe_expert_lists(torch.zeros(2, 2, dtype=torch.int32), 4)
