@@ -131,13 +131,22 @@ __device__ __forceinline__ bool elect_one() {
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
     return p != 0;
 }
+// mbar_try that also acquires what the other block of a cluster released to the barrier
+__device__ __forceinline__ bool mbar_try_cluster(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
 // mbar_wait that also gives up once another role of the block has
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool ring_wait(uint32_t bar, uint32_t parity, const volatile int *fail) {
-    if (mbar_try(bar, parity)) return true;
+    auto passed = [&] { return CLUSTER ? mbar_try_cluster(bar, parity) : mbar_try(bar, parity); };
+    if (passed()) return true;
     const unsigned long long t0 = tc_now();
     for (;;) {
         for (int i = 0; i < 64; i++)
-            if (mbar_try(bar, parity)) return true;
+            if (passed()) return true;
         if (*fail || tc_now() - t0 > kTcWaitNs) return false;
     }
 }
@@ -590,8 +599,8 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) fp8_narrow_kernel(const
 //   wgrad   (MX) A = dy, B = x, both column-quantised.  Their scales are powers of two, so the tensor
 //           core applies them itself (kind::mxf8f6f4; the float32's exponent byte is the ue8m0 scale)
 //           and sums stay in tensor memory for kFlush blocks: 273 ns a stage, the tensor cores' rate
-//           (3.4 PFLOP/s on 2048 x 2048 from 65536 rows).  64 experts' 2048 x 2048 float32 outputs:
-//           273 us, bound by memory traffic (1.07 GB of stores alone take 188 us in this pattern, a
+//           (3.2 PFLOP/s on 2048 x 2048 from 65536 rows).  64 experts' 2048 x 2048 float32 outputs:
+//           277 us, bound by memory traffic (1.07 GB of stores alone take 188 us in this pattern, a
 //           fill 143 us); stores by tensor copies, whose staging takes a stage: 292 us, one long sum 193
 //           for 171 us; prefetching operands, mixing experts' tiles, streaming stores, 6 stages:
 //           no gain or slower.
@@ -612,17 +621,20 @@ struct WideCfg {
     static constexpr int THREADS = 32 * (EW + 4);
     static constexpr bool BIGREG = WC > 64;
     static constexpr int SS = 8;                              // scale ring (matmul)
+    [[maybe_unused]] static constexpr int RS = 8;                              // ring of scales as loaded (MX), in stages
+    [[maybe_unused]] static constexpr int SG = 4, SB = 3;                      // ring of staged scales (MX): SB batches of SG stages
+    [[maybe_unused]] static constexpr int SG0 = SG - 2;                        // the first batch starts there: two stages, ready sooner
     [[maybe_unused]] static constexpr int SFBYTES = 512 + 4 * BN;              // staged scales of a stage (MX): 128 + BN words
     [[maybe_unused]] static constexpr int SFCOLS = 4 + BN / 32;                // their tensor-memory columns
     static constexpr int OUTB = TST ? 8192 : 4096;            // staging of an epilogue warp: (two times) 32 rows x 128 bytes
     static constexpr int NT = MX ? 2 : 512 / BN;              // accumulators: of tiles (MX), of stages
     [[maybe_unused]] static constexpr int ACC1 = MX && 2 * BN + SFCOLS * S > 512 ? 512 - SFCOLS * S - BN : BN;   // from one to the next (MX: may overlap)
     [[maybe_unused]] static constexpr int PLD = BN + 4;                        // floats of a row of partial sums (SPLIT)
-    static constexpr size_t SMEM = 1024 + (size_t)S * STAGE + EW * OUTB + (MX ? S * SFBYTES : 0);
+    static constexpr size_t SMEM = 1024 + (size_t)S * STAGE + EW * OUTB + (MX ? (SB * SG + RS) * SFBYTES : 0);
     // f8f6f4: D f32 at bit 4; mxf8f6f4: ue8m0 scales at bit 23
     static constexpr uint32_t IDESC = (MX ? 1u << 23 : 1u << 4) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(ROWS >> 4) << 24);
     static_assert(!SPLIT || (!PAIR && 128 * PLD * 4 <= S * STAGE), "partial sums reuse the stage ring");
-    static_assert(SMEM + 16 * 1024 <= 227 * 1024, "the rings and the static arrays fit one block's shared memory");
+    static_assert(SMEM + (MX ? 2 : 16) * 1024 <= 227 * 1024, "the rings and the static arrays fit one block's shared memory");
 };
 
 // address of this shared variable in the cluster's first block
@@ -631,11 +643,14 @@ __device__ __forceinline__ uint32_t in_leader(uint32_t saddr) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(saddr));
     return a;
 }
-// arrival on a barrier of the other block.  No ordinary memory passes between the blocks (tensor
-// memory is ordered by tcgen05.fence, the scales by a proxy fence in their own block), so no
-// cluster-wide release: it costs a memory barrier of a microsecond (measured: 447 -> see below)
+// arrival on a barrier of the other block that hands over tensor memory alone (tcgen05.fence orders
+// it): no cluster-wide release, which costs a memory barrier of about a microsecond
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t caddr) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(caddr) : "memory");
+}
+// the same after ordinary stores to shared memory, which an operation that the other block issues reads
+__device__ __forceinline__ void mbar_release_cluster(uint32_t caddr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(caddr) : "memory");
 }
 template <bool PAIR>
 __device__ __forceinline__ void wide_load(uint32_t dst, const void *map, int x, int y, int z, uint32_t bar) {
@@ -882,13 +897,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
     extern __shared__ unsigned char smem_raw[];
     __shared__ __align__(8) unsigned long long s_full[C::S], s_empty[C::S];
     __shared__ __align__(8) unsigned long long s_tfull[C::NT], s_tempty[C::NT];
-    __shared__ __align__(8) unsigned long long s_sfull[C::SS], s_sempty[C::SS];   // MX: s_sfull by stage
+    __shared__ __align__(8) unsigned long long s_sfull[C::SS], s_sempty[C::SS];   // MX: by batch of stages
     __shared__ __align__(8) unsigned long long s_drain;
     __shared__ float s_scale[C::MX ? 1 : C::SS][128], s_wscale[C::MX ? 1 : C::SS][2];   // matmul: rows', weight blocks'
     __shared__ int s_first[C::MX ? 1 : kMaxExperts + 1];
     __shared__ uint32_t s_taddr;
     __shared__ int s_fail, s_issued;
-    static_assert(C::S <= C::SS, "a scale barrier for every stage");
+    __shared__ __align__(8) unsigned long long s_rfull[C::MX ? C::RS : 1], s_rempty[C::MX ? C::RS : 1];
+    static_assert(C::SB <= C::SS, "barriers for every batch of scales");
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t staging = ring + (uint32_t)(C::S * C::STAGE), sfring = staging + (uint32_t)(C::EW * C::OUTB);
@@ -909,8 +925,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
             mbar_init(smem_u32(&s_tempty[i]), NB * C::EW);
         }
         for (int i = 0; i < C::SS; i++) {
-            mbar_init(smem_u32(&s_sfull[i]), C::MX ? NB * 32 : 32);
-            mbar_init(smem_u32(&s_sempty[i]), C::EW);
+            mbar_init(smem_u32(&s_sfull[i]), C::MX ? NB : 32);
+            mbar_init(smem_u32(&s_sempty[i]), C::MX ? 1 : C::EW);
+        }
+        for (int i = 0; C::MX && i < C::RS; i++) {
+            mbar_init(smem_u32(&s_rfull[i]), 32);
+            mbar_init(smem_u32(&s_rempty[i]), 1);
         }
         mbar_init(smem_u32(&s_drain), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -949,6 +969,70 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
             r.k0 = lo;
         }
         return r;
+    };
+    // MX: stages the exponent bytes of the scales of this block's 128 rows of A and of all columns of B from
+    // the float32 values that another warp copied, in batches of SG stages.  A pair's tensor copies of
+    // them are issued by its first block, so that the second's stores need a release and an acquire for
+    // the whole cluster.  The release takes 1.4 us, a stage 0.27: hence one for a batch, by a warp that waits
+    // for no loads, and in the second block two such warps (`which` 0 and 1) that take the batches in turn.
+    // 2048 x 2048 from 65536 rows: a release for every stage 424 us, batches of 3 / 4 / 6 with as many
+    // batches as fit 182 / 173 / 191, one warp for loads and stores 208.
+    [[maybe_unused]] constexpr int NV = 4 + C::BN / 32;      // values a lane: 128 rows of A, the tile's of B
+    [[maybe_unused]] const uint32_t raw = sfring + (uint32_t)(C::SB * C::SG * C::SFBYTES);
+    [[maybe_unused]] auto stage_scales = [&](int which) {
+        Ring<C::RS> q;
+        Ring<C::SB> sb;
+        int sg = C::SG0;
+        bool ok = true, any = false, mine = which == 0;
+        auto hand_over = [&] {      // the batch so far
+            if (mine) {
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) {
+                    if (rank) mbar_release_cluster(in_leader(smem_u32(&s_sfull[sb.slot])));
+                    else mbar_arrive(smem_u32(&s_sfull[sb.slot]));
+                }
+            }
+            if (rank) mine = !mine;
+            sb.next();
+            sg = 0;
+        };
+        for (int t = t0; t < total && ok; t += tstep) {
+            const WideTile ti = tile_at(t);
+            for (int kb = ti.k0; kb < ti.k1; kb++) {
+                if (mine) {
+                    if (!__all_sync(0xffffffffu, (sg > 0 || ring_wait(smem_u32(&s_sempty[sb.slot]), sb.phase ^ 1u, fail)) &&
+                                                     ring_wait(smem_u32(&s_rfull[q.slot]), q.phase, fail))) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t src = raw + (uint32_t)(q.slot * C::SFBYTES + lane * 4);
+                    // word of row r: 16-byte line r % 32, its (r / 32) % 4-th word, 512 bytes per 128 rows
+                    const uint32_t sf = sfring + (uint32_t)((sb.slot * C::SG + sg) * C::SFBYTES + lane * 16);
+                    uint32_t w[NV];
+#pragma unroll
+                    for (int i = 0; i < NV; i++) {
+                        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[i]) : "r"(src + 128u * i) : "memory");
+                        w[i] = ((w[i] >> 23) & 0xFFu) * 0x01010101u;
+                    }
+#pragma unroll
+                    for (int i = 0; i < NV; i += 4)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sf + 128u * i), "r"(w[i]), "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]) : "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&s_rempty[q.slot]));
+                }
+                q.next();
+                any = true;
+                if (++sg == C::SG) hand_over();
+            }
+        }
+        if (ok && any && sg > 0) hand_over();
+        // the arrivals that free the last batches are in before this block ends
+        for (int i = 0; i < C::SB && ok; i++) {
+            ok = __all_sync(0xffffffffu, ring_wait(smem_u32(&s_sempty[sb.slot]), sb.phase ^ 1u, fail));
+            sb.next();
+        }
+        if (!ok) *fail = 1;
     };
 
     if (warp < C::EW) {
@@ -1088,6 +1172,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
             if (rank == 0) {
                 Ring<C::S> r;
                 Ring<C::NT> q;  // matmul: accumulator of the stage; MX: of the tile
+                Ring<C::SB> sb; // MX: batch of scales, the stage's number in it
+                int sg = C::SG0;
                 int sums = 0;   // MX: accumulators begun
                 bool ok = true, any = false;
                 const uint64_t ad0 = sw128_desc(ring), bd0 = sw128_desc(ring + kABytes);
@@ -1107,7 +1193,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
                         const bool last = C::MX && (kb + 1 == k1 || (kb + 1 - ti.k0) % kFlush == 0);
                         // the operands first: they are there early, the accumulator comes back last
                         const bool w = ring_wait(smem_u32(&s_full[r.slot]), r.phase, fail) &&
-                                       (C::MX ? ring_wait(smem_u32(&s_sfull[r.slot]), r.phase, fail)
+                                       (C::MX ? (sg > 0 && any) || ring_wait<C::PAIR>(smem_u32(&s_sfull[sb.slot]), sb.phase, fail)
                                               : ring_wait(smem_u32(&s_tempty[q.slot]), q.phase ^ 1u, fail));
                         if (!__all_sync(0xffffffffu, w)) {
                             ok = false;
@@ -1118,7 +1204,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
                             const uint64_t off = (uint64_t)((r.slot * C::STAGE) >> 4);
                             if constexpr (C::MX) {
                                 const uint32_t tsf = taddr + (uint32_t)(512 - C::SFCOLS * (C::S - r.slot));
-                                const uint64_t sd = sd0 + (uint64_t)((r.slot * C::SFBYTES) >> 4);
+                                const uint64_t sd = sd0 + (uint64_t)(((sb.slot * C::SG + sg) * C::SFBYTES) >> 4);
 #pragma unroll
                                 for (int i = 0; i < 1 + C::BN / 128; i++) wide_cp_scales<C::PAIR>(tsf + 4 * i, sd + (uint64_t)(i * (512 >> 4)));
                                 const uint32_t d = taddr + (uint32_t)(q.slot ? C::ACC1 : 0);
@@ -1131,11 +1217,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
                                 for (int ks = 0; ks < 4; ks++) wide_mma<C::PAIR>(d, ad0 + off + 2 * ks, bd0 + off + 2 * ks, C::IDESC, ks > 0);
                             }
                             wide_commit<C::PAIR>(smem_u32(&s_empty[r.slot]));
+                            if (C::MX && sg + 1 == C::SG) wide_commit<C::PAIR>(smem_u32(&s_sempty[sb.slot]));
                             if (!C::MX || last) wide_commit<C::PAIR>(smem_u32(&s_tfull[q.slot]));
                         }
                         r.next();
                         if (!C::MX || last) q.next();
                         if (last) sums++;
+                        if (C::MX && ++sg == C::SG) {
+                            sg = 0;
+                            sb.next();
+                        }
                         any = true;
                     }
                 }
@@ -1144,6 +1235,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
                     // every MMA is done before the shared memory and the tensor memory go (bounded)
                     __syncwarp();
                     if (elect_one()) {
+                        if (C::MX && sg > 0) wide_commit<C::PAIR>(smem_u32(&s_sempty[sb.slot]));
                         if constexpr (C::PAIR)
                             asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(&s_drain)) : "memory");
                         else
@@ -1151,6 +1243,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
                     }
                     if (!mbar_wait(smem_u32(&s_drain), 0u)) *fail = 1;
                 }
+            } else if constexpr (C::MX) {
+                stage_scales(0);
             }
         } else if constexpr (!C::MX) {
             if (warp == C::EW + 2) {
@@ -1183,75 +1277,33 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
                 asm volatile("cp.async.wait_all;" ::: "memory");
             }
         } else {
-            // scales: the exponent bytes of this block's 128 rows of A and all columns' of B, by two warps in
-            // turn, each D of its stages ahead in registers
-            constexpr int D = 3;
-            int t = t0, kb = 0, n = 0, mine = warp - (C::EW + 2);    // next stage to load: its tile, block and number
-            WideTile ti = {};
-            bool live = t < total;
-            if (live) {
-                ti = tile_at(t);
-                kb = ti.k0;
-            }
-            constexpr int NV = 4 + C::BN / 32;      // values a lane: 128 rows of A, the tile's of B
-            float v[D][NV];
-            int num[D];
-            auto load = [&](float (&d)[NV]) {
-                // this warp's next stage into d; its number, -1 behind the last
-                for (;;) {
-                    while (live && kb >= ti.k1) {
-                        t += tstep;
-                        live = t < total;
-                        if (live) {
-                            ti = tile_at(t);
-                            kb = ti.k0;
+            if (warp == C::EW + 2) {
+                // the scales' float32 values, copied asynchronously up to RS stages ahead
+                Ring<C::RS> q;
+                bool ok = true;
+                for (int t = t0; t < total && ok; t += tstep) {
+                    const WideTile ti = tile_at(t);
+                    for (int kb = ti.k0; kb < ti.k1; kb++) {
+                        if (!__all_sync(0xffffffffu, ring_wait(smem_u32(&s_rempty[q.slot]), q.phase ^ 1u, fail))) {
+                            *fail = 1;
+                            ok = false;
+                            break;
                         }
+                        const uint32_t dst = raw + (uint32_t)(q.slot * C::SFBYTES + lane * 4);
+                        const float *a = p.sa + (size_t)kb * p.na, *b = p.sb + (size_t)kb * p.nb;
+#pragma unroll
+                        for (int i = 0; i < NV; i++) {
+                            const int r = (i < 4 ? ti.r0 : ti.c0 - 128) + 32 * i + lane;
+                            const bool in = r < (i < 4 ? p.na : p.nb);
+                            cp_async4(dst + 128u * i, in ? (i < 4 ? a : b) + r : p.sa, in);
+                        }
+                        cp_async_arrive(smem_u32(&s_rfull[q.slot]));
+                        q.next();
                     }
-                    if (!live) return -1;
-                    if (n == mine) break;
-                    const int skip = min(mine - n, ti.k1 - kb);
-                    n += skip;
-                    kb += skip;
                 }
-#pragma unroll
-                for (int i = 0; i < NV; i++) {
-                    const int r = (i < 4 ? ti.r0 : ti.c0 - 128) + 32 * i + lane;
-                    d[i] = r < (i < 4 ? p.na : p.nb) ? load_in(i < 4 ? p.sa + (size_t)kb * p.na + r : p.sb + (size_t)kb * p.nb + r) : 0.0f;
-                }
-                mine += 2;
-                n++;
-                kb++;
-                return n - 1;
-            };
-#pragma unroll
-            for (int d = 0; d < D; d++) num[d] = load(v[d]);
-            bool ok = true;
-            while (ok) {
-#pragma unroll
-                for (int d = 0; d < D; d++) {
-                    const int it = num[d];
-                    if (it < 0) ok = false;
-                    if (!ok) break;
-                    const int s = it % C::S;
-                    if (!__all_sync(0xffffffffu, ring_wait(smem_u32(&s_empty[s]), (uint32_t)(it / C::S + 1) & 1u, fail))) {
-                        *fail = 1;
-                        ok = false;
-                        break;
-                    }
-                    // word of row r: 16-byte line r % 32, its (r / 32) % 4-th word, 512 bytes per 128 rows
-                    const uint32_t sf = sfring + (uint32_t)(s * C::SFBYTES + lane * 16);
-#pragma unroll
-                    for (int i = 0; i < NV / 4; i++) {
-                        uint32_t b[4];
-#pragma unroll
-                        for (int k = 0; k < 4; k++) b[k] = ((__float_as_uint(v[d][4 * i + k]) >> 23) & 0xFFu) * 0x01010101u;
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sf + (uint32_t)(i * 512)), "r"(b[0]), "r"(b[1]), "r"(b[2]), "r"(b[3]) : "memory");
-                    }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    if (C::PAIR) mbar_arrive_cluster(in_leader(smem_u32(&s_sfull[s])));
-                    else mbar_arrive(smem_u32(&s_sfull[s]));
-                    num[d] = load(v[d]);
-                }
+                asm volatile("cp.async.wait_all;" ::: "memory");
+            } else {
+                stage_scales(rank);
             }
         }
     }

@@ -409,6 +409,22 @@ def test_wgrad_many_tiles_with_and_without_rows(gpu):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("blocks", [1, 2, 3, 5, 6, 7, 10, 13, 30])
+def test_wgrad_pairs_with_scales_of_every_stage(gpu, blocks):
+    """Tiles of two blocks, whose scales are staged in batches of row blocks by either block and copied to
+    the tensor cores by the first: sums of fewer, as many and more row blocks than a batch or the ring of
+    batches holds, each with scales of its own; the same bits every time."""
+    R, N, K = 128 * blocks, 2048, 1152
+    check_wgrad(gpu, R, N, K)
+    xt, xs, dyt, ds = (t.cuda() for t in wgrad_case(R, N, K, blocks))
+    off = torch.tensor([0, 0, 128 * (blocks // 2), 128 * (blocks // 2), R], dtype=torch.int32, device="cuda")
+    first = [gpu.moe_fp8_wgrad(xt, xs, dyt, ds), gpu.moe_fp8_wgrad(xt, xs, dyt, ds, offsets=off)]
+    for _ in range(10):
+        assert torch.equal(gpu.moe_fp8_wgrad(xt, xs, dyt, ds), first[0])
+        assert torch.equal(gpu.moe_fp8_wgrad(xt, xs, dyt, ds, offsets=off), first[1])
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("N,K,off", [(256, 256, None), (130, 300, None), (200, 136, [0, 2048, 2048, 4096]), (512, 500, [0, 128, 4096])])
 def test_wgrad_few_outputs_from_many_rows(gpu, N, K, off):
     """Blocks that share a tile's rows, experts with fewer row blocks than sharers and with none."""
