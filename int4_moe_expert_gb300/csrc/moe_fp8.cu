@@ -1166,6 +1166,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
                 }
             }
             if (lane == 0) s_issued = n;
+            if (C::PAIR && ok) {
+                // the first block's MMAs free this block's slots too: the last of those arrivals are in
+                // before this block ends
+                for (int i = 0; i < C::S && ok; i++) {
+                    ok = __all_sync(0xffffffffu, ring_wait(smem_u32(&s_empty[r.slot]), r.phase ^ 1u, fail));
+                    r.next();
+                }
+            }
             if (!ok) *fail = 1;
         } else if (warp == C::EW + 1) {
             // MMA issue (by the tile's first block)

@@ -449,6 +449,20 @@ def test_wgrad_long_sums_keep_float32(gpu, N, K):
 
 
 @pytest.mark.gpu
+def test_pairs_one_after_another(gpu):
+    """Short calls of both products in tiles of two blocks, each starting as the one before ends: the
+    arrivals on a block's barriers belong to its own call."""
+    xt, xs, dyt, ds = (t.cuda() for t in wgrad_case(256, 2048, 1152, 8))
+    x, xsc, w, ws = (t.cuda() for t in matmul_case(2300, 2048, 2048, 1, 8))
+    first = None
+    for _ in range(60):
+        got = [gpu.moe_fp8_wgrad(xt, xs, dyt, ds), gpu.moe_fp8_wgrad(xt[:, :128].contiguous(), xs[:1], dyt[:, :128].contiguous(), ds[:1]),
+               gpu.moe_fp8_matmul(x, xsc, w[0], ws[0]), gpu.moe_fp8_matmul(x, xsc, w[0], ws[0])]
+        first = first or got
+        assert all(torch.equal(a, b) for a, b in zip(got, first))
+
+
+@pytest.mark.gpu
 def test_wgrad_no_rows_and_nan(gpu):
     z = lambda *s: torch.zeros(*s, device="cuda")    # noqa: E731
     dw = gpu.moe_fp8_wgrad(z(16, 0).to(F8), z(0, 16), z(24, 0).to(F8), z(0, 24), offsets=torch.zeros(4, dtype=torch.int32, device="cuda"))
