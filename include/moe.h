@@ -504,6 +504,14 @@ moe_status moe_fp8_wgrad(const uint8_t *xt, const float *xt_scale, const uint8_t
  * output is invalid); returns MOE_ERR_CUDA when it was set. */
 moe_status moe_fp8_device_error(uint32_t *flags);
 
+/* Testing of the products' bounded waits (not a step of the method).  In the
+ * next moe_fp8_matmul or moe_fp8_wgrad that this host thread launches, block
+ * number `block` of each tile's (0..7; 0 where a tile has one) stops copying
+ * operands after `stages` 128-blocks: the waits for the missing ones run out
+ * (after about 0.5 s), the kernel sets the error word and returns; the call's
+ * output is invalid.  With fewer stages a block the call runs as usual. */
+moe_status moe_fp8_debug_stall_next_call(int32_t stages, int32_t block);
+
 #ifdef __cplusplus
 }
 #endif

@@ -29,7 +29,7 @@ __all__ = [
     "moe_uses_streaming_decode", "moe_streaming_decode_max_tokens", "moe_uses_tensor_cores",
     "MOE_DTYPE_F32", "MOE_DTYPE_F16", "MOE_DTYPE_BF16",
     "moe_expert_lists", "moe_balance_forward", "moe_balance_backward", "moe_fp8_quantize",
-    "moe_fp8_quantize_weights", "moe_fp8_matmul", "moe_fp8_wgrad", "moe_fp8_device_error",
+    "moe_fp8_quantize_weights", "moe_fp8_matmul", "moe_fp8_wgrad", "moe_fp8_device_error", "moe_fp8_debug_stall_next_call",
 ]
 
 MOE_OK, MOE_ERR_INVALID, MOE_ERR_CUDA, MOE_ERR_NOMEM, MOE_ERR_UNSUPPORTED = 0, 1, 2, 3, 4
@@ -138,6 +138,8 @@ def lib():
         L.moe_fp8_matmul.argtypes = [vp, vp, i32, vp, vp, i32, i32, i32, vp, vp, i32, i64, vp]
         L.moe_fp8_wgrad.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, i32, vp]
         L.moe_fp8_device_error.argtypes = [C.POINTER(C.c_uint32)]
+        L.moe_fp8_debug_stall_next_call.argtypes = [i32, i32]
+        L.moe_fp8_debug_stall_next_call.restype = C.c_int
         for name in ("moe_expert_lists", "moe_balance_forward", "moe_balance_backward", "moe_fp8_quantize",
                      "moe_fp8_quantize_weights", "moe_fp8_matmul", "moe_fp8_wgrad", "moe_fp8_device_error"):
             getattr(L, name).restype = C.c_int
@@ -479,3 +481,8 @@ def moe_fp8_device_error(check: bool = True) -> int:
     if check or st != MOE_ERR_CUDA or f.value == 0:
         _check(st, "moe_fp8_device_error")
     return f.value
+
+
+def moe_fp8_debug_stall_next_call(stages: int, block: int = 0) -> None:
+    """Testing of the block-scaled products' bounded waits: see include/moe.h."""
+    _check(lib().moe_fp8_debug_stall_next_call(stages, block), "moe_fp8_debug_stall_next_call")

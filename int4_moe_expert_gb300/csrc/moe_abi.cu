@@ -647,6 +647,13 @@ moe_status moe_fp8_wgrad(const uint8_t *xt, const float *xt_scale, const uint8_t
     return launched(moe::launch_fp8_wgrad(xt, xt_scale, dyt, dyt_scale, R, N, K, E, offsets, dw, dw_dtype, st), "moe_fp8_wgrad");
 }
 
+moe_status moe_fp8_debug_stall_next_call(int32_t stages, int32_t block) {
+    MOE_NEED(stages >= 0, MOE_ERR_INVALID, "stages=%d is negative", stages);
+    MOE_NEED(block >= 0 && block < 8, MOE_ERR_INVALID, "block=%d: need 0..7", block);
+    moe::fp8_stall_next(stages, block);
+    return MOE_OK;
+}
+
 moe_status moe_fp8_device_error(uint32_t *flags) {
     MOE_NEED(flags, MOE_ERR_INVALID, "flags is NULL");
     *flags = 0;

@@ -27,6 +27,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <climits>
 #include <cstring>
 #include <type_traits>
 
@@ -54,6 +55,7 @@ struct NarrowArgs {
     int E;
     int out_dtype;
     unsigned *err;
+    int stall, stall_block;       // testing: this block of every tile's stops copying after `stall` stages
 };
 
 template <bool SPLIT_>
@@ -258,6 +260,13 @@ __device__ __forceinline__ float ld_peer(uint32_t addr) {
     return v;
 }
 
+__device__ __forceinline__ void st_peer(uint32_t addr, int v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+// counts `bytes` as copied on this block's barrier
+__device__ __forceinline__ void mbar_complete_tx(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ float4 ld_peer4(uint32_t addr) {
     float4 v;
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
@@ -452,11 +461,14 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) fp8_narrow_kernel(const
         if (warp == C::EW) {
             // tensor copies
             Ring<C::S> r;
-            bool ok = true;
+            bool ok = true, stalled = false;
             int n = 0;
-            for (int t = t0; t < total && ok; t += tstep) {
+            const int most = (int)crank == p.stall_block ? p.stall : INT_MAX;
+            for (int t = t0; t < total && ok && !stalled; t += tstep) {
                 Tile ti = walk.at(t);
                 part(ti);
+                stalled = ti.k1 - ti.k0 > most - n;
+                if (stalled) ti.k1 = ti.k0 + most - n;
                 for (int kb = ti.k0; kb < ti.k1; kb++) {
                     // a fresh ring's slots pass: the phase before the first is over
                     if (!__all_sync(0xffffffffu, ring_wait(smem_u32(&s_empty[r.slot]), r.phase ^ 1u, fail))) {
@@ -711,6 +723,7 @@ struct WideArgs {
     int na, nb, nkb, E, out_dtype;
     int vec;                              // every output row starts on a 16-byte boundary (2: and the tensor copies can take it)
     unsigned *err;
+    int stall, stall_block;               // as in NarrowArgs
 };
 
 // rows [r0, rend) (this block's 128), columns c0.., inner blocks [k0, k1) of expert e
@@ -902,7 +915,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
     __shared__ float s_scale[C::MX ? 1 : C::SS][128], s_wscale[C::MX ? 1 : C::SS][2];   // matmul: rows', weight blocks'
     __shared__ int s_first[C::MX ? 1 : kMaxExperts + 1];
     __shared__ uint32_t s_taddr;
-    __shared__ int s_fail, s_issued;
+    __shared__ int s_fail, s_issued, s_peer_issued;
     __shared__ __align__(8) unsigned long long s_rfull[C::MX ? C::RS : 1], s_rempty[C::MX ? C::RS : 1];
     static_assert(C::SB <= C::SS, "barriers for every batch of scales");
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -1144,11 +1157,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
         if (warp == C::EW) {
             // tensor copies: this block's rows of A and its part of B
             Ring<C::S> r;
-            bool ok = true;
+            bool ok = true, stalled = false;
             int n = 0;
+            const int most = rank + crank == p.stall_block ? p.stall : INT_MAX;
             const uint32_t full0 = C::PAIR ? in_leader(smem_u32(&s_full[0])) : smem_u32(&s_full[0]);
-            for (int t = t0; t < total && ok; t += tstep) {
-                const WideTile ti = tile_at(t);
+            for (int t = t0; t < total && ok && !stalled; t += tstep) {
+                WideTile ti = tile_at(t);
+                stalled = ti.k1 - ti.k0 > most - n;
+                if (stalled) ti.k1 = ti.k0 + most - n;
                 for (int kb = ti.k0; kb < ti.k1; kb++) {
                     // a fresh ring's slots pass: the phase before the first is over
                     if (!__all_sync(0xffffffffu, ring_wait(smem_u32(&s_empty[r.slot]), r.phase ^ 1u, fail))) {
@@ -1166,7 +1182,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
                 }
             }
             if (lane == 0) s_issued = n;
-            if (C::PAIR && ok) {
+            if (C::PAIR && ok && !stalled) {
                 // the first block's MMAs free this block's slots too: the last of those arrivals are in
                 // before this block ends
                 for (int i = 0; i < C::S && ok; i++) {
@@ -1317,10 +1333,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
     }
     __syncthreads();
     if (s_fail && tid == 0) {
-        // after a wait that ran out: copies still in flight land before the shared memory goes (bounded)
-        if (rank == 0)
+        if (C::PAIR) {      // the other block gives up too (below)
+            st_peer(peer_addr(smem_u32(&s_fail), (uint32_t)(rank ^ 1)), 1);
+        } else {
+            // after a wait that ran out: copies still in flight land before the shared memory goes (bounded)
             for (int i = max(0, s_issued - C::S); i < s_issued; i++) mbar_wait(smem_u32(&s_full[i % C::S]), (uint32_t)(i / C::S) & 1u);
-        atomicOr(p.err, MOE_DEVICE_ERR_TC);
+            atomicOr(p.err, MOE_DEVICE_ERR_TC);
+        }
     }
     if constexpr (C::SPLIT) {
         // sums of all blocks of the cluster, in block order: block r adds rows r, r + csize, ..., a warp a
@@ -1363,7 +1382,25 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
-    if (C::PAIR) cluster_sync_all();     // the other block's MMAs, copies and arrivals reach into this one's memory
+    if constexpr (C::PAIR) {
+        cluster_sync_all();     // the other block's MMAs, copies and arrivals reach into this one's memory
+        if (s_fail) {
+            // A wait ran out.  Both blocks' copies in flight land before the shared memory goes (bounded): they
+            // count on the first block's barriers, which makes up for the stages that one block alone began
+            if (rank == 1 && tid == 0) st_peer(peer_addr(smem_u32(&s_peer_issued), 0u), s_issued);
+            cluster_sync_all();
+            if (rank == 0 && tid == 0) {
+                const int lo = min(s_issued, s_peer_issued), hi = max(s_issued, s_peer_issued);
+                for (int i = lo; i < hi; i++) {
+                    if (hi == s_issued) mbar_complete_tx(smem_u32(&s_full[i % C::S]), C::STAGE);
+                    else mbar_expect_tx(smem_u32(&s_full[i % C::S]), C::STAGE);
+                }
+                for (int i = max(0, hi - C::S); i < hi; i++) mbar_wait(smem_u32(&s_full[i % C::S]), (uint32_t)(i / C::S) & 1u);
+                atomicOr(p.err, MOE_DEVICE_ERR_TC);
+            }
+            cluster_sync_all();
+        }
+    }
     if (warp == C::EW + 3) {
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         if constexpr (C::PAIR) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(taddr) : "memory");
@@ -1779,6 +1816,19 @@ cudaError_t error_word(unsigned **err) {
     return cudaSuccess;
 }
 
+// what moe_fp8_debug_stall_next_call asked of this thread's next product
+struct Stall {
+    int stages, block;
+};
+constexpr Stall kNoStall = {INT_MAX, 0};
+thread_local Stall t_stall = kNoStall;
+template <class Args>
+void take_stall(Args &p) {
+    p.stall = t_stall.stages;
+    p.stall_block = t_stall.block;
+    t_stall = kNoStall;
+}
+
 // grid: blocks (of clusters of `cluster`); the B map's box is the tile's columns
 template <class C>
 cudaError_t launch_narrow(const NarrowArgs &p, const CUtensorMap &am, const uint8_t *b, uint64_t b_cols, uint64_t b_rows,
@@ -1844,6 +1894,7 @@ cudaError_t launch_fp8_matmul(const uint8_t *x, const float *xs, int R, const ui
     if (e != cudaSuccess) return e;
     CUtensorMap am;
     if (!tmap(&am, 3, w, K, N, E, kARows)) return cudaErrorInvalidValue;
+    take_stall(p);
     const long long nat = (N + kARows - 1) / kARows;
     const int used = offsets ? (E < R ? E : R) : 1;      // weight matrices that rows can belong to
     const int each = (R + used - 1) / used;
@@ -1869,6 +1920,8 @@ cudaError_t launch_fp8_matmul(const uint8_t *x, const float *xs, int R, const ui
     q.out_dtype = y_dtype;
     q.vec = rows_aligned(y, ldy, y_dtype);
     q.err = p.err;
+    q.stall = p.stall;
+    q.stall_block = p.stall_block;
     auto wide_tiles = [&](int rows, int bn, int per_expert) {      // at most (2) or expected (1: half a tile more an expert)
         return (long long)((N + bn - 1) / bn) * (offsets ? (long long)R / rows + (used * per_expert + 1) / 2 : ((long long)R + rows - 1) / rows);
     };
@@ -1912,6 +1965,7 @@ cudaError_t launch_fp8_wgrad(const uint8_t *xt, const float *xs, const uint8_t *
     p.vec = rows_aligned(dw, K, dw_dtype);
     const cudaError_t e = error_word(&p.err);
     if (e != cudaSuccess) return e;
+    take_stall(p);
     auto tiles = [&](int rows, int bn) { return (long long)E * ((N + rows - 1) / rows) * ((K + bn - 1) / bn); };
     // Few outputs from many rows: 128 x 128 tiles, whose inner range a cluster shares, all at once (clusters
     // of eight fit about 14 times); else a pair's 256 x 256 tiles.  Estimated in us from measurements: a
@@ -1930,6 +1984,8 @@ cudaError_t launch_fp8_wgrad(const uint8_t *xt, const float *xs, const uint8_t *
     if (split > 1 && 0.31 * per / split + 2.5 < pair) return go(WideCfg<false, true, 128, true>{}, split);
     return go(WideCfg<true, true>{}, 1);
 }
+
+void fp8_stall_next(int stages, int block) { t_stall = {stages, block}; }
 
 cudaError_t fp8_error_read(unsigned *flags) {
     unsigned *word = nullptr;

@@ -201,5 +201,6 @@ cudaError_t launch_fp8_matmul(const uint8_t *x, const float *xs, int R, const ui
 cudaError_t launch_fp8_wgrad(const uint8_t *xt, const float *xs, const uint8_t *dyt, const float *dys, int R, int N, int K, int E,
                              const int *offsets, void *dw, int dw_dtype, cudaStream_t st);
 cudaError_t fp8_error_read(unsigned *flags);
+void fp8_stall_next(int stages, int block);
 
 }  // namespace moe

@@ -1,5 +1,7 @@
 """Block-scaled e4m3 quantisers and products (moe_fp8_*): refusals on the host; on the GPU, codes bit
 for bit against a plain 64-bit quantiser and products against 64-bit sums of the codes' values."""
+import time
+
 import numpy as np
 import pytest
 
@@ -69,6 +71,12 @@ def test_product_refusals(moe):
         assert wg(**kw) == moe.MOE_ERR_UNSUPPORTED, kw
     assert "need" in moe.moe_last_error()
     assert L.moe_fp8_device_error(None) == moe.MOE_ERR_INVALID
+
+
+def test_stall_refusals(moe):
+    f = moe.lib().moe_fp8_debug_stall_next_call
+    for a in ((-1, 0), (0, -1), (0, 8)):
+        assert f(*a) == moe.MOE_ERR_INVALID, a
 
 
 # ------------------------------------------------------------------------------------------------ quantisers
@@ -482,6 +490,45 @@ def test_wgrad_bad_offsets_stay_in_bounds(gpu):
     for off in ([-128, 130, 2**31 - 1, 100], [512, 0, -2**31, 2**31 - 1]):
         gpu.moe_fp8_wgrad(xt.cuda(), xs.cuda(), dyt.cuda(), ds.cuda(), offsets=torch.tensor(off, dtype=torch.int32, device="cuda"), out=pool[1:4])
         assert bool((pool[0] == 7).all()) and bool((pool[4] == 7).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("op,R,N,K,E,blocks,stalls", [
+    ("matmul", 700, 640, 1152, 48, (0,), (0, 4, 7)),          # 16-row tiles
+    ("matmul", 1, 640, 4096, 1, (0, 3), (0, 3)),              # shared by a cluster
+    ("matmul", 200, 640, 2048, 1, (0, 3), (0, 2)),            # 128 x 128, shared
+    ("matmul", 700, 1300, 1024, 1, (0,), (0, 6)),             # 128 x 128
+    ("matmul", 2300, 1300, 1280, 1, (0,), (0, 2, 8)),         # 128 x 256
+    ("matmul", 2300, 2048, 2048, 1, (0, 1), (0, 3, 9)),       # a pair's 256 x 256
+    ("wgrad", 1664, 2048, 1152, 1, (0, 1), (0, 3, 9)),        # a pair's
+    ("wgrad", 4096, 256, 256, 1, (0, 5), (0, 3))])            # 128 x 128, shared
+def test_waits_that_run_out_end_the_call(gpu, op, R, N, K, E, blocks, stalls):
+    """A block that stops copying its operands: the waits for them give up after half a second (no fault, no
+    hang), the call returns and reports the flag, and the next calls are right again."""
+    if op == "matmul":
+        x, xs, w, ws = (t.cuda() for t in matmul_case(R, N, K, E, 1))
+        off = torch.arange(E + 1, device="cuda").mul_(R).div_(E, rounding_mode="floor").int()
+        call = lambda: gpu.moe_fp8_matmul(x, xs, w, ws, offsets=off)        # noqa: E731
+    else:
+        xt, xs, dyt, ds = (t.cuda() for t in wgrad_case(R, N, K, 1))
+        call = lambda: gpu.moe_fp8_wgrad(xt, xs, dyt, ds)                    # noqa: E731
+    want = call()
+    assert gpu.moe_fp8_device_error() == 0
+    for block in blocks:
+        for stages in stalls:
+            gpu.moe_fp8_debug_stall_next_call(stages, block)
+            t0 = time.perf_counter()
+            call()
+            torch.cuda.synchronize()
+            waited = time.perf_counter() - t0
+            assert gpu.moe_fp8_device_error(check=False) == gpu.MOE_DEVICE_ERR_TC, (block, stages)
+            assert waited < 10.0, waited
+            assert gpu.moe_fp8_device_error() == 0               # cleared by the read
+            for _ in range(2):
+                assert torch.equal(call(), want), (block, stages)
+            assert gpu.moe_fp8_device_error() == 0
+    gpu.moe_fp8_debug_stall_next_call(1000, 0)               # more stages than a block has: the usual call
+    assert torch.equal(call(), want) and gpu.moe_fp8_device_error() == 0
 
 
 @pytest.mark.gpu
