@@ -617,6 +617,10 @@ __global__ void __launch_bounds__(kBalThreads) balance_grad_kernel(const BalArgs
 #pragma unroll
                     for (int j = 0; j < J; j++) x[u][j] = pr[j] * (c[j] - dot) * c1[j];
                 }
+                if (p.mask && !on[u]) {      // zeros whatever the counts are multiplied by: 0 times an infinite gradient is none
+#pragma unroll
+                    for (int j = 0; j < J; j++) x[u][j] = 0.0f;
+                }
                 if (tt < b) L::store(out + (long long)tt * p.ldd, p.E, l, x[u]);
             }
         }

@@ -320,6 +320,30 @@ def test_balance_infinities_and_masked_nans(gpu, score):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("score", [0, 1])
+@pytest.mark.parametrize("E,dtype", [(8, torch.float32), (13, torch.bfloat16), (64, torch.bfloat16), (300, torch.float16), (1024, torch.float32)])
+@pytest.mark.parametrize("g", [float("inf"), -float("inf"), float("nan"), 3e38])
+def test_balance_masked_rows_are_zeros_for_any_upstream_gradient(gpu, score, E, dtype, g):
+    """An upstream gradient that overflowed: zeros in masked rows (and outside the segments), the formula's
+    infinities and NaN in the others."""
+    T, K = 77, 4
+    x, idx = router(T, E, K, 5, dtype)
+    mask = torch.rand(T, generator=torch.Generator().manual_seed(6)) < 0.6
+    mask[60:70] = False                                       # a segment without a token left
+    x[~mask] = float("nan")
+    seq = torch.tensor([3, 20, 60, 70, 75], dtype=torch.int32, device="cuda")
+    x, idx, m = x.cuda(), idx.cuda(), mask.cuda()
+    _, counts, _, tokens = gpu.moe_balance_forward(x, idx, 0.5, score, seq_offsets=seq, mask=m)
+    up = torch.tensor([g], device="cuda")
+    d = gpu.moe_balance_backward(x, K, counts, tokens, 0.5, score, seq_offsets=seq, mask=m, grad_loss=up)
+    inside = torch.zeros(T, dtype=torch.bool)
+    inside[3:75] = True
+    assert bool((d.cpu()[~mask | ~inside] == 0).all())
+    if g != 3e38:
+        assert not bool(d.cpu()[mask & inside].float().isfinite().all(1).any())
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("pad,shift", [(0, 1), (3, 0), (4, 4), (8, 0)])
 def test_balance_strided_rows(gpu, dtype, pad, shift):
