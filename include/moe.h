@@ -476,7 +476,9 @@ moe_status moe_fp8_quantize_weights(const void *w, int32_t dtype, int32_t E, int
 /* y[r, n] = sum_b x_scale[b, r] w_scale[e, n / 128, b] sum_{k in block b} x[r, k] w[e, n, k]
  * over the 128-blocks b of the inner axis, in float32, rounded once to y's
  * dtype: x[R, K] and w[E, N, K] e4m3 codes, x_scale[ceil(K / 128), R] and
- * w_scale[E, ceil(N / 128), ceil(K / 128)] any float32 values.  With offsets
+ * w_scale[E, ceil(N / 128), ceil(K / 128)] any float32 values (rows with a pair
+ * of scales whose product overflows float32, or loses bits below its normal
+ * range, take much longer).  With offsets
  * (device int32 [E + 1], ascending) row r belongs to the expert e with
  * offsets[e] <= r < offsets[e + 1]; rows outside every segment are left as they
  * are in y.  offsets NULL: E = 1, every row.  y[R, N], rows ldy elements apart.

@@ -198,6 +198,52 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
+// The two scales of a block's sum, whose product may lie outside float32's normal range although the
+// scaled sum lies inside: the sum times f, times p, times q, of which f keeps the mantissas, so that
+// only the last product can overflow or lose bits.
+struct FarScale {
+    float f, p, q;
+    __device__ __forceinline__ FarScale(float a, float b) {
+        int e = 0;
+        f = mantissa(a, e) * mantissa(b, e);
+        e = min(max(e, -250), 250);      // beyond it any sum but 0 leaves float32 (they lie between 2^-18 and 2^25)
+        p = __uint_as_float((unsigned)(127 + e / 2) << 23);
+        q = __uint_as_float((unsigned)(127 + e - e / 2) << 23);
+    }
+    // v / 2^e in [1, 2), e added to `e`; 0, infinities and NaN as they are
+    static __device__ __forceinline__ float mantissa(float v, int &e) {
+        if (fabsf(v) < 0x1p-126f) {
+            v *= 0x1p24f;
+            e -= 24;
+        }
+        const uint32_t u = __float_as_uint(v);
+        if (v == 0.0f || (u & 0x7F800000u) == 0x7F800000u) return v;
+        e += (int)((u >> 23) & 0xFFu) - 127;
+        return __uint_as_float((u & 0x807FFFFFu) | 0x3F800000u);
+    }
+    __device__ __forceinline__ uint32_t times(uint32_t sum) const { return __float_as_uint(__uint_as_float(sum) * f * p * q); }
+};
+__device__ __forceinline__ bool is_finite(float v) { return (__float_as_uint(v) & 0x7F800000u) != 0x7F800000u; }
+// kFar or more: not a normal number
+constexpr uint32_t kFar = 0xFE000000u;
+__device__ __forceinline__ uint32_t farness(float product) { return 2u * __float_as_uint(product) - 0x01000000u; }
+// the product of two numbers overflows, or loses bits below the normal range (that of powers of two hardly does)
+__device__ __forceinline__ bool far_scales(float a, float b) {
+    const float f = a * b;
+    return farness(f) >= kFar && a != 0.0f && b != 0.0f && is_finite(a) && is_finite(b) && (!is_finite(f) || a * 0x1p48f * b != f * 0x1p48f);
+}
+// c and the products of four e4m3 codes
+__device__ __forceinline__ float dot4(uint32_t a, uint32_t b, float c) {
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        uint32_t u, v;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(u) : "h"((uint16_t)(a >> (16 * i))));
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(v) : "h"((uint16_t)(b >> (16 * i))));
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&u)), g = __half22float2(*reinterpret_cast<const __half2 *>(&v));
+        c = fmaf(f.x, g.x, fmaf(f.y, g.y, c));
+    }
+    return c;
+}
 __device__ __forceinline__ void lds_2x64(uint32_t addr, uint64_t &a, uint64_t &b) {
     asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr) : "memory");
 }
@@ -427,12 +473,21 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) fp8_narrow_kernel(const
                 // the accumulator is in registers: the slot may be written again
                 asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
                 if (lane == 0) mbar_arrive(smem_u32(&s_tempty[q]));
+                const float mine = s_scale[s][lane % C::BT], wscale = __uint_as_float(f);
+                if (__any_sync(0xffffffffu, farness(mine * wscale) >= kFar && mine != 0.0f && wscale != 0.0f)) {
 #pragma unroll
-                for (int i = 0; i < C::BT; i += 4) {
-                    uint64_t s0, s1;
-                    lds_2x64(sc + 4u * i, s0, s1);
-                    acc[i / 2] = fma2(pack2(r[i], r[i + 1]), mul2(s0, ws), acc[i / 2]);
-                    acc[i / 2 + 1] = fma2(pack2(r[i + 2], r[i + 3]), mul2(s1, ws), acc[i / 2 + 1]);
+                    for (int i = 0; i < C::BT; i += 2) {
+                        const FarScale a(s_scale[s][i], wscale), b(s_scale[s][i + 1], wscale);
+                        acc[i / 2] = add2(acc[i / 2], pack2(a.times(r[i]), b.times(r[i + 1])));
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < C::BT; i += 4) {
+                        uint64_t s0, s1;
+                        lds_2x64(sc + 4u * i, s0, s1);
+                        acc[i / 2] = fma2(pack2(r[i], r[i + 1]), mul2(s0, ws), acc[i / 2]);
+                        acc[i / 2 + 1] = fma2(pack2(r[i + 2], r[i + 3]), mul2(s1, ws), acc[i / 2 + 1]);
+                    }
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&s_sempty[s]));
@@ -715,6 +770,8 @@ __device__ __forceinline__ void wide_cp_scales(uint32_t taddr, uint64_t desc) {
 constexpr int kFlush = 16;
 
 struct WideArgs {
+    const uint8_t *a, *b;   // matmul: the codes [na][K], [E][nb][K]
+    int K;
     const float *sa;        // row scales of A [nkb][na] (wgrad: power of two)
     const float *sb;        // matmul: block scales of B [E][ceil(nb / 128)][nkb]; wgrad: row scales [nkb][nb]
     const int *offsets;     // [E + 1] or NULL
@@ -903,6 +960,35 @@ __device__ __forceinline__ void store_async(const uint64_t (&v)[64], uint32_t st
     }
 }
 
+// The outputs of those of a warp's 32 rows that have far scales, once more: each block's sum in float32 by
+// ordinary instructions, scaled without an intermediate value that leaves float32's range.  Such scales
+// are rare (gradients next to either end of the range), and a second way through the loop over the blocks
+// costs the usual one moves of its sums: 16381 x 4096 x 6144 281 -> 345 us, against no more time for
+// one maximum of the products' farness in the loop.  Called once no other role waits for this warp.
+// x, xs: the first row's codes and scale (block kb's at xs + kb na); w, ws: the first column's
+__device__ __noinline__ void far_rows(const uint8_t *x, const float *xs, int na, const uint8_t *w, const float *ws, int K, int k0, int k1, int rows,
+                                      int cols, void *out, long long ldo, int dtype, int lane) {
+    bool mine = false;
+#pragma unroll 4
+    for (int kb = k0; kb < (lane < rows ? k1 : k0); kb++) mine |= far_scales(load_in(xs + (size_t)kb * na + lane), load_in(ws + kb));
+    for (unsigned todo = __ballot_sync(0xffffffffu, mine); todo; todo &= todo - 1) {
+        const int r = __ffs(todo) - 1;
+        for (int c = lane; c < cols; c += 32) {
+            float sum = 0.0f;
+            for (int kb = k0; kb < k1; kb++) {
+                float s = 0.0f;
+                for (int k = kb * kKB; k < min((kb + 1) * kKB, K); k += 16) {
+                    const uint4 a = load_in(reinterpret_cast<const uint4 *>(x + (size_t)r * K + k)), b = load_in(reinterpret_cast<const uint4 *>(w + (size_t)c * K + k));
+                    s = dot4(a.x, b.x, dot4(a.y, b.y, dot4(a.z, b.z, dot4(a.w, b.w, s))));
+                }
+                sum += __uint_as_float(FarScale(load_in(xs + (size_t)kb * na + r), load_in(ws + kb)).times(__float_as_uint(s)));
+            }
+            store_out(out, (long long)r * ldo + c, sum, dtype);
+        }
+    }
+    __syncwarp();
+}
+
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_constant__ CUtensorMap amap,
                                                                  const __grid_constant__ CUtensorMap bmap,
@@ -1062,10 +1148,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
                 else mbar_arrive(te0 + 8u * q);
             }
         };
+        [[maybe_unused]] auto w_scales = [&](const WideTile &ti, int c0) { return p.sb + ((size_t)ti.e * ((p.nb + kKB - 1) / kKB) + c0 / kKB) * p.nkb; };
+        [[maybe_unused]] float *ring_out = reinterpret_cast<float *>(smem_raw + (ring - smem_u32(smem_raw)));
         Ring<C::NT> tq;
         Ring<C::SS> ts;
         int done = 0;
-        bool ok = true;
+        bool ok = true, far = false;      // far: of a row of this lane's (matmul)
         for (int t = t0; t < total && ok; t += tstep) {
             const WideTile ti = tile_at(t);
             const int row = ti.r0 + 32 * q4, rows = ti.rend - row, c0 = ti.c0 + C::WC * half, cols = p.nb - c0;
@@ -1104,6 +1192,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
                 }
             } else {
                 uint64_t acc[C::WC / 2];
+                uint32_t worst = 0;      // farness of the scales
 #pragma unroll
                 for (int i = 0; i < C::WC / 2; i++) acc[i] = 0ull;
                 for (int kb = ti.k0; kb < ti.k1; kb++) {
@@ -1117,8 +1206,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
                     tq.next();
                     ts.next();
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                    const uint32_t f = __float_as_uint(s_scale[s][32 * q4 + lane] * s_wscale[s][C::WC * half / kKB]);
+                    const float xscale = s_scale[s][32 * q4 + lane], wscale = s_wscale[s][C::WC * half / kKB];
+                    const uint32_t f = __float_as_uint(xscale * wscale);
                     const uint64_t sc = pack2(f, f);
+                    worst = max(worst, farness(__uint_as_float(f)));
                     const uint32_t base = trow + (uint32_t)(C::BN * q + C::WC * half);
 #pragma unroll
                     for (int l = 0; l < C::WC / 64; l++) {
@@ -1132,9 +1223,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
                     if (lane == 0) mbar_arrive(smem_u32(&s_sempty[s]));
                 }
                 if (!ok) break;
+                far |= worst >= kFar && lane < rows && cols > 0;
                 if constexpr (C::SPLIT) {
                     // partial sums [row][column] over the stage ring: every copy into it was consumed
                     partial_64(acc, ring + (uint32_t)((32 * q4 + lane) * C::PLD + C::WC * half) * 4u);
+                    __syncwarp();
+                    if (__any_sync(0xffffffffu, far))
+                        far_rows(p.a + (size_t)row * p.K, p.sa + row, p.na, p.b + ((size_t)ti.e * p.nb + c0) * p.K, w_scales(ti, c0), p.K, ti.k0, ti.k1,
+                                 rows, min(cols, C::WC), ring_out + (32 * q4) * C::PLD + C::WC * half, C::PLD, MOE_DTYPE_F32, lane);
                 } else if (C::TST && p.vec == 2 && rows >= 32 && cols >= 128) {
                     if constexpr (C::TST) {
                         if (p.out_dtype == MOE_DTYPE_F32) store_async<float>(acc, stage, &omap, row, c0, lane);
@@ -1152,6 +1248,19 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_wide_kernel(const __grid_co
             }
         }
         if (C::TST && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        if (!C::MX && !C::SPLIT && ok && __any_sync(0xffffffffu, far)) {
+            // once no other role waits for this one
+            __syncwarp();
+            walk.e = 0;
+            for (int t = t0; t < total; t += tstep) {
+                const WideTile ti = tile_at(t);
+                const int row = ti.r0 + 32 * q4, rows = ti.rend - row, c0 = ti.c0 + C::WC * half, cols = p.nb - c0;
+                if (rows > 0 && cols > 0)
+                    far_rows(p.a + (size_t)row * p.K, p.sa + row, p.na, p.b + ((size_t)ti.e * p.nb + c0) * p.K, w_scales(ti, c0), p.K, ti.k0, ti.k1,
+                             rows, min(cols, C::WC), static_cast<char *>(p.out) + ((long long)row * p.ldo + c0) * (p.out_dtype == MOE_DTYPE_F32 ? 4 : 2), p.ldo,
+                             p.out_dtype, lane);
+            }
+        }
     } else {
         if constexpr (C::BIGREG) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == C::EW) {
@@ -1908,6 +2017,9 @@ cudaError_t launch_fp8_matmul(const uint8_t *x, const float *xs, int R, const ui
         return launch_narrow<NarrowCfg<false>>(p, am, x, K, R, most, 2, 1, st);
     }
     WideArgs q = {};
+    q.a = x;
+    q.b = w;
+    q.K = K;
     q.sa = xs;
     q.sb = ws;
     q.offsets = offsets;

@@ -346,6 +346,56 @@ def test_matmul_keeps_rows_apart(gpu, R):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("R,N,K,E", [(3, 300, 400, 1), (40, 200, 272, 5), (60, 640, 1168, 1), (200, 640, 2048, 1), (700, 1300, 1024, 1),
+                                     (2300, 1300, 1280, 1), (2300, 2048, 2048, 1)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_matmul_scales_whose_product_leaves_float32(gpu, R, N, K, E, dtype):
+    """Scales as small and as large as float32 has them: their product alone may be subnormal, zero or
+    infinite where the scaled sum is an ordinary number (or 0)."""
+    g = torch.Generator().manual_seed(R + N)
+    kb, nb = -(-K // B), -(-N // B)
+    small = (2.0 ** -6 * torch.randn(E, N, K, generator=g)).clamp(-0.0625, 0.0625)
+    x, w = codes_of(g, R, K).float(), small.to(F8)
+    xe, we = torch.randint(-4, 3, (kb, R), generator=g).float(), torch.randint(-8, 0, (E, nb, kb), generator=g).float()
+    far = torch.arange(R) % 5
+    x[far == 1] = 2.0 ** -9 * torch.randint(-1, 2, (int((far == 1).sum()), K), generator=g).float()       # tiny sums, some of them 0
+    x[far == 2] = 0.0
+    xe[:, far == 1] = 100.0 + torch.randint(0, 4, (kb, int((far == 1).sum())), generator=g)
+    xe[:, far == 2] = 120.0
+    xe[:, far == 3] = -126.0
+    xe[:, far == 4] = -149.0 + 24
+    we[:, :, ::2] = 30.0                                    # every other block: 2^130 with the rows of sums of 2^-9 2^-6 n
+    we[:, :, 1::4] = -20.0
+    xs, ws = torch.exp2(xe) * (1 + torch.rand(kb, R, generator=g)), torch.exp2(we) * (1 + torch.rand(E, nb, kb, generator=g))
+    xs[:, far == 4] = torch.where(torch.rand(kb, int((far == 4).sum()), generator=g) < 0.5, xs[:, far == 4] * 2.0 ** -20, xs[:, far == 4])    # subnormal
+    x = x.to(F8)
+    off = [R * e // E for e in range(E + 1)]
+    ref, size = matmul_ref(x, xs, w, ws, off)
+    assert float(ref.abs().max()) < torch.finfo(dtype).max / 4 and bool((ref[far == 2] == 0).all())
+    y = gpu.moe_fp8_matmul(x.cuda(), xs.cuda(), w.cuda(), ws.cuda(), offsets=torch.tensor(off, dtype=torch.int32, device="cuda"), out_dtype=dtype)
+    close(y, ref, size, K, dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("R,N,K", [(5, 200, 272), (300, 640, 400), (2300, 2048, 2048)])
+def test_matmul_of_the_smallest_quantised_rows(gpu, R, N, K):
+    """Rows whose scale is the quantiser's least, 2^-126, with weights' scales below 1: the products are
+    subnormal powers of two.  Others with a scale that is none (NaN rows), which stay NaN."""
+    g = torch.Generator().manual_seed(R)
+    x = torch.randn(R, K, generator=g) * torch.exp2(torch.randint(-127, -116, (R, 1), generator=g).float())
+    x[1] = float("inf")
+    w = 0.02 * torch.randn(N, K, generator=g)
+    q, s = gpu.moe_fp8_quantize(x.cuda())
+    wq, wscale = gpu.moe_fp8_quantize_weights(w.cuda())
+    y = gpu.moe_fp8_matmul(q, s, wq, wscale, out_dtype=torch.float32)
+    keep = torch.arange(R) != 1
+    assert bool(y[1].isnan().all())
+    ref, size = matmul_ref(q.float().cpu()[keep], s.cpu()[:, keep], wq.float().cpu()[None], wscale.cpu()[None], [0, R - 1])
+    assert float(s[:, 0].min()) >= 2.0 ** -126 and bool((s == 2.0 ** -126).any())
+    close(y[keep.cuda()], ref, size, K, torch.float32)
+
+
+@pytest.mark.gpu
 def test_matmul_bad_offsets_stay_in_bounds(gpu):
     """Offsets outside the rows or falling are cut to the rows: nothing else is read or written."""
     x, xs, w, ws = matmul_case(100, 136, 144, 3, 1)
