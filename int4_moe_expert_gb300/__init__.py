@@ -405,6 +405,10 @@ def _native():
         import importlib.machinery
         import importlib.util
         import torch  # noqa: F401  (its libraries come first)
+        from . import _build
+        if _build.binding_built_for() != _build.binding_key():
+            raise RuntimeError(f"{path} was built for {_build.binding_built_for()}, this is {_build.binding_key()}: "
+                               "build it again with `python -c 'import __graft_entry__ as g; g.build()'`")
         spec = importlib.util.spec_from_file_location("_moe_torch", path, loader=importlib.machinery.ExtensionFileLoader("_moe_torch", str(path)))
         m = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(m)
