@@ -32,7 +32,7 @@ struct ListArgs {
     int *counts, *offsets, *rows, *pos;
     int *hist;          // [blocks][E] (more than one block)
     long long pairs, room;
-    int K, E, align, chunk, blocks, small;   // small: pair numbers fit 32 bits
+    int K, E, align, chunk, blocks;
 };
 
 __device__ __forceinline__ int pair_expert(const ListArgs &p, long long i, long long end) {
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kListThreads, 1) lists_kernel(const ListArgs p
             if (j < whi) {
                 if (e >= 0) at += off[e];
                 p.pos[j] = e >= 0 ? at : -1;
-                if (e >= 0) p.rows[at] = p.small ? (int)((unsigned)j / (unsigned)p.K) : (int)(j / p.K);
+                if (e >= 0) p.rows[at] = (int)((unsigned)j / (unsigned)p.K);      // below 2^31, as the rows are
             }
             __syncwarp();
         }
@@ -678,7 +678,7 @@ size_t lists_workspace(long long pairs, int E) {
 
 cudaError_t launch_lists(const int *idx, int T, int K, int E, int align, long long room, int *counts, int *offsets, int *rows,
                          int *pos, void *ws, cudaStream_t st) {
-    ListArgs p = {idx, counts, offsets, rows, pos, static_cast<int *>(ws), (long long)T * K, room, K, E, align, 0, 1, (long long)T * K < (1ll << 31)};
+    ListArgs p = {idx, counts, offsets, rows, pos, static_cast<int *>(ws), (long long)T * K, room, K, E, align, 0, 1};
     p.blocks = lists_blocks(p.pairs);
     p.chunk = (int)((p.pairs + p.blocks - 1) / p.blocks);
     if (p.blocks > 1) {
