@@ -377,6 +377,34 @@ def test_matmul_scales_whose_product_leaves_float32(gpu, R, N, K, E, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("R,N,K", [(1, 512, 6144), (16, 4096, 6144), (128, 1024, 6144), (512, 2000, 6144), (1500, 4096, 4096), (2300, 2048, 6144)])
+def test_matmul_error_in_the_2_norm(gpu, R, N, K):
+    """Random signs: a block's 4 truncated steps are off by 4 x 2^-23 of its sum at most, and the nb float32
+    additions of the blocks by 2^-24 of running sums, whose roots of the sums of squares make
+    sqrt(nb / 2) of the last one's: with 48 blocks 13 x 2^-24 in all."""
+    x, xs, w, ws = (t.cuda() for t in matmul_case(R, N, K, 1, 4))
+    xs.fill_(0.75), ws.fill_(0.0013)
+    y = gpu.moe_fp8_matmul(x, xs, w[0], ws[0], out_dtype=torch.float32)
+    ref = (x.double() @ w[0].double().t()) * (xs[0, 0].double() * ws[0, 0, 0].double())
+    assert float((y.double() - ref).norm() / ref.norm()) <= 16 * 2.0 ** -24
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("R,E,most", [(4000, 300, 4000), (16384, 1024, 15000), (9000, 8, 8993), (20000, 64, 12345)])
+def test_matmul_skewed_routing(gpu, R, E, most):
+    """One expert has nearly all rows, so that the rows of an expert on average say little."""
+    N, K = 200, 272
+    x, xs, w, ws = (t.cuda() for t in matmul_case(R, N, K, E, 3))
+    g = torch.Generator().manual_seed(R)
+    counts = torch.bincount(torch.randint(0, E, (R - most,), generator=g), minlength=E)
+    counts[E // 2] += most
+    off = [0] + counts.cumsum(0).tolist()
+    y = gpu.moe_fp8_matmul(x, xs, w, ws, offsets=torch.tensor(off, dtype=torch.int32, device="cuda"), out_dtype=torch.float32)
+    ref, size = matmul_ref(x.cpu(), xs.cpu(), w.cpu(), ws.cpu(), off)
+    close(y, ref, size, K, torch.float32)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("R,N,K", [(5, 200, 272), (300, 640, 400), (2300, 2048, 2048)])
 def test_matmul_of_the_smallest_quantised_rows(gpu, R, N, K):
     """Rows whose scale is the quantiser's least, 2^-126, with weights' scales below 1: the products are
@@ -504,6 +532,23 @@ def test_wgrad_long_sums_keep_float32(gpu, N, K):
     for r in range(0, R, 4096):
         ref += dyt[:, r:r + 4096].double() @ xt[:, r:r + 4096].double().t()
     assert float((dw.double() - ref).norm() / ref.norm()) <= 16 * 2.0 ** -24
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("R,N,K", [(256, 256, 256), (2048, 2048, 1152), (32768, 256, 256), (32768, 2000, 2560)])
+def test_wgrad_sums_of_one_sign(gpu, R, N, K):
+    """Codes of one sign, where truncated additions all err the same way.  The tensor core adds the 128 rows
+    of a block in 4 steps, 16 blocks in a row: at most 64 truncations of 2^-23 of the running sum, which is
+    half of the last one on average; then a float32 addition of 2^-24 for each 16 blocks, of a running
+    sum again."""
+    xt, _, dyt, _ = (t.cuda() for t in wgrad_case(R, N, K, 9))
+    xt, dyt = xt.float().abs().to(F8), dyt.float().abs().to(F8)
+    dw = gpu.moe_fp8_wgrad(xt, torch.ones(R // B, K, device="cuda"), dyt, torch.ones(R // B, N, device="cuda"))
+    ref = torch.zeros(N, K, dtype=torch.float64, device="cuda")
+    for r in range(0, R, 4096):
+        ref += dyt[:, r:r + 4096].double() @ xt[:, r:r + 4096].double().t()
+    steps, flushes = 4 * min(16, R // B), -(-R // (16 * B))
+    assert float((dw.double() - ref).norm() / ref.norm()) <= (steps + 1) / 2 * 2.0 ** -23 + (flushes + 1) / 2 * 2.0 ** -24
 
 
 @pytest.mark.gpu
