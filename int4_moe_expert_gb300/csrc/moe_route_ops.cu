@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kListThreads, 1) lists_kernel(const ListArgs p
     }
     // rows without a token: behind each expert's pairs (its block's warps) and behind the last segment
     for (int e = (int)blockIdx.x * kListWarps + warp; e < p.E; e += p.blocks * kListWarps)
-        for (int r = off[e] + total[e] + lane; r < off[e + 1]; r += 32) p.rows[r] = -1;
+        for (long long r = (long long)off[e] + total[e] + lane; r < off[e + 1]; r += 32) p.rows[r] = -1;      // may step past 2^31
     for (long long r = off[p.E] + (long long)blockIdx.x * kListThreads + tid; r < p.room; r += (long long)p.blocks * kListThreads)
         p.rows[r] = -1;
 }

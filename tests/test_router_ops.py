@@ -160,6 +160,41 @@ def test_lists_extremes(gpu, T):
 
 
 @pytest.mark.gpu
+def test_lists_up_to_the_last_row_number(gpu):
+    """Segments that end next to row 2^31: a warp's lanes behind them have numbers beyond it."""
+    if torch.cuda.mem_get_info()[0] < 60 * 2**30:
+        pytest.skip("needs 60 GB")
+    T, K = 2**28 - 1, 8
+    for E, align, dropped in ((3, 1, 0), (3, 2, 5), (1, 2, 1)):
+        t = torch.arange(T, dtype=torch.int32, device="cuda")
+        idx = torch.empty(T, K, dtype=torch.int32, device="cuda")
+        for k in range(K):
+            idx[:, k] = (t + k) % E
+        idx.view(-1)[T * K - dropped:] = -1
+        counts, off, rows, pos = gpu.moe_expert_lists(idx, E, align)
+        want = torch.zeros(E, dtype=torch.int64, device="cuda")
+        for k in range(K):
+            for e in range(E):
+                want[e] += (idx[:, k] == e).sum()
+        assert counts.tolist() == want.tolist() and rows.numel() < 2**31
+        seg = [0]
+        for c in counts.tolist():
+            seg.append(seg[-1] + -(-c // align) * align)
+        assert off.tolist() == seg and seg[-1] >= 2**31 - 16
+        for k in range(K):      # every pair's row holds its token, in its expert's segment
+            p, e = pos[:, k].long(), idx[:, k]
+            on = e >= 0
+            assert bool((p[~on] == -1).all())
+            p, e = p[on], e[on].long()
+            assert torch.equal(rows[p], t[on])
+            assert bool((p >= off[:-1].long()[e]).all()) and bool((p < off[1:].long()[e]).all())
+            del p, e, on
+        assert int((rows == -1).sum()) == rows.numel() - int(counts.sum())
+        del t, idx, counts, off, rows, pos
+        torch.cuda.empty_cache()
+
+
+@pytest.mark.gpu
 def test_lists_refuses_in_the_binding(gpu):
     idx = torch.zeros(4, 2, dtype=torch.int32, device="cuda")
     for bad in (idx.long(), idx[:, ::2], idx[0], idx.cpu()):
