@@ -482,6 +482,8 @@ moe_status moe_fp8_quantize_weights(const void *w, int32_t dtype, int32_t E, int
  * (device int32 [E + 1], ascending) row r belongs to the expert e with
  * offsets[e] <= r < offsets[e + 1]; rows outside every segment are left as they
  * are in y.  offsets NULL: E = 1, every row.  y[R, N], rows ldy elements apart.
+ * The tiles go by the sizes, R / min(E, R) rows an expert: with 16 or fewer, an
+ * expert that has many more all the same reads its weights once for every 16.
  * K: a multiple of 16 in 16..131072; N in 1..131072; E in 1..1024; x and w
  * 16-byte aligned. */
 moe_status moe_fp8_matmul(const uint8_t *x, const float *x_scale, int32_t R, const uint8_t *w, const float *w_scale,

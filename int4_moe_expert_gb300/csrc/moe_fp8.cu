@@ -2006,7 +2006,7 @@ cudaError_t launch_fp8_matmul(const uint8_t *x, const float *xs, int R, const ui
     take_stall(p);
     const long long nat = (N + kARows - 1) / kARows;
     const int used = offsets ? (E < R ? E : R) : 1;      // weight matrices that rows can belong to
-    const int each = (R + used - 1) / used;
+    const int each = (R + used - 1) / used;              // rows of one on average: the offsets are on the device
     if (each <= 16) {
         // few rows of every weight matrix: weights as lanes, 16 rows as columns, two blocks an SM; bound by
         // the weights' bytes.  Up to eight blocks share a tile's inner axis while all fit at once.

@@ -212,8 +212,9 @@ __global__ void __launch_bounds__(kListThreads, 1) lists_kernel(const ListArgs p
 // registers and adds the blocks' sums in block order; the gradient needs every count first, so it reads
 // the logits again and writes.  A block of tokens b that meets segment s leaves its sums in slot b + s:
 // both only grow along the tokens, so slots never meet.  Long batches are bound by the instructions of
-// the scores (131072 x 64 bf16, softmax: forward 16 us, gradient 13 us, 64 % of the issue slots while
-// active; their bytes alone would take 3 and 5 us), short ones by launches and dependent loads.
+// the scores and their latency (131072 x 64 bf16, softmax: forward 15.2 us, gradient 12.9 us; 59 % of the
+// issue slots while active, 44 and 47 % over the launches; their bytes alone would take 3 and 5 us), short
+// ones by launches and dependent loads.
 // ---------------------------------------------------------------------------
 
 constexpr int kBalThreads = 256;
@@ -736,7 +737,8 @@ cudaError_t launch_balance_forward(const void *logits, int dtype, long long ld, 
         if (er != cudaSuccess) return er;
         return launch_early(balance_loss_kernel, 1, kLossThreads, 0, st, 1, p.part_loss, S * groups, loss);
     };
-    // By the slots of a sequence: many strands for many of them, else few blocks.  The forward of 32768
+    // By the slots of a sequence on average (the offsets are on the device): many strands for many of
+    // them, else few blocks.  The forward of 32768
     // x 256 scores, 1024 slots, by 8 experts x 128 strands / 32 x 8 / 256 x 1: 1 sequence 17 / 28 / 91 us,
     // 9 18 / 22 / 43, 32 24 / 19 / 28, 128 48 / 21 / 23, 500 133 / 29 / 24, 4000 901 / 87 / 49.
     const size_t each = slots / S;
