@@ -505,6 +505,97 @@ moe_status moe_fp8_wgrad(const uint8_t *xt, const float *xt_scale, const uint8_t
                          int32_t R, int32_t N, int32_t K, int32_t E, const int32_t *offsets, void *dw,
                          int32_t dw_dtype, void *stream);
 
+/* The choice of a router from its logits[T, E] (dtype; rows ld elements apart): the selection and the
+ * weights that moe_route_noalloc describes, for any number of tokens.  key = sigmoid(l) + bias (bias[E]
+ * float32, NULL: none; sigmoid only) or softmax(l); with n_group > 1 (sigmoid) only experts of the
+ * topk_group groups with the best sums of their two best keys (one in groups of one) keep theirs, the
+ * others have -infinity.  Writes the top_k experts of the largest keys, in descending order, to
+ * topk_idx[T, K] (int32) and their weights to topk_w[T, K] (float32): p = sigmoid(l) or softmax(l),
+ * w = routed_scale p / (sum of the chosen p + 1e-20) with norm_topk (the softmax needs no such term: its
+ * weights are the softmax over the chosen logits), else routed_scale p.  mask[T] (device, one byte per
+ * token; NULL: none): tokens with 0 get the expert -1 and the weight 0, whatever their logits hold.
+ * Keys are compared as their float64 values (without a bias as the logits themselves); the lower index
+ * wins a tie; a NaN ranks with -infinity.  A token whose choice hangs on less than float32 tells, or on
+ * very many equal keys, takes some microseconds more.
+ * Limits: E in 1..1024, top_k 1..min(E, 32), n_group 1..32, top_k <= topk_group E / n_group. */
+moe_status moe_route_forward(const void *logits, int32_t dtype, int64_t ld, int32_t T, int32_t n_experts,
+                             const float *bias, int32_t top_k, int32_t score_func, int32_t n_group,
+                             int32_t topk_group, int32_t norm_topk, float routed_scale, const uint8_t *mask,
+                             int32_t *topk_idx, float *topk_w, void *stream);
+
+/* The gradient of its weights (the choice is a constant, so bias and groups have none): dlogits[T, E]
+ * (dtype, rows ldd elements apart) from grad_w[T, K] (float32) and the choice topk_idx[T, K].  Entries of
+ * topk_idx outside [0, E) have no weight (a masked token's row is zeros, whatever its logits hold); an
+ * expert that stands twice in a row gets the sum of both gradients.  accumulate not 0: the gradient is
+ * added to what dlogits holds (that of the balance loss, say), in float32, rounded once. */
+moe_status moe_route_backward(const void *logits, int32_t dtype, int64_t ld, int32_t T, int32_t n_experts,
+                              const int32_t *topk_idx, int32_t top_k, int32_t score_func, int32_t norm_topk,
+                              float routed_scale, const float *grad_w, void *dlogits, int64_t ldd,
+                              int32_t accumulate, void *stream);
+
+/* Root-mean-square norm of a residual stream.  x[T, width] (dtype); with residual[T, width]
+ * (stream_dtype: float32 or dtype) h = x + residual, added in float32, rounded to stream_dtype and
+ * written to h[T, width] (which may be residual itself); without it (NULL) h = x and nothing is written.
+ *   rstd = 1 / sqrt(mean over the row of h^2 + eps)      y = h rstd weight
+ * weight[width] float32 or dtype (weight_dtype), NULL: 1.  Each output may be NULL: y[T, width] (dtype,
+ * one rounding), rstd[T] (float32; moe_norm_backward needs it), codes[T, width] with
+ * scales[ceil(width / 128), T]: y in e4m3 with a scale per 1 x 128 block, as moe_fp8_quantize makes them
+ * and moe_fp8_matmul reads them, from y in float32 before it is rounded to dtype.  (Where a block's
+ * largest magnitude is so near a scale's step that float32 cannot tell, float64 decides.)
+ * width: 1..16384; with codes a multiple of 16, and every row of the other tensors, and weight, on a
+ * 16-byte boundary.  Rows may be strided (ldx, ldr, ldh, ldy). */
+moe_status moe_norm_forward(const void *x, int32_t dtype, int64_t ldx, const void *residual, int32_t stream_dtype,
+                            int64_t ldr, const void *weight, int32_t weight_dtype, int32_t T, int32_t width, double eps,
+                            void *h, int64_t ldh, void *y, int64_t ldy, float *rstd, uint8_t *codes, float *scales,
+                            void *stream);
+
+/* Its gradient: with n = h rstd and d = dy weight,
+ *   dh = (d - n mean over the row of (d n)) rstd + grad_h      dweight = sum over the tokens of dy n
+ * dy[T, width] (dtype) is the gradient of y, grad_h[T, width] (stream_dtype, NULL: 0) the one that reaches
+ * h otherwise; h (stream_dtype; x where there was no residual) and rstd are the forward's.  dh[T, width]
+ * (stream_dtype; may be grad_h itself) is the gradient of x and of residual; dweight[width] float32 (NULL:
+ * not computed).  workspace: moe_norm_workspace(...) bytes, 16-byte aligned (only with dweight). */
+size_t moe_norm_workspace(int32_t T, int32_t width);
+moe_status moe_norm_backward(const void *dy, int32_t dtype, int64_t lddy, const void *h, int32_t stream_dtype,
+                             int64_t ldh, const float *rstd, const void *weight, int32_t weight_dtype,
+                             const void *grad_h, int64_t ldg, int32_t T, int32_t width, void *dh, int64_t ldd,
+                             float *dweight, void *workspace, size_t workspace_bytes, void *stream);
+
+/* The weighted sum of a token's rows: y[t] = sum_k topk_w[t, k] rows[pos[t, k]] + add[t] in float32, in the
+ * order of k, rounded once to y's dtype.  rows[R, N] (dtype) the experts' outputs, pos[T, K] (int32) as
+ * moe_expert_lists writes it: pairs with a value outside [0, R) are left out, so rows without a token are
+ * never read.  topk_w NULL: 1; add[T, N] (y_dtype) NULL: none (it may be y itself).  N in 1..131072, K in
+ * 1..32, T times ceil(N / 256) up to 2^33. */
+moe_status moe_combine_forward(const void *rows, int32_t dtype, int64_t ld, int32_t R, int32_t N, const int32_t *pos,
+                               int32_t T, int32_t top_k, const float *topk_w, const void *add, int64_t ldadd, void *y,
+                               int32_t y_dtype, int64_t ldy, void *stream);
+
+/* Its gradients, from dy[T, N] (dtype, as rows): drows[R, N] (dtype) with drows[pos[t, k]] = topk_w[t, k] dy[t]
+ * and dtopk_w[T, K] = rows[pos[t, k]] . dy[t] (0 for pairs without a row).  tokens[R] is the token of every
+ * row (moe_expert_lists' `rows`): a row takes the gradient of its own token, with the sum of the weights
+ * where that names it more than once; every other row gets zeros.  drows or dtopk_w may be NULL.  T up to
+ * 2^30. */
+moe_status moe_combine_backward(const void *dy, int32_t dtype, int64_t lddy, const void *rows, int64_t ld, int32_t R,
+                                int32_t N, const int32_t *pos, int32_t T, int32_t top_k, const int32_t *tokens,
+                                const float *topk_w, void *drows, int64_t ldd, float *dtopk_w, void *stream);
+
+/* norm[1] = the 2-norm of all gradients together (float32; the squares' sums are float64, so they neither
+ * overflow nor vanish; a NaN or an infinity anywhere is one in norm).  grads, dtypes, sizes: host arrays of n_tensors
+ * (0..65536) device addresses on their elements' boundary, MOE_DTYPE_* and numbers of elements (up to 2^45
+ * in all); read during the call alone, so that a captured call needs none of them later.  workspace:
+ * moe_grad_norm_workspace(n_tensors) bytes on the current device, 16-byte aligned. */
+size_t moe_grad_norm_workspace(int32_t n_tensors);
+moe_status moe_grad_norm(int32_t n_tensors, const void *const *grads, const int32_t *dtypes, const int64_t *sizes,
+                         float *norm, void *workspace, size_t workspace_bytes, void *stream);
+
+/* out[i] = grads[i] min(1, max_norm / (norm[0] + 1e-6)), in float32, rounded to the gradient's type; out
+ * NULL: in place (which moves nothing where the factor is 1).  norm is device memory: moe_grad_norm's, or
+ * what expert-parallel ranks made of theirs.  An infinite norm makes zeros (NaN of infinities), a NaN
+ * makes every gradient NaN.  max_norm: finite, 0 or more.  No output may overlap another tensor of the
+ * call but its own input. */
+moe_status moe_grad_clip(int32_t n_tensors, const void *const *grads, const int32_t *dtypes, const int64_t *sizes,
+                         const float *norm, float max_norm, void *const *out, void *stream);
+
 /* Waits for the device, then reads and clears the error word of the two
  * products on it: MOE_DEVICE_ERR_TC if a pipeline wait of a kernel ran out (its
  * output is invalid); returns MOE_ERR_CUDA when it was set. */

@@ -30,6 +30,8 @@ __all__ = [
     "MOE_DTYPE_F32", "MOE_DTYPE_F16", "MOE_DTYPE_BF16",
     "moe_expert_lists", "moe_balance_forward", "moe_balance_backward", "moe_fp8_quantize",
     "moe_fp8_quantize_weights", "moe_fp8_matmul", "moe_fp8_wgrad", "moe_fp8_device_error", "moe_fp8_debug_stall_next_call",
+    "moe_route_forward", "moe_route_backward", "moe_norm_forward", "moe_norm_backward", "moe_combine_forward", "moe_combine_backward",
+    "moe_grad_norm", "moe_grad_clip",
 ]
 
 MOE_OK, MOE_ERR_INVALID, MOE_ERR_CUDA, MOE_ERR_NOMEM, MOE_ERR_UNSUPPORTED = 0, 1, 2, 3, 4
@@ -140,7 +142,21 @@ def lib():
         L.moe_fp8_device_error.argtypes = [C.POINTER(C.c_uint32)]
         L.moe_fp8_debug_stall_next_call.argtypes = [i32, i32]
         L.moe_fp8_debug_stall_next_call.restype = C.c_int
-        for name in ("moe_expert_lists", "moe_balance_forward", "moe_balance_backward", "moe_fp8_quantize",
+        f64 = C.c_double
+        L.moe_route_forward.argtypes = [vp, i32, i64, i32, i32, vp, i32, i32, i32, i32, i32, f32, vp, vp, vp, vp]
+        L.moe_route_backward.argtypes = [vp, i32, i64, i32, i32, vp, i32, i32, i32, f32, vp, vp, i64, i32, vp]
+        L.moe_norm_forward.argtypes = [vp, i32, i64, vp, i32, i64, vp, i32, i32, i32, f64, vp, i64, vp, i64, vp, vp, vp, vp]
+        L.moe_norm_workspace.argtypes = [i32, i32]
+        L.moe_norm_workspace.restype = sz
+        L.moe_norm_backward.argtypes = [vp, i32, i64, vp, i32, i64, vp, vp, i32, vp, i64, i32, i32, vp, i64, vp, vp, sz, vp]
+        L.moe_combine_forward.argtypes = [vp, i32, i64, i32, i32, vp, i32, i32, vp, vp, i64, vp, i32, i64, vp]
+        L.moe_combine_backward.argtypes = [vp, i32, i64, vp, i64, i32, i32, vp, i32, i32, vp, vp, vp, i64, vp, vp]
+        L.moe_grad_norm_workspace.argtypes = [i32]
+        L.moe_grad_norm_workspace.restype = sz
+        L.moe_grad_norm.argtypes = [i32, vp, vp, vp, vp, vp, sz, vp]
+        L.moe_grad_clip.argtypes = [i32, vp, vp, vp, vp, f32, vp, vp]
+        for name in ("moe_route_forward", "moe_route_backward", "moe_norm_forward", "moe_norm_backward", "moe_combine_forward",
+                     "moe_combine_backward", "moe_grad_norm", "moe_grad_clip", "moe_expert_lists", "moe_balance_forward", "moe_balance_backward", "moe_fp8_quantize",
                      "moe_fp8_quantize_weights", "moe_fp8_matmul", "moe_fp8_wgrad", "moe_fp8_device_error"):
             getattr(L, name).restype = C.c_int
         _lib = L
@@ -475,6 +491,64 @@ def moe_fp8_wgrad(xt, xt_scale, dyt, dyt_scale, offsets=None, out=None, out_dtyp
     one matrix).
     -> dw [E, N, K] ([N, K] without offsets), float32 by default."""
     return _native().fp8_wgrad(xt, xt_scale, dyt, dyt_scale, offsets, out, out_dtype, _handle(stream))
+
+
+def moe_route_forward(logits, top_k: int, bias=None, score_func: int = MOE_SCORE_SIGMOID, n_group: int = 1, topk_group: int = 1,
+                      norm_topk: bool = True, routed_scale: float = 1.0, mask=None, stream=None):
+    """The choice of a router from logits [T, E] float32 / float16 / bfloat16 (rows may be strided): the top_k experts of
+    the largest sigmoid(logits) + bias [E] float32 (within the topk_group best of n_group groups) or
+    softmax(logits), and their weights.  mask [T] bool (False: no choice).
+    -> topk_idx [T, K] int32 (descending; -1 for masked tokens), topk_w [T, K] float32."""
+    return _native().route_forward(logits, top_k, bias, score_func, n_group, topk_group, norm_topk, routed_scale, mask, _handle(stream))
+
+
+def moe_route_backward(logits, topk_idx, grad_w, score_func: int = MOE_SCORE_SIGMOID, norm_topk: bool = True, routed_scale: float = 1.0,
+                       out=None, accumulate: bool = False, stream=None):
+    """Gradient of moe_route_forward's weights: grad_w [T, K] float32 for the choice topk_idx [T, K] int32.
+    accumulate: added to what `out` holds (moe_balance_backward's, say).  -> dlogits [T, E] in logits' dtype."""
+    return _native().route_backward(logits, topk_idx, grad_w, score_func, norm_topk, routed_scale, out, accumulate, _handle(stream))
+
+
+def moe_norm_forward(x, residual=None, weight=None, eps: float = 1e-5, values: bool = True, quantize: bool = False, out=None, stream=None):
+    """Root-mean-square norm of h = x + residual: x [T, width] float32 / float16 / bfloat16, residual of x's
+    type or float32 (None: h is x), weight [width] of x's type or float32 (None: 1).  out: where h goes (a new
+    tensor; may be residual).  -> y [T, width] in x's dtype (None without values), h, rstd [T] float32; with
+    quantize also codes [T, width] float8_e4m3fn and scales [ceil(width / 128), T] of y, as moe_fp8_quantize
+    makes them."""
+    return _native().norm_forward(x, residual, weight, eps, values, quantize, out, _handle(stream))
+
+
+def moe_norm_backward(dy, h, rstd, weight=None, grad_h=None, out=None, stream=None):
+    """Gradients of moe_norm_forward from that of y (dy, x's dtype) and the one that reaches h otherwise
+    (grad_h, h's dtype; None: none), with its h and rstd.  out may be grad_h.
+    -> dh [T, width] in h's dtype (the gradient of x and of residual), dweight [width] float32 (None without weight)."""
+    return _native().norm_backward(dy, h, rstd, weight, grad_h, out, _handle(stream))
+
+
+def moe_combine_forward(rows, pos, topk_w=None, add=None, out=None, out_dtype=None, stream=None):
+    """y [T, N] = the sum over k of topk_w [T, K] float32 (None: 1) times rows [R, N] at pos [T, K] int32 (of
+    moe_expert_lists; pairs outside [0, R) are left out), plus add [T, N] in y's dtype.
+    out_dtype: that of add, or of rows, by default."""
+    return _native().combine_forward(rows, pos, topk_w, add, out, out_dtype, _handle(stream))
+
+
+def moe_combine_backward(dy, rows, pos, tokens, topk_w=None, out=None, stream=None):
+    """Gradients of moe_combine_forward from dy [T, N] in rows' dtype; tokens [R] int32: the token of every
+    row (moe_expert_lists' rows).  -> drows [R, N] (zeros for rows that no pair of their token names),
+    dtopk_w [T, K] float32."""
+    return _native().combine_backward(dy, rows, pos, tokens, topk_w, out, _handle(stream))
+
+
+def moe_grad_norm(grads, stream=None):
+    """The 2-norm of all tensors of grads together (float32 / float16 / bfloat16, mixed, on the current device;
+    elements in any order but without gaps).  -> norm [1] float32, on the device."""
+    return _native().grad_norm(list(grads), _handle(stream))
+
+
+def moe_grad_clip(grads, norm, max_norm: float, out=None, stream=None) -> None:
+    """Scales grads by min(1, max_norm / (norm + 1e-6)), in place or into the tensors of out; norm float32,
+    one value on the device (moe_grad_norm's)."""
+    _native().grad_clip(list(grads), norm, max_norm, None if out is None else list(out), _handle(stream))
 
 
 def moe_fp8_device_error(check: bool = True) -> int:

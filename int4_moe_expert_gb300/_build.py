@@ -16,7 +16,7 @@ BUILD = PKG / "_build"
 LIB = PKG / "libmoe_gb300.so"
 BINDING = PKG / "_moe_torch.so"
 KEY = "moe_torch.key"          # in BUILD: what the binding was built for
-SOURCES = ["moe_kernels.cu", "moe_decode.cu", "moe_fp8.cu", "moe_route_ops.cu", "moe_abi.cu"]
+SOURCES = ["moe_kernels.cu", "moe_decode.cu", "moe_fp8.cu", "moe_route_ops.cu", "moe_select.cu", "moe_norm.cu", "moe_stream.cu", "moe_abi.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

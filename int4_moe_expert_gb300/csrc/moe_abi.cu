@@ -6,7 +6,10 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <algorithm>
+#include <exception>
 #include <new>
+#include <vector>
 
 #include "moe_internal.h"
 
@@ -645,6 +648,224 @@ moe_status moe_fp8_wgrad(const uint8_t *xt, const float *xt_scale, const uint8_t
     MOE_NEED(aligned16(xt) && aligned16(dyt) && aligned4(xt_scale) && aligned4(dyt_scale) && aligned4(offsets), MOE_ERR_INVALID,
              "codes must be 16-byte aligned, scales and offsets 4-byte aligned");
     return launched(moe::launch_fp8_wgrad(xt, xt_scale, dyt, dyt_scale, R, N, K, E, offsets, dw, dw_dtype, st), "moe_fp8_wgrad");
+}
+
+static bool aligned_rows(const void *p, int64_t ld, int32_t dtype) {
+    return aligned16(p) && ld * (dtype == MOE_DTYPE_F32 ? 4 : 2) % 16 == 0;
+}
+
+static moe_status check_route(const void *logits, int32_t dtype, int64_t ld, int32_t T, int32_t E, int32_t top_k, int32_t score_func,
+                              int32_t norm_topk, float scale) {
+    MOE_NEED(dtype_ok(dtype), MOE_ERR_INVALID, "dtype=%d: need a MOE_DTYPE_* value", dtype);
+    MOE_NEED(T >= 0, MOE_ERR_INVALID, "T=%d is negative", T);
+    MOE_NEED(E >= 1 && E <= 1024, MOE_ERR_UNSUPPORTED, "n_experts=%d: need 1..1024", E);
+    MOE_NEED(top_k >= 1 && top_k <= E && top_k <= 32, MOE_ERR_INVALID, "top_k=%d: need 1..min(n_experts, 32)", top_k);
+    MOE_NEED(ld >= E, MOE_ERR_INVALID, "ld=%lld: need n_experts or more", (long long)ld);
+    MOE_NEED(score_func == MOE_SCORE_SIGMOID || score_func == MOE_SCORE_SOFTMAX, MOE_ERR_INVALID,
+             "score_func=%d: need MOE_SCORE_SIGMOID or MOE_SCORE_SOFTMAX", score_func);
+    MOE_NEED(norm_topk == 0 || norm_topk == 1, MOE_ERR_INVALID, "norm_topk=%d: need 0 or 1", norm_topk);
+    MOE_NEED(isfinite(scale), MOE_ERR_INVALID, "routed_scale is not finite");
+    MOE_NEED(T == 0 || logits, MOE_ERR_INVALID, "logits is NULL");
+    MOE_NEED(aligned_el(logits, dtype), MOE_ERR_INVALID, "logits is not aligned to its elements");
+    return MOE_OK;
+}
+
+moe_status moe_route_forward(const void *logits, int32_t dtype, int64_t ld, int32_t T, int32_t n_experts, const float *bias,
+                             int32_t top_k, int32_t score_func, int32_t n_group, int32_t topk_group, int32_t norm_topk,
+                             float routed_scale, const uint8_t *mask, int32_t *topk_idx, float *topk_w, void *stream) {
+    const moe_status s = check_route(logits, dtype, ld, T, n_experts, top_k, score_func, norm_topk, routed_scale);
+    if (s != MOE_OK) return s;
+    MOE_NEED(n_group >= 1 && n_group <= 32 && n_experts % n_group == 0, MOE_ERR_INVALID,
+             "n_group=%d: need 1..32, a divisor of n_experts", n_group);
+    MOE_NEED(score_func == MOE_SCORE_SIGMOID || (n_group == 1 && !bias), MOE_ERR_INVALID, "groups and bias go with the sigmoid score alone");
+    MOE_NEED(n_group == 1 || (topk_group >= 1 && topk_group <= n_group), MOE_ERR_INVALID, "topk_group=%d: need 1..n_group", topk_group);
+    MOE_NEED(n_group == 1 || top_k <= topk_group * (n_experts / n_group), MOE_ERR_INVALID,
+             "top_k=%d: need topk_group * n_experts / n_group or fewer", top_k);
+    MOE_NEED(T == 0 || (topk_idx && topk_w), MOE_ERR_INVALID, "topk_idx / topk_w is NULL");
+    MOE_NEED(aligned4(bias) && aligned4(topk_idx) && aligned4(topk_w), MOE_ERR_INVALID, "int32 / float32 buffers must be 4-byte aligned");
+    if (T == 0) return MOE_OK;
+    return launched(moe::launch_route_forward(logits, dtype, ld, T, n_experts, bias, top_k, score_func == MOE_SCORE_SOFTMAX, n_group,
+                                              n_group > 1 ? topk_group : 1, norm_topk, routed_scale, mask, topk_idx, topk_w,
+                                              static_cast<cudaStream_t>(stream)), "moe_route_forward");
+}
+
+moe_status moe_route_backward(const void *logits, int32_t dtype, int64_t ld, int32_t T, int32_t n_experts, const int32_t *topk_idx,
+                              int32_t top_k, int32_t score_func, int32_t norm_topk, float routed_scale, const float *grad_w,
+                              void *dlogits, int64_t ldd, int32_t accumulate, void *stream) {
+    const moe_status s = check_route(logits, dtype, ld, T, n_experts, top_k, score_func, norm_topk, routed_scale);
+    if (s != MOE_OK) return s;
+    MOE_NEED(ldd >= n_experts, MOE_ERR_INVALID, "ldd=%lld: need n_experts or more", (long long)ldd);
+    MOE_NEED(T == 0 || (topk_idx && grad_w && dlogits), MOE_ERR_INVALID, "topk_idx / grad_w / dlogits is NULL");
+    MOE_NEED(aligned4(topk_idx) && aligned4(grad_w) && aligned_el(dlogits, dtype), MOE_ERR_INVALID, "a buffer is not aligned to its elements");
+    if (T == 0) return MOE_OK;
+    return launched(moe::launch_route_backward(logits, dtype, ld, T, n_experts, topk_idx, top_k, score_func == MOE_SCORE_SOFTMAX, norm_topk,
+                                               routed_scale, grad_w, dlogits, ldd, accumulate != 0, static_cast<cudaStream_t>(stream)),
+                    "moe_route_backward");
+}
+
+static const int32_t kMaxNorm = 16384;
+
+static moe_status check_norm(int32_t dtype, int32_t stream_dtype, const void *weight, int32_t weight_dtype, int32_t T, int32_t width) {
+    MOE_NEED(dtype_ok(dtype), MOE_ERR_INVALID, "dtype=%d: need a MOE_DTYPE_* value", dtype);
+    MOE_NEED(stream_dtype == dtype || stream_dtype == MOE_DTYPE_F32, MOE_ERR_INVALID, "stream_dtype=%d: need dtype or MOE_DTYPE_F32", stream_dtype);
+    MOE_NEED(!weight || weight_dtype == dtype || weight_dtype == MOE_DTYPE_F32, MOE_ERR_INVALID,
+             "weight_dtype=%d: need dtype or MOE_DTYPE_F32", weight_dtype);
+    MOE_NEED(T >= 0, MOE_ERR_INVALID, "T=%d is negative", T);
+    MOE_NEED(width >= 1 && width <= kMaxNorm, MOE_ERR_UNSUPPORTED, "width=%d: need 1..%d", width, kMaxNorm);
+    MOE_NEED(!weight || aligned_el(weight, weight_dtype), MOE_ERR_INVALID, "weight is not aligned to its elements");
+    return MOE_OK;
+}
+
+moe_status moe_norm_forward(const void *x, int32_t dtype, int64_t ldx, const void *residual, int32_t stream_dtype, int64_t ldr,
+                            const void *weight, int32_t weight_dtype, int32_t T, int32_t width, double eps, void *h, int64_t ldh,
+                            void *y, int64_t ldy, float *rstd, uint8_t *codes, float *scales, void *stream) {
+    if (!residual) stream_dtype = dtype;
+    const moe_status s = check_norm(dtype, stream_dtype, weight, weight_dtype, T, width);
+    if (s != MOE_OK) return s;
+    MOE_NEED(isfinite(eps) && eps >= 0, MOE_ERR_INVALID, "eps: need a finite value, 0 or more");
+    MOE_NEED((codes == nullptr) == (scales == nullptr), MOE_ERR_INVALID, "codes and scales: give both or neither");
+    MOE_NEED(ldx >= width && (!residual || (ldr >= width && ldh >= width)) && (!y || ldy >= width), MOE_ERR_INVALID,
+             "a row stride is less than width=%d", width);
+    MOE_NEED(!codes || width % 16 == 0, MOE_ERR_UNSUPPORTED, "width=%d: need a multiple of 16 for codes", width);
+    if (T == 0) return MOE_OK;
+    MOE_NEED(x && (!residual || h), MOE_ERR_INVALID, "x / h is NULL");
+    MOE_NEED(aligned_el(x, dtype) && aligned_el(residual, stream_dtype) && aligned_el(h, stream_dtype) && aligned_el(y, dtype) &&
+             aligned4(rstd) && aligned4(scales), MOE_ERR_INVALID, "a buffer is not aligned to its elements");
+    MOE_NEED(!codes || (aligned16(codes) && aligned_rows(x, ldx, dtype) && (!y || aligned_rows(y, ldy, dtype)) && aligned16(weight) &&
+             (!residual || (aligned_rows(residual, ldr, stream_dtype) && aligned_rows(h, ldh, stream_dtype)))),
+             MOE_ERR_INVALID, "with codes every row, weight and codes must start on a 16-byte boundary");
+    return launched(moe::launch_norm_forward(x, dtype, ldx, residual, stream_dtype, ldr, weight, weight_dtype, T, width, eps, h, ldh, y, ldy,
+                                             rstd, codes, scales, static_cast<cudaStream_t>(stream)), "moe_norm_forward");
+}
+
+size_t moe_norm_workspace(int32_t T, int32_t width) {
+    return T < 0 || width < 1 || width > kMaxNorm ? 0 : moe::norm_grad_workspace(T, width);
+}
+
+moe_status moe_norm_backward(const void *dy, int32_t dtype, int64_t lddy, const void *h, int32_t stream_dtype, int64_t ldh,
+                             const float *rstd, const void *weight, int32_t weight_dtype, const void *grad_h, int64_t ldg, int32_t T,
+                             int32_t width, void *dh, int64_t ldd, float *dweight, void *workspace, size_t workspace_bytes, void *stream) {
+    const moe_status s = check_norm(dtype, stream_dtype, weight, weight_dtype, T, width);
+    if (s != MOE_OK) return s;
+    MOE_NEED(lddy >= width && ldh >= width && (!grad_h || ldg >= width) && ldd >= width, MOE_ERR_INVALID,
+             "a row stride is less than width=%d", width);
+    MOE_NEED(aligned4(dweight), MOE_ERR_INVALID, "dweight must be 4-byte aligned");
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (T == 0) return dweight ? launched(cudaMemsetAsync(dweight, 0, (size_t)width * 4, st), "moe_norm_backward") : MOE_OK;
+    MOE_NEED(dy && h && rstd && dh, MOE_ERR_INVALID, "dy / h / rstd / dh is NULL");
+    MOE_NEED(aligned_el(dy, dtype) && aligned_el(h, stream_dtype) && aligned_el(grad_h, stream_dtype) && aligned_el(dh, stream_dtype) &&
+             aligned4(rstd), MOE_ERR_INVALID, "a buffer is not aligned to its elements");
+    const size_t need = dweight ? moe_norm_workspace(T, width) : 0;
+    MOE_NEED(need == 0 || (workspace && aligned16(workspace) && workspace_bytes >= need), MOE_ERR_INVALID,
+             "workspace: need %zu bytes, 16-byte aligned", need);
+    return launched(moe::launch_norm_backward(dy, dtype, lddy, h, stream_dtype, ldh, rstd, weight, weight_dtype, grad_h, ldg, T, width, dh, ldd,
+                                              dweight, workspace, st), "moe_norm_backward");
+}
+
+static moe_status check_combine(int32_t dtype, int64_t ld, int32_t R, int32_t N, int32_t T, int32_t top_k) {
+    MOE_NEED(dtype_ok(dtype), MOE_ERR_INVALID, "dtype=%d: need a MOE_DTYPE_* value", dtype);
+    MOE_NEED(T >= 0 && R >= 0, MOE_ERR_INVALID, "T=%d, R=%d: negative", T, R);
+    MOE_NEED(N >= 1 && N <= kMaxWidth, MOE_ERR_UNSUPPORTED, "N=%d: need 1..%d", N, kMaxWidth);
+    MOE_NEED(top_k >= 1 && top_k <= 32, MOE_ERR_UNSUPPORTED, "top_k=%d: need 1..32", top_k);
+    MOE_NEED(ld >= N, MOE_ERR_INVALID, "ld=%lld: need N or more", (long long)ld);
+    return MOE_OK;
+}
+
+moe_status moe_combine_forward(const void *rows, int32_t dtype, int64_t ld, int32_t R, int32_t N, const int32_t *pos, int32_t T,
+                               int32_t top_k, const float *topk_w, const void *add, int64_t ldadd, void *y, int32_t y_dtype,
+                               int64_t ldy, void *stream) {
+    const moe_status s = check_combine(dtype, ld, R, N, T, top_k);
+    if (s != MOE_OK) return s;
+    MOE_NEED(dtype_ok(y_dtype), MOE_ERR_INVALID, "y_dtype=%d: need a MOE_DTYPE_* value", y_dtype);
+    MOE_NEED((int64_t)T * ((N + 255) / 256) <= 1ll << 33, MOE_ERR_UNSUPPORTED, "T=%d: need 2^33 / ceil(N / 256) or fewer", T);
+    MOE_NEED(ldy >= N && (!add || ldadd >= N), MOE_ERR_INVALID, "a row stride is less than N=%d", N);
+    if (T == 0) return MOE_OK;
+    MOE_NEED((rows || R == 0) && pos && y, MOE_ERR_INVALID, "rows / pos / y is NULL");
+    MOE_NEED(aligned_el(rows, dtype) && aligned_el(add, y_dtype) && aligned_el(y, y_dtype) && aligned4(pos) && aligned4(topk_w),
+             MOE_ERR_INVALID, "a buffer is not aligned to its elements");
+    return launched(moe::launch_combine_forward(rows, dtype, ld, R, N, pos, T, top_k, topk_w, add, ldadd, y, y_dtype, ldy,
+                                                static_cast<cudaStream_t>(stream)), "moe_combine_forward");
+}
+
+moe_status moe_combine_backward(const void *dy, int32_t dtype, int64_t lddy, const void *rows, int64_t ld, int32_t R, int32_t N,
+                                const int32_t *pos, int32_t T, int32_t top_k, const int32_t *tokens, const float *topk_w,
+                                void *drows, int64_t ldd, float *dtopk_w, void *stream) {
+    const moe_status s = check_combine(dtype, dtopk_w ? ld : N, R, N, T, top_k);
+    if (s != MOE_OK) return s;
+    MOE_NEED(T <= 1 << 30, MOE_ERR_UNSUPPORTED, "T=%d: need 2^30 or fewer", T);
+    MOE_NEED(lddy >= N && (!drows || ldd >= N), MOE_ERR_INVALID, "a row stride is less than N=%d", N);
+    MOE_NEED(T == 0 || (dy && pos), MOE_ERR_INVALID, "dy / pos is NULL");
+    MOE_NEED(R == 0 || (tokens && (rows || !dtopk_w)), MOE_ERR_INVALID, "tokens / rows is NULL");
+    MOE_NEED(aligned_el(dy, dtype) && aligned_el(rows, dtype) && aligned_el(drows, dtype) && aligned4(pos) && aligned4(tokens) &&
+             aligned4(topk_w) && aligned4(dtopk_w), MOE_ERR_INVALID, "a buffer is not aligned to its elements");
+    if ((T == 0 && (R == 0 || !drows)) || (!drows && !dtopk_w)) return MOE_OK;
+    return launched(moe::launch_combine_backward(dy, dtype, lddy, rows, ld, R, N, pos, T, top_k, tokens, topk_w, drows, ldd, dtopk_w,
+                                                 static_cast<cudaStream_t>(stream)), "moe_combine_backward");
+}
+
+static moe_status check_grads(int32_t n, const void *const *grads, const int32_t *dtypes, const int64_t *sizes, const float *norm) {
+    MOE_NEED(n >= 0, MOE_ERR_INVALID, "n_tensors=%d is negative", n);
+    MOE_NEED(n <= 65536, MOE_ERR_UNSUPPORTED, "n_tensors=%d: need 65536 or fewer", n);
+    MOE_NEED(norm && aligned4(norm), MOE_ERR_INVALID, "norm is NULL or not 4-byte aligned");
+    MOE_NEED(n == 0 || (grads && dtypes && sizes), MOE_ERR_INVALID, "grads / dtypes / sizes is NULL");
+    int64_t all = 0;
+    for (int32_t i = 0; i < n; i++) {
+        MOE_NEED(dtype_ok(dtypes[i]), MOE_ERR_INVALID, "tensor %d: dtype=%d: need a MOE_DTYPE_* value", i, dtypes[i]);
+        MOE_NEED(sizes[i] >= 0, MOE_ERR_INVALID, "tensor %d: size=%lld is negative", i, (long long)sizes[i]);
+        MOE_NEED(sizes[i] <= (1ll << 45) - all, MOE_ERR_UNSUPPORTED, "more than 2^45 elements");
+        MOE_NEED(sizes[i] == 0 || (grads[i] && aligned_el(grads[i], dtypes[i])), MOE_ERR_INVALID,
+                 "tensor %d: NULL or not aligned to its elements", i);
+        all += sizes[i];
+    }
+    return MOE_OK;
+}
+
+size_t moe_grad_norm_workspace(int32_t n_tensors) { return n_tensors < 0 || n_tensors > 65536 ? 0 : moe::grad_norm_workspace(n_tensors); }
+
+moe_status moe_grad_norm(int32_t n_tensors, const void *const *grads, const int32_t *dtypes, const int64_t *sizes, float *norm,
+                         void *workspace, size_t workspace_bytes, void *stream) {
+    const moe_status s = check_grads(n_tensors, grads, dtypes, sizes, norm);
+    if (s != MOE_OK) return s;
+    const size_t need = moe_grad_norm_workspace(n_tensors);
+    MOE_NEED(workspace && aligned16(workspace) && workspace_bytes >= need, MOE_ERR_INVALID, "workspace: need %zu bytes, 16-byte aligned", need);
+    return launched(moe::launch_grad_norm(n_tensors, grads, dtypes, sizes, norm, workspace, static_cast<cudaStream_t>(stream)), "moe_grad_norm");
+}
+
+moe_status moe_grad_clip(int32_t n_tensors, const void *const *grads, const int32_t *dtypes, const int64_t *sizes, const float *norm,
+                         float max_norm, void *const *out, void *stream) {
+    const moe_status s = check_grads(n_tensors, grads, dtypes, sizes, norm);
+    if (s != MOE_OK) return s;
+    MOE_NEED(isfinite(max_norm) && max_norm >= 0, MOE_ERR_INVALID, "max_norm: need a finite value, 0 or more");
+    void *const *to = out ? out : const_cast<void *const *>(reinterpret_cast<const void *const *>(grads));
+    // no output on top of another tensor: ranges in order of their addresses, the written ones against all
+    struct Range {
+        uintptr_t a, b;
+        int32_t tensor;
+        bool written;
+    };
+    try {
+        std::vector<Range> r;
+        r.reserve(2 * (size_t)n_tensors);
+        for (int32_t i = 0; i < n_tensors; i++) {
+            if (sizes[i] == 0) continue;
+            const uintptr_t bytes = (uintptr_t)sizes[i] * (dtypes[i] == MOE_DTYPE_F32 ? 4 : 2);
+            MOE_NEED(to[i] && aligned_el(to[i], dtypes[i]), MOE_ERR_INVALID, "output %d: NULL or not aligned to its elements", i);
+            const uintptr_t a = reinterpret_cast<uintptr_t>(grads[i]), b = reinterpret_cast<uintptr_t>(to[i]);
+            if (a != b) r.push_back({a, a + bytes, i, false});
+            r.push_back({b, b + bytes, i, true});
+        }
+        std::sort(r.begin(), r.end(), [](const Range &x, const Range &y) { return x.a < y.a; });
+        const Range *far = nullptr, *far_written = nullptr;       // the furthest end so far, of all and of the written ones
+        for (const Range &q : r) {
+            const Range *other = q.written ? far : far_written;
+            MOE_NEED(!other || other->b <= q.a, MOE_ERR_INVALID, "tensors %d and %d overlap, and one of them is written", other->tensor, q.tensor);
+            if (!far || q.b > far->b) far = &q;
+            if (q.written && (!far_written || q.b > far_written->b)) far_written = &q;
+        }
+    } catch (const std::exception &) {
+        return fail(MOE_ERR_NOMEM, "no host memory for %d tensors", n_tensors);
+    }
+    return launched(moe::launch_grad_clip(n_tensors, grads, dtypes, sizes, norm, max_norm, to, static_cast<cudaStream_t>(stream)), "moe_grad_clip");
 }
 
 moe_status moe_fp8_debug_stall_next_call(int32_t stages, int32_t block) {

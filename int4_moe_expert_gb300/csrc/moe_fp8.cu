@@ -31,6 +31,7 @@
 #include <cstring>
 #include <type_traits>
 
+#include "moe_elem.h"
 #include "moe_internal.h"
 #include "moe_ptx.h"
 
@@ -1541,29 +1542,8 @@ __device__ __forceinline__ float4 load4<__half>(const __half *p) {
     const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&v.x)), b = __half22float2(*reinterpret_cast<const __half2 *>(&v.y));
     return make_float4(a.x, a.y, b.x, b.y);
 }
-__device__ __forceinline__ unsigned abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 __device__ __forceinline__ unsigned max_bits(float4 v) {
     return max(max(abs_bits(v.x), abs_bits(v.y)), max(abs_bits(v.z), abs_bits(v.w)));
-}
-// The least power of two s >= 2^-126 with largest / s <= 448 = 1.75 x 2^8 (1 for a block of zeros,
-// NaN for one with a NaN or an infinity) and 1 / s, from the largest magnitude's bits.
-__device__ __forceinline__ float block_scale(unsigned largest, float &inv) {
-    if (largest >= 0x7F800000u) {
-        inv = __uint_as_float(0x7FC00000u);
-        return inv;
-    }
-    if (largest == 0) {
-        inv = 1.0f;
-        return 1.0f;
-    }
-    const int j = max((int)(largest >> 23) - 127 - 8 + ((largest & 0x7FFFFFu) > 0x600000u ? 1 : 0), -126);
-    inv = __uint_as_float((unsigned)(127 - j) << 23);
-    return __uint_as_float((unsigned)(127 + j) << 23);
-}
-__device__ __forceinline__ uint32_t codes2(float a, float b) {   // a in the low byte
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
-    return r;
 }
 __device__ __forceinline__ uint32_t codes4(float4 v, float inv) {
     return codes2(v.x * inv, v.y * inv) | (codes2(v.z * inv, v.w * inv) << 16);
@@ -1835,6 +1815,8 @@ __global__ void __launch_bounds__(kQThreads, sizeof(T) == 4 ? 2 : 4) quantize_ti
     }
 }
 
+}  // namespace
+
 int sm_count() {
     static std::atomic<int> n[64] = {};
     int dev = 0;
@@ -1843,8 +1825,6 @@ int sm_count() {
     if (!v && cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess) n[dev].store(v, std::memory_order_relaxed);
     return v > 0 ? v : 152;
 }
-
-}  // namespace
 
 cudaError_t launch_quantize(const void *x, int dtype, long long ld, int n_src, int width, const int *rows, int R,
                             uint8_t *codes, float *scales, uint8_t *codes_t, float *scales_t, cudaStream_t st) {

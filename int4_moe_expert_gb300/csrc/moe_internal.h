@@ -191,6 +191,32 @@ cudaError_t launch_balance_backward(const void *logits, int dtype, long long ld,
                                     const uint8_t *mask, const float *grad, void *dlogits, long long ldd, bool zero_rest,
                                     cudaStream_t st);
 
+// The choice from logits and its gradient (moe_select.cu).
+cudaError_t launch_route_forward(const void *logits, int dtype, long long ld, int T, int E, const float *bias, int K, int softmax,
+                                 int groups, int kept, int renorm, float scale, const uint8_t *mask, int *idx, float *w, cudaStream_t st);
+cudaError_t launch_route_backward(const void *logits, int dtype, long long ld, int T, int E, const int *idx, int K, int softmax,
+                                  int renorm, float scale, const float *dw, void *out, long long ldd, bool add, cudaStream_t st);
+
+// Norm of the residual stream (moe_norm.cu).
+size_t norm_grad_workspace(int T, int H);
+cudaError_t launch_norm_forward(const void *x, int dtype, long long ldx, const void *res, int s_dtype, long long ldr, const void *w,
+                                int w_dtype, int T, int H, double eps, void *h, long long ldh, void *y, long long ldy, float *rstd,
+                                uint8_t *codes, float *scales, cudaStream_t st);
+cudaError_t launch_norm_backward(const void *dy, int dtype, long long lddy, const void *h, int s_dtype, long long ldh, const float *rstd,
+                                 const void *w, int w_dtype, const void *gh, long long ldg, int T, int H, void *out, long long ldo,
+                                 float *dw, void *ws, cudaStream_t st);
+
+// Weighted sum of experts' rows, gradients' norm and clipping (moe_stream.cu).
+cudaError_t launch_combine_forward(const void *rows, int dtype, long long ld, long long R, int N, const int *pos, int T, int K,
+                                   const float *w, const void *add, long long ldadd, void *y, int y_dtype, long long ldy, cudaStream_t st);
+cudaError_t launch_combine_backward(const void *dy, int dtype, long long lddy, const void *rows, long long ld, long long R, int N,
+                                    const int *pos, int T, int K, const int *tokens, const float *w, void *drows, long long ldd,
+                                    float *dw, cudaStream_t st);
+size_t grad_norm_workspace(int count);
+cudaError_t launch_grad_norm(int count, const void *const *grads, const int32_t *dtype, const int64_t *n, float *norm, void *ws, cudaStream_t st);
+cudaError_t launch_grad_clip(int count, const void *const *grads, const int32_t *dtype, const int64_t *n, const float *norm, float most,
+                             void *const *out, cudaStream_t st);
+
 // Block-scaled e4m3 quantisers and products (moe_fp8.cu).
 cudaError_t launch_quantize(const void *x, int dtype, long long ld, int n_src, int width, const int *rows, int R,
                             uint8_t *codes, float *scales, uint8_t *codes_t, float *scales_t, cudaStream_t st);

@@ -1,0 +1,466 @@
+// The weighted sum of a token's rows behind the experts with its gradient, and the norm and clipping of
+// all gradients.  Bound by memory, or by latency for few tokens.  No float atomics: results are the same
+// bits every run.
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "moe_elem.h"
+#include "moe_internal.h"
+
+namespace moe {
+namespace {
+
+// ---------------------------------------------------------------------------
+// Weighted sum of a token's rows: y_t = sum_k w_tk rows[pos_tk] (+ add_t), in float32, in the order of
+// k; pairs without a row (pos outside [0, R)) are left out.  A warp a token and 32 runs of its columns,
+// every pair's load in flight.
+// ---------------------------------------------------------------------------
+
+constexpr int kCombWarps = 8;
+
+struct CombineArgs {
+    const void *rows;
+    long long ld, ldadd, ldy;
+    const int *pos;
+    const float *w;          // [T, K] or NULL: 1
+    const void *add;
+    void *y;
+    long long R;
+    int T, K, N, parts;      // parts: warps of a token
+};
+
+template <typename T, typename Y, int V, int C>
+__global__ void __launch_bounds__(32 * kCombWarps) combine_kernel(const CombineArgs p) {
+    const int lane = threadIdx.x & 31;
+    const long long job = (long long)blockIdx.x * kCombWarps + (threadIdx.x >> 5);
+    wait_for_stream();
+    const long long t = job / p.parts;
+    if (t >= p.T) return;
+    const int base = (int)(job - t * p.parts) * (32 * V * C) + V * lane;
+    int pos = lane < p.K ? load_in(p.pos + t * p.K + lane) : -1;
+    const float wt = lane < p.K ? (p.w ? load_in(p.w + t * p.K + lane) : 1.0f) : 0.0f;
+    if (pos >= p.R) pos = -1;
+    float acc[C][V] = {};
+    constexpr int U = 4;       // pairs in flight
+    for (int k0 = 0; k0 < p.K; k0 += U) {
+        Vec<T, V> r[U][C];
+        float w[U];
+        bool on[U];
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const int k = min(k0 + u, 31), at = __shfl_sync(0xffffffffu, pos, k);
+            w[u] = __shfl_sync(0xffffffffu, wt, k);
+            on[u] = k0 + u < p.K && at >= 0;
+#pragma unroll
+            for (int i = 0; i < C; i++) {
+                const int c = base + 32 * V * i;
+                if (on[u] && c < p.N) r[u][i].load(static_cast<const T *>(p.rows) + at * p.ld + c);
+                else r[u][i].zero();
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            if (!on[u]) continue;
+#pragma unroll
+            for (int i = 0; i < C; i++) {
+                float v[V];
+                r[u][i].get(v);
+#pragma unroll
+                for (int k = 0; k < V; k++) acc[i][k] = fmaf(w[u], v[k], acc[i][k]);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < C; i++) {
+        const int c = base + 32 * V * i;
+        if (c >= p.N) continue;
+        Vec<Y, V> o;
+        if (p.add) {
+            float u[V];
+            o.load(static_cast<const Y *>(p.add) + t * p.ldadd + c);
+            o.get(u);
+#pragma unroll
+            for (int k = 0; k < V; k++) acc[i][k] += u[k];
+        }
+        o.set(acc[i]);
+        o.store(static_cast<Y *>(p.y) + t * p.ldy + c);
+    }
+}
+
+// Gradients: drows[r] = w_tk dy_t for the pair of token t = tokens[r] whose row r is (the sum of the
+// weights if the token names r more than once), zeros for rows that no pair of their token names;
+// dw_tk = rows[pos_tk] . dy_t.  Blocks of tokens read each row once and write its gradient beside it;
+// further blocks look for rows without a pair, 32 a warp, and fill them.
+struct CombineGradArgs {
+    const void *dy, *rows;
+    long long lddy, ld, ldd;
+    const int *pos, *tokens;
+    const float *w;
+    void *drows;
+    float *dw;
+    long long R;
+    int T, K, N, token_blocks;
+};
+
+constexpr int kCombGradThreads = 128;
+
+template <typename T, int V>
+__global__ void __launch_bounds__(kCombGradThreads) combine_grad_kernel(const CombineGradArgs p) {
+    constexpr int NW = kCombGradThreads / 32, U = 8;
+    __shared__ int s_pos[32], s_write[32];
+    __shared__ float s_w[32], s_part[NW][U];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    wait_for_stream();
+    T *drows = static_cast<T *>(p.drows);
+    if ((int)blockIdx.x >= p.token_blocks) {
+        const long long r = ((long long)((int)blockIdx.x - p.token_blocks) * NW + warp) * 32 + lane;
+        bool empty = r < p.R;
+        if (empty) {
+            const int t = load_in(p.tokens + r);
+            if ((unsigned)t < (unsigned)p.T)
+                for (int k = 0; k < p.K && empty; k++) empty = load_in(p.pos + (long long)t * p.K + k) != r;
+        }
+        unsigned todo = __ballot_sync(0xffffffffu, empty);
+        Vec<T, V> z;
+        z.zero();
+        while (todo) {
+            T *d = drows + (r - lane + __ffs(todo) - 1) * p.ldd;
+            todo &= todo - 1;
+            for (int c = V * lane; c < p.N; c += 32 * V) z.store(d + c);
+        }
+        return;
+    }
+    const long long t = blockIdx.x;
+    if (warp == 0) {
+        int pos = lane < p.K ? load_in(p.pos + t * p.K + lane) : -1;
+        if (pos >= p.R) pos = -1;
+        float w = lane < p.K ? (p.w ? load_in(p.w + t * p.K + lane) : 1.0f) : 0.0f;
+        const bool ours = pos >= 0 && load_in(p.tokens + pos) == t;
+        // a row that the token names twice: its first pair writes, with the sum of the weights
+        const unsigned same = __match_any_sync(0xffffffffu, pos >= 0 ? pos : (int)(0x80000000u | lane));
+        if (__ballot_sync(0xffffffffu, (same & (same - 1u)) != 0)) {
+            float sum = 0.0f;
+            for (int i = 0; i < 32; i++) {
+                const float o = __shfl_sync(0xffffffffu, w, i);
+                if (same >> i & 1u) sum += o;
+            }
+            w = sum;
+        }
+        s_pos[lane] = pos;
+        s_write[lane] = ours && lane == __ffs(same) - 1;
+        s_w[lane] = w;
+    }
+    __syncthreads();
+    const T *dy = static_cast<const T *>(p.dy) + t * p.lddy, *rows = static_cast<const T *>(p.rows);
+    for (int k0 = 0; k0 < p.K; k0 += U) {
+        float dot[U] = {};
+        for (int c = V * tid; c < p.N; c += V * kCombGradThreads) {
+            Vec<T, V> g, r[U];
+            float d[V];
+            g.load(dy + c);
+            if (p.dw) {
+#pragma unroll
+                for (int u = 0; u < U; u++) {
+                    const int at = k0 + u < p.K ? s_pos[k0 + u] : -1;
+                    if (at >= 0) r[u].load(rows + at * p.ld + c);
+                    else r[u].zero();
+                }
+            }
+            g.get(d);
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                if (k0 + u >= p.K || s_pos[k0 + u] < 0) continue;
+                float v[V];
+                if (p.dw) {
+                    r[u].get(v);
+#pragma unroll
+                    for (int k = 0; k < V; k++) dot[u] = fmaf(v[k], d[k], dot[u]);
+                }
+                if (p.drows && s_write[k0 + u]) {
+                    const float w = s_w[k0 + u];
+#pragma unroll
+                    for (int k = 0; k < V; k++) v[k] = w * d[k];
+                    r[u].set(v);
+                    r[u].store(drows + s_pos[k0 + u] * p.ldd + c);
+                }
+            }
+        }
+        if (p.dw) {
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+#pragma unroll
+                for (int i = 16; i; i >>= 1) dot[u] += __shfl_xor_sync(0xffffffffu, dot[u], i);
+                if (lane == 0) s_part[warp][u] = dot[u];
+            }
+            __syncthreads();
+            if (tid < U && k0 + tid < p.K) {
+                float s = s_part[0][tid];
+#pragma unroll
+                for (int i = 1; i < NW; i++) s += s_part[i][tid];
+                p.dw[t * p.K + k0 + tid] = s_pos[k0 + tid] >= 0 ? s : 0.0f;
+            }
+            __syncthreads();
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Norm of all gradients together, and clipping.  The tensors' addresses come as kernel parameters (no
+// table to upload, nothing to keep while a captured call lives).  A chunk is kChunk elements of one
+// tensor; blocks take every gridDim-th chunk.  Squares are added in float32 over a thread's batch, which
+// is added to a float64 sum; a batch whose largest magnitude's square would leave float32's normal range
+// (2^-50, 2^56) is squared in float64.  Clipping takes the chunks from the last to the first: what the
+// norm read last is still in L2.
+// ---------------------------------------------------------------------------
+
+constexpr int kChunk = 32768;
+constexpr int kClipThreads = 256;
+
+template <int MOST>
+struct ClipTable {
+    const void *in[MOST];
+    void *out[MOST];
+    long long n[MOST];
+    unsigned first[MOST + 1];       // first chunk of every tensor
+    uint8_t dtype[MOST];
+    int count;
+};
+
+template <int MOST>
+__device__ __forceinline__ int tensor_of(const ClipTable<MOST> &p, unsigned chunk) {
+    int lo = 0, hi = p.count - 1;
+    while (lo < hi) {
+        const int m = (lo + hi + 1) >> 1;
+        if (p.first[m] <= chunk) lo = m;
+        else hi = m - 1;
+    }
+    return lo;
+}
+
+// squares of a batch of magnitudes' float32 values
+template <int N>
+__device__ __forceinline__ double squares(const float (&v)[N]) {
+    float s = 0.0f, m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+        s = fmaf(v[i], v[i], s);
+        m = fmaxf(m, fabsf(v[i]));
+    }
+    if (m == 0.0f || (m > 8.8817842e-16f && m < 7.2057594e16f)) return (double)s;
+    double d = 0.0;
+#pragma unroll 1
+    for (int i = 0; i < N; i++) d = fma((double)v[i], (double)v[i], d);
+    return d;
+}
+
+// f(first element, elements) of a chunk by 16-byte runs, or elements where it begins or ends inside one
+template <typename T, typename HEAD, typename BODY>
+__device__ __forceinline__ void over_chunk(const T *p, int n, HEAD &&one, BODY &&run) {
+    constexpr int V = 16 / (int)sizeof(T);
+    const int off = (int)((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(T)), head = min(n, off ? V - off : 0);
+    const int body = (n - head) / V, tail = n - head - body * V;
+    if ((int)threadIdx.x < head) one(threadIdx.x);
+    if ((int)threadIdx.x >= 32 && (int)threadIdx.x - 32 < tail) one(head + body * V + (int)threadIdx.x - 32);
+    run(head, body);
+}
+
+template <typename T>
+__device__ __forceinline__ double chunk_squares(const T *p, int n) {
+    constexpr int V = 16 / (int)sizeof(T), U = 4;
+    double sum = 0.0;
+    over_chunk<T>(
+        p, n,
+        [&](int i) {
+            const double v = (double)to_float(load_in(p + i));
+            sum += v * v;
+        },
+        [&](int head, int body) {
+            for (int i = threadIdx.x; i < body; i += U * kClipThreads) {
+                Vec<T, V> r[U];
+                float v[U * V];
+#pragma unroll
+                for (int u = 0; u < U; u++) {
+                    if (i + u * kClipThreads < body) r[u].load(p + head + (long long)(i + u * kClipThreads) * V);
+                    else r[u].zero();
+                }
+#pragma unroll
+                for (int u = 0; u < U; u++) r[u].get(&v[u * V]);
+                sum += squares(v);
+            }
+        });
+    return sum;
+}
+
+template <int MOST>
+__global__ void __launch_bounds__(kClipThreads) grad_squares_kernel(const __grid_constant__ ClipTable<MOST> p, double *part) {
+    __shared__ double s_sum[32];
+    wait_for_stream();
+    double sum = 0.0;
+    for (unsigned c = blockIdx.x; c < p.first[p.count]; c += gridDim.x) {
+        const int k = tensor_of(p, c);
+        const long long at = (long long)(c - p.first[k]) * kChunk;
+        const int n = (int)min((long long)kChunk, p.n[k] - at);
+        if (p.dtype[k] == MOE_DTYPE_F32) sum += chunk_squares(static_cast<const float *>(p.in[k]) + at, n);
+        else if (p.dtype[k] == MOE_DTYPE_BF16) sum += chunk_squares(static_cast<const __nv_bfloat16 *>(p.in[k]) + at, n);
+        else sum += chunk_squares(static_cast<const __half *>(p.in[k]) + at, n);
+    }
+    sum = sum_all<false>(sum, s_sum);
+    if (threadIdx.x == 0) part[blockIdx.x] = sum;
+}
+
+__global__ void __launch_bounds__(1024) grad_norm_kernel(const double *part, int n, float *norm) {
+    __shared__ double s_sum[32];
+    wait_for_stream();
+    double v = 0.0;
+    for (int i = threadIdx.x; i < n; i += 1024) v += load_in(part + i);
+    v = sum_all<false>(v, s_sum);
+    if (threadIdx.x == 0) *norm = (float)sqrt(v);
+}
+
+template <typename T>
+__device__ __forceinline__ void chunk_scale(const T *p, T *out, int n, float c) {
+    constexpr int V = 16 / (int)sizeof(T), U = 4;
+    if ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(out)) & 15u) {      // runs of one are no runs of the other
+        for (int i = threadIdx.x; i < n; i += kClipThreads) out[i] = from_float<T>(to_float(load_in(p + i)) * c);
+        return;
+    }
+    over_chunk<T>(
+        p, n, [&](int i) { out[i] = from_float<T>(to_float(load_in(p + i)) * c); },
+        [&](int head, int body) {
+            for (int i = threadIdx.x; i < body; i += U * kClipThreads) {
+                Vec<T, V> r[U];
+#pragma unroll
+                for (int u = 0; u < U; u++)
+                    if (i + u * kClipThreads < body) r[u].load(p + head + (long long)(i + u * kClipThreads) * V);
+#pragma unroll
+                for (int u = 0; u < U; u++) {
+                    if (i + u * kClipThreads >= body) continue;
+                    float v[V];
+                    r[u].get(v);
+#pragma unroll
+                    for (int k = 0; k < V; k++) v[k] *= c;
+                    r[u].set(v);
+                    r[u].store(out + head + (long long)(i + u * kClipThreads) * V);
+                }
+            }
+        });
+}
+
+template <int MOST>
+__global__ void __launch_bounds__(kClipThreads) grad_clip_kernel(const __grid_constant__ ClipTable<MOST> p, const float *norm, float most) {
+    wait_for_stream();
+    const float ratio = most / (load_in(norm) + 1e-6f), c = ratio >= 1.0f ? 1.0f : ratio;      // a NaN stays one
+    const unsigned chunks = p.first[p.count];
+    for (unsigned i = blockIdx.x; i < chunks; i += gridDim.x) {
+        const unsigned ch = chunks - 1 - i;
+        const int k = tensor_of(p, ch);
+        if (c == 1.0f && p.in[k] == p.out[k]) continue;      // as they are
+        const long long at = (long long)(ch - p.first[k]) * kChunk;
+        const int n = (int)min((long long)kChunk, p.n[k] - at);
+        if (p.dtype[k] == MOE_DTYPE_F32) chunk_scale(static_cast<const float *>(p.in[k]) + at, static_cast<float *>(p.out[k]) + at, n, c);
+        else if (p.dtype[k] == MOE_DTYPE_BF16)
+            chunk_scale(static_cast<const __nv_bfloat16 *>(p.in[k]) + at, static_cast<__nv_bfloat16 *>(p.out[k]) + at, n, c);
+        else chunk_scale(static_cast<const __half *>(p.in[k]) + at, static_cast<__half *>(p.out[k]) + at, n, c);
+    }
+}
+
+constexpr int kClipFew = 64, kClipMany = 512;      // tensors of a launch: 2 and 17 KB of parameters
+constexpr int kClipPerSm = 6;
+
+// f(table, blocks) for tables of up to MOST tensors (2^45 elements in all at most: chunks are 32-bit)
+template <int MOST, typename F>
+cudaError_t by_tables(int count, const void *const *in, void *const *out, const int32_t *dtype, const int64_t *n, F &&f) {
+    ClipTable<MOST> p;
+    for (int i = 0; i < count;) {
+        p.count = 0;
+        unsigned chunks = 0;
+        for (; i < count && p.count < MOST; i++) {
+            if (n[i] == 0) continue;
+            p.in[p.count] = in[i];
+            p.out[p.count] = out ? out[i] : nullptr;
+            p.n[p.count] = n[i];
+            p.dtype[p.count] = (uint8_t)dtype[i];
+            p.first[p.count++] = chunks;
+            chunks += (unsigned)((n[i] + kChunk - 1) / kChunk);
+        }
+        if (p.count == 0) break;
+        p.first[p.count] = chunks;
+        const unsigned most = (unsigned)sm_count() * kClipPerSm;
+        const cudaError_t e = f(p, chunks < most ? chunks : most);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_combine_forward(const void *rows, int dtype, long long ld, long long R, int N, const int *pos, int T, int K, const float *w,
+                                   const void *add, long long ldadd, void *y, int y_dtype, long long ldy, cudaStream_t st) {
+    CombineArgs p = {rows, ld, ldadd, ldy, pos, w, add, y, R, T, K, N, 1};
+    return by_dtype(dtype, [&](auto rt) {
+        using X = decltype(rt);
+        return by_dtype(y_dtype, [&](auto yt) {
+            using Y = decltype(yt);
+            auto fits = [&](int v) {
+                const int by = min(16, v * (int)sizeof(Y));
+                return N % v == 0 && runs_of(rows, ld, sizeof(X), min(16, v * (int)sizeof(X))) && runs_of(y, ldy, sizeof(Y), by) &&
+                       (!add || runs_of(add, ldadd, sizeof(Y), by));
+            };
+            auto go = [&](auto kernel, int each) {
+                p.parts = (N + 32 * each - 1) / (32 * each);
+                return launch_early(kernel, (unsigned)(((long long)T * p.parts + kCombWarps - 1) / kCombWarps), 32 * kCombWarps, 0, st, 1, p);
+            };
+            if (fits(8)) return go(combine_kernel<X, Y, 8, 1>, 8);
+            if (fits(2)) return go(combine_kernel<X, Y, 2, 4>, 8);
+            return go(combine_kernel<X, Y, 1, 8>, 8);
+        });
+    });
+}
+
+cudaError_t launch_combine_backward(const void *dy, int dtype, long long lddy, const void *rows, long long ld, long long R, int N, const int *pos,
+                                    int T, int K, const int *tokens, const float *w, void *drows, long long ldd, float *dw, cudaStream_t st) {
+    CombineGradArgs p = {dy, rows, lddy, ld, ldd, pos, tokens, w, drows, dw, R, T, K, N, T};
+    const long long more = drows ? (R + kCombGradThreads - 1) / kCombGradThreads : 0;
+    return by_dtype(dtype, [&](auto t) {
+        using X = decltype(t);
+        auto fits = [&](int v) {
+            const int b = min(16, v * (int)sizeof(X));
+            return N % v == 0 && runs_of(dy, lddy, sizeof(X), b) && (!dw || runs_of(rows, ld, sizeof(X), b)) && (!drows || runs_of(drows, ldd, sizeof(X), b));
+        };
+        auto go = [&](auto kernel) { return launch_early(kernel, (unsigned)(T + more), kCombGradThreads, 0, st, 1, p); };
+        if (fits(8)) return go(combine_grad_kernel<X, 8>);
+        if (fits(2)) return go(combine_grad_kernel<X, 2>);
+        return go(combine_grad_kernel<X, 1>);
+    });
+}
+
+size_t grad_norm_workspace(int count) {
+    const size_t tables = count <= kClipFew ? 1 : ((size_t)count + kClipMany - 1) / kClipMany;
+    return tables * sm_count() * kClipPerSm * sizeof(double);
+}
+
+cudaError_t launch_grad_norm(int count, const void *const *grads, const int32_t *dtype, const int64_t *n, float *norm, void *ws, cudaStream_t st) {
+    double *part = static_cast<double *>(ws);
+    int parts = 0;
+    auto go = [&](auto &table, unsigned blocks) {
+        constexpr int MOST = sizeof(table.in) / sizeof(void *);
+        const cudaError_t e = launch_early(grad_squares_kernel<MOST>, blocks, kClipThreads, 0, st, 1, table, part + parts);
+        parts += (int)blocks;
+        return e;
+    };
+    const cudaError_t e = count <= kClipFew ? by_tables<kClipFew>(count, grads, nullptr, dtype, n, go) : by_tables<kClipMany>(count, grads, nullptr, dtype, n, go);
+    if (e != cudaSuccess) return e;
+    return launch_early(grad_norm_kernel, 1, 1024, 0, st, 1, part, parts, norm);
+}
+
+cudaError_t launch_grad_clip(int count, const void *const *grads, const int32_t *dtype, const int64_t *n, const float *norm, float most,
+                             void *const *out, cudaStream_t st) {
+    auto go = [&](auto &table, unsigned blocks) {
+        constexpr int MOST = sizeof(table.in) / sizeof(void *);
+        return launch_early(grad_clip_kernel<MOST>, blocks, kClipThreads, 0, st, 1, table, norm, most);
+    };
+    return count <= kClipFew ? by_tables<kClipFew>(count, grads, out, dtype, n, go) : by_tables<kClipMany>(count, grads, out, dtype, n, go);
+}
+
+}  // namespace moe

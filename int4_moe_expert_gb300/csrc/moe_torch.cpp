@@ -61,9 +61,12 @@ public:
     // stream: None (the current one) or a handle
     Call(const char *where, PyObject *const *args, Py_ssize_t n, Py_ssize_t want) : where_(where) {
         if (n != want) refuse(where, MOE_ERR_INVALID, "%zd arguments, need %zd", n, want);
-        const at::Tensor &t = tensor(args[0], "the first argument");
-        if (!t.is_cuda()) fail("the tensors must be on a CUDA device");
-        dev_ = t.get_device();
+        dev_ = c10::cuda::current_device();
+        if (!PyList_Check(args[0]) || PyList_GET_SIZE(args[0])) {       // a list: its first tensor
+            const at::Tensor &t = tensor(PyList_Check(args[0]) ? PyList_GET_ITEM(args[0], 0) : args[0], "the first argument");
+            if (!t.is_cuda()) fail("the tensors must be on a CUDA device");
+            dev_ = t.get_device();
+        }
         if (dev_ != c10::cuda::current_device())
             fail("the tensors are on cuda:%d, the current device is cuda:%d", dev_, (int)c10::cuda::current_device());
         const auto now = c10::cuda::getCurrentCUDAStream(dev_);
@@ -127,13 +130,19 @@ public:
         if (over || v < INT32_MIN || v > INT32_MAX) fail("%s: does not fit 32 bits", name);
         return (int32_t)v;
     }
-    float real(PyObject *o, const char *name) const {
+    float real(PyObject *o, const char *name) const { return (float)real64(o, name); }
+    double real64(PyObject *o, const char *name) const {
         const double v = PyFloat_AsDouble(o);
         if (v == -1.0 && PyErr_Occurred()) {
             PyErr_Clear();
             fail("%s: need a number", name);
         }
-        return (float)v;
+        return v;
+    }
+    bool flag(PyObject *o) const {
+        const int v = PyObject_IsTrue(o);
+        if (v < 0) throw Refused{};
+        return v != 0;
     }
     at::Tensor empty(at::IntArrayRef shape, at::ScalarType type) const {
         return at::empty(shape, at::TensorOptions().dtype(type).device(at::Device(at::kCUDA, (c10::DeviceIndex)dev_)));
@@ -355,6 +364,221 @@ PyObject *fp8_wgrad(PyObject *const *a, Py_ssize_t n) {
     return THPVariable_Wrap(out);
 }
 
+// logits, top_k, bias, score_func, n_group, topk_group, norm_topk, routed_scale, mask, stream
+PyObject *route_forward(PyObject *const *a, Py_ssize_t n) {
+    const Call c("moe_route_forward", a, n, 10);
+    const at::Tensor &x = c.dims(a[0], "logits", 2);
+    const void *p = c.need(x, "logits", kFloats, x.sizes(), true);
+    const int32_t T = c.size(x.size(0), "tokens"), E = c.size(x.size(1), "experts"), K = c.integer(a[1], "top_k");
+    const float *bias = a[2] == Py_None ? nullptr : static_cast<const float *>(c.need(a[2], "bias", kF32, {E}));
+    const uint8_t *mask = a[8] == Py_None ? nullptr : static_cast<const uint8_t *>(c.need(a[8], "mask", kMask, {T}));
+    const int64_t k = K >= 1 && K <= E ? K : 0;      // sizes that the call refuses allocate nothing first
+    at::Tensor idx = c.empty({T, k}, at::kInt), w = c.empty({T, k}, at::kFloat);
+    c.check(moe_route_forward(p, dtype_code(x.scalar_type()), Call::row_stride(x), T, E, bias, K, c.integer(a[3], "score_func"),
+                              c.integer(a[4], "n_group"), c.integer(a[5], "topk_group"), c.flag(a[6]), c.real(a[7], "routed_scale"), mask,
+                              idx.data_ptr<int32_t>(), w.data_ptr<float>(), c.stream()));
+    return tuple({idx, w});
+}
+
+// logits, topk_idx, grad_w, score_func, norm_topk, routed_scale, out, accumulate, stream
+PyObject *route_backward(PyObject *const *a, Py_ssize_t n) {
+    const Call c("moe_route_backward", a, n, 9);
+    const at::Tensor &x = c.dims(a[0], "logits", 2), &idx = c.dims(a[1], "topk_idx", 2);
+    const void *p = c.need(x, "logits", kFloats, x.sizes(), true);
+    const int32_t T = c.size(x.size(0), "tokens"), E = c.size(x.size(1), "experts"), K = c.size(idx.size(1), "top_k");
+    const void *pi = c.need(idx, "topk_idx", kI32, {T, K}), *pg = c.need(a[2], "grad_w", kF32, {T, K});
+    const bool add = c.flag(a[7]);
+    if (add && a[6] == Py_None) c.fail("accumulate: need out");
+    at::Tensor out = c.output(a[6], Py_None, {T, E}, x.scalar_type(), true);
+    if (out.scalar_type() != x.scalar_type())
+        c.fail("out: its type is %s, that of logits %s", at::toString(out.scalar_type()), at::toString(x.scalar_type()));
+    c.check(moe_route_backward(p, dtype_code(x.scalar_type()), Call::row_stride(x), T, E, static_cast<const int32_t *>(pi), K,
+                               c.integer(a[3], "score_func"), c.flag(a[4]), c.real(a[5], "routed_scale"), static_cast<const float *>(pg),
+                               out.data_ptr(), Call::row_stride(out), add, c.stream()));
+    return THPVariable_Wrap(out);
+}
+
+// the norm's weight: float32 or the type of x
+struct NormWeight {
+    const void *p = nullptr;
+    int32_t dtype = MOE_DTYPE_F32;
+    NormWeight(const Call &c, PyObject *o, const at::Tensor &x) {
+        if (o == Py_None) return;
+        const at::Tensor &t = c.tensor(o, "weight");
+        p = c.need(t, "weight", {at::kFloat, x.scalar_type()}, {x.size(1)});
+        dtype = dtype_code(t.scalar_type());
+    }
+};
+
+// x, residual, weight, eps, values, quantize, out, stream
+PyObject *norm_forward(PyObject *const *a, Py_ssize_t n) {
+    const Call c("moe_norm_forward", a, n, 8);
+    const at::Tensor &x = c.dims(a[0], "x", 2);
+    const void *p = c.need(x, "x", kFloats, x.sizes(), true), *res = nullptr;
+    const NormWeight w(c, a[2], x);
+    const bool values = c.flag(a[4]), quant = c.flag(a[5]);
+    const double eps = c.real64(a[3], "eps");
+    const int32_t T = c.size(x.size(0), "tokens"), H = c.size(x.size(1), "width");
+    at::Tensor h = x;
+    int64_t ldr = H;
+    if (a[1] != Py_None) {
+        const at::Tensor &r = c.tensor(a[1], "residual");
+        res = c.need(r, "residual", {at::kFloat, x.scalar_type()}, x.sizes(), true);
+        ldr = Call::row_stride(r);
+        h = c.output(a[6], Py_None, x.sizes(), r.scalar_type(), true);
+        if (h.scalar_type() != r.scalar_type())
+            c.fail("out: its type is %s, that of residual %s", at::toString(h.scalar_type()), at::toString(r.scalar_type()));
+    } else if (a[6] != Py_None) {
+        c.fail("out: is the sum with a residual, and there is none");
+    }
+    at::Tensor y, codes, scales, rstd = c.empty({T}, at::kFloat);
+    if (values) y = c.empty(x.sizes(), x.scalar_type());
+    if (quant) {
+        codes = c.empty(x.sizes(), at::kFloat8_e4m3fn);
+        scales = c.empty({blocks(H), T}, at::kFloat);
+    }
+    c.check(moe_norm_forward(p, dtype_code(x.scalar_type()), Call::row_stride(x), res, dtype_code(h.scalar_type()), ldr, w.p, w.dtype, T, H, eps,
+                             res ? h.data_ptr() : nullptr, Call::row_stride(h), values ? y.data_ptr() : nullptr, H, rstd.data_ptr<float>(),
+                             quant && T ? static_cast<uint8_t *>(codes.data_ptr()) : nullptr, quant && T ? scales.data_ptr<float>() : nullptr,
+                             c.stream()));
+    return quant ? tuple({y, h, rstd, codes, scales}) : tuple({y, h, rstd});
+}
+
+// dy, h, rstd, weight, grad_h, out, stream
+PyObject *norm_backward(PyObject *const *a, Py_ssize_t n) {
+    const Call c("moe_norm_backward", a, n, 7);
+    const at::Tensor &dy = c.dims(a[0], "dy", 2), &h = c.tensor(a[1], "h");
+    const void *pd = c.need(dy, "dy", kFloats, dy.sizes(), true), *ph = c.need(h, "h", {at::kFloat, dy.scalar_type()}, dy.sizes(), true), *pg = nullptr;
+    const int32_t T = c.size(dy.size(0), "tokens"), H = c.size(dy.size(1), "width");
+    const void *pr = c.need(a[2], "rstd", kF32, {T});
+    const NormWeight w(c, a[3], dy);
+    int64_t ldg = H;
+    if (a[4] != Py_None) {
+        const at::Tensor &g = c.tensor(a[4], "grad_h");
+        pg = c.need(g, "grad_h", {h.scalar_type()}, dy.sizes(), true);
+        ldg = Call::row_stride(g);
+    }
+    at::Tensor out = c.output(a[5], Py_None, dy.sizes(), h.scalar_type(), true), dw, ws;
+    if (out.scalar_type() != h.scalar_type())
+        c.fail("out: its type is %s, that of h %s", at::toString(out.scalar_type()), at::toString(h.scalar_type()));
+    const size_t need = w.p ? moe_norm_workspace(T, H) : 0;
+    if (w.p) dw = c.empty({H}, at::kFloat);
+    if (need) ws = c.empty({(int64_t)need}, at::kByte);
+    c.check(moe_norm_backward(pd, dtype_code(dy.scalar_type()), Call::row_stride(dy), ph, dtype_code(h.scalar_type()), Call::row_stride(h),
+                              static_cast<const float *>(pr), w.p, w.dtype, pg, ldg, T, H, out.data_ptr(), Call::row_stride(out),
+                              w.p ? dw.data_ptr<float>() : nullptr, need ? ws.data_ptr() : nullptr, need, c.stream()));
+    return tuple({out, dw});
+}
+
+struct Combine {
+    const int32_t *pos;
+    const float *w = nullptr;
+    int32_t T, K;
+    Combine(const Call &c, PyObject *pos_o, PyObject *w_o) {
+        const at::Tensor &t = c.dims(pos_o, "pos", 2);
+        pos = static_cast<const int32_t *>(c.need(t, "pos", kI32, t.sizes()));
+        T = c.size(t.size(0), "tokens");
+        K = c.size(t.size(1), "top_k");
+        if (w_o != Py_None) w = static_cast<const float *>(c.need(w_o, "topk_w", kF32, {T, K}));
+    }
+};
+
+// rows, pos, topk_w, add, out, out_dtype, stream
+PyObject *combine_forward(PyObject *const *a, Py_ssize_t n) {
+    const Call c("moe_combine_forward", a, n, 7);
+    const at::Tensor &r = c.dims(a[0], "rows", 2);
+    const void *p = c.need(r, "rows", kFloats, r.sizes(), true), *add = nullptr;
+    const Combine q(c, a[1], a[2]);
+    const int32_t R = c.size(r.size(0), "rows"), N = c.size(r.size(1), "width");
+    at::Tensor out = c.output(a[4], a[5], {q.T, N}, a[3] == Py_None ? r.scalar_type() : c.tensor(a[3], "add").scalar_type(), true);
+    int64_t ldadd = N;
+    if (a[3] != Py_None) {
+        const at::Tensor &t = c.tensor(a[3], "add");
+        add = c.need(t, "add", {out.scalar_type()}, {q.T, N}, true);
+        ldadd = Call::row_stride(t);
+    }
+    c.check(moe_combine_forward(p, dtype_code(r.scalar_type()), Call::row_stride(r), R, N, q.pos, q.T, q.K, q.w, add, ldadd, out.data_ptr(),
+                                dtype_code(out.scalar_type()), Call::row_stride(out), c.stream()));
+    return THPVariable_Wrap(out);
+}
+
+// dy, rows, pos, tokens, topk_w, out, stream
+PyObject *combine_backward(PyObject *const *a, Py_ssize_t n) {
+    const Call c("moe_combine_backward", a, n, 7);
+    const at::Tensor &dy = c.dims(a[0], "dy", 2), &r = c.dims(a[1], "rows", 2);
+    const Combine q(c, a[2], a[4]);
+    const int32_t R = c.size(r.size(0), "rows"), N = c.size(r.size(1), "width");
+    const void *pd = c.need(dy, "dy", kFloats, {q.T, N}, true), *pr = c.need(r, "rows", {dy.scalar_type()}, r.sizes(), true);
+    const void *pt = c.need(a[3], "tokens", kI32, {R});
+    at::Tensor out = c.output(a[5], Py_None, r.sizes(), r.scalar_type(), true), dw = c.empty({q.T, q.K}, at::kFloat);
+    if (out.scalar_type() != r.scalar_type())
+        c.fail("out: its type is %s, that of rows %s", at::toString(out.scalar_type()), at::toString(r.scalar_type()));
+    c.check(moe_combine_backward(pd, dtype_code(dy.scalar_type()), Call::row_stride(dy), pr, Call::row_stride(r), R, N, q.pos, q.T, q.K,
+                                 static_cast<const int32_t *>(pt), q.w, out.data_ptr(), Call::row_stride(out), dw.data_ptr<float>(), c.stream()));
+    return tuple({out, dw});
+}
+
+// a list of gradients: float tensors on the device whose elements lie together, in any order
+struct Grads {
+    std::vector<const void *> p;
+    std::vector<int32_t> dtype;
+    std::vector<int64_t> n;
+    Grads(const Call &c, PyObject *list) {
+        const Py_ssize_t count = PyList_GET_SIZE(list);
+        p.reserve(count);
+        dtype.reserve(count);
+        n.reserve(count);
+        for (Py_ssize_t i = 0; i < count; i++) {
+            const at::Tensor &t = c.tensor(PyList_GET_ITEM(list, i), "grads");
+            if (t.layout() != at::kStrided || !t.is_non_overlapping_and_dense()) c.fail("grads: tensor %zd has gaps between its elements", i);
+            if (!t.is_cuda() || t.get_device() != c10::cuda::current_device())
+                c.fail("grads: tensor %zd is on %s, the call on cuda:%d", i, t.device().str().c_str(), (int)c10::cuda::current_device());
+            const int d = dtype_code(t.scalar_type());
+            if (d < 0) c.fail("grads: the type of tensor %zd is %s", i, at::toString(t.scalar_type()));
+            p.push_back(t.data_ptr());
+            dtype.push_back(d);
+            n.push_back(t.numel());
+        }
+    }
+};
+
+// grads, stream
+PyObject *grad_norm(PyObject *const *a, Py_ssize_t n) {
+    if (n < 1 || !PyList_Check(a[0])) refuse("moe_grad_norm", MOE_ERR_INVALID, "grads: need a list of tensors");
+    const Call c("moe_grad_norm", a, n, 2);
+    const Grads g(c, a[0]);
+    at::Tensor norm = c.empty({1}, at::kFloat);
+    const size_t need = moe_grad_norm_workspace(c.size((int64_t)g.p.size(), "grads"));
+    at::Tensor ws = c.empty({(int64_t)need}, at::kByte);
+    c.check(moe_grad_norm((int32_t)g.p.size(), g.p.data(), g.dtype.data(), g.n.data(), norm.data_ptr<float>(), ws.data_ptr(), need, c.stream()));
+    return THPVariable_Wrap(norm);
+}
+
+// grads, norm, max_norm, out, stream
+PyObject *grad_clip(PyObject *const *a, Py_ssize_t n) {
+    if (n < 4 || !PyList_Check(a[0]) || (a[3] != Py_None && !PyList_Check(a[3])))
+        refuse("moe_grad_clip", MOE_ERR_INVALID, "grads, out: need lists of tensors");
+    const Call c("moe_grad_clip", a, n, 5);
+    const Grads g(c, a[0]);
+    const at::Tensor &norm = c.tensor(a[1], "norm");
+    if (norm.numel() != 1) c.fail("norm: need one value");
+    const void *pn = c.need(norm, "norm", kF32, norm.sizes());
+    std::vector<void *> out;
+    if (a[3] != Py_None) {
+        const Grads o(c, a[3]);
+        if (o.p.size() != g.p.size()) c.fail("out: %zu tensors, grads has %zu", o.p.size(), g.p.size());
+        for (size_t i = 0; i < o.p.size(); i++) {
+            const at::Tensor &s = THPVariable_Unpack(PyList_GET_ITEM(a[0], i)), &t = THPVariable_Unpack(PyList_GET_ITEM(a[3], i));
+            if (s.scalar_type() != t.scalar_type() || !s.sizes().equals(t.sizes()) || !s.strides().equals(t.strides()))
+                c.fail("out: tensor %zu differs from its gradient in type, shape or strides", i);
+            out.push_back(const_cast<void *>(o.p[i]));
+        }
+    }
+    c.check(moe_grad_clip(c.size((int64_t)g.p.size(), "grads"), g.p.data(), g.dtype.data(), g.n.data(), static_cast<const float *>(pn),
+                          c.real(a[2], "max_norm"), a[3] != Py_None ? out.data() : nullptr, c.stream()));
+    Py_RETURN_NONE;
+}
+
 template <PyObject *(*F)(PyObject *const *, Py_ssize_t)>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
@@ -374,7 +598,9 @@ PyObject *set_error(PyObject *, PyObject *cls) {
 
 #define MOE_ENTRY(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(entry<f>)), METH_FASTCALL, nullptr}
 PyMethodDef kMethods[] = {MOE_ENTRY(expert_lists), MOE_ENTRY(balance_forward), MOE_ENTRY(balance_backward), MOE_ENTRY(fp8_quantize),
-                          MOE_ENTRY(fp8_quantize_weights), MOE_ENTRY(fp8_matmul), MOE_ENTRY(fp8_wgrad),
+                          MOE_ENTRY(fp8_quantize_weights), MOE_ENTRY(fp8_matmul), MOE_ENTRY(fp8_wgrad), MOE_ENTRY(route_forward), MOE_ENTRY(route_backward),
+                          MOE_ENTRY(norm_forward), MOE_ENTRY(norm_backward), MOE_ENTRY(combine_forward), MOE_ENTRY(combine_backward),
+                          MOE_ENTRY(grad_norm), MOE_ENTRY(grad_clip),
                           {"set_error", set_error, METH_O, nullptr}, {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_moe_torch", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 
