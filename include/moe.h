@@ -580,7 +580,7 @@ moe_status moe_combine_backward(const void *dy, int32_t dtype, int64_t lddy, con
                                 const float *topk_w, void *drows, int64_t ldd, float *dtopk_w, void *stream);
 
 /* norm[1] = the 2-norm of all gradients together (float32; the squares' sums are float64, so they neither
- * overflow nor vanish; a NaN or an infinity anywhere is one in norm).  grads, dtypes, sizes: host arrays of n_tensors
+ * overflow nor vanish; a NaN or an infinity anywhere is one in norm, and a norm beyond float32 infinite).  grads, dtypes, sizes: host arrays of n_tensors
  * (0..65536) device addresses on their elements' boundary, MOE_DTYPE_* and numbers of elements (up to 2^45
  * in all); read during the call alone, so that a captured call needs none of them later.  workspace:
  * moe_grad_norm_workspace(n_tensors) bytes on the current device, 16-byte aligned. */

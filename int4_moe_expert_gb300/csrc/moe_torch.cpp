@@ -61,11 +61,12 @@ public:
     // stream: None (the current one) or a handle
     Call(const char *where, PyObject *const *args, Py_ssize_t n, Py_ssize_t want) : where_(where) {
         if (n != want) refuse(where, MOE_ERR_INVALID, "%zd arguments, need %zd", n, want);
-        dev_ = c10::cuda::current_device();
         if (!PyList_Check(args[0]) || PyList_GET_SIZE(args[0])) {       // a list: its first tensor
             const at::Tensor &t = tensor(PyList_Check(args[0]) ? PyList_GET_ITEM(args[0], 0) : args[0], "the first argument");
             if (!t.is_cuda()) fail("the tensors must be on a CUDA device");
             dev_ = t.get_device();
+        } else {
+            dev_ = c10::cuda::current_device();
         }
         if (dev_ != c10::cuda::current_device())
             fail("the tensors are on cuda:%d, the current device is cuda:%d", dev_, (int)c10::cuda::current_device());
