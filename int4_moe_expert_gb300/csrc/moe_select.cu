@@ -16,9 +16,9 @@ namespace {
 // the experts at or above it (8.9 on average for 8 of 256 in 32 lanes, 10.4 in 16) contain the choice:
 // one sort of LPT maxima and one ranking of at most LPT candidates instead of K rounds over all
 // experts.  Maxima and candidates go by a fast sigmoid less a margin for its error; the candidates'
-// keys are computed again, one a lane.  The order is that of the exact keys: where two neighbours of the
-// ranking are nearer than float32 tells (and not equal by construction), or there are more candidates
-// than lanes, the warp does the row over in float64.
+// keys are computed again, one a lane.  The order is that of the float64 keys: where two neighbours of the
+// ranking are nearer than float32 tells, or there are more candidates than lanes, the whole warp ranks them in
+// float64; where two groups' scores are that near, or more than 32 candidates, it does the row over.
 // ---------------------------------------------------------------------------
 
 constexpr int kRouteWarps = 4;
@@ -37,9 +37,13 @@ struct RouteArgs {
     float scale;
 };
 
-// Of a sigmoid's value and its sum with a bias, in float32: 2^-22 of 1 + the key covers exp (2 units),
-// the sum, the quotient and the sum with the bias; with the fast exp and reciprocal 2^-20.
-constexpr float kNear = 1.0f / (1 << 20), kFast = 1.0f / (1 << 19);
+// Errors of a key v = sigmoid + bias in float32, in units u = 2^-24.  exp(-l) to 2 ulp: at most 1 u of the
+// sigmoid (its derivative by the relative error is s (1 - s) <= 1/4); the sum, the quotient and the
+// sum with the bias: s, s and |v|.  So 3 + |v| in all.  The fast exp is documented to (2 + 1.173 |l|) ulp:
+// (0.5 + 0.263) 2 u since |l| s (1 - s) < 0.2240; the sum s, the fast quotient 2 ulp, 4 s, the bias |v|: below 7 + |v|.
+constexpr float kUnit = 1.0f / (1 << 24);
+__device__ __forceinline__ float key_error(float v) { return kUnit * (3.0f + fabsf(v)); }
+__device__ __forceinline__ float fast_error(float v) { return kUnit * (7.0f + fabsf(v)); }
 
 __device__ __forceinline__ float sigmoid_fast(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
 __device__ __forceinline__ float sigmoid(float x) {
@@ -136,7 +140,7 @@ __global__ void __launch_bounds__(kRouteThreads, L::PER_SM) route_kernel(const R
     extern __shared__ double route_sm[];                  // [warps][E]: float64 keys; or scores [G][E] float32
     __shared__ Chosen s_sel[kRouteWarps][G][LPT + 1];
     __shared__ float s_key[kRouteWarps][G][LPT + 1];
-    __shared__ short s_cand[kRouteWarps][G][LPT];
+    __shared__ short s_cand[kRouteWarps][G][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % LPT, g = lane / LPT;
     const unsigned lanes = LPT == 32 ? 0xffffffffu : (1u << LPT) - 1u;
     double *key64 = route_sm + (size_t)warp * p.E;
@@ -174,7 +178,7 @@ __global__ void __launch_bounds__(kRouteThreads, L::PER_SM) route_kernel(const R
             for (int j = 0; j < J; j++)
                 if (expert(j) < p.E) score[expert(j)] = a[j];
             __syncwarp();
-            float best = -INFINITY;
+            float best = -INFINITY, err = 0.0f;
             if (l < p.groups) {
                 float b1 = -INFINITY, b2 = -INFINITY;
                 const float *s = score + l * p.per_group;
@@ -186,6 +190,7 @@ __global__ void __launch_bounds__(kRouteThreads, L::PER_SM) route_kernel(const R
                     if (++i == p.per_group) i = 0;
                 }
                 best = p.per_group > 1 ? b1 + b2 : b1;
+                err = p.per_group > 1 ? fast_error(b1) + fast_error(b2) + kUnit * fabsf(best) : fast_error(b1);
             }
             int rank = 0;
             for (int i = 0; i < p.groups; i++) {
@@ -193,15 +198,15 @@ __global__ void __launch_bounds__(kRouteThreads, L::PER_SM) route_kernel(const R
                 rank += v > best || (v == best && i < l) ? 1 : 0;
             }
             const bool keep = l < p.groups && rank < p.kept;
-            float lo = keep ? best : INFINITY, hi = l < p.groups && !keep ? best : -INFINITY;
+            float lo = keep ? best - err : INFINITY, hi = l < p.groups && !keep ? best + err : -INFINITY;
 #pragma unroll
             for (int d = LPT / 2; d; d >>= 1) {
                 lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, d));
                 hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, d));
             }
-            // a group's NaN or infinite score: float64 decides, as between near ones
-            if (p.kept < p.groups) slow = !(lo - hi > 2.0f * kFast * (2.0f + fabsf(lo)));
-            slow |= __ballot_sync(0xffffffffu, isnan(best)) != 0;
+            // near ones, and a group's NaN or infinite score: float64 decides
+            if (p.kept < p.groups) slow = !(lo > hi);
+            slow |= __ballot_sync(0xffffffffu, isnan(best) || isnan(err)) != 0;
             const unsigned kept = __ballot_sync(0xffffffffu, keep) >> (g * LPT) & lanes;
 #pragma unroll
             for (int j = 0; j < J; j++) {
@@ -225,7 +230,7 @@ __global__ void __launch_bounds__(kRouteThreads, L::PER_SM) route_kernel(const R
                 m = ((l & k) == 0) == ((l & d) == 0) ? fmaxf(m, o) : fminf(m, o);
             }
         const float kth = __shfl_sync(0xffffffffu, m, p.K - 1, LPT);
-        const float least = biased ? kth - kFast * (1.0f + fabsf(kth)) : kth;
+        const float least = biased ? kth - 2.0f * fast_error(kth) : kth;
         slow |= !(least > -INFINITY);
         unsigned mine = 0;
 #pragma unroll
@@ -240,15 +245,17 @@ __global__ void __launch_bounds__(kRouteThreads, L::PER_SM) route_kernel(const R
         }
         const int n = __shfl_sync(0xffffffffu, at, LPT - 1, LPT);
         at -= own;
-        while (mine != 0 && at < LPT) {
+        while (mine != 0 && at < 32) {
             const int j = __ffs(mine) - 1;
             mine &= mine - 1;
             s_cand[warp][g][at++] = (short)(V * (l + LPT * (j / V)) + j % V);
         }
-        slow |= n > LPT;
+        slow |= n > 32;
+        const bool many = on && !slow && n > LPT;
+        unsigned again = LPT < 32 ? __ballot_sync(0xffffffffu, many) : 0u;
         __syncwarp();
         // candidates: their keys, their ranks
-        const bool one = on && !slow && l < n;
+        const bool one = on && !slow && !many && l < n;
         const int e = one ? s_cand[warp][g][l] : -1;
         const float xe = one ? to_float(load_in(row + e)) : 0.0f;
         const float be = one && biased ? load_in(p.bias + e) : 0.0f;
@@ -273,15 +280,31 @@ __global__ void __launch_bounds__(kRouteThreads, L::PER_SM) route_kernel(const R
         if (biased) {
             // neighbours that float32 does not tell apart; the same logit and bias are equal
             bool near = false;
-            if (on && !slow && l < p.K && l + 1 < n) {
+            if (one && l < p.K && l + 1 < n) {
                 const Chosen u = s_sel[warp][g][l], v = s_sel[warp][g][l + 1];
                 const float ku = s_key[warp][g][l], kv = s_key[warp][g][l + 1];
-                near = !(ku - kv > kNear * (1.0f + fabsf(ku))) && !(u.x == v.x && load_in(p.bias + u.e) == load_in(p.bias + v.e));
+                near = !(ku - kv > 2.0f * key_error(ku)) && !(u.x == v.x && load_in(p.bias + u.e) == load_in(p.bias + v.e));
             }
-            slow |= (__ballot_sync(0xffffffffu, near) >> (g * LPT) & lanes) != 0;
+            again |= __ballot_sync(0xffffffffu, near);
             __syncwarp();
         }
-        unsigned again = __ballot_sync(0xffffffffu, slow && on && l == 0);
+        // those tokens' candidates by all lanes, in float64
+        while (again) {
+            const int r = (__ffs(again) - 1) / LPT, count = __shfl_sync(0xffffffffu, n, r * LPT);
+            again &= r + 1 < G ? ~0u << ((r + 1) * LPT % 32) : 0u;
+            const int ec = lane < count ? s_cand[warp][r][lane] : -1;
+            const float xc = lane < count ? logit<T>(p, t0 + r, ec) : 0.0f;
+            const double k64 = biased && lane < count ? sigmoid64((double)xc) + (double)load_in(p.bias + ec) : (double)xc;
+            int r64 = 0;
+            for (int c = 0; c < count; c++) {
+                const double v = __shfl_sync(0xffffffffu, k64, c);
+                const int o = __shfl_sync(0xffffffffu, ec, c);
+                r64 += v > k64 || (v == k64 && o < ec) ? 1 : 0;
+            }
+            if (lane < count && r64 < p.K) s_sel[warp][r][r64] = {ec, xc};
+            __syncwarp();
+        }
+        again = __ballot_sync(0xffffffffu, slow && on && l == 0);
         while (again) {
             const int r = (__ffs(again) - 1) / LPT;
             again &= again - 1;
