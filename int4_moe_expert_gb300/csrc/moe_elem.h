@@ -34,6 +34,18 @@ __device__ __forceinline__ uint32_t codes2(float a, float b) {   // a in the low
     return r;
 }
 
+// 2^x to a relative 2^-22 and 1 / x to 2^-23 (the documented errors), subnormals as zeros
+__device__ __forceinline__ float ex2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // two neighbours of one 32-bit word, and back (rounded to nearest even)
 template <typename T>
 __device__ __forceinline__ void from_word(uint32_t w, float &a, float &b) {

@@ -27,6 +27,7 @@ constexpr int kRouteThreads = 32 * kRouteWarps;
 struct RouteArgs {
     const void *logits;
     long long ld;
+    int dtype;
     const float *bias;       // [E] or NULL
     const uint8_t *mask;     // [T] or NULL
     int *idx;                // [T, K]
@@ -37,46 +38,53 @@ struct RouteArgs {
     float scale;
 };
 
-// Errors of a key v = sigmoid + bias in float32, in units u = 2^-24.  exp(-l) to 2 ulp: at most 1 u of the
-// sigmoid (its derivative by the relative error is s (1 - s) <= 1/4); the sum, the quotient and the
-// sum with the bias: s, s and |v|.  So 3 + |v| in all.  The fast exp is documented to (2 + 1.173 |l|) ulp:
-// (0.5 + 0.263) 2 u since |l| s (1 - s) < 0.2240; the sum s, the fast quotient 2 ulp, 4 s, the bias |v|: below 7 + |v|.
+// Errors of a key v = s + bias, s = sigmoid(l), in float32, in units u = 2^-24.  exp(-l) to 2 ulp makes at
+// most 1 u of s, whose derivative by the relative error is s (1 - s) <= 1/4; the sum s, a quotient to
+// 2 ulp 4 s, the bias |v|: 6 + |v|.  The fast one: the exponent's two roundings 2 |l| u and 2^-22 are
+// (0.25 x 4 + 0.224 x 2) u since |l| s (1 - s) < 0.224; the sum s, the reciprocal 2 s, the bias |v|: 5 + |v|.
 constexpr float kUnit = 1.0f / (1 << 24);
-__device__ __forceinline__ float key_error(float v) { return kUnit * (3.0f + fabsf(v)); }
-__device__ __forceinline__ float fast_error(float v) { return kUnit * (7.0f + fabsf(v)); }
+__device__ __forceinline__ float key_error(float v) { return kUnit * (6.0f + fabsf(v)); }
 
-__device__ __forceinline__ float sigmoid_fast(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
+__device__ __forceinline__ float sigmoid_fast(float x) { return rcp_fast(1.0f + ex2_fast(x * -1.44269504f)); }
 __device__ __forceinline__ float sigmoid(float x) {
-    const float t = expf(-fabsf(x)), r = 1.0f / (1.0f + t);
+    const float t = expf(-fabsf(x)), r = __fdividef(1.0f, 1.0f + t);
     return x >= 0.0f ? r : t * r;      // a NaN stays one
+}
+// calls f with a value of the type that `dtype` names; element e of a row of that type
+template <typename F>
+__device__ __forceinline__ void by_type(int dtype, F &&f) {
+    if (dtype == MOE_DTYPE_F32) f(float{});
+    else if (dtype == MOE_DTYPE_BF16) f(__nv_bfloat16{});
+    else f(__half{});
+}
+__device__ __forceinline__ float load_el(const char *row, int dtype, int e) {
+    if (dtype == MOE_DTYPE_F32) return load_in(reinterpret_cast<const float *>(row) + e);
+    const unsigned short v = load_in(reinterpret_cast<const unsigned short *>(row) + e);
+    return dtype == MOE_DTYPE_BF16 ? __uint_as_float((unsigned)v << 16) : __half2float(__ushort_as_half(v));
 }
 __device__ __forceinline__ double sigmoid64(double x) { return 1.0 / (1.0 + exp(-x)); }
 
-template <typename T>
-__device__ __forceinline__ float logit(const RouteArgs &p, long long t, int e) {
-    return to_float(load_in(static_cast<const T *>(p.logits) + t * p.ld + e));
-}
-
-// What a token's choice leaves for the weights: expert, logit.
+// What a token's choice leaves for the weights: expert, and its sigmoid if there is a bias, else its logit.
 struct Chosen {
     int e;
     float x;
 };
 
 // One token by a whole warp in float64: keys of all experts in shared memory, the groups, K rounds.
-template <typename T>
-__device__ __noinline__ void choose64(const RouteArgs &p, long long t, double *key, Chosen *out) {
-    const int lane = threadIdx.x & 31;
-    const bool biased = !p.softmax && p.bias;
+// (Its arguments one by one: the address of the kernel's parameters would have them copied to local memory.)
+__device__ __noinline__ void choose64(const char *row, int dtype, const float *bias, int E, int K, int groups, int kept, unsigned group_of, double *key,
+                                      Chosen *out) {
+    const int lane = threadIdx.x & 31, per_group = E / groups;
+    const bool biased = bias != nullptr;
     unsigned on = 0xffffffffu;
-    if (p.groups > 1) {
-        for (int e = lane; e < p.E; e += 32) key[e] = sigmoid64((double)logit<T>(p, t, e)) + (biased ? (double)load_in(p.bias + e) : 0.0);
+    if (groups > 1) {
+        for (int e = lane; e < E; e += 32) key[e] = sigmoid64((double)load_el(row, dtype, e)) + (biased ? (double)load_in(bias + e) : 0.0);
         __syncwarp();
         double best = -INFINITY;       // of group `lane`: the sum of its two best, or its one
-        if (lane < p.groups) {
+        if (lane < groups) {
             double b1 = -INFINITY, b2 = -INFINITY;
-            for (int i = 0; i < p.per_group; i++) {
-                const double v = key[lane * p.per_group + i];
+            for (int i = 0; i < per_group; i++) {
+                const double v = key[lane * per_group + i];
                 if (v > b1) {
                     b2 = b1;
                     b1 = v;
@@ -84,27 +92,27 @@ __device__ __noinline__ void choose64(const RouteArgs &p, long long t, double *k
                     b2 = v;
                 }
             }
-            best = p.per_group > 1 ? b1 + b2 : b1;
+            best = per_group > 1 ? b1 + b2 : b1;
             if (isnan(best)) best = -INFINITY;
         }
         int rank = 0;
-        for (int g = 0; g < p.groups; g++) {
+        for (int g = 0; g < groups; g++) {
             const double v = __shfl_sync(0xffffffffu, best, g);
             rank += v > best || (v == best && g < lane) ? 1 : 0;
         }
-        on = __ballot_sync(0xffffffffu, lane < p.groups && rank < p.kept);
+        on = __ballot_sync(0xffffffffu, lane < groups && rank < kept);
     }
-    for (int e = lane; e < p.E; e += 32) {
-        const float x = logit<T>(p, t, e);
-        double v = biased ? (p.groups > 1 ? key[e] : sigmoid64((double)x) + (double)load_in(p.bias + e)) : (double)x;
-        if (isnan(v) || (p.groups > 1 && !(on >> ((unsigned)e * p.group_of >> 20) & 1u))) v = -INFINITY;
+    for (int e = lane; e < E; e += 32) {
+        const float x = load_el(row, dtype, e);
+        double v = biased ? (groups > 1 ? key[e] : sigmoid64((double)x) + (double)load_in(bias + e)) : (double)x;
+        if (isnan(v) || (groups > 1 && !(on >> ((unsigned)e * group_of >> 20) & 1u))) v = -INFINITY;
         key[e] = v;
     }
     __syncwarp();
-    for (int k = 0; k < p.K; k++) {
+    for (int k = 0; k < K; k++) {
         double best = -INFINITY;
         int at = 0x7fffffff;
-        for (int e = lane; e < p.E; e += 32)
+        for (int e = lane; e < E; e += 32)
             if (key[e] > best || (key[e] == best && e < at)) {       // what was taken is NaN
                 best = key[e];
                 at = e;
@@ -120,22 +128,25 @@ __device__ __noinline__ void choose64(const RouteArgs &p, long long t, double *k
         }
         if (lane == 0) {
             key[at] = __longlong_as_double(0x7ff8000000000000ll);
-            out[k] = {at, logit<T>(p, t, at)};
+            const float x = load_el(row, dtype, at);
+            out[k] = {at, biased ? sigmoid(x) : x};
         }
         __syncwarp();
     }
 }
 
-template <typename T_, int J_, int LPT_, int V_>
+// J experts a lane in runs of V, LPT lanes a token; BIAS: keys sigmoid(l) + bias, else the logits
+template <bool BIAS_, int J_, int LPT_, int V_, bool FULL_ = false>
 struct RouteLay {
-    using T = T_;
+    static constexpr bool BIAS = BIAS_;
     static constexpr int J = J_, LPT = LPT_, V = V_, G = 32 / LPT;
-    static constexpr int PER_SM = J >= 32 ? 4 : J >= 16 ? 6 : 8;      // blocks
+    static constexpr bool FULL = FULL_;      // E = J LPT
+    static constexpr int PER_SM = J >= 32 ? 4 : 8;      // blocks
 };
 
 template <class L>
 __global__ void __launch_bounds__(kRouteThreads, L::PER_SM) route_kernel(const RouteArgs p) {
-    using T = typename L::T;
+    constexpr bool BIAS = L::BIAS;
     constexpr int J = L::J, LPT = L::LPT, V = L::V, G = L::G;
     extern __shared__ double route_sm[];                  // [warps][E]: float64 keys; or scores [G][E] float32
     __shared__ Chosen s_sel[kRouteWarps][G][LPT + 1];
@@ -146,51 +157,89 @@ __global__ void __launch_bounds__(kRouteThreads, L::PER_SM) route_kernel(const R
     double *key64 = route_sm + (size_t)warp * p.E;
     float *score = reinterpret_cast<float *>(key64) + (size_t)g * p.E;
     auto expert = [&](int j) { return V * (l + LPT * (j / V)) + j % V; };
-    const bool biased = !p.softmax && p.bias;
+    auto within = [&](int j) { return L::FULL || expert(j) < p.E; };
+    auto row_of = [&](long long t) { return static_cast<const char *>(p.logits) + t * p.ld * (p.dtype == MOE_DTYPE_F32 ? 4 : 2); };
     wait_for_stream();
-    float b[J];
+    float b[BIAS ? J : 1];
+    if constexpr (BIAS) {
 #pragma unroll
-    for (int j = 0; j < J; j++) b[j] = biased && expert(j) < p.E ? load_in(p.bias + expert(j)) : 0.0f;
+        for (int j = 0; j < J; j++) b[j] = within(j) ? load_in(p.bias + expert(j)) : 0.0f;
+    }
     const long long step = (long long)gridDim.x * kRouteWarps * G;
     for (long long t0 = ((long long)blockIdx.x * kRouteWarps + warp) * G; t0 < p.T; t0 += step) {
         const long long t = t0 + g;
         const bool here = t < p.T, on = here && (!p.mask || load_in(p.mask + t));
-        const T *row = static_cast<const T *>(p.logits) + t * p.ld;
-        float x[J], a[J];
+        const char *row = row_of(t);
+        float a[J];
+        // the logits: -infinity beyond E and for tokens that are masked
+        auto logits = [&](float (&x)[J]) {
+            by_type(p.dtype, [&](auto el) {
+                using T = decltype(el);
 #pragma unroll
-        for (int j = 0; j < J; j += V) {
-            if (on && expert(j) < p.E) {
-                Vec<T, V> v;
-                v.load(row + expert(j));
-                v.get(&x[j]);
-            } else {
+                for (int j = 0; j < J; j += V) {
+                    if (on && within(j)) {
+                        Vec<T, V> v;
+                        v.load(reinterpret_cast<const T *>(row) + expert(j));
+                        v.get(&x[j]);
+                    } else {
 #pragma unroll
-                for (int i = 0; i < V; i++) x[j + i] = -INFINITY;
+                        for (int i = 0; i < V; i++) x[j + i] = -INFINITY;
+                    }
+                }
+            });
+        };
+        logits(a);
+        bool slow = false;
+        if (BIAS || p.groups > 1) {
+#pragma unroll
+            for (int j = 0; j < J; j++) {
+                const float s = sigmoid_fast(a[j]);
+                if constexpr (BIAS) a[j] = within(j) ? s + b[j] : -INFINITY;
+                else a[j] = within(j) ? s : -INFINITY;
             }
         }
-        bool slow = false;
-        if (biased || p.groups > 1) {
-#pragma unroll
-            for (int j = 0; j < J; j++) a[j] = expert(j) < p.E ? sigmoid_fast(x[j]) + b[j] : -INFINITY;
-        }
         if (p.groups > 1) {
+            float best = -INFINITY, err = 0.0f, b1 = -INFINITY, b2 = -INFINITY;
+            auto join = [&](float v1, float v2) {      // the two best of b1 >= b2 and v1 >= v2
+                b2 = fmaxf(fmaxf(b2, v2), fminf(b1, v1));
+                b1 = fmaxf(b1, v1);
+            };
+            if (V == 4 && p.per_group % 4 == 0) {
+                // the two best of every quad, then of a group's quads
+                float2 *two = reinterpret_cast<float2 *>(score);
 #pragma unroll
-            for (int j = 0; j < J; j++)
-                if (expert(j) < p.E) score[expert(j)] = a[j];
-            __syncwarp();
-            float best = -INFINITY, err = 0.0f;
-            if (l < p.groups) {
-                float b1 = -INFINITY, b2 = -INFINITY;
-                const float *s = score + l * p.per_group;
-                int i = l % p.per_group;           // lanes begin at different banks
-                for (int n = 0; n < p.per_group; n++) {
-                    const float v = s[i];
-                    b2 = fmaxf(b2, fminf(b1, v));
-                    b1 = fmaxf(b1, v);
-                    if (++i == p.per_group) i = 0;
+                for (int j = 0; j + 3 < J; j += 4) {
+                    if (!within(j)) continue;
+                    const float h1 = fmaxf(a[j], a[j + 1]), l1 = fminf(a[j], a[j + 1]), h2 = fmaxf(a[j + 2], a[j + 3]), l2 = fminf(a[j + 2], a[j + 3]);
+                    two[expert(j) / 4] = make_float2(fmaxf(h1, h2), fmaxf(fminf(h1, h2), fmaxf(l1, l2)));
                 }
+                __syncwarp();
+                if (l < p.groups) {
+                    const int quads = p.per_group / 4;
+                    int i = l % quads;                 // lanes begin at different banks
+#pragma unroll 4
+                    for (int n = 0; n < quads; n++) {
+                        const float2 v = two[l * quads + i];
+                        join(v.x, v.y);
+                        if (++i == quads) i = 0;
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < J; j++)
+                    if (within(j)) score[expert(j)] = a[j];
+                __syncwarp();
+                if (l < p.groups) {
+                    int i = l % p.per_group;
+                    for (int n = 0; n < p.per_group; n++) {
+                        join(score[l * p.per_group + i], -INFINITY);
+                        if (++i == p.per_group) i = 0;
+                    }
+                }
+            }
+            if (l < p.groups) {
                 best = p.per_group > 1 ? b1 + b2 : b1;
-                err = p.per_group > 1 ? fast_error(b1) + fast_error(b2) + kUnit * fabsf(best) : fast_error(b1);
+                err = kUnit * (5.0f + fabsf(b1) + (p.per_group > 1 ? 5.0f + fabsf(b2) + fabsf(best) : 0.0f));
             }
             int rank = 0;
             for (int i = 0; i < p.groups; i++) {
@@ -208,15 +257,13 @@ __global__ void __launch_bounds__(kRouteThreads, L::PER_SM) route_kernel(const R
             if (p.kept < p.groups) slow = !(lo > hi);
             slow |= __ballot_sync(0xffffffffu, isnan(best) || isnan(err)) != 0;
             const unsigned kept = __ballot_sync(0xffffffffu, keep) >> (g * LPT) & lanes;
+            if constexpr (!BIAS) logits(a);
 #pragma unroll
             for (int j = 0; j < J; j++) {
-                const bool in = expert(j) < p.E && (kept >> ((unsigned)expert(j) * p.group_of >> 20) & 1u);
-                a[j] = in ? (biased ? a[j] : x[j]) : -INFINITY;
+                const bool in = within(j) && (kept >> ((unsigned)expert(j) * p.group_of >> 20) & 1u);
+                a[j] = in ? a[j] : -INFINITY;
             }
             __syncwarp();
-        } else if (!biased) {
-#pragma unroll
-            for (int j = 0; j < J; j++) a[j] = x[j];
         }
         // the K-th largest of the lanes' maxima
         float m = -INFINITY;       // a NaN is passed over
@@ -230,7 +277,7 @@ __global__ void __launch_bounds__(kRouteThreads, L::PER_SM) route_kernel(const R
                 m = ((l & k) == 0) == ((l & d) == 0) ? fmaxf(m, o) : fminf(m, o);
             }
         const float kth = __shfl_sync(0xffffffffu, m, p.K - 1, LPT);
-        const float least = biased ? kth - 2.0f * fast_error(kth) : kth;
+        const float least = BIAS ? kth - 2.0f * kUnit * (5.0f + fabsf(kth)) : kth;
         slow |= !(least > -INFINITY);
         unsigned mine = 0;
 #pragma unroll
@@ -257,33 +304,48 @@ __global__ void __launch_bounds__(kRouteThreads, L::PER_SM) route_kernel(const R
         // candidates: their keys, their ranks
         const bool one = on && !slow && !many && l < n;
         const int e = one ? s_cand[warp][g][l] : -1;
-        const float xe = one ? to_float(load_in(row + e)) : 0.0f;
-        const float be = one && biased ? load_in(p.bias + e) : 0.0f;
-        const float key = (biased ? sigmoid(xe) + be : xe) + 0.0f;       // no zero but +0
+        float score_e = one ? load_el(row, p.dtype, e) : 0.0f, key = score_e;
+        if constexpr (BIAS) {
+            score_e = sigmoid(score_e);
+            key = score_e + (one ? load_in(p.bias + e) : 0.0f);
+        }
+        key += 0.0f;       // no zero but +0
         const unsigned bits = __float_as_uint(key);
-        const unsigned hi = one ? bits ^ ((unsigned)((int)bits >> 31) | 0x80000000u) : 0u, lo = one ? ~(unsigned)e : 0u;
-        const unsigned long long code = (unsigned long long)hi << 32 | lo;
-        int most = n;
+        const unsigned order = one ? bits ^ ((unsigned)((int)bits >> 31) | 0x80000000u) : 0u;
+        int most = min(n, LPT);
 #pragma unroll
         for (int d = LPT; d < 32; d *= 2) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
-        most = min(most, LPT);
         int rank = 0;
-        for (int c = 0; c < most; c++) {
-            const unsigned h = __shfl_sync(0xffffffffu, hi, c, LPT), lw = __shfl_sync(0xffffffffu, lo, c, LPT);
-            rank += ((unsigned long long)h << 32 | lw) > code ? 1 : 0;
-        }
+#pragma unroll 4
+        for (int c = 0; c < most; c++) rank += __shfl_sync(0xffffffffu, order, c, LPT) > order ? 1 : 0;
         if (one) {
-            s_sel[warp][g][rank] = {e, xe};
+            s_sel[warp][g][rank] = {e, score_e};
             s_key[warp][g][rank] = key;
         }
         __syncwarp();
-        if (biased) {
+        // equal keys meet in one place: the lower expert first
+        const bool met = one && s_sel[warp][g][rank].e != e;
+        if (__any_sync(0xffffffffu, met)) {
+            for (int c = 0; c < most; c++) {
+                const unsigned o = __shfl_sync(0xffffffffu, order, c, LPT);
+                const int oe = __shfl_sync(0xffffffffu, e, c, LPT);
+                rank += one && o == order && oe < e ? 1 : 0;
+            }
+            if (one) {
+                s_sel[warp][g][rank] = {e, score_e};
+                s_key[warp][g][rank] = key;
+            }
+            __syncwarp();
+        }
+        if constexpr (BIAS) {
             // neighbours that float32 does not tell apart; the same logit and bias are equal
             bool near = false;
             if (one && l < p.K && l + 1 < n) {
-                const Chosen u = s_sel[warp][g][l], v = s_sel[warp][g][l + 1];
                 const float ku = s_key[warp][g][l], kv = s_key[warp][g][l + 1];
-                near = !(ku - kv > 2.0f * key_error(ku)) && !(u.x == v.x && load_in(p.bias + u.e) == load_in(p.bias + v.e));
+                if (!(ku - kv > 2.0f * key_error(ku))) {
+                    const int u = s_sel[warp][g][l].e, v = s_sel[warp][g][l + 1].e;
+                    near = load_el(row, p.dtype, u) != load_el(row, p.dtype, v) || load_in(p.bias + u) != load_in(p.bias + v);
+                }
             }
             again |= __ballot_sync(0xffffffffu, near);
             __syncwarp();
@@ -293,47 +355,49 @@ __global__ void __launch_bounds__(kRouteThreads, L::PER_SM) route_kernel(const R
             const int r = (__ffs(again) - 1) / LPT, count = __shfl_sync(0xffffffffu, n, r * LPT);
             again &= r + 1 < G ? ~0u << ((r + 1) * LPT % 32) : 0u;
             const int ec = lane < count ? s_cand[warp][r][lane] : -1;
-            const float xc = lane < count ? logit<T>(p, t0 + r, ec) : 0.0f;
-            const double k64 = biased && lane < count ? sigmoid64((double)xc) + (double)load_in(p.bias + ec) : (double)xc;
+            const float xc = lane < count ? load_el(row_of(t0 + r), p.dtype, ec) : 0.0f;
+            const double k64 = BIAS && lane < count ? sigmoid64((double)xc) + (double)load_in(p.bias + ec) : (double)xc;
             int r64 = 0;
             for (int c = 0; c < count; c++) {
                 const double v = __shfl_sync(0xffffffffu, k64, c);
                 const int o = __shfl_sync(0xffffffffu, ec, c);
                 r64 += v > k64 || (v == k64 && o < ec) ? 1 : 0;
             }
-            if (lane < count && r64 < p.K) s_sel[warp][r][r64] = {ec, xc};
+            if (lane < count && r64 < p.K) s_sel[warp][r][r64] = {ec, BIAS ? sigmoid(xc) : xc};
             __syncwarp();
         }
         again = __ballot_sync(0xffffffffu, slow && on && l == 0);
         while (again) {
             const int r = (__ffs(again) - 1) / LPT;
             again &= again - 1;
-            choose64<T>(p, t0 + r, key64, s_sel[warp][r]);
+            choose64(row_of(t0 + r), p.dtype, BIAS ? p.bias : nullptr, p.E, p.K, p.groups, p.kept, p.group_of, key64, s_sel[warp][r]);
             __syncwarp();
         }
         // weights: lane k of the token its k-th choice
         const bool out = on && l < p.K;
         const Chosen c = out ? s_sel[warp][g][l] : Chosen{-1, -INFINITY};
-        float pr, w;
-        if (p.softmax) {
+        float pr, w, z;
+        if (!BIAS && p.softmax) {
             const float top = __shfl_sync(0xffffffffu, c.x, 0, LPT), base = top == -INFINITY ? 0.0f : top;
             pr = out ? expf(c.x - base) : 0.0f;
-            float z = 0.0f;
+            z = 0.0f;
             if (p.renorm) {
                 z = pr;
             } else {
 #pragma unroll
-                for (int j = 0; j < J; j++) z += expf(x[j] - base);
+                for (int j = 0; j < J; j++) z += expf(a[j] - base);
             }
-#pragma unroll
-            for (int d = LPT / 2; d; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
-            w = p.scale * (z == 0.0f ? 0.0f : pr / z);
         } else {
-            pr = out ? sigmoid(c.x) : 0.0f;
-            float z = pr;
+            pr = out ? (BIAS ? c.x : sigmoid(c.x)) : 0.0f;
+            z = pr;
+        }
+        const bool soft = !BIAS && p.softmax;
+        if (soft || p.renorm) {
 #pragma unroll
             for (int d = LPT / 2; d; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
-            w = p.scale * (p.renorm ? pr / (z + 1e-20f) : pr);
+            w = p.scale * (soft ? (z == 0.0f ? 0.0f : __fdividef(pr, z)) : __fdividef(pr, z + 1e-20f));
+        } else {
+            w = p.scale * pr;
         }
         if (here && l < p.K) {
             p.idx[t * p.K + l] = c.e;
@@ -378,16 +442,26 @@ __device__ __forceinline__ float sum_over(float v, unsigned same) {
     return s;
 }
 
+// Whether the lane's expert e (any of its token's others) stands twice in the row: each lane leaves its number
+// in the expert's byte of the token's E and looks whether it is still there.
+__device__ __forceinline__ bool repeated(uint8_t *row, int e, bool used, int k) {
+    if (used) row[e] = (uint8_t)k;
+    __syncwarp();
+    return __any_sync(0xffffffffu, used && row[e] != (uint8_t)k);
+}
+
 template <typename T, int KP, int V>
 __global__ void __launch_bounds__(32 * kGradWarps) route_grad_kernel(const RouteGradArgs p) {
     constexpr int G = 32 / KP;
+    extern __shared__ uint8_t route_seen[];      // [warps][G][E]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = lane % KP, g = lane / KP;
+    uint8_t *seen = route_seen + (size_t)(warp * G + g) * p.E;
     wait_for_stream();
     const long long step = (long long)gridDim.x * kGradWarps * G;
     for (long long t0 = ((long long)blockIdx.x * kGradWarps + warp) * G; t0 < p.T; t0 += step) {
         const long long t = t0 + g;
         const bool on = t < p.T && k < p.K;
-        int e = on ? load_in(p.idx + t * p.K + k) : -1;
+        const int e = on ? load_in(p.idx + t * p.K + k) : -1;
         const bool used = (unsigned)e < (unsigned)p.E;
         const float d = used ? load_in(p.dw + t * p.K + k) : 0.0f;
         const float x = used ? to_float(load_in(static_cast<const T *>(p.logits) + t * p.ld + e)) : -INFINITY;
@@ -395,9 +469,15 @@ __global__ void __launch_bounds__(32 * kGradWarps) route_grad_kernel(const Route
         if (!p.add) {      // the rows of the warp's tokens
             Vec<T, V> z;
             z.zero();
-            const int quads = p.E / V;
-            for (int r = 0; r < G && t0 + r < p.T; r++)
-                for (int c = lane; c < quads; c += 32) z.store(out + (t0 + r) * p.ldd + (long long)c * V);
+            const int rows = (int)min((long long)G, p.T - t0), runs = p.E / V;
+            T *first = out + t0 * p.ldd;
+            if (p.ldd == p.E) {
+#pragma unroll 4
+                for (int c = lane; c < rows * runs; c += 32) z.store(first + c * V);
+            } else {
+                for (int r = 0; r < rows; r++)
+                    for (int c = lane; c < runs; c += 32) z.store(first + r * p.ldd + c * V);
+            }
         }
         auto sum = [](float v) {
 #pragma unroll
@@ -410,23 +490,27 @@ __global__ void __launch_bounds__(32 * kGradWarps) route_grad_kernel(const Route
 #pragma unroll
             for (int i = KP / 2; i; i >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
             if (m == -INFINITY) m = 0.0f;
-            const float pr = used ? expf(x - m) : 0.0f, z = sum(pr), q = z == 0.0f ? 0.0f : pr / z;
+            const float pr = used ? expf(x - m) : 0.0f, z = sum(pr), q = z == 0.0f ? 0.0f : __fdividef(pr, z);
             v = q * p.scale * (d - sum(d * q));
         } else {
-            const float tt = expf(-fabsf(x)), r = 1.0f / (1.0f + tt);
+            const float tt = expf(-fabsf(x)), r = __fdividef(1.0f, 1.0f + tt);
             const float pr = used ? (x >= 0.0f ? r : tt * r) : 0.0f, c1 = x >= 0.0f ? tt * r : r;
             if (p.renorm) {
-                const float inv = 1.0f / (sum(pr) + 1e-20f), q = pr * inv;
+                const float q = __fdividef(pr, sum(pr) + 1e-20f);
                 v = q * p.scale * (d - sum(d * q)) * c1;
             } else {
                 v = p.scale * d * pr * c1;
             }
         }
         // an expert twice: the first of its lanes writes the sum
-        const unsigned same = __match_any_sync(0xffffffffu, used ? (g << 16 | e) : (int)(0x80000000u | lane));
-        if (__ballot_sync(0xffffffffu, (same & (same - 1u)) != 0)) v = sum_over(v, same);
+        bool writes = used;
+        if (repeated(seen, e, used, k)) {
+            const unsigned same = __match_any_sync(0xffffffffu, used ? (g << 16 | e) : (int)(0x80000000u | lane));
+            v = sum_over(v, same);
+            writes = used && lane == __ffs(same) - 1;
+        }
         __syncwarp();
-        if (used && lane == __ffs(same) - 1) {
+        if (writes) {
             T *at = out + t * p.ldd + e;
             if (p.add) v += to_float(*at);
             *at = from_float<T>(v);
@@ -434,17 +518,28 @@ __global__ void __launch_bounds__(32 * kGradWarps) route_grad_kernel(const Route
     }
 }
 
-// softmax without renormalisation: every logit has a gradient; a warp a token, its logits in registers
-template <typename T, int J, int V>
+// softmax without renormalisation: every logit has a gradient; LPT lanes a token, its logits in registers
+template <typename T, int J, int LPT, int V>
 __global__ void __launch_bounds__(32 * kGradWarps) route_grad_dense_kernel(const RouteGradArgs p) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    auto expert = [&](int j) { return V * (lane + 32 * (j / V)) + j % V; };
+    constexpr int G = 32 / LPT;
+    extern __shared__ uint8_t route_seen[];      // [warps][G][E]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % LPT, g = lane / LPT;
+    uint8_t *seen = route_seen + (size_t)(warp * G + g) * p.E;
+    auto expert = [&](int j) { return V * (l + LPT * (j / V)) + j % V; };
+    auto sum = [](float v) {
+#pragma unroll
+        for (int i = LPT / 2; i; i >>= 1) v += __shfl_xor_sync(0xffffffffu, v, i);
+        return v;
+    };
     wait_for_stream();
-    const long long step = (long long)gridDim.x * kGradWarps;
-    for (long long t = (long long)blockIdx.x * kGradWarps + warp; t < p.T; t += step) {
-        const int e = lane < p.K ? load_in(p.idx + t * p.K + lane) : -1;
+    const long long step = (long long)gridDim.x * kGradWarps * G;
+    for (long long t0 = ((long long)blockIdx.x * kGradWarps + warp) * G; t0 < p.T; t0 += step) {
+        const long long t = t0 + g;
+        const bool here = t < p.T;
+        const int e = here && l < p.K ? load_in(p.idx + t * p.K + l) : -1;
         const bool used = (unsigned)e < (unsigned)p.E;
-        const bool any = __any_sync(0xffffffffu, used);       // a masked token: zeros, whatever its logits hold
+        const unsigned group = LPT == 32 ? 0xffffffffu : ((1u << LPT % 32) - 1u) << (g * LPT);
+        const bool any = (__ballot_sync(0xffffffffu, used) & group) != 0;       // a masked token: zeros, whatever its logits hold
         const T *row = static_cast<const T *>(p.logits) + t * p.ld;
         T *out = static_cast<T *>(p.out) + t * p.ldd;
         float x[J];
@@ -459,32 +554,32 @@ __global__ void __launch_bounds__(32 * kGradWarps) route_grad_dense_kernel(const
                 for (int i = 0; i < V; i++) x[j + i] = -INFINITY;
             }
         }
-        const float xe = used ? to_float(load_in(row + e)) : -INFINITY, d = used ? load_in(p.dw + t * p.K + lane) : 0.0f;
+        const float xe = used ? to_float(load_in(row + e)) : -INFINITY, d = used ? load_in(p.dw + t * p.K + l) : 0.0f;
         float m = -INFINITY, z = 0.0f;
 #pragma unroll
         for (int j = 0; j < J; j++) m = fmaxf(m, x[j]);
 #pragma unroll
-        for (int i = 16; i; i >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
+        for (int i = LPT / 2; i; i >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
         if (m == -INFINITY) m = 0.0f;
 #pragma unroll
         for (int j = 0; j < J; j++) {
             x[j] = expf(x[j] - m);
             z += x[j];
         }
-#pragma unroll
-        for (int i = 16; i; i >>= 1) z += __shfl_xor_sync(0xffffffffu, z, i);
-        const float inv = z == 0.0f ? 0.0f : 1.0f / z, pe = used ? expf(xe - m) * inv : 0.0f;
-        float dot = d * pe;
-#pragma unroll
-        for (int i = 16; i; i >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, i);
-        const unsigned same = __match_any_sync(0xffffffffu, used ? e : (int)(0x80000000u | lane));
+        z = sum(z);
+        const float inv = z == 0.0f ? 0.0f : __fdividef(1.0f, z), pe = used ? expf(xe - m) * inv : 0.0f;
+        const float dot = sum(d * pe);
         float de = d;
-        if (__ballot_sync(0xffffffffu, (same & (same - 1u)) != 0)) de = sum_over(d, same);
-        const bool writes = used && lane == __ffs(same) - 1;
+        bool writes = used;
+        if (repeated(seen, e, used, l)) {
+            const unsigned same = __match_any_sync(0xffffffffu, used ? (g << 16 | e) : (int)(0x80000000u | lane));
+            de = sum_over(d, same);
+            writes = used && lane == __ffs(same) - 1;
+        }
         float v = pe * p.scale * (de - dot);
         if (writes && p.add) v += to_float(out[e]);
         __syncwarp();
-        if (any || !p.add) {
+        if (here && (any || !p.add)) {
             const float up = -dot * p.scale * inv;
 #pragma unroll
             for (int j = 0; j < J; j += V) {
@@ -516,30 +611,31 @@ bool rows_of(const void *x, long long ld, int el, int E, int V) {
 
 cudaError_t launch_route_forward(const void *logits, int dtype, long long ld, int T, int E, const float *bias, int K, int softmax,
                                  int groups, int kept, int renorm, float scale, const uint8_t *mask, int *idx, float *w, cudaStream_t st) {
-    RouteArgs p = {logits, ld, bias, mask, idx, w, T, E, K, groups, kept, E / groups, 0, softmax, renorm, scale};
+    RouteArgs p = {logits, ld, dtype, bias, mask, idx, w, T, E, K, groups, kept, E / groups, 0, softmax, renorm, scale};
     p.group_of = ((1u << 20) + p.per_group - 1) / p.per_group;
-    return by_dtype(dtype, [&](auto t) {
-        using El = decltype(t);
-        auto go = [&](auto lay) {
-            using L = decltype(lay);
-            const size_t smem = (size_t)kRouteWarps * E * sizeof(double);
-            const cudaError_t e = allow_smem<route_kernel<L>>((size_t)kRouteWarps * 1024 * sizeof(double));
-            if (e != cudaSuccess) return e;
-            const long long need = ((long long)T + kRouteWarps * L::G - 1) / (kRouteWarps * L::G), most = (long long)sm_count() * L::PER_SM;
-            return launch_early(route_kernel<L>, (unsigned)(need < most ? need : most), kRouteThreads, smem, st, 1, p);
-        };
-        const bool quads = rows_of(logits, ld, sizeof(El), E, 4);
+    auto go = [&](auto lay) {
+        using L = decltype(lay);
+        const size_t smem = (size_t)kRouteWarps * E * sizeof(double);
+        const cudaError_t e = allow_smem<route_kernel<L>>((size_t)kRouteWarps * 1024 * sizeof(double));
+        if (e != cudaSuccess) return e;
+        const long long need = ((long long)T + kRouteWarps * L::G - 1) / (kRouteWarps * L::G), most = (long long)sm_count() * L::PER_SM;
+        return launch_early(route_kernel<L>, (unsigned)(need < most ? need : most), kRouteThreads, smem, st, 1, p);
+    };
+    const bool quads = rows_of(logits, ld, dtype == MOE_DTYPE_F32 ? 4 : 2, E, 4);
+    auto by_size = [&](auto bias_) {
+        constexpr bool B = decltype(bias_)::value;
         if (K <= 8 && groups <= 16) {
-            if (E <= 32) return go(RouteLay<El, 2, 16, 1>{});
-            if (E <= 64) return quads && E == 64 ? go(RouteLay<El, 4, 16, 4>{}) : go(RouteLay<El, 4, 16, 1>{});
-            if (E <= 128) return quads ? go(RouteLay<El, 8, 16, 4>{}) : go(RouteLay<El, 8, 16, 1>{});
-            if (E <= 256) return quads ? go(RouteLay<El, 16, 16, 4>{}) : go(RouteLay<El, 16, 16, 1>{});
+            if (E <= 32) return go(RouteLay<B, 2, 16, 1>{});
+            if (E <= 64) return quads && E == 64 ? go(RouteLay<B, 4, 16, 4, true>{}) : go(RouteLay<B, 4, 16, 1>{});
+            if (E <= 128) return quads ? go(RouteLay<B, 8, 16, 4>{}) : go(RouteLay<B, 8, 16, 1>{});
+            if (E <= 256) return !quads ? go(RouteLay<B, 16, 16, 1>{}) : E == 256 ? go(RouteLay<B, 16, 16, 4, true>{}) : go(RouteLay<B, 16, 16, 4>{});
         } else {
-            if (E <= 64) return go(RouteLay<El, 2, 32, 1>{});
-            if (E <= 256) return quads && E >= 128 ? go(RouteLay<El, 8, 32, 4>{}) : go(RouteLay<El, 8, 32, 1>{});
+            if (E <= 64) return go(RouteLay<B, 2, 32, 1>{});
+            if (E <= 256) return quads && E >= 128 ? go(RouteLay<B, 8, 32, 4>{}) : go(RouteLay<B, 8, 32, 1>{});
         }
-        return quads ? go(RouteLay<El, 32, 32, 4>{}) : go(RouteLay<El, 32, 32, 1>{});
-    });
+        return quads ? go(RouteLay<B, 32, 32, 4>{}) : go(RouteLay<B, 32, 32, 1>{});
+    };
+    return bias && !softmax ? by_size(std::true_type{}) : by_size(std::false_type{});
 }
 
 cudaError_t launch_route_backward(const void *logits, int dtype, long long ld, int T, int E, const int *idx, int K, int softmax, int renorm,
@@ -548,24 +644,20 @@ cudaError_t launch_route_backward(const void *logits, int dtype, long long ld, i
     return by_dtype(dtype, [&](auto t) {
         using El = decltype(t);
         const int el = (int)sizeof(El);
-        const long long most = (long long)sm_count() * 8;
-        auto blocks = [&](long long per) {
-            const long long need = (T + per - 1) / per;
-            return (unsigned)(need < most ? need : most);
+        auto run = [&](auto kernel, int tokens) {      // of a warp
+            const long long per = kGradWarps * tokens, need = (T + per - 1) / per, most = (long long)sm_count() * 8;
+            return launch_early(kernel, (unsigned)(need < most ? need : most), 32 * kGradWarps, (size_t)kGradWarps * tokens * E, st, 1, p);
         };
         if (softmax && !renorm) {
-            auto go = [&](auto kernel) { return launch_early(kernel, blocks(kGradWarps), 32 * kGradWarps, 0, st, 1, p); };
             const bool quads = rows_of(logits, ld, el, E, 4) && rows_of(out, ldd, el, E, 4);
-            if (E <= 64) return go(route_grad_dense_kernel<El, 2, 1>);
-            if (E <= 256) return quads ? go(route_grad_dense_kernel<El, 8, 4>) : go(route_grad_dense_kernel<El, 8, 1>);
-            return quads ? go(route_grad_dense_kernel<El, 32, 4>) : go(route_grad_dense_kernel<El, 32, 1>);
+            if (K <= 16 && E <= 64) return quads ? run(route_grad_dense_kernel<El, 4, 16, 4>, 2) : run(route_grad_dense_kernel<El, 4, 16, 1>, 2);
+            if (K <= 16 && E <= 256) return quads ? run(route_grad_dense_kernel<El, 16, 16, 4>, 2) : run(route_grad_dense_kernel<El, 16, 16, 1>, 2);
+            return quads ? run(route_grad_dense_kernel<El, 32, 32, 4>, 1) : run(route_grad_dense_kernel<El, 32, 32, 1>, 1);
         }
         constexpr int V = 16 / (int)sizeof(El);
-        auto go = [&](auto wide, auto narrow, int kp) {
-            return launch_early(rows_of(out, ldd, el, E, V) ? wide : narrow, blocks(kGradWarps * (32 / kp)), 32 * kGradWarps, 0, st, 1, p);
-        };
-        if (K <= 8) return go(route_grad_kernel<El, 8, V>, route_grad_kernel<El, 8, 1>, 8);
-        return go(route_grad_kernel<El, 32, V>, route_grad_kernel<El, 32, 1>, 32);
+        const bool wide = rows_of(out, ldd, el, E, V);
+        if (K <= 8) return wide ? run(route_grad_kernel<El, 8, V>, 4) : run(route_grad_kernel<El, 8, 1>, 4);
+        return wide ? run(route_grad_kernel<El, 32, V>, 1) : run(route_grad_kernel<El, 32, 1>, 1);
     });
 }
 
