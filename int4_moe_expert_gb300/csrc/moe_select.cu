@@ -17,8 +17,8 @@ namespace {
 // one sort of LPT maxima and one ranking of at most LPT candidates instead of K rounds over all
 // experts.  Maxima and candidates go by a fast sigmoid less a margin for its error; the candidates'
 // keys are computed again, one a lane.  The order is that of the float64 keys: where two neighbours of the
-// ranking are nearer than float32 tells, or there are more candidates than lanes, the whole warp ranks them in
-// float64; where two groups' scores are that near, or more than 32 candidates, it does the row over.
+// ranking are nearer than float32 tells, the whole warp ranks them in float64, and so the groups whose scores
+// are that near; with more candidates than lanes it ranks them, with more than 32 it does the row over.
 // ---------------------------------------------------------------------------
 
 constexpr int kRouteWarps = 4;
@@ -38,18 +38,20 @@ struct RouteArgs {
     float scale;
 };
 
-// Errors of a key v = s + bias, s = sigmoid(l), in float32, in units u = 2^-24.  exp(-l) to 2 ulp makes at
-// most 1 u of s, whose derivative by the relative error is s (1 - s) <= 1/4; the sum s, a quotient to
-// 2 ulp 4 s, the bias |v|: 6 + |v|.  The fast one: the exponent's two roundings 2 |l| u and 2^-22 are
-// (0.25 x 4 + 0.224 x 2) u since |l| s (1 - s) < 0.224; the sum s, the reciprocal 2 s, the bias |v|: 5 + |v|.
+// Errors of a key v = s + bias, s = sigmoid(l), in float32, in units u = 2^-24: the exponent's two roundings 2 |l| u
+// and the exponential's 2^-22 make (0.224 x 2 + 0.25 x 4) u, since |l| s (1 - s) < 0.224 and s (1 - s) <= 1/4 is the
+// derivative by the exponential's relative error; the sum s, the reciprocal 2 s, the bias |v|: 5 + |v|.
 constexpr float kUnit = 1.0f / (1 << 24);
-__device__ __forceinline__ float key_error(float v) { return kUnit * (6.0f + fabsf(v)); }
-
+__device__ __forceinline__ float key_error(float v) { return kUnit * (5.0f + fabsf(v)); }
 __device__ __forceinline__ float sigmoid_fast(float x) { return rcp_fast(1.0f + ex2_fast(x * -1.44269504f)); }
+// the same to 2^-20 of its value (of those that are no subnormals): the exponent with its rounding's remainder
 __device__ __forceinline__ float sigmoid(float x) {
-    const float t = expf(-fabsf(x)), r = __fdividef(1.0f, 1.0f + t);
-    return x >= 0.0f ? r : t * r;      // a NaN stays one
+    const float hi = x * -1.44269504f, lo = fmaf(x, -1.44269504f, -hi) + x * -1.92596299e-8f;      // log2(e) in two parts
+    const float t = ex2_fast(hi);
+    return rcp_fast(1.0f + (fabsf(x) < 88.0f ? fmaf(t, lo * 0.693147181f, t) : t));      // beyond, t may be infinite, and the result is 1 or 0
 }
+__device__ __forceinline__ double sigmoid64(double x) { return 1.0 / (1.0 + exp(-x)); }
+
 // calls f with a value of the type that `dtype` names; element e of a row of that type
 template <typename F>
 __device__ __forceinline__ void by_type(int dtype, F &&f) {
@@ -62,12 +64,11 @@ __device__ __forceinline__ float load_el(const char *row, int dtype, int e) {
     const unsigned short v = load_in(reinterpret_cast<const unsigned short *>(row) + e);
     return dtype == MOE_DTYPE_BF16 ? __uint_as_float((unsigned)v << 16) : __half2float(__ushort_as_half(v));
 }
-__device__ __forceinline__ double sigmoid64(double x) { return 1.0 / (1.0 + exp(-x)); }
 
-// What a token's choice leaves for the weights: expert, and its sigmoid if there is a bias, else its logit.
-struct Chosen {
+// A place of a token's ranking.
+struct __align__(16) Chosen {
     int e;
-    float x;
+    float x, key, bias;      // logit, key, bias
 };
 
 // One token by a whole warp in float64: keys of all experts in shared memory, the groups, K rounds.
@@ -128,8 +129,7 @@ __device__ __noinline__ void choose64(const char *row, int dtype, const float *b
         }
         if (lane == 0) {
             key[at] = __longlong_as_double(0x7ff8000000000000ll);
-            const float x = load_el(row, dtype, at);
-            out[k] = {at, biased ? sigmoid(x) : x};
+            out[k] = {at, load_el(row, dtype, at), 0.0f, 0.0f};
         }
         __syncwarp();
     }
@@ -148,54 +148,61 @@ template <class L>
 __global__ void __launch_bounds__(kRouteThreads, L::PER_SM) route_kernel(const RouteArgs p) {
     constexpr bool BIAS = L::BIAS;
     constexpr int J = L::J, LPT = L::LPT, V = L::V, G = L::G;
-    extern __shared__ double route_sm[];                  // [warps][E]: float64 keys; or scores [G][E] float32
+    extern __shared__ __align__(16) double route_sm[];                  // [warps][E]: float64 keys; or scores [G][E] float32; then the bias
     __shared__ Chosen s_sel[kRouteWarps][G][LPT + 1];
-    __shared__ float s_key[kRouteWarps][G][LPT + 1];
     __shared__ short s_cand[kRouteWarps][G][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % LPT, g = lane / LPT;
     const unsigned lanes = LPT == 32 ? 0xffffffffu : (1u << LPT) - 1u;
     double *key64 = route_sm + (size_t)warp * p.E;
     float *score = reinterpret_cast<float *>(key64) + (size_t)g * p.E;
+    float *bias = reinterpret_cast<float *>(route_sm + (size_t)kRouteWarps * p.E);
     auto expert = [&](int j) { return V * (l + LPT * (j / V)) + j % V; };
     auto within = [&](int j) { return L::FULL || expert(j) < p.E; };
     auto row_of = [&](long long t) { return static_cast<const char *>(p.logits) + t * p.ld * (p.dtype == MOE_DTYPE_F32 ? 4 : 2); };
     wait_for_stream();
-    float b[BIAS ? J : 1];
     if constexpr (BIAS) {
-#pragma unroll
-        for (int j = 0; j < J; j++) b[j] = within(j) ? load_in(p.bias + expert(j)) : 0.0f;
+        for (int e = threadIdx.x; e < p.E; e += kRouteThreads) bias[e] = load_in(p.bias + e);
+        __syncthreads();
     }
     const long long step = (long long)gridDim.x * kRouteWarps * G;
-    for (long long t0 = ((long long)blockIdx.x * kRouteWarps + warp) * G; t0 < p.T; t0 += step) {
+    long long t0 = ((long long)blockIdx.x * kRouteWarps + warp) * G;
+    for (; t0 < p.T; t0 += step) {
         const long long t = t0 + g;
         const bool here = t < p.T, on = here && (!p.mask || load_in(p.mask + t));
         const char *row = row_of(t);
         float a[J];
-        // the logits: -infinity beyond E and for tokens that are masked
-        auto logits = [&](float (&x)[J]) {
+        auto logits = [&] {       // -infinity beyond E
             by_type(p.dtype, [&](auto el) {
                 using T = decltype(el);
 #pragma unroll
                 for (int j = 0; j < J; j += V) {
-                    if (on && within(j)) {
-                        Vec<T, V> v;
-                        v.load(reinterpret_cast<const T *>(row) + expert(j));
-                        v.get(&x[j]);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < V; i++) x[j + i] = -INFINITY;
-                    }
+                    Vec<T, V> v;
+                    v.zero();
+                    if (on && within(j)) v.load(reinterpret_cast<const T *>(row) + expert(j));
+                    v.get(&a[j]);
                 }
             });
-        };
-        logits(a);
-        bool slow = false;
-        if (BIAS || p.groups > 1) {
+            if constexpr (!L::FULL) {
 #pragma unroll
-            for (int j = 0; j < J; j++) {
-                const float s = sigmoid_fast(a[j]);
-                if constexpr (BIAS) a[j] = within(j) ? s + b[j] : -INFINITY;
-                else a[j] = within(j) ? s : -INFINITY;
+                for (int j = 0; j < J; j++) a[j] = within(j) ? a[j] : -INFINITY;
+            }
+        };
+        logits();
+        const bool scores = BIAS || p.groups > 1;
+        bool slow = false;
+        if (scores) {
+#pragma unroll
+            for (int j = 0; j < J; j += V) {
+                float b[V] = {};
+                if constexpr (BIAS) {
+                    if (within(j)) {
+                        Vec<float, V> v;
+                        v.load(bias + expert(j));
+                        v.get(b);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < V; i++) a[j + i] = within(j) ? sigmoid_fast(a[j + i]) + b[i] : -INFINITY;
             }
         }
         if (p.groups > 1) {
@@ -246,18 +253,50 @@ __global__ void __launch_bounds__(kRouteThreads, L::PER_SM) route_kernel(const R
                 const float v = __shfl_sync(0xffffffffu, best, i, LPT);
                 rank += v > best || (v == best && i < l) ? 1 : 0;
             }
-            const bool keep = l < p.groups && rank < p.kept;
+            bool keep = l < p.groups && rank < p.kept;
             float lo = keep ? best - err : INFINITY, hi = l < p.groups && !keep ? best + err : -INFINITY;
 #pragma unroll
             for (int d = LPT / 2; d; d >>= 1) {
                 lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, d));
                 hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, d));
             }
-            // near ones, and a group's NaN or infinite score: float64 decides
-            if (p.kept < p.groups) slow = !(lo > hi);
-            slow |= __ballot_sync(0xffffffffu, isnan(best) || isnan(err)) != 0;
+            // a group's NaN or infinite score: the whole row in float64
+            const bool odd = l < p.groups && !(fabsf(best) + err < INFINITY);
+            slow = (__ballot_sync(0xffffffffu, odd) >> (g * LPT) & lanes) != 0;
+            // between the last kept and the first other: those groups' sums in float64, by all lanes
+            const bool doubt = p.kept < p.groups && !slow && on && lo <= hi && l < p.groups && best + err >= lo && best - err <= hi;
+            unsigned doubts = __ballot_sync(0xffffffffu, doubt);
+            if (doubts) {
+                double sum = 0.0;
+                for (unsigned left = doubts; left; left &= left - 1) {
+                    const int who = __ffs(left) - 1, gr = who % LPT;
+                    const char *other = row_of(t0 + who / LPT);
+                    double b1 = -INFINITY, b2 = -INFINITY;
+                    for (int i = lane; i < p.per_group; i += 32) {
+                        const int e = gr * p.per_group + i;
+                        const double v = sigmoid64((double)load_el(other, p.dtype, e)) + (BIAS ? (double)bias[e] : 0.0);
+                        b2 = fmax(b2, fmin(b1, v));
+                        b1 = fmax(b1, v);
+                    }
+#pragma unroll
+                    for (int d = 16; d; d >>= 1) {
+                        const double v1 = __shfl_xor_sync(0xffffffffu, b1, d), v2 = __shfl_xor_sync(0xffffffffu, b2, d);
+                        b2 = fmax(fmax(b2, v2), fmin(b1, v1));
+                        b1 = fmax(b1, v1);
+                    }
+                    if (lane == who) sum = p.per_group > 1 ? b1 + b2 : b1;
+                }
+                const unsigned mine = doubts >> (g * LPT) & lanes;
+                const int places = __popc((__ballot_sync(0xffffffffu, keep) >> (g * LPT) & lanes) & mine);
+                int ahead = 0;
+                for (int i = 0; i < p.groups; i++) {
+                    const double v = __shfl_sync(0xffffffffu, sum, i, LPT);
+                    if (mine >> i & 1u) ahead += v > sum || (v == sum && i < l) ? 1 : 0;
+                }
+                if (doubt) keep = ahead < places;
+            }
             const unsigned kept = __ballot_sync(0xffffffffu, keep) >> (g * LPT) & lanes;
-            if constexpr (!BIAS) logits(a);
+            if constexpr (!BIAS) logits();
 #pragma unroll
             for (int j = 0; j < J; j++) {
                 const bool in = within(j) && (kept >> ((unsigned)expert(j) * p.group_of >> 20) & 1u);
@@ -279,10 +318,11 @@ __global__ void __launch_bounds__(kRouteThreads, L::PER_SM) route_kernel(const R
         const float kth = __shfl_sync(0xffffffffu, m, p.K - 1, LPT);
         const float least = BIAS ? kth - 2.0f * kUnit * (5.0f + fabsf(kth)) : kth;
         slow |= !(least > -INFINITY);
+        // bit J - 1 - j: a_j is not below (a NaN neither: it is found among the candidates)
         unsigned mine = 0;
 #pragma unroll
-        for (int j = 0; j < J; j++) mine |= a[j] >= least ? 1u << j : 0u;
-        if (slow) mine = 0;
+        for (int j = 0; j < J; j++) mine = __funnelshift_l(__float_as_uint(a[j] - least), mine, 1);
+        mine = slow ? 0u : ~mine & (J == 32 ? 0xffffffffu : (1u << J % 32) - 1u);
         const int own = __popc(mine);
         int at = own;      // the candidates of this lane and those before it
 #pragma unroll
@@ -292,11 +332,16 @@ __global__ void __launch_bounds__(kRouteThreads, L::PER_SM) route_kernel(const R
         }
         const int n = __shfl_sync(0xffffffffu, at, LPT - 1, LPT);
         at -= own;
-        while (mine != 0 && at < 32) {
-            const int j = __ffs(mine) - 1;
-            mine &= mine - 1;
-            s_cand[warp][g][at++] = (short)(V * (l + LPT * (j / V)) + j % V);
-        }
+        auto next = [&] {
+            const int bit = 31 - __clz(mine), j = J - 1 - bit;
+            if (mine != 0 && at < 32) s_cand[warp][g][at] = (short)(V * l + j + (LPT - 1) * V * (j / V));
+            at++;
+            mine &= ~(1u << (bit & 31));
+        };
+#pragma unroll
+        for (int i = 0; i < (J < 3 ? J : 3); i++) next();
+        if (J > 3)
+            while (__any_sync(0xffffffffu, mine != 0 && at < 32)) next();
         slow |= n > 32;
         const bool many = on && !slow && n > LPT;
         unsigned again = LPT < 32 ? __ballot_sync(0xffffffffu, many) : 0u;
@@ -304,24 +349,25 @@ __global__ void __launch_bounds__(kRouteThreads, L::PER_SM) route_kernel(const R
         // candidates: their keys, their ranks
         const bool one = on && !slow && !many && l < n;
         const int e = one ? s_cand[warp][g][l] : -1;
-        float score_e = one ? load_el(row, p.dtype, e) : 0.0f, key = score_e;
+        const float xe = one ? load_el(row, p.dtype, e) : 0.0f;
+        float be = 0.0f, key = xe;
         if constexpr (BIAS) {
-            score_e = sigmoid(score_e);
-            key = score_e + (one ? load_in(p.bias + e) : 0.0f);
+            be = one ? bias[e] : 0.0f;
+            key = sigmoid_fast(xe) + be;
         }
         key += 0.0f;       // no zero but +0
+        slow |= (__ballot_sync(0xffffffffu, one && isnan(key)) >> (g * LPT) & lanes) != 0;
         const unsigned bits = __float_as_uint(key);
         const unsigned order = one ? bits ^ ((unsigned)((int)bits >> 31) | 0x80000000u) : 0u;
         int most = min(n, LPT);
 #pragma unroll
         for (int d = LPT; d < 32; d *= 2) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
         int rank = 0;
-#pragma unroll 4
-        for (int c = 0; c < most; c++) rank += __shfl_sync(0xffffffffu, order, c, LPT) > order ? 1 : 0;
-        if (one) {
-            s_sel[warp][g][rank] = {e, score_e};
-            s_key[warp][g][rank] = key;
-        }
+        constexpr int kUsual = 12;       // places without a candidate have the order 0
+#pragma unroll
+        for (int c = 0; c < kUsual; c++) rank += __shfl_sync(0xffffffffu, order, c, LPT) > order ? 1 : 0;
+        for (int c = kUsual; c < most; c++) rank += __shfl_sync(0xffffffffu, order, c, LPT) > order ? 1 : 0;
+        if (one) s_sel[warp][g][rank] = {e, xe, key, be};
         __syncwarp();
         // equal keys meet in one place: the lower expert first
         const bool met = one && s_sel[warp][g][rank].e != e;
@@ -331,51 +377,61 @@ __global__ void __launch_bounds__(kRouteThreads, L::PER_SM) route_kernel(const R
                 const int oe = __shfl_sync(0xffffffffu, e, c, LPT);
                 rank += one && o == order && oe < e ? 1 : 0;
             }
-            if (one) {
-                s_sel[warp][g][rank] = {e, score_e};
-                s_key[warp][g][rank] = key;
-            }
+            if (one) s_sel[warp][g][rank] = {e, xe, key, be};
             __syncwarp();
         }
         if constexpr (BIAS) {
             // neighbours that float32 does not tell apart; the same logit and bias are equal
             bool near = false;
             if (one && l < p.K && l + 1 < n) {
-                const float ku = s_key[warp][g][l], kv = s_key[warp][g][l + 1];
-                if (!(ku - kv > 2.0f * key_error(ku))) {
-                    const int u = s_sel[warp][g][l].e, v = s_sel[warp][g][l + 1].e;
-                    near = load_el(row, p.dtype, u) != load_el(row, p.dtype, v) || load_in(p.bias + u) != load_in(p.bias + v);
-                }
+                const Chosen u = s_sel[warp][g][l], v = s_sel[warp][g][l + 1];
+                near = !(u.key - v.key > 2.0f * key_error(u.key)) && !(u.x == v.x && u.bias == v.bias);
             }
             again |= __ballot_sync(0xffffffffu, near);
             __syncwarp();
         }
-        // those tokens' candidates by all lanes, in float64
+        // those tokens' candidates by all lanes: in float32 if there were too many of them, in float64 if near
         while (again) {
             const int r = (__ffs(again) - 1) / LPT, count = __shfl_sync(0xffffffffu, n, r * LPT);
             again &= r + 1 < G ? ~0u << ((r + 1) * LPT % 32) : 0u;
-            const int ec = lane < count ? s_cand[warp][r][lane] : -1;
-            const float xc = lane < count ? load_el(row_of(t0 + r), p.dtype, ec) : 0.0f;
-            const double k64 = BIAS && lane < count ? sigmoid64((double)xc) + (double)load_in(p.bias + ec) : (double)xc;
-            int r64 = 0;
-            for (int c = 0; c < count; c++) {
-                const double v = __shfl_sync(0xffffffffu, k64, c);
-                const int o = __shfl_sync(0xffffffffu, ec, c);
-                r64 += v > k64 || (v == k64 && o < ec) ? 1 : 0;
+            const bool in = lane < count;
+            const int ec = in ? s_cand[warp][r][lane] : -1;
+            const float xc = in ? load_el(row_of(t0 + r), p.dtype, ec) : -INFINITY, bc = BIAS && in ? bias[ec] : 0.0f;
+            const float kc = BIAS ? sigmoid_fast(xc) + bc : xc;
+            if (__any_sync(0xffffffffu, in && isnan(kc))) {
+                slow |= g == r;
+                continue;
             }
-            if (lane < count && r64 < p.K) s_sel[warp][r][r64] = {ec, BIAS ? sigmoid(xc) : xc};
+            int place = 0;
+            bool near = false;      // to one of the first K: more than the ranking needs, but rare
+            for (int c = 0; c < count; c++) {
+                const float v = __shfl_sync(0xffffffffu, kc, c), x = __shfl_sync(0xffffffffu, xc, c), bb = __shfl_sync(0xffffffffu, bc, c);
+                const int o = __shfl_sync(0xffffffffu, ec, c);
+                place += v > kc || (v == kc && o < ec) ? 1 : 0;
+                if (BIAS) near |= !(fabsf(v - kc) > key_error(v) + key_error(kc)) && !(x == xc && bb == bc);
+            }
+            if (BIAS && __any_sync(0xffffffffu, in && near && place <= p.K)) {
+                const double k64 = in ? sigmoid64((double)xc) + (double)bc : 0.0;
+                place = 0;
+                for (int c = 0; c < count; c++) {
+                    const double v = __shfl_sync(0xffffffffu, k64, c);
+                    const int o = __shfl_sync(0xffffffffu, ec, c);
+                    place += v > k64 || (v == k64 && o < ec) ? 1 : 0;
+                }
+            }
+            if (in && place < p.K) s_sel[warp][r][place] = {ec, xc, kc, bc};
             __syncwarp();
         }
         again = __ballot_sync(0xffffffffu, slow && on && l == 0);
         while (again) {
             const int r = (__ffs(again) - 1) / LPT;
             again &= again - 1;
-            choose64(row_of(t0 + r), p.dtype, BIAS ? p.bias : nullptr, p.E, p.K, p.groups, p.kept, p.group_of, key64, s_sel[warp][r]);
+            choose64(row_of(t0 + r), p.dtype, BIAS ? bias : nullptr, p.E, p.K, p.groups, p.kept, p.group_of, key64, s_sel[warp][r]);
             __syncwarp();
         }
         // weights: lane k of the token its k-th choice
         const bool out = on && l < p.K;
-        const Chosen c = out ? s_sel[warp][g][l] : Chosen{-1, -INFINITY};
+        const Chosen c = out ? s_sel[warp][g][l] : Chosen{-1, -INFINITY, 0.0f, 0.0f};
         float pr, w, z;
         if (!BIAS && p.softmax) {
             const float top = __shfl_sync(0xffffffffu, c.x, 0, LPT), base = top == -INFINITY ? 0.0f : top;
@@ -388,7 +444,7 @@ __global__ void __launch_bounds__(kRouteThreads, L::PER_SM) route_kernel(const R
                 for (int j = 0; j < J; j++) z += expf(a[j] - base);
             }
         } else {
-            pr = out ? (BIAS ? c.x : sigmoid(c.x)) : 0.0f;
+            pr = out ? sigmoid(c.x) : 0.0f;
             z = pr;
         }
         const bool soft = !BIAS && p.softmax;
@@ -615,23 +671,25 @@ cudaError_t launch_route_forward(const void *logits, int dtype, long long ld, in
     p.group_of = ((1u << 20) + p.per_group - 1) / p.per_group;
     auto go = [&](auto lay) {
         using L = decltype(lay);
-        const size_t smem = (size_t)kRouteWarps * E * sizeof(double);
-        const cudaError_t e = allow_smem<route_kernel<L>>((size_t)kRouteWarps * 1024 * sizeof(double));
+        auto smem = [](int e) { return (size_t)kRouteWarps * e * sizeof(double) + (size_t)e * sizeof(float); };
+        const cudaError_t e = allow_smem<route_kernel<L>>(smem(1024));
         if (e != cudaSuccess) return e;
         const long long need = ((long long)T + kRouteWarps * L::G - 1) / (kRouteWarps * L::G), most = (long long)sm_count() * L::PER_SM;
-        return launch_early(route_kernel<L>, (unsigned)(need < most ? need : most), kRouteThreads, smem, st, 1, p);
+        return launch_early(route_kernel<L>, (unsigned)(need < most ? need : most), kRouteThreads, smem(E), st, 1, p);
     };
     const bool quads = rows_of(logits, ld, dtype == MOE_DTYPE_F32 ? 4 : 2, E, 4);
     auto by_size = [&](auto bias_) {
         constexpr bool B = decltype(bias_)::value;
-        if (K <= 8 && groups <= 16) {
+        // Two tokens a warp while at most half of their lanes' maxima are wanted.  Not with groups: the kept ones
+        // may share few lanes, which leaves many candidates (16381 x 256 in 8 groups of which 4: 39 and 19 us).
+        if (K <= 8 && groups == 1) {
             if (E <= 32) return go(RouteLay<B, 2, 16, 1>{});
             if (E <= 64) return quads && E == 64 ? go(RouteLay<B, 4, 16, 4, true>{}) : go(RouteLay<B, 4, 16, 1>{});
             if (E <= 128) return quads ? go(RouteLay<B, 8, 16, 4>{}) : go(RouteLay<B, 8, 16, 1>{});
             if (E <= 256) return !quads ? go(RouteLay<B, 16, 16, 1>{}) : E == 256 ? go(RouteLay<B, 16, 16, 4, true>{}) : go(RouteLay<B, 16, 16, 4>{});
         } else {
             if (E <= 64) return go(RouteLay<B, 2, 32, 1>{});
-            if (E <= 256) return quads && E >= 128 ? go(RouteLay<B, 8, 32, 4>{}) : go(RouteLay<B, 8, 32, 1>{});
+            if (E <= 256) return !quads || E < 128 ? go(RouteLay<B, 8, 32, 1>{}) : E == 256 ? go(RouteLay<B, 8, 32, 4, true>{}) : go(RouteLay<B, 8, 32, 4>{});
         }
         return quads ? go(RouteLay<B, 32, 32, 4>{}) : go(RouteLay<B, 32, 32, 1>{});
     };
