@@ -32,19 +32,35 @@ struct NormArgs {
 
 constexpr int kWarpRows = 4;       // rows of a block whose warps take a row each
 
-// w's elements c .. c + V - 1 (float32, or the type T of x)
+// w's elements c .. c + V - 1 (float32, or the type T of x), as loaded
 template <typename T, int V>
-__device__ __forceinline__ void load_w(const void *w, int w_dtype, int c, float *v) {
-    if (w_dtype == MOE_DTYPE_F32) {
-        Vec<float, V> u;
-        u.load(static_cast<const float *>(w) + c);
-        u.get(v);
-    } else {
-        Vec<T, V> u;
-        u.load(static_cast<const T *>(w) + c);
-        u.get(v);
+struct Weights {
+    uint32_t w[V];
+    __device__ __forceinline__ void load(const void *p, int w_dtype, int c) {
+        if (w_dtype == MOE_DTYPE_F32) {
+            Vec<float, V> u;
+            u.load(static_cast<const float *>(p) + c);
+#pragma unroll
+            for (int i = 0; i < V; i++) w[i] = u.w[i];
+        } else {
+            Vec<T, V> u;
+            u.load(static_cast<const T *>(p) + c);
+#pragma unroll
+            for (int i = 0; i < Vec<T, V>::W; i++) w[i] = u.w[i];
+        }
     }
-}
+    __device__ __forceinline__ void get(int w_dtype, float *v) const {
+        if (w_dtype == MOE_DTYPE_F32) {
+#pragma unroll
+            for (int i = 0; i < V; i++) v[i] = __uint_as_float(w[i]);
+        } else {
+            Vec<T, V> u;
+#pragma unroll
+            for (int i = 0; i < Vec<T, V>::W; i++) u.w[i] = w[i];
+            u.get(v);
+        }
+    }
+};
 
 // 448 = 1.75 x 2^8: a magnitude (its bits) within 64 units of the step of its block's scale.  float32's
 // error: 32 and 10 additions, half of it behind the root, and three more roundings, 24 units at most.
@@ -52,7 +68,7 @@ __device__ __forceinline__ bool at_border(unsigned m) { return (unsigned)(abs((i
 
 // S: the stream's type (T or float); N elements a thread
 template <typename T, typename S, int V, int N, bool WARP>
-__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : N <= 8 ? 1024 : 512) norm_kernel(const NormArgs p) {
+__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) norm_kernel(const NormArgs p) {
     constexpr int C = N / V;
     __shared__ float s_sum[2][32];
     __shared__ double s_sum64[32];
@@ -62,6 +78,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : N <= 8 ? 1024 : 512) n
     int turn = 0;
     for (long long t = (long long)blockIdx.x * per + (WARP ? threadIdx.x >> 5 : 0); t < p.T; t += (long long)gridDim.x * per) {
         float v[N];
+        Weights<T, V> wt[C];       // on their way during the sum
         {
             Vec<T, V> a[C];
             Vec<S, V> b[C];
@@ -73,6 +90,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : N <= 8 ? 1024 : 512) n
                 if (c < p.H) {
                     a[i].load(static_cast<const T *>(p.x) + t * p.ldx + c);
                     if (p.res) b[i].load(static_cast<const S *>(p.res) + t * p.ldr + c);
+                    if (p.w) wt[i].load(p.w, p.w_dtype, c);
                 }
             }
 #pragma unroll
@@ -102,7 +120,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : N <= 8 ? 1024 : 512) n
         for (int i = 0; i < C; i++) {
             const int c = V * (tid + nt * i);
             float w[V] = {};
-            if (p.w && c < p.H) load_w<T, V>(p.w, p.w_dtype, c, w);
+            if (p.w && c < p.H) wt[i].get(p.w_dtype, w);
 #pragma unroll
             for (int k = 0; k < V; k++) v[V * i + k] = p.w ? v[V * i + k] * r * w[k] : v[V * i + k] * r;
             if (p.y && c < p.H) {
@@ -161,7 +179,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : N <= 8 ? 1024 : 512) n
                         double u[V];
                         float w[V];
                         again(c, u);
-                        if (p.w) load_w<T, V>(p.w, p.w_dtype, c, w);
+                        if (p.w) wt[i].get(p.w_dtype, w);
 #pragma unroll
                         for (int k = 0; k < V; k++) m = fmax(m, fabs(p.w ? u[k] * (double)w[k] : u[k]));
                     }
@@ -203,8 +221,8 @@ struct NormGradArgs {
     int T, H, w_dtype;
 };
 
-template <typename T, typename S, int V, int N, bool WARP>
-__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 512) norm_grad_kernel(const NormGradArgs p) {
+template <typename T, typename S, int V, int N, int THREADS, int PER_SM, bool WARP>
+__global__ void __launch_bounds__(THREADS, PER_SM) norm_grad_kernel(const NormGradArgs p) {
     constexpr int C = N / V;
     extern __shared__ float norm_sm[];      // WARP: [warps][H]
     __shared__ float s_sum[2][32];
@@ -212,8 +230,12 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 512) norm_grad_kernel(
     const int per = WARP ? kWarpRows : 1;
     wait_for_stream();
     float acc[N];
+    Weights<T, V> wt[C];
 #pragma unroll
     for (int i = 0; i < N; i++) acc[i] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < C; i++)
+        if (p.w && V * (tid + nt * i) < p.H) wt[i].load(p.w, p.w_dtype, V * (tid + nt * i));
     int turn = 0;
     for (long long t = (long long)blockIdx.x * per + (WARP ? threadIdx.x >> 5 : 0); t < p.T; t += (long long)gridDim.x * per) {
         Vec<T, V> a[C];
@@ -234,11 +256,10 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 512) norm_grad_kernel(
         float dot = 0.0f;
 #pragma unroll
         for (int i = 0; i < C; i++) {
-            const int c = V * (tid + nt * i);
             float d[V], n[V], w[V] = {};
             a[i].get(d);
             b[i].get(n);
-            if (p.w && c < p.H) load_w<T, V>(p.w, p.w_dtype, c, w);
+            if (p.w && V * (tid + nt * i) < p.H) wt[i].get(p.w_dtype, w);
 #pragma unroll
             for (int k = 0; k < V; k++) {
                 const float dn = d[k] * (n[k] * r);
@@ -256,7 +277,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 512) norm_grad_kernel(
             a[i].get(d);
             b[i].get(n);
             g[i].get(u);
-            if (p.w) load_w<T, V>(p.w, p.w_dtype, c, w);
+            if (p.w) wt[i].get(p.w_dtype, w);
 #pragma unroll
             for (int k = 0; k < V; k++) u[k] = fmaf((p.w ? d[k] * w[k] : d[k]) - n[k] * r * dot, r, u[k]);
             g[i].set(u);
@@ -307,20 +328,20 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(const float *part, int n,
     if (lane == 0 && col < H) dw[col] = v;
 }
 
-// elements of a thread; a warp takes a row of up to 32 times as many
-constexpr int kNormN = 32;
-
 }  // namespace
 
-// 16 elements a thread up to 8192, 32 beyond; a warp a row up to 1024
-int norm_grad_threads(int H) {
-    const int n = H <= 8192 ? kNormN / 2 : kNormN;
-    return H <= 32 * kNormN ? 32 * kWarpRows : ((H + n - 1) / n + 31) / 32 * 32;
+// 16 elements a thread in blocks that leave it 85 registers (8 up to 256, a warp a row, and from 6145 to 8192)
+struct GradShape {
+    int threads, per_sm;
+};
+static GradShape norm_grad_shape(int H) {
+    if (H <= 256) return {32 * kWarpRows, 8};
+    const int n = H > 6144 && H <= 8192 ? 8 : 16, threads = ((H + n - 1) / n + 31) / 32 * 32;
+    return {threads, threads <= 128 ? 6 : threads <= 256 ? 3 : threads <= 384 ? 2 : 1};
 }
 int norm_grad_blocks(int T, int H) {
     if (T <= 0) return 0;
-    const int per = H <= 32 * kNormN ? kWarpRows : 1, threads = norm_grad_threads(H);
-    const long long most = (long long)sm_count() * (threads <= 128 ? 4 : threads <= 256 ? 2 : 1), need = ((long long)T + per - 1) / per;
+    const long long per = H <= 256 ? kWarpRows : 1, most = (long long)sm_count() * norm_grad_shape(H).per_sm, need = (T + per - 1) / per;
     return (int)(need < most ? need : most);
 }
 size_t norm_grad_workspace(int T, int H) { return (size_t)norm_grad_blocks(T, H) * H * sizeof(float); }
@@ -342,21 +363,18 @@ cudaError_t launch_norm_forward(const void *x, int dtype, long long ldx, const v
             const int threads = ((H + n - 1) / n + 31) / 32 * 32;
             return launch_early(kernel, (unsigned)T, threads, 0, st, 1, p);
         };
-        const bool few = T < 2 * sm_count();
-        if (H <= 32 * kNormN / 4) {
-            if (fits(8)) return run(norm_kernel<X, S, 8, 8, true>, 8, true);
-            return run(norm_kernel<X, S, 1, 8, true>, 8, true);
-        }
-        if (few && H <= 8 * 1024) {
-            if (fits(8)) return run(norm_kernel<X, S, 8, 8, false>, 8, false);
-            return run(norm_kernel<X, S, 1, 8, false>, 8, false);
-        }
-        if (H <= 32 * kNormN) {
-            if (fits(8)) return run(norm_kernel<X, S, 8, kNormN, true>, kNormN, true);
-            return run(norm_kernel<X, S, 1, kNormN, true>, kNormN, true);
-        }
-        if (fits(8)) return run(norm_kernel<X, S, 8, kNormN, false>, kNormN, false);
-        return run(norm_kernel<X, S, 1, kNormN, false>, kNormN, false);
+        // 8 elements a thread where that makes the block for few rows, 16 otherwise
+        const bool few = T < 2 * sm_count() && H <= 8192;
+        auto by_run = [&](auto v) {
+            constexpr int V = decltype(v)::value;
+            if (H <= 256) return run(norm_kernel<X, S, V, 8, true>, 8, true);
+            if (few) return run(norm_kernel<X, S, V, 8, false>, 8, false);
+            if (H <= 512) return run(norm_kernel<X, S, V, 16, true>, 16, true);
+            return run(norm_kernel<X, S, V, 16, false>, 16, false);
+        };
+        if (fits(8)) return by_run(std::integral_constant<int, 8>{});
+        if (fits(2)) return by_run(std::integral_constant<int, 2>{});
+        return by_run(std::integral_constant<int, 1>{});
     };
     return by_dtype(dtype, [&](auto xt) {
         if (s_dtype == MOE_DTYPE_F32) return go(xt, float{});
@@ -377,18 +395,20 @@ cudaError_t launch_norm_backward(const void *dy, int dtype, long long lddy, cons
             return H % v == 0 && runs_of(dy, lddy, sizeof(X), bx) && runs_of(h, ldh, sizeof(S), bs) && runs_of(out, ldo, sizeof(S), bs) &&
                    (!gh || runs_of(gh, ldg, sizeof(S), bs)) && (!w || runs_of(w, 0, 4, min(16, v * (w_dtype == MOE_DTYPE_F32 ? 4 : 2))));
         };
-        if (H <= 32 * kNormN) {
-            const size_t smem = dw ? (size_t)kWarpRows * H * sizeof(float) : 0;
-            if (fits(8)) return launch_early(norm_grad_kernel<X, S, 8, kNormN, true>, blocks, 32 * kWarpRows, smem, st, 1, p);
-            return launch_early(norm_grad_kernel<X, S, 1, kNormN, true>, blocks, 32 * kWarpRows, smem, st, 1, p);
-        }
-        const int threads = norm_grad_threads(H);
-        if (H <= 8192) {
-            if (fits(8)) return launch_early(norm_grad_kernel<X, S, 8, kNormN / 2, false>, blocks, threads, 0, st, 1, p);
-            return launch_early(norm_grad_kernel<X, S, 1, kNormN / 2, false>, blocks, threads, 0, st, 1, p);
-        }
-        if (fits(8)) return launch_early(norm_grad_kernel<X, S, 8, kNormN, false>, blocks, threads, 0, st, 1, p);
-        return launch_early(norm_grad_kernel<X, S, 1, kNormN, false>, blocks, threads, 0, st, 1, p);
+        const int threads = norm_grad_shape(H).threads;
+        auto by_run = [&](auto v) {
+            constexpr int V = decltype(v)::value;
+            if (H <= 256)
+                return launch_early(norm_grad_kernel<X, S, V, 8, 32 * kWarpRows, 8, true>, blocks, threads, dw ? (size_t)kWarpRows * H * sizeof(float) : 0, st, 1, p);
+            if (threads <= 128) return launch_early(norm_grad_kernel<X, S, V, 16, 128, 6, false>, blocks, threads, 0, st, 1, p);
+            if (threads <= 256) return launch_early(norm_grad_kernel<X, S, V, 16, 256, 3, false>, blocks, threads, 0, st, 1, p);
+            if (threads <= 384) return launch_early(norm_grad_kernel<X, S, V, 16, 384, 2, false>, blocks, threads, 0, st, 1, p);
+            if (H <= 8192) return launch_early(norm_grad_kernel<X, S, V, 8, 1024, 1, false>, blocks, threads, 0, st, 1, p);
+            return launch_early(norm_grad_kernel<X, S, V, 16, 1024, 1, false>, blocks, threads, 0, st, 1, p);
+        };
+        if (fits(8)) return by_run(std::integral_constant<int, 8>{});
+        if (fits(2)) return by_run(std::integral_constant<int, 2>{});
+        return by_run(std::integral_constant<int, 1>{});
     };
     const cudaError_t e = by_dtype(dtype, [&](auto xt) {
         if (s_dtype == MOE_DTYPE_F32) return go(xt, float{});
