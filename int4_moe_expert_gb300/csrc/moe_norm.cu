@@ -13,7 +13,7 @@ namespace {
 // ---------------------------------------------------------------------------
 // Norm.  h = x + residual (rounded to the stream's type), r = 1 / sqrt(mean h^2 + eps), y = h r w.  A
 // row's elements stay in registers between the sum and the outputs: each thread holds N of them in runs of
-// V neighbours, V the most that the rows' alignment allows.  A block a row, or for short rows a warp.
+// V neighbours.  A block a row, or for short rows a warp.
 // The e4m3 codes are those of y; with 8 neighbours a lane, 16 lanes hold a 1 x 128 block.  A block's scale steps where its
 // largest magnitude passes 448 times a power of two: a row with a block that is nearer to that than
 // float32's error has its sum of squares done over in float64, so the scales are those of the formula.
@@ -31,6 +31,7 @@ struct NormArgs {
 };
 
 constexpr int kWarpRows = 4;       // rows of a block whose warps take a row each
+extern __shared__ uint4 norm_shared[];
 
 // w's elements c .. c + V - 1 (float32, or the type T of x), as loaded
 template <typename T, int V>
@@ -62,16 +63,144 @@ struct Weights {
     }
 };
 
+// the larger magnitude; a NaN is the largest
+__device__ __forceinline__ float larger(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+    return r;
+}
+
 // 448 = 1.75 x 2^8: a magnitude (its bits) within 64 units of the step of its block's scale.  float32's
 // error: 32 and 10 additions, half of it behind the root, and three more roundings, 24 units at most.
 __device__ __forceinline__ bool at_border(unsigned m) { return (unsigned)(abs((int)(m & 0x7FFFFFu) - 0x600000)) <= 64u && m < 0x7F800000u; }
 
-// S: the stream's type (T or float); N elements a thread
-template <typename T, typename S, int V, int N, bool WARP>
-__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) norm_kernel(const NormArgs p) {
+// The thread's elements of h (v) become y, codes and scales; S: the stream's type (T or float), V neighbours
+// together, N elements a thread.  weight(i, w): the weights of run i.
+template <typename T, typename S, int V, int N, typename F>
+__device__ __forceinline__ void norm_outputs(const NormArgs &p, long long t, int tid, int nt, float (&v)[N], float r, F &&weight) {
+    constexpr int C = N / V;
+#pragma unroll
+    for (int i = 0; i < C; i++) {
+        const int c = V * (tid + nt * i);
+        float w[V] = {};
+        if (p.w && c < p.H) weight(i, w);
+#pragma unroll
+        for (int k = 0; k < V; k++) v[V * i + k] = p.w ? v[V * i + k] * r * w[k] : v[V * i + k] * r;
+        if (p.y && c < p.H) {
+            Vec<T, V> o;
+            o.set(&v[V * i]);
+            o.store(static_cast<T *>(p.y) + t * p.ldy + c);
+        }
+    }
+    if constexpr (V == 8) {
+        if (!p.codes) return;
+        // The largest magnitude of a run's 1 x 128 block, over its 16 lanes.  Two runs meet in one butterfly: the lanes'
+        // upper half ends with the second's.
+        static_assert(C == 1 || C == 2, "");
+        const bool upper = C == 2 && (threadIdx.x & 8);
+        float m[C];
+#pragma unroll
+        for (int i = 0; i < C; i++) {
+            m[i] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < V; k++) m[i] = larger(m[i], v[V * i + k]);
+        }
+        float mine = upper ? m[C - 1] : m[0];
+        mine = larger(mine, __shfl_xor_sync(0xffffffffu, C == 2 && !upper ? m[C - 1] : m[0], 8));
+#pragma unroll
+        for (int d = 4; d; d >>= 1) mine = larger(mine, __shfl_xor_sync(0xffffffffu, mine, d));
+        unsigned most = __float_as_uint(mine);
+        const bool near = at_border(most);
+        if (__any_sync(0xffffffffu, near)) {
+            // h once more, as it was written, or x: the row's sum by this warp alone
+            auto again = [&](int c, double (&u)[V]) {
+                float f[V];
+                if (p.res) {
+                    Vec<S, V> b;
+                    b.load(static_cast<const S *>(p.h) + t * p.ldh + c);
+                    b.get(f);
+                } else {
+                    Vec<T, V> a;
+                    a.load(static_cast<const T *>(p.x) + t * p.ldx + c);
+                    a.get(f);
+                }
+#pragma unroll
+                for (int k = 0; k < V; k++) u[k] = (double)f[k];
+            };
+            double s = 0.0;
+#pragma unroll 1
+            for (int c = V * (threadIdx.x & 31); c < p.H; c += 32 * V) {
+                double u[V];
+                again(c, u);
+#pragma unroll
+                for (int k = 0; k < V; k++) s = fma(u[k], u[k], s);
+            }
+#pragma unroll
+            for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+            const double r64 = 1.0 / sqrt(s / (double)p.H + p.eps);
+            double m64[C];
+#pragma unroll
+            for (int i = 0; i < C; i++) {
+                const int c = V * (tid + nt * i);
+                m64[i] = 0.0;
+                if (c < p.H) {
+                    double u[V];
+                    float w[V];
+                    again(c, u);
+                    if (p.w) weight(i, w);
+#pragma unroll
+                    for (int k = 0; k < V; k++) m64[i] = fmax(m64[i], fabs(p.w ? u[k] * (double)w[k] : u[k]));
+                }
+#pragma unroll
+                for (int d = 8; d; d >>= 1) m64[i] = fmax(m64[i], __shfl_xor_sync(0xffffffffu, m64[i], d));
+            }
+            if (near) {      // on the side that float64 says
+                const unsigned at = (most & 0x7F800000u) | 0x600000u;
+                most = (upper ? m64[C - 1] : m64[0]) * r64 > (double)__uint_as_float(at) ? at + 1 : at;
+            }
+        }
+        float inv_mine;
+        const float scale = block_scale(most, inv_mine);
+        const float inv_other = C == 2 ? __shfl_xor_sync(0xffffffffu, inv_mine, 8) : inv_mine;
+        {      // the first lane of a run's 16, and for the second run the first of the upper half
+            const int c = V * ((tid & ~8) + (upper ? nt : 0));
+            if ((threadIdx.x & 7) == 0 && (C == 2 || !(threadIdx.x & 8)) && c < p.H) p.scales[(size_t)(c / 128) * p.T + t] = scale;
+        }
+#pragma unroll
+        for (int i = 0; i < C; i++) {
+            const int c = V * (tid + nt * i);
+            const float inv = upper == (i == 1) ? inv_mine : inv_other;
+            if (c < p.H) {
+                uint2 o;
+                const float *u = &v[V * i];
+                o.x = codes2(u[0] * inv, u[1] * inv) | codes2(u[2] * inv, u[3] * inv) << 16;
+                o.y = codes2(u[4] * inv, u[5] * inv) | codes2(u[6] * inv, u[7] * inv) << 16;
+                *reinterpret_cast<uint2 *>(p.codes + (size_t)t * p.H + c) = o;
+            }
+        }
+    }
+}
+
+// h of a run of V elements from x and the residual, written if there is one
+template <typename T, typename S, int V>
+__device__ __forceinline__ void norm_add(const NormArgs &p, long long t, int c, const Vec<T, V> &a, Vec<S, V> &b, float *v) {
+    a.get(v);
+    if (p.res) {
+        float u[V];
+        b.get(u);
+#pragma unroll
+        for (int k = 0; k < V; k++) u[k] += v[k];
+        b.set(u);
+        b.get(v);
+        if (c < p.H) b.store(static_cast<S *>(p.h) + t * p.ldh + c);
+    }
+}
+__device__ __forceinline__ float norm_rstd(const NormArgs &p, float ss) { return 1.0f / sqrtf(ss / (float)p.H + (float)p.eps); }
+
+template <typename T, typename S, int V, int N, int THREADS, int PER_SM, bool WARP>
+__global__ void __launch_bounds__(THREADS, PER_SM) norm_kernel(const NormArgs p) {
     constexpr int C = N / V;
     __shared__ float s_sum[2][32];
-    __shared__ double s_sum64[32];
     const int tid = WARP ? threadIdx.x & 31 : threadIdx.x, nt = WARP ? 32 : blockDim.x;
     const int per = WARP ? kWarpRows : 1;
     wait_for_stream();
@@ -79,133 +208,30 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) norm_kernel(cons
     for (long long t = (long long)blockIdx.x * per + (WARP ? threadIdx.x >> 5 : 0); t < p.T; t += (long long)gridDim.x * per) {
         float v[N];
         Weights<T, V> wt[C];       // on their way during the sum
-        {
-            Vec<T, V> a[C];
-            Vec<S, V> b[C];
+        Vec<T, V> a[C];
+        Vec<S, V> b[C];
 #pragma unroll
-            for (int i = 0; i < C; i++) {
-                const int c = V * (tid + nt * i);
-                a[i].zero();
-                b[i].zero();
-                if (c < p.H) {
-                    a[i].load(static_cast<const T *>(p.x) + t * p.ldx + c);
-                    if (p.res) b[i].load(static_cast<const S *>(p.res) + t * p.ldr + c);
-                    if (p.w) wt[i].load(p.w, p.w_dtype, c);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < C; i++) {
-                a[i].get(&v[V * i]);
-                if (p.res) {
-                    float u[V];
-                    b[i].get(u);
-#pragma unroll
-                    for (int k = 0; k < V; k++) u[k] += v[V * i + k];
-                    b[i].set(u);
-                    b[i].get(&v[V * i]);
-                    const int c = V * (tid + nt * i);
-                    if (c < p.H) b[i].store(static_cast<S *>(p.h) + t * p.ldh + c);
-                }
+        for (int i = 0; i < C; i++) {
+            const int c = V * (tid + nt * i);
+            a[i].zero();
+            b[i].zero();
+            if (c < p.H) {
+                a[i].load(static_cast<const T *>(p.x) + t * p.ldx + c);
+                if (p.res) b[i].load(static_cast<const S *>(p.res) + t * p.ldr + c);
+                if (p.w) wt[i].load(p.w, p.w_dtype, c);
             }
         }
+#pragma unroll
+        for (int i = 0; i < C; i++) norm_add<T, S, V>(p, t, V * (tid + nt * i), a[i], b[i], &v[V * i]);
         float ss = 0.0f;
 #pragma unroll
         for (int i = 0; i < N; i++) ss = fmaf(v[i], v[i], ss);
         ss = sum_all<WARP>(ss, s_sum[turn]);
+        if (WARP) __syncwarp();      // the row's h is written, for all lanes
         turn ^= 1;
-        const float r = 1.0f / sqrtf(ss / (float)p.H + (float)p.eps);
+        const float r = norm_rstd(p, ss);
         if (tid == 0 && p.rstd) p.rstd[t] = r;
-        // y in place of h
-#pragma unroll
-        for (int i = 0; i < C; i++) {
-            const int c = V * (tid + nt * i);
-            float w[V] = {};
-            if (p.w && c < p.H) wt[i].get(p.w_dtype, w);
-#pragma unroll
-            for (int k = 0; k < V; k++) v[V * i + k] = p.w ? v[V * i + k] * r * w[k] : v[V * i + k] * r;
-            if (p.y && c < p.H) {
-                Vec<T, V> o;
-                o.set(&v[V * i]);
-                o.store(static_cast<T *>(p.y) + t * p.ldy + c);
-            }
-        }
-        if constexpr (V == 8) {
-            if (!p.codes) continue;
-            unsigned most[C];
-            bool near = false;
-#pragma unroll
-            for (int i = 0; i < C; i++) {
-                unsigned m = 0;
-#pragma unroll
-                for (int k = 0; k < V; k++) m = max(m, abs_bits(v[V * i + k]));
-#pragma unroll
-                for (int d = 8; d; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-                most[i] = m;
-                near |= at_border(m);
-            }
-            if (WARP ? __any_sync(0xffffffffu, near) : __syncthreads_or(near)) {
-                // the thread's own elements of h once more: as it wrote them, or x
-                auto again = [&](int c, double (&u)[V]) {
-                    float f[V];
-                    if (p.res) {
-                        Vec<S, V> b;
-                        b.load(static_cast<const S *>(p.h) + t * p.ldh + c);
-                        b.get(f);
-                    } else {
-                        Vec<T, V> a;
-                        a.load(static_cast<const T *>(p.x) + t * p.ldx + c);
-                        a.get(f);
-                    }
-#pragma unroll
-                    for (int k = 0; k < V; k++) u[k] = (double)f[k];
-                };
-                double s = 0.0;
-#pragma unroll 1
-                for (int i = 0; i < C; i++) {
-                    const int c = V * (tid + nt * i);
-                    double u[V];
-                    if (c >= p.H) break;
-                    again(c, u);
-#pragma unroll
-                    for (int k = 0; k < V; k++) s = fma(u[k], u[k], s);
-                }
-                s = sum_all<WARP>(s, s_sum64);
-                const double r64 = 1.0 / sqrt(s / (double)p.H + p.eps);
-#pragma unroll
-                for (int i = 0; i < C; i++) {
-                    const int c = V * (tid + nt * i);
-                    double m = 0.0;
-                    if (c < p.H) {
-                        double u[V];
-                        float w[V];
-                        again(c, u);
-                        if (p.w) wt[i].get(p.w_dtype, w);
-#pragma unroll
-                        for (int k = 0; k < V; k++) m = fmax(m, fabs(p.w ? u[k] * (double)w[k] : u[k]));
-                    }
-#pragma unroll
-                    for (int d = 8; d; d >>= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, d));
-                    if (at_border(most[i])) {      // on the side that float64 says
-                        const unsigned at = (most[i] & 0x7F800000u) | 0x600000u;
-                        most[i] = m * r64 > (double)__uint_as_float(at) ? at + 1 : at;
-                    }
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < C; i++) {
-                const int c = V * (tid + nt * i);
-                float inv;
-                const float s = block_scale(most[i], inv);
-                if (c < p.H) {
-                    uint2 o;
-                    const float *u = &v[V * i];
-                    o.x = codes2(u[0] * inv, u[1] * inv) | codes2(u[2] * inv, u[3] * inv) << 16;
-                    o.y = codes2(u[4] * inv, u[5] * inv) | codes2(u[6] * inv, u[7] * inv) << 16;
-                    *reinterpret_cast<uint2 *>(p.codes + (size_t)t * p.H + c) = o;
-                    if (c % 128 == 0) p.scales[(size_t)(c / 128) * p.T + t] = s;
-                }
-            }
-        }
+        norm_outputs<T, S, V, N>(p, t, tid, nt, v, r, [&](int i, float *w) { wt[i].get(p.w_dtype, w); });
     }
 }
 
@@ -224,18 +250,19 @@ struct NormGradArgs {
 template <typename T, typename S, int V, int N, int THREADS, int PER_SM, bool WARP>
 __global__ void __launch_bounds__(THREADS, PER_SM) norm_grad_kernel(const NormGradArgs p) {
     constexpr int C = N / V;
-    extern __shared__ float norm_sm[];      // WARP: [warps][H]
+    float *norm_sm = reinterpret_cast<float *>(norm_shared);      // WARP: [warps][H]
     __shared__ float s_sum[2][32];
     const int tid = WARP ? threadIdx.x & 31 : threadIdx.x, nt = WARP ? 32 : blockDim.x;
     const int per = WARP ? kWarpRows : 1;
     wait_for_stream();
     float acc[N];
-    Weights<T, V> wt[C];
 #pragma unroll
     for (int i = 0; i < N; i++) acc[i] = 0.0f;
-#pragma unroll
-    for (int i = 0; i < C; i++)
-        if (p.w && V * (tid + nt * i) < p.H) wt[i].load(p.w, p.w_dtype, V * (tid + nt * i));
+    auto weight = [&](int c, float *w) {      // from L1: no registers to spare
+        Weights<T, V> q;
+        q.load(p.w, p.w_dtype, c);
+        q.get(p.w_dtype, w);
+    };
     int turn = 0;
     for (long long t = (long long)blockIdx.x * per + (WARP ? threadIdx.x >> 5 : 0); t < p.T; t += (long long)gridDim.x * per) {
         Vec<T, V> a[C];
@@ -259,7 +286,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) norm_grad_kernel(const NormGr
             float d[V], n[V], w[V] = {};
             a[i].get(d);
             b[i].get(n);
-            if (p.w && V * (tid + nt * i) < p.H) wt[i].get(p.w_dtype, w);
+            if (p.w && V * (tid + nt * i) < p.H) weight(V * (tid + nt * i), w);
 #pragma unroll
             for (int k = 0; k < V; k++) {
                 const float dn = d[k] * (n[k] * r);
@@ -277,7 +304,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) norm_grad_kernel(const NormGr
             a[i].get(d);
             b[i].get(n);
             g[i].get(u);
-            if (p.w) wt[i].get(p.w_dtype, w);
+            if (p.w) weight(c, w);
 #pragma unroll
             for (int k = 0; k < V; k++) u[k] = fmaf((p.w ? d[k] * w[k] : d[k]) - n[k] * r * dot, r, u[k]);
             g[i].set(u);
@@ -310,6 +337,151 @@ __global__ void __launch_bounds__(THREADS, PER_SM) norm_grad_kernel(const NormGr
     }
 }
 
+// 16-bit streams: every thread copies its own elements of the next D - 1 rows to shared memory while it works on
+// one (asynchronous copies of 16 bytes, which no other thread waits for), so that the bytes in flight do not
+// depend on the registers (16384 x 2048 bf16: 60 us without, 53 us with; 16381 x 6144 170 and 145 us).  Float32
+// streams do without: the copies fill the shared memory that their warps would need (32768 x 2048, bf16 on
+// float32: 146 and 213 us).
+__device__ __forceinline__ void async_copy(uint4 *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void async_wait_all_but(int n) {      // groups: 0, 1 or 2
+    if (n == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else if (n == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+constexpr int kRingN = 16;      // elements a thread
+
+// unit u of the thread in a ring of units
+__device__ __forceinline__ uint4 *ring_unit(int u) { return norm_shared + (size_t)u * blockDim.x + threadIdx.x; }
+template <typename T>
+__device__ __forceinline__ void ring_fetch(int u, const T *src) {      // 8 elements
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; i++) async_copy(ring_unit(u + i), reinterpret_cast<const uint4 *>(src) + i);
+}
+template <typename T>
+__device__ __forceinline__ Vec<T, 8> ring_get(int u) {
+    Vec<T, 8> v;
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; i++) {
+        const uint4 q = *ring_unit(u + i);
+        v.w[4 * i] = q.x;
+        v.w[4 * i + 1] = q.y;
+        v.w[4 * i + 2] = q.z;
+        v.w[4 * i + 3] = q.w;
+    }
+    return v;
+}
+constexpr int ring_units(int n, int t, int s, int streams, int d) { return (n / 8) * d * (t / 2 + streams * (s / 2)); }
+
+// The same through a ring of D rows of dy, h and grad_h.
+template <typename T, typename S, int THREADS, int PER_SM, bool WARP>
+__global__ void __launch_bounds__(THREADS, PER_SM) norm_grad_ring_kernel(const NormGradArgs p, const int D) {
+    constexpr int N = kRingN, C = N / 8, UX = sizeof(T) / 2, US = sizeof(S) / 2, STAGE = C * (UX + 2 * US);
+    __shared__ float s_sum[2][32];
+    const int tid = WARP ? threadIdx.x & 31 : threadIdx.x, nt = WARP ? 32 : blockDim.x;
+    const int per = WARP ? kWarpRows : 1;
+    const long long first = (long long)blockIdx.x * per + (WARP ? threadIdx.x >> 5 : 0), step = (long long)gridDim.x * per;
+    wait_for_stream();
+    auto fetch = [&](long long t, int stage) {
+        if (t < p.T) {
+#pragma unroll
+            for (int i = 0; i < C; i++) {
+                const int c = 8 * (tid + nt * i), u = stage * STAGE;
+                if (c < p.H) {
+                    ring_fetch(u + i * UX, static_cast<const T *>(p.dy) + t * p.lddy + c);
+                    ring_fetch(u + C * UX + i * US, static_cast<const S *>(p.h) + t * p.ldh + c);
+                    if (p.gh) ring_fetch(u + C * (UX + US) + i * US, static_cast<const S *>(p.gh) + t * p.ldg + c);
+                }
+            }
+        }
+        async_commit();
+    };
+    float r_next = first < p.T ? load_in(p.rstd + first) : 0.0f;
+    for (int d = 0; d < D - 1; d++) fetch(first + d * step, d);
+    float acc[N], w[N];
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+        acc[i] = 0.0f;
+        w[i] = 1.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < C; i++)
+        if (p.w && 8 * (tid + nt * i) < p.H) {
+            Weights<T, 8> q;
+            q.load(p.w, p.w_dtype, 8 * (tid + nt * i));
+            q.get(p.w_dtype, &w[8 * i]);
+        }
+    int turn = 0, stage = 0;
+    for (long long t = first; t < p.T; t += step) {
+        fetch(t + (D - 1) * step, stage == 0 ? D - 1 : stage - 1);
+        const float r = r_next;
+        if (t + step < p.T) r_next = load_in(p.rstd + t + step);
+        async_wait_all_but(D - 1);
+        const int u = stage * STAGE;
+        float d[N], h[N], dot = 0.0f;      // d = dy w
+#pragma unroll
+        for (int i = 0; i < C; i++) {
+            if (8 * (tid + nt * i) >= p.H) continue;
+            ring_get<T>(u + i * UX).get(&d[8 * i]);
+            ring_get<S>(u + C * UX + i * US).get(&h[8 * i]);
+#pragma unroll
+            for (int k = 8 * i; k < 8 * i + 8; k++) {
+                acc[k] = fmaf(d[k] * h[k], r, acc[k]);
+                d[k] *= w[k];
+                dot = fmaf(d[k], h[k], dot);
+            }
+        }
+        dot = sum_all<WARP>(dot, s_sum[turn]);
+        turn ^= 1;
+        const float back = -(dot * r / (float)p.H) * r;      // h times this: n mean(d n)
+#pragma unroll
+        for (int i = 0; i < C; i++) {
+            const int c = 8 * (tid + nt * i);
+            if (c >= p.H) continue;
+            float o[8] = {};
+            Vec<S, 8> q;
+            if (p.gh) {
+                q = ring_get<S>(u + C * (UX + US) + i * US);
+                q.get(o);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; k++) o[k] = fmaf(fmaf(h[8 * i + k], back, d[8 * i + k]), r, o[k]);
+            q.set(o);
+            q.store(static_cast<S *>(p.out) + t * p.ldo + c);
+        }
+        stage = stage == D - 1 ? 0 : stage + 1;
+    }
+    async_wait_all_but(0);
+    if (!p.part) return;
+    if constexpr (WARP) {      // the warps' parts, in order, through the ring
+        float *sums = reinterpret_cast<float *>(norm_shared);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            const int c = 8 * (tid + nt * (i / 8)) + i % 8;
+            if (c < p.H) sums[(threadIdx.x >> 5) * p.H + c] = acc[i];
+        }
+        __syncthreads();
+        for (int c = threadIdx.x; c < p.H; c += blockDim.x) {
+            float s = sums[c];
+#pragma unroll
+            for (int k = 1; k < kWarpRows; k++) s += sums[k * p.H + c];
+            p.part[(size_t)blockIdx.x * p.H + c] = s;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < C; i++) {
+            const int c = 8 * (tid + nt * i);
+            if (c >= p.H) continue;
+#pragma unroll
+            for (int k = 0; k < 2; k++)
+                *reinterpret_cast<float4 *>(p.part + (size_t)blockIdx.x * p.H + c + 4 * k) = make_float4(acc[8 * i + 4 * k], acc[8 * i + 4 * k + 1], acc[8 * i + 4 * k + 2], acc[8 * i + 4 * k + 3]);
+        }
+    }
+}
+
 // dw: 32 columns a block, its warps strands of the parts
 __global__ void __launch_bounds__(1024) norm_dw_kernel(const float *part, int n, int H, float *dw) {
     __shared__ float s[32][33];
@@ -330,19 +502,49 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(const float *part, int n,
 
 }  // namespace
 
-// 16 elements a thread in blocks that leave it 85 registers (8 up to 256, a warp a row, and from 6145 to 8192)
-struct GradShape {
-    int threads, per_sm;
+// A ring kernel's shape: 16 elements a thread, a warp a row up to 512, blocks that leave a thread 85 registers (64 from
+// 384 threads on), rings of three rows where an SM holds them for its blocks, else of two, else of two for fewer
+// blocks; none (depth 0) for rows that are too long.
+struct RingShape {
+    int threads, depth, per_sm;
+    size_t smem;
 };
-static GradShape norm_grad_shape(int H) {
-    if (H <= 256) return {32 * kWarpRows, 8};
-    const int n = H > 6144 && H <= 8192 ? 8 : 16, threads = ((H + n - 1) / n + 31) / 32 * 32;
-    return {threads, threads <= 128 ? 6 : threads <= 256 ? 3 : threads <= 384 ? 2 : 1};
+constexpr size_t kRingSmem = 220 * 1024;       // of an SM
+static int ring_threads(int H) { return H <= 32 * kRingN ? 32 * kWarpRows : ((H + kRingN - 1) / kRingN + 31) / 32 * 32; }
+static int ring_per_sm(int threads) { return threads <= 128 ? 6 : threads <= 256 ? 3 : threads <= 512 ? 2 : 1; }
+static RingShape ring_shape(int H, int t, int s, int streams) {
+    RingShape r = {ring_threads(H), 0, 0, 0};
+    const int want = ring_per_sm(r.threads);
+    for (int per_sm = want; per_sm >= 1; per_sm--)
+        for (int d = per_sm == want ? 3 : 2; d >= 2; d--) {
+            const size_t bytes = (size_t)ring_units(kRingN, t, s, streams, d) * r.threads * 16;
+            if (per_sm * (bytes + 1536) <= kRingSmem) return {r.threads, d, per_sm, bytes};
+        }
+    return r;
 }
+static int norm_blocks(int T, int per, int per_sm) {      // per: rows of a block
+    const long long most = (long long)sm_count() * per_sm, need = ((long long)T + per - 1) / per;
+    return (int)(need < most ? need : most);
+}
+// f(kernel's threads, blocks of an SM, a warp a row): the class of a ring kernel
+template <typename F>
+static cudaError_t ring_class(int H, int threads, F &&f) {
+    using std::integral_constant;
+    if (H <= 32 * kRingN) return f(integral_constant<int, 128>{}, integral_constant<int, 6>{}, std::true_type{});
+    if (threads <= 128) return f(integral_constant<int, 128>{}, integral_constant<int, 6>{}, std::false_type{});
+    if (threads <= 256) return f(integral_constant<int, 256>{}, integral_constant<int, 3>{}, std::false_type{});
+    if (threads <= 384) return f(integral_constant<int, 384>{}, integral_constant<int, 2>{}, std::false_type{});
+    if (threads <= 512) return f(integral_constant<int, 512>{}, integral_constant<int, 2>{}, std::false_type{});
+    return f(integral_constant<int, 1024>{}, integral_constant<int, 1>{}, std::false_type{});
+}
+// threads and blocks of an SM of the kernel that reads straight from memory: 16 elements a thread, a warp a row up to 256
+static int direct_threads(int H) { return H <= 256 ? 32 * kWarpRows : ((H + 15) / 16 + 31) / 32 * 32; }
+static int direct_per_sm(int H, int threads) { return H <= 256 ? 6 : threads <= 128 ? 5 : threads <= 256 ? 2 : 1; }
+// at most, whatever the types and alignment
 int norm_grad_blocks(int T, int H) {
     if (T <= 0) return 0;
-    const long long per = H <= 256 ? kWarpRows : 1, most = (long long)sm_count() * norm_grad_shape(H).per_sm, need = (T + per - 1) / per;
-    return (int)(need < most ? need : most);
+    const int a = norm_blocks(T, H <= 32 * kRingN ? kWarpRows : 1, ring_per_sm(ring_threads(H))), b = norm_blocks(T, H <= 256 ? kWarpRows : 1, direct_per_sm(H, direct_threads(H)));
+    return a > b ? a : b;
 }
 size_t norm_grad_workspace(int T, int H) { return (size_t)norm_grad_blocks(T, H) * H * sizeof(float); }
 
@@ -358,19 +560,19 @@ cudaError_t launch_norm_forward(const void *x, int dtype, long long ldx, const v
             return H % v == 0 && runs_of(x, ldx, sizeof(X), min(16, v * (int)sizeof(X))) && (!res || (runs_of(res, ldr, sizeof(S), min(16, v * (int)sizeof(S))) && runs_of(h, ldh, sizeof(S), min(16, v * (int)sizeof(S))))) &&
                    (!y || runs_of(y, ldy, sizeof(X), min(16, v * (int)sizeof(X)))) && (!w || runs_of(w, 0, 4, min(16, v * (w_dtype == MOE_DTYPE_F32 ? 4 : 2))));
         };
-        auto run = [&](auto kernel, int n, bool warp) {
-            if (warp) return launch_early(kernel, (unsigned)((T + kWarpRows - 1) / kWarpRows), 32 * kWarpRows, 0, st, 1, p);
-            const int threads = ((H + n - 1) / n + 31) / 32 * 32;
-            return launch_early(kernel, (unsigned)T, threads, 0, st, 1, p);
+        auto run = [&](auto kernel, int threads, int rows) {
+            return launch_early(kernel, (unsigned)((T + rows - 1) / rows), threads, 0, st, 1, p);
         };
-        // 8 elements a thread where that makes the block for few rows, 16 otherwise
-        const bool few = T < 2 * sm_count() && H <= 8192;
+        auto up = [](int n) { return (n + 31) / 32 * 32; };
+        const int few = up((H + 7) / 8), threads = up((H + 15) / 16);      // with 8 and 16 elements a thread
         auto by_run = [&](auto v) {
             constexpr int V = decltype(v)::value;
-            if (H <= 256) return run(norm_kernel<X, S, V, 8, true>, 8, true);
-            if (few) return run(norm_kernel<X, S, V, 8, false>, 8, false);
-            if (H <= 512) return run(norm_kernel<X, S, V, 16, true>, 16, true);
-            return run(norm_kernel<X, S, V, 16, false>, 16, false);
+            if (H <= 256) return run(norm_kernel<X, S, V, 8, 32 * kWarpRows, 8, true>, 32 * kWarpRows, kWarpRows);
+            if (T < 2 * sm_count() && H <= 8192) return run(norm_kernel<X, S, V, 8, 1024, 1, false>, few, 1);
+            if (threads <= 128) return run(norm_kernel<X, S, V, 16, 128, 8, false>, threads, 1);
+            if (threads <= 256) return run(norm_kernel<X, S, V, 16, 256, 4, false>, threads, 1);
+            if (threads <= 384) return run(norm_kernel<X, S, V, 16, 384, 3, false>, threads, 1);
+            return run(norm_kernel<X, S, V, 16, 1024, 1, false>, threads, 1);
         };
         if (fits(8)) return by_run(std::integral_constant<int, 8>{});
         if (fits(2)) return by_run(std::integral_constant<int, 2>{});
@@ -386,7 +588,7 @@ cudaError_t launch_norm_backward(const void *dy, int dtype, long long lddy, cons
                                  int w_dtype, const void *gh, long long ldg, int T, int H, void *out, long long ldo, float *dw, void *ws,
                                  cudaStream_t st) {
     const NormGradArgs p = {dy, h, w, gh, rstd, lddy, ldh, ldg, ldo, out, dw ? static_cast<float *>(ws) : nullptr, T, H, w_dtype};
-    const int blocks = norm_grad_blocks(T, H);
+    int blocks = 0;
     auto go = [&](auto xt, auto stt) {
         using X = decltype(xt);
         using S = decltype(stt);
@@ -395,18 +597,30 @@ cudaError_t launch_norm_backward(const void *dy, int dtype, long long lddy, cons
             return H % v == 0 && runs_of(dy, lddy, sizeof(X), bx) && runs_of(h, ldh, sizeof(S), bs) && runs_of(out, ldo, sizeof(S), bs) &&
                    (!gh || runs_of(gh, ldg, sizeof(S), bs)) && (!w || runs_of(w, 0, 4, min(16, v * (w_dtype == MOE_DTYPE_F32 ? 4 : 2))));
         };
-        const int threads = norm_grad_shape(H).threads;
+        const bool eights = fits(8);
+        if constexpr (sizeof(S) == 2) {
+            const RingShape r = ring_shape(H, sizeof(X), sizeof(S), 2);
+            if (eights && r.depth) {
+                blocks = norm_blocks(T, H <= 32 * kRingN ? kWarpRows : 1, r.per_sm);
+                return ring_class(H, r.threads, [&](auto th, auto per, auto warp) {
+                    constexpr auto kernel = norm_grad_ring_kernel<X, S, decltype(th)::value, decltype(per)::value, decltype(warp)::value>;
+                    const cudaError_t e = allow_smem<kernel>(kRingSmem);
+                    return e != cudaSuccess ? e : launch_early(kernel, blocks, r.threads, r.smem, st, 1, p, r.depth);
+                });
+            }
+        }
+        const int threads = direct_threads(H);
+        blocks = norm_blocks(T, H <= 256 ? kWarpRows : 1, direct_per_sm(H, threads));
         auto by_run = [&](auto v) {
             constexpr int V = decltype(v)::value;
             if (H <= 256)
-                return launch_early(norm_grad_kernel<X, S, V, 8, 32 * kWarpRows, 8, true>, blocks, threads, dw ? (size_t)kWarpRows * H * sizeof(float) : 0, st, 1, p);
-            if (threads <= 128) return launch_early(norm_grad_kernel<X, S, V, 16, 128, 6, false>, blocks, threads, 0, st, 1, p);
-            if (threads <= 256) return launch_early(norm_grad_kernel<X, S, V, 16, 256, 3, false>, blocks, threads, 0, st, 1, p);
-            if (threads <= 384) return launch_early(norm_grad_kernel<X, S, V, 16, 384, 2, false>, blocks, threads, 0, st, 1, p);
-            if (H <= 8192) return launch_early(norm_grad_kernel<X, S, V, 8, 1024, 1, false>, blocks, threads, 0, st, 1, p);
+                return launch_early(norm_grad_kernel<X, S, V, 8, 32 * kWarpRows, 6, true>, blocks, threads, dw ? (size_t)kWarpRows * H * sizeof(float) : 0, st, 1, p);
+            if (threads <= 128) return launch_early(norm_grad_kernel<X, S, V, 16, 128, 5, false>, blocks, threads, 0, st, 1, p);
+            if (threads <= 256) return launch_early(norm_grad_kernel<X, S, V, 16, 256, 2, false>, blocks, threads, 0, st, 1, p);
+            if (threads <= 512) return launch_early(norm_grad_kernel<X, S, V, 16, 512, 1, false>, blocks, threads, 0, st, 1, p);
             return launch_early(norm_grad_kernel<X, S, V, 16, 1024, 1, false>, blocks, threads, 0, st, 1, p);
         };
-        if (fits(8)) return by_run(std::integral_constant<int, 8>{});
+        if (eights) return by_run(std::integral_constant<int, 8>{});
         if (fits(2)) return by_run(std::integral_constant<int, 2>{});
         return by_run(std::integral_constant<int, 1>{});
     };
