@@ -70,7 +70,7 @@ def _link_binding(obj: Path, key: str) -> None:
     libs = Path(torch.__file__).resolve().parent / "lib"
     tmp = BINDING.with_suffix(".so.tmp%d" % os.getpid())
     (BUILD / KEY).unlink(missing_ok=True)
-    subprocess.run(["g++", "-shared", "-o", str(tmp), str(obj), f"-L{libs}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+    subprocess.run(["g++", "-shared", "-o", str(tmp), str(obj), f"-L{libs}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda",
                     f"-L{PKG}", f"-l:{LIB.name}", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{libs}"], check=True)
     os.replace(tmp, BINDING)
     (BUILD / KEY).write_text(key)

@@ -511,7 +511,7 @@ struct RingShape {
 };
 constexpr size_t kRingSmem = 220 * 1024;       // of an SM
 static int ring_threads(int H) { return H <= 32 * kRingN ? 32 * kWarpRows : ((H + kRingN - 1) / kRingN + 31) / 32 * 32; }
-static int ring_per_sm(int threads) { return threads <= 128 ? 6 : threads <= 256 ? 3 : threads <= 512 ? 2 : 1; }
+static int ring_per_sm(int threads) { return threads <= 128 ? 768 / threads : threads <= 256 ? 3 : threads <= 512 ? 2 : 1; }
 static RingShape ring_shape(int H, int t, int s, int streams) {
     RingShape r = {ring_threads(H), 0, 0, 0};
     const int want = ring_per_sm(r.threads);
@@ -539,7 +539,7 @@ static cudaError_t ring_class(int H, int threads, F &&f) {
 }
 // threads and blocks of an SM of the kernel that reads straight from memory: 16 elements a thread, a warp a row up to 256
 static int direct_threads(int H) { return H <= 256 ? 32 * kWarpRows : ((H + 15) / 16 + 31) / 32 * 32; }
-static int direct_per_sm(int H, int threads) { return H <= 256 ? 6 : threads <= 128 ? 5 : threads <= 256 ? 2 : 1; }
+static int direct_per_sm(int H, int threads) { return H <= 256 ? 6 : threads <= 128 ? 640 / threads : threads <= 256 ? 2 : 1; }
 // at most, whatever the types and alignment
 int norm_grad_blocks(int T, int H) {
     if (T <= 0) return 0;
@@ -569,9 +569,11 @@ cudaError_t launch_norm_forward(const void *x, int dtype, long long ldx, const v
             constexpr int V = decltype(v)::value;
             if (H <= 256) return run(norm_kernel<X, S, V, 8, 32 * kWarpRows, 8, true>, 32 * kWarpRows, kWarpRows);
             if (T < 2 * sm_count() && H <= 8192) return run(norm_kernel<X, S, V, 8, 1024, 1, false>, few, 1);
-            if (threads <= 128) return run(norm_kernel<X, S, V, 16, 128, 8, false>, threads, 1);
-            if (threads <= 256) return run(norm_kernel<X, S, V, 16, 256, 4, false>, threads, 1);
-            if (threads <= 384) return run(norm_kernel<X, S, V, 16, 384, 3, false>, threads, 1);
+            // 64 registers a thread, 56 for 384 threads (three blocks: 16381 x 6144 with codes 155 us, with two 165); single
+            // elements need 85, for their addresses
+            if (threads <= 128) return run(norm_kernel<X, S, V, 16, 128, V == 1 ? 6 : 8, false>, threads, 1);
+            if (threads <= 256) return run(norm_kernel<X, S, V, 16, 256, V == 1 ? 3 : 4, false>, threads, 1);
+            if (threads <= 384) return run(norm_kernel<X, S, V, 16, 384, V == 1 ? 2 : 3, false>, threads, 1);
             return run(norm_kernel<X, S, V, 16, 1024, 1, false>, threads, 1);
         };
         if (fits(8)) return by_run(std::integral_constant<int, 8>{});

@@ -207,35 +207,48 @@ __global__ void __launch_bounds__(kCombGradThreads) combine_grad_kernel(const Co
 
 // ---------------------------------------------------------------------------
 // Norm of all gradients together, and clipping.  The tensors' addresses come as kernel parameters (no
-// table to upload, nothing to keep while a captured call lives).  A chunk is kChunk elements of one
-// tensor; blocks take every gridDim-th chunk.  Squares are added in float32 over a thread's batch, which
+// table to upload, nothing to keep while a captured call lives).  A chunk is a power of two of elements of one
+// tensor, 32768 or as many as give every block one; blocks take every gridDim-th chunk.  Squares are added in float32 over a thread's batch, which
 // is added to a float64 sum; a batch whose largest magnitude's square would leave float32's normal range
 // (2^-50, 2^56) is squared in float64.  Clipping takes the chunks from the last to the first: what the
 // norm read last is still in L2.
 // ---------------------------------------------------------------------------
 
-constexpr int kChunk = 32768;
+constexpr int kChunkMost = 15, kChunkLeast = 11;       // log2 of a chunk's elements
 constexpr int kClipThreads = 256;
+constexpr int kClipFew = 64, kClipMany = 512;      // tensors of a launch: 2 and 18 KB of parameters
+constexpr int kSquaresPerSm = 5, kClipPerSm = 4;       // blocks, all resident
 
+struct ClipTensor {
+    const void *in;
+    void *out;
+    long long n;
+    int dtype;
+};
 template <int MOST>
 struct ClipTable {
-    const void *in[MOST];
-    void *out[MOST];
-    long long n[MOST];
     unsigned first[MOST + 1];       // first chunk of every tensor
-    uint8_t dtype[MOST];
-    int count;
+    int count, chunk;               // tensors, log2 of a chunk's elements
+    ClipTensor tensor[MOST];
 };
 
+// The tensor that holds a chunk, by all threads of the block: the parameters' first reads come from far, and a
+// search by one thread would wait for several of them one after another.
 template <int MOST>
 __device__ __forceinline__ int tensor_of(const ClipTable<MOST> &p, unsigned chunk) {
-    int lo = 0, hi = p.count - 1;
-    while (lo < hi) {
-        const int m = (lo + hi + 1) >> 1;
-        if (p.first[m] <= chunk) lo = m;
-        else hi = m - 1;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < MOST; i += kClipThreads) {
+        const int k = i + (int)threadIdx.x;
+        n += __syncthreads_count(k < p.count && p.first[k < MOST ? k : 0] <= chunk);
     }
-    return lo;
+    return n - 1;
+}
+
+// 16 bytes that are read once
+template <typename T>
+__device__ __forceinline__ void load_once(Vec<T, 16 / (int)sizeof(T)> &v, const T *p) {
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3]) : "l"(p));
 }
 
 // squares of a batch of magnitudes' float32 values
@@ -249,7 +262,7 @@ __device__ __forceinline__ double squares(const float (&v)[N]) {
     }
     if (m == 0.0f || (m > 8.8817842e-16f && m < 7.2057594e16f)) return (double)s;
     double d = 0.0;
-#pragma unroll 1
+#pragma unroll      // (a loop would index v, and have it in local memory on the usual way too: half the rate)
     for (int i = 0; i < N; i++) d = fma((double)v[i], (double)v[i], d);
     return d;
 }
@@ -281,7 +294,7 @@ __device__ __forceinline__ double chunk_squares(const T *p, int n) {
                 float v[U * V];
 #pragma unroll
                 for (int u = 0; u < U; u++) {
-                    if (i + u * kClipThreads < body) r[u].load(p + head + (long long)(i + u * kClipThreads) * V);
+                    if (i + u * kClipThreads < body) load_once(r[u], p + head + (long long)(i + u * kClipThreads) * V);
                     else r[u].zero();
                 }
 #pragma unroll
@@ -292,29 +305,45 @@ __device__ __forceinline__ double chunk_squares(const T *p, int n) {
     return sum;
 }
 
+// The sum over the block, in thread 0: by one warp, since float64 additions of all warps would queue for an SM's
+// two float64 lanes (738 blocks of 2048 elements: 10.0 us with every warp's shuffles, 6.1 so).
+__device__ __forceinline__ double sum64(double v) {
+    __shared__ double s_sum[kClipThreads];
+    s_sum[threadIdx.x] = v;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        v = s_sum[threadIdx.x];
+#pragma unroll
+        for (int i = 32; i < kClipThreads; i += 32) v += s_sum[threadIdx.x + i];
+#pragma unroll
+        for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    }
+    return v;
+}
+
 template <int MOST>
-__global__ void __launch_bounds__(kClipThreads) grad_squares_kernel(const __grid_constant__ ClipTable<MOST> p, double *part) {
-    __shared__ double s_sum[32];
+__global__ void __launch_bounds__(kClipThreads, kSquaresPerSm) grad_squares_kernel(const __grid_constant__ ClipTable<MOST> p, double *part) {
     wait_for_stream();
     double sum = 0.0;
     for (unsigned c = blockIdx.x; c < p.first[p.count]; c += gridDim.x) {
         const int k = tensor_of(p, c);
-        const long long at = (long long)(c - p.first[k]) * kChunk;
-        const int n = (int)min((long long)kChunk, p.n[k] - at);
-        if (p.dtype[k] == MOE_DTYPE_F32) sum += chunk_squares(static_cast<const float *>(p.in[k]) + at, n);
-        else if (p.dtype[k] == MOE_DTYPE_BF16) sum += chunk_squares(static_cast<const __nv_bfloat16 *>(p.in[k]) + at, n);
-        else sum += chunk_squares(static_cast<const __half *>(p.in[k]) + at, n);
+        const ClipTensor q = p.tensor[k];
+        const long long at = (long long)(c - p.first[k]) << p.chunk;
+        const int n = (int)min(1ll << p.chunk, q.n - at);
+        if (q.dtype == MOE_DTYPE_F32) sum += chunk_squares(static_cast<const float *>(q.in) + at, n);
+        else if (q.dtype == MOE_DTYPE_BF16) sum += chunk_squares(static_cast<const __nv_bfloat16 *>(q.in) + at, n);
+        else sum += chunk_squares(static_cast<const __half *>(q.in) + at, n);
     }
-    sum = sum_all<false>(sum, s_sum);
+    sum = sum64(sum);
     if (threadIdx.x == 0) part[blockIdx.x] = sum;
 }
 
-__global__ void __launch_bounds__(1024) grad_norm_kernel(const double *part, int n, float *norm) {
-    __shared__ double s_sum[32];
+__global__ void __launch_bounds__(kClipThreads) grad_norm_kernel(const double *part, int n, float *norm) {
     wait_for_stream();
     double v = 0.0;
-    for (int i = threadIdx.x; i < n; i += 1024) v += load_in(part + i);
-    v = sum_all<false>(v, s_sum);
+#pragma unroll 4
+    for (int i = threadIdx.x; i < n; i += kClipThreads) v += load_in(part + i);
+    v = sum64(v);
     if (threadIdx.x == 0) *norm = (float)sqrt(v);
 }
 
@@ -332,7 +361,7 @@ __device__ __forceinline__ void chunk_scale(const T *p, T *out, int n, float c) 
                 Vec<T, V> r[U];
 #pragma unroll
                 for (int u = 0; u < U; u++)
-                    if (i + u * kClipThreads < body) r[u].load(p + head + (long long)(i + u * kClipThreads) * V);
+                    if (i + u * kClipThreads < body) load_once(r[u], p + head + (long long)(i + u * kClipThreads) * V);
 #pragma unroll
                 for (int u = 0; u < U; u++) {
                     if (i + u * kClipThreads >= body) continue;
@@ -348,45 +377,44 @@ __device__ __forceinline__ void chunk_scale(const T *p, T *out, int n, float c) 
 }
 
 template <int MOST>
-__global__ void __launch_bounds__(kClipThreads) grad_clip_kernel(const __grid_constant__ ClipTable<MOST> p, const float *norm, float most) {
+__global__ void __launch_bounds__(kClipThreads, kClipPerSm) grad_clip_kernel(const __grid_constant__ ClipTable<MOST> p, const float *norm, float most) {
     wait_for_stream();
     const float ratio = most / (load_in(norm) + 1e-6f), c = ratio >= 1.0f ? 1.0f : ratio;      // a NaN stays one
     const unsigned chunks = p.first[p.count];
     for (unsigned i = blockIdx.x; i < chunks; i += gridDim.x) {
         const unsigned ch = chunks - 1 - i;
         const int k = tensor_of(p, ch);
-        if (c == 1.0f && p.in[k] == p.out[k]) continue;      // as they are
-        const long long at = (long long)(ch - p.first[k]) * kChunk;
-        const int n = (int)min((long long)kChunk, p.n[k] - at);
-        if (p.dtype[k] == MOE_DTYPE_F32) chunk_scale(static_cast<const float *>(p.in[k]) + at, static_cast<float *>(p.out[k]) + at, n, c);
-        else if (p.dtype[k] == MOE_DTYPE_BF16)
-            chunk_scale(static_cast<const __nv_bfloat16 *>(p.in[k]) + at, static_cast<__nv_bfloat16 *>(p.out[k]) + at, n, c);
-        else chunk_scale(static_cast<const __half *>(p.in[k]) + at, static_cast<__half *>(p.out[k]) + at, n, c);
+        const ClipTensor q = p.tensor[k];
+        if (c == 1.0f && q.in == q.out) continue;      // as they are
+        const long long at = (long long)(ch - p.first[k]) << p.chunk;
+        const int n = (int)min(1ll << p.chunk, q.n - at);
+        if (q.dtype == MOE_DTYPE_F32) chunk_scale(static_cast<const float *>(q.in) + at, static_cast<float *>(q.out) + at, n, c);
+        else if (q.dtype == MOE_DTYPE_BF16)
+            chunk_scale(static_cast<const __nv_bfloat16 *>(q.in) + at, static_cast<__nv_bfloat16 *>(q.out) + at, n, c);
+        else chunk_scale(static_cast<const __half *>(q.in) + at, static_cast<__half *>(q.out) + at, n, c);
     }
 }
 
-constexpr int kClipFew = 64, kClipMany = 512;      // tensors of a launch: 2 and 17 KB of parameters
-constexpr int kClipPerSm = 6;
-
 // f(table, blocks) for tables of up to MOST tensors (2^45 elements in all at most: chunks are 32-bit)
 template <int MOST, typename F>
-cudaError_t by_tables(int count, const void *const *in, void *const *out, const int32_t *dtype, const int64_t *n, F &&f) {
+cudaError_t by_tables(int count, const void *const *in, void *const *out, const int32_t *dtype, const int64_t *n, int per_sm, F &&f) {
     ClipTable<MOST> p;
+    const unsigned most = (unsigned)sm_count() * per_sm;
+    unsigned long long all = 0;
+    for (int i = 0; i < count; i++) all += (unsigned long long)n[i];
+    p.chunk = kChunkMost;
+    while (p.chunk > kChunkLeast && all >> p.chunk < most) p.chunk--;
     for (int i = 0; i < count;) {
         p.count = 0;
         unsigned chunks = 0;
         for (; i < count && p.count < MOST; i++) {
             if (n[i] == 0) continue;
-            p.in[p.count] = in[i];
-            p.out[p.count] = out ? out[i] : nullptr;
-            p.n[p.count] = n[i];
-            p.dtype[p.count] = (uint8_t)dtype[i];
+            p.tensor[p.count] = {in[i], out ? out[i] : nullptr, (long long)n[i], dtype[i]};
             p.first[p.count++] = chunks;
-            chunks += (unsigned)((n[i] + kChunk - 1) / kChunk);
+            chunks += (unsigned)((n[i] + (1ll << p.chunk) - 1) >> p.chunk);
         }
         if (p.count == 0) break;
         p.first[p.count] = chunks;
-        const unsigned most = (unsigned)sm_count() * kClipPerSm;
         const cudaError_t e = f(p, chunks < most ? chunks : most);
         if (e != cudaSuccess) return e;
     }
@@ -437,30 +465,31 @@ cudaError_t launch_combine_backward(const void *dy, int dtype, long long lddy, c
 
 size_t grad_norm_workspace(int count) {
     const size_t tables = count <= kClipFew ? 1 : ((size_t)count + kClipMany - 1) / kClipMany;
-    return tables * sm_count() * kClipPerSm * sizeof(double);
+    return tables * sm_count() * kSquaresPerSm * sizeof(double);
 }
 
 cudaError_t launch_grad_norm(int count, const void *const *grads, const int32_t *dtype, const int64_t *n, float *norm, void *ws, cudaStream_t st) {
     double *part = static_cast<double *>(ws);
     int parts = 0;
     auto go = [&](auto &table, unsigned blocks) {
-        constexpr int MOST = sizeof(table.in) / sizeof(void *);
+        constexpr int MOST = sizeof(table.tensor) / sizeof(ClipTensor);
         const cudaError_t e = launch_early(grad_squares_kernel<MOST>, blocks, kClipThreads, 0, st, 1, table, part + parts);
         parts += (int)blocks;
         return e;
     };
-    const cudaError_t e = count <= kClipFew ? by_tables<kClipFew>(count, grads, nullptr, dtype, n, go) : by_tables<kClipMany>(count, grads, nullptr, dtype, n, go);
+    const cudaError_t e = count <= kClipFew ? by_tables<kClipFew>(count, grads, nullptr, dtype, n, kSquaresPerSm, go)
+                                        : by_tables<kClipMany>(count, grads, nullptr, dtype, n, kSquaresPerSm, go);
     if (e != cudaSuccess) return e;
-    return launch_early(grad_norm_kernel, 1, 1024, 0, st, 1, part, parts, norm);
+    return launch_early(grad_norm_kernel, 1, kClipThreads, 0, st, 1, part, parts, norm);
 }
 
 cudaError_t launch_grad_clip(int count, const void *const *grads, const int32_t *dtype, const int64_t *n, const float *norm, float most,
                              void *const *out, cudaStream_t st) {
     auto go = [&](auto &table, unsigned blocks) {
-        constexpr int MOST = sizeof(table.in) / sizeof(void *);
+        constexpr int MOST = sizeof(table.tensor) / sizeof(ClipTensor);
         return launch_early(grad_clip_kernel<MOST>, blocks, kClipThreads, 0, st, 1, table, norm, most);
     };
-    return count <= kClipFew ? by_tables<kClipFew>(count, grads, out, dtype, n, go) : by_tables<kClipMany>(count, grads, out, dtype, n, go);
+    return count <= kClipFew ? by_tables<kClipFew>(count, grads, out, dtype, n, kClipPerSm, go) : by_tables<kClipMany>(count, grads, out, dtype, n, kClipPerSm, go);
 }
 
 }  // namespace moe
