@@ -33,32 +33,45 @@ struct NormArgs {
 constexpr int kWarpRows = 4;       // rows of a block whose warps take a row each
 extern __shared__ uint4 norm_shared[];
 
-// w's elements c .. c + V - 1 (float32, or the type T of x), as loaded
-template <typename T, int V>
+// A thread's weights (float32, or the type T of x) as loaded: C runs of V, nt V apart.  Every condition that all
+// elements share stands outside the loops over them: rows of single elements would be branches otherwise.
+template <typename T, int V, int C>
 struct Weights {
-    uint32_t w[V];
-    __device__ __forceinline__ void load(const void *p, int w_dtype, int c) {
-        if (w_dtype == MOE_DTYPE_F32) {
-            Vec<float, V> u;
-            u.load(static_cast<const float *>(p) + c);
+    uint32_t w[C * V];
+    __device__ __forceinline__ void load(const void *p, int w_dtype, int tid, int nt, int H) {
+        if (w_dtype == MOE_DTYPE_F32) load_as(static_cast<const float *>(p), tid, nt, H);
+        else load_as(static_cast<const T *>(p), tid, nt, H);
+    }
+    // f(i, weights of run i as float32) for every run
+    template <typename F>
+    __device__ __forceinline__ void each(int w_dtype, F &&f) const {
+        if (w_dtype == MOE_DTYPE_F32) each_as<float>(f);
+        else each_as<T>(f);
+    }
+
+private:
+    template <typename E>
+    __device__ __forceinline__ void load_as(const E *p, int tid, int nt, int H) {
 #pragma unroll
-            for (int i = 0; i < V; i++) w[i] = u.w[i];
-        } else {
-            Vec<T, V> u;
-            u.load(static_cast<const T *>(p) + c);
+        for (int i = 0; i < C; i++) {
+            const int c = V * (tid + nt * i);
+            Vec<E, V> u;
+            u.zero();
+            if (c < H) u.load(p + c);
 #pragma unroll
-            for (int i = 0; i < Vec<T, V>::W; i++) w[i] = u.w[i];
+            for (int k = 0; k < Vec<E, V>::W; k++) w[V * i + k] = u.w[k];
         }
     }
-    __device__ __forceinline__ void get(int w_dtype, float *v) const {
-        if (w_dtype == MOE_DTYPE_F32) {
+    template <typename E, typename F>
+    __device__ __forceinline__ void each_as(F &&f) const {
 #pragma unroll
-            for (int i = 0; i < V; i++) v[i] = __uint_as_float(w[i]);
-        } else {
-            Vec<T, V> u;
+        for (int i = 0; i < C; i++) {
+            Vec<E, V> u;
+            float v[V];
 #pragma unroll
-            for (int i = 0; i < Vec<T, V>::W; i++) u.w[i] = w[i];
+            for (int k = 0; k < Vec<E, V>::W; k++) u.w[k] = w[V * i + k];
             u.get(v);
+            f(i, v);
         }
     }
 };
@@ -75,21 +88,25 @@ __device__ __forceinline__ float larger(float a, float b) {
 __device__ __forceinline__ bool at_border(unsigned m) { return (unsigned)(abs((int)(m & 0x7FFFFFu) - 0x600000)) <= 64u && m < 0x7F800000u; }
 
 // The thread's elements of h (v) become y, codes and scales; S: the stream's type (T or float), V neighbours
-// together, N elements a thread.  weight(i, w): the weights of run i.
-template <typename T, typename S, int V, int N, typename F>
-__device__ __forceinline__ void norm_outputs(const NormArgs &p, long long t, int tid, int nt, float (&v)[N], float r, F &&weight) {
+// together, N elements a thread.
+template <typename T, typename S, int V, int N>
+__device__ __forceinline__ void norm_outputs(const NormArgs &p, long long t, int tid, int nt, float (&v)[N], float r, const Weights<T, V, N / V> &wt) {
     constexpr int C = N / V;
 #pragma unroll
-    for (int i = 0; i < C; i++) {
-        const int c = V * (tid + nt * i);
-        float w[V] = {};
-        if (p.w && c < p.H) weight(i, w);
+    for (int i = 0; i < N; i++) v[i] *= r;
+    if (p.w)
+        wt.each(p.w_dtype, [&](int i, const float *w) {
 #pragma unroll
-        for (int k = 0; k < V; k++) v[V * i + k] = p.w ? v[V * i + k] * r * w[k] : v[V * i + k] * r;
-        if (p.y && c < p.H) {
+            for (int k = 0; k < V; k++) v[V * i + k] *= w[k];
+        });
+    if (p.y) {
+        T *y = static_cast<T *>(p.y) + t * p.ldy;
+#pragma unroll
+        for (int i = 0; i < C; i++) {
+            const int c = V * (tid + nt * i);
             Vec<T, V> o;
             o.set(&v[V * i]);
-            o.store(static_cast<T *>(p.y) + t * p.ldy + c);
+            if (c < p.H) o.store(y + c);
         }
     }
     if constexpr (V == 8) {
@@ -147,9 +164,19 @@ __device__ __forceinline__ void norm_outputs(const NormArgs &p, long long t, int
                     double u[V];
                     float w[V];
                     again(c, u);
-                    if (p.w) weight(i, w);
 #pragma unroll
-                    for (int k = 0; k < V; k++) m64[i] = fmax(m64[i], fabs(p.w ? u[k] * (double)w[k] : u[k]));
+                    for (int k = 0; k < V; k++) w[k] = 1.0f;
+                    if (p.w && p.w_dtype == MOE_DTYPE_F32) {
+                        Vec<float, V> q;
+                        q.load(static_cast<const float *>(p.w) + c);
+                        q.get(w);
+                    } else if (p.w) {
+                        Vec<T, V> q;
+                        q.load(static_cast<const T *>(p.w) + c);
+                        q.get(w);
+                    }
+#pragma unroll
+                    for (int k = 0; k < V; k++) m64[i] = fmax(m64[i], fabs(u[k] * (double)w[k]));
                 }
 #pragma unroll
                 for (int d = 8; d; d >>= 1) m64[i] = fmax(m64[i], __shfl_xor_sync(0xffffffffu, m64[i], d));
@@ -181,20 +208,6 @@ __device__ __forceinline__ void norm_outputs(const NormArgs &p, long long t, int
     }
 }
 
-// h of a run of V elements from x and the residual, written if there is one
-template <typename T, typename S, int V>
-__device__ __forceinline__ void norm_add(const NormArgs &p, long long t, int c, const Vec<T, V> &a, Vec<S, V> &b, float *v) {
-    a.get(v);
-    if (p.res) {
-        float u[V];
-        b.get(u);
-#pragma unroll
-        for (int k = 0; k < V; k++) u[k] += v[k];
-        b.set(u);
-        b.get(v);
-        if (c < p.H) b.store(static_cast<S *>(p.h) + t * p.ldh + c);
-    }
-}
 __device__ __forceinline__ float norm_rstd(const NormArgs &p, float ss) { return 1.0f / sqrtf(ss / (float)p.H + (float)p.eps); }
 
 template <typename T, typename S, int V, int N, int THREADS, int PER_SM, bool WARP>
@@ -207,22 +220,44 @@ __global__ void __launch_bounds__(THREADS, PER_SM) norm_kernel(const NormArgs p)
     int turn = 0;
     for (long long t = (long long)blockIdx.x * per + (WARP ? threadIdx.x >> 5 : 0); t < p.T; t += (long long)gridDim.x * per) {
         float v[N];
-        Weights<T, V> wt[C];       // on their way during the sum
-        Vec<T, V> a[C];
-        Vec<S, V> b[C];
+        Weights<T, V, C> wt;       // on their way during the sum
+        {
+            Vec<T, V> a[C];
+            const T *x = static_cast<const T *>(p.x) + t * p.ldx;
 #pragma unroll
-        for (int i = 0; i < C; i++) {
-            const int c = V * (tid + nt * i);
-            a[i].zero();
-            b[i].zero();
-            if (c < p.H) {
-                a[i].load(static_cast<const T *>(p.x) + t * p.ldx + c);
-                if (p.res) b[i].load(static_cast<const S *>(p.res) + t * p.ldr + c);
-                if (p.w) wt[i].load(p.w, p.w_dtype, c);
+            for (int i = 0; i < C; i++) {
+                const int c = V * (tid + nt * i);
+                a[i].zero();
+                if (c < p.H) a[i].load(x + c);
+            }
+            if (p.w) wt.load(p.w, p.w_dtype, tid, nt, p.H);
+            if (p.res) {
+                Vec<S, V> b[C];
+                const S *res = static_cast<const S *>(p.res) + t * p.ldr;
+                S *h = static_cast<S *>(p.h) + t * p.ldh;
+#pragma unroll
+                for (int i = 0; i < C; i++) {
+                    const int c = V * (tid + nt * i);
+                    b[i].zero();
+                    if (c < p.H) b[i].load(res + c);
+                }
+#pragma unroll
+                for (int i = 0; i < C; i++) {
+                    const int c = V * (tid + nt * i);
+                    float u[V];
+                    a[i].get(&v[V * i]);
+                    b[i].get(u);
+#pragma unroll
+                    for (int k = 0; k < V; k++) u[k] += v[V * i + k];
+                    b[i].set(u);
+                    b[i].get(&v[V * i]);
+                    if (c < p.H) b[i].store(h + c);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < C; i++) a[i].get(&v[V * i]);
             }
         }
-#pragma unroll
-        for (int i = 0; i < C; i++) norm_add<T, S, V>(p, t, V * (tid + nt * i), a[i], b[i], &v[V * i]);
         float ss = 0.0f;
 #pragma unroll
         for (int i = 0; i < N; i++) ss = fmaf(v[i], v[i], ss);
@@ -231,7 +266,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) norm_kernel(const NormArgs p)
         turn ^= 1;
         const float r = norm_rstd(p, ss);
         if (tid == 0 && p.rstd) p.rstd[t] = r;
-        norm_outputs<T, S, V, N>(p, t, tid, nt, v, r, [&](int i, float *w) { wt[i].get(p.w_dtype, w); });
+        norm_outputs<T, S, V, N>(p, t, tid, nt, v, r, wt);
     }
 }
 
@@ -258,16 +293,13 @@ __global__ void __launch_bounds__(THREADS, PER_SM) norm_grad_kernel(const NormGr
     float acc[N];
 #pragma unroll
     for (int i = 0; i < N; i++) acc[i] = 0.0f;
-    auto weight = [&](int c, float *w) {      // from L1: no registers to spare
-        Weights<T, V> q;
-        q.load(p.w, p.w_dtype, c);
-        q.get(p.w_dtype, w);
-    };
     int turn = 0;
     for (long long t = (long long)blockIdx.x * per + (WARP ? threadIdx.x >> 5 : 0); t < p.T; t += (long long)gridDim.x * per) {
         Vec<T, V> a[C];
         Vec<S, V> b[C], g[C];
         const float r = load_in(p.rstd + t);
+        const T *dy = static_cast<const T *>(p.dy) + t * p.lddy;
+        const S *h = static_cast<const S *>(p.h) + t * p.ldh, *gh = static_cast<const S *>(p.gh) + t * p.ldg;
 #pragma unroll
         for (int i = 0; i < C; i++) {
             const int c = V * (tid + nt * i);
@@ -275,41 +307,102 @@ __global__ void __launch_bounds__(THREADS, PER_SM) norm_grad_kernel(const NormGr
             b[i].zero();
             g[i].zero();
             if (c < p.H) {
-                a[i].load(static_cast<const T *>(p.dy) + t * p.lddy + c);
-                b[i].load(static_cast<const S *>(p.h) + t * p.ldh + c);
-                if (p.gh) g[i].load(static_cast<const S *>(p.gh) + t * p.ldg + c);
+                a[i].load(dy + c);
+                b[i].load(h + c);
             }
         }
+        if (p.gh) {
+#pragma unroll
+            for (int i = 0; i < C; i++) {
+                const int c = V * (tid + nt * i);
+                if (c < p.H) g[i].load(gh + c);
+            }
+        }
+        S *out = static_cast<S *>(p.out) + t * p.ldo;
         float dot = 0.0f;
+        if constexpr (V == 8) {
+            // dy w run by run, before the sum and behind it: its registers are worth more than the loads from L1
+            // (32768 x 2048, bf16 on float32: 145 us, kept in registers 155)
+            auto weight = [&](int c, float *w) {
+                if (p.w_dtype == MOE_DTYPE_F32) {
+                    Vec<float, V> q;
+                    q.load(static_cast<const float *>(p.w) + c);
+                    q.get(w);
+                } else {
+                    Vec<T, V> q;
+                    q.load(static_cast<const T *>(p.w) + c);
+                    q.get(w);
+                }
+            };
 #pragma unroll
-        for (int i = 0; i < C; i++) {
-            float d[V], n[V], w[V] = {};
-            a[i].get(d);
-            b[i].get(n);
-            if (p.w && V * (tid + nt * i) < p.H) weight(V * (tid + nt * i), w);
+            for (int i = 0; i < C; i++) {
+                const int c = V * (tid + nt * i);
+                float d[V], n[V], w[V] = {};
+                a[i].get(d);
+                b[i].get(n);
+                if (p.w && c < p.H) weight(c, w);
 #pragma unroll
-            for (int k = 0; k < V; k++) {
-                const float dn = d[k] * (n[k] * r);
-                acc[V * i + k] += dn;
-                dot = p.w ? fmaf(dn, w[k], dot) : dot + dn;
+                for (int k = 0; k < V; k++) {
+                    const float dn = d[k] * (n[k] * r);
+                    acc[V * i + k] += dn;
+                    dot = p.w ? fmaf(dn, w[k], dot) : dot + dn;
+                }
+            }
+            dot = sum_all<WARP>(dot, s_sum[turn]) / (float)p.H;
+#pragma unroll
+            for (int i = 0; i < C; i++) {
+                const int c = V * (tid + nt * i);
+                if (c >= p.H) continue;
+                float d[V], n[V], w[V], u[V];
+                a[i].get(d);
+                b[i].get(n);
+                g[i].get(u);
+                if (p.w) weight(c, w);
+#pragma unroll
+                for (int k = 0; k < V; k++) u[k] = fmaf((p.w ? d[k] * w[k] : d[k]) - n[k] * r * dot, r, u[k]);
+                g[i].set(u);
+                g[i].store(out + c);
+            }
+        } else {
+            float d[N];      // dy w
+#pragma unroll
+            for (int i = 0; i < C; i++) {
+                float n[V];
+                a[i].get(&d[V * i]);
+                b[i].get(n);
+#pragma unroll
+                for (int k = 0; k < V; k++) acc[V * i + k] = fmaf(d[V * i + k] * n[k], r, acc[V * i + k]);
+            }
+            if (p.w) {
+                Weights<T, V, C> wt;
+                wt.load(p.w, p.w_dtype, tid, nt, p.H);
+                wt.each(p.w_dtype, [&](int i, const float *w) {
+#pragma unroll
+                    for (int k = 0; k < V; k++) d[V * i + k] *= w[k];
+                });
+            }
+#pragma unroll
+            for (int i = 0; i < C; i++) {
+                float n[V];
+                b[i].get(n);
+#pragma unroll
+                for (int k = 0; k < V; k++) dot = fmaf(d[V * i + k], n[k], dot);
+            }
+            dot = sum_all<WARP>(dot, s_sum[turn]);
+            const float back = -(dot * r / (float)p.H) * r;      // h times this: n mean(d n)
+#pragma unroll
+            for (int i = 0; i < C; i++) {
+                const int c = V * (tid + nt * i);
+                float n[V], u[V];
+                b[i].get(n);
+                g[i].get(u);
+#pragma unroll
+                for (int k = 0; k < V; k++) u[k] = fmaf(fmaf(n[k], back, d[V * i + k]), r, u[k]);
+                g[i].set(u);
+                if (c < p.H) g[i].store(out + c);
             }
         }
-        dot = sum_all<WARP>(dot, s_sum[turn]) / (float)p.H;
         turn ^= 1;
-#pragma unroll
-        for (int i = 0; i < C; i++) {
-            const int c = V * (tid + nt * i);
-            if (c >= p.H) continue;
-            float d[V], n[V], w[V], u[V];
-            a[i].get(d);
-            b[i].get(n);
-            g[i].get(u);
-            if (p.w) weight(c, w);
-#pragma unroll
-            for (int k = 0; k < V; k++) u[k] = fmaf((p.w ? d[k] * w[k] : d[k]) - n[k] * r * dot, r, u[k]);
-            g[i].set(u);
-            g[i].store(static_cast<S *>(p.out) + t * p.ldo + c);
-        }
     }
     if (!p.part) return;
     if constexpr (WARP) {
@@ -406,13 +499,14 @@ __global__ void __launch_bounds__(THREADS, PER_SM) norm_grad_ring_kernel(const N
         acc[i] = 0.0f;
         w[i] = 1.0f;
     }
+    if (p.w) {
+        Weights<T, 8, C> q;
+        q.load(p.w, p.w_dtype, tid, nt, p.H);
+        q.each(p.w_dtype, [&](int i, const float *f) {
 #pragma unroll
-    for (int i = 0; i < C; i++)
-        if (p.w && 8 * (tid + nt * i) < p.H) {
-            Weights<T, 8> q;
-            q.load(p.w, p.w_dtype, 8 * (tid + nt * i));
-            q.get(p.w_dtype, &w[8 * i]);
-        }
+            for (int k = 0; k < 8; k++) w[8 * i + k] = f[k];
+        });
+    }
     int turn = 0, stage = 0;
     for (long long t = first; t < p.T; t += step) {
         fetch(t + (D - 1) * step, stage == 0 ? D - 1 : stage - 1);
