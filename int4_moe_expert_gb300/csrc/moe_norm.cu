@@ -633,7 +633,7 @@ static cudaError_t ring_class(int H, int threads, F &&f) {
 }
 // threads and blocks of an SM of the kernel that reads straight from memory: 16 elements a thread, a warp a row up to 256
 static int direct_threads(int H) { return H <= 256 ? 32 * kWarpRows : ((H + 15) / 16 + 31) / 32 * 32; }
-static int direct_per_sm(int H, int threads) { return H <= 256 ? 6 : threads <= 128 ? 640 / threads : threads <= 256 ? 2 : 1; }
+static int direct_per_sm(int H, int threads) { return H <= 256 ? 6 : threads <= 128 ? 640 / threads : threads <= 256 ? 3 : threads <= 384 ? 2 : 1; }
 // at most, whatever the types and alignment
 int norm_grad_blocks(int T, int H) {
     if (T <= 0) return 0;
@@ -712,7 +712,8 @@ cudaError_t launch_norm_backward(const void *dy, int dtype, long long lddy, cons
             if (H <= 256)
                 return launch_early(norm_grad_kernel<X, S, V, 8, 32 * kWarpRows, 6, true>, blocks, threads, dw ? (size_t)kWarpRows * H * sizeof(float) : 0, st, 1, p);
             if (threads <= 128) return launch_early(norm_grad_kernel<X, S, V, 16, 128, 5, false>, blocks, threads, 0, st, 1, p);
-            if (threads <= 256) return launch_early(norm_grad_kernel<X, S, V, 16, 256, 2, false>, blocks, threads, 0, st, 1, p);
+            if (threads <= 256) return launch_early(norm_grad_kernel<X, S, V, 16, 256, 3, false>, blocks, threads, 0, st, 1, p);
+            if (threads <= 384) return launch_early(norm_grad_kernel<X, S, V, 16, 384, 2, false>, blocks, threads, 0, st, 1, p);
             if (threads <= 512) return launch_early(norm_grad_kernel<X, S, V, 16, 512, 1, false>, blocks, threads, 0, st, 1, p);
             return launch_early(norm_grad_kernel<X, S, V, 16, 1024, 1, false>, blocks, threads, 0, st, 1, p);
         };
