@@ -34,6 +34,7 @@ struct RouteArgs {
     float *w;                // [T, K]
     int T, E, K, groups, kept, per_group;
     unsigned group_of;       // e / per_group = e * group_of >> 20
+    int sub;                 // log2 of the lanes that look at a group
     int softmax, renorm;
     float scale;
 };
@@ -206,6 +207,9 @@ __global__ void __launch_bounds__(kRouteThreads, L::PER_SM) route_kernel(const R
             }
         }
         if (p.groups > 1) {
+            // 2^sub lanes a group
+            const int gr = l >> p.sub, part = l & ((1 << p.sub) - 1);
+            const bool valid = gr < p.groups;
             float best = -INFINITY, err = 0.0f, b1 = -INFINITY, b2 = -INFINITY;
             auto join = [&](float v1, float v2) {      // the two best of b1 >= b2 and v1 >= v2
                 b2 = fmaxf(fmaxf(b2, v2), fminf(b1, v1));
@@ -221,59 +225,54 @@ __global__ void __launch_bounds__(kRouteThreads, L::PER_SM) route_kernel(const R
                     two[expert(j) / 4] = make_float2(fmaxf(h1, h2), fmaxf(fminf(h1, h2), fmaxf(l1, l2)));
                 }
                 __syncwarp();
-                if (l < p.groups) {
-                    const int quads = p.per_group / 4;
-                    int i = l % quads;                 // lanes begin at different banks
-#pragma unroll 4
-                    for (int n = 0; n < quads; n++) {
-                        const float2 v = two[l * quads + i];
+                const int quads = p.per_group / 4;
+                if (valid)
+                    for (int i = part; i < quads; i += 1 << p.sub) {
+                        const float2 v = two[gr * quads + i];
                         join(v.x, v.y);
-                        if (++i == quads) i = 0;
                     }
-                }
             } else {
 #pragma unroll
                 for (int j = 0; j < J; j++)
                     if (within(j)) score[expert(j)] = a[j];
                 __syncwarp();
-                if (l < p.groups) {
-                    int i = l % p.per_group;
-                    for (int n = 0; n < p.per_group; n++) {
-                        join(score[l * p.per_group + i], -INFINITY);
-                        if (++i == p.per_group) i = 0;
-                    }
-                }
+                if (valid)
+                    for (int i = part; i < p.per_group; i += 1 << p.sub) join(score[gr * p.per_group + i], -INFINITY);
             }
-            if (l < p.groups) {
+            for (int d = 1 << p.sub >> 1; d; d >>= 1) {
+                const float v1 = __shfl_xor_sync(0xffffffffu, b1, d), v2 = __shfl_xor_sync(0xffffffffu, b2, d);
+                join(v1, v2);
+            }
+            if (valid) {
                 best = p.per_group > 1 ? b1 + b2 : b1;
                 err = kUnit * (5.0f + fabsf(b1) + (p.per_group > 1 ? 5.0f + fabsf(b2) + fabsf(best) : 0.0f));
             }
             int rank = 0;
             for (int i = 0; i < p.groups; i++) {
-                const float v = __shfl_sync(0xffffffffu, best, i, LPT);
-                rank += v > best || (v == best && i < l) ? 1 : 0;
+                const float v = __shfl_sync(0xffffffffu, best, i << p.sub, LPT);
+                rank += v > best || (v == best && i < gr) ? 1 : 0;
             }
-            bool keep = l < p.groups && rank < p.kept;
-            float lo = keep ? best - err : INFINITY, hi = l < p.groups && !keep ? best + err : -INFINITY;
+            bool keep = valid && rank < p.kept;
+            float lo = keep ? best - err : INFINITY, hi = valid && !keep ? best + err : -INFINITY;
 #pragma unroll
             for (int d = LPT / 2; d; d >>= 1) {
                 lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, d));
                 hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, d));
             }
             // a group's NaN or infinite score: the whole row in float64
-            const bool odd = l < p.groups && !(fabsf(best) + err < INFINITY);
+            const bool odd = valid && !(fabsf(best) + err < INFINITY);
             slow = (__ballot_sync(0xffffffffu, odd) >> (g * LPT) & lanes) != 0;
             // between the last kept and the first other: those groups' sums in float64, by all lanes
-            const bool doubt = p.kept < p.groups && !slow && on && lo <= hi && l < p.groups && best + err >= lo && best - err <= hi;
+            const bool doubt = p.kept < p.groups && !slow && on && lo <= hi && valid && part == 0 && best + err >= lo && best - err <= hi;
             unsigned doubts = __ballot_sync(0xffffffffu, doubt);
             if (doubts) {
                 double sum = 0.0;
                 for (unsigned left = doubts; left; left &= left - 1) {
-                    const int who = __ffs(left) - 1, gr = who % LPT;
+                    const int who = __ffs(left) - 1, group = who % LPT >> p.sub;
                     const char *other = row_of(t0 + who / LPT);
                     double b1 = -INFINITY, b2 = -INFINITY;
                     for (int i = lane; i < p.per_group; i += 32) {
-                        const int e = gr * p.per_group + i;
+                        const int e = group * p.per_group + i;
                         const double v = sigmoid64((double)load_el(other, p.dtype, e)) + (BIAS ? (double)bias[e] : 0.0);
                         b2 = fmax(b2, fmin(b1, v));
                         b1 = fmax(b1, v);
@@ -290,16 +289,16 @@ __global__ void __launch_bounds__(kRouteThreads, L::PER_SM) route_kernel(const R
                 const int places = __popc((__ballot_sync(0xffffffffu, keep) >> (g * LPT) & lanes) & mine);
                 int ahead = 0;
                 for (int i = 0; i < p.groups; i++) {
-                    const double v = __shfl_sync(0xffffffffu, sum, i, LPT);
-                    if (mine >> i & 1u) ahead += v > sum || (v == sum && i < l) ? 1 : 0;
+                    const double v = __shfl_sync(0xffffffffu, sum, i << p.sub, LPT);
+                    if (mine >> (i << p.sub) & 1u) ahead += v > sum || (v == sum && i < gr) ? 1 : 0;
                 }
                 if (doubt) keep = ahead < places;
             }
-            const unsigned kept = __ballot_sync(0xffffffffu, keep) >> (g * LPT) & lanes;
+            const unsigned kept = __ballot_sync(0xffffffffu, keep) >> (g * LPT) & lanes;      // a group's first lane counts
             if constexpr (!BIAS) logits();
 #pragma unroll
             for (int j = 0; j < J; j++) {
-                const bool in = within(j) && (kept >> ((unsigned)expert(j) * p.group_of >> 20) & 1u);
+                const bool in = within(j) && (kept >> (((unsigned)expert(j) * p.group_of >> 20) << p.sub) & 1u);
                 a[j] = in ? a[j] : -INFINITY;
             }
             __syncwarp();
@@ -363,7 +362,7 @@ __global__ void __launch_bounds__(kRouteThreads, L::PER_SM) route_kernel(const R
 #pragma unroll
         for (int d = LPT; d < 32; d *= 2) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
         int rank = 0;
-        constexpr int kUsual = 12;       // places without a candidate have the order 0
+        constexpr int kUsual = LPT < 12 ? LPT : 12;       // places without a candidate have the order 0
 #pragma unroll
         for (int c = 0; c < kUsual; c++) rank += __shfl_sync(0xffffffffu, order, c, LPT) > order ? 1 : 0;
         for (int c = kUsual; c < most; c++) rank += __shfl_sync(0xffffffffu, order, c, LPT) > order ? 1 : 0;
@@ -667,22 +666,25 @@ bool rows_of(const void *x, long long ld, int el, int E, int V) {
 
 cudaError_t launch_route_forward(const void *logits, int dtype, long long ld, int T, int E, const float *bias, int K, int softmax,
                                  int groups, int kept, int renorm, float scale, const uint8_t *mask, int *idx, float *w, cudaStream_t st) {
-    RouteArgs p = {logits, ld, dtype, bias, mask, idx, w, T, E, K, groups, kept, E / groups, 0, softmax, renorm, scale};
+    RouteArgs p = {logits, ld, dtype, bias, mask, idx, w, T, E, K, groups, kept, E / groups, 0, 0, softmax, renorm, scale};
     p.group_of = ((1u << 20) + p.per_group - 1) / p.per_group;
     auto go = [&](auto lay) {
         using L = decltype(lay);
         auto smem = [](int e) { return (size_t)kRouteWarps * e * sizeof(double) + (size_t)e * sizeof(float); };
         const cudaError_t e = allow_smem<route_kernel<L>>(smem(1024));
         if (e != cudaSuccess) return e;
+        while (groups > 1 && groups << (p.sub + 1) <= L::LPT) p.sub++;
         const long long need = ((long long)T + kRouteWarps * L::G - 1) / (kRouteWarps * L::G), most = (long long)sm_count() * L::PER_SM;
         return launch_early(route_kernel<L>, (unsigned)(need < most ? need : most), kRouteThreads, smem(E), st, 1, p);
     };
     const bool quads = rows_of(logits, ld, dtype == MOE_DTYPE_F32 ? 4 : 2, E, 4);
     auto by_size = [&](auto bias_) {
         constexpr bool B = decltype(bias_)::value;
-        // Two tokens a warp while at most half of their lanes' maxima are wanted.  Not with groups: the kept ones
-        // may share few lanes, which leaves many candidates (16381 x 256 in 8 groups of which 4: 39 and 19 us).
-        if (K <= 8 && groups == 1) {
+        // Four tokens a warp for few choices of few experts, two while at most half of the lanes' maxima are wanted.
+        // With groups the kept ones may share lanes, which leaves more candidates: then where that many lanes are
+        // left in any case (16381 x 256 in 8 groups of which 4: two tokens 39 us, one 19).
+        if (K <= 4 && groups == 1 && E <= 64) return E <= 16 ? go(RouteLay<B, 2, 8, 1>{}) : go(RouteLay<B, 8, 8, 1>{});
+        if (K <= 8 && groups <= 16 && kept * 8 >= groups * K) {
             if (E <= 32) return go(RouteLay<B, 2, 16, 1>{});
             if (E <= 64) return quads && E == 64 ? go(RouteLay<B, 4, 16, 4, true>{}) : go(RouteLay<B, 4, 16, 1>{});
             if (E <= 128) return quads ? go(RouteLay<B, 8, 16, 4>{}) : go(RouteLay<B, 8, 16, 1>{});
@@ -691,6 +693,7 @@ cudaError_t launch_route_forward(const void *logits, int dtype, long long ld, in
             if (E <= 64) return go(RouteLay<B, 2, 32, 1>{});
             if (E <= 256) return !quads || E < 128 ? go(RouteLay<B, 8, 32, 1>{}) : E == 256 ? go(RouteLay<B, 8, 32, 4, true>{}) : go(RouteLay<B, 8, 32, 4>{});
         }
+        if (E <= 512) return quads ? go(RouteLay<B, 16, 32, 4>{}) : go(RouteLay<B, 16, 32, 1>{});
         return quads ? go(RouteLay<B, 32, 32, 4>{}) : go(RouteLay<B, 32, 32, 1>{});
     };
     return bias && !softmax ? by_size(std::true_type{}) : by_size(std::false_type{});
