@@ -88,6 +88,70 @@ __global__ void __launch_bounds__(32 * kCombWarps) combine_kernel(const CombineA
     }
 }
 
+// Rows of 16-bit elements of an odd width: their starts are on no boundary that a load of several elements could
+// use.  A warp copies the 16-byte pieces that cover its 256 columns of up to 8 rows to shared memory, all at once
+// (the pieces that a row shares with its neighbours element by element), and reads single elements there
+// (8192 x 8 rows of 2047: 153 us by single loads, 105 so).
+constexpr int kShiftCols = 256, kShiftRows = 8, kShiftBytes = 2 * kShiftCols + 16;
+
+template <typename T, typename Y>
+__global__ void __launch_bounds__(32 * kCombWarps) combine_shift_kernel(const CombineArgs p) {
+    static_assert(sizeof(T) == 2, "");
+    __shared__ __align__(16) unsigned char s_rows[kCombWarps][kShiftRows][kShiftBytes];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long job = (long long)blockIdx.x * kCombWarps + warp;
+    wait_for_stream();
+    const long long t = job / p.parts;
+    if (t >= p.T) return;
+    const int c0 = (int)(job - t * p.parts) * kShiftCols;
+    int pos = lane < p.K ? load_in(p.pos + t * p.K + lane) : -1;
+    const float wt = lane < p.K ? (p.w ? load_in(p.w + t * p.K + lane) : 1.0f) : 0.0f;
+    if (pos >= p.R) pos = -1;
+    constexpr int C = kShiftCols / 32;
+    float acc[C] = {};
+    for (int k0 = 0; k0 < p.K; k0 += kShiftRows) {
+        const int rows = min(kShiftRows, p.K - k0);
+        for (int u = 0; u < rows; u++) {
+            const int at = __shfl_sync(0xffffffffu, pos, k0 + u);
+            if (at < 0) continue;
+            const T *row = static_cast<const T *>(p.rows) + at * p.ld;
+            const int off = (int)((reinterpret_cast<uintptr_t>(row + c0) & 15u) / 2);      // elements before c0 in its piece
+            for (int g = lane; g < kShiftBytes / 16; g += 32) {
+                const int c = c0 - off + 8 * g;      // the piece's first column
+                unsigned char *to = s_rows[warp][u] + 16 * g;
+                if (c >= 0 && c + 8 <= p.N) {
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(row + c) : "memory");
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; i++)
+                        if (c + i >= 0 && c + i < p.N) reinterpret_cast<T *>(to)[i] = load_in(row + c + i);
+                }
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncwarp();
+        for (int u = 0; u < rows; u++) {
+            const int at = __shfl_sync(0xffffffffu, pos, k0 + u);
+            const float w = __shfl_sync(0xffffffffu, wt, k0 + u);
+            if (at < 0) continue;
+            const int off = (int)((reinterpret_cast<uintptr_t>(static_cast<const T *>(p.rows) + at * p.ld + c0) & 15u) / 2);
+            const T *q = reinterpret_cast<const T *>(s_rows[warp][u]) + off + lane;
+#pragma unroll
+            for (int i = 0; i < C; i++)
+                if (c0 + 32 * i + lane < p.N) acc[i] = fmaf(w, to_float(q[32 * i]), acc[i]);
+        }
+        __syncwarp();
+    }
+#pragma unroll
+    for (int i = 0; i < C; i++) {
+        const int c = c0 + 32 * i + lane;
+        if (c >= p.N) continue;
+        if (p.add) acc[i] += to_float(load_in(static_cast<const Y *>(p.add) + t * p.ldadd + c));
+        static_cast<Y *>(p.y)[t * p.ldy + c] = from_float<Y>(acc[i]);
+    }
+}
+
 // Gradients: drows[r] = w_tk dy_t for the pair of token t = tokens[r] whose row r is (the sum of the
 // weights if the token names r more than once), zeros for rows that no pair of their token names;
 // dw_tk = rows[pos_tk] . dy_t.  Blocks of tokens read each row once and write its gradient beside it;
@@ -103,6 +167,8 @@ struct CombineGradArgs {
     int T, K, N, token_blocks;
 };
 
+// Warps hide the loads: the pairs' rows and weights stay in shared memory, since in registers they cost half the
+// warps (rows of 2047 bf16: 175 us, with them in registers 243; several runs of a thread at once 405).
 constexpr int kCombGradThreads = 128;
 
 template <typename T, int V>
@@ -441,7 +507,8 @@ cudaError_t launch_combine_forward(const void *rows, int dtype, long long ld, lo
             };
             if (fits(8)) return go(combine_kernel<X, Y, 8, 1>, 8);
             if (fits(2)) return go(combine_kernel<X, Y, 2, 4>, 8);
-            return go(combine_kernel<X, Y, 1, 8>, 8);
+            if constexpr (sizeof(X) == 2) return go(combine_shift_kernel<X, Y>, kShiftCols / 32);
+            else return go(combine_kernel<X, Y, 1, 8>, 8);
         });
     });
 }
