@@ -169,8 +169,9 @@ __global__ void __launch_bounds__(kRouteThreads, L::PER_SM) route_kernel(const R
     long long t0 = ((long long)blockIdx.x * kRouteWarps + warp) * G;
     for (; t0 < p.T; t0 += step) {
         const long long t = t0 + g;
-        const bool here = t < p.T, on = here && (!p.mask || load_in(p.mask + t));
-        const char *row = row_of(t);
+        const bool here = t < p.T;
+        const bool on = here && (!p.mask || load_in(p.mask + t));      // what is ranked for others is not written
+        const char *row = row_of(here ? t : p.T - 1);
         float a[J];
         auto logits = [&] {       // -infinity beyond E
             by_type(p.dtype, [&](auto el) {
@@ -178,8 +179,8 @@ __global__ void __launch_bounds__(kRouteThreads, L::PER_SM) route_kernel(const R
 #pragma unroll
                 for (int j = 0; j < J; j += V) {
                     Vec<T, V> v;
-                    v.zero();
-                    if (on && within(j)) v.load(reinterpret_cast<const T *>(row) + expert(j));
+                    if constexpr (!L::FULL) v.zero();
+                    if (within(j)) v.load(reinterpret_cast<const T *>(row) + expert(j));
                     v.get(&a[j]);
                 }
             });
@@ -321,7 +322,7 @@ __global__ void __launch_bounds__(kRouteThreads, L::PER_SM) route_kernel(const R
         unsigned mine = 0;
 #pragma unroll
         for (int j = 0; j < J; j++) mine = __funnelshift_l(__float_as_uint(a[j] - least), mine, 1);
-        mine = slow ? 0u : ~mine & (J == 32 ? 0xffffffffu : (1u << J % 32) - 1u);
+        mine = ~mine & (J == 32 ? 0xffffffffu : (1u << J % 32) - 1u);
         const int own = __popc(mine);
         int at = own;      // the candidates of this lane and those before it
 #pragma unroll
@@ -330,18 +331,19 @@ __global__ void __launch_bounds__(kRouteThreads, L::PER_SM) route_kernel(const R
             if (l >= d) at += o;
         }
         const int n = __shfl_sync(0xffffffffu, at, LPT - 1, LPT);
+        slow |= n > 32;
         at -= own;
+        if (slow) mine = 0;
         auto next = [&] {
             const int bit = 31 - __clz(mine), j = J - 1 - bit;
-            if (mine != 0 && at < 32) s_cand[warp][g][at] = (short)(V * l + j + (LPT - 1) * V * (j / V));
+            if (mine != 0) s_cand[warp][g][at] = (short)(V * l + j + (LPT - 1) * V * (j / V));
             at++;
             mine &= ~(1u << (bit & 31));
         };
 #pragma unroll
         for (int i = 0; i < (J < 3 ? J : 3); i++) next();
         if (J > 3)
-            while (__any_sync(0xffffffffu, mine != 0 && at < 32)) next();
-        slow |= n > 32;
+            while (__any_sync(0xffffffffu, mine != 0)) next();
         const bool many = on && !slow && n > LPT;
         unsigned again = LPT < 32 ? __ballot_sync(0xffffffffu, many) : 0u;
         __syncwarp();
@@ -379,16 +381,18 @@ __global__ void __launch_bounds__(kRouteThreads, L::PER_SM) route_kernel(const R
             if (one) s_sel[warp][g][rank] = {e, xe, key, be};
             __syncwarp();
         }
+        Chosen c = s_sel[warp][g][l];
         if constexpr (BIAS) {
             // neighbours that float32 does not tell apart; the same logit and bias are equal
-            bool near = false;
-            if (one && l < p.K && l + 1 < n) {
-                const Chosen u = s_sel[warp][g][l], v = s_sel[warp][g][l + 1];
-                near = !(u.key - v.key > 2.0f * key_error(u.key)) && !(u.x == v.x && u.bias == v.bias);
+            const float below = __shfl_down_sync(0xffffffffu, c.key, 1, LPT);
+            const bool tight = one && l < p.K && l + 1 < n && !(c.key - below > 2.0f * key_error(c.key));
+            if (__any_sync(0xffffffffu, tight)) {
+                const float x = __shfl_down_sync(0xffffffffu, c.x, 1, LPT), b = __shfl_down_sync(0xffffffffu, c.bias, 1, LPT);
+                again |= __ballot_sync(0xffffffffu, tight && !(c.x == x && c.bias == b));
             }
-            again |= __ballot_sync(0xffffffffu, near);
-            __syncwarp();
         }
+        const bool redo = (again | __ballot_sync(0xffffffffu, slow && on)) != 0;
+        __syncwarp();
         // those tokens' candidates by all lanes: in float32 if there were too many of them, in float64 if near
         while (again) {
             const int r = (__ffs(again) - 1) / LPT, count = __shfl_sync(0xffffffffu, n, r * LPT);
@@ -428,9 +432,10 @@ __global__ void __launch_bounds__(kRouteThreads, L::PER_SM) route_kernel(const R
             choose64(row_of(t0 + r), p.dtype, BIAS ? bias : nullptr, p.E, p.K, p.groups, p.kept, p.group_of, key64, s_sel[warp][r]);
             __syncwarp();
         }
+        if (redo) c = s_sel[warp][g][l];
         // weights: lane k of the token its k-th choice
         const bool out = on && l < p.K;
-        const Chosen c = out ? s_sel[warp][g][l] : Chosen{-1, -INFINITY, 0.0f, 0.0f};
+        if (!out) c = {-1, -INFINITY, 0.0f, 0.0f};
         float pr, w, z;
         if (!BIAS && p.softmax) {
             const float top = __shfl_sync(0xffffffffu, c.x, 0, LPT), base = top == -INFINITY ? 0.0f : top;
@@ -448,8 +453,13 @@ __global__ void __launch_bounds__(kRouteThreads, L::PER_SM) route_kernel(const R
         }
         const bool soft = !BIAS && p.softmax;
         if (soft || p.renorm) {
+            if (LPT == 32 || (soft && !p.renorm)) {
 #pragma unroll
-            for (int d = LPT / 2; d; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
+                for (int d = LPT / 2; d; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
+            } else {      // K is at most half the lanes
+#pragma unroll
+                for (int d = LPT / 4; d; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
+            }
             w = p.scale * (soft ? (z == 0.0f ? 0.0f : __fdividef(pr, z)) : __fdividef(pr, z + 1e-20f));
         } else {
             w = p.scale * pr;
