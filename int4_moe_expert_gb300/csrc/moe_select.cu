@@ -149,15 +149,16 @@ template <class L>
 __global__ void __launch_bounds__(kRouteThreads, L::PER_SM) route_kernel(const RouteArgs p) {
     constexpr bool BIAS = L::BIAS;
     constexpr int J = L::J, LPT = L::LPT, V = L::V, G = L::G;
-    extern __shared__ __align__(16) double route_sm[];                  // [warps][E]: float64 keys; or scores [G][E] float32; then the bias
+    extern __shared__ __align__(16) double route_sm[];                  // [warps][E + 32]: float64 keys; or scores [G][E + 2 LPT] float32; then the bias
     __shared__ Chosen s_sel[kRouteWarps][G][LPT + 1];
     __shared__ short s_cand[kRouteWarps][G][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % LPT, g = lane / LPT;
     const unsigned lanes = LPT == 32 ? 0xffffffffu : (1u << LPT) - 1u;
-    double *key64 = route_sm + (size_t)warp * p.E;
-    float *score = reinterpret_cast<float *>(key64) + (size_t)g * p.E;
-    float *bias = reinterpret_cast<float *>(route_sm + (size_t)kRouteWarps * p.E);
+    double *key64 = route_sm + (size_t)warp * (p.E + 32);
+    float *score = reinterpret_cast<float *>(key64) + (size_t)g * (p.E + 2 * LPT);
+    float *bias = reinterpret_cast<float *>(route_sm + (size_t)kRouteWarps * (p.E + 32));
     auto expert = [&](int j) { return V * (l + LPT * (j / V)) + j % V; };
+    auto group_at = [&](int j) { return (unsigned)expert(j) * p.group_of >> 20; };
     auto within = [&](int j) { return L::FULL || expert(j) < p.E; };
     auto row_of = [&](long long t) { return static_cast<const char *>(p.logits) + t * p.ld * (p.dtype == MOE_DTYPE_F32 ? 4 : 2); };
     wait_for_stream();
@@ -216,29 +217,35 @@ __global__ void __launch_bounds__(kRouteThreads, L::PER_SM) route_kernel(const R
                 b2 = fmaxf(fmaxf(b2, v2), fminf(b1, v1));
                 b1 = fmaxf(b1, v1);
             };
-            if (V == 4 && p.per_group % 4 == 0) {
-                // the two best of every quad, then of a group's quads
+            // a group's scores 2^sub places apart from the next one's, for the banks
+            if (V > 1 && p.per_group % V == 0) {
+                // the two best of every run, then of a group's runs
                 float2 *two = reinterpret_cast<float2 *>(score);
 #pragma unroll
-                for (int j = 0; j + 3 < J; j += 4) {
+                for (int j = 0; j + V <= J; j += V) {
                     if (!within(j)) continue;
-                    const float h1 = fmaxf(a[j], a[j + 1]), l1 = fminf(a[j], a[j + 1]), h2 = fmaxf(a[j + 2], a[j + 3]), l2 = fminf(a[j + 2], a[j + 3]);
-                    two[expert(j) / 4] = make_float2(fmaxf(h1, h2), fmaxf(fminf(h1, h2), fmaxf(l1, l2)));
+                    float h = fmaxf(a[j], a[j + V / 2]), low = fminf(a[j], a[j + V / 2]);
+                    if constexpr (V == 4) {
+                        const float h2 = fmaxf(a[j + 1], a[j + 3]), l2 = fminf(a[j + 1], a[j + 3]);
+                        low = fmaxf(fminf(h, h2), fmaxf(low, l2));
+                        h = fmaxf(h, h2);
+                    }
+                    two[expert(j) / V + (group_at(j) << p.sub)] = make_float2(h, low);
                 }
                 __syncwarp();
-                const int quads = p.per_group / 4;
+                const int runs = p.per_group / V;
                 if (valid)
-                    for (int i = part; i < quads; i += 1 << p.sub) {
-                        const float2 v = two[gr * quads + i];
+                    for (int i = part; i < runs; i += 1 << p.sub) {
+                        const float2 v = two[gr * (runs + (1 << p.sub)) + i];
                         join(v.x, v.y);
                     }
             } else {
 #pragma unroll
                 for (int j = 0; j < J; j++)
-                    if (within(j)) score[expert(j)] = a[j];
+                    if (within(j)) score[expert(j) + (group_at(j) << p.sub)] = a[j];
                 __syncwarp();
                 if (valid)
-                    for (int i = part; i < p.per_group; i += 1 << p.sub) join(score[gr * p.per_group + i], -INFINITY);
+                    for (int i = part; i < p.per_group; i += 1 << p.sub) join(score[gr * (p.per_group + (1 << p.sub)) + i], -INFINITY);
             }
             for (int d = 1 << p.sub >> 1; d; d >>= 1) {
                 const float v1 = __shfl_xor_sync(0xffffffffu, b1, d), v2 = __shfl_xor_sync(0xffffffffu, b2, d);
@@ -297,10 +304,19 @@ __global__ void __launch_bounds__(kRouteThreads, L::PER_SM) route_kernel(const R
             }
             const unsigned kept = __ballot_sync(0xffffffffu, keep) >> (g * LPT) & lanes;      // a group's first lane counts
             if constexpr (!BIAS) logits();
+            if (V > 1 && p.per_group % V == 0) {
 #pragma unroll
-            for (int j = 0; j < J; j++) {
-                const bool in = within(j) && (kept >> (((unsigned)expert(j) * p.group_of >> 20) << p.sub) & 1u);
-                a[j] = in ? a[j] : -INFINITY;
+                for (int j = 0; j + V <= J; j += V) {
+                    const bool in = within(j) && (kept >> (group_at(j) << p.sub) & 1u);
+#pragma unroll
+                    for (int i = 0; i < V; i++) a[j + i] = in ? a[j + i] : -INFINITY;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < J; j++) {
+                    const bool in = within(j) && (kept >> (group_at(j) << p.sub) & 1u);
+                    a[j] = in ? a[j] : -INFINITY;
+                }
             }
             __syncwarp();
         }
@@ -680,20 +696,28 @@ cudaError_t launch_route_forward(const void *logits, int dtype, long long ld, in
     p.group_of = ((1u << 20) + p.per_group - 1) / p.per_group;
     auto go = [&](auto lay) {
         using L = decltype(lay);
-        auto smem = [](int e) { return (size_t)kRouteWarps * e * sizeof(double) + (size_t)e * sizeof(float); };
+        auto smem = [](int e) { return (size_t)kRouteWarps * (e + 32) * sizeof(double) + (size_t)e * sizeof(float); };
         const cudaError_t e = allow_smem<route_kernel<L>>(smem(1024));
         if (e != cudaSuccess) return e;
         while (groups > 1 && groups << (p.sub + 1) <= L::LPT) p.sub++;
         const long long need = ((long long)T + kRouteWarps * L::G - 1) / (kRouteWarps * L::G), most = (long long)sm_count() * L::PER_SM;
         return launch_early(route_kernel<L>, (unsigned)(need < most ? need : most), kRouteThreads, smem(E), st, 1, p);
     };
-    const bool quads = rows_of(logits, ld, dtype == MOE_DTYPE_F32 ? 4 : 2, E, 4);
+    const int el = dtype == MOE_DTYPE_F32 ? 4 : 2;
+    const bool quads = rows_of(logits, ld, el, E, 4), pairs = rows_of(logits, ld, el, E, 2) && p.per_group % 2 == 0;
     auto by_size = [&](auto bias_) {
         constexpr bool B = decltype(bias_)::value;
         // Four tokens a warp for few choices of few experts, two while at most half of the lanes' maxima are wanted.
-        // With groups the kept ones may share lanes, which leaves more candidates: then where that many lanes are
-        // left in any case (16381 x 256 in 8 groups of which 4: two tokens 39 us, one 19).
+        // With groups the kept ones may share lanes, which leaves more candidates: two tokens where each group covers
+        // all their lanes (in runs of two logits 32 experts, one by one 16), or where enough lanes are left in any
+        // case (16381 x 256 in 8 groups of which 4: one token in runs of four 19.5 us, two in runs of two 13.9).
         if (K <= 4 && groups == 1 && E <= 64) return E <= 16 ? go(RouteLay<B, 2, 8, 1>{}) : go(RouteLay<B, 8, 8, 1>{});
+        if (groups > 1 && K <= 8 && groups <= 16 && p.per_group >= 16 && E > 32 && E <= 256) {
+            if (E <= 64) return go(RouteLay<B, 4, 16, 1>{});
+            if (E <= 128) return go(RouteLay<B, 8, 16, 1>{});
+            if (pairs && p.per_group >= 32) return E == 256 ? go(RouteLay<B, 16, 16, 2, true>{}) : go(RouteLay<B, 16, 16, 2>{});
+            return go(RouteLay<B, 16, 16, 1>{});
+        }
         if (K <= 8 && groups <= 16 && kept * 8 >= groups * K) {
             if (E <= 32) return go(RouteLay<B, 2, 16, 1>{});
             if (E <= 64) return quads && E == 64 ? go(RouteLay<B, 4, 16, 4, true>{}) : go(RouteLay<B, 4, 16, 1>{});
