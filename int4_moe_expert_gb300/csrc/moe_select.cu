@@ -334,10 +334,11 @@ __global__ void __launch_bounds__(kRouteThreads, L::PER_SM) route_kernel(const R
         const float kth = __shfl_sync(0xffffffffu, m, p.K - 1, LPT);
         const float least = BIAS ? kth - 2.0f * kUnit * (5.0f + fabsf(kth)) : kth;
         slow |= !(least > -INFINITY);
-        // bit J - 1 - j: a_j is not below (a NaN neither: it is found among the candidates)
+        // bit J - 1 - j: a_j is not below (a NaN neither: it is found among the candidates; 0 - least: -0 is not below +0)
+        const float up = 0.0f - least;
         unsigned mine = 0;
 #pragma unroll
-        for (int j = 0; j < J; j++) mine = __funnelshift_l(__float_as_uint(a[j] - least), mine, 1);
+        for (int j = 0; j < J; j++) mine = __funnelshift_l(__float_as_uint(a[j] + up), mine, 1);
         mine = ~mine & (J == 32 ? 0xffffffffu : (1u << J % 32) - 1u);
         const int own = __popc(mine);
         int at = own;      // the candidates of this lane and those before it

@@ -298,6 +298,34 @@ def test_route_ties_go_to_the_lowest_index(gpu, E, K):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("E,G,dtype,shift", [(64, 4, F32, 0), (64, 4, BF16, 1), (128, 8, F16, 0), (160, 4, F32, 0), (160, 8, BF16, 0), (200, 8, F32, 0), (250, 5, F16, 0),
+                                             (255, 15, F32, 0), (256, 8, BF16, 0), (256, 8, F32, 1), (256, 16, F16, 0), (512, 8, F32, 0), (1000, 4, BF16, 0), (256, 32, F32, 0)])
+def test_route_groups_of_every_layout(gpu, E, G, dtype, shift):
+    """Groups that lanes hold in runs of one, two and four logits; ties, keys near one another, rows of one value, NaN and infinities."""
+    T = 67
+    g = gen(E, G, shift)
+    K = min(8, E // G)
+    x = torch.randn(T, E, generator=g)
+    x[:9] = (x[:9] * 2).round() / 2
+    x[9:18] = torch.randint(0, 2, (9, E), generator=g).float()
+    x[18] = 0.0
+    x[19, ::3] = nan
+    x[20, 1::2] = -inf
+    x[21] = -inf
+    x = x.to(dtype)
+    bias = 0.2 * torch.randn(E, generator=g)
+    near = (0.7 + 1e-8 * torch.randperm(E, generator=g).double() - torch.sigmoid(x[40].double())).float()      # row 40: all keys next to 0.7
+    for b in (None, torch.zeros(E), bias, near):
+        for kept in sorted({1, (G + 1) // 2, G}):
+            v = strided(x, shift, shift)
+            idx, w = gpu.moe_route_forward(v, K, bias=None if b is None else b.cuda(), n_group=G, topk_group=kept)
+            ref, want = route_ref(x, K, bias=b, G=G, kept=kept)
+            assert torch.equal(idx.cpu().long(), ref), (kept, (idx.cpu() != ref).nonzero()[:4])
+            ok = ~torch.isnan(want)
+            assert bool(((w.cpu().double() - want)[ok].abs() <= 2.0 ** -20 * want[ok] + 1e-30).all()) and torch.equal(torch.isnan(w.cpu()), ~ok)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("gap", [0.0, 1e-12, 1e-9, 3e-8, 1e-7, 1e-6])
 def test_route_keys_nearer_than_float32_tells(gpu, gap):
     """Keys sigmoid(l) + bias that are `gap` apart: the order is that of their float64 values."""
