@@ -17,7 +17,7 @@ namespace {
 // every pair's load in flight.
 // ---------------------------------------------------------------------------
 
-constexpr int kCombWarps = 8;
+constexpr int kCombWarps = 8, kPieceLanes = 31;
 
 struct CombineArgs {
     const void *rows;
@@ -88,68 +88,161 @@ __global__ void __launch_bounds__(32 * kCombWarps) combine_kernel(const CombineA
     }
 }
 
-// Rows of 16-bit elements of an odd width: their starts are on no boundary that a load of several elements could
-// use.  A warp copies the 16-byte pieces that cover its 256 columns of up to 8 rows to shared memory, all at once
-// (the pieces that a row shares with its neighbours element by element), and reads single elements there
-// (8192 x 8 rows of 2047: 153 us by single loads, 105 so).
-constexpr int kShiftCols = 256, kShiftRows = 8, kShiftBytes = 2 * kShiftCols + 16;
-
-template <typename T, typename Y>
-__global__ void __launch_bounds__(32 * kCombWarps) combine_shift_kernel(const CombineArgs p) {
-    static_assert(sizeof(T) == 2, "");
-    __shared__ __align__(16) unsigned char s_rows[kCombWarps][kShiftRows][kShiftBytes];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long job = (long long)blockIdx.x * kCombWarps + warp;
-    wait_for_stream();
-    const long long t = job / p.parts;
-    if (t >= p.T) return;
-    const int c0 = (int)(job - t * p.parts) * kShiftCols;
-    int pos = lane < p.K ? load_in(p.pos + t * p.K + lane) : -1;
-    const float wt = lane < p.K ? (p.w ? load_in(p.w + t * p.K + lane) : 1.0f) : 0.0f;
-    if (pos >= p.R) pos = -1;
-    constexpr int C = kShiftCols / 32;
-    float acc[C] = {};
-    for (int k0 = 0; k0 < p.K; k0 += kShiftRows) {
-        const int rows = min(kShiftRows, p.K - k0);
-        for (int u = 0; u < rows; u++) {
-            const int at = __shfl_sync(0xffffffffu, pos, k0 + u);
-            if (at < 0) continue;
-            const T *row = static_cast<const T *>(p.rows) + at * p.ld;
-            const int off = (int)((reinterpret_cast<uintptr_t>(row + c0) & 15u) / 2);      // elements before c0 in its piece
-            for (int g = lane; g < kShiftBytes / 16; g += 32) {
-                const int c = c0 - off + 8 * g;      // the piece's first column
-                unsigned char *to = s_rows[warp][u] + 16 * g;
-                if (c >= 0 && c + 8 <= p.N) {
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(row + c) : "memory");
-                } else {
+// E elements of a row from column c on, whatever the boundary: the 16-byte pieces that hold them, shifted to their
+// place when they are used.  Columns outside [0, N) are anything.  Pieces that are not all of the tensor
+// [first, end) are read element by element.
+struct Extent {
+    uintptr_t first, end;
+};
+template <typename T, int E, bool ALIGNED = false>
+struct Pieces {
+    static constexpr int W = E * (int)sizeof(T) / 4, P = W / 4 + (ALIGNED ? 0 : 1);
+    uint32_t w[4 * P];
+    unsigned s;        // bytes before the first element
+    __device__ __forceinline__ void load(const T *row, int c, int N, const Extent x) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(row) + (intptr_t)c * (int)sizeof(T);
+        s = ALIGNED ? 0u : (unsigned)at & 15u;
+        const uintptr_t q = at - s;
+        if (q >= x.first && q + 16 * (W / 4 + (s ? 1 : 0)) <= x.end) {
 #pragma unroll
-                    for (int i = 0; i < 8; i++)
-                        if (c + i >= 0 && c + i < p.N) reinterpret_cast<T *>(to)[i] = load_in(row + c + i);
+            for (int i = 0; i < P; i++) {
+                if (i == W / 4 && s == 0) break;
+                const uint4 v = load_in(reinterpret_cast<const uint4 *>(q) + i);
+                w[4 * i] = v.x;
+                w[4 * i + 1] = v.y;
+                w[4 * i + 2] = v.z;
+                w[4 * i + 3] = v.w;
+            }
+        } else {
+            s = 0;
+            constexpr int PER = 4 / (int)sizeof(T);
+#pragma unroll
+            for (int i = 0; i < W; i++) {
+                w[i] = 0;
+#pragma unroll
+                for (int h = 0; h < PER; h++) {
+                    const int col = c + PER * i + h;
+                    if (col < 0 || col >= N) continue;
+                    if constexpr (PER == 2) w[i] |= (unsigned)load_in(reinterpret_cast<const unsigned short *>(row) + col) << (16 * h);
+                    else w[i] = load_in(reinterpret_cast<const unsigned *>(row) + col);
                 }
             }
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-        __syncwarp();
-        for (int u = 0; u < rows; u++) {
-            const int at = __shfl_sync(0xffffffffu, pos, k0 + u);
-            const float w = __shfl_sync(0xffffffffu, wt, k0 + u);
-            if (at < 0) continue;
-            const int off = (int)((reinterpret_cast<uintptr_t>(static_cast<const T *>(p.rows) + at * p.ld + c0) & 15u) / 2);
-            const T *q = reinterpret_cast<const T *>(s_rows[warp][u]) + off + lane;
+    }
+    __device__ __forceinline__ void get(float *v) const {
+        Vec<T, E> o;
+        if constexpr (ALIGNED) {
 #pragma unroll
-            for (int i = 0; i < C; i++)
-                if (c0 + 32 * i + lane < p.N) acc[i] = fmaf(w, to_float(q[32 * i]), acc[i]);
+            for (int i = 0; i < W; i++) o.w[i] = w[i];
+        } else {
+            uint32_t b[W + 2];
+#pragma unroll
+            for (int i = 0; i < W + 2; i++) b[i] = s & 8u ? w[i + 2] : w[i];
+#pragma unroll
+            for (int i = 0; i < W + 1; i++) b[i] = s & 4u ? b[i + 1] : b[i];
+#pragma unroll
+            for (int i = 0; i < W; i++) o.w[i] = sizeof(T) == 4 ? b[i] : __funnelshift_r(b[i], b[i + 1], 8u * (s & 2u));
         }
-        __syncwarp();
+        o.get(v);
     }
+};
+// the columns of v[E] from c on that the row has; c's address on a 16-byte boundary
+template <typename T, int E>
+__device__ __forceinline__ void store_run(T *row, int c, int N, const float *v) {
+    Vec<T, E> o;
+    o.set(v);
+    if (c >= 0 && c + E <= N) {
+        o.store(row + c);
+    } else {
 #pragma unroll
-    for (int i = 0; i < C; i++) {
-        const int c = c0 + 32 * i + lane;
-        if (c >= p.N) continue;
-        if (p.add) acc[i] += to_float(load_in(static_cast<const Y *>(p.add) + t * p.ldadd + c));
-        static_cast<Y *>(p.y)[t * p.ldy + c] = from_float<Y>(acc[i]);
+        for (int i = 0; i < E; i++)
+            if (c + i >= 0 && c + i < N) row[c + i] = from_float<T>(v[i]);
     }
+}
+template <typename T>
+__device__ __forceinline__ int off_boundary(const T *p) {      // elements since the last 16-byte boundary
+    return (int)((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(T));
+}
+template <typename T>
+__device__ __forceinline__ Extent extent(const void *x, long long rows, long long ld, int N) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(x);
+    return {at, at + (uintptr_t)(((rows - 1) * ld + N) * (long long)sizeof(T))};
+}
+
+// Rows that start off 16-byte boundaries or end off a run: the same, in runs that begin on the boundaries of y.  A lane
+// loads the pieces that begin in its run and takes the one behind from the next lane, so that 31 lanes have a run:
+// eight pairs in flight (8192 x 8 rows of 2047 bf16: 76 us; single elements through shared memory 105, single loads
+// 153).
+template <typename T, typename Y>
+__global__ void __launch_bounds__(32 * kCombWarps, 4) combine_pieces_kernel(const CombineArgs p) {
+    constexpr int E = sizeof(T) == 4 && sizeof(Y) == 4 ? 4 : 8, W = E * (int)sizeof(T) / 4;
+    constexpr int U = W == 4 ? 8 : 4;       // pairs in flight
+    const int lane = threadIdx.x & 31;
+    const long long job = (long long)blockIdx.x * kCombWarps + (threadIdx.x >> 5);
+    wait_for_stream();
+    const long long t = job / p.parts;
+    if (t >= p.T) return;
+    Y *y = static_cast<Y *>(p.y) + t * p.ldy;
+    const int c = ((int)(job - t * p.parts) * kPieceLanes + lane) * E - off_boundary(y);
+    int pos = lane < p.K ? load_in(p.pos + t * p.K + lane) : -1;
+    const float wt = lane < p.K ? (p.w ? load_in(p.w + t * p.K + lane) : 1.0f) : 0.0f;
+    if (pos >= p.R) pos = -1;
+    const Extent x = extent<T>(p.rows, p.R, p.ld, p.N);
+    float acc[E] = {};
+    for (int k0 = 0; k0 < p.K; k0 += U) {
+        uint32_t r[U][W];
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const int at = __shfl_sync(0xffffffffu, pos, min(k0 + u, 31));
+#pragma unroll
+            for (int i = 0; i < W; i++) r[u][i] = 0;
+            if (k0 + u >= p.K || at < 0 || c - E >= p.N) continue;
+            const uintptr_t q = (reinterpret_cast<uintptr_t>(static_cast<const T *>(p.rows) + at * p.ld) + (intptr_t)c * (int)sizeof(T)) & ~(uintptr_t)15;
+            if (q >= x.first && q + 4 * W <= x.end) {
+#pragma unroll
+                for (int i = 0; i < W; i += 4) {
+                    const uint4 v = load_in(reinterpret_cast<const uint4 *>(q) + i / 4);
+                    r[u][i] = v.x;
+                    r[u][i + 1] = v.y;
+                    r[u][i + 2] = v.z;
+                    r[u][i + 3] = v.w;
+                }
+            } else {       // partly outside the tensor
+#pragma unroll
+                for (int i = 0; i < 4 * W; i += (int)sizeof(T))
+                    if (q + i >= x.first && q + i < x.end) {
+                        if constexpr (sizeof(T) == 2) r[u][i / 4] |= (unsigned)load_in(reinterpret_cast<const unsigned short *>(q + i)) << (8 * (i & 2));
+                        else r[u][i / 4] = load_in(reinterpret_cast<const unsigned *>(q + i));
+                    }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const int k = min(k0 + u, 31), at = __shfl_sync(0xffffffffu, pos, k);
+            const float w = __shfl_sync(0xffffffffu, wt, k);
+            if (k0 + u >= p.K || at < 0) continue;
+            Pieces<T, E> o;
+            o.s = (unsigned)(reinterpret_cast<uintptr_t>(static_cast<const T *>(p.rows) + at * p.ld) + (intptr_t)c * (int)sizeof(T)) & 15u;
+#pragma unroll
+            for (int i = 0; i < W; i++) o.w[i] = r[u][i];
+#pragma unroll
+            for (int i = 0; i < 4; i++) o.w[W + i] = __shfl_down_sync(0xffffffffu, r[u][i], 1);
+            float v[E];
+            o.get(v);
+#pragma unroll
+            for (int i = 0; i < E; i++) acc[i] = fmaf(w, v[i], acc[i]);
+        }
+    }
+    if (lane >= kPieceLanes || c >= p.N) return;
+    if (p.add) {
+        Pieces<Y, E> o;
+        float v[E];
+        o.load(static_cast<const Y *>(p.add) + t * p.ldadd, c, p.N, extent<Y>(p.add, p.T, p.ldadd, p.N));
+        o.get(v);
+#pragma unroll
+        for (int k = 0; k < E; k++) acc[k] += v[k];
+    }
+    store_run<Y, E>(y, c, p.N, acc);
 }
 
 // Gradients: drows[r] = w_tk dy_t for the pair of token t = tokens[r] whose row r is (the sum of the
@@ -167,56 +260,72 @@ struct CombineGradArgs {
     int T, K, N, token_blocks;
 };
 
-// Warps hide the loads: the pairs' rows and weights stay in shared memory, since in registers they cost half the
-// warps (rows of 2047 bf16: 175 us, with them in registers 243; several runs of a thread at once 405).
-constexpr int kCombGradThreads = 128;
+constexpr int kCombGradThreads = 128, kCombGradWarps = kCombGradThreads / 32;
 
-template <typename T, int V>
+// the rows without a pair among the block's: f(row) by whole warps
+template <typename F>
+__device__ __forceinline__ void empty_rows(const CombineGradArgs &p, F &&f) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long r = ((long long)((int)blockIdx.x - p.token_blocks) * kCombGradWarps + warp) * 32 + lane;
+    bool empty = r < p.R;
+    if (empty) {
+        const int t = load_in(p.tokens + r);
+        if ((unsigned)t < (unsigned)p.T)
+            for (int k = 0; k < p.K && empty; k++) empty = load_in(p.pos + (long long)t * p.K + k) != r;
+    }
+    unsigned todo = __ballot_sync(0xffffffffu, empty);
+    while (todo) {
+        f(r - lane + __ffs(todo) - 1);
+        todo &= todo - 1;
+    }
+}
+
+// Token t's pairs by one warp: row (-1: none), whether the pair writes its row's gradient, and with which weight.
+struct Pairs {
+    int pos[32], write[32];
+    float w[32];
+};
+__device__ __forceinline__ void token_pairs(const CombineGradArgs &p, long long t, int lane, Pairs &s) {
+    int pos = lane < p.K ? load_in(p.pos + t * p.K + lane) : -1;
+    if (pos >= p.R) pos = -1;
+    float w = lane < p.K ? (p.w ? load_in(p.w + t * p.K + lane) : 1.0f) : 0.0f;
+    const bool ours = pos >= 0 && load_in(p.tokens + pos) == t;
+    // a row that the token names twice: its first pair writes, with the sum of the weights
+    const unsigned same = __match_any_sync(0xffffffffu, pos >= 0 ? pos : (int)(0x80000000u | lane));
+    if (__ballot_sync(0xffffffffu, (same & (same - 1u)) != 0)) {
+        float sum = 0.0f;
+        for (int i = 0; i < 32; i++) {
+            const float o = __shfl_sync(0xffffffffu, w, i);
+            if (same >> i & 1u) sum += o;
+        }
+        w = sum;
+    }
+    s.pos[lane] = pos;
+    s.write[lane] = ours && lane == __ffs(same) - 1;
+    s.w[lane] = w;
+}
+
+// Warps hide the loads: the pairs' rows and weights stay in shared memory, since in registers they cost half the
+// warps and as much of the speed (8192 x 8 rows of 2048 bf16: 104 us of 89).
+template <typename T>
 __global__ void __launch_bounds__(kCombGradThreads) combine_grad_kernel(const CombineGradArgs p) {
-    constexpr int NW = kCombGradThreads / 32, U = 8;
-    __shared__ int s_pos[32], s_write[32];
-    __shared__ float s_w[32], s_part[NW][U];
+    constexpr int V = 8;
+    constexpr int NW = kCombGradWarps, U = 8;
+    __shared__ Pairs s;
+    __shared__ float s_part[NW][U];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     wait_for_stream();
     T *drows = static_cast<T *>(p.drows);
     if ((int)blockIdx.x >= p.token_blocks) {
-        const long long r = ((long long)((int)blockIdx.x - p.token_blocks) * NW + warp) * 32 + lane;
-        bool empty = r < p.R;
-        if (empty) {
-            const int t = load_in(p.tokens + r);
-            if ((unsigned)t < (unsigned)p.T)
-                for (int k = 0; k < p.K && empty; k++) empty = load_in(p.pos + (long long)t * p.K + k) != r;
-        }
-        unsigned todo = __ballot_sync(0xffffffffu, empty);
         Vec<T, V> z;
         z.zero();
-        while (todo) {
-            T *d = drows + (r - lane + __ffs(todo) - 1) * p.ldd;
-            todo &= todo - 1;
-            for (int c = V * lane; c < p.N; c += 32 * V) z.store(d + c);
-        }
+        empty_rows(p, [&](long long r) {
+            for (int c = V * lane; c < p.N; c += 32 * V) z.store(drows + r * p.ldd + c);
+        });
         return;
     }
     const long long t = blockIdx.x;
-    if (warp == 0) {
-        int pos = lane < p.K ? load_in(p.pos + t * p.K + lane) : -1;
-        if (pos >= p.R) pos = -1;
-        float w = lane < p.K ? (p.w ? load_in(p.w + t * p.K + lane) : 1.0f) : 0.0f;
-        const bool ours = pos >= 0 && load_in(p.tokens + pos) == t;
-        // a row that the token names twice: its first pair writes, with the sum of the weights
-        const unsigned same = __match_any_sync(0xffffffffu, pos >= 0 ? pos : (int)(0x80000000u | lane));
-        if (__ballot_sync(0xffffffffu, (same & (same - 1u)) != 0)) {
-            float sum = 0.0f;
-            for (int i = 0; i < 32; i++) {
-                const float o = __shfl_sync(0xffffffffu, w, i);
-                if (same >> i & 1u) sum += o;
-            }
-            w = sum;
-        }
-        s_pos[lane] = pos;
-        s_write[lane] = ours && lane == __ffs(same) - 1;
-        s_w[lane] = w;
-    }
+    if (warp == 0) token_pairs(p, t, lane, s);
     __syncthreads();
     const T *dy = static_cast<const T *>(p.dy) + t * p.lddy, *rows = static_cast<const T *>(p.rows);
     for (int k0 = 0; k0 < p.K; k0 += U) {
@@ -228,7 +337,7 @@ __global__ void __launch_bounds__(kCombGradThreads) combine_grad_kernel(const Co
             if (p.dw) {
 #pragma unroll
                 for (int u = 0; u < U; u++) {
-                    const int at = k0 + u < p.K ? s_pos[k0 + u] : -1;
+                    const int at = k0 + u < p.K ? s.pos[k0 + u] : -1;
                     if (at >= 0) r[u].load(rows + at * p.ld + c);
                     else r[u].zero();
                 }
@@ -236,19 +345,19 @@ __global__ void __launch_bounds__(kCombGradThreads) combine_grad_kernel(const Co
             g.get(d);
 #pragma unroll
             for (int u = 0; u < U; u++) {
-                if (k0 + u >= p.K || s_pos[k0 + u] < 0) continue;
+                if (k0 + u >= p.K || s.pos[k0 + u] < 0) continue;
                 float v[V];
                 if (p.dw) {
                     r[u].get(v);
 #pragma unroll
                     for (int k = 0; k < V; k++) dot[u] = fmaf(v[k], d[k], dot[u]);
                 }
-                if (p.drows && s_write[k0 + u]) {
-                    const float w = s_w[k0 + u];
+                if (p.drows && s.write[k0 + u]) {
+                    const float w = s.w[k0 + u];
 #pragma unroll
                     for (int k = 0; k < V; k++) v[k] = w * d[k];
                     r[u].set(v);
-                    r[u].store(drows + s_pos[k0 + u] * p.ldd + c);
+                    r[u].store(drows + s.pos[k0 + u] * p.ldd + c);
                 }
             }
         }
@@ -261,12 +370,83 @@ __global__ void __launch_bounds__(kCombGradThreads) combine_grad_kernel(const Co
             }
             __syncthreads();
             if (tid < U && k0 + tid < p.K) {
-                float s = s_part[0][tid];
+                float sum = s_part[0][tid];
 #pragma unroll
-                for (int i = 1; i < NW; i++) s += s_part[i][tid];
-                p.dw[t * p.K + k0 + tid] = s_pos[k0 + tid] >= 0 ? s : 0.0f;
+                for (int i = 1; i < NW; i++) sum += s_part[i][tid];
+                p.dw[t * p.K + k0 + tid] = s.pos[k0 + tid] >= 0 ? sum : 0.0f;
             }
             __syncthreads();
+        }
+    }
+}
+
+// The same for rows off 16-byte boundaries, each on its own: a warp a pair, in runs that begin on the boundaries of the
+// gradient's row (of the row where there is no gradient); ALIGNED: the row has the same.  8192 x 8 rows of 2047 bf16:
+// 135 us (one element at a time 243; the runs inside the rows on a path of their own, with the shift as a constant, 144).
+template <typename T, bool ALIGNED>
+__global__ void __launch_bounds__(kCombGradThreads) combine_grad_pieces_kernel(const CombineGradArgs p) {
+    constexpr int E = 16 / (int)sizeof(T), C = 4;      // runs in flight
+    __shared__ Pairs s;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    wait_for_stream();
+    T *drows = static_cast<T *>(p.drows);
+    if ((int)blockIdx.x >= p.token_blocks) {
+        empty_rows(p, [&](long long r) {
+            const float zero[E] = {};
+            T *d = drows + r * p.ldd;
+            for (int c = E * lane - off_boundary(d); c < p.N; c += 32 * E) store_run<T, E>(d, c, p.N, zero);
+        });
+        return;
+    }
+    const long long t = blockIdx.x;
+    if (warp == 0) token_pairs(p, t, lane, s);
+    __syncthreads();
+    const T *dy = static_cast<const T *>(p.dy) + t * p.lddy;
+    const Extent in = extent<T>(p.dy, p.T, p.lddy, p.N), of_rows = extent<T>(p.rows, p.R, p.ld, p.N);
+    for (int k = warp; k < p.K; k += kCombGradWarps) {
+        const long long at = s.pos[k];
+        const bool write = drows && at >= 0 && s.write[k];
+        float dot = 0.0f;
+        if (at >= 0 && (write || p.dw)) {
+            const T *row = static_cast<const T *>(p.rows) + at * p.ld;
+            T *d = drows + at * p.ldd;
+            const float w = s.w[k];
+            for (int c0 = E * lane - (drows ? off_boundary(d) : off_boundary(row)); c0 < p.N; c0 += 32 * E * C) {
+                Pieces<T, E, ALIGNED> r[C];
+                if (p.dw) {
+#pragma unroll
+                    for (int i = 0; i < C; i++)
+                        if (c0 + 32 * E * i < p.N) r[i].load(row, c0 + 32 * E * i, p.N, of_rows);
+                }
+#pragma unroll
+                for (int i = 0; i < C; i++) {
+                    const int c = c0 + 32 * E * i;
+                    if (c >= p.N) break;
+                    Pieces<T, E> g;
+                    float x[E], v[E];
+                    g.load(dy, c, p.N, in);
+                    g.get(x);
+                    if (p.dw) {
+                        r[i].get(v);
+                        const bool inside = c >= 0 && c + E <= p.N;
+                        float sum = 0.0f;       // of the run: few roundings on the way
+#pragma unroll
+                        for (int j = 0; j < E; j++)
+                            if (inside || (c + j >= 0 && c + j < p.N)) sum = fmaf(v[j], x[j], sum);
+                        dot += sum;
+                    }
+                    if (write) {
+#pragma unroll
+                        for (int j = 0; j < E; j++) v[j] = w * x[j];
+                        store_run<T, E>(d, c, p.N, v);
+                    }
+                }
+            }
+        }
+        if (p.dw) {
+#pragma unroll
+            for (int i = 16; i; i >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, i);
+            if (lane == 0) p.dw[t * p.K + k] = dot;
         }
     }
 }
@@ -496,19 +676,20 @@ cudaError_t launch_combine_forward(const void *rows, int dtype, long long ld, lo
         using X = decltype(rt);
         return by_dtype(y_dtype, [&](auto yt) {
             using Y = decltype(yt);
+            auto go = [&](auto kernel, int columns, int each) {       // columns of a warp
+                p.parts = (columns + each - 1) / each;
+                const long long blocks = ((long long)T * p.parts + kCombWarps - 1) / kCombWarps;
+                return blocks <= 0x7fffffff ? launch_early(kernel, (unsigned)blocks, 32 * kCombWarps, 0, st, 1, p) : cudaErrorInvalidConfiguration;
+            };
             auto fits = [&](int v) {
                 const int by = min(16, v * (int)sizeof(Y));
                 return N % v == 0 && runs_of(rows, ld, sizeof(X), min(16, v * (int)sizeof(X))) && runs_of(y, ldy, sizeof(Y), by) &&
                        (!add || runs_of(add, ldadd, sizeof(Y), by));
             };
-            auto go = [&](auto kernel, int each) {
-                p.parts = (N + 32 * each - 1) / (32 * each);
-                return launch_early(kernel, (unsigned)(((long long)T * p.parts + kCombWarps - 1) / kCombWarps), 32 * kCombWarps, 0, st, 1, p);
-            };
-            if (fits(8)) return go(combine_kernel<X, Y, 8, 1>, 8);
-            if (fits(2)) return go(combine_kernel<X, Y, 2, 4>, 8);
-            if constexpr (sizeof(X) == 2) return go(combine_shift_kernel<X, Y>, kShiftCols / 32);
-            else return go(combine_kernel<X, Y, 1, 8>, 8);
+            // pairs need no shifts (8192 x 8 rows of 2046 bf16: 68 us, in pieces 76; float32 113 and 124)
+            if (fits(8)) return go(combine_kernel<X, Y, 8, 1>, N, 8 * 32);
+            if (fits(2)) return go(combine_kernel<X, Y, 2, 4>, N, 8 * 32);
+            return go(combine_pieces_kernel<X, Y>, N + 16 / (int)sizeof(Y) - 1, (sizeof(X) == 4 && sizeof(Y) == 4 ? 4 : 8) * kPieceLanes);
         });
     });
 }
@@ -519,14 +700,12 @@ cudaError_t launch_combine_backward(const void *dy, int dtype, long long lddy, c
     const long long more = drows ? (R + kCombGradThreads - 1) / kCombGradThreads : 0;
     return by_dtype(dtype, [&](auto t) {
         using X = decltype(t);
-        auto fits = [&](int v) {
-            const int b = min(16, v * (int)sizeof(X));
-            return N % v == 0 && runs_of(dy, lddy, sizeof(X), b) && (!dw || runs_of(rows, ld, sizeof(X), b)) && (!drows || runs_of(drows, ldd, sizeof(X), b));
-        };
+        constexpr int el = (int)sizeof(X);
         auto go = [&](auto kernel) { return launch_early(kernel, (unsigned)(T + more), kCombGradThreads, 0, st, 1, p); };
-        if (fits(8)) return go(combine_grad_kernel<X, 8>);
-        if (fits(2)) return go(combine_grad_kernel<X, 2>);
-        return go(combine_grad_kernel<X, 1>);
+        if (N % 8 == 0 && runs_of(dy, lddy, el, 16) && (!dw || runs_of(rows, ld, el, 16)) && (!drows || runs_of(drows, ldd, el, 16)))
+            return go(combine_grad_kernel<X>);
+        const bool alike = !drows || !dw || ((reinterpret_cast<uintptr_t>(rows) - reinterpret_cast<uintptr_t>(drows)) % 16 == 0 && (ld - ldd) * el % 16 == 0);
+        return alike ? go(combine_grad_pieces_kernel<X, true>) : go(combine_grad_pieces_kernel<X, false>);
     });
 }
 

@@ -865,6 +865,36 @@ def test_combine_rows_named_twice_or_by_others(gpu, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("N", [1, 7, 17, 248, 257, 1030])
+def test_combine_rows_on_every_boundary(gpu, dtype, N):
+    """Rows, sums and gradients that start on different boundaries, the first and last rows of a tensor among the chosen ones."""
+    T, K = 9, 3
+    for shift in range(16 // rows_el(dtype)):
+        g = gen(N, shift)
+        tokens, pos = lists_of(gpu, T, 4, K, 1, shift, dropped=0.0)
+        R = tokens.numel()
+        rows = strided(torch.randn(R, N, generator=g).to(dtype), 0, shift)
+        dy = strided(torch.randn(T, N, generator=g).to(dtype), 1, 1)
+        w = torch.randn(T, K, generator=g).cuda()
+        for out_dtype in (F32, BF16):
+            more = strided(torch.randn(T, N, generator=g).to(out_dtype), 1, shift)
+            out = torch.full((T + 1, N + 3), 7.0, dtype=out_dtype, device="cuda")
+            check_combine(gpu, rows, pos, w, more, out_dtype=out_dtype, out=out[:T, 2:N + 2])
+            assert bool((out[:, :2] == 7).all()) and bool((out[:, N + 2:] == 7).all()) and bool((out[T] == 7).all())
+        same = torch.full((R * N + shift + 9,), 7.0, dtype=dtype, device="cuda")
+        check_combine_grad(gpu, dy, rows, pos, tokens, w, out=same[shift:shift + R * N].view(R, N))
+        assert bool((same[:shift] == 7).all()) and bool((same[shift + R * N:] == 7).all())
+        other = torch.full((R + 1, N + 2), 7.0, dtype=dtype, device="cuda")
+        check_combine_grad(gpu, dy, rows, pos, tokens, w, out=other[:R, 1:N + 1])
+        assert bool((other[:, :1] == 7).all()) and bool((other[:, N + 1:] == 7).all()) and bool((other[R] == 7).all())
+
+
+def rows_el(dtype):
+    return torch.finfo(dtype).bits // 8
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [F32, F16])
 @pytest.mark.parametrize("pad,shift", [(0, 1), (3, 0), (2, 2), (8, 8)])
 def test_combine_strided_rows(gpu, dtype, pad, shift):
