@@ -515,8 +515,8 @@ moe_status moe_fp8_wgrad(const uint8_t *xt, const float *xt_scale, const uint8_t
  * weights are the softmax over the chosen logits), else routed_scale p.  mask[T] (device, one byte per
  * token; NULL: none): tokens with 0 get the expert -1 and the weight 0, whatever their logits hold.
  * Keys are compared as their float64 values (without a bias as the logits themselves); the lower index
- * wins a tie; a NaN ranks with -infinity.  A token whose choice hangs on less than float32 tells, or on
- * very many equal keys, takes some microseconds more.
+ * wins a tie; a NaN ranks with -infinity.  A token whose choice hangs on less than float32 tells takes some
+ * microseconds more, one with very many equal keys about one.
  * Limits: E in 1..1024, top_k 1..min(E, 32), n_group 1..32, top_k <= topk_group E / n_group. */
 moe_status moe_route_forward(const void *logits, int32_t dtype, int64_t ld, int32_t T, int32_t n_experts,
                              const float *bias, int32_t top_k, int32_t score_func, int32_t n_group,
@@ -527,7 +527,8 @@ moe_status moe_route_forward(const void *logits, int32_t dtype, int64_t ld, int3
  * (dtype, rows ldd elements apart) from grad_w[T, K] (float32) and the choice topk_idx[T, K].  Entries of
  * topk_idx outside [0, E) have no weight (a masked token's row is zeros, whatever its logits hold); an
  * expert that stands twice in a row gets the sum of both gradients.  accumulate not 0: the gradient is
- * added to what dlogits holds (that of the balance loss, say), in float32, rounded once. */
+ * added to what dlogits holds (that of the balance loss, say), in float32, rounded once.  dlogits must not
+ * overlap logits. */
 moe_status moe_route_backward(const void *logits, int32_t dtype, int64_t ld, int32_t T, int32_t n_experts,
                               const int32_t *topk_idx, int32_t top_k, int32_t score_func, int32_t norm_topk,
                               float routed_scale, const float *grad_w, void *dlogits, int64_t ldd,
@@ -564,8 +565,8 @@ moe_status moe_norm_backward(const void *dy, int32_t dtype, int64_t lddy, const 
 /* The weighted sum of a token's rows: y[t] = sum_k topk_w[t, k] rows[pos[t, k]] + add[t] in float32, in the
  * order of k, rounded once to y's dtype.  rows[R, N] (dtype) the experts' outputs, pos[T, K] (int32) as
  * moe_expert_lists writes it: pairs with a value outside [0, R) are left out, so rows without a token are
- * never read.  topk_w NULL: 1; add[T, N] (y_dtype) NULL: none (it may be y itself).  N in 1..131072, K in
- * 1..32, T times ceil(N / 256) up to 2^33. */
+ * never read.  topk_w NULL: 1; add[T, N] (y_dtype) NULL: none (it may be y itself; rows must not overlap y).
+ * N in 1..131072, K in 1..32, T times ceil(N / 256) up to 2^33. */
 moe_status moe_combine_forward(const void *rows, int32_t dtype, int64_t ld, int32_t R, int32_t N, const int32_t *pos,
                                int32_t T, int32_t top_k, const float *topk_w, const void *add, int64_t ldadd, void *y,
                                int32_t y_dtype, int64_t ldy, void *stream);
@@ -573,8 +574,8 @@ moe_status moe_combine_forward(const void *rows, int32_t dtype, int64_t ld, int3
 /* Its gradients, from dy[T, N] (dtype, as rows): drows[R, N] (dtype) with drows[pos[t, k]] = topk_w[t, k] dy[t]
  * and dtopk_w[T, K] = rows[pos[t, k]] . dy[t] (0 for pairs without a row).  tokens[R] is the token of every
  * row (moe_expert_lists' `rows`): a row takes the gradient of its own token, with the sum of the weights
- * where that names it more than once; every other row gets zeros.  drows or dtopk_w may be NULL.  T up to
- * 2^30. */
+ * where that names it more than once; every other row gets zeros.  drows or dtopk_w may be NULL; drows must
+ * not overlap rows or dy.  T up to 2^30. */
 moe_status moe_combine_backward(const void *dy, int32_t dtype, int64_t lddy, const void *rows, int64_t ld, int32_t R,
                                 int32_t N, const int32_t *pos, int32_t T, int32_t top_k, const int32_t *tokens,
                                 const float *topk_w, void *drows, int64_t ldd, float *dtopk_w, void *stream);

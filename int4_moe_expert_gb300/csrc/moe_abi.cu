@@ -698,6 +698,7 @@ moe_status moe_route_backward(const void *logits, int32_t dtype, int64_t ld, int
     MOE_NEED(T == 0 || (topk_idx && grad_w && dlogits), MOE_ERR_INVALID, "topk_idx / grad_w / dlogits is NULL");
     MOE_NEED(aligned4(topk_idx) && aligned4(grad_w) && aligned_el(dlogits, dtype), MOE_ERR_INVALID, "a buffer is not aligned to its elements");
     if (T == 0) return MOE_OK;
+    MOE_NEED(dlogits != logits, MOE_ERR_INVALID, "dlogits is logits");
     return launched(moe::launch_route_backward(logits, dtype, ld, T, n_experts, topk_idx, top_k, score_func == MOE_SCORE_SOFTMAX, norm_topk,
                                                routed_scale, grad_w, dlogits, ldd, accumulate != 0, static_cast<cudaStream_t>(stream)),
                     "moe_route_backward");
@@ -781,6 +782,7 @@ moe_status moe_combine_forward(const void *rows, int32_t dtype, int64_t ld, int3
     MOE_NEED(ldy >= N && (!add || ldadd >= N), MOE_ERR_INVALID, "a row stride is less than N=%d", N);
     if (T == 0) return MOE_OK;
     MOE_NEED((rows || R == 0) && pos && y, MOE_ERR_INVALID, "rows / pos / y is NULL");
+    MOE_NEED(y != rows, MOE_ERR_INVALID, "y is rows");
     MOE_NEED(aligned_el(rows, dtype) && aligned_el(add, y_dtype) && aligned_el(y, y_dtype) && aligned4(pos) && aligned4(topk_w),
              MOE_ERR_INVALID, "a buffer is not aligned to its elements");
     return launched(moe::launch_combine_forward(rows, dtype, ld, R, N, pos, T, top_k, topk_w, add, ldadd, y, y_dtype, ldy,
@@ -799,6 +801,7 @@ moe_status moe_combine_backward(const void *dy, int32_t dtype, int64_t lddy, con
     MOE_NEED(aligned_el(dy, dtype) && aligned_el(rows, dtype) && aligned_el(drows, dtype) && aligned4(pos) && aligned4(tokens) &&
              aligned4(topk_w) && aligned4(dtopk_w), MOE_ERR_INVALID, "a buffer is not aligned to its elements");
     if ((T == 0 && (R == 0 || !drows)) || (!drows && !dtopk_w)) return MOE_OK;
+    MOE_NEED(!drows || (drows != rows && drows != dy), MOE_ERR_INVALID, "drows is rows or dy");
     return launched(moe::launch_combine_backward(dy, dtype, lddy, rows, ld, R, N, pos, T, top_k, tokens, topk_w, drows, ldd, dtopk_w,
                                                  static_cast<cudaStream_t>(stream)), "moe_combine_backward");
 }
