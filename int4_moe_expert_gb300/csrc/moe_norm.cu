@@ -30,6 +30,7 @@ struct NormArgs {
     float *scales;         // [blocks(H), T]
     int T, H, w_dtype;
     double eps;
+    float per_h, per_h_rest, eps32, eps_rest;      // 1 / H and eps in two parts
 };
 
 constexpr int kWarpRows = 4;       // rows of a block whose warps take a row each
@@ -210,7 +211,15 @@ __device__ __forceinline__ void norm_outputs(const NormArgs &p, long long t, int
     }
 }
 
-__device__ __forceinline__ float norm_rstd(const NormArgs &p, float ss) { return 1.0f / sqrtf(ss / (float)p.H + (float)p.eps); }
+// 1 / sqrt(ss / H + eps) with little more than its last rounding: the mean and the sum in two parts each, and one step
+// of Newton's from the function's value.  (An error here is one of the whole row, and of its codes near a rounding.)
+__device__ __forceinline__ float norm_rstd(const NormArgs &p, float ss) {
+    const float mean = ss * p.per_h, s = mean + p.eps32, back = s - mean;
+    if (!(s > 0x1p-100f && s < 0x1p100f)) return 1.0f / sqrtf(ss / (float)p.H + p.eps32);
+    const float rest = fmaf(ss, p.per_h, -mean) + fmaf(ss, p.per_h_rest, p.eps_rest) + ((mean - (s - back)) + (p.eps32 - back));
+    const float r = rsqrtf(s), q = s * r;
+    return fmaf(0.5f * r, fmaf(-q, r, 1.0f) - fmaf(rest, r, fmaf(s, r, -q)) * r, r);
+}
 
 template <typename T, typename S, int V, int N, int THREADS, int PER_SM, bool WARP>
 __global__ void __launch_bounds__(THREADS, PER_SM) norm_kernel(const NormArgs p) {
@@ -647,7 +656,7 @@ size_t norm_grad_workspace(int T, int H) { return (size_t)norm_grad_blocks(T, H)
 cudaError_t launch_norm_forward(const void *x, int dtype, long long ldx, const void *res, int s_dtype, long long ldr, const void *w, int w_dtype,
                                 int T, int H, double eps, void *h, long long ldh, void *y, long long ldy, float *rstd, uint8_t *codes,
                                 float *scales, cudaStream_t st) {
-    const NormArgs p = {x, res, w, ldx, ldr, ldh, ldy, h, y, rstd, codes, scales, T, H, w_dtype, eps};
+    const NormArgs p = {x, res, w, ldx, ldr, ldh, ldy, h, y, rstd, codes, scales, T, H, w_dtype, eps, (float)(1.0 / H), (float)(1.0 / H - (float)(1.0 / H)), (float)eps, (float)(eps - (float)eps)};
     auto go = [&](auto xt, auto stt) {
         using X = decltype(xt);
         using S = decltype(stt);
