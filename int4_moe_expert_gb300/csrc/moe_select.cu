@@ -18,7 +18,8 @@ namespace {
 // experts.  Maxima and candidates go by a fast sigmoid less a margin for its error; the candidates'
 // keys are computed again, one a lane.  The order is that of the float64 keys: where two neighbours of the
 // ranking are nearer than float32 tells, the whole warp ranks them in float64, and so the groups whose scores
-// are that near; with more candidates than lanes it ranks them, with more than 32 it does the row over.
+// are that near; with more candidates than lanes it ranks them, with more than 32 it does the row over (in float32
+// where ties are of the same logit and bias).
 // Bound by the issue of instructions (two thirds of the slots, half of the ALU's; about 600 for the two tokens of a
 // warp, of which 200 for scores, 180 for candidates and their keys, 160 for sort and ranking): 65536 x 256 float32
 // 27 us (10.5 to move the bytes), 16381 x 256 bf16 in 8 groups 14 us, 32768 x 64 bf16 softmax 12 us.  More blocks
@@ -140,6 +141,53 @@ __device__ __noinline__ void choose64(const char *row, int dtype, const float *b
     }
 }
 
+// The same in float32, K rounds over the order of the keys as integers: for rows with too many candidates, most of them
+// equal.  `kept`: a bit for each group's first lane (1 << sub lanes a group).  False: the choice hangs on neighbours
+// that float32 does not tell apart and that are not the same logit and bias, or a kept group has a NaN.
+__device__ __noinline__ bool choose32(const char *row, int dtype, const float *bias, int E, int K, unsigned kept, unsigned group_of, int sub, float *x,
+                                      unsigned *order, Chosen *out) {
+    const int lane = threadIdx.x & 31;
+    bool unsure = false;
+    auto key_of = [](unsigned o) { return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o); };
+    for (int e = lane; e < E; e += 32) {
+        x[e] = load_el(row, dtype, e);
+        float v = (bias ? sigmoid_fast(x[e]) + bias[e] : x[e]) + 0.0f;
+        const bool in = kept >> (((unsigned)e * group_of >> 20) << sub) & 1u;
+        unsure |= isnan(v) && in && kept != ~0u;       // its group was chosen with a score that is not the formula's
+        if (isnan(v) || !in) v = -INFINITY;
+        const unsigned bits = __float_as_uint(v);
+        order[e] = bits ^ ((unsigned)((int)bits >> 31) | 0x80000000u);
+    }
+    __syncwarp();
+    // not surely below u, and neither both infinite nor the same
+    auto near = [&](float u, float v, int a, int b) {
+        return !(u - v > 2.0f * key_error(u)) && !(u == v && isinf(u)) && !(x[a] == x[b] && bias[a] == bias[b]);
+    };
+    float last = 0.0f;
+    int last_at = -1;
+    for (int k = 0; k < K; k++) {
+        unsigned best = 0;
+        int at = 0x7fffffff;
+        for (int e = lane; e < E; e += 32)
+            if (order[e] > best) {       // what was taken is 0
+                best = order[e];
+                at = e;
+            }
+        const unsigned top = __reduce_max_sync(0xffffffffu, best);
+        at = __reduce_min_sync(0xffffffffu, best == top ? at : 0x7fffffff);
+        const float v = key_of(top);
+        if (bias && k > 0) unsure |= near(last, v, last_at, at);
+        last = v;
+        last_at = at;
+        if (lane == 0) out[k] = {at, x[at], v, bias ? bias[at] : 0.0f};
+        if (lane == (at & 31)) order[at] = 0;
+        __syncwarp();
+    }
+    if (bias)
+        for (int e = lane; e < E; e += 32) unsure |= order[e] != 0 && near(last, key_of(order[e]), last_at, e);
+    return !__any_sync(0xffffffffu, unsure);
+}
+
 // J experts a lane in runs of V, LPT lanes a token; BIAS: keys sigmoid(l) + bias, else the logits
 template <bool BIAS_, int J_, int LPT_, int V_, bool FULL_ = false>
 struct RouteLay {
@@ -196,7 +244,8 @@ __global__ void __launch_bounds__(kRouteThreads, L::PER_SM) route_kernel(const R
         };
         logits();
         const bool scores = BIAS || p.groups > 1;
-        bool slow = false;
+        bool slow = false, hard = false;      // rows done over: in float32, or at once in float64
+        unsigned kept = ~0u;
         if (scores) {
 #pragma unroll
             for (int j = 0; j < J; j += V) {
@@ -273,7 +322,8 @@ __global__ void __launch_bounds__(kRouteThreads, L::PER_SM) route_kernel(const R
             }
             // a group's NaN or infinite score: the whole row in float64
             const bool odd = valid && !(fabsf(best) + err < INFINITY);
-            slow = (__ballot_sync(0xffffffffu, odd) >> (g * LPT) & lanes) != 0;
+            hard = (__ballot_sync(0xffffffffu, odd) >> (g * LPT) & lanes) != 0;
+            slow = hard;
             // between the last kept and the first other: those groups' sums in float64, by all lanes
             const bool doubt = p.kept < p.groups && !slow && on && lo <= hi && valid && part == 0 && best + err >= lo && best - err <= hi;
             unsigned doubts = __ballot_sync(0xffffffffu, doubt);
@@ -306,7 +356,7 @@ __global__ void __launch_bounds__(kRouteThreads, L::PER_SM) route_kernel(const R
                 }
                 if (doubt) keep = ahead < places;
             }
-            const unsigned kept = __ballot_sync(0xffffffffu, keep) >> (g * LPT) & lanes;      // a group's first lane counts
+            kept = __ballot_sync(0xffffffffu, keep) >> (g * LPT) & lanes;      // a group's first lane counts
             if constexpr (!BIAS) logits();
             if (V > 1 && p.per_group % V == 0) {
 #pragma unroll
@@ -404,9 +454,11 @@ __global__ void __launch_bounds__(kRouteThreads, L::PER_SM) route_kernel(const R
         }
         Chosen c = s_sel[warp][g][l];
         if constexpr (BIAS) {
-            // neighbours that float32 does not tell apart; the same logit and bias are equal
-            const float below = __shfl_down_sync(0xffffffffu, c.key, 1, LPT);
-            const bool tight = one && l < p.K && l + 1 < n && !(c.key - below > 2.0f * key_error(c.key));
+            // neighbours that float32 does not tell apart, down to the last that is that near to the K-th; the same logit and
+            // bias are equal
+            const float below = __shfl_down_sync(0xffffffffu, c.key, 1, LPT), last = __shfl_sync(0xffffffffu, c.key, p.K - 1, LPT);
+            const float margin = 2.0f * key_error(c.key);
+            const bool tight = one && l + 1 < n && !(c.key - below > margin) && (l < p.K || !(last - c.key > margin));
             if (__any_sync(0xffffffffu, tight)) {
                 const float x = __shfl_down_sync(0xffffffffu, c.x, 1, LPT), b = __shfl_down_sync(0xffffffffu, c.bias, 1, LPT);
                 again |= __ballot_sync(0xffffffffu, tight && !(c.x == x && c.bias == b));
@@ -448,9 +500,17 @@ __global__ void __launch_bounds__(kRouteThreads, L::PER_SM) route_kernel(const R
         }
         again = __ballot_sync(0xffffffffu, slow && on && l == 0);
         while (again) {
-            const int r = (__ffs(again) - 1) / LPT;
+            const int first = __ffs(again) - 1, r = first / LPT;
             again &= again - 1;
-            choose64(row_of(t0 + r), p.dtype, BIAS ? bias : nullptr, p.E, p.K, p.groups, p.kept, p.group_of, key64, s_sel[warp][r]);
+            const unsigned groups_kept = __shfl_sync(0xffffffffu, kept, first);
+            const bool at_once = __shfl_sync(0xffffffffu, (int)hard, first) != 0;
+            const char *other = row_of(t0 + r);
+            float *x = reinterpret_cast<float *>(key64);
+            if (at_once || !choose32(other, p.dtype, BIAS ? bias : nullptr, p.E, p.K, groups_kept, p.groups > 1 ? p.group_of : 0u, p.sub, x,
+                                     reinterpret_cast<unsigned *>(x + p.E), s_sel[warp][r])) {
+                __syncwarp();
+                choose64(other, p.dtype, BIAS ? bias : nullptr, p.E, p.K, p.groups, p.kept, p.group_of, key64, s_sel[warp][r]);
+            }
             __syncwarp();
         }
         if (redo) c = s_sel[warp][g][l];

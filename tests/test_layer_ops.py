@@ -182,6 +182,14 @@ def test_grad_refusals(moe):
     assert L.moe_grad_norm_workspace(-1) == L.moe_grad_norm_workspace(65537) == 0 < L.moe_grad_norm_workspace(0) < L.moe_grad_norm_workspace(600)
 
 
+def test_outputs_on_top_of_what_others_read_are_refused(moe):
+    L, Q = moe.lib(), P + 4096
+    assert L.moe_route_backward(P, 0, 8, 4, 8, Q, 2, 0, 1, 1.0, Q, P, 8, 0, None) == moe.MOE_ERR_INVALID
+    assert L.moe_combine_forward(P, 0, 8, 4, 8, Q, 4, 2, Q, None, 0, P, 0, 8, None) == moe.MOE_ERR_INVALID
+    assert L.moe_combine_backward(Q, 0, 8, P, 8, 4, 8, Q, 4, 2, Q, Q, P, 8, Q, None) == moe.MOE_ERR_INVALID
+    assert L.moe_combine_backward(P, 0, 8, Q, 8, 4, 8, Q, 4, 2, Q, Q, P, 8, Q, None) == moe.MOE_ERR_INVALID
+
+
 def test_binding_refuses_what_is_not_on_the_device(moe):
     x, i = torch.zeros(2, 16), torch.zeros(2, 1, dtype=torch.int32)
     for call in (lambda: moe.moe_route_forward(x, 1), lambda: moe.moe_norm_forward(x), lambda: moe.moe_combine_forward(x, i),
@@ -323,6 +331,42 @@ def test_route_groups_of_every_layout(gpu, E, G, dtype, shift):
             assert torch.equal(idx.cpu().long(), ref), (kept, (idx.cpu() != ref).nonzero()[:4])
             ok = ~torch.isnan(want)
             assert bool(((w.cpu().double() - want)[ok].abs() <= 2.0 ** -20 * want[ok] + 1e-30).all()) and torch.equal(torch.isnan(w.cpu()), ~ok)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E,K,G,dtype", [(64, 6, 1, F32), (256, 8, 1, BF16), (256, 8, 8, F32), (1000, 32, 1, F32), (96, 4, 4, F16), (40, 8, 1, F32), (33, 33 - 1, 1, F32)])
+def test_route_many_equal_keys(gpu, E, K, G, dtype):
+    """Rows with more equal keys than a warp has lanes: of one logit, of few, with infinities, NaN, and neighbours that float32 does not tell apart."""
+    T = 24
+    g = gen(E, K, G)
+    x = torch.zeros(T, E)
+    x[1] = -3.5
+    x[2] = torch.randint(0, 2, (E,), generator=g).float()
+    x[3] = torch.randint(0, 3, (E,), generator=g).float() - 40.0
+    x[4, E // 2:] = -inf
+    x[5, ::3] = nan
+    x[6, 3] = inf
+    x[7] = nan
+    x[8] = -inf
+    x[9, 1::2] = -0.0
+    x[10, E - K // 2:] = 2.0
+    x[11] = torch.randn(E, generator=g)
+    x[12] = 90.0                                       # a sigmoid of 1
+    x[13] = (torch.arange(E) % 2) * 1e-6
+    x[14, :5] = inf
+    x = x.to(dtype)
+    off = torch.zeros(E)
+    off[torch.randperm(E, generator=g)[K // 2:]] = -inf          # fewer experts than choices
+    lone = torch.zeros(E)
+    lone[E - 1] = inf
+    step = (0.25 + 2.0 ** -26 * torch.randint(0, 3, (E,), generator=g).double()).float()
+    for score, bias in ((0, None), (1, None), (0, torch.zeros(E)), (0, off), (0, lone), (0, step), (0, torch.full((E,), nan))):
+        for kept in sorted({1, G}) if score == 0 else (1,):
+            if K > kept * (E // G) or (score == 1 and G > 1):
+                continue
+            idx, _ = gpu.moe_route_forward(x.cuda(), K, bias=None if bias is None else bias.cuda(), score_func=score, n_group=G, topk_group=kept)
+            ref, _ = route_ref(x, K, bias=bias, score=score, G=G, kept=kept)
+            assert torch.equal(idx.cpu().long(), ref), (score, kept, (idx.cpu() != ref).nonzero()[:4])
 
 
 @pytest.mark.gpu
