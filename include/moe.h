@@ -514,6 +514,7 @@ moe_status moe_fp8_wgrad(const uint8_t *xt, const float *xt_scale, const uint8_t
  * w = routed_scale p / (sum of the chosen p + 1e-20) with norm_topk (the softmax needs no such term: its
  * weights are the softmax over the chosen logits), else routed_scale p.  mask[T] (device, one byte per
  * token; NULL: none): tokens with 0 get the expert -1 and the weight 0, whatever their logits hold.
+ * (A p below 2^-126 counts as 0.)
  * Keys are compared as their float64 values (without a bias as the logits themselves); the lower index
  * wins a tie; a NaN ranks with -infinity.  A token whose choice hangs on less than float32 tells takes some
  * microseconds more, one with very many equal keys about one.
