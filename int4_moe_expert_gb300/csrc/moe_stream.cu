@@ -30,21 +30,22 @@ struct CombineArgs {
     int T, K, N, parts;      // parts: warps of a token
 };
 
-template <typename T, typename Y, int V, int C>
+template <typename T, typename Y>
 __global__ void __launch_bounds__(32 * kCombWarps) combine_kernel(const CombineArgs p) {
+    constexpr int V = 8;
     const int lane = threadIdx.x & 31;
     const long long job = (long long)blockIdx.x * kCombWarps + (threadIdx.x >> 5);
     wait_for_stream();
     const long long t = job / p.parts;
     if (t >= p.T) return;
-    const int base = (int)(job - t * p.parts) * (32 * V * C) + V * lane;
+    const int c = ((int)(job - t * p.parts) * 32 + lane) * V;
     int pos = lane < p.K ? load_in(p.pos + t * p.K + lane) : -1;
     const float wt = lane < p.K ? (p.w ? load_in(p.w + t * p.K + lane) : 1.0f) : 0.0f;
     if (pos >= p.R) pos = -1;
-    float acc[C][V] = {};
+    float acc[V] = {};
     constexpr int U = 4;       // pairs in flight
     for (int k0 = 0; k0 < p.K; k0 += U) {
-        Vec<T, V> r[U][C];
+        Vec<T, V> r[U];
         float w[U];
         bool on[U];
 #pragma unroll
@@ -52,40 +53,29 @@ __global__ void __launch_bounds__(32 * kCombWarps) combine_kernel(const CombineA
             const int k = min(k0 + u, 31), at = __shfl_sync(0xffffffffu, pos, k);
             w[u] = __shfl_sync(0xffffffffu, wt, k);
             on[u] = k0 + u < p.K && at >= 0;
-#pragma unroll
-            for (int i = 0; i < C; i++) {
-                const int c = base + 32 * V * i;
-                if (on[u] && c < p.N) r[u][i].load(static_cast<const T *>(p.rows) + at * p.ld + c);
-                else r[u][i].zero();
-            }
+            if (on[u] && c < p.N) r[u].load(static_cast<const T *>(p.rows) + at * p.ld + c);
+            else r[u].zero();
         }
 #pragma unroll
         for (int u = 0; u < U; u++) {
             if (!on[u]) continue;
+            float v[V];
+            r[u].get(v);
 #pragma unroll
-            for (int i = 0; i < C; i++) {
-                float v[V];
-                r[u][i].get(v);
-#pragma unroll
-                for (int k = 0; k < V; k++) acc[i][k] = fmaf(w[u], v[k], acc[i][k]);
-            }
+            for (int k = 0; k < V; k++) acc[k] = fmaf(w[u], v[k], acc[k]);
         }
     }
+    if (c >= p.N) return;
+    Vec<Y, V> o;
+    if (p.add) {
+        float v[V];
+        o.load(static_cast<const Y *>(p.add) + t * p.ldadd + c);
+        o.get(v);
 #pragma unroll
-    for (int i = 0; i < C; i++) {
-        const int c = base + 32 * V * i;
-        if (c >= p.N) continue;
-        Vec<Y, V> o;
-        if (p.add) {
-            float u[V];
-            o.load(static_cast<const Y *>(p.add) + t * p.ldadd + c);
-            o.get(u);
-#pragma unroll
-            for (int k = 0; k < V; k++) acc[i][k] += u[k];
-        }
-        o.set(acc[i]);
-        o.store(static_cast<Y *>(p.y) + t * p.ldy + c);
+        for (int k = 0; k < V; k++) acc[k] += v[k];
     }
+    o.set(acc);
+    o.store(static_cast<Y *>(p.y) + t * p.ldy + c);
 }
 
 // E elements of a row from column c on, whatever the boundary: the 16-byte pieces that hold them, shifted to their
@@ -170,13 +160,13 @@ __device__ __forceinline__ Extent extent(const void *x, long long rows, long lon
 }
 
 // Rows that start off 16-byte boundaries or end off a run: the same, in runs that begin on the boundaries of y.  A lane
-// loads the pieces that begin in its run and takes the one behind from the next lane, so that 31 lanes have a run:
-// eight pairs in flight (8192 x 8 rows of 2047 bf16: 76 us; single elements through shared memory 105, single loads
-// 153).
+// loads the 8-byte pieces that begin in its run and takes the words behind from the next lane, so that 31 lanes have a
+// run; what is left of the shift is a word and a half.  8192 x 8 rows of 2047 bf16: 66 us (16-byte pieces, whose words
+// are three selections from their place, 76; single elements 153).
 template <typename T, typename Y>
-__global__ void __launch_bounds__(32 * kCombWarps, 4) combine_pieces_kernel(const CombineArgs p) {
+__global__ void __launch_bounds__(32 * kCombWarps, sizeof(T) > sizeof(Y) ? 4 : 5) combine_pieces_kernel(const CombineArgs p) {
     constexpr int E = sizeof(T) == 4 && sizeof(Y) == 4 ? 4 : 8, W = E * (int)sizeof(T) / 4;
-    constexpr int U = W == 4 ? 8 : 4;       // pairs in flight
+    constexpr int U = 4;       // pairs in flight
     const int lane = threadIdx.x & 31;
     const long long job = (long long)blockIdx.x * kCombWarps + (threadIdx.x >> 5);
     wait_for_stream();
@@ -184,50 +174,61 @@ __global__ void __launch_bounds__(32 * kCombWarps, 4) combine_pieces_kernel(cons
     if (t >= p.T) return;
     Y *y = static_cast<Y *>(p.y) + t * p.ldy;
     const int c = ((int)(job - t * p.parts) * kPieceLanes + lane) * E - off_boundary(y);
-    int pos = lane < p.K ? load_in(p.pos + t * p.K + lane) : -1;
+    const int pos = lane < p.K ? load_in(p.pos + t * p.K + lane) : -1;
     const float wt = lane < p.K ? (p.w ? load_in(p.w + t * p.K + lane) : 1.0f) : 0.0f;
-    if (pos >= p.R) pos = -1;
+    const bool has = pos >= 0 && pos < p.R;
+    const unsigned on = __ballot_sync(0xffffffffu, has);
+    const unsigned long long row = (unsigned long long)reinterpret_cast<uintptr_t>(static_cast<const T *>(p.rows) + (has ? pos : 0) * p.ld);
+    // rows next to the tensor's ends, where pieces may lie partly outside it
+    const bool ends = __any_sync(0xffffffffu, has && (pos * p.ld < 64 || (p.R - 1 - pos) * p.ld < 64));
     const Extent x = extent<T>(p.rows, p.R, p.ld, p.N);
+    const bool wanted = c - E < p.N;
+    const int by = c * (int)sizeof(T);
     float acc[E] = {};
     for (int k0 = 0; k0 < p.K; k0 += U) {
         uint32_t r[U][W];
 #pragma unroll
         for (int u = 0; u < U; u++) {
-            const int at = __shfl_sync(0xffffffffu, pos, min(k0 + u, 31));
+            const uintptr_t q = (uintptr_t)(__shfl_sync(0xffffffffu, row, k0 + u) + by) & ~(uintptr_t)7;
 #pragma unroll
-            for (int i = 0; i < W; i++) r[u][i] = 0;
-            if (k0 + u >= p.K || at < 0 || c - E >= p.N) continue;
-            const uintptr_t q = (reinterpret_cast<uintptr_t>(static_cast<const T *>(p.rows) + at * p.ld) + (intptr_t)c * (int)sizeof(T)) & ~(uintptr_t)15;
-            if (q >= x.first && q + 4 * W <= x.end) {
+            for (int i = 0; i < W; i += 2) {
+                uint2 v = make_uint2(0, 0);
+                if (wanted && on >> (k0 + u) & 1u && (!ends || (q + 4 * i >= x.first && q + 4 * i + 8 <= x.end)))
+                    v = load_in(reinterpret_cast<const uint2 *>(q) + i / 2);
+                r[u][i] = v.x;
+                r[u][i + 1] = v.y;
+            }
+        }
+        if (ends) {
 #pragma unroll
-                for (int i = 0; i < W; i += 4) {
-                    const uint4 v = load_in(reinterpret_cast<const uint4 *>(q) + i / 4);
-                    r[u][i] = v.x;
-                    r[u][i + 1] = v.y;
-                    r[u][i + 2] = v.z;
-                    r[u][i + 3] = v.w;
+            for (int u = 0; u < U; u++) {
+                const uintptr_t q = (uintptr_t)(__shfl_sync(0xffffffffu, row, k0 + u) + by) & ~(uintptr_t)7;
+                if (!wanted || !(on >> (k0 + u) & 1u)) continue;
+#pragma unroll
+                for (int i = 0; i < 4 * W; i += (int)sizeof(T)) {
+                    const uintptr_t at = q + i, piece = q + (i & ~7);
+                    if (at < x.first || at >= x.end || (piece >= x.first && piece + 8 <= x.end)) continue;
+                    if constexpr (sizeof(T) == 2) r[u][i / 4] |= (unsigned)load_in(reinterpret_cast<const unsigned short *>(at)) << (8 * (i & 2));
+                    else r[u][i / 4] = load_in(reinterpret_cast<const unsigned *>(at));
                 }
-            } else {       // partly outside the tensor
-#pragma unroll
-                for (int i = 0; i < 4 * W; i += (int)sizeof(T))
-                    if (q + i >= x.first && q + i < x.end) {
-                        if constexpr (sizeof(T) == 2) r[u][i / 4] |= (unsigned)load_in(reinterpret_cast<const unsigned short *>(q + i)) << (8 * (i & 2));
-                        else r[u][i / 4] = load_in(reinterpret_cast<const unsigned *>(q + i));
-                    }
             }
         }
 #pragma unroll
         for (int u = 0; u < U; u++) {
-            const int k = min(k0 + u, 31), at = __shfl_sync(0xffffffffu, pos, k);
-            const float w = __shfl_sync(0xffffffffu, wt, k);
-            if (k0 + u >= p.K || at < 0) continue;
-            Pieces<T, E> o;
-            o.s = (unsigned)(reinterpret_cast<uintptr_t>(static_cast<const T *>(p.rows) + at * p.ld) + (intptr_t)c * (int)sizeof(T)) & 15u;
+            if (!(on >> (k0 + u) & 1u)) continue;
+            const float w = __shfl_sync(0xffffffffu, wt, k0 + u);
+            const unsigned s = (unsigned)__shfl_sync(0xffffffffu, (unsigned)row, k0 + u) + (unsigned)by;      // the same boundary in all lanes
+            const uint32_t next = __shfl_down_sync(0xffffffffu, r[u][0], 1), after = sizeof(T) == 2 ? __shfl_down_sync(0xffffffffu, r[u][1], 1) : 0u;
+            uint32_t b[W + 1];
 #pragma unroll
-            for (int i = 0; i < W; i++) o.w[i] = r[u][i];
-#pragma unroll
-            for (int i = 0; i < 4; i++) o.w[W + i] = __shfl_down_sync(0xffffffffu, r[u][i], 1);
+            for (int i = 0; i <= W; i++) {
+                const uint32_t here = i < W ? r[u][i] : next, behind = i + 1 < W ? r[u][i + 1] : i + 1 == W ? next : after;
+                b[i] = s & 4u ? behind : here;
+            }
+            Vec<T, E> o;
             float v[E];
+#pragma unroll
+            for (int i = 0; i < W; i++) o.w[i] = sizeof(T) == 4 ? b[i] : __funnelshift_r(b[i], b[i + 1], 8u * (s & 2u));
             o.get(v);
 #pragma unroll
             for (int i = 0; i < E; i++) acc[i] = fmaf(w, v[i], acc[i]);
@@ -684,14 +685,8 @@ cudaError_t launch_combine_forward(const void *rows, int dtype, long long ld, lo
                 const long long blocks = ((long long)T * p.parts + kCombWarps - 1) / kCombWarps;
                 return blocks <= 0x7fffffff ? launch_early(kernel, (unsigned)blocks, 32 * kCombWarps, 0, st, 1, p) : cudaErrorInvalidConfiguration;
             };
-            auto fits = [&](int v) {
-                const int by = min(16, v * (int)sizeof(Y));
-                return N % v == 0 && runs_of(rows, ld, sizeof(X), min(16, v * (int)sizeof(X))) && runs_of(y, ldy, sizeof(Y), by) &&
-                       (!add || runs_of(add, ldadd, sizeof(Y), by));
-            };
-            // pairs need no shifts (8192 x 8 rows of 2046 bf16: 68 us, in pieces 76; float32 113 and 124)
-            if (fits(8)) return go(combine_kernel<X, Y, 8, 1>, N, 8 * 32);
-            if (fits(2)) return go(combine_kernel<X, Y, 2, 4>, N, 8 * 32);
+            if (N % 8 == 0 && runs_of(rows, ld, sizeof(X), 16) && runs_of(y, ldy, sizeof(Y), 16) && (!add || runs_of(add, ldadd, sizeof(Y), 16)))
+                return go(combine_kernel<X, Y>, N, 8 * 32);
             return go(combine_pieces_kernel<X, Y>, N + 16 / (int)sizeof(Y) - 1, (sizeof(X) == 4 && sizeof(Y) == 4 ? 4 : 8) * kPieceLanes);
         });
     });
