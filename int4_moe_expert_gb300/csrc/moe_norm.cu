@@ -17,8 +17,9 @@ namespace {
 // The e4m3 codes are those of y; with 8 neighbours a lane, 16 lanes hold a 1 x 128 block.  A block's scale steps where its
 // largest magnitude passes 448 times a power of two: a row with a block that is nearer to that than
 // float32's error has its sum of squares done over in float64, so the scales are those of the formula.
-// 32768 x 2048 bf16 on a float32 stream: 117 us at the copy rate; 16381 x 6144 bf16 with values and codes 151 us of
-// 134 (two thirds of the issue slots: codes and scales).  Rows of odd widths go element by element, at a third of it.
+// 32768 x 2048 bf16 on a float32 stream: 117 us at the copy rate; 16381 x 6144 bf16 with values and codes 142 us of
+// 134 (two thirds of the issue slots: codes and scales).  Rows of odd widths go element by element: 8192 x 4095 bf16
+// 58 us of 40, f32 82 us of 79.
 // ---------------------------------------------------------------------------
 
 struct NormArgs {
@@ -224,61 +225,62 @@ __device__ __forceinline__ float norm_rstd(const NormArgs &p, float ss) {
 template <typename T, typename S, int V, int N, int THREADS, int PER_SM, bool WARP>
 __global__ void __launch_bounds__(THREADS, PER_SM) norm_kernel(const NormArgs p) {
     constexpr int C = N / V;
-    __shared__ float s_sum[2][32];
-    const int tid = WARP ? threadIdx.x & 31 : threadIdx.x, nt = WARP ? 32 : blockDim.x;
+    // weights on their way during the sum; not beside four bytes an element of x (8192 x 6144 f32: 125 us so, 118 behind it)
+    constexpr bool EARLY = sizeof(T) == 2;
+    __shared__ float s_sum[32];
+    const int tid = WARP ? threadIdx.x & 31 : threadIdx.x, nt = WARP ? 32 : V < 8 && N == 16 ? THREADS : blockDim.x;
     const int per = WARP ? kWarpRows : 1;
     wait_for_stream();
-    int turn = 0;
-    for (long long t = (long long)blockIdx.x * per + (WARP ? threadIdx.x >> 5 : 0); t < p.T; t += (long long)gridDim.x * per) {
-        float v[N];
-        Weights<T, V, C> wt;       // on their way during the sum
-        {
-            Vec<T, V> a[C];
-            const T *x = static_cast<const T *>(p.x) + t * p.ldx;
+    const long long t = (long long)blockIdx.x * per + (WARP ? threadIdx.x >> 5 : 0);
+    if (t >= p.T) return;      // a warp without a row
+    float v[N];
+    Weights<T, V, C> wt;
+    {
+        Vec<T, V> a[C];
+        const T *x = static_cast<const T *>(p.x) + t * p.ldx;
+#pragma unroll
+        for (int i = 0; i < C; i++) {
+            const int c = V * (tid + nt * i);
+            a[i].zero();
+            if (c < p.H) a[i].load(x + c);
+        }
+        if (EARLY && p.w) wt.load(p.w, p.w_dtype, tid, nt, p.H);
+        if (p.res) {
+            Vec<S, V> b[C];
+            const S *res = static_cast<const S *>(p.res) + t * p.ldr;
+            S *h = static_cast<S *>(p.h) + t * p.ldh;
 #pragma unroll
             for (int i = 0; i < C; i++) {
                 const int c = V * (tid + nt * i);
-                a[i].zero();
-                if (c < p.H) a[i].load(x + c);
+                b[i].zero();
+                if (c < p.H) b[i].load(res + c);
             }
-            if (p.w) wt.load(p.w, p.w_dtype, tid, nt, p.H);
-            if (p.res) {
-                Vec<S, V> b[C];
-                const S *res = static_cast<const S *>(p.res) + t * p.ldr;
-                S *h = static_cast<S *>(p.h) + t * p.ldh;
 #pragma unroll
-                for (int i = 0; i < C; i++) {
-                    const int c = V * (tid + nt * i);
-                    b[i].zero();
-                    if (c < p.H) b[i].load(res + c);
-                }
+            for (int i = 0; i < C; i++) {
+                const int c = V * (tid + nt * i);
+                float u[V];
+                a[i].get(&v[V * i]);
+                b[i].get(u);
 #pragma unroll
-                for (int i = 0; i < C; i++) {
-                    const int c = V * (tid + nt * i);
-                    float u[V];
-                    a[i].get(&v[V * i]);
-                    b[i].get(u);
-#pragma unroll
-                    for (int k = 0; k < V; k++) u[k] += v[V * i + k];
-                    b[i].set(u);
-                    b[i].get(&v[V * i]);
-                    if (c < p.H) b[i].store(h + c);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < C; i++) a[i].get(&v[V * i]);
+                for (int k = 0; k < V; k++) u[k] += v[V * i + k];
+                b[i].set(u);
+                b[i].get(&v[V * i]);
+                if (c < p.H) b[i].store(h + c);
             }
+        } else {
+#pragma unroll
+            for (int i = 0; i < C; i++) a[i].get(&v[V * i]);
         }
-        float ss = 0.0f;
-#pragma unroll
-        for (int i = 0; i < N; i++) ss = fmaf(v[i], v[i], ss);
-        ss = sum_all<WARP>(ss, s_sum[turn]);
-        if (WARP) __syncwarp();      // the row's h is written, for all lanes
-        turn ^= 1;
-        const float r = norm_rstd(p, ss);
-        if (tid == 0 && p.rstd) p.rstd[t] = r;
-        norm_outputs<T, S, V, N>(p, t, tid, nt, v, r, wt);
     }
+    float ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; i++) ss = fmaf(v[i], v[i], ss);
+    ss = sum_all<WARP>(ss, s_sum);
+    if (WARP) __syncwarp();      // the row's h is written, for all lanes
+    const float r = norm_rstd(p, ss);
+    if (!EARLY && p.w) wt.load(p.w, p.w_dtype, tid, nt, p.H);
+    if (tid == 0 && p.rstd) p.rstd[t] = r;
+    norm_outputs<T, S, V, N>(p, t, tid, nt, v, r, wt);
 }
 
 // Gradient.  n = h r, d = dy w: dh = (d - n mean(d n)) r + grad_h, dw = sum over the tokens of dy n.
@@ -666,7 +668,7 @@ cudaError_t launch_norm_forward(const void *x, int dtype, long long ldx, const v
                    (!y || runs_of(y, ldy, sizeof(X), min(16, v * (int)sizeof(X)))) && (!w || runs_of(w, 0, 4, min(16, v * (w_dtype == MOE_DTYPE_F32 ? 4 : 2))));
         };
         auto run = [&](auto kernel, int threads, int rows) {
-            return launch_early(kernel, (unsigned)((T + rows - 1) / rows), threads, 0, st, 1, p);
+            return launch_early(kernel, (unsigned)(((long long)T + rows - 1) / rows), threads, 0, st, 1, p);
         };
         auto up = [](int n) { return (n + 31) / 32 * 32; };
         const int few = up((H + 7) / 8), threads = up((H + 15) / 16);      // with 8 and 16 elements a thread
@@ -674,12 +676,17 @@ cudaError_t launch_norm_forward(const void *x, int dtype, long long ldx, const v
             constexpr int V = decltype(v)::value;
             if (H <= 256) return run(norm_kernel<X, S, V, 8, 32 * kWarpRows, 8, true>, 32 * kWarpRows, kWarpRows);
             if (T < 2 * sm_count() && H <= 8192) return run(norm_kernel<X, S, V, 8, 1024, 1, false>, few, 1);
-            // 64 registers a thread, 56 for 384 threads (three blocks: 16381 x 6144 with codes 155 us, with two 165); single
-            // elements need 85, for their addresses
-            if (threads <= 128) return run(norm_kernel<X, S, V, 16, 128, V == 1 ? 6 : 8, false>, threads, 1);
-            if (threads <= 256) return run(norm_kernel<X, S, V, 16, 256, V == 1 ? 3 : 4, false>, threads, 1);
-            if (threads <= 384) return run(norm_kernel<X, S, V, 16, 384, V == 1 ? 2 : 3, false>, threads, 1);
-            return run(norm_kernel<X, S, V, 16, 1024, 1, false>, threads, 1);
+            // 64 registers a thread, 56 for 384 threads (three blocks: 16381 x 6144 bf16 with codes 155 us, with two 165).
+            // Single elements and pairs take every thread of their class, whose number is a constant then: elements that
+            // a number known at run time lies between have an address each (8192 x 4095 bf16: 110 us, 60 so).
+            constexpr bool WHOLE = V < 8;
+            if (WHOLE && threads <= 32) return run(norm_kernel<X, S, V, 16, 32, 32, false>, 32, 1);
+            if (WHOLE && threads <= 64) return run(norm_kernel<X, S, V, 16, 64, 16, false>, 64, 1);
+            if (threads <= 128) return run(norm_kernel<X, S, V, 16, 128, 8, false>, WHOLE ? 128 : threads, 1);
+            if (threads <= 256) return run(norm_kernel<X, S, V, 16, 256, 4, false>, WHOLE ? 256 : threads, 1);
+            if (threads <= 384) return run(norm_kernel<X, S, V, 16, 384, WHOLE ? 2 : 3, false>, WHOLE ? 384 : threads, 1);
+            if (threads <= 512) return run(norm_kernel<X, S, V, 16, 512, 2, false>, WHOLE ? 512 : threads, 1);
+            return run(norm_kernel<X, S, V, 16, 1024, 1, false>, WHOLE ? 1024 : threads, 1);
         };
         if (fits(8)) return by_run(std::integral_constant<int, 8>{});
         if (fits(2)) return by_run(std::integral_constant<int, 2>{});

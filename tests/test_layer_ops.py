@@ -806,6 +806,23 @@ def test_norm_more_than_two_to_the_31_elements(gpu, H):
 
 
 @pytest.mark.gpu
+def test_norm_of_almost_two_to_the_31_rows(gpu):
+    if torch.cuda.mem_get_info()[0] < 60 * 2**30:
+        pytest.skip("needs 60 GB")
+    T = 2**31 - 1
+    x = torch.randn(T, 1, device="cuda", dtype=BF16)
+    y, h, r = gpu.moe_norm_forward(x)
+    d = gpu.moe_norm_backward(y, h, r, grad_h=x)[0]
+    for at in (0, T // 2, T - 40):
+        i = slice(at, at + 40)
+        a = gpu.moe_norm_forward(x[i])
+        assert torch.equal(y[i], a[0]) and torch.equal(r[i], a[2])
+        assert torch.equal(d[i], gpu.moe_norm_backward(y[i], h[i], r[i], grad_h=x[i])[0])
+    del x, y, h, r, d
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.gpu
 def test_norm_refuses_in_the_binding(gpu):
     x, w = torch.zeros(4, 32, device="cuda", dtype=BF16), torch.ones(32, device="cuda", dtype=BF16)
     for kw in (dict(x=x.double()), dict(x=x[0]), dict(x=x.t()), dict(residual=x.half()), dict(residual=x[:3]), dict(weight=w.half()), dict(weight=w[:16]),
