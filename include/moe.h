@@ -543,7 +543,9 @@ moe_status moe_route_backward(const void *logits, int32_t dtype, int64_t ld, int
  * one rounding), rstd[T] (float32; moe_norm_backward needs it), codes[T, width] with
  * scales[ceil(width / 128), T]: y in e4m3 with a scale per 1 x 128 block, as moe_fp8_quantize makes them
  * and moe_fp8_matmul reads them, from y in float32 before it is rounded to dtype.  (Where a block's
- * largest magnitude is so near a scale's step that float32 cannot tell, float64 decides.)
+ * largest magnitude is so near a scale's step that float32 cannot tell, float64 decides.)  Rows of any size have
+ * the formula's values; where rstd is more than float32 holds (eps = 0 and a row below 2^-128) it is infinite, and
+ * the row's gradient is none.
  * width: 1..16384; with codes a multiple of 16, and every row of the other tensors, and weight, on a
  * 16-byte boundary.  Rows may be strided (ldx, ldr, ldh, ldy). */
 moe_status moe_norm_forward(const void *x, int32_t dtype, int64_t ldx, const void *residual, int32_t stream_dtype,

@@ -16,7 +16,8 @@ namespace {
 // V neighbours.  A block a row, or for short rows a warp.
 // The e4m3 codes are those of y; with 8 neighbours a lane, 16 lanes hold a 1 x 128 block.  A block's scale steps where its
 // largest magnitude passes 448 times a power of two: a row with a block that is nearer to that than
-// float32's error has its sum of squares done over in float64, so the scales are those of the formula.
+// float32's error has its sum of squares done over in float64, so the scales are those of the formula.  A row whose
+// squares leave float32's range is squared once more behind a power of two.
 // 32768 x 2048 bf16 on a float32 stream: 117 us at the copy rate; 16381 x 6144 bf16 with values and codes 142 us of
 // 134 (two thirds of the issue slots: codes and scales).  Rows of odd widths go element by element: 8192 x 4095 bf16
 // 58 us of 40, f32 82 us of 79.
@@ -31,7 +32,7 @@ struct NormArgs {
     float *scales;         // [blocks(H), T]
     int T, H, w_dtype;
     double eps;
-    float per_h, per_h_rest, eps32, eps_rest;      // 1 / H and eps in two parts
+    float per_h, per_h_rest, eps32, eps_rest, eps_root;      // 1 / H and eps in two parts, the square root of eps
 };
 
 constexpr int kWarpRows = 4;       // rows of a block whose warps take a row each
@@ -212,12 +213,11 @@ __device__ __forceinline__ void norm_outputs(const NormArgs &p, long long t, int
     }
 }
 
-// 1 / sqrt(ss / H + eps) with little more than its last rounding: the mean and the sum in two parts each, and one step
-// of Newton's from the function's value.  (An error here is one of the whole row, and of its codes near a rounding.)
-__device__ __forceinline__ float norm_rstd(const NormArgs &p, float ss) {
-    const float mean = ss * p.per_h, s = mean + p.eps32, back = s - mean;
-    if (!(s > 0x1p-100f && s < 0x1p100f)) return 1.0f / sqrtf(ss / (float)p.H + p.eps32);
-    const float rest = fmaf(ss, p.per_h, -mean) + fmaf(ss, p.per_h_rest, p.eps_rest) + ((mean - (s - back)) + (p.eps32 - back));
+// 1 / sqrt(s) of s = mean + eps with little more than its last rounding: the mean and the sum in two parts each, and one
+// step of Newton's from the function's value.  (An error here is one of the whole row, and of its codes near a rounding.)
+__device__ __forceinline__ float norm_rstd(const NormArgs &p, float ss, float mean, float s, float eps, float eps_rest) {
+    const float back = s - mean;
+    const float rest = fmaf(ss, p.per_h, -mean) + fmaf(ss, p.per_h_rest, eps_rest) + ((mean - (s - back)) + (eps - back));
     const float r = rsqrtf(s), q = s * r;
     return fmaf(0.5f * r, fmaf(-q, r, 1.0f) - fmaf(rest, r, fmaf(s, r, -q)) * r, r);
 }
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) norm_kernel(const NormArgs p)
     constexpr int C = N / V;
     // weights on their way during the sum; not beside four bytes an element of x (8192 x 6144 f32: 125 us so, 118 behind it)
     constexpr bool EARLY = sizeof(T) == 2;
-    __shared__ float s_sum[32];
+    __shared__ float s_sum[2][32];
     const int tid = WARP ? threadIdx.x & 31 : threadIdx.x, nt = WARP ? 32 : V < 8 && N == 16 ? THREADS : blockDim.x;
     const int per = WARP ? kWarpRows : 1;
     wait_for_stream();
@@ -272,18 +272,49 @@ __global__ void __launch_bounds__(THREADS, PER_SM) norm_kernel(const NormArgs p)
             for (int i = 0; i < C; i++) a[i].get(&v[V * i]);
         }
     }
-    float ss = 0.0f;
+    // Squares that leave float32's range are taken again behind a power of two.  A mean between 2^-100 and 2^100 is
+    // none of them: the row's sum is below 2^114, and what a square below 2^-126 loses, 2^-150, is nothing.  Scaled
+    // ones are between 2^-98 and 2^114.  Small rows stay scaled (no element is past 2^-43), so that y is right where
+    // rstd is more than float32 holds; large ones would lose small elements.
+    float r, up = 1.0f, down = 1.0f, eps = p.eps32, eps_rest = p.eps_rest;
+    for (int turn = 0;; turn++) {
+        float ss = 0.0f;
+        if (down == 1.0f) {
 #pragma unroll
-    for (int i = 0; i < N; i++) ss = fmaf(v[i], v[i], ss);
-    ss = sum_all<WARP>(ss, s_sum);
+            for (int i = 0; i < N; i++) ss = fmaf(v[i], v[i], ss);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; i++) ss = fmaf(v[i] * down, v[i] * down, ss);
+        }
+        ss = sum_all<WARP>(ss, s_sum[turn]);       // alike in all threads of the row
+        const float mean = ss * p.per_h, s = mean + eps;
+        if (s > 0x1p-100f && s < 0x1p100f) {
+            r = norm_rstd(p, ss, mean, s, eps, eps_rest) * down;
+            break;
+        }
+        if (turn == 1) {       // zeros, or an infinity or a NaN
+            r = rsqrtf(s);
+            break;
+        }
+        if (s < 1.0f) {
+            up = 0x1p100f;
+#pragma unroll
+            for (int i = 0; i < N; i++) v[i] *= up;
+        } else {
+            down = 0x1p-80f;
+        }
+        const float root = p.eps_root * (up * down);
+        eps = root * root;
+        eps_rest = 0.0f;
+    }
     if (WARP) __syncwarp();      // the row's h is written, for all lanes
-    const float r = norm_rstd(p, ss);
     if (!EARLY && p.w) wt.load(p.w, p.w_dtype, tid, nt, p.H);
-    if (tid == 0 && p.rstd) p.rstd[t] = r;
+    if (tid == 0 && p.rstd) p.rstd[t] = r * up;
     norm_outputs<T, S, V, N>(p, t, tid, nt, v, r, wt);
 }
 
-// Gradient.  n = h r, d = dy w: dh = (d - n mean(d n)) r + grad_h, dw = sum over the tokens of dy n.
+// Gradient.  n = h r, d = dy w: dh = (d - n mean(d n)) r + grad_h, dw = sum over the tokens of dy n.  n comes first
+// everywhere: d h leaves float32's range where d n does not.
 // Blocks stay and take every gridDim-th row; a thread's columns are the same in each, so its part of dw
 // stays in registers, and a second kernel adds the blocks' parts in block order.
 struct NormGradArgs {
@@ -300,7 +331,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) norm_grad_kernel(const NormGr
     constexpr int C = N / V;
     float *norm_sm = reinterpret_cast<float *>(norm_shared);      // WARP: [warps][H]
     __shared__ float s_sum[2][32];
-    const int tid = WARP ? threadIdx.x & 31 : threadIdx.x, nt = WARP ? 32 : blockDim.x;
+    const int tid = WARP ? threadIdx.x & 31 : threadIdx.x, nt = WARP ? 32 : V == 1 ? THREADS : blockDim.x;
     const int per = WARP ? kWarpRows : 1;
     wait_for_stream();
     float acc[N];
@@ -377,14 +408,16 @@ __global__ void __launch_bounds__(THREADS, PER_SM) norm_grad_kernel(const NormGr
                 g[i].store(out + c);
             }
         } else {
-            float d[N];      // dy w
+            float d[N], n[N];      // d: dy w
 #pragma unroll
             for (int i = 0; i < C; i++) {
-                float n[V];
                 a[i].get(&d[V * i]);
-                b[i].get(n);
+                b[i].get(&n[V * i]);
+            }
 #pragma unroll
-                for (int k = 0; k < V; k++) acc[V * i + k] = fmaf(d[V * i + k] * n[k], r, acc[V * i + k]);
+            for (int i = 0; i < N; i++) {
+                n[i] *= r;
+                acc[i] = fmaf(d[i], n[i], acc[i]);
             }
             if (p.w) {
                 Weights<T, V, C> wt;
@@ -395,22 +428,15 @@ __global__ void __launch_bounds__(THREADS, PER_SM) norm_grad_kernel(const NormGr
                 });
             }
 #pragma unroll
-            for (int i = 0; i < C; i++) {
-                float n[V];
-                b[i].get(n);
-#pragma unroll
-                for (int k = 0; k < V; k++) dot = fmaf(d[V * i + k], n[k], dot);
-            }
-            dot = sum_all<WARP>(dot, s_sum[turn]);
-            const float back = -(dot * r / (float)p.H) * r;      // h times this: n mean(d n)
+            for (int i = 0; i < N; i++) dot = fmaf(d[i], n[i], dot);
+            const float back = -sum_all<WARP>(dot, s_sum[turn]) / (float)p.H;
 #pragma unroll
             for (int i = 0; i < C; i++) {
                 const int c = V * (tid + nt * i);
-                float n[V], u[V];
-                b[i].get(n);
+                float u[V];
                 g[i].get(u);
 #pragma unroll
-                for (int k = 0; k < V; k++) u[k] = fmaf(fmaf(n[k], back, d[V * i + k]), r, u[k]);
+                for (int k = 0; k < V; k++) u[k] = fmaf(fmaf(n[V * i + k], back, d[V * i + k]), r, u[k]);
                 g[i].set(u);
                 if (c < p.H) g[i].store(out + c);
             }
@@ -527,22 +553,22 @@ __global__ void __launch_bounds__(THREADS, PER_SM) norm_grad_ring_kernel(const N
         if (t + step < p.T) r_next = load_in(p.rstd + t + step);
         async_wait_all_but(D - 1);
         const int u = stage * STAGE;
-        float d[N], h[N], dot = 0.0f;      // d = dy w
+        float d[N], n[N], dot = 0.0f;      // d = dy w
 #pragma unroll
         for (int i = 0; i < C; i++) {
             if (8 * (tid + nt * i) >= p.H) continue;
             ring_get<T>(u + i * UX).get(&d[8 * i]);
-            ring_get<S>(u + C * UX + i * US).get(&h[8 * i]);
+            ring_get<S>(u + C * UX + i * US).get(&n[8 * i]);
 #pragma unroll
             for (int k = 8 * i; k < 8 * i + 8; k++) {
-                acc[k] = fmaf(d[k] * h[k], r, acc[k]);
+                n[k] *= r;
+                acc[k] = fmaf(d[k], n[k], acc[k]);
                 d[k] *= w[k];
-                dot = fmaf(d[k], h[k], dot);
+                dot = fmaf(d[k], n[k], dot);
             }
         }
-        dot = sum_all<WARP>(dot, s_sum[turn]);
+        const float back = -sum_all<WARP>(dot, s_sum[turn]) / (float)p.H;
         turn ^= 1;
-        const float back = -(dot * r / (float)p.H) * r;      // h times this: n mean(d n)
 #pragma unroll
         for (int i = 0; i < C; i++) {
             const int c = 8 * (tid + nt * i);
@@ -554,7 +580,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) norm_grad_ring_kernel(const N
                 q.get(o);
             }
 #pragma unroll
-            for (int k = 0; k < 8; k++) o[k] = fmaf(fmaf(h[8 * i + k], back, d[8 * i + k]), r, o[k]);
+            for (int k = 0; k < 8; k++) o[k] = fmaf(fmaf(n[8 * i + k], back, d[8 * i + k]), r, o[k]);
             q.set(o);
             q.store(static_cast<S *>(p.out) + t * p.ldo + c);
         }
@@ -658,7 +684,7 @@ size_t norm_grad_workspace(int T, int H) { return (size_t)norm_grad_blocks(T, H)
 cudaError_t launch_norm_forward(const void *x, int dtype, long long ldx, const void *res, int s_dtype, long long ldr, const void *w, int w_dtype,
                                 int T, int H, double eps, void *h, long long ldh, void *y, long long ldy, float *rstd, uint8_t *codes,
                                 float *scales, cudaStream_t st) {
-    const NormArgs p = {x, res, w, ldx, ldr, ldh, ldy, h, y, rstd, codes, scales, T, H, w_dtype, eps, (float)(1.0 / H), (float)(1.0 / H - (float)(1.0 / H)), (float)eps, (float)(eps - (float)eps)};
+    const NormArgs p = {x, res, w, ldx, ldr, ldh, ldy, h, y, rstd, codes, scales, T, H, w_dtype, eps, (float)(1.0 / H), (float)(1.0 / H - (float)(1.0 / H)), (float)eps, (float)(eps - (float)eps), (float)sqrt(eps)};
     auto go = [&](auto xt, auto stt) {
         using X = decltype(xt);
         using S = decltype(stt);
@@ -723,16 +749,24 @@ cudaError_t launch_norm_backward(const void *dy, int dtype, long long lddy, cons
                 });
             }
         }
-        const int threads = direct_threads(H);
-        blocks = norm_blocks(T, H <= 256 ? kWarpRows : 1, direct_per_sm(H, threads));
         auto by_run = [&](auto v) {
             constexpr int V = decltype(v)::value;
+            // single elements take every thread of their class, as in the forward pass (8192 x 4095 bf16: 127 us, 85 so);
+            // pairs gain less and lose beyond 8192 (4096 x 9002 bf16: 117 us, 138 so)
+            constexpr bool WHOLE = V == 1;
+            const int own = direct_threads(H);
+            const int threads = !WHOLE || H <= 256 ? own : own <= 32 ? 32 : own <= 64 ? 64 : own <= 128 ? 128 : own <= 256 ? 256 : own <= 384 ? 384 : own <= 512 ? 512 : own <= 768 ? 768 : 1024;
+            blocks = norm_blocks(T, H <= 256 ? kWarpRows : 1, direct_per_sm(H, threads));
             if (H <= 256)
                 return launch_early(norm_grad_kernel<X, S, V, 8, 32 * kWarpRows, 6, true>, blocks, threads, dw ? (size_t)kWarpRows * H * sizeof(float) : 0, st, 1, p);
+            if (WHOLE && threads <= 32) return launch_early(norm_grad_kernel<X, S, V, 16, 32, 20, false>, blocks, threads, 0, st, 1, p);
+            if (WHOLE && threads <= 64) return launch_early(norm_grad_kernel<X, S, V, 16, 64, 10, false>, blocks, threads, 0, st, 1, p);
             if (threads <= 128) return launch_early(norm_grad_kernel<X, S, V, 16, 128, 5, false>, blocks, threads, 0, st, 1, p);
             if (threads <= 256) return launch_early(norm_grad_kernel<X, S, V, 16, 256, 3, false>, blocks, threads, 0, st, 1, p);
             if (threads <= 384) return launch_early(norm_grad_kernel<X, S, V, 16, 384, 2, false>, blocks, threads, 0, st, 1, p);
             if (threads <= 512) return launch_early(norm_grad_kernel<X, S, V, 16, 512, 1, false>, blocks, threads, 0, st, 1, p);
+            // 80 registers (4096 x 10240 f32 131 us, 9002 bf16 96 us; with the last class's 64: 162 and 131)
+            if (threads <= 768) return launch_early(norm_grad_kernel<X, S, V, 16, 768, 1, false>, blocks, threads, 0, st, 1, p);
             return launch_early(norm_grad_kernel<X, S, V, 16, 1024, 1, false>, blocks, threads, 0, st, 1, p);
         };
         if (eights) return by_run(std::integral_constant<int, 8>{});

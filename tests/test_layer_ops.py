@@ -720,6 +720,52 @@ def test_norm_zeros_nan_and_extremes(gpu):
     assert bool(torch.isinf(z[0]).all())
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [9, 324])
+@pytest.mark.parametrize("H", [1, 200, 255, 1001, 2046, 2048, 6144, 8192])
+@pytest.mark.parametrize("dtype,stream", [(F32, None), (BF16, None), (BF16, BF16), (BF16, F32)])
+def test_norm_rows_whose_squares_leave_float32(gpu, T, H, dtype, stream):
+    """Rows from 1e-37 to 1e38, without an epsilon and with one: values, codes and gradients are the formula's."""
+    g = gen(T, H, 9)
+    size = torch.tensor([1e-37, 1e-30, 1e-24, 1e-21, 1.0, 1e17, 1e20, 1e30, 1e38], dtype=torch.float64).repeat(T // 9)[:, None]
+    x = (torch.randn(T, H, generator=g).clamp(-3, 3).double() * size)
+    x[4, 0] = 2e19                                     # one value alone
+    x = x.to(dtype)
+    x[x == 0] = 1e-37
+    res = None if stream is None else (0.1 * torch.randn(T, H, generator=g).clamp(-3, 3).double() * size).to(stream)
+    w = (1 + 0.3 * torch.randn(H, generator=g)).to(dtype)
+    dy = torch.randn(T, H, generator=g).to(dtype)
+    for eps in (0.0, 1e-5):
+        y, h, r, *codes = gpu.moe_norm_forward(x.cuda(), residual=None if res is None else res.cuda(), weight=w.cuda(), eps=eps, quantize=H % 16 == 0)
+        h64, r64, y64 = norm_ref(x, res, w, eps)
+        # 1 / rms beyond float32's largest value (one value below 2^-128 and no epsilon) is rounded to infinity; y is the formula's
+        held = r64 <= torch.finfo(F32).max
+        assert torch.equal(h.cpu(), h64) and bool((r.cpu()[~held] == inf).all())
+        assert bool(((r.cpu().double() - r64)[held].abs() <= 2.0 ** -18 * r64[held]).all())
+        assert bool(((y.cpu().double() - y64).abs() <= (2.0 ** -18 + half_step(dtype)) * y64.abs() + torch.finfo(dtype).tiny).all())
+        if codes:
+            check_codes(codes[0], codes[1], y64)
+        check_norm_grad(gpu, x[held], None if res is None else res[held], w, dy[held], None, eps=eps)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H", [128, 2048, 6144])
+def test_norm_scales_at_their_step_of_large_and_small_rows(gpu, H):
+    """A power of two times a row is the same row behind the norm (eps = 0): the same codes and scales, next to a scale's step too."""
+    x = torch.randn(6, H, generator=gen(H, 2))
+    _, r, _ = norm_ref(x, None, None, 0.0)
+    for t in range(6):
+        for ulps in (-2, 0, 2):
+            w = 0.001 * torch.ones(H)
+            w[5] = float(1.75 / (x[t, 5].double().abs() * r[t])) * (1 + ulps * 2.0 ** -24)
+            want = gpu.moe_norm_forward(x.cuda(), weight=w.cuda(), quantize=True, eps=0.0)
+            assert torch.equal(want[4].cpu().double(), scales_ref(norm_ref(x, None, w, 0.0)[2]))
+            for by in (2.0 ** -80, 2.0 ** 60, 2.0 ** 120):
+                got = gpu.moe_norm_forward((x * by).cuda(), weight=w.cuda(), quantize=True, eps=0.0)
+                assert torch.equal(got[4], want[4])
+                check_codes(got[3], got[4], norm_ref(x, None, w, 0.0)[2])
+
+
 def check_norm_grad(moe, x, res, w, dy, gh, eps=1e-5):
     """dh: 2^-17 of the sizes of its terms (the row's sum has 16 or 32 additions a thread and 10 levels),
     then the rounding; dw: the tokens of a block one after another (34 at most here) and 32 + 5 more: 2^-17."""
