@@ -547,7 +547,9 @@ moe_status moe_route_backward(const void *logits, int32_t dtype, int64_t ld, int
  * the formula's values; where rstd is more than float32 holds (eps = 0 and a row below 2^-128) it is infinite, and
  * the row's gradient is none.
  * width: 1..16384; with codes a multiple of 16, and every row of the other tensors, and weight, on a
- * 16-byte boundary.  Rows may be strided (ldx, ldr, ldh, ldy). */
+ * 16-byte boundary.  Rows may be strided (ldx, ldr, ldh, ldy).  No output may overlap another tensor of the call,
+ * but h and y may be the very rows of x or residual, and y those of h; with codes y may not be those of h (x
+ * where there is no residual). */
 moe_status moe_norm_forward(const void *x, int32_t dtype, int64_t ldx, const void *residual, int32_t stream_dtype,
                             int64_t ldr, const void *weight, int32_t weight_dtype, int32_t T, int32_t width, double eps,
                             void *h, int64_t ldh, void *y, int64_t ldy, float *rstd, uint8_t *codes, float *scales,

@@ -9,6 +9,7 @@
 #include <algorithm>
 #include <exception>
 #include <new>
+#include <numeric>
 #include <vector>
 
 #include "moe_internal.h"
@@ -654,6 +655,30 @@ static bool aligned_rows(const void *p, int64_t ld, int32_t dtype) {
     return aligned16(p) && ld * (dtype == MOE_DTYPE_F32 ? 4 : 2) % 16 == 0;
 }
 
+// A tensor in memory: rows of `width` bytes, `pitch` bytes apart.
+struct Rows {
+    uintptr_t at;
+    int64_t rows, pitch, width;
+    Rows(const void *p, int64_t n, int64_t ld, int64_t elements, int64_t el)
+        : at(reinterpret_cast<uintptr_t>(p)), rows(p ? n : 0), pitch(ld <= INT64_MAX / el ? ld * el : INT64_MAX), width(elements * el) {}
+    Rows(const void *p, int64_t bytes) : Rows(p, bytes > 0, bytes, bytes, 1) {}
+    int64_t bytes() const { return rows < 2 ? width : pitch > INT64_MAX / rows ? INT64_MAX : (rows - 1) * pitch + width; }
+};
+static int64_t el_size(int32_t dtype) { return dtype == MOE_DTYPE_F32 ? 4 : 2; }
+// Whether the two have bytes in common: slices of other columns of one buffer's rows have none.
+static bool overlap(const Rows &a, const Rows &b) {
+    if (a.rows < 1 || b.rows < 1) return false;
+    const int64_t d = (int64_t)(b.at - a.at);
+    if (d >= a.bytes() || -d >= b.bytes()) return false;
+    if (a.rows < 2 && b.rows < 2) return true;
+    const int64_t g = a.rows < 2 ? b.pitch : b.rows < 2 ? a.pitch : std::gcd(a.pitch, b.pitch), r = (d % g + g) % g;
+    return r < a.width || r + b.width > g;
+}
+// The same, but rows on top of one another: each is read by who writes it, before it does.
+static bool askew(const Rows &a, const Rows &b) {
+    return overlap(a, b) && !(a.at == b.at && a.rows == b.rows && a.width == b.width && (a.rows < 2 || a.pitch == b.pitch));
+}
+
 static moe_status check_route(const void *logits, int32_t dtype, int64_t ld, int32_t T, int32_t E, int32_t top_k, int32_t score_func,
                               int32_t norm_topk, float scale) {
     MOE_NEED(dtype_ok(dtype), MOE_ERR_INVALID, "dtype=%d: need a MOE_DTYPE_* value", dtype);
@@ -735,6 +760,15 @@ moe_status moe_norm_forward(const void *x, int32_t dtype, int64_t ldx, const voi
     MOE_NEED(!codes || (aligned16(codes) && aligned_rows(x, ldx, dtype) && (!y || aligned_rows(y, ldy, dtype)) && aligned16(weight) &&
              (!residual || (aligned_rows(residual, ldr, stream_dtype) && aligned_rows(h, ldh, stream_dtype)))),
              MOE_ERR_INVALID, "with codes every row, weight and codes must start on a 16-byte boundary");
+    const int64_t el = el_size(dtype), es = el_size(stream_dtype);
+    const Rows rx(x, T, ldx, width, el), rr(residual, T, ldr, width, es), rh(residual ? h : nullptr, T, ldh, width, es), ry(y, T, ldy, width, el),
+        rw(weight, width * el_size(weight_dtype)), rs(rstd, (int64_t)T * 4), rc(codes, (int64_t)T * width), rb(scales, (width + 127) / 128 * (int64_t)T * 4);
+    // a row next to a scale's step is read again, from h or x, while others write y
+    MOE_NEED(!askew(rh, rr) && !askew(rh, rx) && !askew(ry, rx) && !askew(ry, rr) && !askew(ry, rh) && (!codes || !overlap(ry, residual ? rh : rx)),
+             MOE_ERR_INVALID, "h or y overlaps another tensor");
+    for (const Rows *o : {&rs, &rc, &rb})
+        for (const Rows *i : {&rx, &rr, &rh, &ry, &rw}) MOE_NEED(!overlap(*o, *i), MOE_ERR_INVALID, "rstd, codes or scales overlap another tensor");
+    MOE_NEED(!overlap(rs, rc) && !overlap(rs, rb) && !overlap(rc, rb) && !overlap(rw, rh) && !overlap(rw, ry), MOE_ERR_INVALID, "two outputs, or weight and one, overlap");
     return launched(moe::launch_norm_forward(x, dtype, ldx, residual, stream_dtype, ldr, weight, weight_dtype, T, width, eps, h, ldh, y, ldy,
                                              rstd, codes, scales, static_cast<cudaStream_t>(stream)), "moe_norm_forward");
 }

@@ -190,6 +190,23 @@ def test_outputs_on_top_of_what_others_read_are_refused(moe):
     assert L.moe_combine_backward(P, 0, 8, Q, 8, 4, 8, Q, 4, 2, Q, Q, P, 8, Q, None) == moe.MOE_ERR_INVALID
 
 
+def test_norm_refuses_outputs_on_top_of_other_tensors(moe):
+    L, T, H = moe.lib(), 4, 64
+    far = {n: P + 65536 * (i + 1) for i, n in enumerate("xrwhyscb")}
+
+    def fwd(dt=2, sd=0, ld=64, quant=True, **kw):
+        a = {**far, **kw}
+        return L.moe_norm_forward(a["x"], dt, ld, a["r"], sd, ld, a["w"], dt, T, H, 1e-5, a["h"], ld, a["y"], ld, a["s"],
+                                  a["c"] if quant else None, a["b"] if quant else None, None)
+    x, r, w, h, y, s, c, b = (far[n] for n in "xrwhyscb")
+    for kw in (dict(y=x, r=None), dict(y=x + 128, r=None), dict(y=x - 128, r=None), dict(y=h, sd=2), dict(y=h + 16), dict(y=x + 16), dict(y=r), dict(y=r + 256, sd=2),
+               dict(h=r + 256), dict(h=r - 16), dict(h=x), dict(h=x + 128, sd=2), dict(h=r + 4, quant=False), dict(y=x + 2, quant=False), dict(y=w), dict(w=h),
+               dict(s=x), dict(s=y + 4), dict(s=h + 1020), dict(c=x), dict(c=y + 16), dict(c=w), dict(b=r), dict(b=c + 252), dict(b=s + 12), dict(s=c)):
+        assert fwd(**kw) == moe.MOE_ERR_INVALID, kw
+    # columns that run into the next one's, in rows of one buffer; single rows inside another tensor's rows
+    assert fwd(ld=128, r=None, y=x + 112) == fwd(ld=128, r=None, y=x + 144) == fwd(ld=128, h=r + 240) == moe.MOE_ERR_INVALID
+
+
 def test_binding_refuses_what_is_not_on_the_device(moe):
     x, i = torch.zeros(2, 16), torch.zeros(2, 1, dtype=torch.int32)
     for call in (lambda: moe.moe_route_forward(x, 1), lambda: moe.moe_norm_forward(x), lambda: moe.moe_combine_forward(x, i),
@@ -694,6 +711,41 @@ def test_norm_in_place_and_repeatable(gpu, H):
     dy = torch.randn(500, H, generator=gen(2)).to(BF16).cuda()
     p, q = (gpu.moe_norm_backward(dy, a[1], a[2], weight=w.cuda()) for _ in range(2))
     assert torch.equal(p[0], q[0]) and torch.equal(p[1], q[1])
+
+
+@pytest.mark.gpu
+def test_norm_in_place_and_beside_its_inputs(gpu):
+    """y on top of x or residual, outputs in other columns of the inputs' buffer: what separate tensors give."""
+    T, H = 40, 512
+    L, st = gpu.lib(), torch.cuda.current_stream().cuda_stream
+    x, res, w = torch.randn(T, H, generator=gen(1)).to(BF16).cuda(), torch.randn(T, H, generator=gen(2)).to(BF16).cuda(), torch.ones(H, dtype=BF16, device="cuda")
+    y, h, r, q, s = gpu.moe_norm_forward(x, residual=res, weight=w, quantize=True)
+    alone = gpu.moe_norm_forward(x, weight=w)[0]
+    wide = torch.full((T, 3 * H), 7.0, dtype=BF16, device="cuda")
+    wide[:, :H], wide[:, H:2 * H] = x, res
+    got = gpu.moe_norm_forward(wide[:, :H], residual=wide[:, H:2 * H], weight=w, quantize=True, out=wide[:, 2 * H:])
+    for a, b in zip(got, (y, h, r, q, s)):
+        assert torch.equal(a.view(torch.uint8) if a.dtype == torch.float8_e4m3fn else a, b.view(torch.uint8) if b.dtype == torch.float8_e4m3fn else b)
+    assert torch.equal(wide[:, :H], x) and torch.equal(wide[:, H:2 * H], res)
+
+    def call(x, res, h, y, codes):
+        c, b = torch.empty(T, H, dtype=torch.uint8, device="cuda"), torch.empty(H // 128, T, device="cuda")
+        assert gpu.MOE_OK == L.moe_norm_forward(x.data_ptr(), 2, H, res.data_ptr() if res is not None else None, 2, H, w.data_ptr(), 2, T, H, 1e-5,
+                                                h.data_ptr() if h is not None else None, H, y.data_ptr(), H, None, c.data_ptr() if codes else None,
+                                                b.data_ptr() if codes else None, st)
+        return (c, b) if codes else None
+    z = x.clone()
+    call(z, None, None, z, False)
+    assert torch.equal(z, alone)
+    z, hh = x.clone(), torch.empty_like(x)
+    c, b = call(z, res, hh, z, True)
+    assert torch.equal(z, y) and torch.equal(hh, h) and torch.equal(c, q.view(torch.uint8)) and torch.equal(b, s)
+    z, hh = res.clone(), torch.empty_like(x)
+    c, b = call(x, z, hh, z, True)
+    assert torch.equal(z, y) and torch.equal(hh, h) and torch.equal(c, q.view(torch.uint8)) and torch.equal(b, s)
+    z = torch.empty_like(x)
+    call(x, res, z, z, False)
+    assert torch.equal(z, y)
 
 
 @pytest.mark.gpu
