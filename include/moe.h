@@ -559,8 +559,9 @@ moe_status moe_norm_forward(const void *x, int32_t dtype, int64_t ldx, const voi
  *   dh = (d - n mean over the row of (d n)) rstd + grad_h      dweight = sum over the tokens of dy n
  * dy[T, width] (dtype) is the gradient of y, grad_h[T, width] (stream_dtype, NULL: 0) the one that reaches
  * h otherwise; h (stream_dtype; x where there was no residual) and rstd are the forward's.  dh[T, width]
- * (stream_dtype; may be grad_h itself) is the gradient of x and of residual; dweight[width] float32 (NULL:
- * not computed).  workspace: moe_norm_workspace(...) bytes, 16-byte aligned (only with dweight). */
+ * (stream_dtype) is the gradient of x and of residual; dweight[width] float32 (NULL:
+ * not computed).  workspace: moe_norm_workspace(...) bytes, 16-byte aligned (only with dweight).  No output
+ * may overlap another tensor of the call, but dh may be the very rows of dy, h or grad_h. */
 size_t moe_norm_workspace(int32_t T, int32_t width);
 moe_status moe_norm_backward(const void *dy, int32_t dtype, int64_t lddy, const void *h, int32_t stream_dtype,
                              int64_t ldh, const float *rstd, const void *weight, int32_t weight_dtype,

@@ -793,6 +793,12 @@ moe_status moe_norm_backward(const void *dy, int32_t dtype, int64_t lddy, const 
     const size_t need = dweight ? moe_norm_workspace(T, width) : 0;
     MOE_NEED(need == 0 || (workspace && aligned16(workspace) && workspace_bytes >= need), MOE_ERR_INVALID,
              "workspace: need %zu bytes, 16-byte aligned", need);
+    const int64_t el = el_size(dtype), es = el_size(stream_dtype);
+    const Rows rd(dy, T, lddy, width, el), rh(h, T, ldh, width, es), rg(grad_h, T, ldg, width, es), ro(dh, T, ldd, width, es), rs(rstd, (int64_t)T * 4),
+        rw(weight, width * el_size(weight_dtype)), rdw(dweight, (int64_t)width * 4), ws(need ? workspace : nullptr, (int64_t)need);
+    MOE_NEED(!askew(ro, rd) && !askew(ro, rh) && !askew(ro, rg) && !overlap(ro, rs) && !overlap(ro, rw), MOE_ERR_INVALID, "dh overlaps another tensor");
+    for (const Rows *i : {&rd, &rh, &rg, &ro, &rs, &rw, &rdw}) MOE_NEED(!overlap(ws, *i), MOE_ERR_INVALID, "workspace overlaps a tensor");
+    MOE_NEED(!overlap(rdw, ro), MOE_ERR_INVALID, "dweight overlaps dh");
     return launched(moe::launch_norm_backward(dy, dtype, lddy, h, stream_dtype, ldh, rstd, weight, weight_dtype, grad_h, ldg, T, width, dh, ldd,
                                               dweight, workspace, st), "moe_norm_backward");
 }

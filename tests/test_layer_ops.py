@@ -207,6 +207,19 @@ def test_norm_refuses_outputs_on_top_of_other_tensors(moe):
     assert fwd(ld=128, r=None, y=x + 112) == fwd(ld=128, r=None, y=x + 144) == fwd(ld=128, h=r + 240) == moe.MOE_ERR_INVALID
 
 
+def test_norm_gradient_refuses_outputs_on_top_of_other_tensors(moe):
+    L, T, H = moe.lib(), 4, 64
+    far = {n: P + 1048576 * (i + 1) for i, n in enumerate("dhsgwozk")}
+
+    def bwd(dt=2, sd=0, ld=64, **kw):
+        a = {**far, **kw}
+        return L.moe_norm_backward(a["d"], dt, ld, a["h"], sd, ld, a["s"], a["w"], dt, a["g"], ld, T, H, a["o"], ld, a["z"], a["k"], 1 << 19, None)
+    d, h, s, g, w, o, z, k = (far[n] for n in "dhsgwozk")
+    for kw in (dict(o=h + 256), dict(o=h - 256), dict(o=g + 4), dict(o=d), dict(o=d + 128, sd=2), dict(o=s), dict(o=s - 1020), dict(o=w), dict(z=o), dict(z=o + 1020),
+               dict(k=d), dict(k=h), dict(k=g), dict(k=o), dict(k=z), dict(k=w), dict(k=s), dict(ld=128, o=h + 144), dict(ld=128, o=g - 144)):
+        assert bwd(**kw) == moe.MOE_ERR_INVALID, kw
+
+
 def test_binding_refuses_what_is_not_on_the_device(moe):
     x, i = torch.zeros(2, 16), torch.zeros(2, 1, dtype=torch.int32)
     for call in (lambda: moe.moe_route_forward(x, 1), lambda: moe.moe_norm_forward(x), lambda: moe.moe_combine_forward(x, i),
@@ -855,6 +868,29 @@ def test_norm_gradient(gpu, T, H, dtype, stream, wt, through):
     dy = torch.randn(T, H, generator=g).to(dtype)
     gh = torch.randn(T, H, generator=g).to(stream or dtype) if through else None
     check_norm_grad(gpu, x, res, w, dy, gh)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H", [200, 1001, 2048])
+@pytest.mark.parametrize("dtype,stream", [(BF16, BF16), (F32, F32), (BF16, F32)])
+def test_norm_gradient_in_place(gpu, H, dtype, stream):
+    """dh on top of dy, h or grad_h, or in other columns of their buffer."""
+    T = 700
+    g = gen(H)
+    dy, res, gh = torch.randn(T, H, generator=g).to(dtype).cuda(), torch.randn(T, H, generator=g).to(stream).cuda(), torch.randn(T, H, generator=g).to(stream).cuda()
+    w = (1 + 0.1 * torch.randn(H, generator=g)).cuda()
+    _, h, r = gpu.moe_norm_forward(dy, residual=res, weight=w)
+    d, dw = gpu.moe_norm_backward(dy, h, r, weight=w, grad_h=gh)
+    for name in ("dy", "h", "gh")[0 if dtype == stream else 1:]:
+        t = dict(dy=dy.clone(), h=h.clone(), gh=gh.clone())
+        a, b = gpu.moe_norm_backward(t["dy"], t["h"], r, weight=w, grad_h=t["gh"], out=t[name])
+        assert a.data_ptr() == t[name].data_ptr() and torch.equal(a, d) and torch.equal(b, dw)
+    n = (H + 7) // 8 * 8
+    wide = torch.zeros(T, 3 * n, dtype=stream, device="cuda")
+    wide[:, :H], wide[:, n:n + H] = h, gh
+    a, b = gpu.moe_norm_backward(dy, wide[:, :H], r, weight=w, grad_h=wide[:, n:n + H], out=wide[:, 2 * n:2 * n + H])
+    tol = 2.0 ** -18 + half_step(stream)       # rows of another boundary may be added in another order
+    assert bool(((a - d).double().abs() <= tol * (2 + 2 * d.double().abs())).all()) and torch.equal(wide[:, :H], h)
 
 
 @pytest.mark.gpu
