@@ -518,7 +518,8 @@ moe_status moe_fp8_wgrad(const uint8_t *xt, const float *xt_scale, const uint8_t
  * Keys are compared as their float64 values (without a bias as the logits themselves); the lower index
  * wins a tie; a NaN ranks with -infinity.  A token whose choice hangs on less than float32 tells takes some
  * microseconds more, one with very many equal keys about one.
- * Limits: E in 1..1024, top_k 1..min(E, 32), n_group 1..32, top_k <= topk_group E / n_group. */
+ * Limits: E in 1..1024, top_k 1..min(E, 32), n_group 1..32, top_k <= topk_group E / n_group.  The outputs must
+ * not overlap one another or an input. */
 moe_status moe_route_forward(const void *logits, int32_t dtype, int64_t ld, int32_t T, int32_t n_experts,
                              const float *bias, int32_t top_k, int32_t score_func, int32_t n_group,
                              int32_t topk_group, int32_t norm_topk, float routed_scale, const uint8_t *mask,
@@ -529,7 +530,7 @@ moe_status moe_route_forward(const void *logits, int32_t dtype, int64_t ld, int3
  * topk_idx outside [0, E) have no weight (a masked token's row is zeros, whatever its logits hold); an
  * expert that stands twice in a row gets the sum of both gradients.  accumulate not 0: the gradient is
  * added to what dlogits holds (that of the balance loss, say), in float32, rounded once.  dlogits must not
- * overlap logits. */
+ * overlap an input. */
 moe_status moe_route_backward(const void *logits, int32_t dtype, int64_t ld, int32_t T, int32_t n_experts,
                               const int32_t *topk_idx, int32_t top_k, int32_t score_func, int32_t norm_topk,
                               float routed_scale, const float *grad_w, void *dlogits, int64_t ldd,

@@ -709,6 +709,11 @@ moe_status moe_route_forward(const void *logits, int32_t dtype, int64_t ld, int3
     MOE_NEED(T == 0 || (topk_idx && topk_w), MOE_ERR_INVALID, "topk_idx / topk_w is NULL");
     MOE_NEED(aligned4(bias) && aligned4(topk_idx) && aligned4(topk_w), MOE_ERR_INVALID, "int32 / float32 buffers must be 4-byte aligned");
     if (T == 0) return MOE_OK;
+    const Rows rx(logits, T, ld, n_experts, el_size(dtype)), ri(topk_idx, (int64_t)T * top_k * 4), rw(topk_w, (int64_t)T * top_k * 4),
+        rb(bias, (int64_t)n_experts * 4), rm(mask, T);
+    for (const Rows *o : {&ri, &rw})
+        MOE_NEED(!overlap(*o, rx) && !overlap(*o, rb) && !overlap(*o, rm), MOE_ERR_INVALID, "topk_idx or topk_w overlaps logits, bias or mask");
+    MOE_NEED(!overlap(ri, rw), MOE_ERR_INVALID, "topk_idx and topk_w overlap");
     return launched(moe::launch_route_forward(logits, dtype, ld, T, n_experts, bias, top_k, score_func == MOE_SCORE_SOFTMAX, n_group,
                                               n_group > 1 ? topk_group : 1, norm_topk, routed_scale, mask, topk_idx, topk_w,
                                               static_cast<cudaStream_t>(stream)), "moe_route_forward");
@@ -723,7 +728,9 @@ moe_status moe_route_backward(const void *logits, int32_t dtype, int64_t ld, int
     MOE_NEED(T == 0 || (topk_idx && grad_w && dlogits), MOE_ERR_INVALID, "topk_idx / grad_w / dlogits is NULL");
     MOE_NEED(aligned4(topk_idx) && aligned4(grad_w) && aligned_el(dlogits, dtype), MOE_ERR_INVALID, "a buffer is not aligned to its elements");
     if (T == 0) return MOE_OK;
-    MOE_NEED(dlogits != logits, MOE_ERR_INVALID, "dlogits is logits");
+    const Rows ro(dlogits, T, ldd, n_experts, el_size(dtype));
+    MOE_NEED(!overlap(ro, Rows(logits, T, ld, n_experts, el_size(dtype))) && !overlap(ro, Rows(topk_idx, (int64_t)T * top_k * 4)) &&
+             !overlap(ro, Rows(grad_w, (int64_t)T * top_k * 4)), MOE_ERR_INVALID, "dlogits overlaps logits, topk_idx or grad_w");
     return launched(moe::launch_route_backward(logits, dtype, ld, T, n_experts, topk_idx, top_k, score_func == MOE_SCORE_SOFTMAX, norm_topk,
                                                routed_scale, grad_w, dlogits, ldd, accumulate != 0, static_cast<cudaStream_t>(stream)),
                     "moe_route_backward");

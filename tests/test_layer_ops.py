@@ -220,6 +220,22 @@ def test_norm_gradient_refuses_outputs_on_top_of_other_tensors(moe):
         assert bwd(**kw) == moe.MOE_ERR_INVALID, kw
 
 
+def test_route_refuses_outputs_on_top_of_other_tensors(moe):
+    L, T, E, K = moe.lib(), 4, 64, 2
+    x, b, m, i, w, d = (P + 65536 * (k + 1) for k in range(6))
+
+    def fwd(i=i, w=w, b=b, ld=E, dt=0):
+        return L.moe_route_forward(x, dt, ld, T, E, b, K, 0, 1, 1, 1, 1.0, m, i, w, None)
+    for kw in (dict(i=x), dict(w=x + 1020), dict(i=x - 28), dict(i=b), dict(w=b + 252), dict(i=m), dict(w=m - 28), dict(i=w), dict(w=i + 28), dict(i=x + 228, ld=128, dt=2)):
+        assert fwd(**kw) == moe.MOE_ERR_INVALID, kw
+
+    def bwd(d=d, ld=E, ldd=E, i=i, w=w, dt=0, add=0):
+        return L.moe_route_backward(x, dt, ld, T, E, i, K, 0, 1, 1.0, w, d, ldd, add, None)
+    for kw in (dict(d=x), dict(d=x + 256), dict(d=x - 256), dict(d=x + 4), dict(d=x + 256, ld=192), dict(d=x + 256, ldd=192), dict(d=x + 252, ld=128, ldd=128),
+               dict(d=x - 252, ld=128, ldd=128), dict(d=i), dict(d=w + 16), dict(d=w - 1020), dict(d=x + 128, dt=2, add=1)):
+        assert bwd(**kw) == moe.MOE_ERR_INVALID, kw
+
+
 def test_binding_refuses_what_is_not_on_the_device(moe):
     x, i = torch.zeros(2, 16), torch.zeros(2, 1, dtype=torch.int32)
     for call in (lambda: moe.moe_route_forward(x, 1), lambda: moe.moe_norm_forward(x), lambda: moe.moe_combine_forward(x, i),
@@ -529,6 +545,25 @@ def test_route_gradient_against_differences(gpu, score, renorm):
             b[t, j] -= e
             # central differences: e^2 times a third derivative of order 1, and 2^-53 / e; logits rounded to float32
             assert abs(float((f(a) - f(b)) / (2 * e)) - float(d[t, j])) <= 1e-6 + 2.0 ** -18
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_route_gradient_beside_its_logits(gpu, dtype):
+    """Logits and their gradient in columns of one buffer, or in every other of its rows; rows in common are refused."""
+    T, E, K = 33, 64, 4
+    x = torch.randn(T, E, generator=gen(E)).to(dtype).cuda()
+    dw = torch.randn(T, K, generator=gen(2)).cuda()
+    idx, _ = gpu.moe_route_forward(x, K)
+    want = gpu.moe_route_backward(x, idx, dw)
+    for both in (torch.zeros(T, 2, E, dtype=dtype, device="cuda"), torch.zeros(T, 5, E, dtype=dtype, device="cuda")):
+        both[:, 0] = x
+        gpu.moe_route_backward(both[:, 0], idx, dw, out=both[:, 1])
+        assert torch.equal(both[:, 0], x) and torch.equal(both[:, 1], want) and bool((both[:, 2:] == 0).all())
+    flat = torch.zeros(T + 1, E, dtype=dtype, device="cuda")
+    for a, b in ((flat[:-1], flat[1:]), (flat[1:], flat[:-1]), (flat.view(-1)[:T * E].view(T, E), flat.view(-1)[1:T * E + 1].view(T, E))):
+        with pytest.raises(gpu.MoeError):
+            gpu.moe_route_backward(a, idx, dw, out=b)
 
 
 @pytest.mark.gpu
