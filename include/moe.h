@@ -572,7 +572,8 @@ moe_status moe_norm_backward(const void *dy, int32_t dtype, int64_t lddy, const 
 /* The weighted sum of a token's rows: y[t] = sum_k topk_w[t, k] rows[pos[t, k]] + add[t] in float32, in the
  * order of k, rounded once to y's dtype.  rows[R, N] (dtype) the experts' outputs, pos[T, K] (int32) as
  * moe_expert_lists writes it: pairs with a value outside [0, R) are left out, so rows without a token are
- * never read.  topk_w NULL: 1; add[T, N] (y_dtype) NULL: none (it may be y itself; rows must not overlap y).
+ * never read.  topk_w NULL: 1; add[T, N] (y_dtype) NULL: none.  y must not overlap another tensor of the call, but
+ * may be the very rows of add.
  * N in 1..131072, K in 1..32, T times ceil(N / 256) up to 2^33. */
 moe_status moe_combine_forward(const void *rows, int32_t dtype, int64_t ld, int32_t R, int32_t N, const int32_t *pos,
                                int32_t T, int32_t top_k, const float *topk_w, const void *add, int64_t ldadd, void *y,
@@ -581,8 +582,8 @@ moe_status moe_combine_forward(const void *rows, int32_t dtype, int64_t ld, int3
 /* Its gradients, from dy[T, N] (dtype, as rows): drows[R, N] (dtype) with drows[pos[t, k]] = topk_w[t, k] dy[t]
  * and dtopk_w[T, K] = rows[pos[t, k]] . dy[t] (0 for pairs without a row).  tokens[R] is the token of every
  * row (moe_expert_lists' `rows`): a row takes the gradient of its own token, with the sum of the weights
- * where that names it more than once; every other row gets zeros.  drows or dtopk_w may be NULL; drows must
- * not overlap rows or dy.  T up to 2^30. */
+ * where that names it more than once; every other row gets zeros.  drows or dtopk_w may be NULL; neither may
+ * overlap another tensor of the call, but dtopk_w may be topk_w itself.  T up to 2^30. */
 moe_status moe_combine_backward(const void *dy, int32_t dtype, int64_t lddy, const void *rows, int64_t ld, int32_t R,
                                 int32_t N, const int32_t *pos, int32_t T, int32_t top_k, const int32_t *tokens,
                                 const float *topk_w, void *drows, int64_t ldd, float *dtopk_w, void *stream);

@@ -829,9 +829,12 @@ moe_status moe_combine_forward(const void *rows, int32_t dtype, int64_t ld, int3
     MOE_NEED(ldy >= N && (!add || ldadd >= N), MOE_ERR_INVALID, "a row stride is less than N=%d", N);
     if (T == 0) return MOE_OK;
     MOE_NEED((rows || R == 0) && pos && y, MOE_ERR_INVALID, "rows / pos / y is NULL");
-    MOE_NEED(y != rows, MOE_ERR_INVALID, "y is rows");
     MOE_NEED(aligned_el(rows, dtype) && aligned_el(add, y_dtype) && aligned_el(y, y_dtype) && aligned4(pos) && aligned4(topk_w),
              MOE_ERR_INVALID, "a buffer is not aligned to its elements");
+    const Rows ry(y, T, ldy, N, el_size(y_dtype));
+    MOE_NEED(!overlap(ry, Rows(rows, R, ld, N, el_size(dtype))) && !askew(ry, Rows(add, T, ldadd, N, el_size(y_dtype))) &&
+             !overlap(ry, Rows(pos, (int64_t)T * top_k * 4)) && !overlap(ry, Rows(topk_w, (int64_t)T * top_k * 4)),
+             MOE_ERR_INVALID, "y overlaps another tensor");
     return launched(moe::launch_combine_forward(rows, dtype, ld, R, N, pos, T, top_k, topk_w, add, ldadd, y, y_dtype, ldy,
                                                 static_cast<cudaStream_t>(stream)), "moe_combine_forward");
 }
@@ -848,7 +851,11 @@ moe_status moe_combine_backward(const void *dy, int32_t dtype, int64_t lddy, con
     MOE_NEED(aligned_el(dy, dtype) && aligned_el(rows, dtype) && aligned_el(drows, dtype) && aligned4(pos) && aligned4(tokens) &&
              aligned4(topk_w) && aligned4(dtopk_w), MOE_ERR_INVALID, "a buffer is not aligned to its elements");
     if ((T == 0 && (R == 0 || !drows)) || (!drows && !dtopk_w)) return MOE_OK;
-    MOE_NEED(!drows || (drows != rows && drows != dy), MOE_ERR_INVALID, "drows is rows or dy");
+    const int64_t el = el_size(dtype), pairs = (int64_t)T * top_k * 4;
+    const Rows ro(drows, R, ldd, N, el), rdy(dy, T, lddy, N, el), rr(dtopk_w ? rows : nullptr, R, ld, N, el), rp(pos, pairs), rt(tokens, (int64_t)R * 4),
+        rw(topk_w, pairs), rdw(dtopk_w, pairs);
+    for (const Rows *i : {&rdy, &rr, &rp, &rt}) MOE_NEED(!overlap(ro, *i) && !overlap(rdw, *i), MOE_ERR_INVALID, "drows or dtopk_w overlaps another tensor");
+    MOE_NEED(!overlap(ro, rw) && !overlap(ro, rdw) && !askew(rdw, rw), MOE_ERR_INVALID, "drows or dtopk_w overlaps another tensor");
     return launched(moe::launch_combine_backward(dy, dtype, lddy, rows, ld, R, N, pos, T, top_k, tokens, topk_w, drows, ldd, dtopk_w,
                                                  static_cast<cudaStream_t>(stream)), "moe_combine_backward");
 }

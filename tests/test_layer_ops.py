@@ -236,6 +236,23 @@ def test_route_refuses_outputs_on_top_of_other_tensors(moe):
         assert bwd(**kw) == moe.MOE_ERR_INVALID, kw
 
 
+def test_combine_refuses_outputs_on_top_of_other_tensors(moe):
+    L, T, R, N, K = moe.lib(), 4, 16, 64, 2
+    r, y, a, q, w, t, d, z = (P + 65536 * (k + 1) for k in range(8))
+
+    def fwd(y=y, a=a, ld=N, ldy=N, dt=0, yt=0):
+        return L.moe_combine_forward(r, dt, ld, R, N, q, T, K, w, a, N, y, yt, ldy, None)
+    for kw in (dict(y=r), dict(y=r + 256), dict(y=r + 4), dict(y=r - 1020), dict(y=r + 15 * 256), dict(y=r + 256, ld=192), dict(y=r + 252, ld=128, ldy=128),
+               dict(y=a + 256), dict(y=a - 4), dict(y=a, ldy=128), dict(y=q), dict(y=w - 1020), dict(y=r + 128, yt=2)):
+        assert fwd(**kw) == moe.MOE_ERR_INVALID, kw
+
+    def bwd(d=d, z=z, dy=y, ld=N, ldd=N):
+        return L.moe_combine_backward(dy, 0, N, r, ld, R, N, q, T, K, t, w, d, ldd, z, None)
+    for kw in (dict(d=r), dict(d=r + 256), dict(d=r - 4), dict(d=y), dict(d=y - 15 * 256), dict(d=r + 256, ld=192), dict(d=q), dict(d=t - 4092), dict(d=w), dict(d=z),
+               dict(z=d + 16), dict(z=r), dict(z=y + 1020), dict(z=q + 28), dict(z=t), dict(z=w + 4), dict(d=r + 252, ld=128, ldd=128)):
+        assert bwd(**kw) == moe.MOE_ERR_INVALID, kw
+
+
 def test_binding_refuses_what_is_not_on_the_device(moe):
     x, i = torch.zeros(2, 16), torch.zeros(2, 1, dtype=torch.int32)
     for call in (lambda: moe.moe_route_forward(x, 1), lambda: moe.moe_norm_forward(x), lambda: moe.moe_combine_forward(x, i),
@@ -1141,6 +1158,43 @@ def test_combine_strided_rows(gpu, dtype, pad, shift):
     out = torch.full((R, N + pad + 1), 7.0, dtype=dtype, device="cuda")
     check_combine_grad(gpu, dy, rows, pos, tokens, w, out=out[:, :N])
     assert bool((out[:, N:] == 7).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [64, 67])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_combine_beside_its_inputs(gpu, dtype, N):
+    """Rows and their gradient, or add and the sum, in columns of one buffer; the weights' gradient on top of the weights; rows in common are refused."""
+    T, E, K = 33, 6, 3
+    g = gen(N)
+    tokens, pos = lists_of(gpu, T, E, K, 4, N)
+    R = tokens.numel()
+    rows, dy, w = torch.randn(R, N, generator=g).to(dtype).cuda(), torch.randn(T, N, generator=g).to(dtype).cuda(), torch.randn(T, K, generator=g).cuda()
+    d, dw = gpu.moe_combine_backward(dy, rows, pos, tokens, w)
+    both = torch.zeros(R, 2, N, dtype=dtype, device="cuda")
+    both[:, 0] = rows
+    a, b = gpu.moe_combine_backward(dy, both[:, 0], pos, tokens, w, out=both[:, 1])
+    check_combine_grad(gpu, dy, both[:, 0], pos, tokens, w, out=both[:, 1])
+    assert torch.equal(both[:, 0], rows) and bool(((b - dw).abs() <= 2.0 ** -17 * N).all()) and torch.equal(a, d)
+    ww = w.clone()
+    code = {F32: 0, BF16: 2}[dtype]
+    out = torch.empty_like(rows)
+    assert gpu.MOE_OK == gpu.lib().moe_combine_backward(dy.data_ptr(), code, N, rows.data_ptr(), N, R, N, pos.data_ptr(), T, K, tokens.data_ptr(), ww.data_ptr(),
+                                                        out.data_ptr(), N, ww.data_ptr(), torch.cuda.current_stream().cuda_stream)
+    assert torch.equal(ww, dw) and torch.equal(out, d)
+    y = gpu.moe_combine_forward(rows, pos, w, add=dy)
+    both = torch.zeros(T, 2, N, dtype=dtype, device="cuda")
+    both[:, 0] = dy
+    gpu.moe_combine_forward(rows, pos, w, add=both[:, 0], out=both[:, 1])
+    assert torch.equal(both[:, 0], dy)
+    check_combine(gpu, rows, pos, w, both[:, 0], out=both[:, 1])
+    check_combine(gpu, rows, pos, w, dy.clone())
+    assert y.shape == (T, N)
+    flat = torch.zeros(R + 1, N, dtype=dtype, device="cuda")
+    for call in (lambda: gpu.moe_combine_forward(flat[:-1], pos, w, out=flat[1:T + 1]), lambda: gpu.moe_combine_forward(rows, pos, w, add=flat[:T], out=flat[1:T + 1]),
+                 lambda: gpu.moe_combine_backward(dy, flat[:-1], pos, tokens, w, out=flat[1:]), lambda: gpu.moe_combine_backward(flat[:T], rows, pos, tokens, w, out=flat[1:])):
+        with pytest.raises(gpu.MoeError):
+            call()
 
 
 @pytest.mark.gpu
