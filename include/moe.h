@@ -592,7 +592,8 @@ moe_status moe_combine_backward(const void *dy, int32_t dtype, int64_t lddy, con
  * overflow nor vanish; a NaN or an infinity anywhere is one in norm, and a norm beyond float32 infinite).  grads, dtypes, sizes: host arrays of n_tensors
  * (0..65536) device addresses on their elements' boundary, MOE_DTYPE_* and numbers of elements (up to 2^45
  * in all); read during the call alone, so that a captured call needs none of them later.  workspace:
- * moe_grad_norm_workspace(n_tensors) bytes on the current device, 16-byte aligned. */
+ * moe_grad_norm_workspace(n_tensors) bytes on the current device, 16-byte aligned; neither it nor norm may
+ * overlap a gradient. */
 size_t moe_grad_norm_workspace(int32_t n_tensors);
 moe_status moe_grad_norm(int32_t n_tensors, const void *const *grads, const int32_t *dtypes, const int64_t *sizes,
                          float *norm, void *workspace, size_t workspace_bytes, void *stream);
@@ -601,7 +602,7 @@ moe_status moe_grad_norm(int32_t n_tensors, const void *const *grads, const int3
  * NULL: in place (which moves nothing where the factor is 1).  norm is device memory: moe_grad_norm's, or
  * what expert-parallel ranks made of theirs.  An infinite norm makes zeros (NaN of infinities), a NaN
  * makes every gradient NaN.  max_norm: finite, 0 or more.  No output may overlap another tensor of the
- * call but its own input. */
+ * call, norm included, but its own input. */
 moe_status moe_grad_clip(int32_t n_tensors, const void *const *grads, const int32_t *dtypes, const int64_t *sizes,
                          const float *norm, float max_norm, void *const *out, void *stream);
 

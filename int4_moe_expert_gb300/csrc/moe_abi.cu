@@ -885,6 +885,12 @@ moe_status moe_grad_norm(int32_t n_tensors, const void *const *grads, const int3
     if (s != MOE_OK) return s;
     const size_t need = moe_grad_norm_workspace(n_tensors);
     MOE_NEED(workspace && aligned16(workspace) && workspace_bytes >= need, MOE_ERR_INVALID, "workspace: need %zu bytes, 16-byte aligned", need);
+    const Rows rn(norm, 4), rw(workspace, (int64_t)need);
+    MOE_NEED(!overlap(rn, rw), MOE_ERR_INVALID, "norm and workspace overlap");
+    for (int32_t i = 0; i < n_tensors; i++) {
+        const Rows g(grads[i], sizes[i] * el_size(dtypes[i]));
+        MOE_NEED(!overlap(g, rn) && !overlap(g, rw), MOE_ERR_INVALID, "norm or workspace overlaps tensor %d", i);
+    }
     return launched(moe::launch_grad_norm(n_tensors, grads, dtypes, sizes, norm, workspace, static_cast<cudaStream_t>(stream)), "moe_grad_norm");
 }
 
@@ -902,7 +908,9 @@ moe_status moe_grad_clip(int32_t n_tensors, const void *const *grads, const int3
     };
     try {
         std::vector<Range> r;
-        r.reserve(2 * (size_t)n_tensors);
+        r.reserve(2 * (size_t)n_tensors + 1);
+        const uintptr_t at = reinterpret_cast<uintptr_t>(norm);       // read by every block
+        r.push_back({at, at + 4, n_tensors, false});
         for (int32_t i = 0; i < n_tensors; i++) {
             if (sizes[i] == 0) continue;
             const uintptr_t bytes = (uintptr_t)sizes[i] * (dtypes[i] == MOE_DTYPE_F32 ? 4 : 2);
@@ -915,7 +923,8 @@ moe_status moe_grad_clip(int32_t n_tensors, const void *const *grads, const int3
         const Range *far = nullptr, *far_written = nullptr;       // the furthest end so far, of all and of the written ones
         for (const Range &q : r) {
             const Range *other = q.written ? far : far_written;
-            MOE_NEED(!other || other->b <= q.a, MOE_ERR_INVALID, "tensors %d and %d overlap, and one of them is written", other->tensor, q.tensor);
+            MOE_NEED(!other || other->b <= q.a, MOE_ERR_INVALID, "tensors %d and %d overlap, and one of them is written (%d: norm)", other->tensor,
+                     q.tensor, n_tensors);
             if (!far || q.b > far->b) far = &q;
             if (q.written && (!far_written || q.b > far_written->b)) far_written = &q;
         }

@@ -253,6 +253,21 @@ def test_combine_refuses_outputs_on_top_of_other_tensors(moe):
         assert bwd(**kw) == moe.MOE_ERR_INVALID, kw
 
 
+def test_grad_norm_on_top_of_gradients_is_refused(moe):
+    """The clipping's blocks read the norm while others write; the norm's blocks write their sums while others read."""
+    L, n = moe.lib(), 1000
+    g, h, ws, far = P, P + 65536, P + 131072, P + 262144
+    ptr = lambda *a: (C.c_void_p * len(a))(*a)   # noqa: E731
+    kinds, sizes = (C.c_int32 * 2)(0, 2), (C.c_int64 * 2)(n, n)
+    for norm in (g, g + 4 * n - 4, h, h + 2 * n - 4):
+        assert L.moe_grad_clip(2, ptr(g, h), kinds, sizes, norm, 1.0, None, None) == moe.MOE_ERR_INVALID
+        assert L.moe_grad_clip(2, ptr(far, far + 65536), kinds, sizes, norm, 1.0, ptr(g, h), None) == moe.MOE_ERR_INVALID
+        assert L.moe_grad_norm(2, ptr(g, h), kinds, sizes, norm, ws, 1 << 16, None) == moe.MOE_ERR_INVALID
+    for w in (g, g + 4 * n - 16, h):
+        assert L.moe_grad_norm(2, ptr(g, h), kinds, sizes, far, w, 1 << 16, None) == moe.MOE_ERR_INVALID
+    assert L.moe_grad_norm(2, ptr(g, h), kinds, sizes, ws + 16, ws, 1 << 16, None) == moe.MOE_ERR_INVALID
+
+
 def test_binding_refuses_what_is_not_on_the_device(moe):
     x, i = torch.zeros(2, 16), torch.zeros(2, 1, dtype=torch.int32)
     for call in (lambda: moe.moe_route_forward(x, 1), lambda: moe.moe_norm_forward(x), lambda: moe.moe_combine_forward(x, i),
@@ -1294,6 +1309,26 @@ def test_clip_unaligned_and_permuted(gpu, shift):
     for a, b in zip(grads, out):
         assert bool(((b.double() - a.double() * 0.25 / (float(n) + 1e-6)).abs() <= 2.0 ** -19 * a.double().abs()).all())
     assert bool((buf[:shift] != 0).all())
+
+
+@pytest.mark.gpu
+def test_clip_norm_beside_the_gradients(gpu):
+    """One buffer holds a gradient, the norm and a gradient; the norm inside one of them is refused."""
+    flat = torch.randn(2049, device="cuda")
+    a, norm, b = flat[:1024], flat[1024:1025], flat[1025:]
+    was = [a.clone(), b.clone()]
+    norm.copy_(gpu.moe_grad_norm([a, b]))
+    n = float(norm)
+    gpu.moe_grad_clip([a, b], norm, 0.5)
+    for x, y in zip((a, b), was):
+        assert bool(((x.double() - y.double() * 0.5 / (n + 1e-6)).abs() <= 2.0 ** -19 * y.double().abs()).all())
+    assert float(norm) == n
+    with pytest.raises(gpu.MoeError):
+        gpu.moe_grad_clip([flat], norm, 0.5)
+    other = [torch.zeros_like(a), torch.zeros_like(b)]
+    gpu.moe_grad_clip([a, b], a[5:6], 0.5, out=other)          # read alone: one of the inputs may hold it
+    with pytest.raises(gpu.MoeError):
+        gpu.moe_grad_clip([a, b], other[1][5:6], 0.5, out=other)
 
 
 @pytest.mark.gpu
