@@ -574,7 +574,7 @@ moe_status moe_norm_backward(const void *dy, int32_t dtype, int64_t lddy, const 
  * moe_expert_lists writes it: pairs with a value outside [0, R) are left out, so rows without a token are
  * never read.  topk_w NULL: 1; add[T, N] (y_dtype) NULL: none.  y must not overlap another tensor of the call, but
  * may be the very rows of add.
- * N in 1..131072, K in 1..32, T times ceil(N / 256) up to 2^33. */
+ * N in 1..131072, K in 1..32, T times ceil((N + 7) / 124) up to 2^33. */
 moe_status moe_combine_forward(const void *rows, int32_t dtype, int64_t ld, int32_t R, int32_t N, const int32_t *pos,
                                int32_t T, int32_t top_k, const float *topk_w, const void *add, int64_t ldadd, void *y,
                                int32_t y_dtype, int64_t ldy, void *stream);

@@ -825,7 +825,8 @@ moe_status moe_combine_forward(const void *rows, int32_t dtype, int64_t ld, int3
     const moe_status s = check_combine(dtype, ld, R, N, T, top_k);
     if (s != MOE_OK) return s;
     MOE_NEED(dtype_ok(y_dtype), MOE_ERR_INVALID, "y_dtype=%d: need a MOE_DTYPE_* value", y_dtype);
-    MOE_NEED((int64_t)T * ((N + 255) / 256) <= 1ll << 33, MOE_ERR_UNSUPPORTED, "T=%d: need 2^33 / ceil(N / 256) or fewer", T);
+    // a warp has 124 columns at least, seven before the row's first boundary among them: 2^30 blocks of 8 warps
+    MOE_NEED((int64_t)T * ((N + 7 + 123) / 124) <= 1ll << 33, MOE_ERR_UNSUPPORTED, "T=%d: need 2^33 / ceil((N + 7) / 124) or fewer", T);
     MOE_NEED(ldy >= N && (!add || ldadd >= N), MOE_ERR_INVALID, "a row stride is less than N=%d", N);
     if (T == 0) return MOE_OK;
     MOE_NEED((rows || R == 0) && pos && y, MOE_ERR_INVALID, "rows / pos / y is NULL");

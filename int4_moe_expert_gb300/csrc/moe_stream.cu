@@ -683,7 +683,7 @@ cudaError_t launch_combine_forward(const void *rows, int dtype, long long ld, lo
             auto go = [&](auto kernel, int columns, int each) {       // columns of a warp
                 p.parts = (columns + each - 1) / each;
                 const long long blocks = ((long long)T * p.parts + kCombWarps - 1) / kCombWarps;
-                return blocks <= 0x7fffffff ? launch_early(kernel, (unsigned)blocks, 32 * kCombWarps, 0, st, 1, p) : cudaErrorInvalidConfiguration;
+                return launch_early(kernel, (unsigned)blocks, 32 * kCombWarps, 0, st, 1, p);
             };
             if (N % 8 == 0 && runs_of(rows, ld, sizeof(X), 16) && runs_of(y, ldy, sizeof(Y), 16) && (!add || runs_of(add, ldadd, sizeof(Y), 16)))
                 return go(combine_kernel<X, Y>, N, 8 * 32);

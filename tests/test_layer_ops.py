@@ -268,6 +268,13 @@ def test_grad_norm_on_top_of_gradients_is_refused(moe):
     assert L.moe_grad_norm(2, ptr(g, h), kinds, sizes, ws + 16, ws, 1 << 16, None) == moe.MOE_ERR_INVALID
 
 
+def test_combine_refuses_more_blocks_than_a_grid_has(moe):
+    """Rows off the boundaries have fewer columns a warp than the others: the limit is theirs, and a refusal, not a failed launch."""
+    L, T, far = moe.lib(), 2**31 - 1, 1 << 50
+    for N, dt in ((1023, 0), (1021, 2), (997, 1)):
+        assert L.moe_combine_forward(P, dt, N, 16, N, far, T, 2, None, None, N, 2 * far, dt, N, None) == moe.MOE_ERR_UNSUPPORTED, N
+
+
 def test_binding_refuses_what_is_not_on_the_device(moe):
     x, i = torch.zeros(2, 16), torch.zeros(2, 1, dtype=torch.int32)
     for call in (lambda: moe.moe_route_forward(x, 1), lambda: moe.moe_norm_forward(x), lambda: moe.moe_combine_forward(x, i),
