@@ -778,24 +778,35 @@ cudaError_t launch_route_forward(const void *logits, int dtype, long long ld, in
         // With groups the kept ones may share lanes, which leaves more candidates: two tokens where each group covers
         // all their lanes (in runs of two logits 32 experts, one by one 16), or where enough lanes are left in any
         // case (16381 x 256 in 8 groups of which 4: one token in runs of four 19.5 us, two in runs of two 13.9).
+        // Experts that are as many as a layout holds in runs (E = J LPT) need no bounds: 65536 x 128 23.1 us, with them
+        // 24.2; x 256 26.0 and 28.3, x 512 48 and 53, x 1024 77 and 84.  64 or fewer take runs of four only where these
+        // fill the lanes: among fewer lanes more experts are candidates (65536 x 48: 22.0 us, one by one 19.8).
+        auto runs = [&](auto j, auto lpt, auto v) {
+            constexpr int J = decltype(j)::value, LPT = decltype(lpt)::value, V = decltype(v)::value;
+            return E == J * LPT ? go(RouteLay<B, J, LPT, V, true>{}) : go(RouteLay<B, J, LPT, V>{});
+        };
+        std::integral_constant<int, 2> two;
+        std::integral_constant<int, 4> four;
+        std::integral_constant<int, 8> eight;
+        std::integral_constant<int, 16> sixteen;
+        std::integral_constant<int, 32> all;
         if (K <= 4 && groups == 1 && E <= 64) return E <= 16 ? go(RouteLay<B, 2, 8, 1>{}) : go(RouteLay<B, 8, 8, 1>{});
         if (groups > 1 && K <= 8 && groups <= 16 && p.per_group >= 16 && E > 32 && E <= 256) {
             if (E <= 64) return go(RouteLay<B, 4, 16, 1>{});
             if (E <= 128) return go(RouteLay<B, 8, 16, 1>{});
-            if (pairs && p.per_group >= 32) return E == 256 ? go(RouteLay<B, 16, 16, 2, true>{}) : go(RouteLay<B, 16, 16, 2>{});
-            return go(RouteLay<B, 16, 16, 1>{});
+            return pairs && p.per_group >= 32 ? runs(sixteen, sixteen, two) : go(RouteLay<B, 16, 16, 1>{});
         }
         if (K <= 8 && groups <= 16 && kept * 8 >= groups * K) {
             if (E <= 32) return go(RouteLay<B, 2, 16, 1>{});
-            if (E <= 64) return quads && E == 64 ? go(RouteLay<B, 4, 16, 4, true>{}) : go(RouteLay<B, 4, 16, 1>{});
-            if (E <= 128) return quads ? go(RouteLay<B, 8, 16, 4>{}) : go(RouteLay<B, 8, 16, 1>{});
-            if (E <= 256) return !quads ? go(RouteLay<B, 16, 16, 1>{}) : E == 256 ? go(RouteLay<B, 16, 16, 4, true>{}) : go(RouteLay<B, 16, 16, 4>{});
+            if (E <= 64) return E == 4 * 16 && quads ? go(RouteLay<B, 4, 16, 4, true>{}) : go(RouteLay<B, 4, 16, 1>{});
+            if (E <= 128) return quads ? runs(eight, sixteen, four) : go(RouteLay<B, 8, 16, 1>{});
+            if (E <= 256) return quads ? runs(sixteen, sixteen, four) : go(RouteLay<B, 16, 16, 1>{});
         } else {
             if (E <= 64) return go(RouteLay<B, 2, 32, 1>{});
-            if (E <= 256) return !quads || E < 128 ? go(RouteLay<B, 8, 32, 1>{}) : E == 256 ? go(RouteLay<B, 8, 32, 4, true>{}) : go(RouteLay<B, 8, 32, 4>{});
+            if (E <= 256) return quads && E >= 128 ? runs(eight, all, four) : go(RouteLay<B, 8, 32, 1>{});
         }
-        if (E <= 512) return quads ? go(RouteLay<B, 16, 32, 4>{}) : go(RouteLay<B, 16, 32, 1>{});
-        return quads ? go(RouteLay<B, 32, 32, 4>{}) : go(RouteLay<B, 32, 32, 1>{});
+        if (E <= 512) return quads ? runs(sixteen, all, four) : go(RouteLay<B, 16, 32, 1>{});
+        return quads ? runs(all, all, four) : go(RouteLay<B, 32, 32, 1>{});
     };
     return bias && !softmax ? by_size(std::true_type{}) : by_size(std::false_type{});
 }

@@ -419,6 +419,22 @@ def test_route_groups_of_every_layout(gpu, E, G, dtype, shift):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("E", [64, 128, 256, 512, 1024])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,K,G", [(1, 8, 1), (37, 6, 1), (70, 12, 1), (41, 8, 4)])
+def test_route_experts_that_fill_the_lanes(gpu, E, dtype, T, K, G):
+    """Rows without an end inside a run, on their boundary and off it; the last expert is among the choices."""
+    g = gen(E, T)
+    x = torch.randn(T, E, generator=g)
+    x[:, E - 1] = 4.0
+    x = x.to(dtype)
+    bias = 0.2 * torch.randn(E, generator=g)
+    for b in (None, bias):
+        for v in (x.cuda(), strided(x, 1, 1), strided(x, 8, 0)):
+            check_route(gpu, v, K, bias=b, G=G, kept=max(1, G // 2))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("E,K,G,dtype", [(64, 6, 1, F32), (256, 8, 1, BF16), (256, 8, 8, F32), (1000, 32, 1, F32), (96, 4, 4, F16), (40, 8, 1, F32), (33, 33 - 1, 1, F32)])
 def test_route_many_equal_keys(gpu, E, K, G, dtype):
     """Rows with more equal keys than a warp has lanes: of one logit, of few, with infinities, NaN, and neighbours that float32 does not tell apart."""
