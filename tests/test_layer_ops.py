@@ -1477,6 +1477,51 @@ def test_capture_and_side_stream(gpu):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("handle", [False, True])
+def test_stream_argument_of_every_operator(gpu, handle):
+    """stream= (an object or its handle) while another stream is the current one: each call waits for what that stream makes before it."""
+    T, E, K, H = 300, 64, 6, 512
+    g = gen(77)
+    inputs = [torch.randn(T, E, generator=g).cuda(), torch.randn(T, H, generator=g).cuda(), torch.randn(T, H, generator=g).cuda()]
+    weight = (1 + 0.1 * torch.randn(H, generator=g)).cuda()
+    other = torch.cuda.Stream()
+
+    def step(held, at=None):
+        s = at if at is None or not handle else at.cuda_stream
+
+        def call(f, *a, **kw):
+            if at is not None:                       # the stream is behind by a millisecond or so before every call
+                with torch.cuda.stream(at):
+                    torch.cuda._sleep(1000000)
+            return f(*a, stream=s, **kw)
+        if at is not None:
+            with torch.cuda.stream(at):
+                torch.cuda._sleep(1000000)
+                for a, b in zip(held, inputs):
+                    a.copy_(b)
+        logits, x, res = held
+        idx, w = call(gpu.moe_route_forward, logits, K)
+        _, _, rows, pos = call(gpu.moe_expert_lists, idx, E, 16)
+        y, h, r, q, sc = call(gpu.moe_norm_forward, x, residual=res, weight=weight, quantize=True)
+        with torch.cuda.stream(at or torch.cuda.current_stream()):
+            each = y.index_select(0, rows.clamp(min=0).long())
+        z = call(gpu.moe_combine_forward, each, pos, w, add=y)
+        d, dw = call(gpu.moe_combine_backward, z, each, pos, rows, w)
+        dl = call(gpu.moe_route_backward, logits, idx, dw)
+        dh, dn = call(gpu.moe_norm_backward, z, h, r, weight=weight, grad_h=z)
+        n = call(gpu.moe_grad_norm, [dl, dn, d])
+        call(gpu.moe_grad_clip, [dl, dn, d], n, 1.0)
+        return [idx, w, pos, y, h, r, q.view(torch.uint8), sc, z, d, dw, dl, dh, dn, n]
+    want = step(inputs)
+    held = [torch.zeros_like(t) for t in inputs]
+    torch.cuda.synchronize()
+    got = step(held, other)
+    other.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
 def test_training_step_of_a_layer(gpu):
     """Norm, routing, lists, quantised products, combine and back, as a trainer runs them: gradients against
     autograd in float64 on the dequantised operands of the same step."""
