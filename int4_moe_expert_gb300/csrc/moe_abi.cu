@@ -655,23 +655,33 @@ static bool aligned_rows(const void *p, int64_t ld, int32_t dtype) {
     return aligned16(p) && ld * (dtype == MOE_DTYPE_F32 ? 4 : 2) % 16 == 0;
 }
 
-// A tensor in memory: rows of `width` bytes, `pitch` bytes apart.
+// A tensor in memory: rows of `width` bytes, `pitch` bytes apart, from `at` to `end` (none: both 0).
 struct Rows {
-    uintptr_t at;
-    int64_t rows, pitch, width;
-    Rows(const void *p, int64_t n, int64_t ld, int64_t elements, int64_t el)
-        : at(reinterpret_cast<uintptr_t>(p)), rows(p ? n : 0), pitch(ld <= INT64_MAX / el ? ld * el : INT64_MAX), width(elements * el) {}
-    Rows(const void *p, int64_t bytes) : Rows(p, bytes > 0, bytes, bytes, 1) {}
-    int64_t bytes() const { return rows < 2 ? width : pitch > INT64_MAX / rows ? INT64_MAX : (rows - 1) * pitch + width; }
+    uintptr_t at = 0, end = 0;
+    int64_t rows = 0, pitch = 0, width = 0;
+    Rows(const void *p, int64_t n, int64_t ld, int64_t elements, int64_t el) {
+        if (!p || n < 1) return;
+        int64_t bytes;
+        at = reinterpret_cast<uintptr_t>(p);
+        rows = n;
+        width = elements * el;
+        if (__builtin_mul_overflow(ld, el, &pitch) || __builtin_mul_overflow(n - 1, pitch, &bytes)) pitch = bytes = n > 1 ? INT64_MAX / 2 : 0;
+        end = at + (uintptr_t)bytes + (uintptr_t)width;
+    }
+    Rows(const void *p, int64_t bytes) {
+        if (!p || bytes < 1) return;
+        at = reinterpret_cast<uintptr_t>(p);
+        end = at + (uintptr_t)bytes;
+        rows = 1;
+        pitch = width = bytes;
+    }
 };
 static int64_t el_size(int32_t dtype) { return dtype == MOE_DTYPE_F32 ? 4 : 2; }
 // Whether the two have bytes in common: slices of other columns of one buffer's rows have none.
 static bool overlap(const Rows &a, const Rows &b) {
-    if (a.rows < 1 || b.rows < 1) return false;
-    const int64_t d = (int64_t)(b.at - a.at);
-    if (d >= a.bytes() || -d >= b.bytes()) return false;
+    if (a.at >= b.end || b.at >= a.end) return false;
     if (a.rows < 2 && b.rows < 2) return true;
-    const int64_t g = a.rows < 2 ? b.pitch : b.rows < 2 ? a.pitch : std::gcd(a.pitch, b.pitch), r = (d % g + g) % g;
+    const int64_t g = a.rows < 2 ? b.pitch : b.rows < 2 ? a.pitch : std::gcd(a.pitch, b.pitch), d = (int64_t)(b.at - a.at) % g, r = d < 0 ? d + g : d;
     return r < a.width || r + b.width > g;
 }
 // The same, but rows on top of one another: each is read by who writes it, before it does.
