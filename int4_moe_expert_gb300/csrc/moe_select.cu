@@ -20,7 +20,8 @@ namespace {
 // ranking are nearer than float32 tells, the whole warp ranks them in float64, and so the groups whose scores
 // are that near; with more candidates than lanes it ranks them, with more than 32 it does the row over (in float32
 // where ties are of the same logit and bias).
-// Bound by the issue of instructions (two thirds of the slots, half of the ALU's; about 600 for the two tokens of a
+// Bound by the instructions of a token and their latency (67 % of the issue slots with 45 % of the warps, half of the
+// ALU's; about 600 instructions for the two tokens of a
 // warp, of which 200 for scores, 180 for candidates and their keys, 160 for sort and ranking): 65536 x 256 float32
 // 27 us (10.5 to move the bytes), 16381 x 256 bf16 in 8 groups 14 us, 32768 x 64 bf16 softmax 12 us.  More blocks
 // an SM with fewer registers, logits loaded a round ahead and K rounds over all experts are slower.
@@ -562,8 +563,9 @@ __global__ void __launch_bounds__(kRouteThreads, L::PER_SM) route_kernel(const R
 // An expert that is named twice gets the sum of its gradients.  All but the last read the chosen logits
 // alone: a batch of KP lanes a token computes them, the warp fills its tokens' rows with zeros and the
 // lanes write their values over them (the same warp's stores, in order).
-// Bound by memory: 65536 x 256 float32, K = 8: 20 us; 10.5 for the row of zeros and the indices, 16 with the 64 bytes
-// that each scattered logit takes from memory.  32768 x 64 bf16 softmax: 6 us, two thirds of the issue slots.
+// Bound by the latency of the loads that hang on one another, index and logit (DRAM at 39 %, a quarter of the issue slots):
+// 65536 x 256 float32, K = 8: 20 us; 10.5 for the row of zeros and the indices, 16 with the 64 bytes that each
+// scattered logit takes from memory.  32768 x 64 bf16 softmax: 6 us, two thirds of the issue slots.
 // ---------------------------------------------------------------------------
 
 struct RouteGradArgs {
