@@ -19,7 +19,7 @@ namespace {
 // float32's error has its sum of squares done over in float64, so the scales are those of the formula.  A row whose
 // squares leave float32's range is squared once more behind a power of two.
 // 32768 x 2048 bf16 on a float32 stream: 117 us at the copy rate; 16381 x 6144 bf16 with values and codes 142 us of
-// 134 (two thirds of the issue slots: codes and scales).  Rows of odd widths go element by element: 8192 x 4095 bf16
+// 134 (59 % of the issue slots: codes and scales).  Rows of odd widths go element by element: 8192 x 4095 bf16
 // 58 us of 40, f32 82 us of 79.
 // ---------------------------------------------------------------------------
 
@@ -708,8 +708,10 @@ cudaError_t launch_norm_forward(const void *x, int dtype, long long ldx, const v
             // Single elements and pairs take every thread of their class, whose number is a constant then: elements that
             // a number known at run time lies between have an address each (8192 x 4095 bf16: 110 us, 60 so).
             constexpr bool WHOLE = V < 8;
-            if (WHOLE && threads <= 32) return run(norm_kernel<X, S, V, 16, 32, 32, false>, 32, 1);
-            if (WHOLE && threads <= 64) return run(norm_kernel<X, S, V, 16, 64, 16, false>, 64, 1);
+            if constexpr (WHOLE) {
+                if (threads <= 32) return run(norm_kernel<X, S, V, 16, 32, 32, false>, 32, 1);
+                if (threads <= 64) return run(norm_kernel<X, S, V, 16, 64, 16, false>, 64, 1);
+            }
             if (threads <= 128) return run(norm_kernel<X, S, V, 16, 128, 8, false>, WHOLE ? 128 : threads, 1);
             if (threads <= 256) return run(norm_kernel<X, S, V, 16, 256, 4, false>, WHOLE ? 256 : threads, 1);
             if (threads <= 384) return run(norm_kernel<X, S, V, 16, 384, WHOLE ? 2 : 3, false>, WHOLE ? 384 : threads, 1);
@@ -761,8 +763,10 @@ cudaError_t launch_norm_backward(const void *dy, int dtype, long long lddy, cons
             blocks = norm_blocks(T, H <= 256 ? kWarpRows : 1, direct_per_sm(H, threads));
             if (H <= 256)
                 return launch_early(norm_grad_kernel<X, S, V, 8, 32 * kWarpRows, 6, true>, blocks, threads, dw ? (size_t)kWarpRows * H * sizeof(float) : 0, st, 1, p);
-            if (WHOLE && threads <= 32) return launch_early(norm_grad_kernel<X, S, V, 16, 32, 20, false>, blocks, threads, 0, st, 1, p);
-            if (WHOLE && threads <= 64) return launch_early(norm_grad_kernel<X, S, V, 16, 64, 10, false>, blocks, threads, 0, st, 1, p);
+            if constexpr (WHOLE) {
+                if (threads <= 32) return launch_early(norm_grad_kernel<X, S, V, 16, 32, 20, false>, blocks, threads, 0, st, 1, p);
+                if (threads <= 64) return launch_early(norm_grad_kernel<X, S, V, 16, 64, 10, false>, blocks, threads, 0, st, 1, p);
+            }
             if (threads <= 128) return launch_early(norm_grad_kernel<X, S, V, 16, 128, 5, false>, blocks, threads, 0, st, 1, p);
             if (threads <= 256) return launch_early(norm_grad_kernel<X, S, V, 16, 256, 3, false>, blocks, threads, 0, st, 1, p);
             if (threads <= 384) return launch_early(norm_grad_kernel<X, S, V, 16, 384, 2, false>, blocks, threads, 0, st, 1, p);
